@@ -22,7 +22,7 @@ FM_OK, FM_ERR_INVALID_ARG, FM_ERR_UNSUPPORTED, FM_ERR_OOM, FM_ERR_CONTEXT_FULL, 
     FM_ERR_TIMEOUT = range(8)
 FM_VARIANT_FLASHMAP, FM_VARIANT_DFLASH = 0, 1
 FM_LM_BF16, FM_LM_Q8_0 = 0, 1
-FM_DTYPE_BF16, FM_DTYPE_Q8_0, FM_DTYPE_F32 = 0, 1, 2
+FM_DTYPE_BF16, FM_DTYPE_Q8_0, FM_DTYPE_F32, FM_DTYPE_F16 = 0, 1, 2, 3
 FM_DEBUG_HIDDEN, FM_DEBUG_HEAD_OUT, FM_DEBUG_LOGITS, FM_DEBUG_CACHE_K, FM_DEBUG_CACHE_V, FM_DEBUG_H0, \
     FM_DEBUG_STEP_TRACE = range(7)
 FM_DEBUG_KEEP_HIDDEN = 1
@@ -36,7 +36,9 @@ EXPORTS = ["fm_create", "fm_time_conditioning", "fm_context_append", "fm_context
            "fm_last_launch_count", "fm_profile_read", "fm_status_str", "fm_last_error", "fm_destroy",
            "fm_policy_init", "fm_policy_next", "fm_policy_after_round", "fm_policy_after_plain",
            "fm_mtp_create", "fm_mtp_forward", "fm_mtp_draft", "fm_mtp_cache", "fm_mtp_last_launch_count",
-           "fm_mtp_last_error", "fm_mtp_destroy"]
+           "fm_mtp_last_error", "fm_mtp_destroy",
+           "fm_kvq_create", "fm_kvq_append", "fm_kvq_read", "fm_kvq_attend", "fm_kvq_set_weights", "fm_kvq_evict",
+           "fm_kvq_length", "fm_kvq_memory_bytes", "fm_kvq_synchronize", "fm_kvq_last_error", "fm_kvq_destroy"]
 
 
 class FmConfig(ctypes.Structure):
@@ -73,6 +75,11 @@ class FmMtpConfig(ctypes.Structure):
                 ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("rot_dims", ctypes.c_int32),
                 ("theta", ctypes.c_float), ("eps", ctypes.c_float), ("vocab", ctypes.c_int32),
                 ("kv_cap", ctypes.c_int32), ("max_rows", ctypes.c_int32)]
+
+
+class FmKvqConfig(ctypes.Structure):
+    _fields_ = [("n_layers", ctypes.c_int32), ("n_seqs", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("max_rows", ctypes.c_int32)]
 
 
 class FmError(RuntimeError):
@@ -129,6 +136,18 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "fm_mtp_last_launch_count": (I32, [P, ctypes.POINTER(I32)]),
         "fm_mtp_last_error": (ctypes.c_char_p, [P]),
         "fm_mtp_destroy": (None, [P]),
+        "fm_kvq_create": (I32, [ctypes.POINTER(FmKvqConfig), P, ctypes.POINTER(P)]),
+        "fm_kvq_append": (I32, [P, I32, I32, P, P, P, P, P, I32, I64, P]),
+        "fm_kvq_read": (I32, [P, I32, I32, P, P, P, P, P, I32, I64, P, I64, P]),
+        "fm_kvq_attend": (I32, [P, I32, I32, P, P, P, I32, I32, I64, ctypes.c_float, I32, I32, P, I64, ctypes.c_float,
+                                P, I64, P]),
+        "fm_kvq_set_weights": (I32, [P, I32, I32, P, P, I64, P]),
+        "fm_kvq_evict": (I32, [P, I32, I32, P, P, I32, I32, P, P]),
+        "fm_kvq_length": (I32, [P, I32, I32, ctypes.POINTER(I32)]),
+        "fm_kvq_memory_bytes": (I32, [P, ctypes.POINTER(I64)]),
+        "fm_kvq_synchronize": (I32, [P, P]),
+        "fm_kvq_last_error": (ctypes.c_char_p, [P]),
+        "fm_kvq_destroy": (None, [P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -473,3 +492,159 @@ def fm_policy_after_round(p: FmVerifyPolicy, accepted: int, ms: float) -> None:
 
 def fm_policy_after_plain(p: FmVerifyPolicy, ms: float, rows_handed: bool) -> None:
     _check(load_library().fm_policy_after_plain(ctypes.byref(p), ms, 1 if rows_handed else 0))
+
+
+class KvqCache(ctypes.c_void_p):
+    """The handle of a 4-bit KV cache; freed by fm_kvq_destroy, or with the last reference to it."""
+
+    def __del__(self):
+        if self.value and _lib is not None:
+            _lib.fm_kvq_destroy(self)
+            self.value = None
+
+
+def _kvq_check(status: int, c=None):
+    if status != FM_OK:
+        lib = load_library()
+        raise FmError(status, f"{lib.fm_status_str(status).decode()}: {lib.fm_kvq_last_error(c).decode()}")
+
+
+def _ints(x, n: int, what: str):
+    """A host int32 array of n values for the library."""
+    if len(x) != n:
+        raise ValueError(f"{what}: {len(x)} values for {n} sequences")
+    return (ctypes.c_int32 * n)(*x)
+
+
+def _kvq_rows(x, rows: int, heads: Optional[int], head_dim: int, what: str):
+    """(pointer, dtype, heads, row stride) of a CUDA tensor [>= rows, heads, head_dim] whose rows are whole: the last
+    two axes contiguous, any stride between rows."""
+    import torch
+    dtype = {torch.float32: FM_DTYPE_F32, torch.float16: FM_DTYPE_F16, torch.bfloat16: FM_DTYPE_BF16}.get(x.dtype)
+    if dtype is None or not x.is_cuda:
+        raise ValueError(f"{what} must be a float32, float16 or bfloat16 CUDA tensor")
+    shape, stride = x.shape, x.stride()
+    if len(shape) != 3 or shape[2] != head_dim or (heads is not None and shape[1] != heads) or shape[0] < rows:
+        raise ValueError(f"{what} has shape {tuple(shape)}, expected [{rows}, {heads or 'heads'}, {head_dim}]")
+    if rows and (stride[2] != 1 or (shape[1] > 1 and stride[1] != head_dim)):
+        raise ValueError(f"{what}: a row's heads must be contiguous")
+    return x.data_ptr(), dtype, shape[1], stride[0] if shape[0] > 1 else shape[1] * head_dim
+
+
+def _kvq_weights(x, n: int, heads: int, what: str):
+    """(pointer, row stride) of a contiguous CUDA float32 tensor [n, heads, rows], or of None."""
+    import torch
+    if x is None:
+        return None, 0
+    if x.dtype != torch.float32 or not x.is_cuda or x.dim() != 3 or x.shape[0] != n or x.shape[1] != heads or \
+            not x.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous float32 CUDA tensor [{n}, {heads}, rows]")
+    return x.data_ptr(), x.shape[2]
+
+
+def fm_kvq_create(n_layers: int, n_seqs: int, n_kv_heads: int, head_dim: int, max_rows: int,
+                  stream=None) -> KvqCache:
+    """An empty KV cache held in 4 bits, on the current device."""
+    g = FmKvqConfig(n_layers, n_seqs, n_kv_heads, head_dim, max_rows)
+    c = KvqCache()
+    _kvq_check(load_library().fm_kvq_create(ctypes.byref(g), _stream(stream), ctypes.byref(c)))
+    c._kv_heads, c._head_dim = n_kv_heads, head_dim
+    return c
+
+
+def fm_kvq_append(c, layer: int, seq_ids: Sequence[int], k, v, n_rows: Sequence[int], starts: Sequence[int],
+                  stream=None) -> None:
+    """Rows k, v (CUDA tensors [sum(n_rows), n_kv_heads, head_dim], float32, float16 or bfloat16, packed in the order
+    of seq_ids) become rows starts[i] .. of their sequences; each length is then starts[i] + n_rows[i]."""
+    n, total = len(seq_ids), sum(n_rows)
+    kp, dtype, _, ld = _kvq_rows(k, total, c._kv_heads, c._head_dim, "k")
+    vp, vt, _, vld = _kvq_rows(v, total, c._kv_heads, c._head_dim, "v")
+    if vt != dtype or vld != ld:
+        raise ValueError("k and v differ in dtype or row stride")
+    _kvq_check(load_library().fm_kvq_append(c, layer, n, _ints(seq_ids, n, "seq_ids"), _ints(n_rows, n, "n_rows"),
+                                            _ints(starts, n, "starts"), kp, vp, dtype, ld, _stream(stream)), c)
+
+
+def fm_kvq_read(c, layer: int, seq_ids: Sequence[int], rows: Sequence[int], n_rows: Sequence[int], k=None, v=None,
+                weights=None, stream=None) -> None:
+    """The values of rows rows[i] .. rows[i] + n_rows[i] - 1 into k and v (CUDA tensors [sum(n_rows), n_kv_heads,
+    head_dim] or None), and their weights into weights (CUDA float32 [n_seqs, n_kv_heads, longest] or None)."""
+    n, total = len(seq_ids), sum(n_rows)
+    dtype, ld = FM_DTYPE_F32, c._kv_heads * c._head_dim
+    kp = vp = None
+    if k is not None:
+        kp, dtype, _, ld = _kvq_rows(k, total, c._kv_heads, c._head_dim, "k")
+    if v is not None:
+        vp, vt, _, vld = _kvq_rows(v, total, c._kv_heads, c._head_dim, "v")
+        if k is not None and (vt != dtype or vld != ld):
+            raise ValueError("k and v differ in dtype or row stride")
+        dtype, ld = vt, vld
+    wp, ldw = _kvq_weights(weights, n, c._kv_heads, "weights")
+    _kvq_check(load_library().fm_kvq_read(c, layer, n, _ints(seq_ids, n, "seq_ids"), _ints(rows, n, "rows"),
+                                          _ints(n_rows, n, "n_rows"), kp, vp, dtype, ld, wp, ldw, _stream(stream)), c)
+
+
+def fm_kvq_attend(c, layer: int, seq_ids: Sequence[int], q, n_rows: Sequence[int], out, scale: Optional[float] = None,
+                  causal: bool = False, first_row: int = 0, decay: Optional[float] = None, weights=None,
+                  stream=None) -> None:
+    """Attention of n_rows[i] query rows of each sequence over its cache rows first_row .. (causal: the rows are the
+    cache's last ones).  q, out: CUDA tensors [sum(n_rows), n_heads, head_dim] of one dtype (float32, float16,
+    bfloat16); n_heads a multiple of n_kv_heads; scale: 1 / sqrt(head_dim) unless given.  decay: None leaves the
+    rows' weights alone; a number d counts them, w = d w + this call's, into weights too (CUDA float32 [n_seqs,
+    n_kv_heads, rows] or None)."""
+    n, total = len(seq_ids), sum(n_rows)
+    qp, dtype, heads, ldq = _kvq_rows(q, total, None, c._head_dim, "q")
+    op, ot, _, ldo = _kvq_rows(out, total, heads, c._head_dim, "out")
+    if ot != dtype:
+        raise ValueError("q and out differ in dtype")
+    wp, ldw = _kvq_weights(weights, n, c._kv_heads, "weights")
+    _kvq_check(load_library().fm_kvq_attend(
+        c, layer, n, _ints(seq_ids, n, "seq_ids"), _ints(n_rows, n, "n_rows"), qp, dtype, heads, ldq,
+        c._head_dim ** -0.5 if scale is None else scale, 1 if causal else 0, first_row, op, ldo,
+        -1.0 if decay is None else decay, wp, ldw, _stream(stream)), c)
+
+
+def fm_kvq_set_weights(c, layer: int, seq_ids: Sequence[int], weights, stream=None) -> None:
+    """The weights of each sequence's rows from a CUDA float32 tensor [n_seqs, n_kv_heads, >= longest]."""
+    n = len(seq_ids)
+    wp, ldw = _kvq_weights(weights, n, c._kv_heads, "weights")
+    _kvq_check(load_library().fm_kvq_set_weights(c, layer, n, _ints(seq_ids, n, "seq_ids"), wp, ldw, _stream(stream)), c)
+
+
+def fm_kvq_evict(c, layer: int, src_ids: Sequence[int], dst_ids: Sequence[int], keep: int, recent: int, kept=None,
+                 stream=None) -> None:
+    """Bring sequences down to keep rows a KV head: the last `recent` and, of the others, those of the largest weight.
+    dst_ids[i] == src_ids[i] works in place.  kept: a contiguous CUDA int32 tensor [n_seqs, n_kv_heads, keep] that
+    receives the rows kept, or None."""
+    n = len(src_ids)
+    if kept is not None:
+        import torch
+        if kept.dtype != torch.int32 or not kept.is_cuda or not kept.is_contiguous() or \
+                tuple(kept.shape) != (n, c._kv_heads, keep):
+            raise ValueError(f"kept must be a contiguous int32 CUDA tensor [{n}, {c._kv_heads}, {keep}]")
+    _kvq_check(load_library().fm_kvq_evict(c, layer, n, _ints(src_ids, n, "src_ids"), _ints(dst_ids, n, "dst_ids"), keep,
+                                           recent, _ptr(kept), _stream(stream)), c)
+
+
+def fm_kvq_length(c, layer: int, seq: int) -> int:
+    v = ctypes.c_int32()
+    if load_library().fm_kvq_length(c, layer, seq, ctypes.byref(v)) != FM_OK:
+        raise FmError(FM_ERR_INVALID_ARG, f"layer {layer}, sequence {seq}")
+    return v.value
+
+
+def fm_kvq_memory_bytes(c) -> int:
+    v = ctypes.c_int64()
+    _kvq_check(load_library().fm_kvq_memory_bytes(c, ctypes.byref(v)), c)
+    return v.value
+
+
+def fm_kvq_synchronize(c, stream=None) -> None:
+    """Wait for the stream; raise FmError(FM_ERR_TIMEOUT) if a bounded device wait gave up since the last check."""
+    _kvq_check(load_library().fm_kvq_synchronize(c, _stream(stream)), c)
+
+
+def fm_kvq_destroy(c) -> None:
+    if c is not None and c.value:
+        load_library().fm_kvq_destroy(c)
+        c.value = None

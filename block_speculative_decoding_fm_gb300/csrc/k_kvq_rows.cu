@@ -1,0 +1,272 @@
+// k_kvq_rows.cu -- rows into the 4-bit KV cache and back out.
+//
+// A group of 32 values x gets the f16 scale d = f16(m / -8), m its value of
+// largest magnitude (the negative one on a tie), and codes
+// c = clamp(rint(x / d) + 8, 0, 15), ties to even, 8 where d = 0; it stands for
+// d (c - 8).  NaN counts as 0, infinities saturate (|d| <= 65504).
+//
+// The code is exact: c' = rint(x * (1 / d)) may be one off next to a border
+// because the reciprocal is rounded, so it is corrected against the borders
+// d (c' +- 1/2), which are exact in f32 (11-bit d times a 5-bit odd number).
+//
+// Bound by memory: a row of n values is read once (2 n or 4 n bytes) and
+// written as 0.5625 n bytes.  Four lanes share a group, eight consecutive values each
+// (one or two 16-byte loads; the lane's eight codes are one 32-bit word of the
+// group's 16-byte unit), and a thread has all its rows' loads in flight.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "dev_common.cuh"
+#include "kvq.h"
+
+namespace fm {
+namespace {
+
+constexpr int kThreads = 256;
+
+template <typename T>
+struct Eight;
+template <>
+struct Eight<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float *p) {
+    a = __ldg(reinterpret_cast<const float4 *>(p));
+    b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  }
+  static __device__ __forceinline__ void store(float *p, const float (&x)[8]) {
+    reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+  }
+};
+template <>
+struct Eight<__half> {
+  uint4 a;
+  __device__ __forceinline__ void load(const __half *p) { a = __ldg(reinterpret_cast<const uint4 *>(p)); }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w = word(a, i);
+      const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+      x[2 * i] = f.x, x[2 * i + 1] = f.y;
+    }
+  }
+  static __device__ __forceinline__ void store(__half *p, const float (&x)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+template <>
+struct Eight<__nv_bfloat16> {
+  uint4 a;
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p) { a = __ldg(reinterpret_cast<const uint4 *>(p)); }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w = word(a, i);
+      x[2 * i] = __uint_as_float(w << 16), x[2 * i + 1] = __uint_as_float(w & 0xffff0000u);
+    }
+  }
+  static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&x)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+
+// the sequence whose tiles hold x (n <= 64 prefix sums)
+__device__ __forceinline__ int find_seq(const int32_t *pre, int n, int x) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (pre[mid] <= x)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+
+// Grid (touched tile, KV head, K or V); thread = (row, eight values).
+template <int HD, typename T>
+__global__ void __launch_bounds__(kThreads) kvq_append_kernel(const __grid_constant__ KvqRowsArgs a) {
+  constexpr int O = HD / 8;                     // eights a row
+  constexpr int RP = kThreads / O;              // rows a pass of the block
+  constexpr int NP = kKvqTile / RP;
+  __shared__ float red[kThreads / 32];
+  pdl_trigger();
+  const int i = find_seq(a.tile0, a.n, blockIdx.x);
+  const int at = a.at[i], rows = a.rows[i];
+  const int tile = at / kKvqTile + (blockIdx.x - a.tile0[i]);
+  const int head = blockIdx.y;
+  const bool isv = blockIdx.z != 0;
+  const int o = threadIdx.x % O, r0 = threadIdx.x / O;
+  const size_t plane = (size_t)a.seq[i] * a.c.n_kv + head;
+  uint8_t *half_tile = a.c.planes + plane * a.c.plane_bytes + (size_t)tile * kvq_tile_bytes(HD) + (isv ? kvq_k_bytes(HD) : 0);
+  const T *src = static_cast<const T *>(isv ? a.v : a.k) + head * HD + o * 8;
+  pdl_wait();
+  Eight<T> in[NP];
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    const int r = tile * kKvqTile + p * RP + r0 - at;   // row of this sequence's input
+    if (r >= 0 && r < rows) in[p].load(src + (a.row0[i] + r) * a.ld);
+  }
+  float dmax = 0.f;
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    const int tr = p * RP + r0, r = tile * kKvqTile + tr - at;
+    const bool ok = r >= 0 && r < rows;
+    float x[8];
+    if (ok) {
+      in[p].get(x);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = 0.f;
+    }
+    float hi = -INFINITY, lo = INFINITY;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      x[e] = x[e] == x[e] ? x[e] : 0.f;
+      hi = fmaxf(hi, x[e]);
+      lo = fminf(lo, x[e]);
+    }
+#pragma unroll
+    for (int s = 1; s < 4; s <<= 1) {
+      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, s));
+      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, s));
+    }
+    const float m = hi > -lo ? hi : lo;
+    const __half dh = __float2half_rn(fminf(fmaxf(m * -0.125f, -65504.f), 65504.f));
+    const float d = __half2float(dh);
+    const float inv = d == 0.f ? 0.f : 1.f / d;
+    uint32_t w = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      // |x / d| <= 8 (1 + 2^-11) unless d was clamped or is subnormal: the first guess is clamped to +-9
+      float c = rintf(fminf(fmaxf(x[e] * inv, -9.f), 9.f));
+      // the borders of code c, in the units of |d|: exact products
+      const float xs = d < 0.f ? -x[e] : x[e], ad = fabsf(d);
+      const float up = ad * (c + 0.5f), dn = ad * (c - 0.5f);
+      const bool odd = (static_cast<int>(c) & 1) != 0;
+      if (xs > up || (xs == up && odd)) c += 1.f;
+      else if (xs < dn || (xs == dn && odd)) c -= 1.f;
+      const int code = d == 0.f ? 8 : min(15, max(0, static_cast<int>(c) + 8));
+      w |= (uint32_t)code << (4 * e);
+    }
+    if (!ok) continue;
+    *reinterpret_cast<uint32_t *>(half_tile + kvq_unit(tr, o >> 2, HD) + (o & 3) * 4) = w;
+    if ((o & 3) == 0) *reinterpret_cast<__half *>(half_tile + kvq_scale(tr, o >> 2, HD)) = dh;
+    if (!isv && o == 0) a.c.weights[plane * a.c.rows_pad + tile * kKvqTile + tr] = 0.f;
+    dmax = fmaxf(dmax, fabsf(d));
+  }
+  if (isv) {   // the plane's largest |V scale| (an upper bound that only grows: the order of the CTAs is no matter)
+    dmax = warp_max(dmax);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = dmax;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+#pragma unroll
+      for (int j = 1; j < kThreads / 32; ++j) dmax = fmaxf(dmax, red[j]);
+      atomicMax(a.c.vmax + plane, __float_as_uint(dmax));
+    }
+  }
+}
+
+// The values the codes stand for, d (c - 8), rounded once to T.
+template <int HD, typename T>
+__global__ void __launch_bounds__(kThreads) kvq_read_kernel(const __grid_constant__ KvqRowsArgs a) {
+  constexpr int O = HD / 8, RP = kThreads / O, NP = kKvqTile / RP;
+  pdl_trigger();
+  const int i = find_seq(a.tile0, a.n, blockIdx.x);
+  const int at = a.at[i], rows = a.rows[i];
+  const int tile = at / kKvqTile + (blockIdx.x - a.tile0[i]);
+  const int head = blockIdx.y;
+  const bool isv = blockIdx.z != 0;
+  const int o = threadIdx.x % O, r0 = threadIdx.x / O;
+  const size_t plane = (size_t)a.seq[i] * a.c.n_kv + head;
+  const uint8_t *half_tile =
+      a.c.planes + plane * a.c.plane_bytes + (size_t)tile * kvq_tile_bytes(HD) + (isv ? kvq_k_bytes(HD) : 0);
+  T *dst = static_cast<T *>(isv ? a.vo : a.ko);
+  pdl_wait();
+  if (a.wo && !isv && threadIdx.x < kKvqTile) {
+    const int r = tile * kKvqTile + threadIdx.x - at;
+    if (r >= 0 && r < rows)
+      a.wo[((size_t)(a.call0 + i) * a.c.n_kv + head) * a.ldw + r] =
+          a.c.weights[plane * a.c.rows_pad + tile * kKvqTile + threadIdx.x];
+  }
+  if (!dst) return;
+  dst += head * HD + o * 8;
+  uint32_t w[NP];
+  __half d[NP];
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    const int tr = p * RP + r0;
+    w[p] = *reinterpret_cast<const uint32_t *>(half_tile + kvq_unit(tr, o >> 2, HD) + (o & 3) * 4);
+    d[p] = *reinterpret_cast<const __half *>(half_tile + kvq_scale(tr, o >> 2, HD));
+  }
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    const int r = tile * kKvqTile + p * RP + r0 - at;
+    if (r < 0 || r >= rows) continue;
+    const float f = __half2float(d[p]);
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = f * static_cast<float>(static_cast<int>((w[p] >> (4 * e)) & 15u) - 8);
+    Eight<T>::store(dst + (a.row0[i] + r) * a.ld, x);
+  }
+}
+
+// weights in: cache rows [0, rows[i]) of each sequence
+__global__ void __launch_bounds__(kThreads) kvq_set_weights_kernel(const __grid_constant__ KvqRowsArgs a) {
+  pdl_trigger();
+  const int i = blockIdx.z, head = blockIdx.y;
+  const int r = blockIdx.x * kThreads + threadIdx.x;
+  pdl_wait();
+  if (r < a.rows[i])
+    a.c.weights[((size_t)a.seq[i] * a.c.n_kv + head) * a.c.rows_pad + r] =
+        a.wi[((size_t)(a.call0 + i) * a.c.n_kv + head) * a.ldw + r];
+}
+
+template <int HD>
+cudaError_t append_hd(const KvqRowsArgs &a, dim3 grid, cudaStream_t s) {
+  if (a.type == KVQ_F32) return kvq_launch(kvq_append_kernel<HD, float>, grid, dim3(kThreads), 0, s, a);
+  if (a.type == KVQ_F16) return kvq_launch(kvq_append_kernel<HD, __half>, grid, dim3(kThreads), 0, s, a);
+  return kvq_launch(kvq_append_kernel<HD, __nv_bfloat16>, grid, dim3(kThreads), 0, s, a);
+}
+template <int HD>
+cudaError_t read_hd(const KvqRowsArgs &a, dim3 grid, cudaStream_t s) {
+  if (a.type == KVQ_F32) return kvq_launch(kvq_read_kernel<HD, float>, grid, dim3(kThreads), 0, s, a);
+  if (a.type == KVQ_F16) return kvq_launch(kvq_read_kernel<HD, __half>, grid, dim3(kThreads), 0, s, a);
+  return kvq_launch(kvq_read_kernel<HD, __nv_bfloat16>, grid, dim3(kThreads), 0, s, a);
+}
+
+}  // namespace
+
+cudaError_t launch_kvq_append(const KvqRowsArgs &a, int hd, cudaStream_t s) {
+  const dim3 grid(a.tiles, a.c.n_kv, 2);
+  return hd == 64 ? append_hd<64>(a, grid, s) : hd == 128 ? append_hd<128>(a, grid, s) : append_hd<256>(a, grid, s);
+}
+
+cudaError_t launch_kvq_read(const KvqRowsArgs &a, int hd, cudaStream_t s) {
+  const dim3 grid(a.tiles, a.c.n_kv, 2);
+  return hd == 64 ? read_hd<64>(a, grid, s) : hd == 128 ? read_hd<128>(a, grid, s) : read_hd<256>(a, grid, s);
+}
+
+cudaError_t launch_kvq_set_weights(const KvqRowsArgs &a, cudaStream_t s) {
+  int most = 0;
+  for (int i = 0; i < a.n; ++i) most = a.rows[i] > most ? a.rows[i] : most;
+  if (most == 0) return cudaSuccess;
+  return kvq_launch(kvq_set_weights_kernel, dim3((most + kThreads - 1) / kThreads, a.c.n_kv, a.n), dim3(kThreads), 0, s, a);
+}
+
+}  // namespace fm

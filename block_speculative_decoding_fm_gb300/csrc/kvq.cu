@@ -1,0 +1,585 @@
+// kvq.cu -- the 4-bit KV cache's host calls: argument checks, the lengths, the
+// split of a call's work over the SMs, the launches (k_kvq_rows.cu,
+// k_kvq_attn.cu, k_kvq_evict.cu).
+//
+// Every value that a call needs on the device rides in the kernels' argument
+// blocks (64 sequences a launch), so nothing is copied or allocated after
+// fm_kvq_create and a call can be captured into a graph.
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+#include <cstring>
+#include <new>
+#include <vector>
+
+#include "../../include/fm.h"
+#include "kvq.h"
+
+using namespace fm;
+
+struct fm_kvq {
+  fm_kvq_config cfg{};
+  int device = 0, n_sm = 0;
+  int ctas[3] = {1, 1, 1};        // attention CTAs an SM holds, by type
+  int rows_pad = 0;
+  size_t plane_bytes = 0;
+  uint8_t *planes = nullptr;
+  float *weights = nullptr, *part_o = nullptr, *lse = nullptr;
+  uint32_t *vmax = nullptr;
+  float2 *part_ml = nullptr;
+  int32_t *list = nullptr, *dev_err = nullptr;
+  int slots = 0;                  // partial results the workspace holds
+  int64_t bytes = 0;
+  std::vector<int32_t> len;       // [layers][seqs]
+  std::vector<uint32_t> mark;     // [seqs] the last call that named a sequence (as a destination)
+  uint32_t call = 0;
+  cudaEvent_t done = nullptr;     // the last eager call's work
+  cudaStream_t last = nullptr;
+  bool has_last = false;
+  char err[512] = "";
+};
+
+namespace {
+
+constexpr int kMaxUnits = 1 << 16;   // (row tile, KV head) units of a call that keeps weights, per launch
+constexpr int kMaxRows = 1 << 24;
+
+thread_local char g_kvq_error[512] = "";
+
+fm_status kfail(fm_kvq *c, fm_status s, const char *fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(c ? c->err : g_kvq_error, sizeof g_kvq_error, fmt, ap);
+  va_end(ap);
+  return s;
+}
+
+#define KCK(expr)                                                                                 \
+  do {                                                                                            \
+    cudaError_t e_ = (expr);                                                                      \
+    if (e_ != cudaSuccess) return kfail(c, FM_ERR_CUDA, "%s: %s", #expr, cudaGetErrorString(e_)); \
+  } while (0)
+#define KTRY(expr)          \
+  do {                      \
+    fm_status s_ = (expr);  \
+    if (s_ != FM_OK) return s_; \
+  } while (0)
+
+int32_t *lengths(fm_kvq *c, int layer) { return c->len.data() + (size_t)layer * c->cfg.n_seqs; }
+
+KvqCache view(const fm_kvq *c, int layer) {
+  const size_t p0 = (size_t)layer * c->cfg.n_seqs * c->cfg.n_kv_heads;
+  KvqCache v;
+  v.planes = c->planes + p0 * c->plane_bytes;
+  v.plane_bytes = c->plane_bytes;
+  v.weights = c->weights + p0 * c->rows_pad;
+  v.vmax = c->vmax + p0;
+  v.rows_pad = c->rows_pad;
+  v.n_kv = c->cfg.n_kv_heads;
+  v.err = c->dev_err;
+  return v;
+}
+
+// the checks that every call begins with
+fm_status check_call(fm_kvq *c, int layer, int n, const int32_t *ids) {
+  int dev = -1;
+  KCK(cudaGetDevice(&dev));
+  if (dev != c->device) return kfail(c, FM_ERR_INVALID_ARG, "the current device is %d, the cache's is %d", dev, c->device);
+  if (layer < 0 || layer >= c->cfg.n_layers)
+    return kfail(c, FM_ERR_INVALID_ARG, "layer %d outside [0, %d)", layer, c->cfg.n_layers);
+  if (n < 1 || n > c->cfg.n_seqs) return kfail(c, FM_ERR_INVALID_ARG, "n_seqs %d outside [1, %d]", n, c->cfg.n_seqs);
+  if (!ids) return kfail(c, FM_ERR_INVALID_ARG, "null sequence ids");
+  for (int i = 0; i < n; ++i)
+    if (ids[i] < 0 || ids[i] >= c->cfg.n_seqs)
+      return kfail(c, FM_ERR_INVALID_ARG, "sequence %d outside [0, %d)", ids[i], c->cfg.n_seqs);
+  return FM_OK;
+}
+
+uint32_t next_call(fm_kvq *c) {
+  if (++c->call == 0) {   // wrapped: no old mark may look new
+    std::fill(c->mark.begin(), c->mark.end(), 0u);
+    c->call = 1;
+  }
+  return c->call;
+}
+
+fm_status check_distinct(fm_kvq *c, int n, const int32_t *ids) {
+  const uint32_t call = next_call(c);
+  for (int i = 0; i < n; ++i) {
+    if (c->mark[ids[i]] == call) return kfail(c, FM_ERR_INVALID_ARG, "sequence %d named twice", ids[i]);
+    c->mark[ids[i]] = call;
+  }
+  return FM_OK;
+}
+
+fm_status type_of(fm_kvq *c, int dtype, int32_t *type, int *size) {
+  switch (dtype) {
+    case FM_DTYPE_F32: *type = KVQ_F32, *size = 4; return FM_OK;
+    case FM_DTYPE_F16: *type = KVQ_F16, *size = 2; return FM_OK;
+    case FM_DTYPE_BF16: *type = KVQ_BF16, *size = 2; return FM_OK;
+  }
+  return kfail(c, FM_ERR_INVALID_ARG, "dtype %d: f32, f16 or bf16", dtype);
+}
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+fm_status check_rows(fm_kvq *c, const char *what, const void *p, int64_t ld, int64_t width, int size) {
+  if (!p || !aligned16(p)) return kfail(c, FM_ERR_INVALID_ARG, "%s: a null or misaligned pointer (16 bytes)", what);
+  if (ld < width || (ld * size) % 16)
+    return kfail(c, FM_ERR_INVALID_ARG, "%s: row stride %lld (at least %lld, whole 16 bytes)", what, (long long)ld,
+                 (long long)width);
+  return FM_OK;
+}
+
+// Calls share the lengths' rows, the weights and the workspace, so work that
+// another stream was given earlier comes first.  (A captured call cannot wait
+// for eager work, nor eager work for a graph: the caller orders those.)
+bool capturing(cudaStream_t s) {
+  cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(s, &st) != cudaSuccess) {
+    cudaGetLastError();
+    return true;
+  }
+  return st != cudaStreamCaptureStatusNone;
+}
+
+fm_status begin(fm_kvq *c, cudaStream_t s) {
+  if (c->has_last && c->last != s && !capturing(s)) KCK(cudaStreamWaitEvent(s, c->done, 0));
+  return FM_OK;
+}
+
+fm_status end(fm_kvq *c, cudaStream_t s) {
+  if (capturing(s)) return FM_OK;
+  KCK(cudaEventRecord(c->done, s));
+  c->last = s;
+  c->has_last = true;
+  return FM_OK;
+}
+
+template <typename T>
+fm_status dev_alloc(fm_kvq *c, T **p, size_t n) {
+  void *q = nullptr;
+  const size_t b = (n ? n : 1) * sizeof(T);
+  if (cudaMalloc(&q, b) != cudaSuccess) {
+    cudaGetLastError();
+    return kfail(c, FM_ERR_OOM, "device allocation of %zu bytes failed", b);
+  }
+  *p = static_cast<T *>(q);
+  c->bytes += (int64_t)b;
+  return FM_OK;
+}
+
+void release(fm_kvq *c) {
+  for (void *p : {(void *)c->planes, (void *)c->weights, (void *)c->part_o, (void *)c->lse, (void *)c->vmax,
+                  (void *)c->part_ml, (void *)c->list, (void *)c->dev_err})
+    if (p) cudaFree(p);
+  if (c->done) cudaEventDestroy(c->done);
+  delete c;
+}
+
+fm_status setup(fm_kvq *c, cudaStream_t s) {
+  const fm_kvq_config &g = c->cfg;
+  KCK(cudaGetDevice(&c->device));
+  KCK(cudaDeviceGetAttribute(&c->n_sm, cudaDevAttrMultiProcessorCount, c->device));
+  c->rows_pad = (g.max_rows + kKvqTile - 1) / kKvqTile * kKvqTile;
+  c->plane_bytes = (size_t)(c->rows_pad / kKvqTile) * kvq_tile_bytes(g.head_dim);
+  const size_t planes = (size_t)g.n_layers * g.n_seqs * g.n_kv_heads;
+  int most = 1;
+  for (int t = 0; t < 3; ++t) {
+    c->ctas[t] = kvq_attn_ctas_per_sm(g.head_dim, t);
+    most = c->ctas[t] > most ? c->ctas[t] : most;
+  }
+  c->slots = 2 * c->n_sm * most + 2 * g.n_kv_heads;
+  KTRY(dev_alloc(c, &c->planes, planes * c->plane_bytes));
+  KTRY(dev_alloc(c, &c->weights, planes * c->rows_pad));
+  KTRY(dev_alloc(c, &c->vmax, planes));
+  KTRY(dev_alloc(c, &c->part_o, (size_t)c->slots * kKvqQRows * g.head_dim));
+  KTRY(dev_alloc(c, &c->part_ml, (size_t)c->slots * kKvqQRows));
+  KTRY(dev_alloc(c, &c->lse, (size_t)kMaxUnits * kKvqQRows));
+  KTRY(dev_alloc(c, &c->list, (size_t)(g.n_seqs < kKvqSeqs ? g.n_seqs : kKvqSeqs) * g.n_kv_heads * c->rows_pad));
+  KTRY(dev_alloc(c, &c->dev_err, 4));
+  // rows behind a sequence's end are read with the last tile: they hold finite values from the start
+  KCK(cudaMemsetAsync(c->planes, 0, planes * c->plane_bytes, s));
+  KCK(cudaMemsetAsync(c->weights, 0, planes * c->rows_pad * sizeof(float), s));
+  KCK(cudaMemsetAsync(c->vmax, 0, planes * sizeof(uint32_t), s));
+  KCK(cudaMemsetAsync(c->dev_err, 0, 16, s));
+  KCK(cudaEventCreateWithFlags(&c->done, cudaEventDisableTiming));
+  KCK(cudaStreamSynchronize(s));
+  return FM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+fm_status fm_kvq_create(const fm_kvq_config *cfg, void *stream, fm_kvq **out) {
+  if (!out) return kfail(nullptr, FM_ERR_INVALID_ARG, "null out");
+  *out = nullptr;
+  if (!cfg) return kfail(nullptr, FM_ERR_INVALID_ARG, "null config");
+  const fm_kvq_config g = *cfg;
+  if (g.head_dim != 64 && g.head_dim != 128 && g.head_dim != 256)
+    return kfail(nullptr, FM_ERR_UNSUPPORTED, "head_dim %d: 64, 128 or 256", g.head_dim);
+  if (g.n_layers < 1 || g.n_layers > 1024 || g.n_seqs < 1 || g.n_seqs > 65536 || g.n_kv_heads < 1 || g.n_kv_heads > 1024 ||
+      g.max_rows < 1 || g.max_rows > kMaxRows)
+    return kfail(nullptr, FM_ERR_INVALID_ARG, "n_layers %d, n_seqs %d, n_kv_heads %d or max_rows %d out of range", g.n_layers,
+                 g.n_seqs, g.n_kv_heads, g.max_rows);
+  fm_kvq *c = new (std::nothrow) fm_kvq();
+  if (!c) return kfail(nullptr, FM_ERR_OOM, "host allocation failed");
+  c->cfg = g;
+  fm_status st;
+  try {
+    c->len.assign((size_t)g.n_layers * g.n_seqs, 0);
+    c->mark.assign(g.n_seqs, 0u);
+    st = setup(c, static_cast<cudaStream_t>(stream));
+  } catch (const std::bad_alloc &) {
+    st = kfail(c, FM_ERR_OOM, "host allocation failed");
+  }
+  if (st != FM_OK) {
+    memcpy(g_kvq_error, c->err, sizeof c->err);
+    release(c);
+    return st;
+  }
+  *out = c;
+  return FM_OK;
+}
+
+fm_status fm_kvq_append(fm_kvq *c, int32_t layer, int32_t n_seqs, const int32_t *seq_ids_host, const int32_t *n_rows_host,
+                        const int32_t *start_host, const void *k_dev, const void *v_dev, int32_t dtype, int64_t ld,
+                        void *stream) {
+  if (!c) return FM_ERR_INVALID_ARG;
+  KTRY(check_call(c, layer, n_seqs, seq_ids_host));
+  if (!n_rows_host || !start_host) return kfail(c, FM_ERR_INVALID_ARG, "null row counts or starts");
+  KTRY(check_distinct(c, n_seqs, seq_ids_host));
+  int32_t type;
+  int size;
+  KTRY(type_of(c, dtype, &type, &size));
+  int32_t *len = lengths(c, layer);
+  int64_t total = 0;
+  for (int i = 0; i < n_seqs; ++i) {
+    const int s = seq_ids_host[i];
+    if (n_rows_host[i] < 0) return kfail(c, FM_ERR_INVALID_ARG, "sequence %d: %d rows", s, n_rows_host[i]);
+    if (start_host[i] < 0 || start_host[i] > len[s])
+      return kfail(c, FM_ERR_STATE, "sequence %d: start %d, length %d", s, start_host[i], len[s]);
+    if ((int64_t)start_host[i] + n_rows_host[i] > c->cfg.max_rows)
+      return kfail(c, FM_ERR_CONTEXT_FULL, "sequence %d: %d + %d rows, the cache holds %d", s, start_host[i], n_rows_host[i],
+                   c->cfg.max_rows);
+    total += n_rows_host[i];
+  }
+  const int64_t width = (int64_t)c->cfg.n_kv_heads * c->cfg.head_dim;
+  if (total > 0) {
+    KTRY(check_rows(c, "k", k_dev, ld, width, size));
+    KTRY(check_rows(c, "v", v_dev, ld, width, size));
+  }
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  KTRY(begin(c, s));
+  KvqRowsArgs a;
+  memset(&a, 0, sizeof a);
+  a.c = view(c, layer);
+  a.k = k_dev;
+  a.v = v_dev;
+  a.ld = ld;
+  a.type = type;
+  int64_t row0 = 0;
+  for (int i0 = 0; i0 < n_seqs; i0 += kKvqSeqs) {
+    a.n = 0;
+    a.tiles = 0;
+    for (int i = i0; i < n_seqs && i < i0 + kKvqSeqs; ++i) {
+      const int n = n_rows_host[i], at = start_host[i];
+      if (n > 0) {
+        a.seq[a.n] = seq_ids_host[i];
+        a.at[a.n] = at;
+        a.rows[a.n] = n;
+        a.row0[a.n] = row0;
+        a.tile0[a.n++] = a.tiles;
+        a.tiles += (at + n - 1) / kKvqTile - at / kKvqTile + 1;
+        row0 += n;
+      }
+    }
+    a.tile0[a.n] = a.tiles;
+    if (a.n) KCK(launch_kvq_append(a, c->cfg.head_dim, s));
+    for (int i = i0; i < n_seqs && i < i0 + kKvqSeqs; ++i) len[seq_ids_host[i]] = start_host[i] + n_rows_host[i];
+  }
+  return end(c, s);
+}
+
+fm_status fm_kvq_read(fm_kvq *c, int32_t layer, int32_t n_seqs, const int32_t *seq_ids_host, const int32_t *row_host,
+                      const int32_t *n_rows_host, void *k_dev, void *v_dev, int32_t dtype, int64_t ld, float *weights_dev,
+                      int64_t ldw, void *stream) {
+  if (!c) return FM_ERR_INVALID_ARG;
+  KTRY(check_call(c, layer, n_seqs, seq_ids_host));
+  if (!n_rows_host || !row_host) return kfail(c, FM_ERR_INVALID_ARG, "null row counts or first rows");
+  int32_t type;
+  int size;
+  KTRY(type_of(c, dtype, &type, &size));
+  const int32_t *len = lengths(c, layer);
+  int64_t total = 0;
+  int most = 0;
+  for (int i = 0; i < n_seqs; ++i) {
+    const int s = seq_ids_host[i];
+    if (n_rows_host[i] < 0 || row_host[i] < 0 || (int64_t)row_host[i] + n_rows_host[i] > len[s])
+      return kfail(c, FM_ERR_INVALID_ARG, "sequence %d: rows %d + %d, length %d", s, row_host[i], n_rows_host[i], len[s]);
+    total += n_rows_host[i];
+    most = n_rows_host[i] > most ? n_rows_host[i] : most;
+  }
+  const int64_t width = (int64_t)c->cfg.n_kv_heads * c->cfg.head_dim;
+  if (total > 0) {
+    if (k_dev) KTRY(check_rows(c, "k", k_dev, ld, width, size));
+    if (v_dev) KTRY(check_rows(c, "v", v_dev, ld, width, size));
+    if (weights_dev && ldw < most)
+      return kfail(c, FM_ERR_INVALID_ARG, "weights: row stride %lld, %d rows", (long long)ldw, most);
+    if (!k_dev && !v_dev && !weights_dev) return kfail(c, FM_ERR_INVALID_ARG, "nothing to read into");
+  }
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  KTRY(begin(c, s));
+  KvqRowsArgs a;
+  memset(&a, 0, sizeof a);
+  a.c = view(c, layer);
+  a.ko = k_dev;
+  a.vo = v_dev;
+  a.ld = ld;
+  a.type = type;
+  a.wo = weights_dev;
+  a.ldw = ldw;
+  int64_t row0 = 0;
+  for (int i0 = 0; i0 < n_seqs; i0 += kKvqSeqs) {
+    a.n = 0;
+    a.tiles = 0;
+    a.call0 = i0;
+    // (every sequence keeps its place: the weights' rows go by it)
+    for (int i = i0; i < n_seqs && i < i0 + kKvqSeqs; ++i) {
+      const int n = n_rows_host[i], at = row_host[i];
+      a.seq[a.n] = seq_ids_host[i];
+      a.at[a.n] = at;
+      a.rows[a.n] = n;
+      a.row0[a.n] = row0;
+      a.tile0[a.n++] = a.tiles;
+      if (n > 0) a.tiles += (at + n - 1) / kKvqTile - at / kKvqTile + 1;
+      row0 += n;
+    }
+    a.tile0[a.n] = a.tiles;
+    if (a.tiles) KCK(launch_kvq_read(a, c->cfg.head_dim, s));
+  }
+  return end(c, s);
+}
+
+fm_status fm_kvq_set_weights(fm_kvq *c, int32_t layer, int32_t n_seqs, const int32_t *seq_ids_host, const float *weights_dev,
+                             int64_t ldw, void *stream) {
+  if (!c) return FM_ERR_INVALID_ARG;
+  KTRY(check_call(c, layer, n_seqs, seq_ids_host));
+  KTRY(check_distinct(c, n_seqs, seq_ids_host));
+  const int32_t *len = lengths(c, layer);
+  int most = 0;
+  for (int i = 0; i < n_seqs; ++i) most = len[seq_ids_host[i]] > most ? len[seq_ids_host[i]] : most;
+  if (most > 0 && (!weights_dev || ldw < most))
+    return kfail(c, FM_ERR_INVALID_ARG, "weights: null, or row stride %lld with %d rows", (long long)ldw, most);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  KTRY(begin(c, s));
+  KvqRowsArgs a;
+  memset(&a, 0, sizeof a);
+  a.c = view(c, layer);
+  a.wi = weights_dev;
+  a.ldw = ldw;
+  for (int i0 = 0; i0 < n_seqs; i0 += kKvqSeqs) {
+    a.n = 0;
+    a.call0 = i0;
+    for (int i = i0; i < n_seqs && i < i0 + kKvqSeqs; ++i) {
+      a.seq[a.n] = seq_ids_host[i];
+      a.rows[a.n++] = len[seq_ids_host[i]];
+    }
+    KCK(launch_kvq_set_weights(a, s));
+  }
+  return end(c, s);
+}
+
+fm_status fm_kvq_attend(fm_kvq *c, int32_t layer, int32_t n_seqs, const int32_t *seq_ids_host, const int32_t *n_rows_host,
+                        const void *q_dev, int32_t dtype, int32_t n_heads, int64_t ldq, float scale, int32_t causal,
+                        int32_t first_row, void *out_dev, int64_t ldo, float decay, float *weights_dev, int64_t ldw,
+                        void *stream) {
+  if (!c) return FM_ERR_INVALID_ARG;
+  KTRY(check_call(c, layer, n_seqs, seq_ids_host));
+  if (!n_rows_host) return kfail(c, FM_ERR_INVALID_ARG, "null row counts");
+  int32_t type;
+  int size;
+  KTRY(type_of(c, dtype, &type, &size));
+  const int nkv = c->cfg.n_kv_heads, hd = c->cfg.head_dim;
+  if (n_heads < 1 || n_heads % nkv || n_heads / nkv > 1024)
+    return kfail(c, FM_ERR_INVALID_ARG, "%d query heads over %d KV heads", n_heads, nkv);
+  if (!std::isfinite(scale)) return kfail(c, FM_ERR_INVALID_ARG, "scale is not finite");
+  if (first_row < 0) return kfail(c, FM_ERR_INVALID_ARG, "first_row %d", first_row);
+  if (!(decay == decay) || std::isinf(decay)) return kfail(c, FM_ERR_INVALID_ARG, "decay is not finite");
+  const bool keep_w = decay >= 0.f;
+  if (!keep_w && weights_dev) return kfail(c, FM_ERR_INVALID_ARG, "weights wanted, but decay < 0 keeps none");
+  if (keep_w) KTRY(check_distinct(c, n_seqs, seq_ids_host));
+  const int32_t *len = lengths(c, layer);
+  const int group = n_heads / nkv;
+  int64_t total = 0;
+  int most = 0;
+  for (int i = 0; i < n_seqs; ++i) {
+    const int n = n_rows_host[i];
+    if (n < 0 || n > (1 << 16)) return kfail(c, FM_ERR_INVALID_ARG, "sequence %d: %d query rows", seq_ids_host[i], n);
+    const int64_t units = ((int64_t)n * group + kKvqQRows - 1) / kKvqQRows * nkv;
+    if (units > kMaxUnits)
+      return kfail(c, FM_ERR_UNSUPPORTED, "sequence %d: %d query rows of %d heads in one call", seq_ids_host[i], n, n_heads);
+    total += n;
+    if (n > 0 && len[seq_ids_host[i]] > most) most = len[seq_ids_host[i]];
+  }
+  const int64_t width = (int64_t)n_heads * hd;
+  if (total > 0) {
+    KTRY(check_rows(c, "q", q_dev, ldq, width, size));
+    KTRY(check_rows(c, "out", out_dev, ldo, width, size));
+    if (weights_dev && ldw < most)
+      return kfail(c, FM_ERR_INVALID_ARG, "weights: row stride %lld, %d rows", (long long)ldw, most);
+  }
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  KTRY(begin(c, s));
+  KvqAttnArgs a;
+  memset(&a, 0, sizeof a);
+  a.c = view(c, layer);
+  a.q = q_dev;
+  a.out = out_dev;
+  a.ldq = ldq;
+  a.ldo = ldo;
+  a.type = type;
+  a.group = group;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.causal = causal != 0;
+  a.first = first_row;
+  a.part_o = c->part_o;
+  a.part_ml = c->part_ml;
+  a.lse = keep_w ? c->lse : nullptr;
+  a.decay = decay;
+  a.w_out = weights_dev;
+  a.ldw = ldw;
+  int64_t row0 = 0;
+  for (int i0 = 0; i0 < n_seqs;) {
+    // the sequences of this launch: 64, and as many units as the workspace has row sums for
+    int64_t units = 0, work = 0;   // work: tiles x units
+    a.n = 0;
+    a.call0 = i0;
+    int i = i0;
+    for (; i < n_seqs && a.n < kKvqSeqs; ++i) {
+      const int n = n_rows_host[i], L = len[seq_ids_host[i]];
+      const int64_t rts = ((int64_t)n * group + kKvqQRows - 1) / kKvqQRows;
+      if (a.n && (units + rts * nkv > kMaxUnits)) break;
+      a.seq[a.n] = seq_ids_host[i];
+      a.len[a.n] = L;
+      a.rows[a.n] = n;
+      a.row0[a.n++] = row0;
+      row0 += n;
+      units += rts * nkv;
+      const int t0 = first_row / kKvqTile, t1 = (L + kKvqTile - 1) / kKvqTile;
+      if (t1 > t0) work += rts * nkv * (t1 - t0);
+    }
+    // Tiles a CTA: the SMs filled once.  Two tiles (a stage) at least, and whole stages; a unit that is
+    // split has two chunks or more, so the chunks of split units are at most twice the aim.
+    const int64_t aim = (int64_t)c->n_sm * c->ctas[type];
+    int64_t chunk = (work + aim - 1) / aim;
+    chunk = chunk < 2 ? 2 : (chunk + 1) / 2 * 2;
+    a.chunk = (int32_t)(chunk > INT_MAX / 2 ? INT_MAX / 2 : chunk);
+    int ctas = 0, un = 0, slot = 0, split = 0, wt = 0;
+    for (int j = 0; j < a.n; ++j) {
+      const int rts = (int)(((int64_t)a.rows[j] * group + kKvqQRows - 1) / kKvqQRows);
+      const int t1 = (a.len[j] + kKvqTile - 1) / kKvqTile;
+      int tiles = t1 - first_row / kKvqTile;
+      if (tiles < 0) tiles = 0;
+      int chunks = (tiles + a.chunk - 1) / a.chunk;
+      if (chunks < 1) chunks = 1;
+      a.cta0[j] = ctas;
+      a.unit0[j] = un;
+      a.slot0[j] = slot;
+      a.split0[j] = split;
+      a.wt0[j] = wt;
+      ctas += chunks * rts;
+      un += rts;
+      if (chunks > 1) {
+        slot += chunks * rts;
+        split += rts;
+      }
+      if (rts > 0) wt += (t1 + kKvqWeightTiles - 1) / kKvqWeightTiles;
+    }
+    a.cta0[a.n] = ctas;
+    a.unit0[a.n] = un;
+    a.slot0[a.n] = slot;
+    a.split0[a.n] = split;
+    a.wt0[a.n] = wt;
+    if ((int64_t)slot * nkv > c->slots) return kfail(c, FM_ERR_UNSUPPORTED, "more partial results than the workspace holds");
+    if (ctas > 0) KCK(launch_kvq_attend(a, hd, s));
+    if (split > 0) KCK(launch_kvq_merge(a, hd, s));
+    if (keep_w && wt > 0) KCK(launch_kvq_weights(a, hd, s));
+    i0 = i;
+  }
+  return end(c, s);
+}
+
+fm_status fm_kvq_evict(fm_kvq *c, int32_t layer, int32_t n_seqs, const int32_t *src_ids_host, const int32_t *dst_ids_host,
+                       int32_t keep, int32_t recent, int32_t *kept_dev, void *stream) {
+  if (!c) return FM_ERR_INVALID_ARG;
+  KTRY(check_call(c, layer, n_seqs, src_ids_host));
+  KTRY(check_call(c, layer, n_seqs, dst_ids_host));
+  if (keep < 0 || keep > c->cfg.max_rows || recent < 0 || recent > keep)
+    return kfail(c, FM_ERR_INVALID_ARG, "keep %d (of at most %d), recent %d", keep, c->cfg.max_rows, recent);
+  KTRY(check_distinct(c, n_seqs, dst_ids_host));
+  // a sequence that is written is read by its own move alone
+  for (int i = 0; i < n_seqs; ++i)
+    if (src_ids_host[i] != dst_ids_host[i] && c->mark[src_ids_host[i]] == c->call)
+      return kfail(c, FM_ERR_INVALID_ARG, "sequence %d is read and written", src_ids_host[i]);
+  int32_t *len = lengths(c, layer);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  KTRY(begin(c, s));
+  KvqEvictArgs a;
+  memset(&a, 0, sizeof a);
+  a.c = view(c, layer);
+  a.keep = keep;
+  a.recent = recent;
+  a.kept = kept_dev;
+  a.list = c->list;
+  for (int i0 = 0; i0 < n_seqs; i0 += kKvqSeqs) {
+    a.n = 0;
+    a.call0 = i0;
+    for (int i = i0; i < n_seqs && i < i0 + kKvqSeqs; ++i) {
+      a.src[a.n] = src_ids_host[i];
+      a.dst[a.n] = dst_ids_host[i];
+      a.len[a.n++] = len[src_ids_host[i]];
+    }
+    KCK(launch_kvq_evict(a, c->cfg.head_dim, s));
+    for (int j = 0; j < a.n; ++j) len[a.dst[j]] = a.len[j] < keep ? a.len[j] : keep;
+  }
+  return end(c, s);
+}
+
+fm_status fm_kvq_length(const fm_kvq *c, int32_t layer, int32_t seq, int32_t *length) {
+  if (!c || !length || layer < 0 || layer >= c->cfg.n_layers || seq < 0 || seq >= c->cfg.n_seqs) return FM_ERR_INVALID_ARG;
+  *length = c->len[(size_t)layer * c->cfg.n_seqs + seq];
+  return FM_OK;
+}
+
+fm_status fm_kvq_memory_bytes(const fm_kvq *c, int64_t *bytes) {
+  if (!c || !bytes) return FM_ERR_INVALID_ARG;
+  *bytes = c->bytes;
+  return FM_OK;
+}
+
+fm_status fm_kvq_synchronize(fm_kvq *c, void *stream) {
+  if (!c) return FM_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int32_t e = 0;
+  KCK(cudaMemcpyAsync(&e, c->dev_err, 4, cudaMemcpyDeviceToHost, s));
+  KCK(cudaStreamSynchronize(s));
+  if (e) {
+    KCK(cudaMemsetAsync(c->dev_err, 0, 4, s));
+    return kfail(c, FM_ERR_TIMEOUT, "a bounded device wait gave up");
+  }
+  return FM_OK;
+}
+
+const char *fm_kvq_last_error(const fm_kvq *c) { return c ? c->err : g_kvq_error; }
+
+void fm_kvq_destroy(fm_kvq *c) {
+  if (!c) return;
+  cudaDeviceSynchronize();
+  release(c);
+}
+
+}  // extern "C"

@@ -1,0 +1,131 @@
+// kvq.h -- the 4-bit KV cache's memory layout, kernel argument blocks and
+// launchers, shared by its host calls (kvq.cu) and its kernels.
+//
+// A plane holds one KV head of one sequence and layer in tiles of 64 rows.  A
+// tile is one contiguous run [K codes | K scales | V codes | V scales]:
+//   codes   64 rows of hd / 2 bytes.  A 16-byte unit holds the 32 values of a
+//           group, value e in bits 4 e of the unit; the row's units are permuted
+//           by unit ^ kvq_swz(row), so that the eight rows of an 8 x 16-byte
+//           matrix fetch (ldmatrix) hit eight distinct bank groups.
+//   scales  f16, [row / 2][group][row % 2]: the scales of two neighbouring rows
+//           form the f16 pair that the tensor-core fragments want.
+// So one bulk copy lands whole tiles in shared memory as the matrix
+// instructions read them, K alone is contiguous too, and a row is written and
+// moved without touching its neighbours' bytes.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+namespace fm {
+
+constexpr int kKvqTile = 64;       // rows a tile
+constexpr int kKvqSeqs = 64;       // sequences a launch
+constexpr int kKvqQRows = 16;      // query rows (block row x head of the group) a CTA carries
+
+enum KvqType : int32_t { KVQ_F32 = 0, KVQ_F16 = 1, KVQ_BF16 = 2 };
+
+__host__ __device__ constexpr int kvq_tile_bytes(int hd) { return 72 * hd; }
+__host__ __device__ constexpr int kvq_k_bytes(int hd) { return 36 * hd; }       // K codes and scales
+__host__ __device__ constexpr int kvq_scale_off(int hd) { return 32 * hd; }     // inside a K or V half
+// which way row r's 16-byte units are permuted: r / (rows per 128 bytes), modulo the units a row
+__host__ __device__ constexpr int kvq_swz(int r, int hd) {
+  return hd == 64 ? (r >> 2) & 1 : hd == 128 ? (r >> 1) & 3 : r & 7;
+}
+// byte offset of unit u (group u's codes) of row r, and of its scale, inside a half tile
+__host__ __device__ constexpr int kvq_unit(int r, int u, int hd) { return r * (hd / 2) + ((u ^ kvq_swz(r, hd)) << 4); }
+__host__ __device__ constexpr int kvq_scale(int r, int u, int hd) {
+  return kvq_scale_off(hd) + (((r >> 1) * (hd / 32) + u) * 2 + (r & 1)) * 2;
+}
+
+// What every launch knows of the cache (pointers of the call's layer).
+struct KvqCache {
+  uint8_t *planes;        // [seqs][kv heads] planes of plane_bytes
+  size_t plane_bytes;
+  float *weights;         // [seqs][kv heads][rows_pad] accumulated attention weights
+  uint32_t *vmax;         // [seqs][kv heads] bits of the largest |V scale| the plane has held
+  int32_t rows_pad;       // rows of a plane (a multiple of 64)
+  int32_t n_kv;
+  int32_t *err;           // raised when a bounded wait gives up
+};
+
+// append and read: rows packed by sequence <-> cache rows at[i] .. at[i] + rows[i] - 1
+struct KvqRowsArgs {
+  KvqCache c;
+  const void *k, *v;      // append: source rows [n][n_kv][hd], row stride ld elements
+  void *ko, *vo;          // read: destination rows (each may be null)
+  int64_t ld;
+  float *wo;              // read: weights out [call sequences][n_kv][ldw], or null
+  const float *wi;        // set_weights: weights in, or null
+  int64_t ldw;
+  int32_t n, type;
+  int32_t tiles;          // tiles touched, all sequences (grid x)
+  int32_t call0;          // the first sequence's place in the call (rows of wo)
+  int64_t row0[kKvqSeqs];
+  int32_t seq[kKvqSeqs], at[kKvqSeqs], rows[kKvqSeqs];
+  int32_t tile0[kKvqSeqs + 1];   // prefix sums of the tiles each sequence touches
+};
+cudaError_t launch_kvq_append(const KvqRowsArgs &a, int hd, cudaStream_t s);
+cudaError_t launch_kvq_read(const KvqRowsArgs &a, int hd, cudaStream_t s);
+cudaError_t launch_kvq_set_weights(const KvqRowsArgs &a, cudaStream_t s);
+
+struct KvqAttnArgs {
+  KvqCache c;
+  const void *q;          // [rows][n_heads][hd], row stride ldq elements
+  void *out;              // the same shape, row stride ldo
+  int64_t ldq, ldo;
+  int32_t type;           // KvqType of q and out
+  int32_t group;          // query heads a KV head
+  float scale_log2;       // scale * log2(e)
+  int32_t causal, first;  // row t of T sees rows first <= j < (causal ? len - T + t + 1 : len)
+  int32_t n;              // sequences of this launch
+  int32_t chunk;          // tiles a CTA
+  int32_t n_split;        // units whose rows are split over CTAs (they have partial results)
+  float *part_o;          // [slots][16][hd] unnormalised partial outputs
+  float2 *part_ml;        // [slots][16] (reference, row sum)
+  float *lse;             // [units][16] log2 of the row sums, for the weights; or null
+  float decay;            // weights: w = decay w + this call's
+  float *w_out;           // [call sequences][n_kv][ldw] or null
+  int64_t ldw;
+  int32_t call0;
+  int64_t row0[kKvqSeqs];
+  int32_t seq[kKvqSeqs], len[kKvqSeqs], rows[kKvqSeqs];
+  int32_t cta0[kKvqSeqs + 1];    // prefix sums of (row tiles x chunks): grid x
+  int32_t unit0[kKvqSeqs + 1];   // prefix sums of row tiles; a unit is (row tile, KV head)
+  int32_t slot0[kKvqSeqs + 1];   // prefix sums of the CTAs of split sequences: partial slots / n_kv
+  int32_t split0[kKvqSeqs + 1];  // prefix sums of row tiles of split sequences: the merge's grid
+  int32_t wt0[kKvqSeqs + 1];     // weights: prefix sums of the CTAs of each sequence
+};
+int kvq_attn_ctas_per_sm(int hd, int type);
+cudaError_t launch_kvq_attend(const KvqAttnArgs &a, int hd, cudaStream_t s);
+cudaError_t launch_kvq_merge(const KvqAttnArgs &a, int hd, cudaStream_t s);
+cudaError_t launch_kvq_weights(const KvqAttnArgs &a, int hd, cudaStream_t s);
+constexpr int kKvqWeightTiles = 8;   // tiles a CTA of the weights pass covers
+
+struct KvqEvictArgs {
+  KvqCache c;
+  int32_t n, keep, recent;
+  int32_t *kept;          // [call sequences][n_kv][keep] or null
+  int32_t *list;          // [n][n_kv][rows_pad] scratch: the rows kept, in order
+  int32_t call0;
+  int32_t src[kKvqSeqs], dst[kKvqSeqs], len[kKvqSeqs];
+};
+cudaError_t launch_kvq_evict(const KvqEvictArgs &a, int hd, cudaStream_t s);
+
+template <typename K, typename... Args>
+inline cudaError_t kvq_launch(K kern, dim3 grid, dim3 block, size_t smem, cudaStream_t s, const Args &...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+}  // namespace fm

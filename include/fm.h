@@ -61,6 +61,7 @@ typedef enum fm_status {
 #define FM_DTYPE_BF16 0
 #define FM_DTYPE_Q8_0 1
 #define FM_DTYPE_F32 2
+#define FM_DTYPE_F16 3  /* rows of the 4-bit cache's calls */
 
 typedef struct fm_config {
   int32_t variant;     /* FM_VARIANT_* */
@@ -532,6 +533,141 @@ FM_API fm_status fm_mtp_cache(fm_mtp *m, int32_t which, int32_t rows, float *dst
 FM_API fm_status fm_mtp_last_launch_count(const fm_mtp *m, int32_t *count);
 FM_API const char *fm_mtp_last_error(const fm_mtp *m);   /* never NULL; NULL m: the last failed fm_mtp_create */
 FM_API void fm_mtp_destroy(fm_mtp *m);
+
+/* ------------------------------------------------------------------------
+ * A KV cache held in 4 bits: rows in (fm_kvq_append) and out (fm_kvq_read),
+ * attention over it (fm_kvq_attend) that can keep count of the attention
+ * weight each row collects, and eviction by that weight (fm_kvq_evict).  The
+ * pages keep their caches in f16 and f32 and hold every row; this cache has no
+ * counterpart there.  It stands by itself, or holds the MTP head's rows
+ * (fm_mtp_use_kvq).
+ *
+ * A row of a KV head is cut into groups of 32 values; a group is held as an
+ * f16 scale d and 32 codes c in 0 .. 15 (4.5 bits a value) and stands for
+ * d (c - 8):  d = f16(m / -8), m the group's value of largest magnitude (the
+ * negative one where +m and -m tie); c = clamp(rint(x / d) + 8, 0, 15), ties
+ * to even, 8 where d = 0.  NaN is stored as 0; infinities and values beyond
+ * 8 * 65504 saturate.
+ *
+ * Each (layer, sequence) has its own length, kept on the host by the calls.
+ * Rows behind it are never read as values and left as they are.  Host arrays
+ * (seq_ids, counts) have n_seqs entries, 1 <= n_seqs <= config.n_seqs.
+ * Calls allocate nothing and may be captured into a graph, which then repeats
+ * the call at the lengths it was captured with.  Eager calls on different
+ * streams are put in the order they were issued in (they share a workspace
+ * and the weights); a captured call is not, so graphs that use one cache are
+ * replayed one after another, and ordered with eager calls, by the caller.
+ * The cache's device must be the current device.  Device pointers are 16-byte
+ * aligned, and row strides (ld, ldq, ldo: elements between rows) whole
+ * multiples of 16 bytes; pointers and strides of weights and kept rows need 4
+ * bytes.  One host thread at a time per cache.
+ * ------------------------------------------------------------------------ */
+typedef struct fm_kvq_config {
+  int32_t n_layers;    /* 1 .. 1024 */
+  int32_t n_seqs;      /* sequences (slots) per layer: 1 .. 65536 */
+  int32_t n_kv_heads;  /* 1 .. 1024 */
+  int32_t head_dim;    /* 64, 128 or 256 */
+  int32_t max_rows;    /* rows per sequence and layer: 1 .. 2^24 */
+} fm_kvq_config;
+
+typedef struct fm_kvq fm_kvq;
+
+/*
+ * fm_kvq_create -- an empty cache on the current device.  Synchronises the
+ * stream.  Errors: FM_ERR_INVALID_ARG, FM_ERR_UNSUPPORTED (head_dim),
+ * FM_ERR_OOM, FM_ERR_CUDA; *out is NULL on failure and the reason is in
+ * fm_kvq_last_error(NULL).
+ */
+FM_API fm_status fm_kvq_create(const fm_kvq_config *cfg, void *stream, fm_kvq **out);
+
+/*
+ * fm_kvq_append -- rows k_dev, v_dev [sum n_rows][n_kv_heads][head_dim] of
+ * dtype FM_DTYPE_F32 / F16 / BF16, row stride ld, packed in the order of
+ * seq_ids, become rows start .. start + n_rows - 1 of their sequence in layer.
+ * start <= length; writing below the length rewinds.  Afterwards length =
+ * start + n_rows (n_rows may be 0: only moves the length).  The new rows'
+ * weights are 0.  Sequence ids are distinct.
+ * Errors: FM_ERR_INVALID_ARG, FM_ERR_STATE (start > length or < 0),
+ *   FM_ERR_CONTEXT_FULL (start + n_rows > max_rows), FM_ERR_CUDA; nothing is
+ *   launched if a check fails.
+ */
+FM_API fm_status fm_kvq_append(fm_kvq *c, int32_t layer, int32_t n_seqs, const int32_t *seq_ids_host,
+                               const int32_t *n_rows_host, const int32_t *start_host, const void *k_dev,
+                               const void *v_dev, int32_t dtype, int64_t ld, void *stream);
+
+/*
+ * fm_kvq_read -- the values that rows row .. row + n_rows - 1 stand for,
+ * rounded once to dtype, into k_dev and v_dev (laid out as in fm_kvq_append;
+ * either may be NULL), and their weights into weights_dev (f32
+ * [n_seqs][n_kv_heads][ldw], entry r = row + r's; or NULL).
+ * Errors: FM_ERR_INVALID_ARG (rows outside the length, ...), FM_ERR_CUDA.
+ */
+FM_API fm_status fm_kvq_read(fm_kvq *c, int32_t layer, int32_t n_seqs, const int32_t *seq_ids_host,
+                             const int32_t *row_host, const int32_t *n_rows_host, void *k_dev, void *v_dev,
+                             int32_t dtype, int64_t ld, float *weights_dev, int64_t ldw, void *stream);
+
+/*
+ * fm_kvq_attend -- attention of n_rows[i] query rows (a draft block, a verify
+ * step's rows, one token) of each sequence over its cache:
+ *   out[r][h] = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q[r][h] . k_j),
+ * head h reading KV head h / (n_heads / n_kv_heads), over the rows
+ * first_row <= j < length, and with causal != 0 only j <= length - n_rows + t
+ * for the sequence's row t (its n_rows rows are the cache's last).  A row that
+ * sees nothing (length 0, first_row past the end, more query rows than cached
+ * ones) gives zeros.  q_dev and out_dev: [sum n_rows][n_heads][head_dim] of
+ * dtype, row strides ldq and ldo, packed in the order of seq_ids; they may not
+ * overlap.  Scores, softmax and sums are f32; the operands keep f32 queries and
+ * f32 / f16 outputs' probabilities to ~22 bits, bf16 outputs' to 11.
+ * decay >= 0 also counts the attention weight each cache row collects, per KV
+ * head:  w_j = decay w_j + sum over the call's rows and the KV head's query
+ * heads of p_j / sum p  (decay 1: plain accumulation; 0: this call's weights
+ * alone), for the rows 0 .. length - 1 of every sequence with n_rows > 0, and
+ * writes the new weights to weights_dev (f32 [n_seqs][n_kv_heads][ldw]) unless
+ * that is NULL.  decay < 0: weights are left alone.
+ * Sequence ids are distinct where weights are counted.
+ * Errors: FM_ERR_INVALID_ARG, FM_ERR_UNSUPPORTED (over 2^20 query rows x heads
+ *   in one sequence), FM_ERR_CUDA.  A bounded device wait that gives up is
+ *   reported by fm_kvq_synchronize.
+ */
+FM_API fm_status fm_kvq_attend(fm_kvq *c, int32_t layer, int32_t n_seqs, const int32_t *seq_ids_host,
+                               const int32_t *n_rows_host, const void *q_dev, int32_t dtype, int32_t n_heads,
+                               int64_t ldq, float scale, int32_t causal, int32_t first_row, void *out_dev,
+                               int64_t ldo, float decay, float *weights_dev, int64_t ldw, void *stream);
+
+/* fm_kvq_set_weights -- the weights of rows 0 .. length - 1 from weights_dev (f32 [n_seqs][n_kv_heads][ldw]): a
+   saved state, or a measure of the caller's own to evict by.  Sequence ids are distinct.  Errors:
+   FM_ERR_INVALID_ARG, FM_ERR_CUDA. */
+FM_API fm_status fm_kvq_set_weights(fm_kvq *c, int32_t layer, int32_t n_seqs, const int32_t *seq_ids_host,
+                                    const float *weights_dev, int64_t ldw, void *stream);
+
+/*
+ * fm_kvq_evict -- bring sequences down to `keep` rows: per KV head the last
+ * `recent` rows stay, and of the rows before them the keep - recent with the
+ * largest weight (ties: the lowest row; NaN ranks below every number), in their
+ * order.  The kept rows, with their weights, become rows 0 .. of sequence
+ * dst_ids[i], whose length is then min(keep, length); a sequence of at most keep rows keeps all.  dst_ids[i] may be
+ * src_ids[i] (in place), or another sequence, whose rows are replaced and
+ * whose source stays as it is (a branch).  Destinations are distinct, and none
+ * is the source of another entry.  kept_dev: int32 [n_seqs][n_kv_heads][keep]
+ * or NULL receives the rows kept; entries past min(keep, length) are left as
+ * they were.  0 <= recent <= keep <= max_rows.
+ * After an eviction the heads of a sequence hold different rows of the past, in
+ * one order: causal calls and first_row go by the place in the cache.
+ * Errors: FM_ERR_INVALID_ARG, FM_ERR_CUDA.
+ */
+FM_API fm_status fm_kvq_evict(fm_kvq *c, int32_t layer, int32_t n_seqs, const int32_t *src_ids_host,
+                              const int32_t *dst_ids_host, int32_t keep, int32_t recent, int32_t *kept_dev,
+                              void *stream);
+
+/* The rows a (layer, sequence) holds.  Errors: FM_ERR_INVALID_ARG. */
+FM_API fm_status fm_kvq_length(const fm_kvq *c, int32_t layer, int32_t seq, int32_t *length);
+/* Device bytes the cache holds (rows, weights, workspace). */
+FM_API fm_status fm_kvq_memory_bytes(const fm_kvq *c, int64_t *bytes);
+/* Wait for the stream; FM_ERR_TIMEOUT if a bounded device wait gave up since the last check (cleared). */
+FM_API fm_status fm_kvq_synchronize(fm_kvq *c, void *stream);
+FM_API const char *fm_kvq_last_error(const fm_kvq *c);   /* never NULL; NULL c: the last failed fm_kvq_create */
+/* Free everything the cache owns.  NULL is ignored. */
+FM_API void fm_kvq_destroy(fm_kvq *c);
 
 #ifdef __cplusplus
 }

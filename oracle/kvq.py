@@ -1,0 +1,68 @@
+"""fp64 oracle of the 4-bit KV cache: the storage rule, attention over the
+stored rows with the weight that each row collects, and eviction by it.  Plain
+loops over sequences, heads and rows; nothing is blocked or fused."""
+from __future__ import annotations
+
+import numpy as np
+
+GROUP = 32
+F16_MAX = 65504.0
+
+
+def quantize(x: np.ndarray):
+    """(codes 0..15, f16 scales) of groups of 32 along the last axis.  NaN counts as 0."""
+    g = np.nan_to_num(np.asarray(x, np.float64), nan=0.0, posinf=np.inf, neginf=-np.inf)
+    g = g.reshape(g.shape[:-1] + (g.shape[-1] // GROUP, GROUP))
+    hi, lo = g.max(-1), g.min(-1)
+    m = np.where(hi > -lo, hi, lo)
+    d = np.clip(m / -8.0, -F16_MAX, F16_MAX).astype(np.float16)
+    dd = d.astype(np.float64)[..., None]
+    with np.errstate(invalid="ignore", divide="ignore"):
+        c = np.where(dd == 0, 8.0, np.clip(np.rint(g / np.where(dd == 0, 1.0, dd)) + 8.0, 0.0, 15.0))
+    return c.astype(np.uint8).reshape(np.asarray(x).shape), d
+
+
+def values(codes: np.ndarray, scales: np.ndarray) -> np.ndarray:
+    """What codes and scales stand for, d (c - 8) (exact in f32 too)."""
+    c = codes.astype(np.float64).reshape(scales.shape + (GROUP,)) - 8.0
+    return (c * scales.astype(np.float64)[..., None]).reshape(codes.shape)
+
+
+def stored(x: np.ndarray) -> np.ndarray:
+    return values(*quantize(x))
+
+
+def attend(q: np.ndarray, k: np.ndarray, v: np.ndarray, scale: float, causal: bool = False, first: int = 0):
+    """q [T, H, hd] over one sequence's rows k, v [L, Hkv, hd] -> (out [T, H, hd], weights [Hkv, L],
+    mass [T, H, hd]: sum_j p_j |v_j|, reach [T, H]: the largest sum_d |q_d k_jd| scale -- the scales of the errors)."""
+    T, H, hd = q.shape
+    L, hkv = k.shape[0], k.shape[1]
+    out, mass = np.zeros((T, H, hd)), np.zeros((T, H, hd))
+    reach = np.zeros((T, H))
+    w = np.zeros((hkv, L))
+    for t in range(T):
+        end = min(L, L - T + t + 1) if causal else L
+        if end <= first:
+            continue
+        for h in range(H):
+            g = h // (H // hkv)
+            kk, vv = k[first:end, g], v[first:end, g]
+            s = kk @ q[t, h] * scale
+            reach[t, h] = abs(scale) * np.max(np.abs(kk) @ np.abs(q[t, h]))
+            p = np.exp(s - s.max())
+            p /= p.sum()
+            out[t, h] = p @ vv
+            mass[t, h] = p @ np.abs(vv)
+            w[g, first:end] += p
+    return out, w, mass, reach
+
+
+def kept_rows(w: np.ndarray, keep: int, recent: int) -> np.ndarray:
+    """The rows of one head that stay, in order: the last `recent`, and of the others the keep - recent with the
+    largest weight, ties to the lowest row, NaN below every number."""
+    n = len(w)
+    if n <= keep:
+        return np.arange(n)
+    old = n - recent
+    rank = sorted(range(old), key=lambda r: (np.isnan(w[r]), 0.0 if np.isnan(w[r]) else -w[r], r))
+    return np.array(sorted(rank[:keep - recent]) + list(range(old, n)), dtype=np.int64)
