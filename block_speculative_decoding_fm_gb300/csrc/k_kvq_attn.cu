@@ -24,18 +24,24 @@ namespace {
 
 using namespace kvq;
 
-constexpr int kCons = 128;                 // consumer threads
-constexpr int kThreads = kCons + 32;
 constexpr float kLazy = 8.f;               // log2 of the growth a reference tolerates
+constexpr int kWThreads = 128;             // the weights pass
 
-template <int HD>
-constexpr int n_stages() {
-  return HD == 256 ? 3 : 4;
-}
-template <int HD, bool QS>
-constexpr int attend_smem() {
-  return n_stages<HD>() * 2 * kvq_tile_bytes(HD) + q_bytes<HD, QS>() + 16 * 4 + 2 * 4 * 16 * 4 + 2 * n_stages<HD>() * 8;
-}
+// The attention kernel's shape: groups of four warps (they take the stages in turn), ring stages, CTAs an SM.
+template <int HD, typename T>
+struct Shape {
+  static constexpr bool QS = sizeof(T) == 4;                          // f32 queries: f16 hi + lo
+  static constexpr bool PS = !std::is_same<T, __nv_bfloat16>::value;  // f16 and f32 outputs: P' too
+  static constexpr bool SV = sizeof(T) == 4;                          // f32 outputs: signed codes (no sums to take off)
+  static constexpr int NG = HD == 256 ? 2 : 1;
+  static constexpr int NS = HD == 64 ? 4 : HD == 128 ? 3 : 2;         // of a group's own ring
+  static constexpr int MB = HD == 64 ? 4 : HD == 128 ? 3 : 1;
+  static constexpr int NW = 4 * NG, kThreads = 128 * NG;
+  static constexpr int SB = kKvqStage * kvq_tile_bytes(HD);
+  static constexpr int HC = 64;                                       // dims joined at a time
+  static constexpr int kScratch = NW / 2 * 16 * HC * 4;
+  static constexpr int kBytes = NG * NS * SB + kScratch + QTile<HD, QS>::kBytes + 2 * NW * 16 * 4 + NG * 2 * NS * 8 + NG * 32;
+};
 
 template <typename T>
 __device__ __forceinline__ void store4(T *p, float4 v) {
@@ -54,228 +60,344 @@ __device__ __forceinline__ void store4(T *p, float4 v) {
   }
 }
 
-// Grid (sequence x chunk x row tile, KV head).
-template <int HD, typename T>
-__global__ void __launch_bounds__(kThreads) kvq_attend_kernel(const __grid_constant__ KvqAttnArgs a) {
-  // f32 queries are split into f16 hi + lo; f16 and f32 outputs keep P split too (a once-rounded
-  // P' alone is as far off as an f16 output's own rounding)
-  constexpr bool QS = sizeof(T) == 4, PS = !std::is_same<T, __nv_bfloat16>::value;
-  constexpr int NS = n_stages<HD>(), SB = 2 * kvq_tile_bytes(HD);
-  extern __shared__ __align__(128) uint8_t smem[];
-  uint8_t *qs = smem + NS * SB;
-  float *mult = reinterpret_cast<float *>(qs + q_bytes<HD, QS>());
-  float *wm = mult + 16, *wl = wm + 4 * 16;             // [warp][row] reference and sum
-  const uint32_t bars = smem_u32(wl + 4 * 16);
-  auto full = [&](int i) { return bars + i * 8; };
-  auto empty = [&](int i) { return bars + (NS + i) * 8; };
-  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+// A stretch of a CTA's share: stages [s0, s0 + n) of one unit.
+struct Stretch {
+  int i, head, rt, s0, n;
+  __device__ __forceinline__ Stretch(const KvqAttnArgs &a, int64_t at, int64_t end) {
+    i = find_seq<int64_t>(a.st0, a.n, at);
+    const int64_t rel = at - a.st0[i];
+    const int S = a.stages[i];
+    const int unit = static_cast<int>(rel / S);
+    s0 = static_cast<int>(rel - (int64_t)unit * S);
+    n = static_cast<int>(min((int64_t)(S - s0), end - at));
+    const int rts = (a.rows[i] * a.group + kKvqQRows - 1) / kKvqQRows;
+    head = unit / rts;
+    rt = unit - head * rts;
+  }
+};
 
-  const int i = find_seq(a.cta0, a.n, blockIdx.x);
-  const int head = blockIdx.y;
-  const int len = a.len[i], T_rows = a.rows[i], R = T_rows * a.group;
-  const int rts = (R + kKvqQRows - 1) / kKvqQRows;
-  const int in_seq = blockIdx.x - a.cta0[i];
-  const int chunk = in_seq / rts, rt = in_seq - chunk * rts;
-  const int chunks = (a.cta0[i + 1] - a.cta0[i]) / rts;
-  const int t_end_all = (len + kKvqTile - 1) / kKvqTile;
-  const int t0 = min(t_end_all, a.first / kKvqTile + chunk * a.chunk), t1 = min(t_end_all, t0 + a.chunk);
-  const int nst = (t1 - t0 + 1) / 2;
-  const size_t plane = (size_t)a.seq[i] * a.c.n_kv + head;
+// Where a group's copies have got to (in shared memory: one lane's business, once a stage).
+struct Cursor {
+  int64_t at;             // the share's stage after the stretch that the cursor is in
+  const uint8_t *src;     // the next stage
+  int32_t left;           // stages of the stretch that are the group's
+  int32_t tiles;          // tiles from the next stage to the unit's end
+  int32_t issued;
+};
+static_assert(sizeof(Cursor) <= 32, "a cursor's place in shared memory");
+
+// The next of the group's stages into its ring; false where a wait gave up.
+template <int HD, typename Sh>
+__device__ __forceinline__ bool issue_stage(const KvqAttnArgs &a, Cursor *cu, int64_t w_end, int grp, uint32_t ring,
+                                            uint32_t full, uint32_t empty) {
+  constexpr int TB = kvq_tile_bytes(HD);
+  int left = cu->left, tiles = cu->tiles;
+  const uint8_t *src = cu->src;
+  while (left == 0) {
+    const int64_t at = cu->at;
+    if (at >= w_end) return true;
+    const Stretch x(a, at, w_end);
+    const int t = a.first / kKvqTile + (x.s0 + grp) * kKvqStage;
+    left = (x.n - grp + Sh::NG - 1) / Sh::NG;
+    tiles = (a.len[x.i] + kKvqTile - 1) / kKvqTile - t;
+    src = a.c.planes + ((size_t)a.seq[x.i] * a.c.n_kv + x.head) * a.c.plane_bytes + (size_t)t * TB;
+    cu->at = at + x.n;
+  }
+  const int g = cu->issued, slot = g % Sh::NS;
+  if (g >= Sh::NS && !mbar_wait_bounded(empty + slot * 8, (g / Sh::NS - 1) & 1, a.c.err)) return false;
+  if (tiles > 0) {
+    const uint32_t bytes = min(kKvqStage, tiles) * TB;
+    mbar_expect_tx(full + slot * 8, bytes);
+    bulk_g2s(ring + slot * Sh::SB, src, bytes, full + slot * 8);
+  } else {
+    mbar_arrive(full + slot * 8);   // a unit without keys has one stage of nothing
+  }
+  cu->left = left - 1;
+  cu->tiles = tiles - Sh::NG * kKvqStage;
+  cu->src = src + Sh::NG * Sh::SB;
+  cu->issued = g + 1;
+  return true;
+}
+
+template <int HD, typename T>
+__global__ void __launch_bounds__(Shape<HD, T>::kThreads, Shape<HD, T>::MB)
+    kvq_attend_kernel(const __grid_constant__ KvqAttnArgs a) {
+  using Sh = Shape<HD, T>;
+  using QT = QTile<HD, Sh::QS>;
+  constexpr bool QS = Sh::QS, PS = Sh::PS, SV = Sh::SV;
+  constexpr int NG = Sh::NG, NS = Sh::NS, NW = Sh::NW, SB = Sh::SB, TB = kvq_tile_bytes(HD), HC = Sh::HC;
+  constexpr int kCons = Sh::kThreads;
+  extern __shared__ __align__(128) uint8_t smem[];
+  float *scratch = reinterpret_cast<float *>(smem + NG * NS * SB);
+  uint8_t *qs = smem + NG * NS * SB + Sh::kScratch;
+  float *wm = reinterpret_cast<float *>(qs + QT::kBytes), *wl = wm + NW * 16;   // [warp][row] reference and sum
+  uint64_t *bar = reinterpret_cast<uint64_t *>(wl + NW * 16);                   // [group][full, empty][stage]
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int grp = NG == 1 ? 0 : w >> 2;     // a group takes the stages grp, grp + NG, ... of a stretch
+  Cursor *cu = reinterpret_cast<Cursor *>(bar + NG * 2 * NS) + grp;
+  const uint32_t full = smem_u32(bar + grp * 2 * NS), empty = full + NS * 8, ring = smem_u32(smem) + grp * NS * SB;
+  const int64_t W = a.st0[a.n];
+  const int64_t w_beg = blockIdx.x * W / a.ctas, w_end = (blockIdx.x + 1) * W / a.ctas;
 
   pdl_trigger();
   if (tid == 0) {
 #pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      mbar_init(full(s), 1);
-      mbar_init(empty(s), 4);
-    }
+    for (int s = 0; s < NG * 2 * NS; ++s) mbar_init(smem_u32(bar + s), s / NS & 1 ? 4 : 1);
     mbar_fence_init();
   }
   __syncthreads();
   pdl_wait();
-
-  if (w == 4) {
-    if (lane == 0) {
-      const uint8_t *src = a.c.planes + plane * a.c.plane_bytes + (size_t)t0 * kvq_tile_bytes(HD);
-      int st = 0;
-      for (; st < nst; ++st) {
-        const int slot = st % NS;
-        if (st >= NS && !mbar_wait_bounded(empty(slot), ((st / NS) - 1) & 1, a.c.err)) break;
-        const uint32_t bytes = (uint32_t)min(2, t1 - t0 - 2 * st) * kvq_tile_bytes(HD);
-        mbar_expect_tx(full(slot), bytes);
-        bulk_g2s(smem_u32(smem + slot * SB), src + (size_t)st * SB, bytes, full(slot));
-      }
-      // nothing is left in flight when the CTA ends (a consumer may have given up)
-      for (int s = max(0, st - NS); s < st; ++s) mbar_wait_drain(full(s % NS), (s / NS) & 1);
-    }
-    __syncthreads();
-    return;
+  const bool copies = lane == 0 && (w & 3) == 0;   // the lane that sends for its group's stages
+  bool ok = true;
+  if (copies) {
+    cu->at = w_beg;
+    cu->left = 0;
+    cu->issued = 0;
+    for (int k = 0; k < NS - 1; ++k) ok = issue_stage<HD, Sh>(a, cu, w_end, grp, ring, full, empty);
   }
 
-  load_q<HD, QS, kCons>(static_cast<const T *>(a.q) + a.row0[i] * a.ldq + (int64_t)head * a.group * HD, a.ldq, a.group,
-                        rt * kKvqQRows, R, a.scale_log2, qs, mult, tid);
-  named_sync(1, kCons);
-  const PRange<PS> range(__ldcg(a.c.vmax + plane));
-  const float bias = range.bias;
-  const float mu0 = mult[lane >> 2], mu1 = mult[(lane >> 2) + 8];
-  // the rows that this lane's two query rows see end at lim; rows past R follow the last (they are not stored)
-  const int ra = min(rt * kKvqQRows + (lane >> 2), R - 1), rb = min(rt * kKvqQRows + (lane >> 2) + 8, R - 1);
-  const int lim0 = a.causal ? len - T_rows + ra / a.group + 1 : len;
-  const int lim1 = a.causal ? len - T_rows + rb / a.group + 1 : len;
-  const int lim_all = a.causal ? len - T_rows + rt * kKvqQRows / a.group + 1 : len;
+  const int wt = (w >> 1) & 1, r0 = (w & 1) * 32;
+  const LaneAt<HD> la(r0, lane);
+  const uint32_t qt = smem_u32(qs);
+  const uint32_t code0 = ring + wt * TB + la.code, scale0 = ring + wt * TB + la.scale;
+  const int row = lane >> 2;
+  int slot = 0;
+  uint32_t par = 0;
+  for (int64_t at = w_beg; at < w_end;) {
+    const Stretch x(a, at, w_end);
+    const int len = a.len[x.i], T_rows = a.rows[x.i], R = T_rows * a.group, rq = x.rt * kKvqQRows;
+    const size_t plane = (size_t)a.seq[x.i] * a.c.n_kv + x.head;
+    load_q<HD, QS, kCons>(static_cast<const T *>(a.q) + a.row0[x.i] * a.ldq + (int64_t)x.head * a.group * HD, a.ldq, a.group,
+                          rq, R, a.scale_log2, qs, tid);
+    const PRange<PS> range(__ldcg(a.c.vmax + plane));
+    named_sync(1, kCons);
+    const float2 mu = *reinterpret_cast<const float2 *>(qs + QT::kMult + row * 8);
+    // the rows that this lane's two query rows see end at lim; rows past R follow the last (they are not stored)
+    const int ra = min(rq + row, R - 1), rb = min(rq + row + 8, R - 1);
+    const int lim0 = a.causal ? len - T_rows + ra / a.group + 1 : len;
+    const int lim1 = a.causal ? len - T_rows + rb / a.group + 1 : len;
+    const int lim_all = a.causal ? len - T_rows + rq / a.group + 1 : len;
 
-  float o[HD / 8][4];
+    float o[HD / 8][4], cor[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int n = 0; n < HD / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
-  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-  const uint32_t qf = smem_u32(qs);
-  for (int st = 0; st < nst; ++st) {
-    const int slot = st % NS;
-    if (!mbar_wait_warp(full(slot), (st / NS) & 1, a.c.err)) break;
-    const int tile = t0 + 2 * st + (w >> 1), r0 = (w & 1) * 32, key0 = tile * kKvqTile + r0;
-    if (tile < t1 && key0 < len && key0 + 32 > a.first) {
-      const uint32_t kb = smem_u32(smem + slot * SB + (w >> 1) * kvq_tile_bytes(HD));
-      float s[4][4];
-      strip_scores<HD, QS>(kb, r0, qf, lane, s);
-      const bool whole = key0 >= a.first && key0 + 32 <= lim_all;
-      float x0 = -INFINITY, x1 = -INFINITY;
+    for (int n = 0; n < HD / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+    float m0 = -INFINITY, m1 = -INFINITY;
+    uint64_t l0 = 0ull, l1 = 0ull;          // row sums, even and odd keys apart
+    int key0 = (a.first / kKvqTile + (x.s0 + grp) * kKvqStage + wt) * kKvqTile + r0;
+    for (int k = grp; k < x.n; k += NG) {
+      // a stage ahead of the ring's end; then this one (a wait that gave up ends the warp's work, not its barriers)
+      if (copies && ok) ok = issue_stage<HD, Sh>(a, cu, w_end, grp, ring, full, empty);
+      ok = __all_sync(0xffffffffu, ok) && mbar_wait_warp(full + slot * 8, par, a.c.err);
+      if (!ok) break;
+      if (key0 < len && key0 + 32 > a.first) {
+        const uint32_t code = code0 + slot * SB, scale = scale0 + slot * SB;
+        uint64_t sp[4][2];
+        strip_scores<HD, QS>(code, scale, qt, lane, sp);
+        float s[4][4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 4; ++j) unpack2(sp[j][0], s[j][0], s[j][1]), unpack2(sp[j][1], s[j][2], s[j][3]);
+        if (key0 < a.first || key0 + 32 > lim_all) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          s[j][e] *= e < 2 ? mu0 : mu1;
-          if (!whole) {
-            const int key = key0 + 8 * j + 2 * (lane & 3) + (e & 1);
-            if (key < a.first || key >= (e < 2 ? lim0 : lim1)) s[j][e] = -INFINITY;
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int key = key0 + 8 * j + 2 * (lane & 3) + (e & 1);
+              if (key < a.first || key >= (e < 2 ? lim0 : lim1)) s[j][e] = -INFINITY;
+            }
+        }
+        float x0 = fmaxf(s[0][0], s[0][1]), x1 = fmaxf(s[0][2], s[0][3]);
+#pragma unroll
+        for (int j = 1; j < 4; ++j) {
+          x0 = fmaxf(x0, fmaxf(s[j][0], s[j][1]));
+          x1 = fmaxf(x1, fmaxf(s[j][2], s[j][3]));
+        }
+#pragma unroll
+        for (int sh = 1; sh < 4; sh <<= 1) {
+          x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, sh));
+          x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, sh));
+        }
+        // (a row that sees none of the strip's keys: -inf, also where its factor is 0)
+        x0 = x0 == -INFINITY ? x0 : x0 * mu.x;
+        x1 = x1 == -INFINITY ? x1 : x1 * mu.y;
+        if (__any_sync(0xffffffffu, x0 > m0 + kLazy || x1 > m1 + kLazy)) {
+          const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
+          const float f0 = n0 == m0 ? 1.f : ex2(m0 - n0), f1 = n1 == m1 ? 1.f : ex2(m1 - n1);
+          m0 = n0, m1 = n1;
+          l0 = fma2(l0, pack2(f0, f0), 0ull), l1 = fma2(l1, pack2(f1, f1), 0ull);
+#pragma unroll
+          for (int n = 0; n < HD / 8; ++n) o[n][0] *= f0, o[n][1] *= f0, o[n][2] *= f1, o[n][3] *= f1;
+          if constexpr (!SV) cor[0] *= f0, cor[1] *= f0, cor[2] *= f1, cor[3] *= f1;
+        }
+        const float b0 = range.bias - (m0 == -INFINITY ? 0.f : m0), b1 = range.bias - (m1 == -INFINITY ? 0.f : m1);
+        const bool masked = key0 < a.first || key0 + 32 > lim_all;
+        const uint64_t mu0 = pack2(mu.x, mu.x), mu1 = pack2(mu.y, mu.y), bb0 = pack2(b0, b0), bb1 = pack2(b1, b1);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float t[4];
+          unpack2(fma2(pack2(s[j][0], s[j][1]), mu0, bb0), t[0], t[1]);
+          unpack2(fma2(pack2(s[j][2], s[j][3]), mu1, bb1), t[2], t[3]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) t[e] = masked && s[j][e] == -INFINITY ? 0.f : ex2(t[e]);
+          l0 = add2(l0, pack2(t[0], t[1]));
+          l1 = add2(l1, pack2(t[2], t[3]));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[j][e] = t[e];
+        }
+        strip_pv<HD, PS, SV>(code + kvq_k_bytes(HD), scale + kvq_k_bytes(HD), lane, range, s, o, cor);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty + slot * 8);
+      if (++slot == NS) slot = 0, par ^= 1;
+      key0 += NG * kKvqStage * kKvqTile;
+    }
+
+    // the warps' results: references and sums first, then the outputs pairwise
+    float ls0, ls1, lt;
+    unpack2(l0, ls0, lt);
+    ls0 += lt;
+    unpack2(l1, ls1, lt);
+    ls1 += lt;
+#pragma unroll
+    for (int sh = 1; sh < 4; sh <<= 1) {
+      ls0 += __shfl_xor_sync(0xffffffffu, ls0, sh);
+      ls1 += __shfl_xor_sync(0xffffffffu, ls1, sh);
+    }
+    if ((lane & 3) == 0) {
+      wm[w * 16 + row] = m0;
+      wm[w * 16 + row + 8] = m1;
+      wl[w * 16 + row] = ls0;
+      wl[w * 16 + row + 8] = ls1;
+    }
+    named_sync(1, kCons);
+    float M0 = -INFINITY, M1 = -INFINITY;
+#pragma unroll
+    for (int v = 0; v < NW; ++v) {
+      M0 = fmaxf(M0, wm[v * 16 + row]);
+      M1 = fmaxf(M1, wm[v * 16 + row + 8]);
+    }
+    finish_o<HD, SV>(o, cor, lane, m0 == M0 ? 1.f : ex2(m0 - M0), m1 == M1 ? 1.f : ex2(m1 - M1));
+    const bool whole = x.n == a.stages[x.i];
+    const size_t slot_g = (size_t)blockIdx.x * 2 + (x.s0 == 0);   // a unit begun here, or one continued
+#pragma unroll
+    for (int c0 = 0; c0 < HD; c0 += HC) {
+#pragma unroll
+      for (int half = NW / 2; half >= 1; half >>= 1) {
+        float4 *buf = reinterpret_cast<float4 *>(scratch) + (w & (half - 1)) * (16 * HC / 4) + lane;
+        if (w >= half && w < 2 * half) {
+#pragma unroll
+          for (int n = 0; n < HC / 8; ++n) {
+            const float(&v)[4] = o[c0 / 8 + n];
+            buf[n * 32] = make_float4(v[0], v[1], v[2], v[3]);
           }
         }
-        x0 = fmaxf(x0, fmaxf(s[j][0], s[j][1]));
-        x1 = fmaxf(x1, fmaxf(s[j][2], s[j][3]));
-      }
+        named_sync(1, kCons);
+        if (w < half) {
 #pragma unroll
-      for (int sh = 1; sh < 4; sh <<= 1) {
-        x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, sh));
-        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, sh));
+          for (int n = 0; n < HC / 8; ++n) {
+            const float4 v = buf[n * 32];
+            float(&y)[4] = o[c0 / 8 + n];
+            y[0] += v.x, y[1] += v.y, y[2] += v.z, y[3] += v.w;
+          }
+        }
       }
-      if (__any_sync(0xffffffffu, x0 > m0 + kLazy || x1 > m1 + kLazy)) {
-        const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
-        const float f0 = n0 == m0 ? 1.f : ex2(m0 - n0), f1 = n1 == m1 ? 1.f : ex2(m1 - n1);
-        m0 = n0, m1 = n1;
-        l0 *= f0, l1 *= f1;
+      if (w == 0) {   // as rows: columns 2 c, 2 c + 1 of tile n are dims d, d + 4
 #pragma unroll
-        for (int n = 0; n < HD / 8; ++n) o[n][0] *= f0, o[n][1] *= f0, o[n][2] *= f1, o[n][3] *= f1;
+        for (int n = 0; n < HC / 8; ++n) {
+          const int d = 32 * (n >> 2) + 8 * (lane & 3) + (n & 3);
+          const float(&v)[4] = o[c0 / 8 + n];
+          scratch[row * HC + d] = v[0];
+          scratch[row * HC + d + 4] = v[1];
+          scratch[(row + 8) * HC + d] = v[2];
+          scratch[(row + 8) * HC + d + 4] = v[3];
+        }
       }
-      const float b0 = (m0 == -INFINITY ? 0.f : m0) - bias, b1 = (m1 == -INFINITY ? 0.f : m1) - bias;
+      named_sync(1, kCons);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        s[j][0] = ex2(s[j][0] - b0);
-        s[j][1] = ex2(s[j][1] - b0);
-        s[j][2] = ex2(s[j][2] - b1);
-        s[j][3] = ex2(s[j][3] - b1);
-        l0 += s[j][0] + s[j][1];
-        l1 += s[j][2] + s[j][3];
+      for (int e = tid; e < 16 * HC / 4; e += kCons) {
+        const int r = e / (HC / 4), d = 4 * (e % (HC / 4)), qr = rq + r;
+        const float4 v = *reinterpret_cast<const float4 *>(scratch + r * HC + d);
+        float M = -INFINITY, L = 0.f;
+#pragma unroll
+        for (int u = 0; u < NW; ++u) M = fmaxf(M, wm[u * 16 + r]);
+#pragma unroll
+        for (int u = 0; u < NW; ++u) L += (wm[u * 16 + r] == M ? 1.f : ex2(wm[u * 16 + r] - M)) * wl[u * 16 + r];
+        if (!whole) {
+          *reinterpret_cast<float4 *>(a.part_o + (slot_g * 16 + r) * HD + c0 + d) = v;
+          if (c0 + d == 0) a.part_ml[slot_g * 16 + r] = make_float2(M, L);
+        } else if (qr < R) {
+          const float inv = L == 0.f ? 0.f : range.undo / L;
+          const int t = qr / a.group;
+          store4(static_cast<T *>(a.out) + (a.row0[x.i] + t) * a.ldo +
+                     ((int64_t)x.head * a.group + qr - t * a.group) * HD + c0 + d,
+                 make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+          if (a.lse && c0 + d == 0)
+            a.lse[((size_t)(a.unit0[x.i] + x.rt) * a.c.n_kv + x.head) * 16 + r] =
+                L == 0.f ? INFINITY : M + log2f(L) - range.bias;
+        }
       }
-      strip_pv<HD, PS>(kb + kvq_k_bytes(HD), r0, lane, range, s, o);
+      if (c0 + HC < HD) named_sync(1, kCons);
     }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(empty(slot));
+    at += x.n;
+    if (at < w_end) named_sync(1, kCons);   // the next stretch writes the queries, the references and the scratch
   }
-#pragma unroll
-  for (int sh = 1; sh < 4; sh <<= 1) {
-    l0 += __shfl_xor_sync(0xffffffffu, l0, sh);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, sh);
-  }
-  // the four warps' results, in warp order, in the ring (every copy into it has landed and been read)
-  if ((lane & 3) == 0) {
-    wm[w * 16 + (lane >> 2)] = m0;
-    wm[w * 16 + (lane >> 2) + 8] = m1;
-    wl[w * 16 + (lane >> 2)] = l0;
-    wl[w * 16 + (lane >> 2) + 8] = l1;
-  }
-  __syncthreads();   // with the copying warp, whose copies have all landed
-  float M0 = -INFINITY, M1 = -INFINITY;
-#pragma unroll
-  for (int v = 0; v < 4; ++v) {
-    M0 = fmaxf(M0, wm[v * 16 + (lane >> 2)]);
-    M1 = fmaxf(M1, wm[v * 16 + (lane >> 2) + 8]);
-  }
-  const float f0 = m0 == M0 ? 1.f : ex2(m0 - M0), f1 = m1 == M1 ? 1.f : ex2(m1 - M1);
-  float *ob = reinterpret_cast<float *>(smem) + w * 16 * HD;
-#pragma unroll
-  for (int n = 0; n < HD / 8; ++n) {
-    const int d = 32 * (n >> 2) + 8 * (lane & 3) + (n & 3);   // columns 2 c, 2 c + 1 of tile n: dims d, d + 4
-    ob[(lane >> 2) * HD + d] = o[n][0] * f0;
-    ob[(lane >> 2) * HD + d + 4] = o[n][1] * f0;
-    ob[((lane >> 2) + 8) * HD + d] = o[n][2] * f1;
-    ob[((lane >> 2) + 8) * HD + d + 4] = o[n][3] * f1;
-  }
-  named_sync(1, kCons);
-  const size_t slot_g = ((size_t)a.slot0[i] + in_seq) * a.c.n_kv + head;
-#pragma unroll
-  for (int it = tid; it < 16 * HD / 4; it += kCons) {
-    const int r = it / (HD / 4), d = 4 * (it % (HD / 4));
-    float M = -INFINITY, L = 0.f;
-#pragma unroll
-    for (int v = 0; v < 4; ++v) M = fmaxf(M, wm[v * 16 + r]);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const float mv = wm[v * 16 + r];
-      L += (mv == M ? 1.f : ex2(mv - M)) * wl[v * 16 + r];
-      const float4 x = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(smem) + (v * 16 + r) * HD + d);
-      acc.x += x.x, acc.y += x.y, acc.z += x.z, acc.w += x.w;
-    }
-    const int row = rt * kKvqQRows + r;
-    if (chunks > 1) {
-      *reinterpret_cast<float4 *>(a.part_o + (slot_g * 16 + r) * HD + d) = acc;
-      if (d == 0) a.part_ml[slot_g * 16 + r] = make_float2(M, L);
-    } else if (row < R) {
-      const float inv = L == 0.f ? 0.f : range.undo / L;
-      const int t = row / a.group;
-      store4(static_cast<T *>(a.out) + (a.row0[i] + t) * a.ldo + ((int64_t)head * a.group + row - t * a.group) * HD + d,
-             make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-      if (a.lse && d == 0)
-        a.lse[((size_t)(a.unit0[i] + rt) * a.c.n_kv + head) * 16 + r] = L == 0.f ? INFINITY : M + log2f(L) - bias;
-    }
-  }
+  // nothing is left in flight when the CTA ends (a consumer may have given up)
+  if (copies)
+    for (int k = max(0, cu->issued - NS); k < cu->issued; ++k) mbar_wait_drain(full + k % NS * 8, (k / NS) & 1);
+  __syncthreads();
 }
 
-// Joins the chunks of a split unit in chunk order.  Grid (split row tile, KV head, 16 HD / 4 / 128 row groups).
+// Joins the parts of a unit that several CTAs share, in their order.  Block x looks after the boundary between
+// CTAs x and x + 1: it works where that is the first boundary inside a unit.  Grid (ctas - 1, 16 HD / 4 / 128).
 template <int HD, typename T>
 __global__ void __launch_bounds__(128) kvq_merge_kernel(const __grid_constant__ KvqAttnArgs a) {
+  constexpr int NB = 8;    // parts whose loads are in flight together
   pdl_trigger();
-  const int i = find_seq(a.split0, a.n, blockIdx.x);
-  const int head = blockIdx.y, rt = blockIdx.x - a.split0[i];
-  const int R = a.rows[i] * a.group, rts = (R + kKvqQRows - 1) / kKvqQRows;
-  const int chunks = (a.cta0[i + 1] - a.cta0[i]) / rts;
-  const int it = blockIdx.z * 128 + threadIdx.x;
-  const int r = it / (HD / 4), d = 4 * (it % (HD / 4)), row = rt * kKvqQRows + r;
-  const size_t step = (size_t)rts * a.c.n_kv;
-  const size_t s0 = ((size_t)a.slot0[i] + rt) * a.c.n_kv + head;
-  pdl_wait();
-  if (row >= R) return;
+  const int64_t W = a.st0[a.n], G = a.ctas;
+  const int64_t cut = (blockIdx.x + 1) * W / G;
+  const Stretch x(a, cut, W);
+  pdl_wait();   // every block, so that a later launch that waits for this one waits for what came before too
+  if (x.s0 == 0 || cut - x.s0 < blockIdx.x * W / G) return;
+  // the last CTA with a stage of the unit: its share begins at or before the unit's last stage
+  const int64_t unit_end = cut - x.s0 + a.stages[x.i];
+  const int c0 = blockIdx.x, c1 = static_cast<int>((unit_end * G - 1) / W);
+  const int it = blockIdx.y * 128 + threadIdx.x;
+  const int r = it / (HD / 4), d = 4 * (it % (HD / 4)), qr = x.rt * kKvqQRows + r;
+  if (qr >= a.rows[x.i] * a.group) return;
   float M = -INFINITY, L = 0.f;
-#pragma unroll 8
-  for (int c = 0; c < chunks; ++c) M = fmaxf(M, __ldcg(&a.part_ml[(s0 + c * step) * 16 + r]).x);
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int c = 0; c < chunks; ++c) {
-    const float2 ml = __ldcg(&a.part_ml[(s0 + c * step) * 16 + r]);
-    const float4 x = __ldcg(reinterpret_cast<const float4 *>(a.part_o + ((s0 + c * step) * 16 + r) * HD + d));
-    const float f = ml.x == M ? 1.f : ex2(ml.x - M);
-    L = fmaf(f, ml.y, L);
-    acc.x = fmaf(f, x.x, acc.x);
-    acc.y = fmaf(f, x.y, acc.y);
-    acc.z = fmaf(f, x.z, acc.z);
-    acc.w = fmaf(f, x.w, acc.w);
+  for (int c = c0; c <= c1; c += NB) {
+    float2 ml[NB];
+    float4 v[NB];
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+      const size_t slot = (size_t)min(c + k, c1) * 2 + (c + k == c0);
+      ml[k] = __ldcg(&a.part_ml[slot * 16 + r]);
+      v[k] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + (slot * 16 + r) * HD + d));
+    }
+    float m = M;
+#pragma unroll
+    for (int k = 0; k < NB; ++k) m = fmaxf(m, ml[k].x);
+    const float f = M == m ? 1.f : ex2(M - m);
+    M = m;
+    L *= f, acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+      if (c + k > c1) break;
+      const float g = ml[k].x == M ? 1.f : ex2(ml[k].x - M);
+      L = fmaf(g, ml[k].y, L);
+      acc.x = fmaf(g, v[k].x, acc.x);
+      acc.y = fmaf(g, v[k].y, acc.y);
+      acc.z = fmaf(g, v[k].z, acc.z);
+      acc.w = fmaf(g, v[k].w, acc.w);
+    }
   }
-  const PRange<!std::is_same<T, __nv_bfloat16>::value> range(__ldcg(a.c.vmax + (size_t)a.seq[i] * a.c.n_kv + head));
+  const PRange<Shape<HD, T>::PS> range(__ldcg(a.c.vmax + (size_t)a.seq[x.i] * a.c.n_kv + x.head));
   const float inv = L == 0.f ? 0.f : range.undo / L;
-  const int t = row / a.group;
-  store4(static_cast<T *>(a.out) + (a.row0[i] + t) * a.ldo + ((int64_t)head * a.group + row - t * a.group) * HD + d,
+  const int t = qr / a.group;
+  store4(static_cast<T *>(a.out) + (a.row0[x.i] + t) * a.ldo + ((int64_t)x.head * a.group + qr - t * a.group) * HD + d,
          make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
   if (a.lse && d == 0)
-    a.lse[((size_t)(a.unit0[i] + rt) * a.c.n_kv + head) * 16 + r] = L == 0.f ? INFINITY : M + log2f(L) - range.bias;
+    a.lse[((size_t)(a.unit0[x.i] + x.rt) * a.c.n_kv + x.head) * 16 + r] = L == 0.f ? INFINITY : M + log2f(L) - range.bias;
 }
 
 // weights[j] = decay weights[j] + sum_r p_rj / sum_j p_rj: with every row's sum
@@ -283,15 +405,15 @@ __global__ void __launch_bounds__(128) kvq_merge_kernel(const __grid_constant__ 
 // formed a second time, which needs no store of rows x keys.  One CTA owns a
 // run of 8 tiles, so nothing is added atomically.  Grid (sequence x run, KV head).
 template <int HD, typename T>
-__global__ void __launch_bounds__(kCons) kvq_weights_kernel(const __grid_constant__ KvqAttnArgs a) {
+__global__ void __launch_bounds__(kWThreads) kvq_weights_kernel(const __grid_constant__ KvqAttnArgs a) {
   constexpr bool QS = sizeof(T) == 4;
   constexpr int KB = kvq_k_bytes(HD), NW = kKvqWeightTiles / 2;
   extern __shared__ __align__(128) uint8_t smem[];
+  using QT = QTile<HD, QS>;
   uint8_t *qs = smem + kKvqWeightTiles * KB;
-  float *mult = reinterpret_cast<float *>(qs + q_bytes<HD, QS>());
-  const uint32_t bars = smem_u32(mult + 16);
+  const uint32_t bars = smem_u32(qs + QT::kBytes);
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  const int i = find_seq(a.wt0, a.n, blockIdx.x), head = blockIdx.y;
+  const int i = find_seq<int32_t>(a.wt0, a.n, blockIdx.x), head = blockIdx.y;
   const int len = a.len[i], T_rows = a.rows[i], R = T_rows * a.group;
   const int rts = (R + kKvqQRows - 1) / kKvqQRows;
   const int t0 = (blockIdx.x - a.wt0[i]) * kKvqWeightTiles;
@@ -310,6 +432,7 @@ __global__ void __launch_bounds__(kCons) kvq_weights_kernel(const __grid_constan
       bulk_g2s(smem_u32(smem + t * KB), a.c.planes + plane * a.c.plane_bytes + (size_t)(t0 + t) * kvq_tile_bytes(HD), KB,
                bars + t * 8);
     }
+  const LaneAt<HD> la((w & 1) * 32, lane);
   float acc[NW][4][2];
 #pragma unroll
   for (int k = 0; k < NW; ++k)
@@ -318,30 +441,33 @@ __global__ void __launch_bounds__(kCons) kvq_weights_kernel(const __grid_constan
   bool ok = true;
   for (int rt = 0; rt < rts; ++rt) {
     if (rt) __syncthreads();
-    load_q<HD, QS, kCons>(static_cast<const T *>(a.q) + a.row0[i] * a.ldq + (int64_t)head * a.group * HD, a.ldq, a.group,
-                          rt * kKvqQRows, R, a.scale_log2, qs, mult, tid);
+    load_q<HD, QS, kWThreads>(static_cast<const T *>(a.q) + a.row0[i] * a.ldq + (int64_t)head * a.group * HD, a.ldq,
+                              a.group, rt * kKvqQRows, R, a.scale_log2, qs, tid);
     __syncthreads();
     const int row0 = rt * kKvqQRows + (lane >> 2), row1 = row0 + 8;
     const float *lse = a.lse + ((size_t)(a.unit0[i] + rt) * a.c.n_kv + head) * 16;
     const float ls0 = row0 < R ? __ldcg(lse + (lane >> 2)) : INFINITY, ls1 = row1 < R ? __ldcg(lse + (lane >> 2) + 8) : INFINITY;
-    const float mu0 = mult[lane >> 2], mu1 = mult[(lane >> 2) + 8];
+    const float2 mu = *reinterpret_cast<const float2 *>(qs + QT::kMult + (lane >> 2) * 8);
     const int lim0 = a.causal ? len - T_rows + row0 / a.group + 1 : len;
     const int lim1 = a.causal ? len - T_rows + row1 / a.group + 1 : len;
     const int lim_all = a.causal ? len - T_rows + rt * kKvqQRows / a.group + 1 : len;
 #pragma unroll
     for (int k = 0; k < NW; ++k) {
-      const int t = 2 * k + (w >> 1), r0 = (w & 1) * 32, key0 = (t0 + t) * kKvqTile + r0;
+      const int t = 2 * k + (w >> 1), key0 = (t0 + t) * kKvqTile + (w & 1) * 32;
       if (t >= nt || key0 >= len || key0 + 32 <= a.first) continue;
       if (rt == 0 && !mbar_wait_warp(bars + t * 8, 0, a.c.err)) ok = false;
       if (!ok) continue;
+      uint64_t sp[4][2];
+      strip_scores<HD, QS>(smem_u32(smem + t * KB) + la.code, smem_u32(smem + t * KB) + la.scale, smem_u32(qs), lane, sp);
       float s[4][4];
-      strip_scores<HD, QS>(smem_u32(smem + t * KB), r0, smem_u32(qs), lane, s);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) unpack2(sp[j][0], s[j][0], s[j][1]), unpack2(sp[j][1], s[j][2], s[j][3]);
       const bool whole = key0 >= a.first && key0 + 32 <= lim_all;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float p = ex2(fmaf(s[j][e], e < 2 ? mu0 : mu1, e < 2 ? -ls0 : -ls1));
+          float p = ex2(fmaf(s[j][e], e < 2 ? mu.x : mu.y, e < 2 ? -ls0 : -ls1));
           if (!whole) {
             const int key = key0 + 8 * j + 2 * (lane & 3) + (e & 1);
             if (key < a.first || key >= (e < 2 ? lim0 : lim1)) p = 0.f;
@@ -380,35 +506,34 @@ __global__ void __launch_bounds__(kCons) kvq_weights_kernel(const __grid_constan
 
 template <int HD, bool QS>
 constexpr int weights_smem() {
-  return kKvqWeightTiles * kvq_k_bytes(HD) + q_bytes<HD, QS>() + 16 * 4 + kKvqWeightTiles * 8;
+  return kKvqWeightTiles * kvq_k_bytes(HD) + QTile<HD, QS>::kBytes + kKvqWeightTiles * 8;
 }
 
 template <int HD, typename T>
 cudaError_t attend_t(const KvqAttnArgs &a, cudaStream_t s) {
-  constexpr int smem = attend_smem<HD, sizeof(T) == 4>();
+  constexpr int smem = Shape<HD, T>::kBytes;
   static_assert(smem <= 227 * 1024, "shared memory of a CTA");
-  static_assert(n_stages<HD>() * 2 * kvq_tile_bytes(HD) >= 4 * 16 * HD * 4, "the warps' results fit the ring");
   cudaError_t e = cudaFuncSetAttribute(kvq_attend_kernel<HD, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return kvq_launch(kvq_attend_kernel<HD, T>, dim3(a.cta0[a.n], a.c.n_kv), dim3(kThreads), smem, s, a);
+  return kvq_launch(kvq_attend_kernel<HD, T>, dim3(a.ctas), dim3(Shape<HD, T>::kThreads), smem, s, a);
 }
 template <int HD, typename T>
 cudaError_t merge_t(const KvqAttnArgs &a, cudaStream_t s) {
-  return kvq_launch(kvq_merge_kernel<HD, T>, dim3(a.split0[a.n], a.c.n_kv, 16 * HD / 4 / 128), dim3(128), 0, s, a);
+  return kvq_launch(kvq_merge_kernel<HD, T>, dim3(a.ctas - 1, 16 * HD / 4 / 128), dim3(128), 0, s, a);
 }
 template <int HD, typename T>
 cudaError_t weights_t(const KvqAttnArgs &a, cudaStream_t s) {
   constexpr int smem = weights_smem<HD, sizeof(T) == 4>();
   cudaError_t e = cudaFuncSetAttribute(kvq_weights_kernel<HD, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return kvq_launch(kvq_weights_kernel<HD, T>, dim3(a.wt0[a.n], a.c.n_kv), dim3(kCons), smem, s, a);
+  return kvq_launch(kvq_weights_kernel<HD, T>, dim3(a.wt0[a.n], a.c.n_kv), dim3(kWThreads), smem, s, a);
 }
 template <int HD, typename T>
 int ctas_t() {
-  constexpr int smem = attend_smem<HD, sizeof(T) == 4>();
+  constexpr int smem = Shape<HD, T>::kBytes;
   int n = 0;
   if (cudaFuncSetAttribute(kvq_attend_kernel<HD, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
-      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kvq_attend_kernel<HD, T>, kThreads, smem) != cudaSuccess)
+      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kvq_attend_kernel<HD, T>, Shape<HD, T>::kThreads, smem) != cudaSuccess)
     return 1;
   return n < 1 ? 1 : n;
 }

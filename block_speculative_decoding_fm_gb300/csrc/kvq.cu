@@ -158,6 +158,18 @@ fm_status end(fm_kvq *c, cudaStream_t s) {
   return FM_OK;
 }
 
+// whether every CTA's share of the stages begins where a unit begins
+bool whole_units(const KvqAttnArgs &a) {
+  const int64_t W = a.st0[a.n];
+  int i = 0;
+  for (int64_t b = 1; b < a.ctas; ++b) {
+    const int64_t x = b * W / a.ctas;
+    while (a.st0[i + 1] <= x) ++i;
+    if ((x - a.st0[i]) % a.stages[i]) return false;
+  }
+  return true;
+}
+
 template <typename T>
 fm_status dev_alloc(fm_kvq *c, T **p, size_t n) {
   void *q = nullptr;
@@ -191,7 +203,7 @@ fm_status setup(fm_kvq *c, cudaStream_t s) {
     c->ctas[t] = kvq_attn_ctas_per_sm(g.head_dim, t);
     most = c->ctas[t] > most ? c->ctas[t] : most;
   }
-  c->slots = 2 * c->n_sm * most + 2 * g.n_kv_heads;
+  c->slots = 2 * c->n_sm * most;
   KTRY(dev_alloc(c, &c->planes, planes * c->plane_bytes));
   KTRY(dev_alloc(c, &c->weights, planes * c->rows_pad));
   KTRY(dev_alloc(c, &c->vmax, planes));
@@ -455,59 +467,43 @@ fm_status fm_kvq_attend(fm_kvq *c, int32_t layer, int32_t n_seqs, const int32_t 
   int64_t row0 = 0;
   for (int i0 = 0; i0 < n_seqs;) {
     // the sequences of this launch: 64, and as many units as the workspace has row sums for
-    int64_t units = 0, work = 0;   // work: tiles x units
+    int64_t units = 0, work = 0;
+    int un = 0, wt = 0;
     a.n = 0;
     a.call0 = i0;
     int i = i0;
     for (; i < n_seqs && a.n < kKvqSeqs; ++i) {
-      const int n = n_rows_host[i], L = len[seq_ids_host[i]];
-      const int64_t rts = ((int64_t)n * group + kKvqQRows - 1) / kKvqQRows;
-      if (a.n && (units + rts * nkv > kMaxUnits)) break;
-      a.seq[a.n] = seq_ids_host[i];
-      a.len[a.n] = L;
-      a.rows[a.n] = n;
-      a.row0[a.n++] = row0;
-      row0 += n;
-      units += rts * nkv;
+      const int n = n_rows_host[i], L = len[seq_ids_host[i]], j = a.n;
+      const int rts = (int)(((int64_t)n * group + kKvqQRows - 1) / kKvqQRows);
+      if (j && units + (int64_t)rts * nkv > kMaxUnits) break;
       const int t0 = first_row / kKvqTile, t1 = (L + kKvqTile - 1) / kKvqTile;
-      if (t1 > t0) work += rts * nkv * (t1 - t0);
-    }
-    // Tiles a CTA: the SMs filled once.  Two tiles (a stage) at least, and whole stages; a unit that is
-    // split has two chunks or more, so the chunks of split units are at most twice the aim.
-    const int64_t aim = (int64_t)c->n_sm * c->ctas[type];
-    int64_t chunk = (work + aim - 1) / aim;
-    chunk = chunk < 2 ? 2 : (chunk + 1) / 2 * 2;
-    a.chunk = (int32_t)(chunk > INT_MAX / 2 ? INT_MAX / 2 : chunk);
-    int ctas = 0, un = 0, slot = 0, split = 0, wt = 0;
-    for (int j = 0; j < a.n; ++j) {
-      const int rts = (int)(((int64_t)a.rows[j] * group + kKvqQRows - 1) / kKvqQRows);
-      const int t1 = (a.len[j] + kKvqTile - 1) / kKvqTile;
-      int tiles = t1 - first_row / kKvqTile;
-      if (tiles < 0) tiles = 0;
-      int chunks = (tiles + a.chunk - 1) / a.chunk;
-      if (chunks < 1) chunks = 1;
-      a.cta0[j] = ctas;
+      a.seq[j] = seq_ids_host[i];
+      a.len[j] = L;
+      a.rows[j] = n;
+      a.row0[j] = row0;
+      a.stages[j] = t1 > t0 ? (t1 - t0 + kKvqStage - 1) / kKvqStage : 1;
+      a.st0[j] = work;
       a.unit0[j] = un;
-      a.slot0[j] = slot;
-      a.split0[j] = split;
       a.wt0[j] = wt;
-      ctas += chunks * rts;
+      row0 += n;
+      units += (int64_t)rts * nkv;
+      work += (int64_t)rts * nkv * a.stages[j];
       un += rts;
-      if (chunks > 1) {
-        slot += chunks * rts;
-        split += rts;
-      }
       if (rts > 0) wt += (t1 + kKvqWeightTiles - 1) / kKvqWeightTiles;
+      ++a.n;
     }
-    a.cta0[a.n] = ctas;
+    a.st0[a.n] = work;
     a.unit0[a.n] = un;
-    a.slot0[a.n] = slot;
-    a.split0[a.n] = split;
     a.wt0[a.n] = wt;
-    if ((int64_t)slot * nkv > c->slots) return kfail(c, FM_ERR_UNSUPPORTED, "more partial results than the workspace holds");
-    if (ctas > 0) KCK(launch_kvq_attend(a, hd, s));
-    if (split > 0) KCK(launch_kvq_merge(a, hd, s));
-    if (keep_w && wt > 0) KCK(launch_kvq_weights(a, hd, s));
+    // every CTA that the SMs hold at once takes the same number of stages, whatever unit they belong to
+    const int64_t most_ctas = (int64_t)c->n_sm * c->ctas[type];
+    a.ctas = (int32_t)(work < most_ctas ? work : most_ctas);
+    if (work > 0) {
+      KCK(launch_kvq_attend(a, hd, s));
+      // (a unit that begins and ends inside a CTA's share needs no joining: no launch where shares are whole units)
+      if (a.ctas > 1 && !whole_units(a)) KCK(launch_kvq_merge(a, hd, s));
+      if (keep_w && wt > 0) KCK(launch_kvq_weights(a, hd, s));
+    }
     i0 = i;
   }
   return end(c, s);

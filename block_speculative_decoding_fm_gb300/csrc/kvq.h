@@ -22,6 +22,7 @@ namespace fm {
 
 constexpr int kKvqTile = 64;       // rows a tile
 constexpr int kKvqSeqs = 64;       // sequences a launch
+constexpr int kKvqStage = 2;       // tiles a stage: what the attention kernel fetches and deals out
 constexpr int kKvqQRows = 16;      // query rows (block row x head of the group) a CTA carries
 
 enum KvqType : int32_t { KVQ_F32 = 0, KVQ_F16 = 1, KVQ_BF16 = 2 };
@@ -80,10 +81,9 @@ struct KvqAttnArgs {
   float scale_log2;       // scale * log2(e)
   int32_t causal, first;  // row t of T sees rows first <= j < (causal ? len - T + t + 1 : len)
   int32_t n;              // sequences of this launch
-  int32_t chunk;          // tiles a CTA
-  int32_t n_split;        // units whose rows are split over CTAs (they have partial results)
-  float *part_o;          // [slots][16][hd] unnormalised partial outputs
-  float2 *part_ml;        // [slots][16] (reference, row sum)
+  int32_t ctas;           // CTAs of the launch; CTA b takes stages [b W / ctas, (b + 1) W / ctas), W = st0[n]
+  float *part_o;          // [2 ctas][16][hd] unnormalised partial outputs
+  float2 *part_ml;        // [2 ctas][16] (reference, row sum)
   float *lse;             // [units][16] log2 of the row sums, for the weights; or null
   float decay;            // weights: w = decay w + this call's
   float *w_out;           // [call sequences][n_kv][ldw] or null
@@ -91,10 +91,10 @@ struct KvqAttnArgs {
   int32_t call0;
   int64_t row0[kKvqSeqs];
   int32_t seq[kKvqSeqs], len[kKvqSeqs], rows[kKvqSeqs];
-  int32_t cta0[kKvqSeqs + 1];    // prefix sums of (row tiles x chunks): grid x
-  int32_t unit0[kKvqSeqs + 1];   // prefix sums of row tiles; a unit is (row tile, KV head)
-  int32_t slot0[kKvqSeqs + 1];   // prefix sums of the CTAs of split sequences: partial slots / n_kv
-  int32_t split0[kKvqSeqs + 1];  // prefix sums of row tiles of split sequences: the merge's grid
+  // A unit is a (KV head, row tile) of a sequence; its keys are stages of two tiles, one at least.
+  int32_t stages[kKvqSeqs];      // of a unit
+  int64_t st0[kKvqSeqs + 1];     // prefix sums of units x stages
+  int32_t unit0[kKvqSeqs + 1];   // prefix sums of row tiles (lse is by (row tile, KV head))
   int32_t wt0[kKvqSeqs + 1];     // weights: prefix sums of the CTAs of each sequence
 };
 int kvq_attn_ctas_per_sm(int hd, int type);

@@ -34,7 +34,8 @@ def stored(x: np.ndarray) -> np.ndarray:
 
 def attend(q: np.ndarray, k: np.ndarray, v: np.ndarray, scale: float, causal: bool = False, first: int = 0):
     """q [T, H, hd] over one sequence's rows k, v [L, Hkv, hd] -> (out [T, H, hd], weights [Hkv, L],
-    mass [T, H, hd]: sum_j p_j |v_j|, reach [T, H]: the largest sum_d |q_d k_jd| scale -- the scales of the errors)."""
+    mass [T, H, hd]: sum_j p_j |v_j|, reach [T, H]: the largest sum_d |q_d| K_jd scale, K_jd the largest |k_j| of d's
+    group -- the scales of the errors)."""
     T, H, hd = q.shape
     L, hkv = k.shape[0], k.shape[1]
     out, mass = np.zeros((T, H, hd)), np.zeros((T, H, hd))
@@ -48,7 +49,8 @@ def attend(q: np.ndarray, k: np.ndarray, v: np.ndarray, scale: float, causal: bo
             g = h // (H // hkv)
             kk, vv = k[first:end, g], v[first:end, g]
             s = kk @ q[t, h] * scale
-            reach[t, h] = abs(scale) * np.max(np.abs(kk) @ np.abs(q[t, h]))
+            top = np.abs(kk).reshape(len(kk), -1, min(GROUP, hd)).max(-1)
+            reach[t, h] = abs(scale) * np.max(np.repeat(top, min(GROUP, hd), -1) @ np.abs(q[t, h]))
             p = np.exp(s - s.max())
             p /= p.sum()
             out[t, h] = p @ vv
