@@ -3,13 +3,14 @@
 //
 //   O[r] = sum_j p_rj v_j / sum_j p_rj,  p_rj = exp2(t_rj - m_r),
 //   t_rj = scale log2(e) q_r . k_j  over the rows j that r sees,
-// one pass over the cache with a running reference m and sum; the keys of a
-// (sequence, KV head) are dealt to CTAs in chunks of whole tiles, and a second,
-// short launch joins the chunks of sequences that have more than one.
+// one pass over the cache with a running reference m and sum; a
+// call's (sequence, KV head, 16 query rows) units lie end to end and every CTA
+// takes an equal share of their stages (two tiles, 128 rows); where a unit is
+// shared, the CTA that finishes last joins the parts, in their order.
 //
-// A CTA carries 16 query rows (block row x head of the KV head's group): warp 4
-// streams stages of two tiles (128 rows, K and V codes and scales in one bulk copy)
-// into a ring; warps 0..3 take a strip of 32 rows each.  With 16 query rows the
+// A CTA carries 16 query rows (block row x head of the KV head's group) at a time.  Its
+// warps work in groups of four: a group has its own ring of stages (K and V codes
+// and scales of 128 rows in one bulk copy) and its warps take a strip of 32 rows each.  With 16 query rows the
 // product is a skinny one, and the codes pass from shared memory (ldmatrix)
 // through a few integer and f16 operations straight into mma.sync fragments:
 // they never go back to shared memory as f16, which a tcgen05 operand would need
@@ -27,19 +28,20 @@ using namespace kvq;
 constexpr float kLazy = 8.f;               // log2 of the growth a reference tolerates
 constexpr int kWThreads = 128;             // the weights pass
 
-// The attention kernel's shape: groups of four warps (they take the stages in turn), ring stages, CTAs an SM.
+// The attention kernel's shape: groups of four warps (they take the stages in turn) and ring stages; one
+// CTA an SM, as wide as the registers allow, so that a unit is in few parts.
 template <int HD, typename T>
 struct Shape {
   static constexpr bool QS = sizeof(T) == 4;                          // f32 queries: f16 hi + lo
   static constexpr bool PS = !std::is_same<T, __nv_bfloat16>::value;  // f16 and f32 outputs: P' too
   static constexpr bool SV = sizeof(T) == 4;                          // f32 outputs: signed codes (no sums to take off)
-  static constexpr int NG = HD == 256 ? 2 : 1;
+  static constexpr int NG = HD == 64 ? 4 : HD == 128 ? 3 : 2;
   static constexpr int NS = HD == 64 ? 4 : HD == 128 ? 3 : 2;         // of a group's own ring
-  static constexpr int MB = HD == 64 ? 4 : HD == 128 ? 3 : 1;
   static constexpr int NW = 4 * NG, kThreads = 128 * NG;
   static constexpr int SB = kKvqStage * kvq_tile_bytes(HD);
   static constexpr int HC = 64;                                       // dims joined at a time
-  static constexpr int kScratch = NW / 2 * 16 * HC * 4;
+  static constexpr int kFold = NW > 8 ? 8 : NW > 4 ? 4 : 2;           // warps left after the first step of the joining
+  static constexpr int kScratch = (NW - kFold > kFold / 2 ? NW - kFold : kFold / 2) * 16 * HC * 4;
   static constexpr int kBytes = NG * NS * SB + kScratch + QTile<HD, QS>::kBytes + 2 * NW * 16 * 4 + NG * 2 * NS * 8 + NG * 32;
 };
 
@@ -60,16 +62,21 @@ __device__ __forceinline__ void store4(T *p, float4 v) {
   }
 }
 
-// A stretch of a CTA's share: stages [s0, s0 + n) of one unit.
+// A CTA's share of the stages
+__device__ __forceinline__ int share_begin(const KvqAttnArgs &a, int b) { return b * a.share + min(b, a.extra); }
+__device__ __forceinline__ int cta_of(const KvqAttnArgs &a, int stage) {
+  const int wide = a.extra * (a.share + 1);
+  return stage < wide ? stage / (a.share + 1) : a.extra + (stage - wide) / a.share;
+}
+
+// A stretch of a share: stages [s0, s0 + n) of one unit.
 struct Stretch {
   int i, head, rt, s0, n;
-  __device__ __forceinline__ Stretch(const KvqAttnArgs &a, int64_t at, int64_t end) {
-    i = find_seq<int64_t>(a.st0, a.n, at);
-    const int64_t rel = at - a.st0[i];
-    const int S = a.stages[i];
-    const int unit = static_cast<int>(rel / S);
-    s0 = static_cast<int>(rel - (int64_t)unit * S);
-    n = static_cast<int>(min((int64_t)(S - s0), end - at));
+  __device__ __forceinline__ Stretch(const KvqAttnArgs &a, int at, int end) {
+    i = find_seq<int32_t>(a.st0, a.n, at);
+    const int rel = at - a.st0[i], S = a.stages[i], unit = rel / S;
+    s0 = rel - unit * S;
+    n = min(S - s0, end - at);
     const int rts = (a.rows[i] * a.group + kKvqQRows - 1) / kKvqQRows;
     head = unit / rts;
     rt = unit - head * rts;
@@ -78,8 +85,8 @@ struct Stretch {
 
 // Where a group's copies have got to (in shared memory: one lane's business, once a stage).
 struct Cursor {
-  int64_t at;             // the share's stage after the stretch that the cursor is in
   const uint8_t *src;     // the next stage
+  int32_t at;             // the share's stage after the stretch that the cursor is in
   int32_t left;           // stages of the stretch that are the group's
   int32_t tiles;          // tiles from the next stage to the unit's end
   int32_t issued;
@@ -88,13 +95,13 @@ static_assert(sizeof(Cursor) <= 32, "a cursor's place in shared memory");
 
 // The next of the group's stages into its ring; false where a wait gave up.
 template <int HD, typename Sh>
-__device__ __forceinline__ bool issue_stage(const KvqAttnArgs &a, Cursor *cu, int64_t w_end, int grp, uint32_t ring,
+__device__ __forceinline__ bool issue_stage(const KvqAttnArgs &a, Cursor *cu, int w_end, int grp, uint32_t ring,
                                             uint32_t full, uint32_t empty) {
   constexpr int TB = kvq_tile_bytes(HD);
   int left = cu->left, tiles = cu->tiles;
   const uint8_t *src = cu->src;
   while (left == 0) {
-    const int64_t at = cu->at;
+    const int at = cu->at;
     if (at >= w_end) return true;
     const Stretch x(a, at, w_end);
     const int t = a.first / kKvqTile + (x.s0 + grp) * kKvqStage;
@@ -119,8 +126,54 @@ __device__ __forceinline__ bool issue_stage(const KvqAttnArgs &a, Cursor *cu, in
   return true;
 }
 
+// The parts of a split unit into its output rows, in part order: CTA `first` has the unit's first stages (its
+// second slot), the CTAs after it up to `last` the rest.
+template <int HD, typename T, int NT>
+__device__ __forceinline__ void join_parts(const KvqAttnArgs &a, const Stretch &x, int first, int last, float undo, float bias,
+                                           float *lse, int tid) {
+  constexpr int NB = 8;    // parts whose loads are in flight together
+  const int R = a.rows[x.i] * a.group;
+  for (int e = tid; e < 16 * HD / 4; e += NT) {
+    const int r = e / (HD / 4), d = 4 * (e % (HD / 4)), qr = x.rt * kKvqQRows + r;
+    if (qr >= R) break;
+    float M = -INFINITY, L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = first; c <= last; c += NB) {
+      float2 ml[NB];
+      float4 v[NB];
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        const size_t slot = (size_t)min(c + k, last) * 2 + (c + k == first);
+        ml[k] = __ldcg(&a.part_ml[slot * 16 + r]);
+        v[k] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + (slot * 16 + r) * HD + d));
+      }
+      float m = M;
+#pragma unroll
+      for (int k = 0; k < NB; ++k) m = fmaxf(m, ml[k].x);
+      const float f = M == m ? 1.f : ex2(M - m);
+      M = m;
+      L *= f, acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        if (c + k > last) break;
+        const float g = ml[k].x == M ? 1.f : ex2(ml[k].x - M);
+        L = fmaf(g, ml[k].y, L);
+        acc.x = fmaf(g, v[k].x, acc.x);
+        acc.y = fmaf(g, v[k].y, acc.y);
+        acc.z = fmaf(g, v[k].z, acc.z);
+        acc.w = fmaf(g, v[k].w, acc.w);
+      }
+    }
+    const float inv = L == 0.f ? 0.f : undo / L;
+    const int t = qr / a.group;
+    store4(static_cast<T *>(a.out) + (a.row0[x.i] + t) * a.ldo + ((int64_t)x.head * a.group + qr - t * a.group) * HD + d,
+           make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+    if (lse && d == 0) lse[r] = L == 0.f ? INFINITY : M + log2f(L) - bias;
+  }
+}
+
 template <int HD, typename T>
-__global__ void __launch_bounds__(Shape<HD, T>::kThreads, Shape<HD, T>::MB)
+__global__ void __launch_bounds__(Shape<HD, T>::kThreads, 1)
     kvq_attend_kernel(const __grid_constant__ KvqAttnArgs a) {
   using Sh = Shape<HD, T>;
   using QT = QTile<HD, Sh::QS>;
@@ -134,10 +187,11 @@ __global__ void __launch_bounds__(Shape<HD, T>::kThreads, Shape<HD, T>::MB)
   uint64_t *bar = reinterpret_cast<uint64_t *>(wl + NW * 16);                   // [group][full, empty][stage]
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int grp = NG == 1 ? 0 : w >> 2;     // a group takes the stages grp, grp + NG, ... of a stretch
+  __shared__ int s_last;
+  __shared__ float2 s_row[16];               // references and sums of the query rows, all warps
   Cursor *cu = reinterpret_cast<Cursor *>(bar + NG * 2 * NS) + grp;
   const uint32_t full = smem_u32(bar + grp * 2 * NS), empty = full + NS * 8, ring = smem_u32(smem) + grp * NS * SB;
-  const int64_t W = a.st0[a.n];
-  const int64_t w_beg = blockIdx.x * W / a.ctas, w_end = (blockIdx.x + 1) * W / a.ctas;
+  const int w_beg = share_begin(a, blockIdx.x), w_end = share_begin(a, blockIdx.x + 1);
 
   pdl_trigger();
   if (tid == 0) {
@@ -163,14 +217,14 @@ __global__ void __launch_bounds__(Shape<HD, T>::kThreads, Shape<HD, T>::MB)
   const int row = lane >> 2;
   int slot = 0;
   uint32_t par = 0;
-  for (int64_t at = w_beg; at < w_end;) {
+  for (int at = w_beg; at < w_end;) {
     const Stretch x(a, at, w_end);
     const int len = a.len[x.i], T_rows = a.rows[x.i], R = T_rows * a.group, rq = x.rt * kKvqQRows;
     const size_t plane = (size_t)a.seq[x.i] * a.c.n_kv + x.head;
     load_q<HD, QS, kCons>(static_cast<const T *>(a.q) + a.row0[x.i] * a.ldq + (int64_t)x.head * a.group * HD, a.ldq, a.group,
                           rq, R, a.scale_log2, qs, tid);
     const PRange<PS> range(__ldcg(a.c.vmax + plane));
-    named_sync(1, kCons);
+    __syncthreads();
     const float2 mu = *reinterpret_cast<const float2 *>(qs + QT::kMult + row * 8);
     // the rows that this lane's two query rows see end at lim; rows past R follow the last (they are not stored)
     const int ra = min(rq + row, R - 1), rb = min(rq + row + 8, R - 1);
@@ -187,7 +241,7 @@ __global__ void __launch_bounds__(Shape<HD, T>::kThreads, Shape<HD, T>::MB)
     for (int k = grp; k < x.n; k += NG) {
       // a stage ahead of the ring's end; then this one (a wait that gave up ends the warp's work, not its barriers)
       if (copies && ok) ok = issue_stage<HD, Sh>(a, cu, w_end, grp, ring, full, empty);
-      ok = __all_sync(0xffffffffu, ok) && mbar_wait_warp(full + slot * 8, par, a.c.err);
+      ok = __all_sync(0xffffffffu, ok && mbar_wait_bounded(full + slot * 8, par, a.c.err));
       if (!ok) break;
       if (key0 < len && key0 + 32 > a.first) {
         const uint32_t code = code0 + slot * SB, scale = scale0 + slot * SB;
@@ -216,20 +270,17 @@ __global__ void __launch_bounds__(Shape<HD, T>::kThreads, Shape<HD, T>::MB)
           x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, sh));
           x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, sh));
         }
-        // (a row that sees none of the strip's keys: -inf, also where its factor is 0)
-        x0 = x0 == -INFINITY ? x0 : x0 * mu.x;
-        x1 = x1 == -INFINITY ? x1 : x1 * mu.y;
+        x0 *= mu.x, x1 *= mu.y;
         if (__any_sync(0xffffffffu, x0 > m0 + kLazy || x1 > m1 + kLazy)) {
           const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
           const float f0 = n0 == m0 ? 1.f : ex2(m0 - n0), f1 = n1 == m1 ? 1.f : ex2(m1 - n1);
           m0 = n0, m1 = n1;
-          l0 = fma2(l0, pack2(f0, f0), 0ull), l1 = fma2(l1, pack2(f1, f1), 0ull);
+          l0 = mul2(l0, pack2(f0, f0)), l1 = mul2(l1, pack2(f1, f1));
 #pragma unroll
           for (int n = 0; n < HD / 8; ++n) o[n][0] *= f0, o[n][1] *= f0, o[n][2] *= f1, o[n][3] *= f1;
           if constexpr (!SV) cor[0] *= f0, cor[1] *= f0, cor[2] *= f1, cor[3] *= f1;
         }
         const float b0 = range.bias - (m0 == -INFINITY ? 0.f : m0), b1 = range.bias - (m1 == -INFINITY ? 0.f : m1);
-        const bool masked = key0 < a.first || key0 + 32 > lim_all;
         const uint64_t mu0 = pack2(mu.x, mu.x), mu1 = pack2(mu.y, mu.y), bb0 = pack2(b0, b0), bb1 = pack2(b1, b1);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -237,7 +288,7 @@ __global__ void __launch_bounds__(Shape<HD, T>::kThreads, Shape<HD, T>::MB)
           unpack2(fma2(pack2(s[j][0], s[j][1]), mu0, bb0), t[0], t[1]);
           unpack2(fma2(pack2(s[j][2], s[j][3]), mu1, bb1), t[2], t[3]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) t[e] = masked && s[j][e] == -INFINITY ? 0.f : ex2(t[e]);
+          for (int e = 0; e < 4; ++e) t[e] = ex2(t[e]);
           l0 = add2(l0, pack2(t[0], t[1]));
           l1 = add2(l1, pack2(t[2], t[3]));
 #pragma unroll
@@ -268,20 +319,25 @@ __global__ void __launch_bounds__(Shape<HD, T>::kThreads, Shape<HD, T>::MB)
       wl[w * 16 + row] = ls0;
       wl[w * 16 + row + 8] = ls1;
     }
-    named_sync(1, kCons);
-    float M0 = -INFINITY, M1 = -INFINITY;
+    __syncthreads();
+    if (tid < 16) {
+      float M = -INFINITY, L = 0.f;
 #pragma unroll
-    for (int v = 0; v < NW; ++v) {
-      M0 = fmaxf(M0, wm[v * 16 + row]);
-      M1 = fmaxf(M1, wm[v * 16 + row + 8]);
+      for (int u = 0; u < NW; ++u) M = fmaxf(M, wm[u * 16 + tid]);
+#pragma unroll
+      for (int u = 0; u < NW; ++u) L += (wm[u * 16 + tid] == M ? 1.f : ex2(wm[u * 16 + tid] - M)) * wl[u * 16 + tid];
+      s_row[tid] = make_float2(M, L);
     }
+    __syncthreads();
+    const float M0 = s_row[row].x, M1 = s_row[row + 8].x;
     finish_o<HD, SV>(o, cor, lane, m0 == M0 ? 1.f : ex2(m0 - M0), m1 == M1 ? 1.f : ex2(m1 - M1));
     const bool whole = x.n == a.stages[x.i];
     const size_t slot_g = (size_t)blockIdx.x * 2 + (x.s0 == 0);   // a unit begun here, or one continued
+    float *lse = a.lse ? a.lse + ((size_t)(a.unit0[x.i] + x.rt) * a.c.n_kv + x.head) * 16 : nullptr;
 #pragma unroll
     for (int c0 = 0; c0 < HD; c0 += HC) {
 #pragma unroll
-      for (int half = NW / 2; half >= 1; half >>= 1) {
+      for (int half = Sh::kFold; half >= 1; half >>= 1) {
         float4 *buf = reinterpret_cast<float4 *>(scratch) + (w & (half - 1)) * (16 * HC / 4) + lane;
         if (w >= half && w < 2 * half) {
 #pragma unroll
@@ -290,8 +346,8 @@ __global__ void __launch_bounds__(Shape<HD, T>::kThreads, Shape<HD, T>::MB)
             buf[n * 32] = make_float4(v[0], v[1], v[2], v[3]);
           }
         }
-        named_sync(1, kCons);
-        if (w < half) {
+        __syncthreads();
+        if (w < half && w + half < NW) {
 #pragma unroll
           for (int n = 0; n < HC / 8; ++n) {
             const float4 v = buf[n * 32];
@@ -311,16 +367,12 @@ __global__ void __launch_bounds__(Shape<HD, T>::kThreads, Shape<HD, T>::MB)
           scratch[(row + 8) * HC + d + 4] = v[3];
         }
       }
-      named_sync(1, kCons);
+      __syncthreads();
 #pragma unroll
       for (int e = tid; e < 16 * HC / 4; e += kCons) {
         const int r = e / (HC / 4), d = 4 * (e % (HC / 4)), qr = rq + r;
         const float4 v = *reinterpret_cast<const float4 *>(scratch + r * HC + d);
-        float M = -INFINITY, L = 0.f;
-#pragma unroll
-        for (int u = 0; u < NW; ++u) M = fmaxf(M, wm[u * 16 + r]);
-#pragma unroll
-        for (int u = 0; u < NW; ++u) L += (wm[u * 16 + r] == M ? 1.f : ex2(wm[u * 16 + r] - M)) * wl[u * 16 + r];
+        const float M = s_row[r].x, L = s_row[r].y;
         if (!whole) {
           *reinterpret_cast<float4 *>(a.part_o + (slot_g * 16 + r) * HD + c0 + d) = v;
           if (c0 + d == 0) a.part_ml[slot_g * 16 + r] = make_float2(M, L);
@@ -330,74 +382,31 @@ __global__ void __launch_bounds__(Shape<HD, T>::kThreads, Shape<HD, T>::MB)
           store4(static_cast<T *>(a.out) + (a.row0[x.i] + t) * a.ldo +
                      ((int64_t)x.head * a.group + qr - t * a.group) * HD + c0 + d,
                  make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
-          if (a.lse && c0 + d == 0)
-            a.lse[((size_t)(a.unit0[x.i] + x.rt) * a.c.n_kv + x.head) * 16 + r] =
-                L == 0.f ? INFINITY : M + log2f(L) - range.bias;
+          if (lse && c0 + d == 0) lse[r] = L == 0.f ? INFINITY : M + log2f(L) - range.bias;
         }
       }
-      if (c0 + HC < HD) named_sync(1, kCons);
+      if (c0 + HC < HD) __syncthreads();
+    }
+    if (!whole) {   // the CTA that finishes the last part of a unit joins them all, in their order
+      int32_t *ticket = a.tickets + (size_t)(a.unit0[x.i] + x.rt) * a.c.n_kv + x.head;
+      const int u0 = at - x.s0, first = cta_of(a, u0), last = cta_of(a, u0 + a.stages[x.i] - 1);
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) s_last = atomicAdd(ticket, 1) == last - first;
+      __syncthreads();
+      if (s_last) {
+        __threadfence();
+        if (tid == 0) *ticket = 0;
+        join_parts<HD, T, kCons>(a, x, first, last, range.undo, range.bias, lse, tid);
+      }
     }
     at += x.n;
-    if (at < w_end) named_sync(1, kCons);   // the next stretch writes the queries, the references and the scratch
+    if (at < w_end) __syncthreads();   // the next stretch writes the queries, the references and the scratch
   }
   // nothing is left in flight when the CTA ends (a consumer may have given up)
   if (copies)
     for (int k = max(0, cu->issued - NS); k < cu->issued; ++k) mbar_wait_drain(full + k % NS * 8, (k / NS) & 1);
   __syncthreads();
-}
-
-// Joins the parts of a unit that several CTAs share, in their order.  Block x looks after the boundary between
-// CTAs x and x + 1: it works where that is the first boundary inside a unit.  Grid (ctas - 1, 16 HD / 4 / 128).
-template <int HD, typename T>
-__global__ void __launch_bounds__(128) kvq_merge_kernel(const __grid_constant__ KvqAttnArgs a) {
-  constexpr int NB = 8;    // parts whose loads are in flight together
-  pdl_trigger();
-  const int64_t W = a.st0[a.n], G = a.ctas;
-  const int64_t cut = (blockIdx.x + 1) * W / G;
-  const Stretch x(a, cut, W);
-  pdl_wait();   // every block, so that a later launch that waits for this one waits for what came before too
-  if (x.s0 == 0 || cut - x.s0 < blockIdx.x * W / G) return;
-  // the last CTA with a stage of the unit: its share begins at or before the unit's last stage
-  const int64_t unit_end = cut - x.s0 + a.stages[x.i];
-  const int c0 = blockIdx.x, c1 = static_cast<int>((unit_end * G - 1) / W);
-  const int it = blockIdx.y * 128 + threadIdx.x;
-  const int r = it / (HD / 4), d = 4 * (it % (HD / 4)), qr = x.rt * kKvqQRows + r;
-  if (qr >= a.rows[x.i] * a.group) return;
-  float M = -INFINITY, L = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int c = c0; c <= c1; c += NB) {
-    float2 ml[NB];
-    float4 v[NB];
-#pragma unroll
-    for (int k = 0; k < NB; ++k) {
-      const size_t slot = (size_t)min(c + k, c1) * 2 + (c + k == c0);
-      ml[k] = __ldcg(&a.part_ml[slot * 16 + r]);
-      v[k] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + (slot * 16 + r) * HD + d));
-    }
-    float m = M;
-#pragma unroll
-    for (int k = 0; k < NB; ++k) m = fmaxf(m, ml[k].x);
-    const float f = M == m ? 1.f : ex2(M - m);
-    M = m;
-    L *= f, acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
-#pragma unroll
-    for (int k = 0; k < NB; ++k) {
-      if (c + k > c1) break;
-      const float g = ml[k].x == M ? 1.f : ex2(ml[k].x - M);
-      L = fmaf(g, ml[k].y, L);
-      acc.x = fmaf(g, v[k].x, acc.x);
-      acc.y = fmaf(g, v[k].y, acc.y);
-      acc.z = fmaf(g, v[k].z, acc.z);
-      acc.w = fmaf(g, v[k].w, acc.w);
-    }
-  }
-  const PRange<Shape<HD, T>::PS> range(__ldcg(a.c.vmax + (size_t)a.seq[x.i] * a.c.n_kv + x.head));
-  const float inv = L == 0.f ? 0.f : range.undo / L;
-  const int t = qr / a.group;
-  store4(static_cast<T *>(a.out) + (a.row0[x.i] + t) * a.ldo + ((int64_t)x.head * a.group + qr - t * a.group) * HD + d,
-         make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-  if (a.lse && d == 0)
-    a.lse[((size_t)(a.unit0[x.i] + x.rt) * a.c.n_kv + x.head) * 16 + r] = L == 0.f ? INFINITY : M + log2f(L) - range.bias;
 }
 
 // weights[j] = decay weights[j] + sum_r p_rj / sum_j p_rj: with every row's sum
@@ -518,10 +527,6 @@ cudaError_t attend_t(const KvqAttnArgs &a, cudaStream_t s) {
   return kvq_launch(kvq_attend_kernel<HD, T>, dim3(a.ctas), dim3(Shape<HD, T>::kThreads), smem, s, a);
 }
 template <int HD, typename T>
-cudaError_t merge_t(const KvqAttnArgs &a, cudaStream_t s) {
-  return kvq_launch(kvq_merge_kernel<HD, T>, dim3(a.ctas - 1, 16 * HD / 4 / 128), dim3(128), 0, s, a);
-}
-template <int HD, typename T>
 cudaError_t weights_t(const KvqAttnArgs &a, cudaStream_t s) {
   constexpr int smem = weights_smem<HD, sizeof(T) == 4>();
   cudaError_t e = cudaFuncSetAttribute(kvq_weights_kernel<HD, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -557,10 +562,6 @@ int kvq_attn_ctas_per_sm(int hd, int type) { KVQ_DISPATCH(ctas_t) }
 cudaError_t launch_kvq_attend(const KvqAttnArgs &a, int hd, cudaStream_t s) {
   const int type = a.type;
   KVQ_DISPATCH(attend_t, a, s)
-}
-cudaError_t launch_kvq_merge(const KvqAttnArgs &a, int hd, cudaStream_t s) {
-  const int type = a.type;
-  KVQ_DISPATCH(merge_t, a, s)
 }
 cudaError_t launch_kvq_weights(const KvqAttnArgs &a, int hd, cudaStream_t s) {
   const int type = a.type;

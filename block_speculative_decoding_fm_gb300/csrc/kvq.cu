@@ -29,7 +29,7 @@ struct fm_kvq {
   float *weights = nullptr, *part_o = nullptr, *lse = nullptr;
   uint32_t *vmax = nullptr;
   float2 *part_ml = nullptr;
-  int32_t *list = nullptr, *dev_err = nullptr;
+  int32_t *list = nullptr, *dev_err = nullptr, *tickets = nullptr;
   int slots = 0;                  // partial results the workspace holds
   int64_t bytes = 0;
   std::vector<int32_t> len;       // [layers][seqs]
@@ -158,18 +158,6 @@ fm_status end(fm_kvq *c, cudaStream_t s) {
   return FM_OK;
 }
 
-// whether every CTA's share of the stages begins where a unit begins
-bool whole_units(const KvqAttnArgs &a) {
-  const int64_t W = a.st0[a.n];
-  int i = 0;
-  for (int64_t b = 1; b < a.ctas; ++b) {
-    const int64_t x = b * W / a.ctas;
-    while (a.st0[i + 1] <= x) ++i;
-    if ((x - a.st0[i]) % a.stages[i]) return false;
-  }
-  return true;
-}
-
 template <typename T>
 fm_status dev_alloc(fm_kvq *c, T **p, size_t n) {
   void *q = nullptr;
@@ -185,7 +173,7 @@ fm_status dev_alloc(fm_kvq *c, T **p, size_t n) {
 
 void release(fm_kvq *c) {
   for (void *p : {(void *)c->planes, (void *)c->weights, (void *)c->part_o, (void *)c->lse, (void *)c->vmax,
-                  (void *)c->part_ml, (void *)c->list, (void *)c->dev_err})
+                  (void *)c->part_ml, (void *)c->list, (void *)c->dev_err, (void *)c->tickets})
     if (p) cudaFree(p);
   if (c->done) cudaEventDestroy(c->done);
   delete c;
@@ -212,11 +200,13 @@ fm_status setup(fm_kvq *c, cudaStream_t s) {
   KTRY(dev_alloc(c, &c->lse, (size_t)kMaxUnits * kKvqQRows));
   KTRY(dev_alloc(c, &c->list, (size_t)(g.n_seqs < kKvqSeqs ? g.n_seqs : kKvqSeqs) * g.n_kv_heads * c->rows_pad));
   KTRY(dev_alloc(c, &c->dev_err, 4));
+  KTRY(dev_alloc(c, &c->tickets, (size_t)kMaxUnits));
   // rows behind a sequence's end are read with the last tile: they hold finite values from the start
   KCK(cudaMemsetAsync(c->planes, 0, planes * c->plane_bytes, s));
   KCK(cudaMemsetAsync(c->weights, 0, planes * c->rows_pad * sizeof(float), s));
   KCK(cudaMemsetAsync(c->vmax, 0, planes * sizeof(uint32_t), s));
   KCK(cudaMemsetAsync(c->dev_err, 0, 16, s));
+  KCK(cudaMemsetAsync(c->tickets, 0, kMaxUnits * sizeof(int32_t), s));
   KCK(cudaEventCreateWithFlags(&c->done, cudaEventDisableTiming));
   KCK(cudaStreamSynchronize(s));
   return FM_OK;
@@ -432,7 +422,8 @@ fm_status fm_kvq_attend(fm_kvq *c, int32_t layer, int32_t n_seqs, const int32_t 
     const int n = n_rows_host[i];
     if (n < 0 || n > (1 << 16)) return kfail(c, FM_ERR_INVALID_ARG, "sequence %d: %d query rows", seq_ids_host[i], n);
     const int64_t units = ((int64_t)n * group + kKvqQRows - 1) / kKvqQRows * nkv;
-    if (units > kMaxUnits)
+    const int64_t stages = (len[seq_ids_host[i]] + kKvqTile * kKvqStage - 1) / (kKvqTile * kKvqStage);
+    if (units > kMaxUnits || units * stages > INT_MAX)
       return kfail(c, FM_ERR_UNSUPPORTED, "sequence %d: %d query rows of %d heads in one call", seq_ids_host[i], n, n_heads);
     total += n;
     if (n > 0 && len[seq_ids_host[i]] > most) most = len[seq_ids_host[i]];
@@ -458,6 +449,7 @@ fm_status fm_kvq_attend(fm_kvq *c, int32_t layer, int32_t n_seqs, const int32_t 
   a.scale_log2 = scale * 1.4426950408889634f;
   a.causal = causal != 0;
   a.first = first_row;
+  a.tickets = c->tickets;
   a.part_o = c->part_o;
   a.part_ml = c->part_ml;
   a.lse = keep_w ? c->lse : nullptr;
@@ -475,33 +467,34 @@ fm_status fm_kvq_attend(fm_kvq *c, int32_t layer, int32_t n_seqs, const int32_t 
     for (; i < n_seqs && a.n < kKvqSeqs; ++i) {
       const int n = n_rows_host[i], L = len[seq_ids_host[i]], j = a.n;
       const int rts = (int)(((int64_t)n * group + kKvqQRows - 1) / kKvqQRows);
-      if (j && units + (int64_t)rts * nkv > kMaxUnits) break;
       const int t0 = first_row / kKvqTile, t1 = (L + kKvqTile - 1) / kKvqTile;
+      const int64_t more = (int64_t)rts * nkv * (t1 > t0 ? (t1 - t0 + kKvqStage - 1) / kKvqStage : 1);
+      if (j && (units + (int64_t)rts * nkv > kMaxUnits || work + more > INT_MAX)) break;
       a.seq[j] = seq_ids_host[i];
       a.len[j] = L;
       a.rows[j] = n;
       a.row0[j] = row0;
       a.stages[j] = t1 > t0 ? (t1 - t0 + kKvqStage - 1) / kKvqStage : 1;
-      a.st0[j] = work;
+      a.st0[j] = (int32_t)work;
       a.unit0[j] = un;
       a.wt0[j] = wt;
       row0 += n;
       units += (int64_t)rts * nkv;
-      work += (int64_t)rts * nkv * a.stages[j];
+      work += more;
       un += rts;
       if (rts > 0) wt += (t1 + kKvqWeightTiles - 1) / kKvqWeightTiles;
       ++a.n;
     }
-    a.st0[a.n] = work;
+    a.st0[a.n] = (int32_t)work;
     a.unit0[a.n] = un;
     a.wt0[a.n] = wt;
     // every CTA that the SMs hold at once takes the same number of stages, whatever unit they belong to
     const int64_t most_ctas = (int64_t)c->n_sm * c->ctas[type];
     a.ctas = (int32_t)(work < most_ctas ? work : most_ctas);
     if (work > 0) {
+      a.share = (int32_t)(work / a.ctas);
+      a.extra = (int32_t)(work % a.ctas);
       KCK(launch_kvq_attend(a, hd, s));
-      // (a unit that begins and ends inside a CTA's share needs no joining: no launch where shares are whole units)
-      if (a.ctas > 1 && !whole_units(a)) KCK(launch_kvq_merge(a, hd, s));
       if (keep_w && wt > 0) KCK(launch_kvq_weights(a, hd, s));
     }
     i0 = i;

@@ -81,7 +81,9 @@ struct KvqAttnArgs {
   float scale_log2;       // scale * log2(e)
   int32_t causal, first;  // row t of T sees rows first <= j < (causal ? len - T + t + 1 : len)
   int32_t n;              // sequences of this launch
-  int32_t ctas;           // CTAs of the launch; CTA b takes stages [b W / ctas, (b + 1) W / ctas), W = st0[n]
+  int32_t ctas;           // CTAs of the launch: of the W = st0[n] stages CTA b takes
+  int32_t share, extra;   // share = W / ctas, and one more where b < extra = W % ctas
+  int32_t *tickets;       // [units] zero between launches: parts of a split unit that are done
   float *part_o;          // [2 ctas][16][hd] unnormalised partial outputs
   float2 *part_ml;        // [2 ctas][16] (reference, row sum)
   float *lse;             // [units][16] log2 of the row sums, for the weights; or null
@@ -93,13 +95,12 @@ struct KvqAttnArgs {
   int32_t seq[kKvqSeqs], len[kKvqSeqs], rows[kKvqSeqs];
   // A unit is a (KV head, row tile) of a sequence; its keys are stages of two tiles, one at least.
   int32_t stages[kKvqSeqs];      // of a unit
-  int64_t st0[kKvqSeqs + 1];     // prefix sums of units x stages
+  int32_t st0[kKvqSeqs + 1];     // prefix sums of units x stages
   int32_t unit0[kKvqSeqs + 1];   // prefix sums of row tiles (lse is by (row tile, KV head))
   int32_t wt0[kKvqSeqs + 1];     // weights: prefix sums of the CTAs of each sequence
 };
 int kvq_attn_ctas_per_sm(int hd, int type);
 cudaError_t launch_kvq_attend(const KvqAttnArgs &a, int hd, cudaStream_t s);
-cudaError_t launch_kvq_merge(const KvqAttnArgs &a, int hd, cudaStream_t s);
 cudaError_t launch_kvq_weights(const KvqAttnArgs &a, int hd, cudaStream_t s);
 constexpr int kKvqWeightTiles = 8;   // tiles a CTA of the weights pass covers
 

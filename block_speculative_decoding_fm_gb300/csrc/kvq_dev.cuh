@@ -77,6 +77,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(d) : "l"(a), "l"(b));
@@ -166,7 +171,8 @@ __device__ __forceinline__ void load_q(const T *q, int64_t ldq, int group, int r
     const float up = copysignf(__uint_as_float((uint32_t)(127 + 7 - ex) << 23), scale_log2);
     const int rs = (r & 7) * 2 + (r >> 3);
     if (o == 0)   // (2^20: the products' unit)
-      reinterpret_cast<float *>(tile + QT::kMult)[rs] = fabsf(scale_log2) * __uint_as_float((uint32_t)(127 + ex - 7 + 20) << 23);
+      reinterpret_cast<float *>(tile + QT::kMult)[rs] =   // (never 0: a masked score is -inf times it)
+          fmaxf(fabsf(scale_log2) * __uint_as_float((uint32_t)(127 + ex - 7 + 20) << 23), 1e-37f);
     const int lane = (r & 7) * 4 + (o & 3), g = o >> 2;
     float sum = 0.f;
 #pragma unroll
@@ -210,8 +216,6 @@ __device__ __forceinline__ void strip_scores(uint32_t code, uint32_t scale, uint
   using QT = QTile<HD, QS>;
   constexpr int G = Dim<HD>::G, GB = Dim<HD>::GB;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) s[j][0] = s[j][1] = 0ull;
-#pragma unroll
   for (int g0 = 0; g0 < G; g0 += GB) {
     uint32_t sc[4][GB];
 #pragma unroll
@@ -242,8 +246,13 @@ __device__ __forceinline__ void strip_scores(uint32_t code, uint32_t scale, uint
       for (int j = 0; j < 4; ++j) {
         const float2 d = pair_f32(sc[j][gi]);
         const uint64_t dd = pack2(d.x, d.y);
-        s[j][0] = fma2(pack2(acc[j][0], acc[j][1]), dd, s[j][0]);
-        s[j][1] = fma2(pack2(acc[j][2], acc[j][3]), dd, s[j][1]);
+        if (g == 0) {
+          s[j][0] = mul2(pack2(acc[j][0], acc[j][1]), dd);
+          s[j][1] = mul2(pack2(acc[j][2], acc[j][3]), dd);
+        } else {
+          s[j][0] = fma2(pack2(acc[j][0], acc[j][1]), dd, s[j][0]);
+          s[j][1] = fma2(pack2(acc[j][2], acc[j][3]), dd, s[j][1]);
+        }
       }
     }
   }
@@ -292,15 +301,15 @@ __device__ __forceinline__ void strip_pv(uint32_t code, uint32_t scale, int lane
   for (int g0 = 0; g0 < G; g0 += GB) {
     uint32_t sc[4][GB];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      lds_words<GB>(scale + j * kPairStep(HD) + g0 * 4, sc[j]);
-      if (!PS && range.shifted) {
+    for (int j = 0; j < 4; ++j) lds_words<GB>(scale + j * kPairStep(HD) + g0 * 4, sc[j]);
+    if (!PS && range.shifted) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int gi = 0; gi < GB; ++gi) {
           const __half2 x = __hmul2(*reinterpret_cast<const __half2 *>(&sc[j][gi]), range.up);
           sc[j][gi] = *reinterpret_cast<const uint32_t *>(&x);
         }
-      }
     }
 #pragma unroll
     for (int gi = 0; gi < GB; ++gi) {
