@@ -180,7 +180,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
           const int row = __ldcg(list + r), t = row / kKvqTile, tr = row % kKvqTile;
           const uint8_t *h = src + (size_t)t * kvq_tile_bytes(HD) + (u >= U ? kvq_k_bytes(HD) : 0);
           code[q] = *reinterpret_cast<const uint4 *>(h + kvq_unit(tr, u % U, HD));
-          sc[q] = *reinterpret_cast<const uint16_t *>(h + kvq_scale(tr, u % U, HD));
+          sc[q] = *reinterpret_cast<const uint16_t *>(h + kvq_scale(tr, u % U, HD, u >= U));
         }
       }
       const bool has_w = tid < RB && r0 + tid < left;
@@ -193,7 +193,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
           const int t = r / kKvqTile, tr = r % kKvqTile;
           uint8_t *h = dst + (size_t)t * kvq_tile_bytes(HD) + (u >= U ? kvq_k_bytes(HD) : 0);
           *reinterpret_cast<uint4 *>(h + kvq_unit(tr, u % U, HD)) = code[q];
-          *reinterpret_cast<uint16_t *>(h + kvq_scale(tr, u % U, HD)) = sc[q];
+          *reinterpret_cast<uint16_t *>(h + kvq_scale(tr, u % U, HD, u >= U)) = sc[q];
         }
       }
       if (has_w) a.c.weights[pd * a.c.rows_pad + r0 + tid] = wt;

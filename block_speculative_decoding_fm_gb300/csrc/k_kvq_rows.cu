@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kThreads) kvq_append_kernel(const __grid_const
     }
     if (!ok) continue;
     *reinterpret_cast<uint32_t *>(half_tile + kvq_unit(tr, o >> 2, HD) + (o & 3) * 4) = w;
-    if ((o & 3) == 0) *reinterpret_cast<__half *>(half_tile + kvq_scale(tr, o >> 2, HD)) = dh;
+    if ((o & 3) == 0) *reinterpret_cast<__half *>(half_tile + kvq_scale(tr, o >> 2, HD, isv)) = dh;
     if (!isv && o == 0) a.c.weights[plane * a.c.rows_pad + tile * kKvqTile + tr] = 0.f;
     dmax = fmaxf(dmax, fabsf(d));
   }
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(kThreads) kvq_read_kernel(const __grid_constan
   for (int p = 0; p < NP; ++p) {
     const int tr = p * RP + r0;
     w[p] = *reinterpret_cast<const uint32_t *>(half_tile + kvq_unit(tr, o >> 2, HD) + (o & 3) * 4);
-    d[p] = *reinterpret_cast<const __half *>(half_tile + kvq_scale(tr, o >> 2, HD));
+    d[p] = *reinterpret_cast<const __half *>(half_tile + kvq_scale(tr, o >> 2, HD, isv));
   }
 #pragma unroll
   for (int p = 0; p < NP; ++p) {

@@ -22,7 +22,6 @@ using namespace fm;
 struct fm_kvq {
   fm_kvq_config cfg{};
   int device = 0, n_sm = 0;
-  int ctas[3] = {1, 1, 1};        // attention CTAs an SM holds, by type
   int rows_pad = 0;
   size_t plane_bytes = 0;
   uint8_t *planes = nullptr;
@@ -43,7 +42,7 @@ struct fm_kvq {
 
 namespace {
 
-constexpr int kMaxUnits = 1 << 16;   // (row tile, KV head) units of a call that keeps weights, per launch
+constexpr int kMaxUnits = 1 << 15;   // (row tile, KV head) units of a launch
 constexpr int kMaxRows = 1 << 24;
 
 thread_local char g_kvq_error[512] = "";
@@ -186,18 +185,13 @@ fm_status setup(fm_kvq *c, cudaStream_t s) {
   c->rows_pad = (g.max_rows + kKvqTile - 1) / kKvqTile * kKvqTile;
   c->plane_bytes = (size_t)(c->rows_pad / kKvqTile) * kvq_tile_bytes(g.head_dim);
   const size_t planes = (size_t)g.n_layers * g.n_seqs * g.n_kv_heads;
-  int most = 1;
-  for (int t = 0; t < 3; ++t) {
-    c->ctas[t] = kvq_attn_ctas_per_sm(g.head_dim, t);
-    most = c->ctas[t] > most ? c->ctas[t] : most;
-  }
-  c->slots = 2 * c->n_sm * most;
+  c->slots = 2 * c->n_sm;
   KTRY(dev_alloc(c, &c->planes, planes * c->plane_bytes));
   KTRY(dev_alloc(c, &c->weights, planes * c->rows_pad));
   KTRY(dev_alloc(c, &c->vmax, planes));
-  KTRY(dev_alloc(c, &c->part_o, (size_t)c->slots * kKvqQRows * g.head_dim));
-  KTRY(dev_alloc(c, &c->part_ml, (size_t)c->slots * kKvqQRows));
-  KTRY(dev_alloc(c, &c->lse, (size_t)kMaxUnits * kKvqQRows));
+  KTRY(dev_alloc(c, &c->part_o, (size_t)c->slots * 8 * kKvqMaxNQ * g.head_dim));
+  KTRY(dev_alloc(c, &c->part_ml, (size_t)c->slots * 8 * kKvqMaxNQ));
+  KTRY(dev_alloc(c, &c->lse, (size_t)kMaxUnits * 8 * kKvqMaxNQ));
   KTRY(dev_alloc(c, &c->list, (size_t)(g.n_seqs < kKvqSeqs ? g.n_seqs : kKvqSeqs) * g.n_kv_heads * c->rows_pad));
   KTRY(dev_alloc(c, &c->dev_err, 4));
   KTRY(dev_alloc(c, &c->tickets, (size_t)kMaxUnits));
@@ -416,13 +410,21 @@ fm_status fm_kvq_attend(fm_kvq *c, int32_t layer, int32_t n_seqs, const int32_t 
   if (keep_w) KTRY(check_distinct(c, n_seqs, seq_ids_host));
   const int32_t *len = lengths(c, layer);
   const int group = n_heads / nkv;
-  int64_t total = 0;
+  int64_t total = 0, widest = 1;
   int most = 0;
+  for (int i = 0; i < n_seqs; ++i) {
+    const int64_t r = (int64_t)n_rows_host[i] * group;
+    widest = r > widest ? r : widest;
+  }
+  // query rows of a unit: all of them up to 32, so that the codes are unpacked once; else tiles of about equal size
+  const int64_t row_tiles = (widest + 8 * kKvqMaxNQ - 1) / (8 * kKvqMaxNQ);
+  const int nq = (int)((widest + 8 * row_tiles - 1) / (8 * row_tiles)), unit_rows = 8 * nq;
+  const int stage_rows = kKvqTile * kvq_stage_tiles(hd);
   for (int i = 0; i < n_seqs; ++i) {
     const int n = n_rows_host[i];
     if (n < 0 || n > (1 << 16)) return kfail(c, FM_ERR_INVALID_ARG, "sequence %d: %d query rows", seq_ids_host[i], n);
-    const int64_t units = ((int64_t)n * group + kKvqQRows - 1) / kKvqQRows * nkv;
-    const int64_t stages = (len[seq_ids_host[i]] + kKvqTile * kKvqStage - 1) / (kKvqTile * kKvqStage);
+    const int64_t units = ((int64_t)n * group + unit_rows - 1) / unit_rows * nkv;
+    const int64_t stages = (len[seq_ids_host[i]] + stage_rows - 1) / stage_rows;
     if (units > kMaxUnits || units * stages > INT_MAX)
       return kfail(c, FM_ERR_UNSUPPORTED, "sequence %d: %d query rows of %d heads in one call", seq_ids_host[i], n, n_heads);
     total += n;
@@ -446,6 +448,7 @@ fm_status fm_kvq_attend(fm_kvq *c, int32_t layer, int32_t n_seqs, const int32_t 
   a.ldo = ldo;
   a.type = type;
   a.group = group;
+  a.nq = nq;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.causal = causal != 0;
   a.first = first_row;
@@ -466,15 +469,16 @@ fm_status fm_kvq_attend(fm_kvq *c, int32_t layer, int32_t n_seqs, const int32_t 
     int i = i0;
     for (; i < n_seqs && a.n < kKvqSeqs; ++i) {
       const int n = n_rows_host[i], L = len[seq_ids_host[i]], j = a.n;
-      const int rts = (int)(((int64_t)n * group + kKvqQRows - 1) / kKvqQRows);
+      const int rts = (int)(((int64_t)n * group + unit_rows - 1) / unit_rows);
       const int t0 = first_row / kKvqTile, t1 = (L + kKvqTile - 1) / kKvqTile;
-      const int64_t more = (int64_t)rts * nkv * (t1 > t0 ? (t1 - t0 + kKvqStage - 1) / kKvqStage : 1);
+      const int stages = t1 > t0 ? (t1 - t0 + kvq_stage_tiles(hd) - 1) / kvq_stage_tiles(hd) : 1;
+      const int64_t more = (int64_t)rts * nkv * stages;
       if (j && (units + (int64_t)rts * nkv > kMaxUnits || work + more > INT_MAX)) break;
       a.seq[j] = seq_ids_host[i];
       a.len[j] = L;
       a.rows[j] = n;
       a.row0[j] = row0;
-      a.stages[j] = t1 > t0 ? (t1 - t0 + kKvqStage - 1) / kKvqStage : 1;
+      a.stages[j] = stages;
       a.st0[j] = (int32_t)work;
       a.unit0[j] = un;
       a.wt0[j] = wt;
@@ -488,14 +492,13 @@ fm_status fm_kvq_attend(fm_kvq *c, int32_t layer, int32_t n_seqs, const int32_t 
     a.st0[a.n] = (int32_t)work;
     a.unit0[a.n] = un;
     a.wt0[a.n] = wt;
-    // every CTA that the SMs hold at once takes the same number of stages, whatever unit they belong to
-    const int64_t most_ctas = (int64_t)c->n_sm * c->ctas[type];
-    a.ctas = (int32_t)(work < most_ctas ? work : most_ctas);
+    // a CTA an SM, each with the same number of stages, whatever unit they belong to
+    a.ctas = (int32_t)(work < c->n_sm ? work : c->n_sm);
     if (work > 0) {
       a.share = (int32_t)(work / a.ctas);
       a.extra = (int32_t)(work % a.ctas);
-      KCK(launch_kvq_attend(a, hd, s));
-      if (keep_w && wt > 0) KCK(launch_kvq_weights(a, hd, s));
+      KCK(launch_kvq_attn(a, hd, false, s));
+      if (keep_w && wt > 0) KCK(launch_kvq_attn(a, hd, true, s));
     }
     i0 = i;
   }

@@ -7,8 +7,9 @@
 //           group, value e in bits 4 e of the unit; the row's units are permuted
 //           by unit ^ kvq_swz(row), so that the eight rows of an 8 x 16-byte
 //           matrix fetch (ldmatrix) hit eight distinct bank groups.
-//   scales  f16, [row / 2][group][row % 2]: the scales of two neighbouring rows
-//           form the f16 pair that the tensor-core fragments want.
+//   scales  f16.  K: [row][group], a row's scales together.  V: [group][row % 8 / 2]
+//           [row / 8][row % 2]: the pairs of neighbouring rows that one lane column of a
+//           tensor-core fragment multiplies, together.
 // So one bulk copy lands whole tiles in shared memory as the matrix
 // instructions read them, K alone is contiguous too, and a row is written and
 // moved without touching its neighbours' bytes.
@@ -22,8 +23,9 @@ namespace fm {
 
 constexpr int kKvqTile = 64;       // rows a tile
 constexpr int kKvqSeqs = 64;       // sequences a launch
-constexpr int kKvqStage = 2;       // tiles a stage: what the attention kernel fetches and deals out
-constexpr int kKvqQRows = 16;      // query rows (block row x head of the group) a CTA carries
+// tiles a stage, what the attention kernel fetches and deals out (four warps' strips of 32 or 16 rows)
+__host__ __device__ constexpr int kvq_stage_tiles(int hd) { return hd == 256 ? 1 : 2; }
+constexpr int kKvqMaxNQ = 4;       // a unit carries 8 nq query rows (block row x head of the group), nq <= 4
 
 enum KvqType : int32_t { KVQ_F32 = 0, KVQ_F16 = 1, KVQ_BF16 = 2 };
 
@@ -34,10 +36,14 @@ __host__ __device__ constexpr int kvq_scale_off(int hd) { return 32 * hd; }     
 __host__ __device__ constexpr int kvq_swz(int r, int hd) {
   return hd == 64 ? (r >> 2) & 1 : hd == 128 ? (r >> 1) & 3 : r & 7;
 }
-// byte offset of unit u (group u's codes) of row r, and of its scale, inside a half tile
+// byte offset of unit u (group u's codes) of row r, and of its scale, inside a K or V half tile
 __host__ __device__ constexpr int kvq_unit(int r, int u, int hd) { return r * (hd / 2) + ((u ^ kvq_swz(r, hd)) << 4); }
-__host__ __device__ constexpr int kvq_scale(int r, int u, int hd) {
-  return kvq_scale_off(hd) + (((r >> 1) * (hd / 32) + u) * 2 + (r & 1)) * 2;
+__host__ __device__ constexpr int kvq_kscale(int r, int u, int hd) { return kvq_scale_off(hd) + (r * (hd / 32) + u) * 2; }
+__host__ __device__ constexpr int kvq_vscale(int r, int u, int hd) {
+  return kvq_scale_off(hd) + ((u * 4 + (r & 7) / 2) * 16 + (r >> 3) * 2 + (r & 1)) * 2;
+}
+__host__ __device__ constexpr int kvq_scale(int r, int u, int hd, bool v) {
+  return v ? kvq_vscale(r, u, hd) : kvq_kscale(r, u, hd);
 }
 
 // What every launch knows of the cache (pointers of the call's layer).
@@ -78,30 +84,34 @@ struct KvqAttnArgs {
   int64_t ldq, ldo;
   int32_t type;           // KvqType of q and out
   int32_t group;          // query heads a KV head
+  int32_t nq;             // query rows of a unit / 8
   float scale_log2;       // scale * log2(e)
   int32_t causal, first;  // row t of T sees rows first <= j < (causal ? len - T + t + 1 : len)
   int32_t n;              // sequences of this launch
   int32_t ctas;           // CTAs of the launch: of the W = st0[n] stages CTA b takes
   int32_t share, extra;   // share = W / ctas, and one more where b < extra = W % ctas
   int32_t *tickets;       // [units] zero between launches: parts of a split unit that are done
-  float *part_o;          // [2 ctas][16][hd] unnormalised partial outputs
-  float2 *part_ml;        // [2 ctas][16] (reference, row sum)
-  float *lse;             // [units][16] log2 of the row sums, for the weights; or null
+  float *part_o;          // [2 ctas][8 nq][hd] unnormalised partial outputs
+  float2 *part_ml;        // [2 ctas][8 nq] (reference, row sum)
+  float *lse;             // [units][8 nq] log2 of the row sums, for the weights; or null
   float decay;            // weights: w = decay w + this call's
   float *w_out;           // [call sequences][n_kv][ldw] or null
   int64_t ldw;
   int32_t call0;
   int64_t row0[kKvqSeqs];
   int32_t seq[kKvqSeqs], len[kKvqSeqs], rows[kKvqSeqs];
-  // A unit is a (KV head, row tile) of a sequence; its keys are stages of two tiles, one at least.
+  // A unit is a (KV head, tile of 8 nq query rows) of a sequence; its keys are stages, one at least.
   int32_t stages[kKvqSeqs];      // of a unit
   int32_t st0[kKvqSeqs + 1];     // prefix sums of units x stages
   int32_t unit0[kKvqSeqs + 1];   // prefix sums of row tiles (lse is by (row tile, KV head))
   int32_t wt0[kKvqSeqs + 1];     // weights: prefix sums of the CTAs of each sequence
 };
-int kvq_attn_ctas_per_sm(int hd, int type);
-cudaError_t launch_kvq_attend(const KvqAttnArgs &a, int hd, cudaStream_t s);
-cudaError_t launch_kvq_weights(const KvqAttnArgs &a, int hd, cudaStream_t s);
+// attention (weights false) or its pass over the weights, which follows it
+template <int HD>
+cudaError_t kvq_attn_call(const KvqAttnArgs &a, bool weights, cudaStream_t s);
+inline cudaError_t launch_kvq_attn(const KvqAttnArgs &a, int hd, bool weights, cudaStream_t s) {
+  return hd == 64 ? kvq_attn_call<64>(a, weights, s) : hd == 128 ? kvq_attn_call<128>(a, weights, s) : kvq_attn_call<256>(a, weights, s);
+}
 constexpr int kKvqWeightTiles = 8;   // tiles a CTA of the weights pass covers
 
 struct KvqEvictArgs {

@@ -1,0 +1,651 @@
+// kvq_attn.cuh -- attention over the 4-bit KV cache, and the attention weight
+// that each cache row collects.
+//
+//   O[r] = sum_j p_rj v_j / sum_j p_rj,  p_rj = exp2(t_rj - m_r),
+//   t_rj = scale log2(e) q_r . k_j  over the rows j that r sees,
+// one pass over the cache with a running reference m and sum.  A unit is a
+// (sequence, KV head, 8 nq query rows); the units lie end to end and every CTA
+// takes an equal share of their stages of 128 rows (64 for head dim 256); where a
+// unit is shared, the CTA that finishes last joins the parts, in their order.
+//
+// A CTA's warps work in groups of four with a ring of stages of their own (K and V codes and scales in one bulk
+// copy).  A warp forms the scores of a quarter of the stage's keys, S^T = K Q^T, and puts its P into
+// shared memory; then each warp takes a quarter of the dims over all the stage's keys, O^T += V^T P^T, so
+// that it holds 8 accumulators a query octet for head dim 128 (64, were the output split by keys), many warps fit an
+// SM, and a unit's end needs no exchange inside a group.  The group shares one reference a row; it moves
+// only when a score beats it by 2^8, and the barrier that hands P over tells everyone whether one did.
+//
+// With at most 32 query rows the product is a skinny one, and the codes pass from shared memory (ldmatrix)
+// through a few integer operations straight into mma.sync fragments: they never go back to shared
+// memory as f16, which a tcgen05 operand would need (64 KB written and read again per 128 rows of
+// head dim 128: 1024 cycles of shared memory against the 784 cycles in which an SM's share of HBM
+// delivers their 18 KB).
+#include <type_traits>
+
+#include "kvq_dev.cuh"
+
+namespace fm {
+namespace {
+
+using namespace kvq;
+
+constexpr float kLazy = 8.f;               // log2 of the growth a reference tolerates
+constexpr int kWThreads = 128;             // the weights pass
+
+constexpr int imin(int a, int b) { return a < b ? a : b; }
+constexpr int imax(int a, int b) { return a > b ? a : b; }
+
+// The attention kernel's shape: NG groups of four warps a CTA, one CTA an SM.
+template <int HD, typename T, int NQ>
+struct Shape : Kind<HD, T, NQ> {
+  using K = Kind<HD, T, NQ>;
+  using QT = QTile<HD, K::QS, NQ>;
+  using PT = PTile<NQ, K::PS, K::KS>;
+  static constexpr int KT = kvq_stage_tiles(HD), SB = KT * kvq_tile_bytes(HD);
+  static constexpr int GP = K::G < 4 ? 1 : K::G / 4;      // groups of dims a warp takes
+  static constexpr int KP = K::G < 4 ? 4 / K::G : 1;      // ways the keys are split in the second product
+  // P twice over, or the group's outputs when they are joined
+  static constexpr int kP = imax(2 * PT::kBytes, KP * HD * K::RT * 4);
+  static constexpr int kMore = 4 * K::RT * 4 * 2 + K::RT * 4 + 32;      // warps' maxima and sums, references, cursor
+  static constexpr int kRoom = 225 * 1024 - QT::kBytes - 1024;
+  static constexpr int NS = HD == 64 ? 3 : 2;
+  static constexpr int kGroup = NS * SB + kP + kMore + 2 * NS * 8;
+  static constexpr int NG = imin(4, kRoom / kGroup);
+  static constexpr int kThreads = 128 * NG;
+  static constexpr int kBytes = NG * kGroup + QT::kBytes;
+  static_assert(NG >= 1, "a group fits an SM");
+};
+
+template <typename T>
+__device__ __forceinline__ void store4(T *p, float4 v) {
+  if constexpr (sizeof(T) == 4) {
+    *reinterpret_cast<float4 *>(p) = v;
+  } else {
+    uint2 w;
+    if constexpr (std::is_same<T, __half>::value) {
+      const __half2 a = __floats2half2_rn(v.x, v.y), b = __floats2half2_rn(v.z, v.w);
+      w = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+    } else {
+      const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+      w = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+    }
+    *reinterpret_cast<uint2 *>(p) = w;
+  }
+}
+
+// A CTA's share of the stages
+__device__ __forceinline__ int share_begin(const KvqAttnArgs &a, int b) { return b * a.share + min(b, a.extra); }
+__device__ __forceinline__ int cta_of(const KvqAttnArgs &a, int stage) {
+  const int wide = a.extra * (a.share + 1);
+  return stage < wide ? stage / (a.share + 1) : a.extra + (stage - wide) / a.share;
+}
+
+// A stretch of a share: stages [s0, s0 + n) of one unit.
+struct Stretch {
+  int i, head, rt, s0, n;
+  __device__ __forceinline__ Stretch(const KvqAttnArgs &a, int at, int end) {
+    i = find_seq<int32_t>(a.st0, a.n, at);
+    const int rel = at - a.st0[i], S = a.stages[i], unit = rel / S;
+    s0 = rel - unit * S;
+    n = min(S - s0, end - at);
+    const int rts = (a.rows[i] * a.group + 8 * a.nq - 1) / (8 * a.nq);
+    head = unit / rts;
+    rt = unit - head * rts;
+  }
+};
+
+// Where a group's copies have got to (in shared memory: one lane's business, once a stage).
+struct Cursor {
+  const uint8_t *src;     // the next stage
+  int32_t at;             // the share's stage after the stretch that the cursor is in
+  int32_t left;           // stages of the stretch that are the group's
+  int32_t tiles;          // tiles from the next stage to the unit's end
+  int32_t issued;
+};
+static_assert(sizeof(Cursor) <= 32, "a cursor's place in shared memory");
+
+// The next of the group's stages into its ring; false where a wait gave up.
+template <int HD, typename Sh>
+__device__ __forceinline__ bool issue_stage(const KvqAttnArgs &a, Cursor *cu, int w_end, int grp, uint32_t ring,
+                                            uint32_t full, uint32_t empty) {
+  constexpr int TB = kvq_tile_bytes(HD);
+  int left = cu->left, tiles = cu->tiles;
+  const uint8_t *src = cu->src;
+  while (left == 0) {
+    const int at = cu->at;
+    if (at >= w_end) return true;
+    const Stretch x(a, at, w_end);
+    const int t = a.first / kKvqTile + (x.s0 + grp) * Sh::KT;
+    left = (x.n - grp + Sh::NG - 1) / Sh::NG;
+    tiles = (a.len[x.i] + kKvqTile - 1) / kKvqTile - t;
+    src = a.c.planes + ((size_t)a.seq[x.i] * a.c.n_kv + x.head) * a.c.plane_bytes + (size_t)t * TB;
+    cu->at = at + x.n;
+  }
+  const int g = cu->issued, slot = g % Sh::NS;
+  if (g >= Sh::NS && !mbar_wait_bounded(empty + slot * 8, (g / Sh::NS - 1) & 1, a.c.err)) return false;
+  if (tiles > 0) {
+    const uint32_t bytes = min(Sh::KT, tiles) * TB;
+    mbar_expect_tx(full + slot * 8, bytes);
+    bulk_g2s(ring + slot * Sh::SB, src, bytes, full + slot * 8);
+  } else {
+    mbar_arrive(full + slot * 8);   // a unit without keys has one stage of nothing
+  }
+  cu->left = left - 1;
+  cu->tiles = tiles - Sh::NG * Sh::KT;
+  cu->src = src + Sh::NG * Sh::SB;
+  cu->issued = g + 1;
+  return true;
+}
+
+// The parts of a split unit into its output rows, in part order: CTA `first` has the unit's first stages (its
+// second slot), the CTAs after it up to `last` the rest.
+template <int HD, typename T, int RT, int NT>
+__device__ __forceinline__ void join_parts(const KvqAttnArgs &a, const Stretch &x, int first, int last, float undo, float bias,
+                                           float *lse, int tid) {
+  constexpr int NB = 8;    // parts whose loads are in flight together
+  const int R = a.rows[x.i] * a.group;
+  for (int e = tid; e < RT * HD / 4; e += NT) {
+    const int r = e / (HD / 4), d = 4 * (e % (HD / 4)), qr = x.rt * RT + r;
+    if (qr >= R) break;
+    float M = -INFINITY, L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = first; c <= last; c += NB) {
+      float2 ml[NB];
+      float4 v[NB];
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        const size_t slot = (size_t)min(c + k, last) * 2 + (c + k == first);
+        ml[k] = __ldcg(&a.part_ml[slot * RT + r]);
+        v[k] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + (slot * RT + r) * HD + d));
+      }
+      float m = M;
+#pragma unroll
+      for (int k = 0; k < NB; ++k) m = fmaxf(m, ml[k].x);
+      const float f = M == m ? 1.f : ex2(M - m);
+      M = m;
+      L *= f, acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        if (c + k > last) break;
+        const float g = ml[k].x == M ? 1.f : ex2(ml[k].x - M);
+        L = fmaf(g, ml[k].y, L);
+        acc.x = fmaf(g, v[k].x, acc.x);
+        acc.y = fmaf(g, v[k].y, acc.y);
+        acc.z = fmaf(g, v[k].z, acc.z);
+        acc.w = fmaf(g, v[k].w, acc.w);
+      }
+    }
+    const float inv = L == 0.f ? 0.f : undo / L;
+    const int t = qr / a.group;
+    store4(static_cast<T *>(a.out) + (a.row0[x.i] + t) * a.ldo + ((int64_t)x.head * a.group + qr - t * a.group) * HD + d,
+           make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+    if (lse && d == 0) lse[r] = L == 0.f ? INFINITY : M + log2f(L) - bias;
+  }
+}
+
+template <int HD, typename T, int NQ>
+__global__ void __launch_bounds__(Shape<HD, T, NQ>::kThreads, 1) kvq_attend_kernel(const __grid_constant__ KvqAttnArgs a) {
+  using Sh = Shape<HD, T, NQ>;
+  using QT = typename Sh::QT;
+  using PT = typename Sh::PT;
+  constexpr bool QS = Sh::QS, PS = Sh::PS;
+  constexpr int NG = Sh::NG, NS = Sh::NS, SB = Sh::SB, TB = kvq_tile_bytes(HD), RT = Sh::RT, KS = Sh::KS, MT = Sh::MT;
+  constexpr int GP = Sh::GP, KP = Sh::KP, NT = Sh::kThreads;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int s_last;
+  __shared__ float2 s_row[RT];              // references and sums of the query rows, all groups
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, grp = NG == 1 ? 0 : w >> 2, wq = w & 3;
+  const int g8 = lane >> 2, c = lane & 3;
+  // rings first (128-byte aligned), then P tiles, the queries, and the rest
+  const uint32_t ring = smem_u32(smem) + grp * NS * SB;
+  uint8_t *ptile = smem + NG * NS * SB + grp * Sh::kP;
+  uint8_t *qs = smem + NG * (NS * SB + Sh::kP);
+  uint8_t *more = qs + QT::kBytes;
+  uint64_t *bar = reinterpret_cast<uint64_t *>(more);                              // [group][full, empty][stage]
+  Cursor *cu = reinterpret_cast<Cursor *>(more + NG * 2 * NS * 8) + grp;
+  float *gm = reinterpret_cast<float *>(more + NG * (2 * NS * 8 + 32));            // [group][row] references
+  float *wl = gm + NG * RT;                                                        // [group][warp][row] sums
+  float *wx = wl + NG * 4 * RT + grp * 4 * RT;                                     // [group][warp][row] maxima
+  const uint32_t full = smem_u32(bar + grp * 2 * NS), empty = full + NS * 8, qt = smem_u32(qs);
+  const int w_beg = share_begin(a, blockIdx.x), w_end = share_begin(a, blockIdx.x + 1);
+
+  pdl_trigger();
+  if (tid == 0) {
+#pragma unroll
+    for (int s = 0; s < NG * 2 * NS; ++s) mbar_init(smem_u32(bar + s), s / NS & 1 ? 4 : 1);
+    mbar_fence_init();
+  }
+  __syncthreads();
+  pdl_wait();
+  const bool copies = lane == 0 && wq == 0;   // the lane that sends for its group's stages
+  bool ok = true;
+  if (copies) {
+    cu->at = w_beg;
+    cu->left = 0;
+    cu->issued = 0;
+    for (int k = 0; k < NS - 1; ++k) ok = issue_stage<HD, Sh>(a, cu, w_end, grp, ring, full, empty);
+  }
+
+  // first product: this warp's strip; second: its groups of dims gw, gw + 4 over the 32-row blocks kp, kp + KP, ...
+  const int strip = wq * KS;
+  const LaneAt<HD, KS> la(strip % kKvqTile, lane);
+  const uint32_t kcode = ring + strip / kKvqTile * TB + la.code, kscale = ring + strip / kKvqTile * TB + la.scale;
+  const int gw = KP == 1 ? wq : wq % Sh::G, kp = KP == 1 ? 0 : wq / Sh::G;
+  const uint32_t vcode = ring + kvq_k_bytes(HD) + kvq_unit(lane, 0, HD);
+  const uint32_t vscale = ring + kvq_k_bytes(HD) + kvq_vscale(2 * c, gw, HD);
+  int slot = 0, buf = 0;
+  uint32_t par = 0;
+  for (int at = w_beg; at < w_end;) {
+    const Stretch x(a, at, w_end);
+    const int len = a.len[x.i], T_rows = a.rows[x.i], R = T_rows * a.group, rq = x.rt * RT;
+    const size_t plane = (size_t)a.seq[x.i] * a.c.n_kv + x.head;
+    load_q<HD, QS, NQ, NT>(static_cast<const T *>(a.q) + a.row0[x.i] * a.ldq + (int64_t)x.head * a.group * HD, a.ldq, a.group,
+                           rq, R, a.scale_log2, qs, tid);
+    const PRange<PS> range(__ldcg(a.c.vmax + plane));
+    __syncthreads();
+    const int lim_all = a.causal ? len - T_rows + rq / a.group + 1 : len;   // the rows that every query row sees end here
+
+    float o[GP][2][NQ][4], m[NQ][2];
+    uint64_t l[NQ];                          // row sums of this warp's strips
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n] = 0ull;
+#pragma unroll
+      for (int u = 0; u < GP; ++u)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) o[u][t][n][0] = o[u][t][n][1] = o[u][t][n][2] = o[u][t][n][3] = 0.f;
+    }
+    int tile0 = a.first / kKvqTile + (x.s0 + grp) * Sh::KT;
+    for (int k = grp; k < x.n; k += NG, tile0 += NG * Sh::KT) {
+      // a stage ahead of the ring's end; then this one (a wait that gave up ends the group's work, not its barriers)
+      if (copies && ok) ok = issue_stage<HD, Sh>(a, cu, w_end, grp, ring, full, empty);
+      ok = __all_sync(0xffffffffu, ok && mbar_wait_bounded(full + slot * 8, par, a.c.err));
+      const int key0 = tile0 * kKvqTile + strip;
+      uint8_t *pt = ptile + buf * PT::kBytes;
+      float s[MT][NQ][4];
+      if (ok && key0 < len && key0 + KS > a.first) {
+        uint64_t sp[MT][NQ][2];
+        strip_scores<HD, QS, NQ, KS>(kcode + slot * SB, kscale + slot * SB, qt, lane, sp);
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int n = 0; n < NQ; ++n) {
+            unpack2(sp[i][n][0], s[i][n][0], s[i][n][1]);
+            unpack2(sp[i][n][1], s[i][n][2], s[i][n][3]);
+          }
+        if (key0 < a.first || key0 + KS > lim_all) {
+#pragma unroll
+          for (int n = 0; n < NQ; ++n)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {   // (rows past R follow the last: they are not stored)
+              const int row = min(rq + 8 * n + 2 * c + h, R - 1);
+              const int lim = a.causal ? len - T_rows + row / a.group + 1 : len;
+#pragma unroll
+              for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const int key = key0 + 16 * i + 8 * e + g8;
+                  if (key < a.first || key >= lim) s[i][n][2 * e + h] = -INFINITY;
+                }
+            }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int n = 0; n < NQ; ++n) s[i][n][0] = s[i][n][1] = s[i][n][2] = s[i][n][3] = -INFINITY;
+      }
+      // P with the references as they are; who beats one by 2^8 says so at the barrier
+      float p[MT][NQ][4];
+      uint64_t add[NQ];
+      bool beat = false;
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+        const float2 mu = *reinterpret_cast<const float2 *>(qs + QT::kMult + (8 * n + 2 * c) * 4);
+        const float b0 = range.bias - (m[n][0] == -INFINITY ? 0.f : m[n][0]), b1 = range.bias - (m[n][1] == -INFINITY ? 0.f : m[n][1]);
+        const uint64_t mm = pack2(mu.x, mu.y), bb = pack2(b0, b1);
+        float x0 = -INFINITY, x1 = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float t0, t1;
+            x0 = fmaxf(x0, s[i][n][2 * e]);
+            x1 = fmaxf(x1, s[i][n][2 * e + 1]);
+            unpack2(fma2(pack2(s[i][n][2 * e], s[i][n][2 * e + 1]), mm, bb), t0, t1);
+            p[i][n][2 * e] = ex2(t0);
+            p[i][n][2 * e + 1] = ex2(t1);
+            const uint64_t pp = pack2(p[i][n][2 * e], p[i][n][2 * e + 1]);
+            add[n] = i + e ? add2(add[n], pp) : pp;
+          }
+        beat |= x0 * mu.x > m[n][0] + kLazy || x1 * mu.y > m[n][1] + kLazy;
+      }
+      put_p<NQ, PS, KS>(pt, strip, lane, p);
+      if (bar_any(1 + grp, 128, beat)) {
+        // the group's new references, what it holds brought to them, and P again
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+          const float2 mu = *reinterpret_cast<const float2 *>(qs + QT::kMult + (8 * n + 2 * c) * 4);
+          float x0 = -INFINITY, x1 = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) x0 = fmaxf(x0, s[i][n][2 * e]), x1 = fmaxf(x1, s[i][n][2 * e + 1]);
+#pragma unroll
+          for (int sh = 4; sh < 32; sh <<= 1) {
+            x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, sh));
+            x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, sh));
+          }
+          if (g8 == 0) *reinterpret_cast<float2 *>(wx + wq * RT + 8 * n + 2 * c) = make_float2(x0 * mu.x, x1 * mu.y);
+        }
+        named_sync(1 + grp, 128);
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+          float n0 = m[n][0], n1 = m[n][1];
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const float2 y = *reinterpret_cast<const float2 *>(wx + v * RT + 8 * n + 2 * c);
+            n0 = fmaxf(n0, y.x), n1 = fmaxf(n1, y.y);
+          }
+          const float f0 = n0 == m[n][0] ? 1.f : ex2(m[n][0] - n0), f1 = n1 == m[n][1] ? 1.f : ex2(m[n][1] - n1);
+          m[n][0] = n0, m[n][1] = n1;
+          l[n] = mul2(l[n], pack2(f0, f1));
+#pragma unroll
+          for (int u = 0; u < GP; ++u)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) o[u][t][n][0] *= f0, o[u][t][n][1] *= f1, o[u][t][n][2] *= f0, o[u][t][n][3] *= f1;
+          const float2 mu = *reinterpret_cast<const float2 *>(qs + QT::kMult + (8 * n + 2 * c) * 4);
+          const float b0 = range.bias - (n0 == -INFINITY ? 0.f : n0), b1 = range.bias - (n1 == -INFINITY ? 0.f : n1);
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              p[i][n][2 * e] = ex2(fmaf(s[i][n][2 * e], mu.x, b0));
+              p[i][n][2 * e + 1] = ex2(fmaf(s[i][n][2 * e + 1], mu.y, b1));
+              const uint64_t pp = pack2(p[i][n][2 * e], p[i][n][2 * e + 1]);
+              add[n] = i + e ? add2(add[n], pp) : pp;
+            }
+        }
+        put_p<NQ, PS, KS>(pt, strip, lane, p);
+        named_sync(1 + grp, 128);
+      }
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) l[n] = add2(l[n], add[n]);
+      if (ok) {
+#pragma unroll
+        for (int kb = 0; kb < 2 * Sh::KT; kb += KP) {
+          const int key = 32 * (kb + kp);               // the block's rows in the stage (warps with kp take every KP-th)
+          if (KP > 1 && key >= 64 * Sh::KT) break;
+          const int tile = key / kKvqTile, r0 = key % kKvqTile;
+          if (tile0 * kKvqTile + key < len) {           // (rows behind the end: P is 0, but their tile may not be there)
+#pragma unroll
+            for (int u = 0; u < GP; ++u) {
+              uint32_t sc[4];
+              const uint4 v = lds128(vscale + slot * SB + tile * TB + (4 * u * 4 * 16) * 2 + r0 / 8 * 4);
+              sc[0] = v.x, sc[1] = v.y, sc[2] = v.z, sc[3] = v.w;
+              if (!PS && range.shifted) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&sc[j]), range.up);
+                  sc[j] = *reinterpret_cast<const uint32_t *>(&y);
+                }
+              }
+              tile_pv<HD, PS, NQ, KS>(vcode + slot * SB + tile * TB + r0 * (HD / 2), gw + 4 * u, sc, pt, key, lane, o[u]);
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty + slot * 8);
+      if (++slot == NS) slot = 0, par ^= 1;
+      buf ^= 1;
+    }
+
+    // the groups' references and the warps' sums, then the outputs
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      float l0, l1;
+      unpack2(l[n], l0, l1);
+#pragma unroll
+      for (int sh = 4; sh < 32; sh <<= 1) {
+        l0 += __shfl_xor_sync(0xffffffffu, l0, sh);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, sh);
+      }
+      if (g8 == 0) {
+        *reinterpret_cast<float2 *>(wl + (grp * 4 + wq) * RT + 8 * n + 2 * c) = make_float2(l0, l1);
+        if (wq == 0) *reinterpret_cast<float2 *>(gm + grp * RT + 8 * n + 2 * c) = make_float2(m[n][0], m[n][1]);
+      }
+    }
+    __syncthreads();
+    if (tid < RT) {
+      float M = -INFINITY, L = 0.f;
+#pragma unroll
+      for (int u = 0; u < NG; ++u) M = fmaxf(M, gm[u * RT + tid]);
+#pragma unroll
+      for (int u = 0; u < NG; ++u) {
+        const float *y = wl + u * 4 * RT + tid;
+        const float mu = gm[u * RT + tid];
+        L += (mu == M ? 1.f : ex2(mu - M)) * ((y[0] + y[RT]) + (y[2 * RT] + y[3 * RT]));
+      }
+      s_row[tid] = make_float2(M, L);
+    }
+    __syncthreads();
+    // in the values' own unit and with the rows' common references; every part but the first group's into shared memory
+    float *ob = reinterpret_cast<float *>(ptile) + (size_t)(kp * Sh::G + (GP == 1 ? gw : wq * GP)) * (2 * NQ * 128) + lane * 4;
+#pragma unroll
+    for (int u = 0; u < GP; ++u)
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+        const float M0 = s_row[8 * n + 2 * c].x, M1 = s_row[8 * n + 2 * c + 1].x;
+        const float f0 = m[n][0] == M0 ? 1.f : ex2(m[n][0] - M0), f1 = m[n][1] == M1 ? 1.f : ex2(m[n][1] - M1);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const float unit = t ? 1.f / kUnitHi : 1.f / kUnitLo;
+          float(&y)[4] = o[u][t][n];
+          y[0] *= unit * f0, y[1] *= unit * f1, y[2] *= unit * f0, y[3] *= unit * f1;
+          if (grp > 0 || kp > 0) *reinterpret_cast<float4 *>(ob + ((u * NQ + n) * 2 + t) * 128) = make_float4(y[0], y[1], y[2], y[3]);
+        }
+      }
+    const bool whole = x.n == a.stages[x.i];
+    float *lse = a.lse ? a.lse + ((size_t)(a.unit0[x.i] + x.rt) * a.c.n_kv + x.head) * RT : nullptr;
+    const size_t slot_g = (size_t)blockIdx.x * 2 + (x.s0 == 0);   // a unit begun here, or one continued
+    __syncthreads();
+    if (grp == 0 && kp == 0) {
+#pragma unroll
+      for (int u = 0; u < GP; ++u)
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+#pragma unroll
+          for (int v = 1; v < NG * KP; ++v) {
+            const float *y = reinterpret_cast<const float *>(smem + NG * NS * SB + v / KP * Sh::kP) +
+                             (size_t)((v % KP) * Sh::G + (GP == 1 ? gw : wq * GP)) * (2 * NQ * 128) + lane * 4;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              const float4 z = *reinterpret_cast<const float4 *>(y + ((u * NQ + n) * 2 + t) * 128);
+              o[u][t][n][0] += z.x, o[u][t][n][1] += z.y, o[u][t][n][2] += z.z, o[u][t][n][3] += z.w;
+            }
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {   // four dims of a query row: tiles' first rows, second rows
+            const int r = 8 * n + 2 * c + h, qr = rq + r, d = 32 * (gw + 4 * u) + 4 * g8;
+            const float4 y = make_float4(o[u][0][n][h], o[u][1][n][h], o[u][0][n][2 + h], o[u][1][n][2 + h]);
+            if (!whole) {
+              *reinterpret_cast<float4 *>(a.part_o + (slot_g * RT + r) * HD + d) = y;
+            } else if (qr < R) {
+              const float L = s_row[r].y, inv = L == 0.f ? 0.f : range.undo / L;
+              const int t = qr / a.group;
+              store4(static_cast<T *>(a.out) + (a.row0[x.i] + t) * a.ldo + ((int64_t)x.head * a.group + qr - t * a.group) * HD + d,
+                     make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
+            }
+          }
+        }
+    }
+    if (tid < RT) {
+      const float M = s_row[tid].x, L = s_row[tid].y;
+      if (!whole)
+        a.part_ml[slot_g * RT + tid] = make_float2(M, L);
+      else if (lse)
+        lse[tid] = L == 0.f ? INFINITY : M + log2f(L) - range.bias;
+    }
+    if (!whole) {   // the CTA that finishes the last part of a unit joins them all, in their order
+      int32_t *ticket = a.tickets + (size_t)(a.unit0[x.i] + x.rt) * a.c.n_kv + x.head;
+      const int u0 = at - x.s0, first = cta_of(a, u0), last = cta_of(a, u0 + a.stages[x.i] - 1);
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) s_last = atomicAdd(ticket, 1) == last - first;
+      __syncthreads();
+      if (s_last) {
+        __threadfence();
+        if (tid == 0) *ticket = 0;
+        join_parts<HD, T, RT, NT>(a, x, first, last, range.undo, range.bias, lse, tid);
+      }
+    }
+    at += x.n;
+    if (at < w_end) __syncthreads();   // the next stretch writes the queries, the references and the outputs' place
+  }
+  // nothing is left in flight when the CTA ends (a consumer may have given up)
+  if (copies)
+    for (int k = max(0, cu->issued - NS); k < cu->issued; ++k) mbar_wait_drain(full + k % NS * 8, (k / NS) & 1);
+  __syncthreads();
+}
+
+// weights[j] = decay weights[j] + sum_r p_rj / sum_j p_rj: with every row's sum
+// known, K alone is read again (from L2 where it still is there) and the scores
+// formed a second time, which needs no store of rows x keys.  One CTA owns a
+// run of 8 tiles, so nothing is added atomically.  Grid (sequence x run, KV head).
+template <int HD, typename T, int NQ>
+__global__ void __launch_bounds__(kWThreads) kvq_weights_kernel(const __grid_constant__ KvqAttnArgs a) {
+  constexpr bool QS = sizeof(T) == 4;
+  constexpr int KB = kvq_k_bytes(HD), NW = kKvqWeightTiles / 2, RT = 8 * NQ, KS = 32;
+  using QT = QTile<HD, QS, NQ>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint8_t *qs = smem + kKvqWeightTiles * KB;
+  const uint32_t bars = smem_u32(qs + QT::kBytes);
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g8 = lane >> 2, c = lane & 3;
+  const int i = find_seq<int32_t>(a.wt0, a.n, blockIdx.x), head = blockIdx.y;
+  const int len = a.len[i], T_rows = a.rows[i], R = T_rows * a.group, rts = (R + RT - 1) / RT;
+  const int t0 = (blockIdx.x - a.wt0[i]) * kKvqWeightTiles;
+  const int nt = min(kKvqWeightTiles, (len + kKvqTile - 1) / kKvqTile - t0);
+  const size_t plane = (size_t)a.seq[i] * a.c.n_kv + head;
+  pdl_trigger();
+  if (tid == 0) {
+    for (int t = 0; t < nt; ++t) mbar_init(bars + t * 8, 1);
+    mbar_fence_init();
+  }
+  __syncthreads();
+  pdl_wait();
+  if (tid == 0)
+    for (int t = 0; t < nt; ++t) {
+      mbar_expect_tx(bars + t * 8, KB);
+      bulk_g2s(smem_u32(smem + t * KB), a.c.planes + plane * a.c.plane_bytes + (size_t)(t0 + t) * kvq_tile_bytes(HD), KB,
+               bars + t * 8);
+    }
+  const LaneAt<HD, KS> la((w & 1) * 32, lane);
+  float acc[NW][4];
+#pragma unroll
+  for (int k = 0; k < NW; ++k) acc[k][0] = acc[k][1] = acc[k][2] = acc[k][3] = 0.f;
+  bool ok = true;
+  for (int rt = 0; rt < rts; ++rt) {
+    if (rt) __syncthreads();
+    load_q<HD, QS, NQ, kWThreads>(static_cast<const T *>(a.q) + a.row0[i] * a.ldq + (int64_t)head * a.group * HD, a.ldq,
+                                  a.group, rt * RT, R, a.scale_log2, qs, tid);
+    __syncthreads();
+    const float *lse = a.lse + ((size_t)(a.unit0[i] + rt) * a.c.n_kv + head) * RT;
+    const int lim_all = a.causal ? len - T_rows + rt * RT / a.group + 1 : len;
+#pragma unroll 1
+    for (int k = 0; k < NW; ++k) {
+      const int t = 2 * k + (w >> 1), key0 = (t0 + t) * kKvqTile + (w & 1) * 32;
+      if (t >= nt || key0 >= len || key0 + 32 <= a.first) continue;
+      if (rt == 0) ok = __all_sync(0xffffffffu, ok && mbar_wait_bounded(bars + t * 8, 0, a.c.err));
+      if (!ok) continue;
+      uint64_t sp[2][NQ][2];
+      strip_scores<HD, QS, NQ, KS>(smem_u32(smem + t * KB) + la.code, smem_u32(smem + t * KB) + la.scale, smem_u32(qs), lane, sp);
+      const bool whole = key0 >= a.first && key0 + 32 <= lim_all;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};     // keys 8 j + lane / 4
+#pragma unroll
+      for (int n = 0; n < NQ; ++n)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = 8 * n + 2 * c + h, row = rt * RT + r;
+          const float ls = row < R ? __ldcg(lse + r) : INFINITY, mu = *reinterpret_cast<const float *>(qs + QT::kMult + r * 4);
+          const int lim = a.causal ? len - T_rows + row / a.group + 1 : len;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float s[2];
+            unpack2(sp[j >> 1][n][j & 1], s[0], s[1]);
+            float p = ex2(fmaf(s[h], mu, -ls));
+            const int key = key0 + 8 * j + g8;
+            if (!whole && (key < a.first || key >= lim)) p = 0.f;
+            sum[j] += ls == INFINITY ? 0.f : p;   // a row without keys, or past the last, has no weight to give
+          }
+        }
+#pragma unroll
+      for (int kk = 0; kk < NW; ++kk)
+        if (kk == k) acc[kk][0] += sum[0], acc[kk][1] += sum[1], acc[kk][2] += sum[2], acc[kk][3] += sum[3];
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < NW; ++k) {
+    const int t = 2 * k + (w >> 1), key0 = (t0 + t) * kKvqTile + (w & 1) * 32;
+    if (t >= nt) continue;
+    float v = 0.f;   // lane 4 g + j ends with key 8 j + g
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float y = acc[k][j];
+      y += __shfl_xor_sync(0xffffffffu, y, 1);
+      y += __shfl_xor_sync(0xffffffffu, y, 2);
+      if (c == j) v = y;
+    }
+    const int key = key0 + 8 * c + g8;
+    if (key < len && ok) {
+      float *p = a.c.weights + plane * a.c.rows_pad + key;
+      if (a.decay != 0.f) v = fmaf(a.decay, *p, v);
+      *p = v;
+      if (a.w_out) a.w_out[((size_t)(a.call0 + i) * a.c.n_kv + head) * a.ldw + key] = v;
+    }
+  }
+  // (a strip that no query row sees was not waited for: nothing is left in flight when the CTA ends)
+  if (tid == 0)
+    for (int t = 0; t < nt; ++t) mbar_wait_drain(bars + t * 8, 0);
+  __syncthreads();
+}
+
+template <int HD, typename T, int NQ>
+cudaError_t attend_t(const KvqAttnArgs &a, cudaStream_t s) {
+  using Sh = Shape<HD, T, NQ>;
+  static_assert(Sh::kBytes <= 226 * 1024, "shared memory of a CTA");
+  cudaError_t e = cudaFuncSetAttribute(kvq_attend_kernel<HD, T, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kBytes);
+  if (e != cudaSuccess) return e;
+  return kvq_launch(kvq_attend_kernel<HD, T, NQ>, dim3(a.ctas), dim3(Sh::kThreads), Sh::kBytes, s, a);
+}
+template <int HD, typename T, int NQ>
+cudaError_t weights_t(const KvqAttnArgs &a, cudaStream_t s) {
+  constexpr int smem = kKvqWeightTiles * kvq_k_bytes(HD) + QTile<HD, sizeof(T) == 4, NQ>::kBytes + kKvqWeightTiles * 8;
+  cudaError_t e = cudaFuncSetAttribute(kvq_weights_kernel<HD, T, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return kvq_launch(kvq_weights_kernel<HD, T, NQ>, dim3(a.wt0[a.n], a.c.n_kv), dim3(kWThreads), smem, s, a);
+}
+
+template <int HD, typename T>
+cudaError_t call_t(const KvqAttnArgs &a, bool weights, cudaStream_t s) {
+  switch (a.nq) {
+    case 1: return weights ? weights_t<HD, T, 1>(a, s) : attend_t<HD, T, 1>(a, s);
+    case 2: return weights ? weights_t<HD, T, 2>(a, s) : attend_t<HD, T, 2>(a, s);
+    case 3: return weights ? weights_t<HD, T, 3>(a, s) : attend_t<HD, T, 3>(a, s);
+    default: return weights ? weights_t<HD, T, 4>(a, s) : attend_t<HD, T, 4>(a, s);
+  }
+}
+
+}  // namespace
+
+// one translation unit a head dim (KVQ_HD), so that they compile side by side
+template <int HD>
+cudaError_t kvq_attn_call(const KvqAttnArgs &a, bool weights, cudaStream_t s) {
+  if (a.type == KVQ_F32) return call_t<HD, float>(a, weights, s);
+  if (a.type == KVQ_F16) return call_t<HD, __half>(a, weights, s);
+  return call_t<HD, __nv_bfloat16>(a, weights, s);
+}
+template cudaError_t kvq_attn_call<KVQ_HD>(const KvqAttnArgs &, bool, cudaStream_t);
+
+}  // namespace fm

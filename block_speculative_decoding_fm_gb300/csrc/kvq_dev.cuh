@@ -1,21 +1,21 @@
 // kvq_dev.cuh -- device parts of the 4-bit KV cache's attention kernels: the
 // query fragments, a strip's scores, the codes' way into f16.
+//
+// The products run with the cache as the matrix instructions' first operand:
+// S^T = K Q^T over 16 keys at a time and O^T += V^T P^T over 16 dims, with 8 query
+// rows a step on the other side, so that few query rows cost few products.
 #pragma once
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "dev_common.cuh"
 #include "kvq.h"
 
 namespace fm {
 namespace kvq {
-
-template <int HD>
-struct Dim {
-  static constexpr int G = HD / 32;            // groups a row
-  static constexpr int GB = G < 4 ? G : 4;     // groups whose scales one shared load fetches
-};
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -53,16 +53,6 @@ __device__ __forceinline__ void codes_f16_signed(uint32_t w, uint32_t (&h)[4]) {
   }
 }
 
-// D = A B + C with D apart from C (C may be the zero register)
-__device__ __forceinline__ void mma_f16_c(float (&d)[4], const uint4 &a, uint32_t b0, uint32_t b1, float c0, float c1,
-                                          float c2, float c3) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%10,%11,%12,%13};\n"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
-}
-
 // two f32 at a time
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
   uint64_t v;
@@ -90,18 +80,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 
 __device__ __forceinline__ float2 pair_f32(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2 *>(&w)); }
 
-// GB consecutive 32-bit words from shared memory
-template <int GB>
-__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[GB]) {
-  if constexpr (GB == 4) {
-    const uint4 v = lds128(addr);
-    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-  } else {
-    const uint2 v = lds64(addr);
-    w[0] = v.x, w[1] = v.y;
-  }
-}
-
 template <typename T>
 __device__ __forceinline__ void load8(const T *p, float (&x)[8]) {
   if constexpr (sizeof(T) == 4) {
@@ -122,35 +100,53 @@ __device__ __forceinline__ void load8(const T *p, float (&x)[8]) {
   }
 }
 
-// A query tile in shared memory: A fragments of 16 rows (hi, and lo where q is
-// split), then per group and row the products' start value, then the rows' factors.
-template <int HD, bool QS>
-struct QTile {
-  static constexpr int kLo = 32 * HD;
-  static constexpr int kOff = 32 * HD * (QS ? 2 : 1);    // f32 [group][row % 8][row / 8]
-  static constexpr int kMult = kOff + HD / 32 * 16 * 4;  // f32 [row % 8][row / 8]
-  static constexpr int kBytes = kMult + 16 * 4;
+// What a kernel instance carries: NQ x 8 query rows, strips of KS keys a warp.
+template <int HD, typename T, int NQ_>
+struct Kind {
+  static constexpr int NQ = NQ_, RT = 8 * NQ, G = HD / 32;
+  static constexpr bool QS = sizeof(T) == 4;                          // f32 queries: f16 hi + lo
+  static constexpr bool PS = !std::is_same<T, __nv_bfloat16>::value;  // f16 and f32 outputs: P' too
+  static constexpr int KS = 16 * kvq_stage_tiles(HD), MT = KS / 16;   // a strip, in 16-key products
 };
 
-// Query rows [r0, r0 + 16) of a (sequence, KV head) -- row r is block row r /
-// group, head r % group of the group -- into A fragments: (group of 32 dims,
-// half) -> 32 lanes x 16 bytes.  Inside a group, the k index of the matrix
-// product is a permutation of the dims that a word's codes dictate: lane column
-// c holds dims 8 c .. 8 c + 7, pair p = dims (p, p + 4) of them; the even pairs' codes
-// come in units 16 times smaller, which their queries make up for.  A row is
-// scaled by a power of two that brings its largest value to [2^7, 2^8), so q up to
-// 2^96 fits f16 (exact for bf16 and f16 inputs down to 2^-22 of the row's
-// largest); the row's factor undoes it and carries the softmax scale, whose
-// sign goes into the queries.  The codes enter the product unsigned, and the start
-// value takes their 8 off: -8 sum q over the group.
+// D = A B + C with D apart from C
+__device__ __forceinline__ void mma_f16_c(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1, float c0, float c1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%11,%10,%11};\n"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+}
+
+// A query tile in shared memory: B fragments of the group's dims (hi, and lo
+// where q is split), the products' start values, the rows' factors.
+template <int HD, bool QS, int NQ>
+struct QTile {
+  static constexpr int kLo = HD * NQ * 16;                      // [group][row / 8][lane] 16 bytes
+  static constexpr int kOff = kLo * (QS ? 2 : 1);               // f32 [group][row]
+  static constexpr int kMult = kOff + HD / 32 * NQ * 8 * 4;     // f32 [row]
+  static constexpr int kBytes = kMult + NQ * 8 * 4;
+};
+
+// Query rows [r0, r0 + 8 NQ) of a (sequence, KV head) -- row r is block row r /
+// group, head r % group of the group -- into B fragments.  Inside a group of 32
+// dims the k index of the matrix product is a permutation of the dims that a
+// word's codes dictate: lane column c holds dims 8 c .. 8 c + 7, pair p = dims (p, p + 4) of
+// them; the even pairs' codes come in units 16 times smaller, which their
+// queries make up for.  A row is scaled by a power of two that brings its
+// largest value to [2^7, 2^8), so q up to 2^96 fits f16 (exact for bf16 and f16
+// inputs down to 2^-22 of the row's largest); the row's factor undoes it and
+// carries the softmax scale, whose sign goes into the queries.  The codes enter the
+// product unsigned, and the start value takes their 8 off: -8 sum q over the group.
 // NT threads, all of which call it; the caller synchronises.
-template <int HD, bool QS, int NT, typename T>
+template <int HD, bool QS, int NQ, int NT, typename T>
 __device__ __forceinline__ void load_q(const T *q, int64_t ldq, int group, int r0, int R, float scale_log2, uint8_t *tile,
                                        int tid) {
-  using QT = QTile<HD, QS>;
+  using QT = QTile<HD, QS, NQ>;
   constexpr int O = HD / 8;
-#pragma unroll
-  for (int it = tid; it < 16 * O; it += NT) {
+#pragma unroll 1
+  for (int it = tid; it < 8 * NQ * O; it += NT) {
     const int r = it / O, o = it % O;
     const int row = r0 + r;
     float x[8];
@@ -169,91 +165,157 @@ __device__ __forceinline__ void load_q(const T *q, int64_t ldq, int group, int r
     // am in [2^ex, 2^(ex + 1)); the factor 2^(7 - ex), its exponent kept in f32's normal range
     const int ex = am > 0.f && am < INFINITY ? min(96, max(-119, static_cast<int>(__float_as_uint(am) >> 23) - 127)) : 7;
     const float up = copysignf(__uint_as_float((uint32_t)(127 + 7 - ex) << 23), scale_log2);
-    const int rs = (r & 7) * 2 + (r >> 3);
-    if (o == 0)   // (2^20: the products' unit)
-      reinterpret_cast<float *>(tile + QT::kMult)[rs] =   // (never 0: a masked score is -inf times it)
+    if (o == 0)   // (2^20: the products' unit; never 0: a masked score is -inf times it)
+      reinterpret_cast<float *>(tile + QT::kMult)[r] =
           fmaxf(fabsf(scale_log2) * __uint_as_float((uint32_t)(127 + ex - 7 + 20) << 23), 1e-37f);
-    const int lane = (r & 7) * 4 + (o & 3), g = o >> 2;
+    const int g = o >> 2, at = ((g * NQ + (r >> 3)) * 32 + (r & 7) * 4 + (o & 3)) * 16;
     float sum = 0.f;
+    uint32_t hi[4], lo[4];
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {   // k halves (p & 1): registers a0 / a1, then a2 / a3 of half p / 2
+    for (int p = 0; p < 4; ++p) {
       const float f = p & 1 ? up : 16.f * up;
-      uint8_t *dst = tile + ((g * 2 + (p >> 1)) * 32 + lane) * 16 + (2 * (p & 1) + (r >> 3)) * 4;
-      uint32_t hi, lo = 0;
       if constexpr (QS) {
-        split2_f16(x[p] * f, x[p + 4] * f, hi, lo);
-        *reinterpret_cast<uint32_t *>(dst + QT::kLo) = lo;
+        split2_f16(x[p] * f, x[p + 4] * f, hi[p], lo[p]);
       } else {
         const __half2 v = __floats2half2_rn(x[p] * f, x[p + 4] * f);
-        hi = *reinterpret_cast<const uint32_t *>(&v);
+        hi[p] = *reinterpret_cast<const uint32_t *>(&v);
+        lo[p] = 0;
       }
-      *reinterpret_cast<uint32_t *>(dst) = hi;
-      const float2 h = pair_f32(hi), l = pair_f32(lo);
+      const float2 h = pair_f32(hi[p]), l = pair_f32(lo[p]);
       sum += (h.x + h.y + (l.x + l.y)) * (p & 1 ? 1.f : 0.0625f);
     }
+    *reinterpret_cast<uint4 *>(tile + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    if constexpr (QS) *reinterpret_cast<uint4 *>(tile + QT::kLo + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     sum += __shfl_xor_sync(0xffffffffu, sum, 1);
     sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-    if ((o & 3) == 0) reinterpret_cast<float *>(tile + QT::kOff)[g * 16 + rs] = -8.f * kUnitHi * sum;
+    if ((o & 3) == 0) reinterpret_cast<float *>(tile + QT::kOff)[g * NQ * 8 + r] = -8.f * kUnitHi * sum;
   }
 }
 
-// Where a lane finds its parts of a 32-row strip, relative to the strip's tile:
-// its row's codes (the unit of group g: XOR 16 g) and its rows' scales.
-template <int HD>
+// Where a lane finds its part of a strip of KS rows from r0 on, relative to the
+// tile: the codes that it addresses for ldmatrix (unit of group g: XOR 16 g; a
+// strip of 16 rows takes two groups a fetch) and the scales of its rows.
+template <int HD, int KS>
 struct LaneAt {
   uint32_t code, scale;
   __device__ __forceinline__ LaneAt(int r0, int lane)
-      : code((uint32_t)kvq_unit(r0 + lane, 0, HD)), scale((uint32_t)kvq_scale(r0 + 2 * (lane & 3), 0, HD)) {}
+      : code((uint32_t)(KS == 32 ? kvq_unit(r0 + lane, 0, HD) : kvq_unit(r0 + (lane & 15), lane >> 4, HD))),
+        scale((uint32_t)kvq_kscale(r0 + (lane >> 2), 0, HD)) {}
 };
-constexpr int kPairStep(int hd) { return hd / 32 * 16; }   // scale bytes of eight rows
 
-// Scores of 16 query rows against the 32 keys of a strip: s[j] is the
-// accumulator fragment of keys 8 j .. 8 j + 7 (columns 2 (lane % 4) and + 1; s[j][0] packs
-// them for row lane / 4, s[j][1] for row lane / 4 + 8).  Per group of 32 dims the product runs
-// over whole codes (exact operands) and the group's scale meets the f32 sum.
-template <int HD, bool QS>
-__device__ __forceinline__ void strip_scores(uint32_t code, uint32_t scale, uint32_t qt, int lane, uint64_t (&s)[4][2]) {
-  using QT = QTile<HD, QS>;
-  constexpr int G = Dim<HD>::G, GB = Dim<HD>::GB;
+// a row's K scales of 4 groups (2 for head dim 64) as f32
+template <int GB>
+__device__ __forceinline__ void row_scales(uint32_t addr, float (&d)[GB]) {
+  if constexpr (GB == 4) {
+    const uint2 v = lds64(addr);
+    const float2 a = pair_f32(v.x), b = pair_f32(v.y);
+    d[0] = a.x, d[1] = a.y, d[2] = b.x, d[3] = b.y;
+  } else {
+    const float2 a = pair_f32(lds32(addr));
+    d[0] = a.x, d[1] = a.y;
+  }
+}
+
+// Scores of 8 NQ query rows against the KS keys of a strip: s[m][n] is the
+// accumulator fragment of keys 16 m + lane / 4 (first pair) and + 8 (second), query rows
+// 8 n + 2 (lane % 4) and + 1.  Per group of 32 dims the product runs over whole codes
+// (exact operands) and the row's scale meets the f32 sum.
+template <int HD, bool QS, int NQ, int KS>
+__device__ __forceinline__ void strip_scores(uint32_t code, uint32_t scale, uint32_t qt, int lane,
+                                             uint64_t (&s)[KS / 16][NQ][2]) {
+  using QT = QTile<HD, QS, NQ>;
+  constexpr int G = HD / 32, GB = G < 4 ? G : 4, MT = KS / 16, GF = 2 / MT;   // GF groups a fetch
 #pragma unroll
   for (int g0 = 0; g0 < G; g0 += GB) {
-    uint32_t sc[4][GB];
+    float d[MT][2][GB];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) lds_words<GB>(scale + j * kPairStep(HD) + g0 * 4, sc[j]);
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int gi = 0; gi < GB; ++gi) {
-      const int g = g0 + gi;
-      uint32_t w[4], h[4][4];
-      ldsm_x4(code ^ (g << 4), w);
-      const uint2 off = lds64(qt + QT::kOff + g * 64 + (lane >> 2) * 8);
-      const float o0 = __uint_as_float(off.x), o1 = __uint_as_float(off.y);
+      for (int h = 0; h < 2; ++h) row_scales<GB>(scale + (16 * m + 8 * h) * (G * 2) + g0 * 2, d[m][h]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) codes_f16(w[j], h[j]);
-      float acc[4][4];
-      const uint4 a0 = lds128(qt + (g * 64 + lane) * 16), a1 = lds128(qt + (g * 64 + 32 + lane) * 16);
+    for (int gi = 0; gi < GB; gi += GF) {
+      uint32_t w[4];
+      ldsm_x4(code ^ ((g0 + gi) << 4), w);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) mma_f16_c(acc[j], a0, h[j][0], h[j][1], o0, o0, o1, o1);
+      for (int f = 0; f < GF; ++f) {
+        const int g = g0 + gi + f;
+        uint32_t h[2 * MT][4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) mma_f16(acc[j], a1.x, a1.y, a1.z, a1.w, h[j][2], h[j][3]);
-      if constexpr (QS) {
-        const uint4 l0 = lds128(qt + QT::kLo + (g * 64 + lane) * 16), l1 = lds128(qt + QT::kLo + (g * 64 + 32 + lane) * 16);
+        for (int j = 0; j < 2 * MT; ++j) codes_f16(w[2 * f * (GF - 1) + j], h[j]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) mma_f16(acc[j], l0.x, l0.y, l0.z, l0.w, h[j][0], h[j][1]);
+        for (int n = 0; n < NQ; ++n) {
+          const uint2 off = lds64(qt + QT::kOff + (g * NQ + n) * 32 + (lane & 3) * 8);
+          const uint4 b = lds128(qt + ((g * NQ + n) * 32 + lane) * 16);
+          float acc[MT][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) mma_f16(acc[j], l1.x, l1.y, l1.z, l1.w, h[j][2], h[j][3]);
-      }
+          for (int m = 0; m < MT; ++m)
+            mma_f16_c(acc[m], h[2 * m][0], h[2 * m + 1][0], h[2 * m][1], h[2 * m + 1][1], b.x, b.y, __uint_as_float(off.x),
+                      __uint_as_float(off.y));
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 d = pair_f32(sc[j][gi]);
-        const uint64_t dd = pack2(d.x, d.y);
-        if (g == 0) {
-          s[j][0] = mul2(pack2(acc[j][0], acc[j][1]), dd);
-          s[j][1] = mul2(pack2(acc[j][2], acc[j][3]), dd);
-        } else {
-          s[j][0] = fma2(pack2(acc[j][0], acc[j][1]), dd, s[j][0]);
-          s[j][1] = fma2(pack2(acc[j][2], acc[j][3]), dd, s[j][1]);
+          for (int m = 0; m < MT; ++m) mma_f16(acc[m], h[2 * m][2], h[2 * m + 1][2], h[2 * m][3], h[2 * m + 1][3], b.z, b.w);
+          if constexpr (QS) {
+            const uint4 l = lds128(qt + QT::kLo + ((g * NQ + n) * 32 + lane) * 16);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) mma_f16(acc[m], h[2 * m][0], h[2 * m + 1][0], h[2 * m][1], h[2 * m + 1][1], l.x, l.y);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) mma_f16(acc[m], h[2 * m][2], h[2 * m + 1][2], h[2 * m][3], h[2 * m + 1][3], l.z, l.w);
+          }
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint64_t dd = pack2(d[m][e][gi + f], d[m][e][gi + f]), x = pack2(acc[m][2 * e], acc[m][2 * e + 1]);
+              s[m][n][e] = g == 0 ? mul2(x, dd) : fma2(x, dd, s[m][n][e]);
+            }
         }
       }
+    }
+  }
+}
+
+// P of a stage of four strips in shared memory, by query row: f16 (a row's keys
+// together, 16 bytes of padding: eight rows' 16-byte pieces in eight bank
+// groups), or f32 where P' = p d is to be split (eight words of padding).
+template <int NQ, bool PS, int KS>
+struct PTile {
+  static constexpr int kRow = PS ? 4 * KS * 4 + 32 : 4 * KS * 2 + 16;
+  static constexpr int kBytes = 8 * NQ * kRow;
+};
+__device__ __forceinline__ void stsm_x4_trans(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};\n" ::"r"(addr), "r"(r0), "r"(r1), "r"(r2),
+               "r"(r3)
+               : "memory");
+}
+__device__ __forceinline__ void stsm_x2_trans(uint32_t addr, uint32_t r0, uint32_t r1) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x2.trans.shared.b16 [%0], {%1,%2};\n" ::"r"(addr), "r"(r0), "r"(r1) : "memory");
+}
+// this warp's strip (fragments as strip_scores') into columns key0 .. of the tile
+template <int NQ, bool PS, int KS>
+__device__ __forceinline__ void put_p(uint8_t *tile, int key0, int lane, const float (&p)[KS / 16][NQ][4]) {
+  using PT = PTile<NQ, PS, KS>;
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) {
+    if constexpr (PS) {
+#pragma unroll
+      for (int m = 0; m < KS / 16; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          *reinterpret_cast<float *>(tile + (8 * n + 2 * (lane & 3) + (e & 1)) * PT::kRow +
+                                     (key0 + 16 * m + 8 * (e >> 1) + (lane >> 2)) * 4) = p[m][n][e];
+    } else {
+      uint32_t r[KS / 8];
+#pragma unroll
+      for (int m = 0; m < KS / 16; ++m)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const __half2 v = __floats2half2_rn(p[m][n][2 * e], p[m][n][2 * e + 1]);
+          r[2 * m + e] = *reinterpret_cast<const uint32_t *>(&v);
+        }
+      const uint32_t at = smem_u32(tile) + (8 * n + (lane & 7)) * PT::kRow + key0 * 2;
+      if constexpr (KS == 32)
+        stsm_x4_trans(at + (lane >> 3) * 16, r[0], r[1], r[2], r[3]);
+      else
+        stsm_x2_trans(at + ((lane >> 3) & 1) * 16, r[0], r[1]);
     }
   }
 }
@@ -278,103 +340,45 @@ struct PRange {
   }
 };
 
-// O += P V over a strip: p as strip_scores' fragments, o[4 g + i] the
-// accumulators of the dims 32 g + 4 n + i (n the fragment's column), in the code
-// pairs' units (i even 2^-24, odd 2^-20).  The V scale of (key, group) goes into P:
-// P' = p d rounded to f16 once more (PS: split into hi + lo, which keeps ~22 bits).
-// SV: the codes enter with their 8 taken off; else unsigned, and column g of cor
-// collects the sum of P' over the keys for group g (a product with a column of
-// ones), which the end takes off eight times.
-template <int HD, bool PS, bool SV>
-__device__ __forceinline__ void strip_pv(uint32_t code, uint32_t scale, int lane, const PRange<PS> &range,
-                                         const float (&p)[4][4], float (&o)[HD / 8][4], float (&cor)[4]) {
-  constexpr int G = Dim<HD>::G, GB = Dim<HD>::GB;
-  __half2 ph[4][2];
-  if constexpr (!PS) {
+// O^T += V^T P^T over the 32 rows from r0 on of a tile (vb: its V half), group g:
+// o[t][n] are the accumulators of dims 32 g + 4 (lane / 4) + t (first pair) and + 2 (second), query
+// rows 8 n + 2 (lane % 4) and + 1, in the code pairs' units (t = 0: 2^-24, t = 1: 2^-20).
+// sc: the V scales of the rows' pairs (kvq_vscale's order).  P' = p d is rounded to
+// f16 once more (PS: split into hi + lo, which keeps ~22 bits).
+template <int HD, bool PS, int NQ, int KS>
+__device__ __forceinline__ void tile_pv(uint32_t code, int g, const uint32_t (&sc)[4], const uint8_t *pt, int key0, int lane,
+                                        float (&o)[2][NQ][4]) {
+  using PT = PTile<NQ, PS, KS>;
+  uint32_t w[4], h[4][4];
+  ldsm_x4_trans(code ^ (g << 4), w[0], w[1], w[2], w[3]);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      ph[j][0] = __floats2half2_rn(p[j][0], p[j][1]);
-      ph[j][1] = __floats2half2_rn(p[j][2], p[j][3]);
-    }
-  }
+  for (int j = 0; j < 4; ++j) codes_f16_signed(w[j], h[j]);
 #pragma unroll
-  for (int g0 = 0; g0 < G; g0 += GB) {
-    uint32_t sc[4][GB];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) lds_words<GB>(scale + j * kPairStep(HD) + g0 * 4, sc[j]);
-    if (!PS && range.shifted) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int gi = 0; gi < GB; ++gi) {
-          const __half2 x = __hmul2(*reinterpret_cast<const __half2 *>(&sc[j][gi]), range.up);
-          sc[j][gi] = *reinterpret_cast<const uint32_t *>(&x);
-        }
-    }
-#pragma unroll
-    for (int gi = 0; gi < GB; ++gi) {
-      const int g = g0 + gi;
-      uint32_t w[4], h[4][4];
-      ldsm_x4_trans(code ^ (g << 4), w[0], w[1], w[2], w[3]);
+  for (int n = 0; n < NQ; ++n) {
+    uint32_t b[4], l[4];
+    if constexpr (PS) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        if constexpr (SV)
-          codes_f16_signed(w[j], h[j]);
-        else
-          codes_f16(w[j], h[j]);
+        const uint2 v = lds64(smem_u32(pt) + (8 * n + (lane >> 2)) * PT::kRow + (key0 + 8 * j + 2 * (lane & 3)) * 4);
+        const float2 d = pair_f32(sc[j]);
+        split2_f16(__uint_as_float(v.x) * d.x, __uint_as_float(v.y) * d.y, b[j], l[j]);
       }
-      const uint32_t one = (lane >> 2) == g ? 0x3c003c00u : 0u;
+    } else {
+      ldsm_x4(smem_u32(pt) + (8 * n + (lane & 7)) * PT::kRow + (key0 + (lane >> 3) * 8) * 2, b);
 #pragma unroll
-      for (int st = 0; st < 2; ++st) {
-        uint32_t a[4], l[4];
-#pragma unroll
-        for (int h2 = 0; h2 < 2; ++h2) {   // keys 16 st + 8 h2 ..
-          const int j = 2 * st + h2;
-          if constexpr (PS) {
-            const float2 d = pair_f32(sc[j][gi]);
-            split2_f16(p[j][0] * d.x, p[j][1] * d.y, a[2 * h2], l[2 * h2]);
-            split2_f16(p[j][2] * d.x, p[j][3] * d.y, a[2 * h2 + 1], l[2 * h2 + 1]);
-          } else {
-            const __half2 d = *reinterpret_cast<const __half2 *>(&sc[j][gi]);
-            const __half2 x = __hmul2(ph[j][0], d), y = __hmul2(ph[j][1], d);
-            a[2 * h2] = *reinterpret_cast<const uint32_t *>(&x);
-            a[2 * h2 + 1] = *reinterpret_cast<const uint32_t *>(&y);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          mma_f16(o[4 * g + i], a[0], a[1], a[2], a[3], h[2 * st][i], h[2 * st + 1][i]);
-          if constexpr (PS) mma_f16(o[4 * g + i], l[0], l[1], l[2], l[3], h[2 * st][i], h[2 * st + 1][i]);
-        }
-        if constexpr (!SV) {
-          mma_f16(cor, a[0], a[1], a[2], a[3], one, one);
-          if constexpr (PS) mma_f16(cor, l[0], l[1], l[2], l[3], one, one);
-        }
+      for (int j = 0; j < 4; ++j) {
+        const __half2 x = __hmul2(*reinterpret_cast<const __half2 *>(&b[j]), *reinterpret_cast<const __half2 *>(&sc[j]));
+        b[j] = *reinterpret_cast<const uint32_t *>(&x);
       }
     }
-  }
-}
-
-// The accumulators in the values' own unit: less 8 times the sum of P', times f0 / f1 (rows lane / 4 and + 8).
-template <int HD, bool SV>
-__device__ __forceinline__ void finish_o(float (&o)[HD / 8][4], const float (&cor)[4], int lane, float f0, float f1) {
 #pragma unroll
-  for (int g = 0; g < HD / 32; ++g) {
-    float c0 = 0.f, c1 = 0.f;
-    if constexpr (!SV) {
-      const int from = (lane & ~3) | (g >> 1);
-      c0 = 8.f * __shfl_sync(0xffffffffu, cor[g & 1], from);
-      c1 = 8.f * __shfl_sync(0xffffffffu, cor[2 + (g & 1)], from);
-    }
+    for (int st = 0; st < 2; ++st)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float u = i & 1 ? 1.f / kUnitHi : 1.f / kUnitLo;
-      float(&x)[4] = o[4 * g + i];
-      x[0] = fmaf(x[0], u, -c0) * f0;
-      x[1] = fmaf(x[1], u, -c0) * f0;
-      x[2] = fmaf(x[2], u, -c1) * f1;
-      x[3] = fmaf(x[3], u, -c1) * f1;
-    }
+      for (int t = 0; t < 2; ++t) {
+        mma_f16(o[t][n], h[2 * st][t], h[2 * st][t + 2], h[2 * st + 1][t], h[2 * st + 1][t + 2], b[2 * st], b[2 * st + 1]);
+        if constexpr (PS)
+          mma_f16(o[t][n], h[2 * st][t], h[2 * st][t + 2], h[2 * st + 1][t], h[2 * st + 1][t + 2], l[2 * st], l[2 * st + 1]);
+      }
   }
 }
 

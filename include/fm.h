@@ -625,8 +625,8 @@ FM_API fm_status fm_kvq_read(fm_kvq *c, int32_t layer, int32_t n_seqs, const int
  * writes the new weights to weights_dev (f32 [n_seqs][n_kv_heads][ldw]) unless
  * that is NULL.  decay < 0: weights are left alone.
  * Sequence ids are distinct where weights are counted.
- * Errors: FM_ERR_INVALID_ARG, FM_ERR_UNSUPPORTED (over 2^20 query rows x heads
- *   in one sequence, or over 2^31 pairs of 16 of those and 128 keys),
+ * Errors: FM_ERR_INVALID_ARG, FM_ERR_UNSUPPORTED (over 2^19 query rows x heads
+ *   in one sequence, or over 2^31 pairs of 32 of those and 128 keys),
  *   FM_ERR_CUDA.  A bounded device wait that gives up is
  *   reported by fm_kvq_synchronize.
  */
