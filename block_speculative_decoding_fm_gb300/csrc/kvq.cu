@@ -182,7 +182,8 @@ fm_status setup(fm_kvq *c, cudaStream_t s) {
   const fm_kvq_config &g = c->cfg;
   KCK(cudaGetDevice(&c->device));
   KCK(cudaDeviceGetAttribute(&c->n_sm, cudaDevAttrMultiProcessorCount, c->device));
-  c->rows_pad = (g.max_rows + kKvqTile - 1) / kKvqTile * kKvqTile;
+  const int stage_rows = kKvqTile * kvq_stage_tiles(g.head_dim);   // (the attention kernel fetches whole stages)
+  c->rows_pad = (g.max_rows + stage_rows - 1) / stage_rows * stage_rows;
   c->plane_bytes = (size_t)(c->rows_pad / kKvqTile) * kvq_tile_bytes(g.head_dim);
   const size_t planes = (size_t)g.n_layers * g.n_seqs * g.n_kv_heads;
   c->slots = 2 * c->n_sm;
@@ -404,6 +405,7 @@ fm_status fm_kvq_attend(fm_kvq *c, int32_t layer, int32_t n_seqs, const int32_t 
     return kfail(c, FM_ERR_INVALID_ARG, "%d query heads over %d KV heads", n_heads, nkv);
   if (!std::isfinite(scale)) return kfail(c, FM_ERR_INVALID_ARG, "scale is not finite");
   if (first_row < 0) return kfail(c, FM_ERR_INVALID_ARG, "first_row %d", first_row);
+  if (first_row > c->cfg.max_rows) first_row = c->cfg.max_rows;   // (past every row either way)
   if (!(decay == decay) || std::isinf(decay)) return kfail(c, FM_ERR_INVALID_ARG, "decay is not finite");
   const bool keep_w = decay >= 0.f;
   if (!keep_w && weights_dev) return kfail(c, FM_ERR_INVALID_ARG, "weights wanted, but decay < 0 keeps none");
@@ -470,8 +472,8 @@ fm_status fm_kvq_attend(fm_kvq *c, int32_t layer, int32_t n_seqs, const int32_t 
     for (; i < n_seqs && a.n < kKvqSeqs; ++i) {
       const int n = n_rows_host[i], L = len[seq_ids_host[i]], j = a.n;
       const int rts = (int)(((int64_t)n * group + unit_rows - 1) / unit_rows);
-      const int t0 = first_row / kKvqTile, t1 = (L + kKvqTile - 1) / kKvqTile;
-      const int stages = t1 > t0 ? (t1 - t0 + kvq_stage_tiles(hd) - 1) / kvq_stage_tiles(hd) : 1;
+      const int t1 = (L + kKvqTile - 1) / kKvqTile;
+      const int s0 = first_row / stage_rows, s1 = (L + stage_rows - 1) / stage_rows, stages = s1 > s0 ? s1 - s0 : 1;
       const int64_t more = (int64_t)rts * nkv * stages;
       if (j && (units + (int64_t)rts * nkv > kMaxUnits || work + more > INT_MAX)) break;
       a.seq[j] = seq_ids_host[i];

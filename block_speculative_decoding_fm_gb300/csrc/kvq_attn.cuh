@@ -99,7 +99,6 @@ struct Cursor {
   const uint8_t *src;     // the next stage
   int32_t at;             // the share's stage after the stretch that the cursor is in
   int32_t left;           // stages of the stretch that are the group's
-  int32_t tiles;          // tiles from the next stage to the unit's end
   int32_t issued;
 };
 static_assert(sizeof(Cursor) <= 32, "a cursor's place in shared memory");
@@ -109,29 +108,23 @@ template <int HD, typename Sh>
 __device__ __forceinline__ bool issue_stage(const KvqAttnArgs &a, Cursor *cu, int w_end, int grp, uint32_t ring,
                                             uint32_t full, uint32_t empty) {
   constexpr int TB = kvq_tile_bytes(HD);
-  int left = cu->left, tiles = cu->tiles;
+  int left = cu->left;
   const uint8_t *src = cu->src;
   while (left == 0) {
     const int at = cu->at;
     if (at >= w_end) return true;
     const Stretch x(a, at, w_end);
-    const int t = a.first / kKvqTile + (x.s0 + grp) * Sh::KT;
+    // (a unit that sees no rows has one stage, whatever is there: every score of it is masked)
+    const int t = min((a.first / (kKvqTile * Sh::KT) + x.s0 + grp) * Sh::KT, a.c.rows_pad / kKvqTile - Sh::KT);
     left = (x.n - grp + Sh::NG - 1) / Sh::NG;
-    tiles = (a.len[x.i] + kKvqTile - 1) / kKvqTile - t;
     src = a.c.planes + ((size_t)a.seq[x.i] * a.c.n_kv + x.head) * a.c.plane_bytes + (size_t)t * TB;
     cu->at = at + x.n;
   }
   const int g = cu->issued, slot = g % Sh::NS;
   if (g >= Sh::NS && !mbar_wait_bounded(empty + slot * 8, (g / Sh::NS - 1) & 1, a.c.err)) return false;
-  if (tiles > 0) {
-    const uint32_t bytes = min(Sh::KT, tiles) * TB;
-    mbar_expect_tx(full + slot * 8, bytes);
-    bulk_g2s(ring + slot * Sh::SB, src, bytes, full + slot * 8);
-  } else {
-    mbar_arrive(full + slot * 8);   // a unit without keys has one stage of nothing
-  }
+  mbar_expect_tx(full + slot * 8, Sh::SB);
+  bulk_g2s(ring + slot * Sh::SB, src, Sh::SB, full + slot * 8);   // (whole stages: planes are padded to them)
   cu->left = left - 1;
-  cu->tiles = tiles - Sh::NG * Sh::KT;
   cu->src = src + Sh::NG * Sh::SB;
   cu->issued = g + 1;
   return true;
@@ -188,7 +181,7 @@ __global__ void __launch_bounds__(Shape<HD, T, NQ>::kThreads, 1) kvq_attend_kern
   using Sh = Shape<HD, T, NQ>;
   using QT = typename Sh::QT;
   using PT = typename Sh::PT;
-  constexpr bool QS = Sh::QS, PS = Sh::PS;
+  constexpr bool QS = Sh::QS, PS = Sh::PS, SV = Sh::SV;
   constexpr int NG = Sh::NG, NS = Sh::NS, SB = Sh::SB, TB = kvq_tile_bytes(HD), RT = Sh::RT, KS = Sh::KS, MT = Sh::MT;
   constexpr int GP = Sh::GP, KP = Sh::KP, NT = Sh::kThreads;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -245,7 +238,11 @@ __global__ void __launch_bounds__(Shape<HD, T, NQ>::kThreads, 1) kvq_attend_kern
     __syncthreads();
     const int lim_all = a.causal ? len - T_rows + rq / a.group + 1 : len;   // the rows that every query row sees end here
 
-    float o[GP][2][NQ][4], m[NQ][2];
+    float o[GP][2][NQ][4], cor[GP][(NQ + 1) / 2][4], m[NQ][2];
+#pragma unroll
+    for (int u = 0; u < GP; ++u)
+#pragma unroll
+      for (int n = 0; n < (NQ + 1) / 2; ++n) cor[u][n][0] = cor[u][n][1] = cor[u][n][2] = cor[u][n][3] = 0.f;
     uint64_t l[NQ];                          // row sums of this warp's strips
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
@@ -256,7 +253,7 @@ __global__ void __launch_bounds__(Shape<HD, T, NQ>::kThreads, 1) kvq_attend_kern
 #pragma unroll
         for (int t = 0; t < 2; ++t) o[u][t][n][0] = o[u][t][n][1] = o[u][t][n][2] = o[u][t][n][3] = 0.f;
     }
-    int tile0 = a.first / kKvqTile + (x.s0 + grp) * Sh::KT;
+    int tile0 = (a.first / (kKvqTile * Sh::KT) + x.s0 + grp) * Sh::KT;
     for (int k = grp; k < x.n; k += NG, tile0 += NG * Sh::KT) {
       // a stage ahead of the ring's end; then this one (a wait that gave up ends the group's work, not its barriers)
       if (copies && ok) ok = issue_stage<HD, Sh>(a, cu, w_end, grp, ring, full, empty);
@@ -264,37 +261,30 @@ __global__ void __launch_bounds__(Shape<HD, T, NQ>::kThreads, 1) kvq_attend_kern
       const int key0 = tile0 * kKvqTile + strip;
       uint8_t *pt = ptile + buf * PT::kBytes;
       float s[MT][NQ][4];
-      if (ok && key0 < len && key0 + KS > a.first) {
-        uint64_t sp[MT][NQ][2];
-        strip_scores<HD, QS, NQ, KS>(kcode + slot * SB, kscale + slot * SB, qt, lane, sp);
+      uint64_t sp[MT][NQ][2];
+      strip_scores<HD, QS, NQ, KS>(kcode + slot * SB, kscale + slot * SB, qt, lane, sp);
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+      for (int i = 0; i < MT; ++i)
 #pragma unroll
-          for (int n = 0; n < NQ; ++n) {
-            unpack2(sp[i][n][0], s[i][n][0], s[i][n][1]);
-            unpack2(sp[i][n][1], s[i][n][2], s[i][n][3]);
-          }
-        if (key0 < a.first || key0 + KS > lim_all) {
-#pragma unroll
-          for (int n = 0; n < NQ; ++n)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {   // (rows past R follow the last: they are not stored)
-              const int row = min(rq + 8 * n + 2 * c + h, R - 1);
-              const int lim = a.causal ? len - T_rows + row / a.group + 1 : len;
-#pragma unroll
-              for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const int key = key0 + 16 * i + 8 * e + g8;
-                  if (key < a.first || key >= lim) s[i][n][2 * e + h] = -INFINITY;
-                }
-            }
+        for (int n = 0; n < NQ; ++n) {
+          unpack2(sp[i][n][0], s[i][n][0], s[i][n][1]);
+          unpack2(sp[i][n][1], s[i][n][2], s[i][n][3]);
         }
-      } else {
+      if (key0 < a.first || key0 + KS > lim_all) {
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+        for (int n = 0; n < NQ; ++n)
 #pragma unroll
-          for (int n = 0; n < NQ; ++n) s[i][n][0] = s[i][n][1] = s[i][n][2] = s[i][n][3] = -INFINITY;
+          for (int h = 0; h < 2; ++h) {   // (rows past R follow the last: they are not stored)
+            const int row = min(rq + 8 * n + 2 * c + h, R - 1);
+            const int lim = a.causal ? len - T_rows + row / a.group + 1 : len;
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int key = key0 + 16 * i + 8 * e + g8;
+                if (key < a.first || key >= lim) s[i][n][2 * e + h] = -INFINITY;
+              }
+          }
       }
       // P with the references as they are; who beats one by 2^8 says so at the barrier
       float p[MT][NQ][4];
@@ -355,6 +345,12 @@ __global__ void __launch_bounds__(Shape<HD, T, NQ>::kThreads, 1) kvq_attend_kern
           for (int u = 0; u < GP; ++u)
 #pragma unroll
             for (int t = 0; t < 2; ++t) o[u][t][n][0] *= f0, o[u][t][n][1] *= f1, o[u][t][n][2] *= f0, o[u][t][n][3] *= f1;
+          if constexpr (!SV) {   // (by query row lane / 4: the factor of column lane / 4)
+            const float e0 = __shfl_sync(0xffffffffu, f0, (lane & ~3) | (g8 >> 1)), e1 = __shfl_sync(0xffffffffu, f1, (lane & ~3) | (g8 >> 1));
+            const float f = g8 & 1 ? e1 : e0;
+#pragma unroll
+            for (int u = 0; u < GP; ++u) cor[u][n / 2][2 * (n & 1)] *= f, cor[u][n / 2][2 * (n & 1) + 1] *= f;
+          }
           const float2 mu = *reinterpret_cast<const float2 *>(qs + QT::kMult + (8 * n + 2 * c) * 4);
           const float b0 = range.bias - (n0 == -INFINITY ? 0.f : n0), b1 = range.bias - (n1 == -INFINITY ? 0.f : n1);
 #pragma unroll
@@ -372,28 +368,36 @@ __global__ void __launch_bounds__(Shape<HD, T, NQ>::kThreads, 1) kvq_attend_kern
       }
 #pragma unroll
       for (int n = 0; n < NQ; ++n) l[n] = add2(l[n], add[n]);
-      if (ok) {
+      {
+        // the warp's blocks of 32 rows (KP > 1: every KP-th) and their scales
+        constexpr int NB = 2 * Sh::KT / KP;
+        uint32_t sc[NB][GP][4];
 #pragma unroll
-        for (int kb = 0; kb < 2 * Sh::KT; kb += KP) {
-          const int key = 32 * (kb + kp);               // the block's rows in the stage (warps with kp take every KP-th)
-          if (KP > 1 && key >= 64 * Sh::KT) break;
-          const int tile = key / kKvqTile, r0 = key % kKvqTile;
-          if (tile0 * kKvqTile + key < len) {           // (rows behind the end: P is 0, but their tile may not be there)
+        for (int kb = 0; kb < NB; ++kb)
 #pragma unroll
-            for (int u = 0; u < GP; ++u) {
-              uint32_t sc[4];
-              const uint4 v = lds128(vscale + slot * SB + tile * TB + (4 * u * 4 * 16) * 2 + r0 / 8 * 4);
-              sc[0] = v.x, sc[1] = v.y, sc[2] = v.z, sc[3] = v.w;
-              if (!PS && range.shifted) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&sc[j]), range.up);
-                  sc[j] = *reinterpret_cast<const uint32_t *>(&y);
-                }
-              }
-              tile_pv<HD, PS, NQ, KS>(vcode + slot * SB + tile * TB + r0 * (HD / 2), gw + 4 * u, sc, pt, key, lane, o[u]);
-            }
+          for (int u = 0; u < GP; ++u) {
+            const int key = 32 * (kb * KP + kp);
+            const uint4 v = lds128(vscale + slot * SB + key / kKvqTile * TB + 4 * u * 128 + key % kKvqTile / 2);
+            sc[kb][u][0] = v.x, sc[kb][u][1] = v.y, sc[kb][u][2] = v.z, sc[kb][u][3] = v.w;
           }
+        if (!PS && range.shifted) {
+#pragma unroll
+          for (int kb = 0; kb < NB; ++kb)
+#pragma unroll
+            for (int u = 0; u < GP; ++u)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&sc[kb][u][j]), range.up);
+                sc[kb][u][j] = *reinterpret_cast<const uint32_t *>(&y);
+              }
+        }
+#pragma unroll
+        for (int kb = 0; kb < NB; ++kb) {
+          const int key = 32 * (kb * KP + kp);
+#pragma unroll
+          for (int u = 0; u < GP; ++u)
+            tile_pv<HD, PS, SV, NQ, KS>(vcode + slot * SB + key / kKvqTile * TB + key % kKvqTile * (HD / 2), gw + 4 * u,
+                                        sc[kb][u], pt, key, lane, o[u], cor[u]);
         }
       }
       __syncwarp();
@@ -439,11 +443,17 @@ __global__ void __launch_bounds__(Shape<HD, T, NQ>::kThreads, 1) kvq_attend_kern
       for (int n = 0; n < NQ; ++n) {
         const float M0 = s_row[8 * n + 2 * c].x, M1 = s_row[8 * n + 2 * c + 1].x;
         const float f0 = m[n][0] == M0 ? 1.f : ex2(m[n][0] - M0), f1 = m[n][1] == M1 ? 1.f : ex2(m[n][1] - M1);
+        float c0 = 0.f, c1 = 0.f;
+        if constexpr (!SV) {
+          c0 = 8.f * __shfl_sync(0xffffffffu, cor[u][n / 2][2 * (n & 1)], 8 * c);
+          c1 = 8.f * __shfl_sync(0xffffffffu, cor[u][n / 2][2 * (n & 1)], 8 * c + 4);
+        }
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           const float unit = t ? 1.f / kUnitHi : 1.f / kUnitLo;
           float(&y)[4] = o[u][t][n];
-          y[0] *= unit * f0, y[1] *= unit * f1, y[2] *= unit * f0, y[3] *= unit * f1;
+          y[0] = fmaf(y[0], unit, -c0) * f0, y[1] = fmaf(y[1], unit, -c1) * f1;
+          y[2] = fmaf(y[2], unit, -c0) * f0, y[3] = fmaf(y[3], unit, -c1) * f1;
           if (grp > 0 || kp > 0) *reinterpret_cast<float4 *>(ob + ((u * NQ + n) * 2 + t) * 128) = make_float4(y[0], y[1], y[2], y[3]);
         }
       }

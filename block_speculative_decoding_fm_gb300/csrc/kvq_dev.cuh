@@ -106,17 +106,18 @@ struct Kind {
   static constexpr int NQ = NQ_, RT = 8 * NQ, G = HD / 32;
   static constexpr bool QS = sizeof(T) == 4;                          // f32 queries: f16 hi + lo
   static constexpr bool PS = !std::is_same<T, __nv_bfloat16>::value;  // f16 and f32 outputs: P' too
+  static constexpr bool SV = sizeof(T) == 4;                          // f32 outputs: signed V codes (no sums to take off)
   static constexpr int KS = 16 * kvq_stage_tiles(HD), MT = KS / 16;   // a strip, in 16-key products
 };
 
 // D = A B + C with D apart from C
 __device__ __forceinline__ void mma_f16_c(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                          uint32_t b1, float c0, float c1) {
+                                          uint32_t b1, const uint4 &c) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%10,%11,%10,%11};\n"
+      "{%10,%11,%12,%13};\n"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(c.x), "r"(c.y), "r"(c.z), "r"(c.w));
 }
 
 // A query tile in shared memory: B fragments of the group's dims (hi, and lo
@@ -124,8 +125,8 @@ __device__ __forceinline__ void mma_f16_c(float (&d)[4], uint32_t a0, uint32_t a
 template <int HD, bool QS, int NQ>
 struct QTile {
   static constexpr int kLo = HD * NQ * 16;                      // [group][row / 8][lane] 16 bytes
-  static constexpr int kOff = kLo * (QS ? 2 : 1);               // f32 [group][row]
-  static constexpr int kMult = kOff + HD / 32 * NQ * 8 * 4;     // f32 [row]
+  static constexpr int kOff = kLo * (QS ? 2 : 1);               // f32 [group][row / 2][the pair, twice] (an accumulator fragment)
+  static constexpr int kMult = kOff + HD / 32 * NQ * 8 * 8;     // f32 [row]
   static constexpr int kBytes = kMult + NQ * 8 * 4;
 };
 
@@ -188,7 +189,10 @@ __device__ __forceinline__ void load_q(const T *q, int64_t ldq, int group, int r
     if constexpr (QS) *reinterpret_cast<uint4 *>(tile + QT::kLo + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     sum += __shfl_xor_sync(0xffffffffu, sum, 1);
     sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-    if ((o & 3) == 0) reinterpret_cast<float *>(tile + QT::kOff)[g * NQ * 8 + r] = -8.f * kUnitHi * sum;
+    if ((o & 3) == 0) {
+      float *off = reinterpret_cast<float *>(tile + QT::kOff) + (g * NQ * 4 + (r >> 1)) * 4 + (r & 1);
+      off[0] = off[2] = -8.f * kUnitHi * sum;
+    }
   }
 }
 
@@ -244,13 +248,12 @@ __device__ __forceinline__ void strip_scores(uint32_t code, uint32_t scale, uint
         for (int j = 0; j < 2 * MT; ++j) codes_f16(w[2 * f * (GF - 1) + j], h[j]);
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
-          const uint2 off = lds64(qt + QT::kOff + (g * NQ + n) * 32 + (lane & 3) * 8);
+          const uint4 off = lds128(qt + QT::kOff + (g * NQ + n) * 64 + (lane & 3) * 16);
           const uint4 b = lds128(qt + ((g * NQ + n) * 32 + lane) * 16);
           float acc[MT][4];
 #pragma unroll
           for (int m = 0; m < MT; ++m)
-            mma_f16_c(acc[m], h[2 * m][0], h[2 * m + 1][0], h[2 * m][1], h[2 * m + 1][1], b.x, b.y, __uint_as_float(off.x),
-                      __uint_as_float(off.y));
+            mma_f16_c(acc[m], h[2 * m][0], h[2 * m + 1][0], h[2 * m][1], h[2 * m + 1][1], b.x, b.y, off);
 #pragma unroll
           for (int m = 0; m < MT; ++m) mma_f16(acc[m], h[2 * m][2], h[2 * m + 1][2], h[2 * m][3], h[2 * m + 1][3], b.z, b.w);
           if constexpr (QS) {
@@ -340,45 +343,66 @@ struct PRange {
   }
 };
 
-// O^T += V^T P^T over the 32 rows from r0 on of a tile (vb: its V half), group g:
+// O^T += V^T P^T over 32 rows of a tile (code: where the lane fetches their unit of group 0), group g:
 // o[t][n] are the accumulators of dims 32 g + 4 (lane / 4) + t (first pair) and + 2 (second), query
 // rows 8 n + 2 (lane % 4) and + 1, in the code pairs' units (t = 0: 2^-24, t = 1: 2^-20).
 // sc: the V scales of the rows' pairs (kvq_vscale's order).  P' = p d is rounded to
-// f16 once more (PS: split into hi + lo, which keeps ~22 bits).
-template <int HD, bool PS, int NQ, int KS>
+// f16 once more (PS: split into hi + lo, which keeps ~22 bits).  SV: the codes enter
+// with their 8 taken off; else unsigned, and cor collects the sums of P' (a
+// product with ones; P's fragments of two query octets serve as its first operand,
+// query row lane / 4 and + 8), which the end takes off eight times.
+template <int HD, bool PS, bool SV, int NQ, int KS>
 __device__ __forceinline__ void tile_pv(uint32_t code, int g, const uint32_t (&sc)[4], const uint8_t *pt, int key0, int lane,
-                                        float (&o)[2][NQ][4]) {
+                                        float (&o)[2][NQ][4], float (&cor)[(NQ + 1) / 2][4]) {
   using PT = PTile<NQ, PS, KS>;
   uint32_t w[4], h[4][4];
   ldsm_x4_trans(code ^ (g << 4), w[0], w[1], w[2], w[3]);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) codes_f16_signed(w[j], h[j]);
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (SV)
+      codes_f16_signed(w[j], h[j]);
+    else
+      codes_f16(w[j], h[j]);
+  }
+  uint32_t b[NQ][4], l[NQ][4];
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
-    uint32_t b[4], l[4];
     if constexpr (PS) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const uint2 v = lds64(smem_u32(pt) + (8 * n + (lane >> 2)) * PT::kRow + (key0 + 8 * j + 2 * (lane & 3)) * 4);
         const float2 d = pair_f32(sc[j]);
-        split2_f16(__uint_as_float(v.x) * d.x, __uint_as_float(v.y) * d.y, b[j], l[j]);
+        split2_f16(__uint_as_float(v.x) * d.x, __uint_as_float(v.y) * d.y, b[n][j], l[n][j]);
       }
     } else {
-      ldsm_x4(smem_u32(pt) + (8 * n + (lane & 7)) * PT::kRow + (key0 + (lane >> 3) * 8) * 2, b);
+      ldsm_x4(smem_u32(pt) + (8 * n + (lane & 7)) * PT::kRow + (key0 + (lane >> 3) * 8) * 2, b[n]);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const __half2 x = __hmul2(*reinterpret_cast<const __half2 *>(&b[j]), *reinterpret_cast<const __half2 *>(&sc[j]));
-        b[j] = *reinterpret_cast<const uint32_t *>(&x);
+        const __half2 x = __hmul2(*reinterpret_cast<const __half2 *>(&b[n][j]), *reinterpret_cast<const __half2 *>(&sc[j]));
+        b[n][j] = *reinterpret_cast<const uint32_t *>(&x);
       }
     }
 #pragma unroll
     for (int st = 0; st < 2; ++st)
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        mma_f16(o[t][n], h[2 * st][t], h[2 * st][t + 2], h[2 * st + 1][t], h[2 * st + 1][t + 2], b[2 * st], b[2 * st + 1]);
+        mma_f16(o[t][n], h[2 * st][t], h[2 * st][t + 2], h[2 * st + 1][t], h[2 * st + 1][t + 2], b[n][2 * st], b[n][2 * st + 1]);
         if constexpr (PS)
-          mma_f16(o[t][n], h[2 * st][t], h[2 * st][t + 2], h[2 * st + 1][t], h[2 * st + 1][t + 2], l[2 * st], l[2 * st + 1]);
+          mma_f16(o[t][n], h[2 * st][t], h[2 * st][t + 2], h[2 * st + 1][t], h[2 * st + 1][t + 2], l[n][2 * st], l[n][2 * st + 1]);
       }
+    if constexpr (!SV) {
+      if ((n & 1) || n + 1 == NQ) {
+        constexpr uint32_t kOnes = 0x3c003c00u;
+        const int e = n & ~1;                // the octet's partner, or nothing
+        const bool two = n & 1;
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+          mma_f16(cor[n / 2], b[e][2 * st], two ? b[n][2 * st] : 0u, b[e][2 * st + 1], two ? b[n][2 * st + 1] : 0u, kOnes, kOnes);
+          if constexpr (PS)
+            mma_f16(cor[n / 2], l[e][2 * st], two ? l[n][2 * st] : 0u, l[e][2 * st + 1], two ? l[n][2 * st + 1] : 0u, kOnes, kOnes);
+        }
+      }
+    }
   }
 }
 

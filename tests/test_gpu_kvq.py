@@ -216,6 +216,8 @@ def test_attend_split(hd, hkv, group, T, name):
     c.append([0, 1, 2], [9000, 5, 700], [0, 0, 0], rng, name)
     attend_case(c, [0, 1, 2], [T, T, T], group, name, rng, causal=True, decay=0.0, qsize=2.0)
     attend_case(c, [0], [T], group, name, rng, first=4321)
+    for first in (8999, 9000, 2 ** 31 - 1):     # one row left, and none
+        attend_case(c, [2, 0], [T, T], group, name, rng, first=first, decay=0.0)
 
 
 def test_weights_accumulate():
