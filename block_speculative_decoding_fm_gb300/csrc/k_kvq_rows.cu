@@ -5,9 +5,14 @@
 // c = clamp(rint(x / d) + 8, 0, 15), ties to even, 8 where d = 0; it stands for
 // d (c - 8).  NaN counts as 0, infinities saturate (|d| <= 65504).
 //
-// The code is exact: c' = rint(x * (1 / d)) may be one off next to a border
-// because the reciprocal is rounded, so it is corrected against the borders
-// d (c' +- 1/2), which are exact in f32 (11-bit d times a 5-bit odd number).
+// The codes are exact without a division.  From 16-bit values: a quotient that is
+// not itself halfway between two codes is at least 2^-12 away from there (x a multiple of
+// d's last place near a border, d an 11-bit number), so x * (1 / d) + 776, rounded by the
+// addition to 2^-14, is halfway exactly where x / d is, whatever the reciprocal's
+// rounding, and adding 1.5 * 2^23 then rounds to the code, ties to even, in the sum's low byte.
+// From f32 values the remainder x - c d, which is exact, tells whether c is off by one.
+// A group with NaN, infinities or a scale at the ends of f16 (rare) takes a slower way: c = rint(x * (1 / d))
+// corrected against the borders d (c +- 1/2), exact in f32 (an 11-bit d times a 5-bit odd number).
 //
 // Bound by memory: a row of n values is read once (2 n or 4 n bytes) and
 // written as 0.5625 n bytes.  Four lanes share a group, eight consecutive values each
@@ -24,6 +29,26 @@ namespace {
 
 constexpr int kThreads = 256;
 
+__device__ __forceinline__ float2 floats(__half2 v) { return __half22float2(v); }
+__device__ __forceinline__ float2 floats(__nv_bfloat162 v) { return __bfloat1622float2(v); }
+
+// largest and smallest of eight 16-bit values, two at a time, and a sum that is 0 unless a value is not finite
+template <typename P>
+__device__ __forceinline__ void extremes_16(const uint4 &a, float &hi, float &lo, float &odd) {
+  const P *v = reinterpret_cast<const P *>(&a);
+  P h = v[0], l = v[0], zero = __hsub2(v[0], v[0]);   // (x - x: 0, or NaN where x is not finite)
+#pragma unroll
+  for (int i = 1; i < 4; ++i) {
+    h = __hmax2(h, v[i]);
+    l = __hmin2(l, v[i]);
+    zero = __hadd2(zero, __hsub2(v[i], v[i]));
+  }
+  const float2 hf = floats(h), lf = floats(l), zf = floats(zero);
+  hi = fmaxf(hf.x, hf.y);
+  lo = fminf(lf.x, lf.y);
+  odd = zf.x + zf.y;
+}
+
 template <typename T>
 struct Eight;
 template <>
@@ -35,6 +60,15 @@ struct Eight<float> {
   }
   __device__ __forceinline__ void get(float (&x)[8]) const {
     x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  }
+  // largest and smallest value, and a sum that is 0 unless a value is not finite
+  __device__ __forceinline__ void extremes(float &hi, float &lo, float &odd) const {
+    float x[8];
+    get(x);
+    hi = lo = x[0];
+    odd = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) hi = fmaxf(hi, x[e]), lo = fminf(lo, x[e]), odd = fmaf(x[e], 0.f, odd);
   }
   static __device__ __forceinline__ void store(float *p, const float (&x)[8]) {
     reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
@@ -53,6 +87,7 @@ struct Eight<__half> {
       x[2 * i] = f.x, x[2 * i + 1] = f.y;
     }
   }
+  __device__ __forceinline__ void extremes(float &hi, float &lo, float &odd) const { extremes_16<__half2>(a, hi, lo, odd); }
   static __device__ __forceinline__ void store(__half *p, const float (&x)[8]) {
     uint32_t w[4];
 #pragma unroll
@@ -74,6 +109,7 @@ struct Eight<__nv_bfloat16> {
       x[2 * i] = __uint_as_float(w << 16), x[2 * i + 1] = __uint_as_float(w & 0xffff0000u);
     }
   }
+  __device__ __forceinline__ void extremes(float &hi, float &lo, float &odd) const { extremes_16<__nv_bfloat162>(a, hi, lo, odd); }
   static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&x)[8]) {
     uint32_t w[4];
 #pragma unroll
@@ -96,6 +132,58 @@ __device__ __forceinline__ int find_seq(const int32_t *pre, int n, int x) {
       hi = mid - 1;
   }
   return lo;
+}
+
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// the codes of eight values of a group with scale d, packed: any values, any scale
+__device__ __forceinline__ uint32_t codes_any(const float (&v)[8], float d) {
+  const float inv = d == 0.f ? 0.f : 1.f / d, ad = fabsf(d);
+  uint32_t w = 0;
+#pragma unroll 1
+  for (int e = 0; e < 8; ++e) {
+    const float x = v[e] == v[e] ? v[e] : 0.f;
+    float c = rintf(fminf(fmaxf(x * inv, -9.f), 9.f));
+    // the borders of code c, in the units of |d|
+    const float xs = d < 0.f ? -x : x, up = ad * (c + 0.5f), dn = ad * (c - 0.5f);
+    const bool odd = (static_cast<int>(c) & 1) != 0;
+    if (xs > up || (xs == up && odd)) c += 1.f;
+    else if (xs < dn || (xs == dn && odd)) c -= 1.f;
+    w |= (uint32_t)(d == 0.f ? 8 : min(15, max(0, static_cast<int>(c) + 8))) << (4 * e);
+  }
+  return w;
+}
+
+// the low bytes of four words, in order
+__device__ __forceinline__ uint32_t low_bytes(const uint32_t (&t)[4]) {
+  return __byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410);
+}
+
+// the same for finite values and 0 or 2^-14 <= |d| < 65504
+template <typename T>
+__device__ __forceinline__ uint32_t codes_fast(const float (&x)[8], float d) {
+  const float inv = d == 0.f ? 0.f : rcp(d);
+  uint32_t even[4], odd[4];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    float t;
+    if constexpr (sizeof(T) == 2) {
+      t = fminf(fmaf(x[e], inv, 776.f), 783.f) + 12582912.f;
+    } else {
+      constexpr float kMagic = 12582912.f;
+      const float c = fmaf(x[e], inv, kMagic) - kMagic, rem = fmaf(-c, d, x[e]);
+      const float half = d == 0.f ? INFINITY : 0.5f * fabsf(d);
+      const bool off = fabsf(rem) > half || (fabsf(rem) == half && (__float_as_uint(c + kMagic) & 1u));
+      const float step = off ? copysignf(1.f, rem) * copysignf(1.f, d) : 0.f;
+      t = fminf(fmaxf(c + step, -8.f), 7.f) + (kMagic + 8.f);
+    }
+    (e & 1 ? odd : even)[e >> 1] = __float_as_uint(t);
+  }
+  return low_bytes(even) | low_bytes(odd) << 4;
 }
 
 // Grid (touched tile, KV head, K or V); thread = (row, eight values).
@@ -127,42 +215,23 @@ __global__ void __launch_bounds__(kThreads) kvq_append_kernel(const __grid_const
   for (int p = 0; p < NP; ++p) {
     const int tr = p * RP + r0, r = tile * kKvqTile + tr - at;
     const bool ok = r >= 0 && r < rows;
-    float x[8];
-    if (ok) {
-      in[p].get(x);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = 0.f;
-    }
-    float hi = -INFINITY, lo = INFINITY;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      x[e] = x[e] == x[e] ? x[e] : 0.f;
-      hi = fmaxf(hi, x[e]);
-      lo = fminf(lo, x[e]);
-    }
+    float x[8], hi = 0.f, lo = 0.f, odd = 0.f;
+    if (ok) in[p].extremes(hi, lo, odd);
 #pragma unroll
     for (int s = 1; s < 4; s <<= 1) {
       hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, s));
       lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, s));
     }
-    const float m = hi > -lo ? hi : lo;
+    // (a lane whose values are all NaN has NaN here: it counts for nothing, and all of them for 0)
+    const float m = hi > -lo ? hi : lo == lo ? lo : 0.f;
     const __half dh = __float2half_rn(fminf(fmaxf(m * -0.125f, -65504.f), 65504.f));
-    const float d = __half2float(dh);
-    const float inv = d == 0.f ? 0.f : 1.f / d;
+    const float d = __half2float(dh), ad = fabsf(d);
+    if (ok) in[p].get(x);
     uint32_t w = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      // |x / d| <= 8 (1 + 2^-11) unless d was clamped or is subnormal: the first guess is clamped to +-9
-      float c = rintf(fminf(fmaxf(x[e] * inv, -9.f), 9.f));
-      // the borders of code c, in the units of |d|: exact products
-      const float xs = d < 0.f ? -x[e] : x[e], ad = fabsf(d);
-      const float up = ad * (c + 0.5f), dn = ad * (c - 0.5f);
-      const bool odd = (static_cast<int>(c) & 1) != 0;
-      if (xs > up || (xs == up && odd)) c += 1.f;
-      else if (xs < dn || (xs == dn && odd)) c -= 1.f;
-      const int code = d == 0.f ? 8 : min(15, max(0, static_cast<int>(c) + 8));
-      w |= (uint32_t)code << (4 * e);
+    if (odd == 0.f && (ad >= 6.103515625e-05f || ad == 0.f) && ad < 65504.f) {
+      if (ok) w = codes_fast<T>(x, d);
+    } else if (ok) {
+      w = codes_any(x, d);
     }
     if (!ok) continue;
     *reinterpret_cast<uint32_t *>(half_tile + kvq_unit(tr, o >> 2, HD) + (o & 3) * 4) = w;

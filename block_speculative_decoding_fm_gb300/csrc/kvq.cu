@@ -218,7 +218,7 @@ fm_status fm_kvq_create(const fm_kvq_config *cfg, void *stream, fm_kvq **out) {
   const fm_kvq_config g = *cfg;
   if (g.head_dim != 64 && g.head_dim != 128 && g.head_dim != 256)
     return kfail(nullptr, FM_ERR_UNSUPPORTED, "head_dim %d: 64, 128 or 256", g.head_dim);
-  if (g.n_layers < 1 || g.n_layers > 1024 || g.n_seqs < 1 || g.n_seqs > 65536 || g.n_kv_heads < 1 || g.n_kv_heads > 1024 ||
+  if (g.n_layers < 1 || g.n_layers > 1024 || g.n_seqs < 1 || g.n_seqs > 65536 || g.n_kv_heads < 1 || g.n_kv_heads > 256 ||
       g.max_rows < 1 || g.max_rows > kMaxRows)
     return kfail(nullptr, FM_ERR_INVALID_ARG, "n_layers %d, n_seqs %d, n_kv_heads %d or max_rows %d out of range", g.n_layers,
                  g.n_seqs, g.n_kv_heads, g.max_rows);

@@ -565,7 +565,7 @@ FM_API void fm_mtp_destroy(fm_mtp *m);
 typedef struct fm_kvq_config {
   int32_t n_layers;    /* 1 .. 1024 */
   int32_t n_seqs;      /* sequences (slots) per layer: 1 .. 65536 */
-  int32_t n_kv_heads;  /* 1 .. 1024 */
+  int32_t n_kv_heads;  /* 1 .. 256 */
   int32_t head_dim;    /* 64, 128 or 256 */
   int32_t max_rows;    /* rows per sequence and layer: 1 .. 2^24 */
 } fm_kvq_config;
