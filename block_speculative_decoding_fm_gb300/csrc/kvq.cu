@@ -28,7 +28,7 @@ struct fm_kvq {
   float *weights = nullptr, *part_o = nullptr, *lse = nullptr;
   uint32_t *vmax = nullptr;
   float2 *part_ml = nullptr;
-  int32_t *list = nullptr, *dev_err = nullptr, *tickets = nullptr;
+  int32_t *list = nullptr, *dev_err = nullptr;
   int slots = 0;                  // partial results the workspace holds
   int64_t bytes = 0;
   std::vector<int32_t> len;       // [layers][seqs]
@@ -172,7 +172,7 @@ fm_status dev_alloc(fm_kvq *c, T **p, size_t n) {
 
 void release(fm_kvq *c) {
   for (void *p : {(void *)c->planes, (void *)c->weights, (void *)c->part_o, (void *)c->lse, (void *)c->vmax,
-                  (void *)c->part_ml, (void *)c->list, (void *)c->dev_err, (void *)c->tickets})
+                  (void *)c->part_ml, (void *)c->list, (void *)c->dev_err})
     if (p) cudaFree(p);
   if (c->done) cudaEventDestroy(c->done);
   delete c;
@@ -186,7 +186,7 @@ fm_status setup(fm_kvq *c, cudaStream_t s) {
   c->rows_pad = (g.max_rows + stage_rows - 1) / stage_rows * stage_rows;
   c->plane_bytes = (size_t)(c->rows_pad / kKvqTile) * kvq_tile_bytes(g.head_dim);
   const size_t planes = (size_t)g.n_layers * g.n_seqs * g.n_kv_heads;
-  c->slots = 2 * c->n_sm;
+  c->slots = 2 * kKvqMaxCtas * c->n_sm;
   KTRY(dev_alloc(c, &c->planes, planes * c->plane_bytes));
   KTRY(dev_alloc(c, &c->weights, planes * c->rows_pad));
   KTRY(dev_alloc(c, &c->vmax, planes));
@@ -195,13 +195,11 @@ fm_status setup(fm_kvq *c, cudaStream_t s) {
   KTRY(dev_alloc(c, &c->lse, (size_t)kMaxUnits * 8 * kKvqMaxNQ));
   KTRY(dev_alloc(c, &c->list, (size_t)(g.n_seqs < kKvqSeqs ? g.n_seqs : kKvqSeqs) * g.n_kv_heads * c->rows_pad));
   KTRY(dev_alloc(c, &c->dev_err, 4));
-  KTRY(dev_alloc(c, &c->tickets, (size_t)kMaxUnits));
   // rows behind a sequence's end are read with the last tile: they hold finite values from the start
   KCK(cudaMemsetAsync(c->planes, 0, planes * c->plane_bytes, s));
   KCK(cudaMemsetAsync(c->weights, 0, planes * c->rows_pad * sizeof(float), s));
   KCK(cudaMemsetAsync(c->vmax, 0, planes * sizeof(uint32_t), s));
   KCK(cudaMemsetAsync(c->dev_err, 0, 16, s));
-  KCK(cudaMemsetAsync(c->tickets, 0, kMaxUnits * sizeof(int32_t), s));
   KCK(cudaEventCreateWithFlags(&c->done, cudaEventDisableTiming));
   KCK(cudaStreamSynchronize(s));
   return FM_OK;
@@ -454,7 +452,6 @@ fm_status fm_kvq_attend(fm_kvq *c, int32_t layer, int32_t n_seqs, const int32_t 
   a.scale_log2 = scale * 1.4426950408889634f;
   a.causal = causal != 0;
   a.first = first_row;
-  a.tickets = c->tickets;
   a.part_o = c->part_o;
   a.part_ml = c->part_ml;
   a.lse = keep_w ? c->lse : nullptr;
@@ -494,8 +491,9 @@ fm_status fm_kvq_attend(fm_kvq *c, int32_t layer, int32_t n_seqs, const int32_t 
     a.st0[a.n] = (int32_t)work;
     a.unit0[a.n] = un;
     a.wt0[a.n] = wt;
-    // a CTA an SM, each with the same number of stages, whatever unit they belong to
-    a.ctas = (int32_t)(work < c->n_sm ? work : c->n_sm);
+    // as many CTAs as the SMs hold, each with the same number of stages, whatever unit they belong to
+    const int64_t most_ctas = (int64_t)c->n_sm * kvq_attn_ctas_per_sm(hd, type, nq);
+    a.ctas = (int32_t)(work < most_ctas ? work : most_ctas);
     if (work > 0) {
       a.share = (int32_t)(work / a.ctas);
       a.extra = (int32_t)(work % a.ctas);

@@ -90,7 +90,6 @@ struct KvqAttnArgs {
   int32_t n;              // sequences of this launch
   int32_t ctas;           // CTAs of the launch: of the W = st0[n] stages CTA b takes
   int32_t share, extra;   // share = W / ctas, and one more where b < extra = W % ctas
-  int32_t *tickets;       // [units] zero between launches: parts of a split unit that are done
   float *part_o;          // [2 ctas][8 nq][hd] unnormalised partial outputs
   float2 *part_ml;        // [2 ctas][8 nq] (reference, row sum)
   float *lse;             // [units][8 nq] log2 of the row sums, for the weights; or null
@@ -109,6 +108,13 @@ struct KvqAttnArgs {
 // attention (weights false) or its pass over the weights, which follows it
 template <int HD>
 cudaError_t kvq_attn_call(const KvqAttnArgs &a, bool weights, cudaStream_t s);
+// CTAs an SM of the attention kernel
+template <int HD>
+int kvq_attn_ctas(int type, int nq);
+constexpr int kKvqMaxCtas = 2;
+inline int kvq_attn_ctas_per_sm(int hd, int type, int nq) {
+  return hd == 64 ? kvq_attn_ctas<64>(type, nq) : hd == 128 ? kvq_attn_ctas<128>(type, nq) : kvq_attn_ctas<256>(type, nq);
+}
 inline cudaError_t launch_kvq_attn(const KvqAttnArgs &a, int hd, bool weights, cudaStream_t s) {
   return hd == 64 ? kvq_attn_call<64>(a, weights, s) : hd == 128 ? kvq_attn_call<128>(a, weights, s) : kvq_attn_call<256>(a, weights, s);
 }

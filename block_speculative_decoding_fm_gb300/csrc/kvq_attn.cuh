@@ -5,8 +5,8 @@
 //   t_rj = scale log2(e) q_r . k_j  over the rows j that r sees,
 // one pass over the cache with a running reference m and sum.  A unit is a
 // (sequence, KV head, 8 nq query rows); the units lie end to end and every CTA
-// takes an equal share of their stages of 128 rows (64 for head dim 256); where a
-// unit is shared, the CTA that finishes last joins the parts, in their order.
+// takes an equal share of their stages of 128 rows (64 for head dim 256); a second,
+// short launch joins the parts of shared units, in their order.
 //
 // A CTA's warps work in groups of four with a ring of stages of their own (K and V codes and scales in one bulk
 // copy).  A warp forms the scores of a quarter of the stage's keys, S^T = K Q^T, and puts its P into
@@ -35,7 +35,9 @@ constexpr int kWThreads = 128;             // the weights pass
 constexpr int imin(int a, int b) { return a < b ? a : b; }
 constexpr int imax(int a, int b) { return a > b ? a : b; }
 
-// The attention kernel's shape: NG groups of four warps a CTA, one CTA an SM.
+// The attention kernel's shape: CTAs an SM, groups of four warps a CTA, P once or twice.  Two CTAs an SM where two groups
+// each fit them (one's ends of units pass under the other's work), else one CTA with as many groups as fit, four at
+// most; fewer where many query rows want more registers than 128 a thread.
 template <int HD, typename T, int NQ>
 struct Shape : Kind<HD, T, NQ> {
   using K = Kind<HD, T, NQ>;
@@ -44,16 +46,24 @@ struct Shape : Kind<HD, T, NQ> {
   static constexpr int KT = kvq_stage_tiles(HD), SB = KT * kvq_tile_bytes(HD);
   static constexpr int GP = K::G < 4 ? 1 : K::G / 4;      // groups of dims a warp takes
   static constexpr int KP = K::G < 4 ? 4 / K::G : 1;      // ways the keys are split in the second product
-  // P twice over, or the group's outputs when they are joined
-  static constexpr int kP = imax(2 * PT::kBytes, KP * HD * K::RT * 4);
-  static constexpr int kMore = 4 * K::RT * 4 * 2 + K::RT * 4 + 32;      // warps' maxima and sums, references, cursor
-  static constexpr int kRoom = 225 * 1024 - QT::kBytes - 1024;
   static constexpr int NS = HD == 64 ? 3 : 2;
-  static constexpr int kGroup = NS * SB + kP + kMore + 2 * NS * 8;
-  static constexpr int NG = imin(4, kRoom / kGroup);
-  static constexpr int kThreads = 128 * NG;
-  static constexpr int kBytes = NG * kGroup + QT::kBytes;
-  static_assert(NG >= 1, "a group fits an SM");
+  static constexpr int kJoin = HD * K::RT * 4;            // one output, when a CTA's are joined
+  static constexpr int p_bytes(int ng, int db) { return imax((1 + db) * PT::kBytes, ((ng * KP - 1) * kJoin / ng + 127) / 128 * 128); }
+  static constexpr int kMore = 4 * K::RT * 4 * 2 + K::RT * 4 + 32 + 2 * NS * 8;   // maxima, sums, references, cursor, barriers
+  static constexpr int bytes(int ng, int db) { return ng * (NS * SB + p_bytes(ng, db) + kMore) + QT::kBytes; }
+  static constexpr int kRoom1 = 226 * 1024, kRoom2 = 112 * 1024 + 512;
+  static constexpr int kMost = NQ <= 2 ? 4 : HD == 256 && NQ == 4 ? 2 : 3;        // groups an SM, by registers
+  static constexpr bool kTwo = kMost == 4 && bytes(2, 0) <= kRoom2;
+  static constexpr int pick_ng() {
+    if (kTwo) return 2;
+    for (int ng = kMost; ng > 1; --ng)
+      if (bytes(ng, 0) <= kRoom1) return ng;
+    return 1;
+  }
+  static constexpr int MB = kTwo ? 2 : 1, NG = pick_ng();
+  static constexpr int DB = bytes(NG, 1) <= (kTwo ? kRoom2 : kRoom1) ? 1 : 0;
+  static constexpr int kP = p_bytes(NG, DB), kBytes = bytes(NG, DB), kThreads = 128 * NG;
+  static_assert(kBytes <= kRoom1, "a group fits an SM");
 };
 
 template <typename T>
@@ -130,62 +140,17 @@ __device__ __forceinline__ bool issue_stage(const KvqAttnArgs &a, Cursor *cu, in
   return true;
 }
 
-// The parts of a split unit into its output rows, in part order: CTA `first` has the unit's first stages (its
-// second slot), the CTAs after it up to `last` the rest.
-template <int HD, typename T, int RT, int NT>
-__device__ __forceinline__ void join_parts(const KvqAttnArgs &a, const Stretch &x, int first, int last, float undo, float bias,
-                                           float *lse, int tid) {
-  constexpr int NB = 8;    // parts whose loads are in flight together
-  const int R = a.rows[x.i] * a.group;
-  for (int e = tid; e < RT * HD / 4; e += NT) {
-    const int r = e / (HD / 4), d = 4 * (e % (HD / 4)), qr = x.rt * RT + r;
-    if (qr >= R) break;
-    float M = -INFINITY, L = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = first; c <= last; c += NB) {
-      float2 ml[NB];
-      float4 v[NB];
-#pragma unroll
-      for (int k = 0; k < NB; ++k) {
-        const size_t slot = (size_t)min(c + k, last) * 2 + (c + k == first);
-        ml[k] = __ldcg(&a.part_ml[slot * RT + r]);
-        v[k] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + (slot * RT + r) * HD + d));
-      }
-      float m = M;
-#pragma unroll
-      for (int k = 0; k < NB; ++k) m = fmaxf(m, ml[k].x);
-      const float f = M == m ? 1.f : ex2(M - m);
-      M = m;
-      L *= f, acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
-#pragma unroll
-      for (int k = 0; k < NB; ++k) {
-        if (c + k > last) break;
-        const float g = ml[k].x == M ? 1.f : ex2(ml[k].x - M);
-        L = fmaf(g, ml[k].y, L);
-        acc.x = fmaf(g, v[k].x, acc.x);
-        acc.y = fmaf(g, v[k].y, acc.y);
-        acc.z = fmaf(g, v[k].z, acc.z);
-        acc.w = fmaf(g, v[k].w, acc.w);
-      }
-    }
-    const float inv = L == 0.f ? 0.f : undo / L;
-    const int t = qr / a.group;
-    store4(static_cast<T *>(a.out) + (a.row0[x.i] + t) * a.ldo + ((int64_t)x.head * a.group + qr - t * a.group) * HD + d,
-           make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-    if (lse && d == 0) lse[r] = L == 0.f ? INFINITY : M + log2f(L) - bias;
-  }
-}
-
 template <int HD, typename T, int NQ>
-__global__ void __launch_bounds__(Shape<HD, T, NQ>::kThreads, 1) kvq_attend_kernel(const __grid_constant__ KvqAttnArgs a) {
+__global__ void __launch_bounds__(Shape<HD, T, NQ>::kThreads, Shape<HD, T, NQ>::MB)
+    kvq_attend_kernel(const __grid_constant__ KvqAttnArgs a) {
   using Sh = Shape<HD, T, NQ>;
   using QT = typename Sh::QT;
   using PT = typename Sh::PT;
-  constexpr bool QS = Sh::QS, PS = Sh::PS, SV = Sh::SV;
+  constexpr bool QS = Sh::QS, SV = Sh::SV;
+  constexpr int PS = Sh::PS, DB = Sh::DB;
   constexpr int NG = Sh::NG, NS = Sh::NS, SB = Sh::SB, TB = kvq_tile_bytes(HD), RT = Sh::RT, KS = Sh::KS, MT = Sh::MT;
   constexpr int GP = Sh::GP, KP = Sh::KP, NT = Sh::kThreads;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int s_last;
   __shared__ float2 s_row[RT];              // references and sums of the query rows, all groups
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, grp = NG == 1 ? 0 : w >> 2, wq = w & 3;
   const int g8 = lane >> 2, c = lane & 3;
@@ -234,7 +199,7 @@ __global__ void __launch_bounds__(Shape<HD, T, NQ>::kThreads, 1) kvq_attend_kern
     const size_t plane = (size_t)a.seq[x.i] * a.c.n_kv + x.head;
     load_q<HD, QS, NQ, NT>(static_cast<const T *>(a.q) + a.row0[x.i] * a.ldq + (int64_t)x.head * a.group * HD, a.ldq, a.group,
                            rq, R, a.scale_log2, qs, tid);
-    const PRange<PS> range(__ldcg(a.c.vmax + plane));
+    const PRange range(__ldcg(a.c.vmax + plane));
     __syncthreads();
     const int lim_all = a.causal ? len - T_rows + rq / a.group + 1 : len;   // the rows that every query row sees end here
 
@@ -259,7 +224,7 @@ __global__ void __launch_bounds__(Shape<HD, T, NQ>::kThreads, 1) kvq_attend_kern
       if (copies && ok) ok = issue_stage<HD, Sh>(a, cu, w_end, grp, ring, full, empty);
       ok = __all_sync(0xffffffffu, ok && mbar_wait_bounded(full + slot * 8, par, a.c.err));
       const int key0 = tile0 * kKvqTile + strip;
-      uint8_t *pt = ptile + buf * PT::kBytes;
+      const uint32_t pt = smem_u32(ptile) + buf * PT::kBytes;
       float s[MT][NQ][4];
       uint64_t sp[MT][NQ][2];
       strip_scores<HD, QS, NQ, KS>(kcode + slot * SB, kscale + slot * SB, qt, lane, sp);
@@ -311,6 +276,7 @@ __global__ void __launch_bounds__(Shape<HD, T, NQ>::kThreads, 1) kvq_attend_kern
           }
         beat |= x0 * mu.x > m[n][0] + kLazy || x1 * mu.y > m[n][1] + kLazy;
       }
+      if (!DB) named_sync(1 + grp, 128);   // the last stage's P has been used
       put_p<NQ, PS, KS>(pt, strip, lane, p);
       if (bar_any(1 + grp, 128, beat)) {
         // the group's new references, what it holds brought to them, and P again
@@ -380,7 +346,7 @@ __global__ void __launch_bounds__(Shape<HD, T, NQ>::kThreads, 1) kvq_attend_kern
             const uint4 v = lds128(vscale + slot * SB + key / kKvqTile * TB + 4 * u * 128 + key % kKvqTile / 2);
             sc[kb][u][0] = v.x, sc[kb][u][1] = v.y, sc[kb][u][2] = v.z, sc[kb][u][3] = v.w;
           }
-        if (!PS && range.shifted) {
+        if (range.shifted) {
 #pragma unroll
           for (int kb = 0; kb < NB; ++kb)
 #pragma unroll
@@ -403,7 +369,7 @@ __global__ void __launch_bounds__(Shape<HD, T, NQ>::kThreads, 1) kvq_attend_kern
       __syncwarp();
       if (lane == 0) mbar_arrive(empty + slot * 8);
       if (++slot == NS) slot = 0, par ^= 1;
-      buf ^= 1;
+      buf ^= DB;
     }
 
     // the groups' references and the warps' sums, then the outputs
@@ -436,7 +402,7 @@ __global__ void __launch_bounds__(Shape<HD, T, NQ>::kThreads, 1) kvq_attend_kern
     }
     __syncthreads();
     // in the values' own unit and with the rows' common references; every part but the first group's into shared memory
-    float *ob = reinterpret_cast<float *>(ptile) + (size_t)(kp * Sh::G + (GP == 1 ? gw : wq * GP)) * (2 * NQ * 128) + lane * 4;
+    float *ob = reinterpret_cast<float *>(smem + NG * NS * SB) + (size_t)((grp * KP + kp - 1) * Sh::G + (GP == 1 ? gw : wq * GP)) * (2 * NQ * 128) + lane * 4;
 #pragma unroll
     for (int u = 0; u < GP; ++u)
 #pragma unroll
@@ -468,8 +434,8 @@ __global__ void __launch_bounds__(Shape<HD, T, NQ>::kThreads, 1) kvq_attend_kern
         for (int n = 0; n < NQ; ++n) {
 #pragma unroll
           for (int v = 1; v < NG * KP; ++v) {
-            const float *y = reinterpret_cast<const float *>(smem + NG * NS * SB + v / KP * Sh::kP) +
-                             (size_t)((v % KP) * Sh::G + (GP == 1 ? gw : wq * GP)) * (2 * NQ * 128) + lane * 4;
+            const float *y = reinterpret_cast<const float *>(smem + NG * NS * SB) +
+                             (size_t)((v - 1) * Sh::G + (GP == 1 ? gw : wq * GP)) * (2 * NQ * 128) + lane * 4;
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
               const float4 z = *reinterpret_cast<const float4 *>(y + ((u * NQ + n) * 2 + t) * 128);
@@ -498,19 +464,6 @@ __global__ void __launch_bounds__(Shape<HD, T, NQ>::kThreads, 1) kvq_attend_kern
       else if (lse)
         lse[tid] = L == 0.f ? INFINITY : M + log2f(L) - range.bias;
     }
-    if (!whole) {   // the CTA that finishes the last part of a unit joins them all, in their order
-      int32_t *ticket = a.tickets + (size_t)(a.unit0[x.i] + x.rt) * a.c.n_kv + x.head;
-      const int u0 = at - x.s0, first = cta_of(a, u0), last = cta_of(a, u0 + a.stages[x.i] - 1);
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) s_last = atomicAdd(ticket, 1) == last - first;
-      __syncthreads();
-      if (s_last) {
-        __threadfence();
-        if (tid == 0) *ticket = 0;
-        join_parts<HD, T, RT, NT>(a, x, first, last, range.undo, range.bias, lse, tid);
-      }
-    }
     at += x.n;
     if (at < w_end) __syncthreads();   // the next stretch writes the queries, the references and the outputs' place
   }
@@ -518,6 +471,89 @@ __global__ void __launch_bounds__(Shape<HD, T, NQ>::kThreads, 1) kvq_attend_kern
   if (copies)
     for (int k = max(0, cu->issued - NS); k < cu->issued; ++k) mbar_wait_drain(full + k % NS * 8, (k / NS) & 1);
   __syncthreads();
+}
+
+// The parts of the units that several CTAs share into their output rows, in part order.  Where the units are no more
+// than the CTAs, block x takes unit x; else the boundary between CTAs x and x + 1, if it is the first one inside a
+// unit.  The block's four quarters take a quarter of the parts each, their loads in flight together.  Grid (units or
+// boundaries, 64 float4 of a unit's outputs).
+constexpr int kJoinThreads = 256;
+template <int HD, typename T, int NQ>
+__global__ void __launch_bounds__(kJoinThreads) kvq_join_kernel(const __grid_constant__ KvqAttnArgs a) {
+  constexpr int RT = 8 * NQ, NB = 8;
+  __shared__ float4 s_acc[4][64];
+  __shared__ float2 s_ml[4][64];
+  pdl_trigger();
+  const int W = a.st0[a.n], units = a.unit0[a.n] * a.c.n_kv;
+  int at;   // a stage of the unit
+  if (units <= a.ctas) {
+    const int i = find_seq<int32_t>(a.unit0, a.n, (int)blockIdx.x / a.c.n_kv);
+    at = a.st0[i] + ((int)blockIdx.x - a.unit0[i] * a.c.n_kv) * a.stages[i];
+  } else {
+    at = share_begin(a, blockIdx.x + 1);
+  }
+  const Stretch x(a, at, W);
+  const int u0 = at - x.s0, first = cta_of(a, u0), last = cta_of(a, u0 + a.stages[x.i] - 1);
+  pdl_wait();   // every block, so that a later launch that waits for this one waits for what came before too
+  if (first == last || (units > a.ctas && first != (int)blockIdx.x)) return;
+  const int q = threadIdx.x >> 6, e = blockIdx.y * 64 + (threadIdx.x & 63);
+  const int r = e / (HD / 4), d = 4 * (e % (HD / 4)), qr = x.rt * RT + r;
+  const int per = (last - first + 4) / 4, c0 = first + q * per, c1 = min(last, c0 + per - 1);
+  float M = -INFINITY, L = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c = c0; c <= c1; c += NB) {
+    float2 ml[NB];
+    float4 v[NB];
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+      const int p = min(c + k, c1);
+      const size_t slot = (size_t)p * 2 + (p == first);
+      ml[k] = __ldcg(&a.part_ml[slot * RT + r]);
+      v[k] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + (slot * RT + r) * HD + d));
+    }
+    float m = M;
+#pragma unroll
+    for (int k = 0; k < NB; ++k) m = fmaxf(m, ml[k].x);
+    const float f = M == m ? 1.f : ex2(M - m);
+    M = m;
+    L *= f, acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+      if (c + k > c1) break;
+      const float g = ml[k].x == M ? 1.f : ex2(ml[k].x - M);
+      L = fmaf(g, ml[k].y, L);
+      acc.x = fmaf(g, v[k].x, acc.x);
+      acc.y = fmaf(g, v[k].y, acc.y);
+      acc.z = fmaf(g, v[k].z, acc.z);
+      acc.w = fmaf(g, v[k].w, acc.w);
+    }
+  }
+  s_acc[q][threadIdx.x & 63] = acc;
+  s_ml[q][threadIdx.x & 63] = make_float2(M, L);
+  __syncthreads();
+  if (q > 0 || qr >= a.rows[x.i] * a.group) return;
+#pragma unroll
+  for (int k = 1; k < 4; ++k) M = fmaxf(M, s_ml[k][threadIdx.x].x);
+  L = 0.f;
+  acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 ml = s_ml[k][threadIdx.x];
+    const float4 v = s_acc[k][threadIdx.x];
+    const float g = ml.x == M ? 1.f : ex2(ml.x - M);
+    L = fmaf(g, ml.y, L);
+    acc.x = fmaf(g, v.x, acc.x);
+    acc.y = fmaf(g, v.y, acc.y);
+    acc.z = fmaf(g, v.z, acc.z);
+    acc.w = fmaf(g, v.w, acc.w);
+  }
+  const PRange range(__ldcg(a.c.vmax + (size_t)a.seq[x.i] * a.c.n_kv + x.head));
+  const float inv = L == 0.f ? 0.f : range.undo / L;
+  const int t = qr / a.group;
+  store4(static_cast<T *>(a.out) + (a.row0[x.i] + t) * a.ldo + ((int64_t)x.head * a.group + qr - t * a.group) * HD + d,
+         make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+  if (a.lse && d == 0)
+    a.lse[((size_t)(a.unit0[x.i] + x.rt) * a.c.n_kv + x.head) * RT + r] = L == 0.f ? INFINITY : M + log2f(L) - range.bias;
 }
 
 // weights[j] = decay weights[j] + sum_r p_rj / sum_j p_rj: with every row's sum
@@ -627,7 +663,14 @@ cudaError_t attend_t(const KvqAttnArgs &a, cudaStream_t s) {
   static_assert(Sh::kBytes <= 226 * 1024, "shared memory of a CTA");
   cudaError_t e = cudaFuncSetAttribute(kvq_attend_kernel<HD, T, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kBytes);
   if (e != cudaSuccess) return e;
-  return kvq_launch(kvq_attend_kernel<HD, T, NQ>, dim3(a.ctas), dim3(Sh::kThreads), Sh::kBytes, s, a);
+  e = kvq_launch(kvq_attend_kernel<HD, T, NQ>, dim3(a.ctas), dim3(Sh::kThreads), Sh::kBytes, s, a);
+  // nothing to join where every share is a unit
+  bool whole = a.extra == 0;
+  for (int i = 0; i < a.n; ++i) whole = whole && (a.rows[i] == 0 || a.stages[i] == a.share);
+  if (e != cudaSuccess || whole) return e;
+  const int units = a.unit0[a.n] * a.c.n_kv;
+  return kvq_launch(kvq_join_kernel<HD, T, NQ>, dim3(units <= a.ctas ? units : a.ctas - 1, 8 * NQ * HD / 4 / 64),
+                    dim3(kJoinThreads), 0, s, a);
 }
 template <int HD, typename T, int NQ>
 cudaError_t weights_t(const KvqAttnArgs &a, cudaStream_t s) {
@@ -637,6 +680,10 @@ cudaError_t weights_t(const KvqAttnArgs &a, cudaStream_t s) {
   return kvq_launch(kvq_weights_kernel<HD, T, NQ>, dim3(a.wt0[a.n], a.c.n_kv), dim3(kWThreads), smem, s, a);
 }
 
+template <int HD, typename T>
+int ctas_t(int nq) {
+  return nq == 1 ? Shape<HD, T, 1>::MB : nq == 2 ? Shape<HD, T, 2>::MB : nq == 3 ? Shape<HD, T, 3>::MB : Shape<HD, T, 4>::MB;
+}
 template <int HD, typename T>
 cudaError_t call_t(const KvqAttnArgs &a, bool weights, cudaStream_t s) {
   switch (a.nq) {
@@ -656,6 +703,11 @@ cudaError_t kvq_attn_call(const KvqAttnArgs &a, bool weights, cudaStream_t s) {
   if (a.type == KVQ_F16) return call_t<HD, __half>(a, weights, s);
   return call_t<HD, __nv_bfloat16>(a, weights, s);
 }
+template <int HD>
+int kvq_attn_ctas(int type, int nq) {
+  return type == KVQ_F32 ? ctas_t<HD, float>(nq) : type == KVQ_F16 ? ctas_t<HD, __half>(nq) : ctas_t<HD, __nv_bfloat16>(nq);
+}
 template cudaError_t kvq_attn_call<KVQ_HD>(const KvqAttnArgs &, bool, cudaStream_t);
+template int kvq_attn_ctas<KVQ_HD>(int, int);
 
 }  // namespace fm

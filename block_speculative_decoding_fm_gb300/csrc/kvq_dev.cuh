@@ -105,7 +105,9 @@ template <int HD, typename T, int NQ_>
 struct Kind {
   static constexpr int NQ = NQ_, RT = 8 * NQ, G = HD / 32;
   static constexpr bool QS = sizeof(T) == 4;                          // f32 queries: f16 hi + lo
-  static constexpr bool PS = !std::is_same<T, __nv_bfloat16>::value;  // f16 and f32 outputs: P' too
+  // P' = p d in f16: rounded twice (p, then the product), which bf16 outputs do not see; once (f16 outputs, whose own
+  // rounding is as large); or split into hi + lo (f32 outputs)
+  static constexpr int PS = sizeof(T) == 4 ? 2 : std::is_same<T, __half>::value ? 1 : 0;
   static constexpr bool SV = sizeof(T) == 4;                          // f32 outputs: signed V codes (no sums to take off)
   static constexpr int KS = 16 * kvq_stage_tiles(HD), MT = KS / 16;   // a strip, in 16-key products
 };
@@ -276,13 +278,14 @@ __device__ __forceinline__ void strip_scores(uint32_t code, uint32_t scale, uint
   }
 }
 
-// P of a stage of four strips in shared memory, by query row: f16 (a row's keys
-// together, 16 bytes of padding: eight rows' 16-byte pieces in eight bank
-// groups), or f32 where P' = p d is to be split (eight words of padding).
-template <int NQ, bool PS, int KS>
+// P of a stage of four strips in shared memory as f16, by query row: a row's keys
+// together, 16 bytes of padding (eight rows' 16-byte pieces in eight bank groups);
+// PS > 0: then what the rounding left of p, in f16 too.
+template <int NQ, int PS, int KS>
 struct PTile {
-  static constexpr int kRow = PS ? 4 * KS * 4 + 32 : 4 * KS * 2 + 16;
-  static constexpr int kBytes = 8 * NQ * kRow;
+  static constexpr int kRow = 4 * KS * 2 + 16;
+  static constexpr int kLo = 8 * NQ * kRow;
+  static constexpr int kBytes = kLo * (PS ? 2 : 1);
 };
 __device__ __forceinline__ void stsm_x4_trans(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
   asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};\n" ::"r"(addr), "r"(r0), "r"(r1), "r"(r2),
@@ -293,66 +296,65 @@ __device__ __forceinline__ void stsm_x2_trans(uint32_t addr, uint32_t r0, uint32
   asm volatile("stmatrix.sync.aligned.m8n8.x2.trans.shared.b16 [%0], {%1,%2};\n" ::"r"(addr), "r"(r0), "r"(r1) : "memory");
 }
 // this warp's strip (fragments as strip_scores') into columns key0 .. of the tile
-template <int NQ, bool PS, int KS>
-__device__ __forceinline__ void put_p(uint8_t *tile, int key0, int lane, const float (&p)[KS / 16][NQ][4]) {
+template <int NQ, int PS, int KS>
+__device__ __forceinline__ void put_p(uint32_t tile, int key0, int lane, const float (&p)[KS / 16][NQ][4]) {
   using PT = PTile<NQ, PS, KS>;
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
-    if constexpr (PS) {
+    uint32_t r[KS / 8], l[KS / 8];
 #pragma unroll
-      for (int m = 0; m < KS / 16; ++m)
+    for (int m = 0; m < KS / 16; ++m)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          *reinterpret_cast<float *>(tile + (8 * n + 2 * (lane & 3) + (e & 1)) * PT::kRow +
-                                     (key0 + 16 * m + 8 * (e >> 1) + (lane >> 2)) * 4) = p[m][n][e];
-    } else {
-      uint32_t r[KS / 8];
-#pragma unroll
-      for (int m = 0; m < KS / 16; ++m)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
+      for (int e = 0; e < 2; ++e) {
+        if constexpr (PS) {
+          split2_f16(p[m][n][2 * e], p[m][n][2 * e + 1], r[2 * m + e], l[2 * m + e]);
+        } else {
           const __half2 v = __floats2half2_rn(p[m][n][2 * e], p[m][n][2 * e + 1]);
           r[2 * m + e] = *reinterpret_cast<const uint32_t *>(&v);
         }
-      const uint32_t at = smem_u32(tile) + (8 * n + (lane & 7)) * PT::kRow + key0 * 2;
-      if constexpr (KS == 32)
-        stsm_x4_trans(at + (lane >> 3) * 16, r[0], r[1], r[2], r[3]);
-      else
-        stsm_x2_trans(at + ((lane >> 3) & 1) * 16, r[0], r[1]);
+      }
+    const uint32_t at = tile + (8 * n + (lane & 7)) * PT::kRow + key0 * 2 + (KS == 32 ? lane >> 3 : (lane >> 3) & 1) * 16;
+    if constexpr (KS == 32) {
+      stsm_x4_trans(at, r[0], r[1], r[2], r[3]);
+      if constexpr (PS) stsm_x4_trans(at + PT::kLo, l[0], l[1], l[2], l[3]);
+    } else {
+      stsm_x2_trans(at, r[0], r[1]);
+      if constexpr (PS) stsm_x2_trans(at + PT::kLo, l[0], l[1]);
     }
   }
 }
 
 // How P' = p d is brought into f16's range: p carries 2^bias (the sums too, so
 // it leaves with the division), d carries 2^shift.  p <= 2^8 (the reference moves
-// late) and d <= vmax < 2^e, so that P' < 2^15 with bias = 7 - e - shift.  Split P' is
-// formed in f32 and takes the whole factor in p; once-rounded P' has p in f16 as
-// well (bias <= 7), and small scales are raised themselves (exactly: f16 times a power of two).
-template <bool PS>
+// late) and d 2^shift <= vmax 2^shift < 2^e, so bias = 7 - max(e, 0) keeps p and P'
+// below 2^15; shift raises scales below 2^-6 (exactly: f16 times a power of two).
 struct PRange {
   float bias, undo;      // undo: 2^-shift
   __half2 up;            // 2^shift
   bool shifted;
   __device__ __forceinline__ explicit PRange(uint32_t vmax_bits) {
-    const int e = max(-32, static_cast<int>(vmax_bits >> 23) - 126);
-    const int shift = PS || e >= -6 ? 0 : min(-e, 15);
+    const int e = max(-24, static_cast<int>(vmax_bits >> 23) - 126);
+    const int shift = e >= -6 ? 0 : min(-e, 15);
     shifted = shift > 0;
-    bias = static_cast<float>(PS ? 7 - e : 7 - max(e + shift, 0));
+    bias = static_cast<float>(7 - max(e + shift, 0));
     undo = __uint_as_float((uint32_t)(127 - shift) << 23);
     up = __float2half2_rn(__uint_as_float((uint32_t)(127 + shift) << 23));
   }
 };
 
+__device__ __forceinline__ __half2 h2(uint32_t w) { return *reinterpret_cast<const __half2 *>(&w); }
+__device__ __forceinline__ uint32_t u32(__half2 v) { return *reinterpret_cast<const uint32_t *>(&v); }
+
 // O^T += V^T P^T over 32 rows of a tile (code: where the lane fetches their unit of group 0), group g:
 // o[t][n] are the accumulators of dims 32 g + 4 (lane / 4) + t (first pair) and + 2 (second), query
 // rows 8 n + 2 (lane % 4) and + 1, in the code pairs' units (t = 0: 2^-24, t = 1: 2^-20).
 // sc: the V scales of the rows' pairs (kvq_vscale's order).  P' = p d is rounded to
-// f16 once more (PS: split into hi + lo, which keeps ~22 bits).  SV: the codes enter
+// f16 (PS 1: p's rest joins the product before its only rounding; PS 2: hi + lo, ~22 bits).  SV: the codes enter
 // with their 8 taken off; else unsigned, and cor collects the sums of P' (a
 // product with ones; P's fragments of two query octets serve as its first operand,
 // query row lane / 4 and + 8), which the end takes off eight times.
-template <int HD, bool PS, bool SV, int NQ, int KS>
-__device__ __forceinline__ void tile_pv(uint32_t code, int g, const uint32_t (&sc)[4], const uint8_t *pt, int key0, int lane,
+template <int HD, int PS, bool SV, int NQ, int KS>
+__device__ __forceinline__ void tile_pv(uint32_t code, int g, const uint32_t (&sc)[4], uint32_t pt, int key0, int lane,
                                         float (&o)[2][NQ][4], float (&cor)[(NQ + 1) / 2][4]) {
   using PT = PTile<NQ, PS, KS>;
   uint32_t w[4], h[4][4];
@@ -367,19 +369,20 @@ __device__ __forceinline__ void tile_pv(uint32_t code, int g, const uint32_t (&s
   uint32_t b[NQ][4], l[NQ][4];
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
-    if constexpr (PS) {
+    const uint32_t at = pt + (8 * n + (lane & 7)) * PT::kRow + (key0 + (lane >> 3) * 8) * 2;
+    ldsm_x4(at, b[n]);
+    if constexpr (PS) ldsm_x4(at + PT::kLo, l[n]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint2 v = lds64(smem_u32(pt) + (8 * n + (lane >> 2)) * PT::kRow + (key0 + 8 * j + 2 * (lane & 3)) * 4);
-        const float2 d = pair_f32(sc[j]);
-        split2_f16(__uint_as_float(v.x) * d.x, __uint_as_float(v.y) * d.y, b[n][j], l[n][j]);
-      }
-    } else {
-      ldsm_x4(smem_u32(pt) + (8 * n + (lane & 7)) * PT::kRow + (key0 + (lane >> 3) * 8) * 2, b[n]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const __half2 x = __hmul2(*reinterpret_cast<const __half2 *>(&b[n][j]), *reinterpret_cast<const __half2 *>(&sc[j]));
-        b[n][j] = *reinterpret_cast<const uint32_t *>(&x);
+    for (int j = 0; j < 4; ++j) {
+      const __half2 p = h2(b[n][j]), d = h2(sc[j]);
+      if constexpr (PS == 0) {
+        b[n][j] = u32(__hmul2(p, d));
+      } else if constexpr (PS == 1) {
+        b[n][j] = u32(__hfma2(p, d, __hmul2(h2(l[n][j]), d)));
+      } else {   // (the product's rest is exact)
+        const __half2 x = __hmul2(p, d);
+        b[n][j] = u32(x);
+        l[n][j] = u32(__hfma2(h2(l[n][j]), d, __hfma2(p, d, __hneg2(x))));
       }
     }
 #pragma unroll
@@ -387,7 +390,7 @@ __device__ __forceinline__ void tile_pv(uint32_t code, int g, const uint32_t (&s
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         mma_f16(o[t][n], h[2 * st][t], h[2 * st][t + 2], h[2 * st + 1][t], h[2 * st + 1][t + 2], b[n][2 * st], b[n][2 * st + 1]);
-        if constexpr (PS)
+        if constexpr (PS == 2)
           mma_f16(o[t][n], h[2 * st][t], h[2 * st][t + 2], h[2 * st + 1][t], h[2 * st + 1][t + 2], l[n][2 * st], l[n][2 * st + 1]);
       }
     if constexpr (!SV) {
@@ -398,7 +401,7 @@ __device__ __forceinline__ void tile_pv(uint32_t code, int g, const uint32_t (&s
 #pragma unroll
         for (int st = 0; st < 2; ++st) {
           mma_f16(cor[n / 2], b[e][2 * st], two ? b[n][2 * st] : 0u, b[e][2 * st + 1], two ? b[n][2 * st + 1] : 0u, kOnes, kOnes);
-          if constexpr (PS)
+          if constexpr (PS == 2)
             mma_f16(cor[n / 2], l[e][2 * st], two ? l[n][2 * st] : 0u, l[e][2 * st + 1], two ? l[n][2 * st + 1] : 0u, kOnes, kOnes);
         }
       }

@@ -10,12 +10,13 @@ S = sum_j p_j |v_j| and A = scale max_j sum_d |q_d| K_jd, K_jd the largest |k_j|
             in the log2 domain 2^-22 x 1.45 A: delta <= (120 + hd / 32) 2^-24 A in all.  A probability is off by the factor
             e^(+-2 delta) with its sum's
   exp2      2^-22 each, its sum's too
-  P V       P' in f16 once, times the f16 scale rounded again: 2 x 2^-11 relative (bf16 outputs); split into hi + lo: 2^-21;
-            below f16's normal range a P' is off by 2^-25 absolute, times a code of at most 8, over 2^bias and a row sum of at
-            least 1 (the reference is never above the largest score).  Split: bias = 7 - e with vmax in [2^(e-1), 2^e), so 8
-            2^-25 2^(e-7) <= 2^-31 V a key, V = 8 vmax the largest value the rows can hold.  Once rounded: bias = 7 - max(e, 0)
-            with e >= -6 (smaller scales are raised to that), so 8 2^-32 <= 2^-25 V for e < 0 and 2^-31 V above.  (Against V, not
-            S: where every key of weight has a 0 in a dimension, S falls below what the keys without weight round to.)
+  P V       P' = p d (d the f16 scale) as f16.  bf16 outputs: p rounded, then the product, 2 x 2^-11 relative.  f16 outputs: p in two
+            parts (2^-22), one rounding of the product 2^-11, of the second part's 2^-22.  f32 outputs: both parts of the product
+            kept, 2^-21 in all.  Below f16's normal range a P' is off by 2^-25 absolute, times a code of at most 8, over 2^bias and a
+            row sum of at least 1 (the reference is never above the largest score); bias = 7 - max(e, 0) with the largest scale
+            vmax in [2^(e-1), 2^e) and e >= -6 (smaller scales are raised to that), so 8 2^-32 <= 2^-25 V a key for e < 0 and
+            8 2^-25 2^(e-7) <= 2^-31 V above, V = 8 vmax the largest value the rows can hold.  (Against V, not S: where every key
+            of weight has a 0 in a dimension, S falls below what the keys without weight round to.)
   sums      L products and the joins of parts in f32: (L + 64) 2^-24 S at most (a part's rescaling is a product more); f16 and
             bf16 outputs sum whole codes (up to 15 / 8 V a key) and take eight times the sum of P' (V) off at the end:
             (L + 64) 2^-24 x 3 V more
@@ -60,9 +61,9 @@ def check_out(got, want, mass, reach, hd, L, name, vals):
     import torch
     eps = torch.finfo(ttype(name)).eps
     delta = (120 + hd / 32) * 2.0 ** -24 * reach[..., None]
-    pv = 2 * 2.0 ** -11 if name == "bf16" else 2.0 ** -21
+    pv = {"bf16": 2 * 2.0 ** -11, "f16": 2.0 ** -11 + 2.0 ** -21, "f32": 2.0 ** -21}[name]
     big = np.abs(vals).max(initial=0.0)
-    floor = 2.0 ** -25 if name == "bf16" and big < 8.0 else 2.0 ** -31
+    floor = 2.0 ** -25 if big < 8.0 else 2.0 ** -31
     tol = mass * (np.expm1(2 * delta) + 2.0 ** -20 + pv + (L + 64) * 2.0 ** -23) + L * floor * big + eps / 2 * np.abs(want)
     tol += 0.0 if name == "f32" else (L + 64) * 2.0 ** -24 * 3 * big
     tol += 2.0 ** -25 if name == "f16" else 0.0    # f16 outputs below the normal range
