@@ -47,6 +47,14 @@ constexpr int kMaxRows = 1 << 24;
 
 thread_local char g_kvq_error[512] = "";
 
+// (the attention kernels are instantiated in a translation unit a head dim)
+int kvq_attn_ctas_per_sm(int hd, int type, int nq) {
+  return hd == 64 ? kvq_attn_ctas<64>(type, nq) : hd == 128 ? kvq_attn_ctas<128>(type, nq) : kvq_attn_ctas<256>(type, nq);
+}
+cudaError_t launch_kvq_attn(const KvqAttnArgs &a, int hd, bool weights, cudaStream_t s) {
+  return hd == 64 ? kvq_attn_call<64>(a, weights, s) : hd == 128 ? kvq_attn_call<128>(a, weights, s) : kvq_attn_call<256>(a, weights, s);
+}
+
 fm_status kfail(fm_kvq *c, fm_status s, const char *fmt, ...) {
   va_list ap;
   va_start(ap, fmt);

@@ -112,12 +112,6 @@ cudaError_t kvq_attn_call(const KvqAttnArgs &a, bool weights, cudaStream_t s);
 template <int HD>
 int kvq_attn_ctas(int type, int nq);
 constexpr int kKvqMaxCtas = 2;
-inline int kvq_attn_ctas_per_sm(int hd, int type, int nq) {
-  return hd == 64 ? kvq_attn_ctas<64>(type, nq) : hd == 128 ? kvq_attn_ctas<128>(type, nq) : kvq_attn_ctas<256>(type, nq);
-}
-inline cudaError_t launch_kvq_attn(const KvqAttnArgs &a, int hd, bool weights, cudaStream_t s) {
-  return hd == 64 ? kvq_attn_call<64>(a, weights, s) : hd == 128 ? kvq_attn_call<128>(a, weights, s) : kvq_attn_call<256>(a, weights, s);
-}
 constexpr int kKvqWeightTiles = 8;   // tiles a CTA of the weights pass covers
 
 struct KvqEvictArgs {

@@ -54,13 +54,8 @@ struct Shape : Kind<HD, T, NQ> {
   static constexpr int kRoom1 = 226 * 1024, kRoom2 = 112 * 1024 + 512;
   static constexpr int kMost = NQ <= 2 ? 4 : HD == 256 && NQ == 4 ? 2 : 3;        // groups an SM, by registers
   static constexpr bool kTwo = kMost == 4 && bytes(2, 0) <= kRoom2;
-  static constexpr int pick_ng() {
-    if (kTwo) return 2;
-    for (int ng = kMost; ng > 1; --ng)
-      if (bytes(ng, 0) <= kRoom1) return ng;
-    return 1;
-  }
-  static constexpr int MB = kTwo ? 2 : 1, NG = pick_ng();
+  static constexpr int fits(int ng) { return ng == 1 || bytes(ng, 0) <= kRoom1 ? ng : fits(ng - 1); }
+  static constexpr int MB = kTwo ? 2 : 1, NG = kTwo ? 2 : fits(kMost);
   static constexpr int DB = bytes(NG, 1) <= (kTwo ? kRoom2 : kRoom1) ? 1 : 0;
   static constexpr int kP = p_bytes(NG, DB), kBytes = bytes(NG, DB), kThreads = 128 * NG;
   static_assert(kBytes <= kRoom1, "a group fits an SM");
@@ -203,11 +198,11 @@ __global__ void __launch_bounds__(Shape<HD, T, NQ>::kThreads, Shape<HD, T, NQ>::
     __syncthreads();
     const int lim_all = a.causal ? len - T_rows + rq / a.group + 1 : len;   // the rows that every query row sees end here
 
-    float o[GP][2][NQ][4], cor[GP][(NQ + 1) / 2][4], m[NQ][2];
+    float o[GP][2][NQ][4], cor[GP][NQ][4], m[NQ][2];
 #pragma unroll
     for (int u = 0; u < GP; ++u)
 #pragma unroll
-      for (int n = 0; n < (NQ + 1) / 2; ++n) cor[u][n][0] = cor[u][n][1] = cor[u][n][2] = cor[u][n][3] = 0.f;
+      for (int n = 0; n < NQ; ++n) cor[u][n][0] = cor[u][n][1] = cor[u][n][2] = cor[u][n][3] = 0.f;
     uint64_t l[NQ];                          // row sums of this warp's strips
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
@@ -315,7 +310,7 @@ __global__ void __launch_bounds__(Shape<HD, T, NQ>::kThreads, Shape<HD, T, NQ>::
             const float e0 = __shfl_sync(0xffffffffu, f0, (lane & ~3) | (g8 >> 1)), e1 = __shfl_sync(0xffffffffu, f1, (lane & ~3) | (g8 >> 1));
             const float f = g8 & 1 ? e1 : e0;
 #pragma unroll
-            for (int u = 0; u < GP; ++u) cor[u][n / 2][2 * (n & 1)] *= f, cor[u][n / 2][2 * (n & 1) + 1] *= f;
+            for (int u = 0; u < GP; ++u) cor[u][n][0] *= f, cor[u][n][1] *= f, cor[u][n][2] *= f, cor[u][n][3] *= f;
           }
           const float2 mu = *reinterpret_cast<const float2 *>(qs + QT::kMult + (8 * n + 2 * c) * 4);
           const float b0 = range.bias - (n0 == -INFINITY ? 0.f : n0), b1 = range.bias - (n1 == -INFINITY ? 0.f : n1);
@@ -411,8 +406,9 @@ __global__ void __launch_bounds__(Shape<HD, T, NQ>::kThreads, Shape<HD, T, NQ>::
         const float f0 = m[n][0] == M0 ? 1.f : ex2(m[n][0] - M0), f1 = m[n][1] == M1 ? 1.f : ex2(m[n][1] - M1);
         float c0 = 0.f, c1 = 0.f;
         if constexpr (!SV) {
-          c0 = 8.f * __shfl_sync(0xffffffffu, cor[u][n / 2][2 * (n & 1)], 8 * c);
-          c1 = 8.f * __shfl_sync(0xffffffffu, cor[u][n / 2][2 * (n & 1)], 8 * c + 4);
+          const float all = 8.f * (cor[u][n][0] + cor[u][n][2]);   // of query row lane / 4
+          c0 = __shfl_sync(0xffffffffu, all, 8 * c);
+          c1 = __shfl_sync(0xffffffffu, all, 8 * c + 4);
         }
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -473,87 +469,85 @@ __global__ void __launch_bounds__(Shape<HD, T, NQ>::kThreads, Shape<HD, T, NQ>::
   __syncthreads();
 }
 
-// The parts of the units that several CTAs share into their output rows, in part order.  Where the units are no more
-// than the CTAs, block x takes unit x; else the boundary between CTAs x and x + 1, if it is the first one inside a
-// unit.  The block's four quarters take a quarter of the parts each, their loads in flight together.  Grid (units or
-// boundaries, 64 float4 of a unit's outputs).
+// The parts of the units that several CTAs share into their output rows, in part order.  Many: the units are no more
+// than the CTAs, and block x takes unit x; its four quarters take a quarter of the parts each, their loads in flight
+// together (grid y: 64 float4 of a unit's outputs).  Else block x takes the boundary between CTAs x and x + 1, if it is
+// the first one inside a unit: few parts, one after another (grid y: 256 float4).
 constexpr int kJoinThreads = 256;
-template <int HD, typename T, int NQ>
+struct Joined {
+  float M = -INFINITY, L = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  // parts c0 .. c1 of which `first` is in its CTA's second slot; NB parts' loads in flight together
+  template <int NB>
+  __device__ __forceinline__ void add(const KvqAttnArgs &a, int RT, int HD, int r, int d, int c0, int c1, int first) {
+    for (int c = c0; c <= c1; c += NB) {
+      float2 ml[NB];
+      float4 v[NB];
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        const int p = min(c + k, c1);
+        const size_t slot = (size_t)p * 2 + (p == first);
+        ml[k] = __ldcg(&a.part_ml[slot * RT + r]);
+        v[k] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + (slot * RT + r) * HD + d));
+      }
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        if (c + k > c1) break;
+        add_one(ml[k], v[k]);
+      }
+    }
+  }
+  __device__ __forceinline__ void add_one(float2 ml, float4 v) {
+    const float m = fmaxf(M, ml.x), f = M == m ? 1.f : ex2(M - m), g = ml.x == m ? 1.f : ex2(ml.x - m);
+    M = m;
+    L = fmaf(L, f, g * ml.y);
+    acc.x = fmaf(acc.x, f, g * v.x);
+    acc.y = fmaf(acc.y, f, g * v.y);
+    acc.z = fmaf(acc.z, f, g * v.z);
+    acc.w = fmaf(acc.w, f, g * v.w);
+  }
+};
+template <int HD, typename T, int NQ, bool Many>
 __global__ void __launch_bounds__(kJoinThreads) kvq_join_kernel(const __grid_constant__ KvqAttnArgs a) {
-  constexpr int RT = 8 * NQ, NB = 8;
-  __shared__ float4 s_acc[4][64];
-  __shared__ float2 s_ml[4][64];
+  constexpr int RT = 8 * NQ, TX = Many ? 64 : kJoinThreads;
   pdl_trigger();
-  const int W = a.st0[a.n], units = a.unit0[a.n] * a.c.n_kv;
   int at;   // a stage of the unit
-  if (units <= a.ctas) {
+  if (Many) {
     const int i = find_seq<int32_t>(a.unit0, a.n, (int)blockIdx.x / a.c.n_kv);
     at = a.st0[i] + ((int)blockIdx.x - a.unit0[i] * a.c.n_kv) * a.stages[i];
   } else {
     at = share_begin(a, blockIdx.x + 1);
   }
-  const Stretch x(a, at, W);
+  const Stretch x(a, at, a.st0[a.n]);
   const int u0 = at - x.s0, first = cta_of(a, u0), last = cta_of(a, u0 + a.stages[x.i] - 1);
   pdl_wait();   // every block, so that a later launch that waits for this one waits for what came before too
-  if (first == last || (units > a.ctas && first != (int)blockIdx.x)) return;
-  const int q = threadIdx.x >> 6, e = blockIdx.y * 64 + (threadIdx.x & 63);
+  if (first == last || (!Many && first != (int)blockIdx.x)) return;
+  const int q = Many ? threadIdx.x >> 6 : 0, e = blockIdx.y * TX + threadIdx.x % TX;
   const int r = e / (HD / 4), d = 4 * (e % (HD / 4)), qr = x.rt * RT + r;
-  const int per = (last - first + 4) / 4, c0 = first + q * per, c1 = min(last, c0 + per - 1);
-  float M = -INFINITY, L = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int c = c0; c <= c1; c += NB) {
-    float2 ml[NB];
-    float4 v[NB];
+  const bool mine = r < RT && qr < a.rows[x.i] * a.group;
+  Joined j;
+  if (Many) {
+    const int per = (last - first + 4) / 4, c0 = first + q * per;
+    if (mine) j.add<8>(a, RT, HD, r, d, c0, min(last, c0 + per - 1), first);
+    __shared__ float4 s_acc[4][64];
+    __shared__ float2 s_ml[4][64];
+    s_acc[q][threadIdx.x & 63] = j.acc;
+    s_ml[q][threadIdx.x & 63] = make_float2(j.M, j.L);
+    __syncthreads();
+    if (q > 0 || !mine) return;
 #pragma unroll
-    for (int k = 0; k < NB; ++k) {
-      const int p = min(c + k, c1);
-      const size_t slot = (size_t)p * 2 + (p == first);
-      ml[k] = __ldcg(&a.part_ml[slot * RT + r]);
-      v[k] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + (slot * RT + r) * HD + d));
-    }
-    float m = M;
-#pragma unroll
-    for (int k = 0; k < NB; ++k) m = fmaxf(m, ml[k].x);
-    const float f = M == m ? 1.f : ex2(M - m);
-    M = m;
-    L *= f, acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
-#pragma unroll
-    for (int k = 0; k < NB; ++k) {
-      if (c + k > c1) break;
-      const float g = ml[k].x == M ? 1.f : ex2(ml[k].x - M);
-      L = fmaf(g, ml[k].y, L);
-      acc.x = fmaf(g, v[k].x, acc.x);
-      acc.y = fmaf(g, v[k].y, acc.y);
-      acc.z = fmaf(g, v[k].z, acc.z);
-      acc.w = fmaf(g, v[k].w, acc.w);
-    }
-  }
-  s_acc[q][threadIdx.x & 63] = acc;
-  s_ml[q][threadIdx.x & 63] = make_float2(M, L);
-  __syncthreads();
-  if (q > 0 || qr >= a.rows[x.i] * a.group) return;
-#pragma unroll
-  for (int k = 1; k < 4; ++k) M = fmaxf(M, s_ml[k][threadIdx.x].x);
-  L = 0.f;
-  acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float2 ml = s_ml[k][threadIdx.x];
-    const float4 v = s_acc[k][threadIdx.x];
-    const float g = ml.x == M ? 1.f : ex2(ml.x - M);
-    L = fmaf(g, ml.y, L);
-    acc.x = fmaf(g, v.x, acc.x);
-    acc.y = fmaf(g, v.y, acc.y);
-    acc.z = fmaf(g, v.z, acc.z);
-    acc.w = fmaf(g, v.w, acc.w);
+    for (int k = 1; k < 4; ++k) j.add_one(s_ml[k][threadIdx.x], s_acc[k][threadIdx.x]);
+  } else {
+    if (!mine) return;
+    j.add<2>(a, RT, HD, r, d, first, last, first);
   }
   const PRange range(__ldcg(a.c.vmax + (size_t)a.seq[x.i] * a.c.n_kv + x.head));
-  const float inv = L == 0.f ? 0.f : range.undo / L;
+  const float inv = j.L == 0.f ? 0.f : range.undo / j.L;
   const int t = qr / a.group;
   store4(static_cast<T *>(a.out) + (a.row0[x.i] + t) * a.ldo + ((int64_t)x.head * a.group + qr - t * a.group) * HD + d,
-         make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+         make_float4(j.acc.x * inv, j.acc.y * inv, j.acc.z * inv, j.acc.w * inv));
   if (a.lse && d == 0)
-    a.lse[((size_t)(a.unit0[x.i] + x.rt) * a.c.n_kv + x.head) * RT + r] = L == 0.f ? INFINITY : M + log2f(L) - range.bias;
+    a.lse[((size_t)(a.unit0[x.i] + x.rt) * a.c.n_kv + x.head) * RT + r] = j.L == 0.f ? INFINITY : j.M + log2f(j.L) - range.bias;
 }
 
 // weights[j] = decay weights[j] + sum_r p_rj / sum_j p_rj: with every row's sum
@@ -668,8 +662,9 @@ cudaError_t attend_t(const KvqAttnArgs &a, cudaStream_t s) {
   bool whole = a.extra == 0;
   for (int i = 0; i < a.n; ++i) whole = whole && (a.rows[i] == 0 || a.stages[i] == a.share);
   if (e != cudaSuccess || whole) return e;
-  const int units = a.unit0[a.n] * a.c.n_kv;
-  return kvq_launch(kvq_join_kernel<HD, T, NQ>, dim3(units <= a.ctas ? units : a.ctas - 1, 8 * NQ * HD / 4 / 64),
+  const int units = a.unit0[a.n] * a.c.n_kv, items = 8 * NQ * HD / 4;
+  if (units <= a.ctas) return kvq_launch(kvq_join_kernel<HD, T, NQ, true>, dim3(units, items / 64), dim3(kJoinThreads), 0, s, a);
+  return kvq_launch(kvq_join_kernel<HD, T, NQ, false>, dim3(a.ctas - 1, (items + kJoinThreads - 1) / kJoinThreads),
                     dim3(kJoinThreads), 0, s, a);
 }
 template <int HD, typename T, int NQ>

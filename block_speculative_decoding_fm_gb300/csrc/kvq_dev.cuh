@@ -350,12 +350,13 @@ __device__ __forceinline__ uint32_t u32(__half2 v) { return *reinterpret_cast<co
 // rows 8 n + 2 (lane % 4) and + 1, in the code pairs' units (t = 0: 2^-24, t = 1: 2^-20).
 // sc: the V scales of the rows' pairs (kvq_vscale's order).  P' = p d is rounded to
 // f16 (PS 1: p's rest joins the product before its only rounding; PS 2: hi + lo, ~22 bits).  SV: the codes enter
-// with their 8 taken off; else unsigned, and cor collects the sums of P' (a
-// product with ones; P's fragments of two query octets serve as its first operand,
-// query row lane / 4 and + 8), which the end takes off eight times.
+// with their 8 taken off; else unsigned, and cor collects the sums of P', which the
+// end takes off eight times: a product with ones whose first operand is an octet's P'
+// fragments as they are, so that row lane / 4 sums the keys of the first and third
+// eight for query row lane / 4 of the octet, and row lane / 4 + 8 the others.
 template <int HD, int PS, bool SV, int NQ, int KS>
 __device__ __forceinline__ void tile_pv(uint32_t code, int g, const uint32_t (&sc)[4], uint32_t pt, int key0, int lane,
-                                        float (&o)[2][NQ][4], float (&cor)[(NQ + 1) / 2][4]) {
+                                        float (&o)[2][NQ][4], float (&cor)[NQ][4]) {
   using PT = PTile<NQ, PS, KS>;
   uint32_t w[4], h[4][4];
   ldsm_x4_trans(code ^ (g << 4), w[0], w[1], w[2], w[3]);
@@ -394,17 +395,9 @@ __device__ __forceinline__ void tile_pv(uint32_t code, int g, const uint32_t (&s
           mma_f16(o[t][n], h[2 * st][t], h[2 * st][t + 2], h[2 * st + 1][t], h[2 * st + 1][t + 2], l[n][2 * st], l[n][2 * st + 1]);
       }
     if constexpr (!SV) {
-      if ((n & 1) || n + 1 == NQ) {
-        constexpr uint32_t kOnes = 0x3c003c00u;
-        const int e = n & ~1;                // the octet's partner, or nothing
-        const bool two = n & 1;
-#pragma unroll
-        for (int st = 0; st < 2; ++st) {
-          mma_f16(cor[n / 2], b[e][2 * st], two ? b[n][2 * st] : 0u, b[e][2 * st + 1], two ? b[n][2 * st + 1] : 0u, kOnes, kOnes);
-          if constexpr (PS == 2)
-            mma_f16(cor[n / 2], l[e][2 * st], two ? l[n][2 * st] : 0u, l[e][2 * st + 1], two ? l[n][2 * st + 1] : 0u, kOnes, kOnes);
-        }
-      }
+      constexpr uint32_t kOnes = 0x3c003c00u;
+      mma_f16(cor[n], b[n][0], b[n][1], b[n][2], b[n][3], kOnes, kOnes);
+      if constexpr (PS == 2) mma_f16(cor[n], l[n][0], l[n][1], l[n][2], l[n][3], kOnes, kOnes);
     }
   }
 }
