@@ -167,12 +167,28 @@ def _ptr(x) -> Optional[int]:
     return int(x)
 
 
+_raw_stream = None   # torch's current stream as an integer; None: not looked up yet, or no CUDA
+
+
+def _find_raw_stream():
+    """The quickest way this torch has to the current stream's handle (a tenth of a stream object's cost), or None
+    without CUDA."""
+    global _raw_stream
+    import torch
+    if torch.cuda.is_available():
+        get, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+        if get is not None and device is not None:
+            torch.cuda.current_stream()   # (sets CUDA up)
+            _raw_stream = lambda: get(device())
+        else:
+            _raw_stream = lambda: torch.cuda.current_stream().cuda_stream
+    return _raw_stream
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        if torch.cuda.is_available():
-            return torch.cuda.current_stream().cuda_stream
-        return None
+        raw = _raw_stream or _find_raw_stream()
+        return raw() if raw is not None else None
     if hasattr(stream, "cuda_stream"):
         return stream.cuda_stream
     return int(stream)
@@ -516,11 +532,16 @@ def _ints(x, n: int, what: str):
     return (ctypes.c_int32 * n)(*x)
 
 
+_kvq_types = {}   # torch dtype -> FM_DTYPE_*
+
+
 def _kvq_rows(x, rows: int, heads: Optional[int], head_dim: int, what: str):
     """(pointer, dtype, heads, row stride) of a CUDA tensor [>= rows, heads, head_dim] whose rows are whole: the last
     two axes contiguous, any stride between rows."""
-    import torch
-    dtype = {torch.float32: FM_DTYPE_F32, torch.float16: FM_DTYPE_F16, torch.bfloat16: FM_DTYPE_BF16}.get(x.dtype)
+    if not _kvq_types:
+        import torch
+        _kvq_types.update({torch.float32: FM_DTYPE_F32, torch.float16: FM_DTYPE_F16, torch.bfloat16: FM_DTYPE_BF16})
+    dtype = _kvq_types.get(x.dtype)
     if dtype is None or not x.is_cuda:
         raise ValueError(f"{what} must be a float32, float16 or bfloat16 CUDA tensor")
     shape, stride = x.shape, x.stride()
@@ -533,9 +554,9 @@ def _kvq_rows(x, rows: int, heads: Optional[int], head_dim: int, what: str):
 
 def _kvq_weights(x, n: int, heads: int, what: str):
     """(pointer, row stride) of a contiguous CUDA float32 tensor [n, heads, rows], or of None."""
-    import torch
     if x is None:
         return None, 0
+    import torch
     if x.dtype != torch.float32 or not x.is_cuda or x.dim() != 3 or x.shape[0] != n or x.shape[1] != heads or \
             not x.is_contiguous():
         raise ValueError(f"{what} must be a contiguous float32 CUDA tensor [{n}, {heads}, rows]")

@@ -4,10 +4,9 @@
 // below everything), in their order.
 //
 // Two launches:
-//   select   one CTA a plane: the weight of rank keep - recent by radix selection on
-//            the ordered bits (11 + 11 + 10, counts in a shared histogram), then the
-//            rows that stay are listed in their order (block scans, no atomics whose
-//            order could show);
+//   select   one CTA a plane, or a cluster of eight: the weight of rank keep - recent by
+//            radix selection on the ordered bits, eight at a time, then the rows that stay are listed in their order, a run of rows a warp (scans, no
+//            atomics whose order could show);
 //   move     16 bytes of codes and their scale an item.  Into another sequence, CTAs
 //            of 64 rows and a plane each, all over the GPU.  In place, a cluster of eight CTAs a plane
 //            goes through the rows in rounds: a kept row never moves up, so the rows that a round
@@ -24,12 +23,11 @@ namespace cg = cooperative_groups;
 namespace fm {
 namespace {
 
-constexpr int kThreads = 512;    // select
-constexpr int kWarps = kThreads / 32;
-constexpr int kBins = 2048;
-constexpr int kRows = 4;         // consecutive rows a thread looks at
+constexpr int kThreads = 512;    // in place
+constexpr int kSelThreads = 512;
+constexpr int kSelSmem = 256 * 32 * 4;
 constexpr int kMoveThreads = 256;
-constexpr int kCluster = 8;      // in place
+constexpr int kCluster = 8;      // in place; select, where planes are few
 constexpr int kItems = 4;        // 16-byte units a thread moves a round
 
 // weights as unsigned integers of the same order; -0 counts as 0, NaN as less than everything
@@ -38,8 +36,9 @@ __device__ __forceinline__ uint32_t ordered(float w) {
   return w != w ? 0u : (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
 
-// exclusive sum over the select block's threads of v, and the total; red holds kWarps words
-__device__ __forceinline__ int block_scan(int v, int *red, int &total) {
+// exclusive sum over the block's NT threads of v; red holds NT / 32 words
+template <int NT>
+__device__ __forceinline__ int block_scan(int v, int *red) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   int x = v;
 #pragma unroll
@@ -50,22 +49,27 @@ __device__ __forceinline__ int block_scan(int v, int *red, int &total) {
   __syncthreads();   // the last call's words have been read
   if (lane == 31) red[w] = x;
   __syncthreads();
-  int base = 0, all = 0;
+  int base = 0;
 #pragma unroll
-  for (int j = 0; j < kWarps; ++j) {
-    base += j < w ? red[j] : 0;
-    all += red[j];
-  }
-  total = all;
+  for (int j = 0; j < NT / 32; ++j) base += j < w ? red[j] : 0;
   return base + x - v;
 }
 
-__global__ void __launch_bounds__(kThreads) kvq_select_kernel(const __grid_constant__ KvqEvictArgs a) {
-  __shared__ int hist[kBins];
-  __shared__ int red[kWarps + 1];
+// A plane's rows over CS CTAs (a cluster of eight where planes are few), an equal run of rows each.  Histograms of 8-bit digits
+// are kept a copy a lane, in the lane's own bank: the weights of a plane crowd into few bins, and the same
+// address from many lanes is what shared-memory atomics are slow at (75 us for four planes of 65535 rows).
+template <int CS>
+__global__ void __launch_bounds__(kSelThreads) kvq_select_kernel(const __grid_constant__ KvqEvictArgs a) {
+  constexpr int NT = kSelThreads, NWarp = NT / 32;
+  extern __shared__ int hist[];            // [256][32]
+  __shared__ int bins[256];
+  __shared__ int red[NWarp];
   __shared__ int s_found[2];
-  const int pl = blockIdx.x, i = pl / a.c.n_kv, head = pl - i * a.c.n_kv;
-  const int tid = threadIdx.x, len = a.len[i];
+  __shared__ int2 s_cnt[NWarp];
+  __shared__ int2 s_all;
+  cg::cluster_group cl = cg::this_cluster();
+  const int rank = CS == 1 ? 0 : blockIdx.x % CS, pl = blockIdx.x / CS, i = pl / a.c.n_kv, head = pl - i * a.c.n_kv;
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, len = a.len[i];
   const float *ws = a.c.weights + ((size_t)a.src[i] * a.c.n_kv + head) * a.c.rows_pad;
   int32_t *list = a.list + (size_t)pl * a.c.rows_pad;
   int32_t *kept = a.kept ? a.kept + ((size_t)(a.call0 + i) * a.c.n_kv + head) * a.keep : nullptr;
@@ -75,82 +79,122 @@ __global__ void __launch_bounds__(kThreads) kvq_select_kernel(const __grid_const
     list[pos] = row;
     if (kept) kept[pos] = row;
   };
+  auto sync = [&]() {
+    if (CS > 1)
+      cl.sync();
+    else
+      __syncthreads();
+  };
   if (len <= a.keep) {
-    for (int r = tid; r < len; r += kThreads) put(r, r);
+    for (int r = rank * NT + tid; r < len; r += CS * NT) put(r, r);
     return;
   }
   const int nc = len - a.recent, m = a.keep - a.recent;   // m of the first nc rows stay
-  for (int r = tid; r < a.recent; r += kThreads) put(m + r, nc + r);
+  for (int r = rank * NT + tid; r < a.recent; r += CS * NT) put(m + r, nc + r);
   if (m == 0) return;
-  // four rows' keys; rows from nc on rank below everything and are never looked for
-  auto keys = [&](int r, uint32_t (&k)[kRows]) {
-    const float4 w = *reinterpret_cast<const float4 *>(ws + r);   // (a plane's rows are padded to 64)
-    k[0] = ordered(w.x), k[1] = ordered(w.y), k[2] = ordered(w.z), k[3] = ordered(w.w);
+  // a warp's run of rows; four rows' keys (a plane's rows are padded to 64)
+  const int per = (nc + CS * NWarp * 128 - 1) / (CS * NWarp * 128) * 128;
+  const int r_beg = (rank * NWarp + w) * per, r_end = min(nc, r_beg + per);
+  auto keys = [&](int r, uint32_t (&k)[4]) {
+    const float4 v = *reinterpret_cast<const float4 *>(ws + r);
+    k[0] = ordered(v.x), k[1] = ordered(v.y), k[2] = ordered(v.z), k[3] = ordered(v.w);
   };
   uint32_t prefix = 0;   // the selected weight's leading bits
   int want = m;          // its rank among the rows that share them
 #pragma unroll 1
-  for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-    for (int x = tid; x < kBins; x += kThreads) hist[x] = 0;
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    for (int x = tid; x < 256 * 32 / 4; x += NT) reinterpret_cast<int4 *>(hist)[x] = make_int4(0, 0, 0, 0);
     __syncthreads();
-#pragma unroll 2
-    for (int r = kRows * tid; r < nc; r += kRows * kThreads) {
-      uint32_t k[kRows];
+#pragma unroll 4
+    for (int r = r_beg + 4 * lane; r < r_end; r += 128) {
+      uint32_t k[4];
       keys(r, k);
 #pragma unroll
-      for (int q = 0; q < kRows; ++q)
-        if (r + q < nc && (pass == 0 || (k[q] >> (shift + bits)) == prefix)) atomicAdd(&hist[(k[q] >> shift) & ((1u << bits) - 1)], 1);
+      for (int q = 0; q < 4; ++q)
+        if (r + q < r_end && (shift == 24 || (k[q] >> (shift + 8)) == prefix)) atomicAdd(&hist[((k[q] >> shift) & 255) * 32 + lane], 1);
     }
     __syncthreads();
-    // bins from the top: thread t has bins kBins - 1 - 4 t .. - 3
-    int cnt[4], sum = 0;
+    for (int b = w; b < 256; b += NWarp) {
+      const int n = __reduce_add_sync(0xffffffffu, hist[b * 32 + lane]);
+      if (lane == 0) bins[b] = n;
+    }
+    sync();
+    // bins from the top: thread t has bin 255 - t, of all CTAs
+    int n = 0;
+    if (tid < 256) {
+      if (CS > 1) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) sum += cnt[q] = hist[kBins - 1 - 4 * tid - q];
-    int total;
-    int before = block_scan(sum, red, total);
-    if (before < want && before + sum >= want) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if (before < want && before + cnt[q] >= want) {
-          s_found[0] = kBins - 1 - 4 * tid - q;
-          s_found[1] = want - before;
-          break;
-        }
-        before += cnt[q];
+        for (int c = 0; c < CS; ++c) n += *cl.map_shared_rank(&bins[255 - tid], c);
+      } else {
+        n = bins[255 - tid];
       }
     }
-    __syncthreads();
-    prefix = (prefix << bits) | (uint32_t)s_found[0];
+    const int before = block_scan<NT>(n, red);
+    if (before < want && before + n >= want) s_found[0] = 255 - tid, s_found[1] = want - before;
+    sync();   // (the counts have been read)
+    prefix = (prefix << 8) | (uint32_t)s_found[0];
     want = s_found[1];
   }
-  // rows above the selected weight stay, and the first `want` that equal it
+  // Rows above the selected weight stay, and the first `want` that equal it: a warp counts both kinds in its run,
+  // and with the counts before it writes its own, in order.
+  int2 cnt = make_int2(0, 0);   // above, equal
+#pragma unroll 4
+  for (int r = r_beg + 4 * lane; r < r_end; r += 128) {
+    uint32_t k[4];
+    keys(r, k);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (r + q < r_end) cnt.x += k[q] > prefix, cnt.y += k[q] == prefix;
+  }
+  cnt.x = __reduce_add_sync(0xffffffffu, cnt.x);
+  cnt.y = __reduce_add_sync(0xffffffffu, cnt.y);
+  if (lane == 0) s_cnt[w] = cnt;
+  __syncthreads();
   int pos = 0, eq = 0;
-  for (int r0 = 0; r0 < nc; r0 += kRows * kThreads) {
-    const int r = r0 + kRows * tid;
-    uint32_t k[kRows] = {};
-    if (r < nc) keys(r, k);
+  if (CS > 1) {
+    if (tid == 0) {
+      int2 t = make_int2(0, 0);
+      for (int v = 0; v < NWarp; ++v) t.x += s_cnt[v].x, t.y += s_cnt[v].y;
+      s_all = t;
+    }
+    cl.sync();
+    for (int c = 0; c < rank; ++c) {
+      const int2 t = *cl.map_shared_rank(&s_all, c);
+      pos += t.x, eq += t.y;
+    }
+  }
+  for (int v = 0; v < w; ++v) pos += s_cnt[v].x, eq += s_cnt[v].y;
+  pos += min(eq, want);
+#pragma unroll 2
+  for (int r0 = r_beg; r0 < r_end; r0 += 128) {
+    const int r = r0 + 4 * lane;
+    uint32_t k[4] = {};
+    if (r < r_end) keys(r, k);
     int ne = 0, ng = 0;
 #pragma unroll
-    for (int q = 0; q < kRows; ++q) {
-      ne += r + q < nc && k[q] == prefix;
-      ng += r + q < nc && k[q] > prefix;
-    }
-    // both counts in one scan (each at most 2048 a round)
-    int both;
-    const int before = block_scan(ne << 16 | ng, red, both);
-    int er = eq + (before >> 16);                                           // equal rows before this thread's
-    int at = pos + (before & 0xffff) + min(er, want) - min(eq, want);       // kept rows before them
+    for (int q = 0; q < 4; ++q) ne += r + q < r_end && k[q] == prefix, ng += r + q < r_end && k[q] > prefix;
+    // both counts in one scan (at most 128 each)
+    const int both = ne << 16 | ng;
+    int x = both;
 #pragma unroll
-    for (int q = 0; q < kRows; ++q) {
-      if (r + q >= nc) break;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    const int all = __shfl_sync(0xffffffffu, x, 31), before = x - both;
+    int er = eq + (before >> 16);                                       // equal rows before this thread's
+    int at = pos + (before & 0xffff) + min(er, want) - min(eq, want);   // kept rows before them
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (r + q >= r_end) break;
       const bool same = k[q] == prefix;
       if (k[q] > prefix || (same && er < want)) put(at++, r + q);
       er += same;
     }
-    pos += (both & 0xffff) + min(eq + (both >> 16), want) - min(eq, want);
-    eq += both >> 16;
+    pos += (all & 0xffff) + min(eq + (all >> 16), want) - min(eq, want);
+    eq += all >> 16;
   }
+  if (CS > 1) cl.sync();   // no CTA leaves while another may read its shared memory
 }
 
 // Rows [r0, r0 + RB) of the list, loaded; then stored.
@@ -240,7 +284,25 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
 template <int HD>
 cudaError_t evict_hd(const KvqEvictArgs &a, cudaStream_t s) {
   const int planes = a.n * a.c.n_kv;
-  cudaError_t e = kvq_launch(kvq_select_kernel, dim3(planes), dim3(kThreads), 0, s, a);
+  cudaError_t e;
+  if (planes * kCluster <= 320) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(planes * kCluster);
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.dynamicSmemBytes = kSelSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = kCluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, kvq_select_kernel<kCluster>, a);
+  } else {
+    e = kvq_launch(kvq_select_kernel<1>, dim3(planes), dim3(kSelThreads), kSelSmem, s, a);
+  }
   int most = 0;   // rows that go to another sequence
   bool same = false;
   for (int i = 0; i < a.n; ++i) {

@@ -15,11 +15,14 @@
 // corrected against the borders d (c +- 1/2), exact in f32 (an 11-bit d times a 5-bit odd number).
 //
 // Bound by memory: a row of n values is read once (2 n or 4 n bytes) and
-// written as 0.5625 n bytes.  Four lanes share a group, eight consecutive values each
-// (one or two 16-byte loads; the lane's eight codes are one 32-bit word of the
-// group's 16-byte unit), and a thread has all its rows' loads in flight.
+// written as 0.5625 n bytes.  Two lanes share a group, 16 consecutive values each
+// (32-byte loads; the lane's codes are half of the group's 16-byte unit), and a
+// thread has all its rows' loads in flight.  (Eight values a lane: the scale's and the
+// extremes' instructions weigh twice as much, 100 us for 32768 rows of 2 x 16 heads x 128 f16.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "dev_common.cuh"
 #include "kvq.h"
@@ -32,22 +35,67 @@ constexpr int kThreads = 256;
 __device__ __forceinline__ float2 floats(__half2 v) { return __half22float2(v); }
 __device__ __forceinline__ float2 floats(__nv_bfloat162 v) { return __bfloat1622float2(v); }
 
-// largest and smallest of eight 16-bit values, two at a time, and a sum that is 0 unless a value is not finite
-template <typename P>
-__device__ __forceinline__ void extremes_16(const uint4 &a, float &hi, float &lo, float &odd) {
-  const P *v = reinterpret_cast<const P *>(&a);
-  P h = v[0], l = v[0], zero = __hsub2(v[0], v[0]);   // (x - x: 0, or NaN where x is not finite)
-#pragma unroll
-  for (int i = 1; i < 4; ++i) {
-    h = __hmax2(h, v[i]);
-    l = __hmin2(l, v[i]);
-    zero = __hadd2(zero, __hsub2(v[i], v[i]));
-  }
-  const float2 hf = floats(h), lf = floats(l), zf = floats(zero);
-  hi = fmaxf(hf.x, hf.y);
-  lo = fminf(lf.x, lf.y);
-  odd = zf.x + zf.y;
+__device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either is
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(y) : "f"(a), "f"(b));
+  return y;
 }
+
+// 32 bytes at a time
+__device__ __forceinline__ void ldg32(const void *p, uint32_t (&w)[8]) {
+  asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p));
+}
+
+// Sixteen consecutive values of a row.
+template <typename T>
+struct Sixteen {
+  static constexpr int W = sizeof(T) * 4;   // 32-bit words
+  uint32_t w[W];
+  __device__ __forceinline__ void load(const T *p, bool whole) {   // whole: p is on a 32-byte boundary
+#pragma unroll
+    for (int i = 0; i < W; i += 8) {
+      if (whole) {
+        uint32_t v[8];
+        ldg32(reinterpret_cast<const uint32_t *>(p) + i, v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) w[i + k] = v[k];
+      } else {
+        const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p) + i / 4), v = __ldg(reinterpret_cast<const uint4 *>(p) + i / 4 + 1);
+        w[i] = u.x, w[i + 1] = u.y, w[i + 2] = u.z, w[i + 3] = u.w;
+        w[i + 4] = v.x, w[i + 5] = v.y, w[i + 6] = v.z, w[i + 7] = v.w;
+      }
+    }
+  }
+  __device__ __forceinline__ float get(int e) const {
+    if constexpr (sizeof(T) == 4) {
+      return __uint_as_float(w[e]);
+    } else if constexpr (std::is_same<T, __half>::value) {
+      const float2 f = floats(*reinterpret_cast<const __half2 *>(&w[e / 2]));
+      return e & 1 ? f.y : f.x;
+    } else {
+      return __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+    }
+  }
+  // the largest value and the largest negated one; NaN where a value is
+  __device__ __forceinline__ void extremes(float &hi, float &nlo) const {
+    if constexpr (sizeof(T) == 4) {
+      hi = get(0), nlo = -get(0);
+#pragma unroll
+      for (int e = 1; e < 16; ++e) hi = max_nan(hi, get(e)), nlo = max_nan(nlo, -get(e));
+    } else {
+      using P = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+      const P *v = reinterpret_cast<const P *>(w);
+      P h = v[0], l = v[0];
+#pragma unroll
+      for (int i = 1; i < 8; ++i) h = __hmax2_nan(h, v[i]), l = __hmin2_nan(l, v[i]);
+      const float2 hf = floats(h), lf = floats(l);
+      hi = max_nan(hf.x, hf.y);
+      nlo = max_nan(-lf.x, -lf.y);
+    }
+  }
+};
 
 template <typename T>
 struct Eight;
@@ -60,15 +108,6 @@ struct Eight<float> {
   }
   __device__ __forceinline__ void get(float (&x)[8]) const {
     x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-  }
-  // largest and smallest value, and a sum that is 0 unless a value is not finite
-  __device__ __forceinline__ void extremes(float &hi, float &lo, float &odd) const {
-    float x[8];
-    get(x);
-    hi = lo = x[0];
-    odd = 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) hi = fmaxf(hi, x[e]), lo = fminf(lo, x[e]), odd = fmaf(x[e], 0.f, odd);
   }
   static __device__ __forceinline__ void store(float *p, const float (&x)[8]) {
     reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
@@ -87,7 +126,6 @@ struct Eight<__half> {
       x[2 * i] = f.x, x[2 * i + 1] = f.y;
     }
   }
-  __device__ __forceinline__ void extremes(float &hi, float &lo, float &odd) const { extremes_16<__half2>(a, hi, lo, odd); }
   static __device__ __forceinline__ void store(__half *p, const float (&x)[8]) {
     uint32_t w[4];
 #pragma unroll
@@ -109,7 +147,6 @@ struct Eight<__nv_bfloat16> {
       x[2 * i] = __uint_as_float(w << 16), x[2 * i + 1] = __uint_as_float(w & 0xffff0000u);
     }
   }
-  __device__ __forceinline__ void extremes(float &hi, float &lo, float &odd) const { extremes_16<__nv_bfloat162>(a, hi, lo, odd); }
   static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&x)[8]) {
     uint32_t w[4];
 #pragma unroll
@@ -140,22 +177,23 @@ __device__ __forceinline__ float rcp(float x) {
   return y;
 }
 
-// the codes of eight values of a group with scale d, packed: any values, any scale
-__device__ __forceinline__ uint32_t codes_any(const float (&v)[8], float d) {
+// the codes of a lane's values of a group with scale d, packed: any values, any scale
+template <typename T>
+__device__ __noinline__ uint2 codes_any(Sixteen<T> v, float d) {
   const float inv = d == 0.f ? 0.f : 1.f / d, ad = fabsf(d);
-  uint32_t w = 0;
-#pragma unroll 1
-  for (int e = 0; e < 8; ++e) {
-    const float x = v[e] == v[e] ? v[e] : 0.f;
+  uint32_t w[2] = {0, 0};
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const float f = v.get(e), x = f == f ? f : 0.f;
     float c = rintf(fminf(fmaxf(x * inv, -9.f), 9.f));
     // the borders of code c, in the units of |d|
     const float xs = d < 0.f ? -x : x, up = ad * (c + 0.5f), dn = ad * (c - 0.5f);
     const bool odd = (static_cast<int>(c) & 1) != 0;
     if (xs > up || (xs == up && odd)) c += 1.f;
     else if (xs < dn || (xs == dn && odd)) c -= 1.f;
-    w |= (uint32_t)(d == 0.f ? 8 : min(15, max(0, static_cast<int>(c) + 8))) << (4 * e);
+    w[e >> 3] |= (uint32_t)(d == 0.f ? 8 : min(15, max(0, static_cast<int>(c) + 8))) << (4 * (e & 7));
   }
-  return w;
+  return make_uint2(w[0], w[1]);
 }
 
 // the low bytes of four words, in order
@@ -163,19 +201,19 @@ __device__ __forceinline__ uint32_t low_bytes(const uint32_t (&t)[4]) {
   return __byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410);
 }
 
-// the same for finite values and 0 or 2^-14 <= |d| < 65504
+// the same for finite values and 0 or 2^-14 <= |d| < 65504 (eight values from e0 on)
 template <typename T>
-__device__ __forceinline__ uint32_t codes_fast(const float (&x)[8], float d) {
-  const float inv = d == 0.f ? 0.f : rcp(d);
+__device__ __forceinline__ uint32_t codes_fast(const Sixteen<T> &v, int e0, float d, float inv) {
   uint32_t even[4], odd[4];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
+    const float x = v.get(e0 + e);
     float t;
     if constexpr (sizeof(T) == 2) {
-      t = fminf(fmaf(x[e], inv, 776.f), 783.f) + 12582912.f;
+      t = fminf(fmaf(x, inv, 776.f), 783.f) + 12582912.f;
     } else {
       constexpr float kMagic = 12582912.f;
-      const float c = fmaf(x[e], inv, kMagic) - kMagic, rem = fmaf(-c, d, x[e]);
+      const float c = fmaf(x, inv, kMagic) - kMagic, rem = fmaf(-c, d, x);
       const float half = d == 0.f ? INFINITY : 0.5f * fabsf(d);
       const bool off = fabsf(rem) > half || (fabsf(rem) == half && (__float_as_uint(c + kMagic) & 1u));
       const float step = off ? copysignf(1.f, rem) * copysignf(1.f, d) : 0.f;
@@ -186,10 +224,10 @@ __device__ __forceinline__ uint32_t codes_fast(const float (&x)[8], float d) {
   return low_bytes(even) | low_bytes(odd) << 4;
 }
 
-// Grid (touched tile, KV head, K or V); thread = (row, eight values).
+// Grid (touched tile, KV head, K or V); thread = (row, 16 values).
 template <int HD, typename T>
 __global__ void __launch_bounds__(kThreads) kvq_append_kernel(const __grid_constant__ KvqRowsArgs a) {
-  constexpr int O = HD / 8;                     // eights a row
+  constexpr int O = HD / 16;                    // lanes a row
   constexpr int RP = kThreads / O;              // rows a pass of the block
   constexpr int NP = kKvqTile / RP;
   __shared__ float red[kThreads / 32];
@@ -199,45 +237,52 @@ __global__ void __launch_bounds__(kThreads) kvq_append_kernel(const __grid_const
   const int tile = at / kKvqTile + (blockIdx.x - a.tile0[i]);
   const int head = blockIdx.y;
   const bool isv = blockIdx.z != 0;
-  const int o = threadIdx.x % O, r0 = threadIdx.x / O;
+  const int o = threadIdx.x % O, r0 = threadIdx.x / O, g = o >> 1;
   const size_t plane = (size_t)a.seq[i] * a.c.n_kv + head;
   uint8_t *half_tile = a.c.planes + plane * a.c.plane_bytes + (size_t)tile * kvq_tile_bytes(HD) + (isv ? kvq_k_bytes(HD) : 0);
-  const T *src = static_cast<const T *>(isv ? a.v : a.k) + head * HD + o * 8;
+  const int first = tile * kKvqTile + r0 - at;   // this thread's first row of the sequence's input
+  const T *src = static_cast<const T *>(isv ? a.v : a.k) + (a.row0[i] + first) * a.ld + head * HD + o * 16;
+  const bool whole = ((reinterpret_cast<uintptr_t>(isv ? a.v : a.k) | (uintptr_t)(a.ld * sizeof(T))) & 31) == 0;
   pdl_wait();
-  Eight<T> in[NP];
+  Sixteen<T> in[NP];
 #pragma unroll
-  for (int p = 0; p < NP; ++p) {
-    const int r = tile * kKvqTile + p * RP + r0 - at;   // row of this sequence's input
-    if (r >= 0 && r < rows) in[p].load(src + (a.row0[i] + r) * a.ld);
-  }
+  for (int p = 0; p < NP; ++p)
+    if (first + p * RP >= 0 && first + p * RP < rows) in[p].load(src + (int64_t)p * RP * a.ld, whole);
   float dmax = 0.f;
 #pragma unroll
   for (int p = 0; p < NP; ++p) {
-    const int tr = p * RP + r0, r = tile * kKvqTile + tr - at;
-    const bool ok = r >= 0 && r < rows;
-    float x[8], hi = 0.f, lo = 0.f, odd = 0.f;
-    if (ok) in[p].extremes(hi, lo, odd);
-#pragma unroll
-    for (int s = 1; s < 4; s <<= 1) {
-      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, s));
-      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, s));
+    const int tr = p * RP + r0;
+    const bool ok = first + p * RP >= 0 && first + p * RP < rows;
+    float hi = 0.f, nlo = 0.f;
+    if (ok) in[p].extremes(hi, nlo);
+    hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, 1));
+    nlo = max_nan(nlo, __shfl_xor_sync(0xffffffffu, nlo, 1));
+    const bool nan = !(hi == hi);
+    if (__any_sync(0xffffffffu, nan)) {   // (rare) NaN counts for nothing
+      float h = 0.f, l = 0.f;
+      if (ok && nan) {
+        h = l = -INFINITY;
+        for (int e = 0; e < 16; ++e) h = fmaxf(h, in[p].get(e)), l = fmaxf(l, -in[p].get(e));
+      }
+      h = fmaxf(h, __shfl_xor_sync(0xffffffffu, h, 1));
+      l = fmaxf(l, __shfl_xor_sync(0xffffffffu, l, 1));
+      if (nan) hi = h > -INFINITY ? h : 0.f, nlo = h > -INFINITY ? l : 0.f;
     }
-    // (a lane whose values are all NaN has NaN here: it counts for nothing, and all of them for 0)
-    const float m = hi > -lo ? hi : lo == lo ? lo : 0.f;
+    const float m = hi > nlo ? hi : -nlo;
     const __half dh = __float2half_rn(fminf(fmaxf(m * -0.125f, -65504.f), 65504.f));
     const float d = __half2float(dh), ad = fabsf(d);
-    if (ok) in[p].get(x);
-    uint32_t w = 0;
-    if (odd == 0.f && (ad >= 6.103515625e-05f || ad == 0.f) && ad < 65504.f) {
-      if (ok) w = codes_fast<T>(x, d);
-    } else if (ok) {
-      w = codes_any(x, d);
-    }
     if (!ok) continue;
-    *reinterpret_cast<uint32_t *>(half_tile + kvq_unit(tr, o >> 2, HD) + (o & 3) * 4) = w;
-    if ((o & 3) == 0) *reinterpret_cast<__half *>(half_tile + kvq_scale(tr, o >> 2, HD, isv)) = dh;
+    uint2 w;
+    if (!nan && (ad >= 6.103515625e-05f || ad == 0.f) && ad < 65504.f) {
+      const float inv = d == 0.f ? 0.f : rcp(d);
+      w = make_uint2(codes_fast(in[p], 0, d, inv), codes_fast(in[p], 8, d, inv));
+    } else {
+      w = codes_any(in[p], d);
+    }
+    *reinterpret_cast<uint2 *>(half_tile + kvq_unit(tr, g, HD) + (o & 1) * 8) = w;
+    if ((o & 1) == 0) *reinterpret_cast<__half *>(half_tile + kvq_scale(tr, g, HD, isv)) = dh;
     if (!isv && o == 0) a.c.weights[plane * a.c.rows_pad + tile * kKvqTile + tr] = 0.f;
-    dmax = fmaxf(dmax, fabsf(d));
+    dmax = fmaxf(dmax, ad);
   }
   if (isv) {   // the plane's largest |V scale| (an upper bound that only grows: the order of the CTAs is no matter)
     dmax = warp_max(dmax);

@@ -488,17 +488,26 @@ fm_status fm_kvq_attend(fm_kvq *c, int32_t layer, int32_t n_seqs, const int32_t 
       a.stages[j] = stages;
       a.st0[j] = (int32_t)work;
       a.unit0[j] = un;
-      a.wt0[j] = wt;
       row0 += n;
       units += (int64_t)rts * nkv;
       work += more;
       un += rts;
-      if (rts > 0) wt += (t1 + kKvqWeightTiles - 1) / kKvqWeightTiles;
+      if (rts > 0) wt += t1;
       ++a.n;
     }
     a.st0[a.n] = (int32_t)work;
     a.unit0[a.n] = un;
-    a.wt0[a.n] = wt;
+    // the weights pass: tiles a CTA so that the CTAs are whole rounds of what the SMs hold (about five each)
+    if (keep_w && wt > 0) {
+      const int64_t room = 5ll * c->n_sm, tiles = (int64_t)wt * nkv, rounds = (tiles + room * kKvqWeightTiles - 1) / (room * kKvqWeightTiles);
+      a.wtiles = (int32_t)((tiles + room * rounds - 1) / (room * rounds));
+      wt = 0;
+      for (int j = 0; j < a.n; ++j) {
+        a.wt0[j] = wt;
+        if (a.rows[j] > 0) wt += ((a.len[j] + kKvqTile - 1) / kKvqTile + a.wtiles - 1) / a.wtiles;
+      }
+      a.wt0[a.n] = wt;
+    }
     // as many CTAs as the SMs hold, each with the same number of stages, whatever unit they belong to
     const int64_t most_ctas = (int64_t)c->n_sm * kvq_attn_ctas_per_sm(hd, type, nq);
     a.ctas = (int32_t)(work < most_ctas ? work : most_ctas);

@@ -93,6 +93,7 @@ struct KvqAttnArgs {
   float *part_o;          // [2 ctas][8 nq][hd] unnormalised partial outputs
   float2 *part_ml;        // [2 ctas][8 nq] (reference, row sum)
   float *lse;             // [units][8 nq] log2 of the row sums, for the weights; or null
+  int32_t wtiles;         // weights: tiles a CTA
   float decay;            // weights: w = decay w + this call's
   float *w_out;           // [call sequences][n_kv][ldw] or null
   int64_t ldw;
@@ -112,7 +113,7 @@ cudaError_t kvq_attn_call(const KvqAttnArgs &a, bool weights, cudaStream_t s);
 template <int HD>
 int kvq_attn_ctas(int type, int nq);
 constexpr int kKvqMaxCtas = 2;
-constexpr int kKvqWeightTiles = 8;   // tiles a CTA of the weights pass covers
+constexpr int kKvqWeightTiles = 8;   // tiles a CTA of the weights pass covers at most
 
 struct KvqEvictArgs {
   KvqCache c;

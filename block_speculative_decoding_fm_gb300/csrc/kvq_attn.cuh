@@ -20,6 +20,7 @@
 // memory as f16, which a tcgen05 operand would need (64 KB written and read again per 128 rows of
 // head dim 128: 1024 cycles of shared memory against the 784 cycles in which an SM's share of HBM
 // delivers their 18 KB).
+#include <atomic>
 #include <type_traits>
 
 #include "kvq_dev.cuh"
@@ -561,44 +562,61 @@ __global__ void __launch_bounds__(kWThreads) kvq_weights_kernel(const __grid_con
   using QT = QTile<HD, QS, NQ>;
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t *qs = smem + kKvqWeightTiles * KB;
-  const uint32_t bars = smem_u32(qs + QT::kBytes);
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g8 = lane >> 2, c = lane & 3;
   const int i = find_seq<int32_t>(a.wt0, a.n, blockIdx.x), head = blockIdx.y;
   const int len = a.len[i], T_rows = a.rows[i], R = T_rows * a.group, rts = (R + RT - 1) / RT;
-  const int t0 = (blockIdx.x - a.wt0[i]) * kKvqWeightTiles;
-  const int nt = min(kKvqWeightTiles, (len + kKvqTile - 1) / kKvqTile - t0);
+  const int t0 = (blockIdx.x - a.wt0[i]) * a.wtiles;
+  const int nt = min(a.wtiles, (len + kKvqTile - 1) / kKvqTile - t0);
   const size_t plane = (size_t)a.seq[i] * a.c.n_kv + head;
   pdl_trigger();
-  if (tid == 0) {
-    for (int t = 0; t < nt; ++t) mbar_init(bars + t * 8, 1);
-    mbar_fence_init();
-  }
-  __syncthreads();
   pdl_wait();
-  if (tid == 0)
-    for (int t = 0; t < nt; ++t) {
-      mbar_expect_tx(bars + t * 8, KB);
-      bulk_g2s(smem_u32(smem + t * KB), a.c.planes + plane * a.c.plane_bytes + (size_t)(t0 + t) * kvq_tile_bytes(HD), KB,
-               bars + t * 8);
-    }
+  // (16-byte copies: a bulk copy a tile's K half, 4.6 KB for head dim 128, takes an SM's copy engine longer than its bytes)
+  const uint8_t *src = a.c.planes + plane * a.c.plane_bytes + (size_t)t0 * kvq_tile_bytes(HD);
+#pragma unroll
+  for (int k = 0; k < NW; ++k) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (2 * k + h < nt)
+        for (int e = tid; e < KB / 16; e += kWThreads)
+          cp_async16(smem_u32(smem) + (2 * k + h) * KB + e * 16, src + (size_t)(2 * k + h) * kvq_tile_bytes(HD) + e * 16, 16);
+    cp_async_commit();
+  }
   const LaneAt<HD, KS> la((w & 1) * 32, lane);
   float acc[NW][4];
 #pragma unroll
   for (int k = 0; k < NW; ++k) acc[k][0] = acc[k][1] = acc[k][2] = acc[k][3] = 0.f;
-  bool ok = true;
   for (int rt = 0; rt < rts; ++rt) {
     if (rt) __syncthreads();
+    const float *lse = a.lse + ((size_t)(a.unit0[i] + rt) * a.c.n_kv + head) * RT;
+    float ls[NQ][2];
+#pragma unroll
+    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = 8 * n + 2 * c + h;
+        ls[n][h] = rt * RT + r < R ? __ldcg(lse + r) : INFINITY;
+      }
     load_q<HD, QS, NQ, kWThreads>(static_cast<const T *>(a.q) + a.row0[i] * a.ldq + (int64_t)head * a.group * HD, a.ldq,
                                   a.group, rt * RT, R, a.scale_log2, qs, tid);
     __syncthreads();
-    const float *lse = a.lse + ((size_t)(a.unit0[i] + rt) * a.c.n_kv + head) * RT;
     const int lim_all = a.causal ? len - T_rows + rt * RT / a.group + 1 : len;
+    float mu[NQ][2];
+#pragma unroll
+    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) mu[n][h] = *reinterpret_cast<const float *>(qs + QT::kMult + (8 * n + 2 * c + h) * 4);
 #pragma unroll 1
     for (int k = 0; k < NW; ++k) {
       const int t = 2 * k + (w >> 1), key0 = (t0 + t) * kKvqTile + (w & 1) * 32;
+      if (2 * k >= nt) break;
+      if (rt == 0) {   // everyone's copies of these two tiles
+        if (k == 0) cp_async_wait<NW - 1>();
+        else if (k == 1) cp_async_wait<NW - 2>();
+        else if (k == 2) cp_async_wait<NW - 3>();
+        else cp_async_wait<0>();
+        __syncthreads();
+      }
       if (t >= nt || key0 >= len || key0 + 32 <= a.first) continue;
-      if (rt == 0) ok = __all_sync(0xffffffffu, ok && mbar_wait_bounded(bars + t * 8, 0, a.c.err));
-      if (!ok) continue;
       uint64_t sp[2][NQ][2];
       strip_scores<HD, QS, NQ, KS>(smem_u32(smem + t * KB) + la.code, smem_u32(smem + t * KB) + la.scale, smem_u32(qs), lane, sp);
       const bool whole = key0 >= a.first && key0 + 32 <= lim_all;
@@ -607,17 +625,16 @@ __global__ void __launch_bounds__(kWThreads) kvq_weights_kernel(const __grid_con
       for (int n = 0; n < NQ; ++n)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int r = 8 * n + 2 * c + h, row = rt * RT + r;
-          const float ls = row < R ? __ldcg(lse + r) : INFINITY, mu = *reinterpret_cast<const float *>(qs + QT::kMult + r * 4);
+          const int row = rt * RT + 8 * n + 2 * c + h;
           const int lim = a.causal ? len - T_rows + row / a.group + 1 : len;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             float s[2];
             unpack2(sp[j >> 1][n][j & 1], s[0], s[1]);
-            float p = ex2(fmaf(s[h], mu, -ls));
+            float p = ex2(fmaf(s[h], mu[n][h], -ls[n][h]));
             const int key = key0 + 8 * j + g8;
             if (!whole && (key < a.first || key >= lim)) p = 0.f;
-            sum[j] += ls == INFINITY ? 0.f : p;   // a row without keys, or past the last, has no weight to give
+            sum[j] += ls[n][h] == INFINITY ? 0.f : p;   // a row without keys, or past the last, has no weight to give
           }
         }
 #pragma unroll
@@ -638,24 +655,34 @@ __global__ void __launch_bounds__(kWThreads) kvq_weights_kernel(const __grid_con
       if (c == j) v = y;
     }
     const int key = key0 + 8 * c + g8;
-    if (key < len && ok) {
+    if (key < len) {
       float *p = a.c.weights + plane * a.c.rows_pad + key;
       if (a.decay != 0.f) v = fmaf(a.decay, *p, v);
       *p = v;
       if (a.w_out) a.w_out[((size_t)(a.call0 + i) * a.c.n_kv + head) * a.ldw + key] = v;
     }
   }
-  // (a strip that no query row sees was not waited for: nothing is left in flight when the CTA ends)
-  if (tid == 0)
-    for (int t = 0; t < nt; ++t) mbar_wait_drain(bars + t * 8, 0);
-  __syncthreads();
+}
+
+// lets a kernel have its dynamic shared memory, once a device (done: a bit a device)
+template <typename K>
+cudaError_t allow_smem(K kern, int bytes, std::atomic<uint64_t> &done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 template <int HD, typename T, int NQ>
 cudaError_t attend_t(const KvqAttnArgs &a, cudaStream_t s) {
   using Sh = Shape<HD, T, NQ>;
   static_assert(Sh::kBytes <= 226 * 1024, "shared memory of a CTA");
-  cudaError_t e = cudaFuncSetAttribute(kvq_attend_kernel<HD, T, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kBytes);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(kvq_attend_kernel<HD, T, NQ>, Sh::kBytes, done);
   if (e != cudaSuccess) return e;
   e = kvq_launch(kvq_attend_kernel<HD, T, NQ>, dim3(a.ctas), dim3(Sh::kThreads), Sh::kBytes, s, a);
   // nothing to join where every share is a unit
@@ -669,8 +696,10 @@ cudaError_t attend_t(const KvqAttnArgs &a, cudaStream_t s) {
 }
 template <int HD, typename T, int NQ>
 cudaError_t weights_t(const KvqAttnArgs &a, cudaStream_t s) {
-  constexpr int smem = kKvqWeightTiles * kvq_k_bytes(HD) + QTile<HD, sizeof(T) == 4, NQ>::kBytes + kKvqWeightTiles * 8;
-  cudaError_t e = cudaFuncSetAttribute(kvq_weights_kernel<HD, T, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  constexpr int smem = kKvqWeightTiles * kvq_k_bytes(HD) + QTile<HD, sizeof(T) == 4, NQ>::kBytes;
+  static_assert(kKvqWeightTiles == 8, "the waits count four pairs of tiles");
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(kvq_weights_kernel<HD, T, NQ>, smem, done);
   if (e != cudaSuccess) return e;
   return kvq_launch(kvq_weights_kernel<HD, T, NQ>, dim3(a.wt0[a.n], a.c.n_kv), dim3(kWThreads), smem, s, a);
 }

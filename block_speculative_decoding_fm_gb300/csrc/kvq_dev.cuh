@@ -148,52 +148,63 @@ __device__ __forceinline__ void load_q(const T *q, int64_t ldq, int group, int r
                                        int tid) {
   using QT = QTile<HD, QS, NQ>;
   constexpr int O = HD / 8;
+  // (the loads of two rounds in flight together)
+  constexpr int kItems = 8 * NQ * O, IP = (kItems + NT - 1) / NT, IB = IP < 2 ? 1 : 2;
 #pragma unroll 1
-  for (int it = tid; it < 8 * NQ * O; it += NT) {
-    const int r = it / O, o = it % O;
-    const int row = r0 + r;
-    float x[8];
-    if (row < R) {
-      const int t = row / group;
-      load8(q + (int64_t)t * ldq + (row - t * group) * HD + o * 8, x);
-    } else {
+  for (int i0 = 0; i0 < IP; i0 += IB) {
+    float xs[IB][8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = 0.f;
-    }
-    float am = 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) am = fmaxf(am, fabsf(x[e]));
-#pragma unroll
-    for (int s = 1; s < O; s <<= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, s));
-    // am in [2^ex, 2^(ex + 1)); the factor 2^(7 - ex), its exponent kept in f32's normal range
-    const int ex = am > 0.f && am < INFINITY ? min(96, max(-119, static_cast<int>(__float_as_uint(am) >> 23) - 127)) : 7;
-    const float up = copysignf(__uint_as_float((uint32_t)(127 + 7 - ex) << 23), scale_log2);
-    if (o == 0)   // (2^20: the products' unit; never 0: a masked score is -inf times it)
-      reinterpret_cast<float *>(tile + QT::kMult)[r] =
-          fmaxf(fabsf(scale_log2) * __uint_as_float((uint32_t)(127 + ex - 7 + 20) << 23), 1e-37f);
-    const int g = o >> 2, at = ((g * NQ + (r >> 3)) * 32 + (r & 7) * 4 + (o & 3)) * 16;
-    float sum = 0.f;
-    uint32_t hi[4], lo[4];
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      const float f = p & 1 ? up : 16.f * up;
-      if constexpr (QS) {
-        split2_f16(x[p] * f, x[p + 4] * f, hi[p], lo[p]);
+    for (int b = 0; b < IB; ++b) {
+      const int it = (i0 + b) * NT + tid, row = r0 + it / O;
+      if (it < kItems && row < R) {
+        const int t = row / group;
+        load8(q + (int64_t)t * ldq + (row - t * group) * HD + it % O * 8, xs[b]);
       } else {
-        const __half2 v = __floats2half2_rn(x[p] * f, x[p + 4] * f);
-        hi[p] = *reinterpret_cast<const uint32_t *>(&v);
-        lo[p] = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) xs[b][e] = 0.f;
       }
-      const float2 h = pair_f32(hi[p]), l = pair_f32(lo[p]);
-      sum += (h.x + h.y + (l.x + l.y)) * (p & 1 ? 1.f : 0.0625f);
     }
-    *reinterpret_cast<uint4 *>(tile + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    if constexpr (QS) *reinterpret_cast<uint4 *>(tile + QT::kLo + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-    if ((o & 3) == 0) {
-      float *off = reinterpret_cast<float *>(tile + QT::kOff) + (g * NQ * 4 + (r >> 1)) * 4 + (r & 1);
-      off[0] = off[2] = -8.f * kUnitHi * sum;
+#pragma unroll
+    for (int b = 0; b < IB; ++b) {
+      const int it = (i0 + b) * NT + tid;
+      if (it >= kItems) break;   // (whole warps)
+      const int r = it / O, o = it % O;
+      float(&x)[8] = xs[b];
+      float am = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) am = fmaxf(am, fabsf(x[e]));
+#pragma unroll
+      for (int s = 1; s < O; s <<= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, s));
+      // am in [2^ex, 2^(ex + 1)); the factor 2^(7 - ex), its exponent kept in f32's normal range
+      const int ex = am > 0.f && am < INFINITY ? min(96, max(-119, static_cast<int>(__float_as_uint(am) >> 23) - 127)) : 7;
+      const float up = copysignf(__uint_as_float((uint32_t)(127 + 7 - ex) << 23), scale_log2);
+      if (o == 0)   // (2^20: the products' unit; never 0: a masked score is -inf times it)
+        reinterpret_cast<float *>(tile + QT::kMult)[r] =
+            fmaxf(fabsf(scale_log2) * __uint_as_float((uint32_t)(127 + ex - 7 + 20) << 23), 1e-37f);
+      const int g = o >> 2, at = ((g * NQ + (r >> 3)) * 32 + (r & 7) * 4 + (o & 3)) * 16;
+      float sum = 0.f;
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const float f = p & 1 ? up : 16.f * up;
+        if constexpr (QS) {
+          split2_f16(x[p] * f, x[p + 4] * f, hi[p], lo[p]);
+        } else {
+          const __half2 v = __floats2half2_rn(x[p] * f, x[p + 4] * f);
+          hi[p] = *reinterpret_cast<const uint32_t *>(&v);
+          lo[p] = 0;
+        }
+        const float2 h = pair_f32(hi[p]), l = pair_f32(lo[p]);
+        sum += (h.x + h.y + (l.x + l.y)) * (p & 1 ? 1.f : 0.0625f);
+      }
+      *reinterpret_cast<uint4 *>(tile + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      if constexpr (QS) *reinterpret_cast<uint4 *>(tile + QT::kLo + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      if ((o & 3) == 0) {
+        float *off = reinterpret_cast<float *>(tile + QT::kOff) + (g * NQ * 4 + (r >> 1)) * 4 + (r & 1);
+        off[0] = off[2] = -8.f * kUnitHi * sum;
+      }
     }
   }
 }
