@@ -24,8 +24,7 @@ namespace fm {
 namespace {
 
 constexpr int kThreads = 512;    // in place
-constexpr int kSelThreads = 512;
-constexpr int kSelSmem = 256 * 32 * 4;
+constexpr int kCopies = 8;
 constexpr int kMoveThreads = 256;
 constexpr int kCluster = 8;      // in place; select, where planes are few
 constexpr int kItems = 4;        // 16-byte units a thread moves a round
@@ -56,12 +55,13 @@ __device__ __forceinline__ int block_scan(int v, int *red) {
 }
 
 // A plane's rows over CS CTAs (a cluster of eight where planes are few), an equal run of rows each.  Histograms of 8-bit digits
-// are kept a copy a lane, in the lane's own bank: the weights of a plane crowd into few bins, and the same
-// address from many lanes is what shared-memory atomics are slow at (75 us for four planes of 65535 rows).
+// are kept in eight copies, a lane's by its number: the weights of a plane crowd into few bins, and the same
+// address from many lanes is what shared-memory atomics are slow at (one copy of 2048 bins in one CTA: 75 us
+// for four planes of 65535 rows).
 template <int CS>
-__global__ void __launch_bounds__(kSelThreads) kvq_select_kernel(const __grid_constant__ KvqEvictArgs a) {
-  constexpr int NT = kSelThreads, NWarp = NT / 32;
-  extern __shared__ int hist[];            // [256][32]
+__global__ void __launch_bounds__(CS == 1 ? 256 : 512, CS == 1 ? 6 : 3) kvq_select_kernel(const __grid_constant__ KvqEvictArgs a) {
+  constexpr int NT = CS == 1 ? 256 : 512, NWarp = NT / 32;
+  __shared__ int hist[kCopies][256];
   __shared__ int bins[256];
   __shared__ int red[NWarp];
   __shared__ int s_found[2];
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kSelThreads) kvq_select_kernel(const __grid_co
   int want = m;          // its rank among the rows that share them
 #pragma unroll 1
   for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int x = tid; x < 256 * 32 / 4; x += NT) reinterpret_cast<int4 *>(hist)[x] = make_int4(0, 0, 0, 0);
+    for (int x = tid; x < 256 * kCopies / 4; x += NT) reinterpret_cast<int4 *>(hist)[x] = make_int4(0, 0, 0, 0);
     __syncthreads();
 #pragma unroll 4
     for (int r = r_beg + 4 * lane; r < r_end; r += 128) {
@@ -111,12 +111,14 @@ __global__ void __launch_bounds__(kSelThreads) kvq_select_kernel(const __grid_co
       keys(r, k);
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        if (r + q < r_end && (shift == 24 || (k[q] >> (shift + 8)) == prefix)) atomicAdd(&hist[((k[q] >> shift) & 255) * 32 + lane], 1);
+        if (r + q < r_end && (shift == 24 || (k[q] >> (shift + 8)) == prefix)) atomicAdd(&hist[lane % kCopies][(k[q] >> shift) & 255], 1);
     }
     __syncthreads();
-    for (int b = w; b < 256; b += NWarp) {
-      const int n = __reduce_add_sync(0xffffffffu, hist[b * 32 + lane]);
-      if (lane == 0) bins[b] = n;
+    if (tid < 256) {
+      int n = 0;
+#pragma unroll
+      for (int c = 0; c < kCopies; ++c) n += hist[c][tid];
+      bins[tid] = n;
     }
     sync();
     // bins from the top: thread t has bin 255 - t, of all CTAs
@@ -288,8 +290,7 @@ cudaError_t evict_hd(const KvqEvictArgs &a, cudaStream_t s) {
   if (planes * kCluster <= 320) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(planes * kCluster);
-    cfg.blockDim = dim3(kSelThreads);
-    cfg.dynamicSmemBytes = kSelSmem;
+    cfg.blockDim = dim3(512);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -301,7 +302,7 @@ cudaError_t evict_hd(const KvqEvictArgs &a, cudaStream_t s) {
     cfg.numAttrs = 2;
     e = cudaLaunchKernelEx(&cfg, kvq_select_kernel<kCluster>, a);
   } else {
-    e = kvq_launch(kvq_select_kernel<1>, dim3(planes), dim3(kSelThreads), kSelSmem, s, a);
+    e = kvq_launch(kvq_select_kernel<1>, dim3(planes), dim3(256), 0, s, a);
   }
   int most = 0;   // rows that go to another sequence
   bool same = false;

@@ -497,10 +497,11 @@ fm_status fm_kvq_attend(fm_kvq *c, int32_t layer, int32_t n_seqs, const int32_t 
     }
     a.st0[a.n] = (int32_t)work;
     a.unit0[a.n] = un;
-    // the weights pass: tiles a CTA so that the CTAs are whole rounds of what the SMs hold (about five each)
+    // the weights pass: tiles a CTA so that the CTAs are whole rounds of what the SMs hold (about four each)
     if (keep_w && wt > 0) {
-      const int64_t room = 5ll * c->n_sm, tiles = (int64_t)wt * nkv, rounds = (tiles + room * kKvqWeightTiles - 1) / (room * kKvqWeightTiles);
-      a.wtiles = (int32_t)((tiles + room * rounds - 1) / (room * rounds));
+      const int64_t room = 4ll * c->n_sm, tiles = (int64_t)wt * nkv, rounds = (tiles + room * kKvqWeightTiles - 1) / (room * kKvqWeightTiles);
+      const int64_t even = (tiles + room * rounds - 1) / (room * rounds);
+      a.wtiles = (int32_t)(even < 2 ? even : (even + 1) / 2 * 2);   // (whole pairs)
       wt = 0;
       for (int j = 0; j < a.n; ++j) {
         a.wt0[j] = wt;

@@ -113,7 +113,7 @@ cudaError_t kvq_attn_call(const KvqAttnArgs &a, bool weights, cudaStream_t s);
 template <int HD>
 int kvq_attn_ctas(int type, int nq);
 constexpr int kKvqMaxCtas = 2;
-constexpr int kKvqWeightTiles = 8;   // tiles a CTA of the weights pass covers at most
+constexpr int kKvqWeightTiles = 16;   // tiles a CTA of the weights pass covers at most
 
 struct KvqEvictArgs {
   KvqCache c;

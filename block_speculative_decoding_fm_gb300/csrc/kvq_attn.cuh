@@ -31,7 +31,7 @@ namespace {
 using namespace kvq;
 
 constexpr float kLazy = 8.f;               // log2 of the growth a reference tolerates
-constexpr int kWThreads = 128;             // the weights pass
+constexpr int kWThreads = 128, kWSlots = 4;   // the weights pass: pairs of tiles in shared memory
 
 constexpr int imin(int a, int b) { return a < b ? a : b; }
 constexpr int imax(int a, int b) { return a > b ? a : b; }
@@ -554,39 +554,40 @@ __global__ void __launch_bounds__(kJoinThreads) kvq_join_kernel(const __grid_con
 // weights[j] = decay weights[j] + sum_r p_rj / sum_j p_rj: with every row's sum
 // known, K alone is read again (from L2 where it still is there) and the scores
 // formed a second time, which needs no store of rows x keys.  One CTA owns a
-// run of 8 tiles, so nothing is added atomically.  Grid (sequence x run, KV head).
+// run of tiles, so nothing is added atomically.  Grid (sequence x run, KV head).
 template <int HD, typename T, int NQ>
 __global__ void __launch_bounds__(kWThreads) kvq_weights_kernel(const __grid_constant__ KvqAttnArgs a) {
   constexpr bool QS = sizeof(T) == 4;
-  constexpr int KB = kvq_k_bytes(HD), NW = kKvqWeightTiles / 2, RT = 8 * NQ, KS = 32;
+  constexpr int KB = kvq_k_bytes(HD), RT = 8 * NQ, KS = 32;
   using QT = QTile<HD, QS, NQ>;
   extern __shared__ __align__(128) uint8_t smem[];
-  uint8_t *qs = smem + kKvqWeightTiles * KB;
+  uint8_t *qs = smem + kWSlots * 2 * KB;
+  // a row's sum so far (a warp's own rows: lane 4 g + j has key 8 j + g of its strip of a pair of tiles)
+  float *acc = reinterpret_cast<float *>(qs + QT::kBytes);
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g8 = lane >> 2, c = lane & 3;
   const int i = find_seq<int32_t>(a.wt0, a.n, blockIdx.x), head = blockIdx.y;
   const int len = a.len[i], T_rows = a.rows[i], R = T_rows * a.group, rts = (R + RT - 1) / RT;
   const int t0 = (blockIdx.x - a.wt0[i]) * a.wtiles;
-  const int nt = min(a.wtiles, (len + kKvqTile - 1) / kKvqTile - t0);
+  const int nt = min(a.wtiles, (len + kKvqTile - 1) / kKvqTile - t0), np = (nt + 1) / 2;
   const size_t plane = (size_t)a.seq[i] * a.c.n_kv + head;
   pdl_trigger();
   pdl_wait();
-  // (16-byte copies: a bulk copy a tile's K half, 4.6 KB for head dim 128, takes an SM's copy engine longer than its bytes)
   const uint8_t *src = a.c.planes + plane * a.c.plane_bytes + (size_t)t0 * kvq_tile_bytes(HD);
+  auto fetch = [&](int p) {   // the K halves of pair p
+    if (p < np)
 #pragma unroll
-  for (int k = 0; k < NW; ++k) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      if (2 * k + h < nt)
-        for (int e = tid; e < KB / 16; e += kWThreads)
-          cp_async16(smem_u32(smem) + (2 * k + h) * KB + e * 16, src + (size_t)(2 * k + h) * kvq_tile_bytes(HD) + e * 16, 16);
+      for (int h = 0; h < 2; ++h)
+        if (2 * p + h < nt)
+          for (int e = tid; e < KB / 16; e += kWThreads)
+            cp_async16(smem_u32(smem) + (p % kWSlots * 2 + h) * KB + e * 16, src + (size_t)(2 * p + h) * kvq_tile_bytes(HD) + e * 16, 16);
     cp_async_commit();
-  }
+  };
   const LaneAt<HD, KS> la((w & 1) * 32, lane);
-  float acc[NW][4];
-#pragma unroll
-  for (int k = 0; k < NW; ++k) acc[k][0] = acc[k][1] = acc[k][2] = acc[k][3] = 0.f;
+  for (int p = 0; p < np; ++p) acc[p * kWThreads + tid] = 0.f;
   for (int rt = 0; rt < rts; ++rt) {
     if (rt) __syncthreads();
+#pragma unroll
+    for (int p = 0; p < kWSlots - 1; ++p) fetch(p);
     const float *lse = a.lse + ((size_t)(a.unit0[i] + rt) * a.c.n_kv + head) * RT;
     float ls[NQ][2];
 #pragma unroll
@@ -606,57 +607,55 @@ __global__ void __launch_bounds__(kWThreads) kvq_weights_kernel(const __grid_con
 #pragma unroll
       for (int h = 0; h < 2; ++h) mu[n][h] = *reinterpret_cast<const float *>(qs + QT::kMult + (8 * n + 2 * c + h) * 4);
 #pragma unroll 1
-    for (int k = 0; k < NW; ++k) {
+    for (int k = 0; k < np; ++k) {
+      cp_async_wait<kWSlots - 2>();
+      __syncthreads();   // everyone's copies of this pair; everyone is done with the pair before it, whose place is next
+      fetch(k + kWSlots - 1);
       const int t = 2 * k + (w >> 1), key0 = (t0 + t) * kKvqTile + (w & 1) * 32;
-      if (2 * k >= nt) break;
-      if (rt == 0) {   // everyone's copies of these two tiles
-        if (k == 0) cp_async_wait<NW - 1>();
-        else if (k == 1) cp_async_wait<NW - 2>();
-        else if (k == 2) cp_async_wait<NW - 3>();
-        else cp_async_wait<0>();
-        __syncthreads();
-      }
       if (t >= nt || key0 >= len || key0 + 32 <= a.first) continue;
+      const uint32_t kb = smem_u32(smem) + (k % kWSlots * 2 + (w >> 1)) * KB;
       uint64_t sp[2][NQ][2];
-      strip_scores<HD, QS, NQ, KS>(smem_u32(smem + t * KB) + la.code, smem_u32(smem + t * KB) + la.scale, smem_u32(qs), lane, sp);
-      const bool whole = key0 >= a.first && key0 + 32 <= lim_all;
+      strip_scores<HD, QS, NQ, KS>(kb + la.code, kb + la.scale, smem_u32(qs), lane, sp);
       float sum[4] = {0.f, 0.f, 0.f, 0.f};     // keys 8 j + lane / 4
+      if (key0 >= a.first && key0 + 32 <= lim_all) {
 #pragma unroll
-      for (int n = 0; n < NQ; ++n)
+        for (int n = 0; n < NQ; ++n)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int row = rt * RT + 8 * n + 2 * c + h;
-          const int lim = a.causal ? len - T_rows + row / a.group + 1 : len;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float s[2];
-            unpack2(sp[j >> 1][n][j & 1], s[0], s[1]);
-            float p = ex2(fmaf(s[h], mu[n][h], -ls[n][h]));
-            const int key = key0 + 8 * j + g8;
-            if (!whole && (key < a.first || key >= lim)) p = 0.f;
-            sum[j] += ls[n][h] == INFINITY ? 0.f : p;   // a row without keys, or past the last, has no weight to give
+          for (int j = 0; j < 4; ++j) {   // (a row without keys, or past the last: the log of its sum is inf, p 0)
+            float s0, s1;
+            unpack2(sp[j >> 1][n][j & 1], s0, s1);
+            sum[j] += ex2(fmaf(s0, mu[n][0], -ls[n][0])) + ex2(fmaf(s1, mu[n][1], -ls[n][1]));
           }
-        }
+      } else {
 #pragma unroll
-      for (int kk = 0; kk < NW; ++kk)
-        if (kk == k) acc[kk][0] += sum[0], acc[kk][1] += sum[1], acc[kk][2] += sum[2], acc[kk][3] += sum[3];
+        for (int n = 0; n < NQ; ++n)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int row = rt * RT + 8 * n + 2 * c + h, lim = a.causal ? len - T_rows + row / a.group + 1 : len;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              float s[2];
+              unpack2(sp[j >> 1][n][j & 1], s[0], s[1]);
+              const int key = key0 + 8 * j + g8;
+              if (key >= a.first && key < lim) sum[j] += ex2(fmaf(s[h], mu[n][h], -ls[n][h]));
+            }
+          }
+      }
+      float v = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float y = sum[j];
+        y += __shfl_xor_sync(0xffffffffu, y, 1);
+        y += __shfl_xor_sync(0xffffffffu, y, 2);
+        if (c == j) v = y;
+      }
+      acc[k * kWThreads + tid] += v;
     }
   }
-#pragma unroll
-  for (int k = 0; k < NW; ++k) {
-    const int t = 2 * k + (w >> 1), key0 = (t0 + t) * kKvqTile + (w & 1) * 32;
-    if (t >= nt) continue;
-    float v = 0.f;   // lane 4 g + j ends with key 8 j + g
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float y = acc[k][j];
-      y += __shfl_xor_sync(0xffffffffu, y, 1);
-      y += __shfl_xor_sync(0xffffffffu, y, 2);
-      if (c == j) v = y;
-    }
-    const int key = key0 + 8 * c + g8;
-    if (key < len) {
-      float *p = a.c.weights + plane * a.c.rows_pad + key;
+  for (int k = 0; k < np; ++k) {
+    const int t = 2 * k + (w >> 1), key = (t0 + t) * kKvqTile + (w & 1) * 32 + 8 * c + g8;
+    if (t < nt && key < len) {
+      float v = acc[k * kWThreads + tid], *p = a.c.weights + plane * a.c.rows_pad + key;
       if (a.decay != 0.f) v = fmaf(a.decay, *p, v);
       *p = v;
       if (a.w_out) a.w_out[((size_t)(a.call0 + i) * a.c.n_kv + head) * a.ldw + key] = v;
@@ -696,8 +695,7 @@ cudaError_t attend_t(const KvqAttnArgs &a, cudaStream_t s) {
 }
 template <int HD, typename T, int NQ>
 cudaError_t weights_t(const KvqAttnArgs &a, cudaStream_t s) {
-  constexpr int smem = kKvqWeightTiles * kvq_k_bytes(HD) + QTile<HD, sizeof(T) == 4, NQ>::kBytes;
-  static_assert(kKvqWeightTiles == 8, "the waits count four pairs of tiles");
+  constexpr int smem = kWSlots * 2 * kvq_k_bytes(HD) + QTile<HD, sizeof(T) == 4, NQ>::kBytes + kKvqWeightTiles / 2 * kWThreads * 4;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_smem(kvq_weights_kernel<HD, T, NQ>, smem, done);
   if (e != cudaSuccess) return e;
