@@ -8,6 +8,7 @@ kernels; there is no CPU fallback: if the library is missing or cannot load,
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 from typing import Dict, Iterable, Optional, Sequence, Tuple
@@ -529,21 +530,27 @@ def _ints(x, n: int, what: str):
     """A host int32 array of n values for the library."""
     if len(x) != n:
         raise ValueError(f"{what}: {len(x)} values for {n} sequences")
-    return (ctypes.c_int32 * n)(*x)
+    return array.array("i", x)   # (a fifth of the time that a ctypes array takes)
+
+
+def _addr(x: array.array) -> int:
+    """Where x's values are; the caller keeps x."""
+    return x.buffer_info()[0]
 
 
 _kvq_types = {}   # torch dtype -> FM_DTYPE_*
 
 
-def _kvq_rows(x, rows: int, heads: Optional[int], head_dim: int, what: str):
-    """(pointer, dtype, heads, row stride) of a CUDA tensor [>= rows, heads, head_dim] whose rows are whole: the last
-    two axes contiguous, any stride between rows."""
+def _kvq_rows(x, rows: int, heads: Optional[int], c, what: str):
+    """(pointer, dtype, heads, row stride) of a tensor [>= rows, heads, head_dim] on the cache's device whose rows are
+    whole: the last two axes contiguous, any stride between rows."""
+    head_dim = c._head_dim
     if not _kvq_types:
         import torch
         _kvq_types.update({torch.float32: FM_DTYPE_F32, torch.float16: FM_DTYPE_F16, torch.bfloat16: FM_DTYPE_BF16})
     dtype = _kvq_types.get(x.dtype)
-    if dtype is None or not x.is_cuda:
-        raise ValueError(f"{what} must be a float32, float16 or bfloat16 CUDA tensor")
+    if dtype is None or x.get_device() != c._device:
+        raise ValueError(f"{what} must be a float32, float16 or bfloat16 tensor on cuda:{c._device}")
     shape, stride = x.shape, x.stride()
     if len(shape) != 3 or shape[2] != head_dim or (heads is not None and shape[1] != heads) or shape[0] < rows:
         raise ValueError(f"{what} has shape {tuple(shape)}, expected [{rows}, {heads or 'heads'}, {head_dim}]")
@@ -552,14 +559,14 @@ def _kvq_rows(x, rows: int, heads: Optional[int], head_dim: int, what: str):
     return x.data_ptr(), dtype, shape[1], stride[0] if shape[0] > 1 else shape[1] * head_dim
 
 
-def _kvq_weights(x, n: int, heads: int, what: str):
-    """(pointer, row stride) of a contiguous CUDA float32 tensor [n, heads, rows], or of None."""
+def _kvq_weights(x, n: int, c, what: str):
+    """(pointer, row stride) of a contiguous float32 tensor [n, n_kv_heads, rows] on the cache's device, or of None."""
     if x is None:
         return None, 0
     import torch
-    if x.dtype != torch.float32 or not x.is_cuda or x.dim() != 3 or x.shape[0] != n or x.shape[1] != heads or \
-            not x.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous float32 CUDA tensor [{n}, {heads}, rows]")
+    if x.dtype != torch.float32 or x.get_device() != c._device or x.dim() != 3 or x.shape[0] != n or \
+            x.shape[1] != c._kv_heads or not x.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous float32 tensor [{n}, {c._kv_heads}, rows] on cuda:{c._device}")
     return x.data_ptr(), x.shape[2]
 
 
@@ -569,7 +576,8 @@ def fm_kvq_create(n_layers: int, n_seqs: int, n_kv_heads: int, head_dim: int, ma
     g = FmKvqConfig(n_layers, n_seqs, n_kv_heads, head_dim, max_rows)
     c = KvqCache()
     _kvq_check(load_library().fm_kvq_create(ctypes.byref(g), _stream(stream), ctypes.byref(c)))
-    c._kv_heads, c._head_dim = n_kv_heads, head_dim
+    import torch
+    c._kv_heads, c._head_dim, c._device = n_kv_heads, head_dim, torch.cuda.current_device()
     return c
 
 
@@ -578,12 +586,13 @@ def fm_kvq_append(c, layer: int, seq_ids: Sequence[int], k, v, n_rows: Sequence[
     """Rows k, v (CUDA tensors [sum(n_rows), n_kv_heads, head_dim], float32, float16 or bfloat16, packed in the order
     of seq_ids) become rows starts[i] .. of their sequences; each length is then starts[i] + n_rows[i]."""
     n, total = len(seq_ids), sum(n_rows)
-    kp, dtype, _, ld = _kvq_rows(k, total, c._kv_heads, c._head_dim, "k")
-    vp, vt, _, vld = _kvq_rows(v, total, c._kv_heads, c._head_dim, "v")
+    kp, dtype, _, ld = _kvq_rows(k, total, c._kv_heads, c, "k")
+    vp, vt, _, vld = _kvq_rows(v, total, c._kv_heads, c, "v")
     if vt != dtype or vld != ld:
         raise ValueError("k and v differ in dtype or row stride")
-    _kvq_check(load_library().fm_kvq_append(c, layer, n, _ints(seq_ids, n, "seq_ids"), _ints(n_rows, n, "n_rows"),
-                                            _ints(starts, n, "starts"), kp, vp, dtype, ld, _stream(stream)), c)
+    seq_ids_, n_rows_, starts_ = _ints(seq_ids, n, "seq_ids"), _ints(n_rows, n, "n_rows"), _ints(starts, n, "starts")
+    _kvq_check(load_library().fm_kvq_append(c, layer, n, _addr(seq_ids_), _addr(n_rows_),
+                                            _addr(starts_), kp, vp, dtype, ld, _stream(stream)), c)
 
 
 def fm_kvq_read(c, layer: int, seq_ids: Sequence[int], rows: Sequence[int], n_rows: Sequence[int], k=None, v=None,
@@ -594,15 +603,18 @@ def fm_kvq_read(c, layer: int, seq_ids: Sequence[int], rows: Sequence[int], n_ro
     dtype, ld = FM_DTYPE_F32, c._kv_heads * c._head_dim
     kp = vp = None
     if k is not None:
-        kp, dtype, _, ld = _kvq_rows(k, total, c._kv_heads, c._head_dim, "k")
+        kp, dtype, _, ld = _kvq_rows(k, total, c._kv_heads, c, "k")
     if v is not None:
-        vp, vt, _, vld = _kvq_rows(v, total, c._kv_heads, c._head_dim, "v")
+        vp, vt, _, vld = _kvq_rows(v, total, c._kv_heads, c, "v")
         if k is not None and (vt != dtype or vld != ld):
             raise ValueError("k and v differ in dtype or row stride")
         dtype, ld = vt, vld
-    wp, ldw = _kvq_weights(weights, n, c._kv_heads, "weights")
-    _kvq_check(load_library().fm_kvq_read(c, layer, n, _ints(seq_ids, n, "seq_ids"), _ints(rows, n, "rows"),
-                                          _ints(n_rows, n, "n_rows"), kp, vp, dtype, ld, wp, ldw, _stream(stream)), c)
+    wp, ldw = _kvq_weights(weights, n, c, "weights")
+    seq_ids_ = _ints(seq_ids, n, "seq_ids")
+    rows_ = _ints(rows, n, "rows")
+    n_rows_ = _ints(n_rows, n, "n_rows")
+    _kvq_check(load_library().fm_kvq_read(c, layer, n, _addr(seq_ids_), _addr(rows_),
+                                          _addr(n_rows_), kp, vp, dtype, ld, wp, ldw, _stream(stream)), c)
 
 
 def fm_kvq_attend(c, layer: int, seq_ids: Sequence[int], q, n_rows: Sequence[int], out, scale: Optional[float] = None,
@@ -614,13 +626,15 @@ def fm_kvq_attend(c, layer: int, seq_ids: Sequence[int], q, n_rows: Sequence[int
     rows' weights alone; a number d counts them, w = d w + this call's, into weights too (CUDA float32 [n_seqs,
     n_kv_heads, rows] or None)."""
     n, total = len(seq_ids), sum(n_rows)
-    qp, dtype, heads, ldq = _kvq_rows(q, total, None, c._head_dim, "q")
-    op, ot, _, ldo = _kvq_rows(out, total, heads, c._head_dim, "out")
+    qp, dtype, heads, ldq = _kvq_rows(q, total, None, c, "q")
+    op, ot, _, ldo = _kvq_rows(out, total, heads, c, "out")
     if ot != dtype:
         raise ValueError("q and out differ in dtype")
-    wp, ldw = _kvq_weights(weights, n, c._kv_heads, "weights")
+    wp, ldw = _kvq_weights(weights, n, c, "weights")
+    seq_ids_ = _ints(seq_ids, n, "seq_ids")
+    n_rows_ = _ints(n_rows, n, "n_rows")
     _kvq_check(load_library().fm_kvq_attend(
-        c, layer, n, _ints(seq_ids, n, "seq_ids"), _ints(n_rows, n, "n_rows"), qp, dtype, heads, ldq,
+        c, layer, n, _addr(seq_ids_), _addr(n_rows_), qp, dtype, heads, ldq,
         c._head_dim ** -0.5 if scale is None else scale, 1 if causal else 0, first_row, op, ldo,
         -1.0 if decay is None else decay, wp, ldw, _stream(stream)), c)
 
@@ -628,8 +642,9 @@ def fm_kvq_attend(c, layer: int, seq_ids: Sequence[int], q, n_rows: Sequence[int
 def fm_kvq_set_weights(c, layer: int, seq_ids: Sequence[int], weights, stream=None) -> None:
     """The weights of each sequence's rows from a CUDA float32 tensor [n_seqs, n_kv_heads, >= longest]."""
     n = len(seq_ids)
-    wp, ldw = _kvq_weights(weights, n, c._kv_heads, "weights")
-    _kvq_check(load_library().fm_kvq_set_weights(c, layer, n, _ints(seq_ids, n, "seq_ids"), wp, ldw, _stream(stream)), c)
+    wp, ldw = _kvq_weights(weights, n, c, "weights")
+    seq_ids_ = _ints(seq_ids, n, "seq_ids")
+    _kvq_check(load_library().fm_kvq_set_weights(c, layer, n, _addr(seq_ids_), wp, ldw, _stream(stream)), c)
 
 
 def fm_kvq_evict(c, layer: int, src_ids: Sequence[int], dst_ids: Sequence[int], keep: int, recent: int, kept=None,
@@ -640,10 +655,12 @@ def fm_kvq_evict(c, layer: int, src_ids: Sequence[int], dst_ids: Sequence[int], 
     n = len(src_ids)
     if kept is not None:
         import torch
-        if kept.dtype != torch.int32 or not kept.is_cuda or not kept.is_contiguous() or \
+        if kept.dtype != torch.int32 or kept.get_device() != c._device or not kept.is_contiguous() or \
                 tuple(kept.shape) != (n, c._kv_heads, keep):
-            raise ValueError(f"kept must be a contiguous int32 CUDA tensor [{n}, {c._kv_heads}, {keep}]")
-    _kvq_check(load_library().fm_kvq_evict(c, layer, n, _ints(src_ids, n, "src_ids"), _ints(dst_ids, n, "dst_ids"), keep,
+            raise ValueError(f"kept must be a contiguous int32 tensor [{n}, {c._kv_heads}, {keep}] on cuda:{c._device}")
+    src_ids_ = _ints(src_ids, n, "src_ids")
+    dst_ids_ = _ints(dst_ids, n, "dst_ids")
+    _kvq_check(load_library().fm_kvq_evict(c, layer, n, _addr(src_ids_), _addr(dst_ids_), keep,
                                            recent, _ptr(kept), _stream(stream)), c)
 
 
