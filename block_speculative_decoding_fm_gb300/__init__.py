@@ -39,7 +39,8 @@ EXPORTS = ["fm_create", "fm_time_conditioning", "fm_context_append", "fm_context
            "fm_mtp_create", "fm_mtp_forward", "fm_mtp_draft", "fm_mtp_cache", "fm_mtp_last_launch_count",
            "fm_mtp_last_error", "fm_mtp_destroy",
            "fm_kvq_create", "fm_kvq_append", "fm_kvq_read", "fm_kvq_attend", "fm_kvq_set_weights", "fm_kvq_evict",
-           "fm_kvq_length", "fm_kvq_memory_bytes", "fm_kvq_synchronize", "fm_kvq_last_error", "fm_kvq_destroy"]
+           "fm_kvq_length", "fm_kvq_get_config", "fm_kvq_last_launch_count", "fm_mtp_use_kvq",
+           "fm_kvq_memory_bytes", "fm_kvq_synchronize", "fm_kvq_last_error", "fm_kvq_destroy"]
 
 
 class FmConfig(ctypes.Structure):
@@ -145,6 +146,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "fm_kvq_set_weights": (I32, [P, I32, I32, P, P, I64, P]),
         "fm_kvq_evict": (I32, [P, I32, I32, P, P, I32, I32, P, P]),
         "fm_kvq_length": (I32, [P, I32, I32, ctypes.POINTER(I32)]),
+        "fm_kvq_get_config": (I32, [P, ctypes.POINTER(FmKvqConfig)]),
+        "fm_kvq_last_launch_count": (I32, [P, ctypes.POINTER(I32)]),
+        "fm_mtp_use_kvq": (I32, [P, P, I32, I32, I64, ctypes.c_float]),
         "fm_kvq_memory_bytes": (I32, [P, ctypes.POINTER(I64)]),
         "fm_kvq_synchronize": (I32, [P, P]),
         "fm_kvq_last_error": (ctypes.c_char_p, [P]),
@@ -669,6 +673,30 @@ def fm_kvq_length(c, layer: int, seq: int) -> int:
     if load_library().fm_kvq_length(c, layer, seq, ctypes.byref(v)) != FM_OK:
         raise FmError(FM_ERR_INVALID_ARG, f"layer {layer}, sequence {seq}")
     return v.value
+
+
+def fm_kvq_get_config(c) -> FmKvqConfig:
+    g = FmKvqConfig()
+    if load_library().fm_kvq_get_config(c, ctypes.byref(g)) != FM_OK:
+        raise FmError(FM_ERR_INVALID_ARG, "no cache")
+    return g
+
+
+def fm_kvq_last_launch_count(c) -> int:
+    n = ctypes.c_int32()
+    _kvq_check(load_library().fm_kvq_last_launch_count(c, ctypes.byref(n)), c)
+    return n.value
+
+
+def fm_mtp_use_kvq(m, c, layer: int = 0, seq: int = 0, next_pos: Optional[int] = None,
+                   decay: Optional[float] = None) -> None:
+    """Keep the MTP head's rows in (layer, seq) of the 4-bit cache c (None: in its own f32 cache).  next_pos: the position
+    after the cache's last row (its length unless given); decay: count the attention weights of every pass (None: do
+    not).  The head keeps c alive while it uses it."""
+    if c is not None and next_pos is None:
+        next_pos = fm_kvq_length(c, layer, seq)
+    _mtp_check(load_library().fm_mtp_use_kvq(m, c, layer, seq, next_pos or 0, -1.0 if decay is None else decay), m)
+    m._kvq = c
 
 
 def fm_kvq_memory_bytes(c) -> int:

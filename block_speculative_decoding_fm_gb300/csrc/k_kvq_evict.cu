@@ -300,6 +300,7 @@ cudaError_t evict_hd(const KvqEvictArgs &a, cudaStream_t s) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
+    ++kvq_launches();
     e = cudaLaunchKernelEx(&cfg, kvq_select_kernel<kCluster>, a);
   } else {
     e = kvq_launch(kvq_select_kernel<1>, dim3(planes), dim3(256), 0, s, a);

@@ -19,6 +19,11 @@
 
 using namespace fm;
 
+int &fm::kvq_launches() {
+  thread_local int n = 0;
+  return n;
+}
+
 struct fm_kvq {
   fm_kvq_config cfg{};
   int device = 0, n_sm = 0;
@@ -37,6 +42,7 @@ struct fm_kvq {
   cudaEvent_t done = nullptr;     // the last eager call's work
   cudaStream_t last = nullptr;
   bool has_last = false;
+  int launches = 0;               // kernels that the last call launched
   char err[512] = "";
 };
 
@@ -153,11 +159,13 @@ bool capturing(cudaStream_t s) {
 }
 
 fm_status begin(fm_kvq *c, cudaStream_t s) {
+  kvq_launches() = 0;
   if (c->has_last && c->last != s && !capturing(s)) KCK(cudaStreamWaitEvent(s, c->done, 0));
   return FM_OK;
 }
 
 fm_status end(fm_kvq *c, cudaStream_t s) {
+  c->launches = kvq_launches();
   if (capturing(s)) return FM_OK;
   KCK(cudaEventRecord(c->done, s));
   c->last = s;
@@ -562,6 +570,18 @@ fm_status fm_kvq_evict(fm_kvq *c, int32_t layer, int32_t n_seqs, const int32_t *
 fm_status fm_kvq_length(const fm_kvq *c, int32_t layer, int32_t seq, int32_t *length) {
   if (!c || !length || layer < 0 || layer >= c->cfg.n_layers || seq < 0 || seq >= c->cfg.n_seqs) return FM_ERR_INVALID_ARG;
   *length = c->len[(size_t)layer * c->cfg.n_seqs + seq];
+  return FM_OK;
+}
+
+fm_status fm_kvq_get_config(const fm_kvq *c, fm_kvq_config *cfg) {
+  if (!c || !cfg) return FM_ERR_INVALID_ARG;
+  *cfg = c->cfg;
+  return FM_OK;
+}
+
+fm_status fm_kvq_last_launch_count(const fm_kvq *c, int32_t *count) {
+  if (!c || !count) return FM_ERR_INVALID_ARG;
+  *count = c->launches;
   return FM_OK;
 }
 

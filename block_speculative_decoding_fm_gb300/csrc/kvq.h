@@ -125,6 +125,8 @@ struct KvqEvictArgs {
 };
 cudaError_t launch_kvq_evict(const KvqEvictArgs &a, int hd, cudaStream_t s);
 
+int &kvq_launches();   // this thread's launches since a call began
+
 template <typename K, typename... Args>
 inline cudaError_t kvq_launch(K kern, dim3 grid, dim3 block, size_t smem, cudaStream_t s, const Args &...args) {
   cudaLaunchConfig_t cfg = {};
@@ -137,6 +139,7 @@ inline cudaError_t kvq_launch(K kern, dim3 grid, dim3 block, size_t smem, cudaSt
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  ++kvq_launches();
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 

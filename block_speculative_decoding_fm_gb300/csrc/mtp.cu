@@ -9,7 +9,9 @@
 // product).  Products with few 128-row tiles are split along K into slices
 // (the table's tiles in slice order, each slice reading its own Y chunks), so
 // that enough SMs stream the weights; the consumer of the output sums the
-// slices.  The KV cache is f32, as the page keeps it.
+// slices.  The KV cache is f32, as the page keeps it, or a 4-bit cache that the
+// caller hands over (fm_mtp_use_kvq): a pass then stores its rows there and
+// attends through fm_kvq_append and fm_kvq_attend.
 #include <algorithm>
 #include <cstdarg>
 #include <cstdio>
@@ -123,10 +125,11 @@ __global__ void __launch_bounds__(kThreads) mtp_add_norm_kernel(float *x, bool r
 }
 
 // Per head: RMSNorm over hd, NEOX RoPE on the first rot dims at the row's position;
-// q heads -> Q, k heads -> the K cache row, v heads -> the V cache row.
+// q heads -> Q, k heads -> the K cache row (row0 + m), v heads -> the V cache row.
 // Block (m, j): j < nh a q head, then nkv k heads, then nkv v heads; thread = dim.
 __global__ void mtp_qk_prep_kernel(const float *qkv, int ldq, int nh, int nkv, int hd, int rot, double theta, float eps,
-                                   const float *w_q, const float *w_k, int pos0, float *Q, float *kc, float *vc) {
+                                   const float *w_q, const float *w_k, int pos0, int row0, float *Q, float *kc,
+                                   float *vc) {
   __shared__ float sh[256];
   __shared__ float red[8];
   pdl_trigger();
@@ -136,7 +139,7 @@ __global__ void mtp_qk_prep_kernel(const float *qkv, int ldq, int nh, int nkv, i
   const float *row = qkv + (size_t)m * ldq;
   if (j >= nh + nkv) {
     const int g = j - nh - nkv;
-    vc[(size_t)pos * nkv * hd + g * hd + d] = __ldcg(row + nh * 2 * hd + nkv * hd + g * hd + d);
+    vc[(size_t)(row0 + m) * nkv * hd + g * hd + d] = __ldcg(row + nh * 2 * hd + nkv * hd + g * hd + d);
     return;
   }
   const bool isq = j < nh;
@@ -162,7 +165,7 @@ __global__ void mtp_qk_prep_kernel(const float *qkv, int ldq, int nh, int nkv, i
   if (isq)
     Q[(size_t)m * nh * hd + j * hd + d] = out;
   else
-    kc[(size_t)pos * nkv * hd + (j - nh) * hd + d] = out;
+    kc[(size_t)(row0 + m) * nkv * hd + (j - nh) * hd + d] = out;
 }
 
 // Causal attention of row m, q head h over cache rows kv_lo .. pos0 + m (KV head
@@ -221,6 +224,23 @@ __global__ void __launch_bounds__(kThreads) mtp_attn_kernel(const float *Q, cons
     const float gate = __ldcg(qkv + (size_t)m * ldq + h * 2 * hd + hd + t);
     store_y1(ylm, m, h * hd + t, acc / l / (1.f + expf(-gate)));
   }
+}
+
+// attention rows over the 4-bit cache (o [M][nh hd]) times sigmoid(gate), as the operand of attn_output.
+__global__ void __launch_bounds__(kThreads) mtp_gate_kernel(const float *o, const float *qkv, int ldq, int nh, int hd,
+                                                            uint8_t *ylm) {
+  pdl_trigger();
+  pdl_wait();
+  const int m = blockIdx.y, c0 = 8 * (blockIdx.x * kThreads + threadIdx.x);
+  if (c0 >= nh * hd) return;
+  const int h = c0 / hd;
+  float v[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float gate = __ldcg(qkv + (size_t)m * ldq + h * 2 * hd + hd + (c0 - h * hd) + e);
+    v[e] = __ldcg(o + (size_t)m * nh * hd + c0 + e) / (1.f + expf(-gate));
+  }
+  store_y8(ylm, m, c0, v);
 }
 
 // silu(gate) * up from the stacked gate / up product, as the operand of ffn_down.
@@ -288,6 +308,13 @@ struct fm_mtp {
   int32_t *ticket = nullptr, *tok = nullptr, *dev_err = nullptr;
   size_t y_floats = 0;
   int last_launches = 0;
+  // the rows in a 4-bit cache instead of kc / vc (fm_mtp_use_kvq)
+  fm_kvq *kvq = nullptr;
+  int kvq_layer = 0, kvq_seq = 0;
+  float kvq_decay = -1.f;
+  int64_t next_pos = 0;          // the position after the cache's last row
+  int kvq_rows = 0;              // rows a sequence of it holds
+  float *kst = nullptr, *vst = nullptr, *ao = nullptr;   // a pass's rows before they are stored, and its attention rows
 };
 
 namespace {
@@ -416,6 +443,42 @@ fm_status run_lin(fm_mtp *m, const fm_mtp::Lin &L, int M, float *out, int32_t *t
   return FM_OK;
 }
 
+#define MKVQ(expr)                                                                               \
+  do {                                                                                           \
+    const fm_status s_ = (expr);                                                                 \
+    if (s_ != FM_OK) return mfail(m, s_, "4-bit cache: %s", fm_kvq_last_error(m->kvq));          \
+    int32_t n_ = 0;                                                                              \
+    fm_kvq_last_launch_count(m->kvq, &n_);                                                       \
+    m->last_launches += n_;                                                                      \
+  } while (0)
+
+// The cache's row of position pos0: as far from the end as pos0 is from the next position.
+fm_status kvq_row_of(fm_mtp *m, int pos0, int32_t *row) {
+  int32_t len = 0;
+  if (fm_kvq_length(m->kvq, m->kvq_layer, m->kvq_seq, &len) != FM_OK)
+    return mfail(m, FM_ERR_STATE, "the 4-bit cache has no layer %d, sequence %d", m->kvq_layer, m->kvq_seq);
+  const int64_t r = len - (m->next_pos - pos0);
+  if (pos0 > m->next_pos || r < 0)
+    return mfail(m, FM_ERR_STATE, "pos0 %d: the 4-bit cache holds %d rows up to position %lld", pos0, len, (long long)m->next_pos);
+  *row = (int32_t)r;
+  return FM_OK;
+}
+
+// a pass's rows into the 4-bit cache, and its queries over it
+fm_status kvq_rows_attend(fm_mtp *m, int M, int pos0, int kv_lo, cudaStream_t s) {
+  const fm_mtp_config &c = m->cfg;
+  int32_t row = 0;
+  MTRY(kvq_row_of(m, pos0, &row));
+  const int32_t seq = m->kvq_seq, rows = M;
+  MKVQ(fm_kvq_append(m->kvq, m->kvq_layer, 1, &seq, &rows, &row, m->kst, m->vst, FM_DTYPE_F32,
+                     (int64_t)c.n_kv_heads * c.head_dim, s));
+  m->next_pos = (int64_t)pos0 + M;
+  const int64_t ld = (int64_t)c.n_heads * c.head_dim;
+  MKVQ(fm_kvq_attend(m->kvq, m->kvq_layer, 1, &seq, &rows, m->Q, FM_DTYPE_F32, c.n_heads, ld, 1.0f / sqrtf((float)c.head_dim),
+                     1, kv_lo, m->ao, ld, m->kvq_decay, nullptr, 0, s));
+  return FM_OK;
+}
+
 // MTPHead.forward over M rows; drafts: per-row argmax of the lm_head, or null
 fm_status mtp_pass(fm_mtp *m, int M, const int32_t *tokens, const float *hn, int ldh, int pos0, int kv_lo,
                    int32_t *drafts, cudaStream_t s) {
@@ -429,11 +492,19 @@ fm_status mtp_pass(fm_mtp *m, int M, const int32_t *tokens, const float *hn, int
              (const float *)m->n_attn, c.eps, m->ylm, (float *)nullptr));
   ++m->last_launches;
   MTRY(run_lin(m, m->qkv, M, m->y, nullptr, s));
+  const bool q4 = m->kvq != nullptr;
   MCK(launch(mtp_qk_prep_kernel, dim3(M, nh + 2 * nkv), dim3(hd), s, (const float *)m->y, m->qkv.N, nh, nkv, hd,
-             c.rot_dims, (double)c.theta, c.eps, (const float *)m->n_q, (const float *)m->n_k, pos0, m->Q, m->kc, m->vc));
+             c.rot_dims, (double)c.theta, c.eps, (const float *)m->n_q, (const float *)m->n_k, pos0, q4 ? 0 : pos0, m->Q,
+             q4 ? m->kst : m->kc, q4 ? m->vst : m->vc));
   ++m->last_launches;
-  MCK(launch(mtp_attn_kernel, dim3(M, nh), dim3(kThreads), s, (const float *)m->Q, (const float *)m->y, m->qkv.N,
-             (const float *)m->kc, (const float *)m->vc, nh, nkv, hd, pos0, kv_lo, 1.0f / sqrtf((float)hd), m->ylm));
+  if (q4) {
+    MTRY(kvq_rows_attend(m, M, pos0, kv_lo, s));
+    MCK(launch(mtp_gate_kernel, dim3((nh * hd / 8 + kThreads - 1) / kThreads, M), dim3(kThreads), s, (const float *)m->ao,
+               (const float *)m->y, m->qkv.N, nh, hd, m->ylm));
+  } else {
+    MCK(launch(mtp_attn_kernel, dim3(M, nh), dim3(kThreads), s, (const float *)m->Q, (const float *)m->y, m->qkv.N,
+               (const float *)m->kc, (const float *)m->vc, nh, nkv, hd, pos0, kv_lo, 1.0f / sqrtf((float)hd), m->ylm));
+  }
   ++m->last_launches;
   // attn_output's slices land beside the q/k/v rows' gates (read above): a separate region
   float *yo = m->y + (size_t)kMaxRows * m->qkv.N;
@@ -459,7 +530,20 @@ fm_status mtp_checks(fm_mtp *m, int M, const int32_t *tokens, const float *hn, i
   if (M < 1 || M > c.max_rows) return mfail(m, FM_ERR_INVALID_ARG, "n_rows %d outside [1, %d]", M, c.max_rows);
   if (!tokens || !hn) return mfail(m, FM_ERR_INVALID_ARG, "null tokens or hidden rows");
   if (pos0 < 0 || kv_lo < 0 || kv_lo > pos0) return mfail(m, FM_ERR_INVALID_ARG, "kv_lo %d outside [0, pos0 %d]", kv_lo, pos0);
+  if (m->kvq) return FM_OK;   // (the 4-bit cache's own size counts)
   if (pos0 + M > c.kv_cap) return mfail(m, FM_ERR_INVALID_ARG, "pos0 + n_rows = %d > kv_cap %d", pos0 + M, c.kv_cap);
+  return FM_OK;
+}
+
+// with a 4-bit cache: `rows` rows from pos0 on fit, before anything is launched
+fm_status mtp_kvq_checks(fm_mtp *m, int rows, int pos0, int kv_lo) {
+  if (!m->kvq) return FM_OK;
+  int32_t row = 0;
+  MTRY(kvq_row_of(m, pos0, &row));
+  if (row + (int64_t)rows > m->kvq_rows)
+    return mfail(m, FM_ERR_CONTEXT_FULL, "row %d + %d rows, the 4-bit cache holds %d", row, rows, m->kvq_rows);
+  if (kv_lo > 0 && row != pos0)
+    return mfail(m, FM_ERR_UNSUPPORTED, "kv_lo %d after an eviction: rows are no longer at their positions", kv_lo);
   return FM_OK;
 }
 
@@ -573,6 +657,7 @@ fm_status fm_mtp_forward(fm_mtp *m, int32_t n_rows, const int32_t *tokens_dev, c
   if (!m) return FM_ERR_INVALID_ARG;
   m->last_launches = 0;
   MTRY(mtp_checks(m, n_rows, tokens_dev, hn_dev, pos0, kv_lo));
+  MTRY(mtp_kvq_checks(m, n_rows, pos0, kv_lo));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   MTRY(mtp_pass(m, n_rows, tokens_dev, hn_dev, m->cfg.hidden, pos0, kv_lo, drafts_dev, s));
   if (hout_dev)
@@ -586,8 +671,9 @@ fm_status fm_mtp_draft(fm_mtp *m, int32_t n_rows, const int32_t *tokens_dev, con
   m->last_launches = 0;
   MTRY(mtp_checks(m, n_rows, tokens_dev, hn_dev, pos0, kv_lo));
   if (!drafts_dev) return mfail(m, FM_ERR_INVALID_ARG, "null drafts");
-  if (depth < 1 || pos0 + n_rows + depth - 1 > m->cfg.kv_cap)
+  if (depth < 1 || (!m->kvq && pos0 + n_rows + depth - 1 > m->cfg.kv_cap))
     return mfail(m, FM_ERR_INVALID_ARG, "depth %d outside [1, %d]", depth, m->cfg.kv_cap - pos0 - n_rows + 1);
+  MTRY(mtp_kvq_checks(m, n_rows + depth - 1, pos0, kv_lo));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int H = m->cfg.hidden;
   MTRY(mtp_pass(m, n_rows, tokens_dev, hn_dev, H, pos0, kv_lo, nullptr, s));
@@ -603,10 +689,41 @@ fm_status fm_mtp_draft(fm_mtp *m, int32_t n_rows, const int32_t *tokens_dev, con
   return FM_OK;
 }
 
+fm_status fm_mtp_use_kvq(fm_mtp *m, fm_kvq *c, int32_t layer, int32_t seq, int64_t next_pos, float decay) {
+  if (!m) return FM_ERR_INVALID_ARG;
+  if (!c) {
+    m->kvq = nullptr;
+    return FM_OK;
+  }
+  fm_kvq_config g;
+  int32_t len = 0;
+  if (fm_kvq_get_config(c, &g) != FM_OK || fm_kvq_length(c, layer, seq, &len) != FM_OK)
+    return mfail(m, FM_ERR_INVALID_ARG, "the 4-bit cache has no layer %d, sequence %d", layer, seq);
+  if (g.n_kv_heads != m->cfg.n_kv_heads || g.head_dim != m->cfg.head_dim)
+    return mfail(m, FM_ERR_INVALID_ARG, "the 4-bit cache has %d heads of %d, the head %d of %d", g.n_kv_heads, g.head_dim,
+                 m->cfg.n_kv_heads, m->cfg.head_dim);
+  if (next_pos < len || next_pos > INT32_MAX) return mfail(m, FM_ERR_INVALID_ARG, "next_pos %lld with %d rows", (long long)next_pos, len);
+  if (!(decay == decay) || decay > 3.0e38f) return mfail(m, FM_ERR_INVALID_ARG, "decay is not finite");
+  if (!m->ao) {
+    const size_t kvw = (size_t)kMaxRows * m->cfg.n_kv_heads * m->cfg.head_dim;
+    if (!m->kst) MTRY(malloc_dev(m, &m->kst, kvw));
+    if (!m->vst) MTRY(malloc_dev(m, &m->vst, kvw));
+    MTRY(malloc_dev(m, &m->ao, (size_t)kMaxRows * m->cfg.n_heads * m->cfg.head_dim));
+  }
+  m->kvq = c;
+  m->kvq_layer = layer;
+  m->kvq_seq = seq;
+  m->kvq_rows = g.max_rows;
+  m->kvq_decay = decay;
+  m->next_pos = next_pos;
+  return FM_OK;
+}
+
 fm_status fm_mtp_cache(fm_mtp *m, int32_t which, int32_t rows, float *dst, void *stream) {
   if (!m) return FM_ERR_INVALID_ARG;
   if ((which != 0 && which != 1) || rows < 0 || rows > m->cfg.kv_cap || !dst)
     return mfail(m, FM_ERR_INVALID_ARG, "bad cache copy arguments");
+  if (m->kvq && rows > 0) return mfail(m, FM_ERR_STATE, "the rows are in a 4-bit cache: fm_kvq_read reads them");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   MCK(cudaMemcpyAsync(dst, which ? m->vc : m->kc, (size_t)rows * m->cfg.n_kv_heads * m->cfg.head_dim * 4,
                       cudaMemcpyDefault, s));

@@ -662,6 +662,10 @@ FM_API fm_status fm_kvq_evict(fm_kvq *c, int32_t layer, int32_t n_seqs, const in
 
 /* The rows a (layer, sequence) holds.  Errors: FM_ERR_INVALID_ARG. */
 FM_API fm_status fm_kvq_length(const fm_kvq *c, int32_t layer, int32_t seq, int32_t *length);
+/* The configuration the cache was made with.  Errors: FM_ERR_INVALID_ARG. */
+FM_API fm_status fm_kvq_get_config(const fm_kvq *c, fm_kvq_config *cfg);
+/* Kernel launches issued by the last call that completed. */
+FM_API fm_status fm_kvq_last_launch_count(const fm_kvq *c, int32_t *count);
 /* Device bytes the cache holds (rows, weights, workspace). */
 FM_API fm_status fm_kvq_memory_bytes(const fm_kvq *c, int64_t *bytes);
 /* Wait for the stream; FM_ERR_TIMEOUT if a bounded device wait gave up since the last check (cleared). */
@@ -669,6 +673,29 @@ FM_API fm_status fm_kvq_synchronize(fm_kvq *c, void *stream);
 FM_API const char *fm_kvq_last_error(const fm_kvq *c);   /* never NULL; NULL c: the last failed fm_kvq_create */
 /* Free everything the cache owns.  NULL is ignored. */
 FM_API void fm_kvq_destroy(fm_kvq *c);
+
+/*
+ * fm_mtp_use_kvq -- keep the MTP head's rows in (layer, seq) of the 4-bit cache
+ * c from the next pass on (c NULL: in the head's own f32 cache again, which
+ * holds what it held).  A pass stores its rows by fm_kvq_append and attends by
+ * fm_kvq_attend; the rows a position may have are c's, not kv_cap's (kv_cap
+ * may be 1 on a head that only ever uses c).  c has the head's n_kv_heads and head_dim, stays the caller's and
+ * outlives its use.
+ *   next_pos: the position after the cache's last row (the length, unless
+ *     rows were evicted before).  A pass at pos0 <= next_pos rewinds
+ *     next_pos - pos0 rows and appends its own.  Rows evicted between passes
+ *     (fm_kvq_evict, in place) are the older ones as long as `recent` covers
+ *     what a pass may rewind; kv_lo is then 0.
+ *   decay: >= 0 counts the attention weights in every pass (fm_kvq_attend),
+ *     for an eviction; < 0 does not.
+ * Passes then also fail with FM_ERR_STATE (pos0 > next_pos, or a rewind past
+ * the rows that are left), FM_ERR_CONTEXT_FULL (the rows do not fit c) and
+ * FM_ERR_UNSUPPORTED (kv_lo > 0 after an eviction); nothing is launched then.
+ * fm_mtp_cache with rows > 0 answers FM_ERR_STATE.
+ * Errors: FM_ERR_INVALID_ARG (other heads or head_dim, no such layer or
+ *   sequence, next_pos below the length, decay not finite), FM_ERR_OOM.
+ */
+FM_API fm_status fm_mtp_use_kvq(fm_mtp *m, fm_kvq *c, int32_t layer, int32_t seq, int64_t next_pos, float decay);
 
 #ifdef __cplusplus
 }
