@@ -88,8 +88,11 @@ struct KvqAttnArgs {
   float scale_log2;       // scale * log2(e)
   int32_t causal, first;  // row t of T sees rows first <= j < (causal ? len - T + t + 1 : len)
   int32_t n;              // sequences of this launch
-  int32_t ctas;           // CTAs of the launch: of the W = st0[n] stages CTA b takes
-  int32_t share, extra;   // share = W / ctas, and one more where b < extra = W % ctas
+  // CTAs of the launch, and their shares of the W = st0[n] stages.  share > 0: CTA b takes share = W / ctas, and one more
+  // where b < extra = W % ctas, whatever units they belong to.  share 0: a unit of sequence i has parts[i] CTAs of its own.
+  int32_t ctas, share, extra;
+  int32_t parts[kKvqSeqs];
+  int32_t cta0[kKvqSeqs + 1];    // share 0: prefix sums of units x parts
   float *part_o;          // [2 ctas][8 nq][hd] unnormalised partial outputs
   float2 *part_ml;        // [2 ctas][8 nq] (reference, row sum)
   float *lse;             // [units][8 nq] log2 of the row sums, for the weights; or null
@@ -109,9 +112,12 @@ struct KvqAttnArgs {
 // attention (weights false) or its pass over the weights, which follows it
 template <int HD>
 cudaError_t kvq_attn_call(const KvqAttnArgs &a, bool weights, cudaStream_t s);
-// CTAs an SM of the attention kernel
+// the attention kernel's CTAs an SM, and the groups of four warps a CTA that take its stages in turn
+struct KvqShape {
+  int ctas, groups;
+};
 template <int HD>
-int kvq_attn_ctas(int type, int nq);
+KvqShape kvq_attn_shape(int type, int nq);
 constexpr int kKvqMaxCtas = 2;
 constexpr int kKvqWeightTiles = 16;   // tiles a CTA of the weights pass covers at most
 

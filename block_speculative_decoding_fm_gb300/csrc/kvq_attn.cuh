@@ -4,9 +4,10 @@
 //   O[r] = sum_j p_rj v_j / sum_j p_rj,  p_rj = exp2(t_rj - m_r),
 //   t_rj = scale log2(e) q_r . k_j  over the rows j that r sees,
 // one pass over the cache with a running reference m and sum.  A unit is a
-// (sequence, KV head, 8 nq query rows); the units lie end to end and every CTA
-// takes an equal share of their stages of 128 rows (64 for head dim 256); a second,
-// short launch joins the parts of shared units, in their order.
+// (sequence, KV head, 8 nq query rows), its keys stages of 128 rows (64 for head
+// dim 256).  Either a unit has CTAs of its own, or the units lie end to end and every CTA
+// takes an equal share of the stages (kvq.cu chooses); a second, short launch joins the parts of
+// units that several CTAs share, in their order.
 //
 // A CTA's warps work in groups of four with a ring of stages of their own (K and V codes and scales in one bulk
 // copy).  A warp forms the scores of a quarter of the stage's keys, S^T = K Q^T, and puts its P into
@@ -79,8 +80,20 @@ __device__ __forceinline__ void store4(T *p, float4 v) {
   }
 }
 
-// A CTA's share of the stages
-__device__ __forceinline__ int share_begin(const KvqAttnArgs &a, int b) { return b * a.share + min(b, a.extra); }
+// A CTA's share of the stages: [w_beg, w_end)
+__device__ __forceinline__ void share_of(const KvqAttnArgs &a, int b, int &w_beg, int &w_end) {
+  if (a.share) {
+    w_beg = b * a.share + min(b, a.extra);
+    w_end = w_beg + a.share + (b < a.extra);
+  } else {
+    const int i = find_seq<int32_t>(a.cta0, a.n, b), n = a.parts[i], S = a.stages[i];
+    const int unit = (b - a.cta0[i]) / n, p = b - a.cta0[i] - unit * n, u0 = a.st0[i] + unit * S;
+    const int q = S / n, r = S - q * n;
+    w_beg = u0 + p * q + min(p, r);
+    w_end = w_beg + q + (p < r);
+  }
+}
+// the CTA with a stage, shares equal
 __device__ __forceinline__ int cta_of(const KvqAttnArgs &a, int stage) {
   const int wide = a.extra * (a.share + 1);
   return stage < wide ? stage / (a.share + 1) : a.extra + (stage - wide) / a.share;
@@ -161,7 +174,8 @@ __global__ void __launch_bounds__(Shape<HD, T, NQ>::kThreads, Shape<HD, T, NQ>::
   float *wl = gm + NG * RT;                                                        // [group][warp][row] sums
   float *wx = wl + NG * 4 * RT + grp * 4 * RT;                                     // [group][warp][row] maxima
   const uint32_t full = smem_u32(bar + grp * 2 * NS), empty = full + NS * 8, qt = smem_u32(qs);
-  const int w_beg = share_begin(a, blockIdx.x), w_end = share_begin(a, blockIdx.x + 1);
+  int w_beg, w_end;
+  share_of(a, blockIdx.x, w_beg, w_end);
 
   pdl_trigger();
   if (tid == 0) {
@@ -512,15 +526,19 @@ template <int HD, typename T, int NQ, bool Many>
 __global__ void __launch_bounds__(kJoinThreads) kvq_join_kernel(const __grid_constant__ KvqAttnArgs a) {
   constexpr int RT = 8 * NQ, TX = Many ? 64 : kJoinThreads;
   pdl_trigger();
-  int at;   // a stage of the unit
+  int at, first, last;   // a stage of the unit; the CTAs that have parts of it
   if (Many) {
-    const int i = find_seq<int32_t>(a.unit0, a.n, (int)blockIdx.x / a.c.n_kv);
-    at = a.st0[i] + ((int)blockIdx.x - a.unit0[i] * a.c.n_kv) * a.stages[i];
+    const int i = find_seq<int32_t>(a.unit0, a.n, (int)blockIdx.x / a.c.n_kv), unit = (int)blockIdx.x - a.unit0[i] * a.c.n_kv;
+    at = a.st0[i] + unit * a.stages[i];
+    if (!a.share) first = a.cta0[i] + unit * a.parts[i], last = first + a.parts[i] - 1;
   } else {
-    at = share_begin(a, blockIdx.x + 1);
+    at = (blockIdx.x + 1) * a.share + min((int)blockIdx.x + 1, a.extra);
   }
   const Stretch x(a, at, a.st0[a.n]);
-  const int u0 = at - x.s0, first = cta_of(a, u0), last = cta_of(a, u0 + a.stages[x.i] - 1);
+  if (!Many || a.share) {
+    const int u0 = at - x.s0;
+    first = cta_of(a, u0), last = cta_of(a, u0 + a.stages[x.i] - 1);
+  }
   pdl_wait();   // every block, so that a later launch that waits for this one waits for what came before too
   if (first == last || (!Many && first != (int)blockIdx.x)) return;
   const int q = Many ? threadIdx.x >> 6 : 0, e = blockIdx.y * TX + threadIdx.x % TX;
@@ -685,8 +703,8 @@ cudaError_t attend_t(const KvqAttnArgs &a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   e = kvq_launch(kvq_attend_kernel<HD, T, NQ>, dim3(a.ctas), dim3(Sh::kThreads), Sh::kBytes, s, a);
   // nothing to join where every share is a unit
-  bool whole = a.extra == 0;
-  for (int i = 0; i < a.n; ++i) whole = whole && (a.rows[i] == 0 || a.stages[i] == a.share);
+  bool whole = a.extra == 0 || a.share == 0;
+  for (int i = 0; i < a.n; ++i) whole = whole && (a.rows[i] == 0 || (a.share ? a.stages[i] == a.share : a.parts[i] == 1));
   if (e != cudaSuccess || whole) return e;
   const int units = a.unit0[a.n] * a.c.n_kv, items = 8 * NQ * HD / 4;
   if (units <= a.ctas) return kvq_launch(kvq_join_kernel<HD, T, NQ, true>, dim3(units, items / 64), dim3(kJoinThreads), 0, s, a);
@@ -702,9 +720,16 @@ cudaError_t weights_t(const KvqAttnArgs &a, cudaStream_t s) {
   return kvq_launch(kvq_weights_kernel<HD, T, NQ>, dim3(a.wt0[a.n], a.c.n_kv), dim3(kWThreads), smem, s, a);
 }
 
+template <typename Sh>
+constexpr KvqShape shape_of() {
+  return {Sh::MB, Sh::NG};
+}
 template <int HD, typename T>
-int ctas_t(int nq) {
-  return nq == 1 ? Shape<HD, T, 1>::MB : nq == 2 ? Shape<HD, T, 2>::MB : nq == 3 ? Shape<HD, T, 3>::MB : Shape<HD, T, 4>::MB;
+KvqShape shape_t(int nq) {
+  return nq == 1   ? shape_of<Shape<HD, T, 1>>()
+         : nq == 2 ? shape_of<Shape<HD, T, 2>>()
+         : nq == 3 ? shape_of<Shape<HD, T, 3>>()
+                   : shape_of<Shape<HD, T, 4>>();
 }
 template <int HD, typename T>
 cudaError_t call_t(const KvqAttnArgs &a, bool weights, cudaStream_t s) {
@@ -726,10 +751,10 @@ cudaError_t kvq_attn_call(const KvqAttnArgs &a, bool weights, cudaStream_t s) {
   return call_t<HD, __nv_bfloat16>(a, weights, s);
 }
 template <int HD>
-int kvq_attn_ctas(int type, int nq) {
-  return type == KVQ_F32 ? ctas_t<HD, float>(nq) : type == KVQ_F16 ? ctas_t<HD, __half>(nq) : ctas_t<HD, __nv_bfloat16>(nq);
+KvqShape kvq_attn_shape(int type, int nq) {
+  return type == KVQ_F32 ? shape_t<HD, float>(nq) : type == KVQ_F16 ? shape_t<HD, __half>(nq) : shape_t<HD, __nv_bfloat16>(nq);
 }
 template cudaError_t kvq_attn_call<KVQ_HD>(const KvqAttnArgs &, bool, cudaStream_t);
-template int kvq_attn_ctas<KVQ_HD>(int, int);
+template KvqShape kvq_attn_shape<KVQ_HD>(int, int);
 
 }  // namespace fm
