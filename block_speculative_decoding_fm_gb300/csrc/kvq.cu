@@ -174,27 +174,29 @@ fm_status end(fm_kvq *c, cudaStream_t s) {
 }
 
 // Deals the launch's stages to at most `most` CTAs (what the SMs hold at once).  Equal shares balance best, but a share
-// that ends one unit and begins another pays for two (queries loaded, outputs written: as long as two or three stages).
-// Where the units are no more than the CTAs, give each CTAs of its own unless that makes the longest share that much
-// longer.  (16 rows of 16 heads over 4161 rows of 128: 14.3 us by equal shares, 9 us this way; 32 ragged sequences whose
-// longest would set the pace stay with equal shares.)
+// that ends one unit and begins another pays for two (queries loaded, outputs written: about kKvqUnitCost stages).
+// Where the units are no more than the CTAs, each gets CTAs of its own unless that makes the longest share that much
+// longer.  (16 rows of 16 heads over 4161 rows of 128: 14.3 us by equal shares, 10.3 us this way; 32 ragged sequences
+// whose longest would set the pace stay with equal shares.)
 void deal(KvqAttnArgs &a, int64_t most, int groups, int nkv, int unit_rows) {
   const int64_t W = a.st0[a.n];
   auto units = [&](int i) { return ((int64_t)a.rows[i] * a.group + unit_rows - 1) / unit_rows * nkv; };
   // (a CTA's groups take its stages in turn: fewer stages than groups leave some idle, and make more parts to join)
-  const int64_t wanted = (W + groups - 1) / groups;
+  const int64_t wanted = (W + groups + kKvqUnitCost - 1) / (groups + kKvqUnitCost);
   a.ctas = (int32_t)(wanted < most ? wanted : most);
   a.share = (int32_t)(W / a.ctas);
   a.extra = (int32_t)(W % a.ctas);
-  int64_t all = 0;
+  int64_t all = 0, stages = 0;
   int longest = 1;
   for (int i = 0; i < a.n; ++i) {
     all += units(i);
+    stages += units(i) * a.stages[i];
     if (a.rows[i] > 0 && a.stages[i] > longest) longest = a.stages[i];
   }
   if (all > most) return;
   // the least number of stages a CTA with which the CTAs suffice
-  int lo = a.share < groups ? groups : a.share, hi = longest < lo ? lo : longest;
+  const int even = (int)((stages + most - 1) / most);   // stages a CTA if they could be dealt out evenly
+  int lo = even < groups ? groups : even, hi = longest < lo ? lo : longest;
   while (lo < hi) {
     const int mid = lo + (hi - lo) / 2;
     int64_t n = 0;
@@ -204,7 +206,7 @@ void deal(KvqAttnArgs &a, int64_t most, int groups, int nkv, int unit_rows) {
     else
       lo = mid + 1;
   }
-  if (lo > a.share + 3 + a.share / 8) return;
+  if (lo > even + kKvqUnitCost + even / 8) return;
   a.share = 0;
   int ctas = 0;
   for (int i = 0; i < a.n; ++i) {
@@ -484,7 +486,7 @@ fm_status fm_kvq_attend(fm_kvq *c, int32_t layer, int32_t n_seqs, const int32_t 
     if (n < 0 || n > (1 << 16)) return kfail(c, FM_ERR_INVALID_ARG, "sequence %d: %d query rows", seq_ids_host[i], n);
     const int64_t units = ((int64_t)n * group + unit_rows - 1) / unit_rows * nkv;
     const int64_t stages = (len[seq_ids_host[i]] + stage_rows - 1) / stage_rows;
-    if (units > kMaxUnits || units * stages > INT_MAX)
+    if (units > kMaxUnits || units * (stages + kKvqUnitCost) > INT_MAX)
       return kfail(c, FM_ERR_UNSUPPORTED, "sequence %d: %d query rows of %d heads in one call", seq_ids_host[i], n, n_heads);
     total += n;
     if (n > 0 && len[seq_ids_host[i]] > most) most = len[seq_ids_host[i]];
@@ -530,7 +532,7 @@ fm_status fm_kvq_attend(fm_kvq *c, int32_t layer, int32_t n_seqs, const int32_t 
       const int rts = (int)(((int64_t)n * group + unit_rows - 1) / unit_rows);
       const int t1 = (L + kKvqTile - 1) / kKvqTile;
       const int s0 = first_row / stage_rows, s1 = (L + stage_rows - 1) / stage_rows, stages = s1 > s0 ? s1 - s0 : 1;
-      const int64_t more = (int64_t)rts * nkv * stages;
+      const int64_t more = (int64_t)rts * nkv * (stages + kKvqUnitCost);
       if (j && (units + (int64_t)rts * nkv > kMaxUnits || work + more > INT_MAX)) break;
       a.seq[j] = seq_ids_host[i];
       a.len[j] = L;

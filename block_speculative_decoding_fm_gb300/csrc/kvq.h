@@ -25,6 +25,9 @@ constexpr int kKvqTile = 64;       // rows a tile
 constexpr int kKvqSeqs = 64;       // sequences a launch
 // tiles a stage, what the attention kernel fetches and deals out (four warps' strips of 32 or 16 rows)
 __host__ __device__ constexpr int kvq_stage_tiles(int hd) { return hd == 256 ? 1 : 2; }
+// what beginning and ending a unit costs a CTA, in stages: a unit takes that many places before its stages' where shares
+// are dealt out, so that shares of many short units are as long as shares of one long one
+constexpr int kKvqUnitCost = 3;
 constexpr int kKvqMaxNQ = 4;       // a unit carries 8 nq query rows (block row x head of the group), nq <= 4
 
 enum KvqType : int32_t { KVQ_F32 = 0, KVQ_F16 = 1, KVQ_BF16 = 2 };
@@ -88,7 +91,7 @@ struct KvqAttnArgs {
   float scale_log2;       // scale * log2(e)
   int32_t causal, first;  // row t of T sees rows first <= j < (causal ? len - T + t + 1 : len)
   int32_t n;              // sequences of this launch
-  // CTAs of the launch, and their shares of the W = st0[n] stages.  share > 0: CTA b takes share = W / ctas, and one more
+  // CTAs of the launch, and their shares of the W = st0[n] places.  share > 0: CTA b takes share = W / ctas, and one more
   // where b < extra = W % ctas, whatever units they belong to.  share 0: a unit of sequence i has parts[i] CTAs of its own.
   int32_t ctas, share, extra;
   int32_t parts[kKvqSeqs];
@@ -105,7 +108,7 @@ struct KvqAttnArgs {
   int32_t seq[kKvqSeqs], len[kKvqSeqs], rows[kKvqSeqs];
   // A unit is a (KV head, tile of 8 nq query rows) of a sequence; its keys are stages, one at least.
   int32_t stages[kKvqSeqs];      // of a unit
-  int32_t st0[kKvqSeqs + 1];     // prefix sums of units x stages
+  int32_t st0[kKvqSeqs + 1];     // prefix sums of units x (kKvqUnitCost + stages)
   int32_t unit0[kKvqSeqs + 1];   // prefix sums of row tiles (lse is by (row tile, KV head))
   int32_t wt0[kKvqSeqs + 1];     // weights: prefix sums of the CTAs of each sequence
 };

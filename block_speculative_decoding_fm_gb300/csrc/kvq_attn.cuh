@@ -6,7 +6,7 @@
 // one pass over the cache with a running reference m and sum.  A unit is a
 // (sequence, KV head, 8 nq query rows), its keys stages of 128 rows (64 for head
 // dim 256).  Either a unit has CTAs of its own, or the units lie end to end and every CTA
-// takes an equal share of the stages (kvq.cu chooses); a second, short launch joins the parts of
+// takes an equal share of them (kvq.cu chooses); a second, short launch joins the parts of
 // units that several CTAs share, in their order.
 //
 // A CTA's warps work in groups of four with a ring of stages of their own (K and V codes and scales in one bulk
@@ -80,33 +80,36 @@ __device__ __forceinline__ void store4(T *p, float4 v) {
   }
 }
 
-// A CTA's share of the stages: [w_beg, w_end)
+// A CTA's share of the places: [w_beg, w_end)
 __device__ __forceinline__ void share_of(const KvqAttnArgs &a, int b, int &w_beg, int &w_end) {
   if (a.share) {
     w_beg = b * a.share + min(b, a.extra);
     w_end = w_beg + a.share + (b < a.extra);
   } else {
     const int i = find_seq<int32_t>(a.cta0, a.n, b), n = a.parts[i], S = a.stages[i];
-    const int unit = (b - a.cta0[i]) / n, p = b - a.cta0[i] - unit * n, u0 = a.st0[i] + unit * S;
+    const int unit = (b - a.cta0[i]) / n, p = b - a.cta0[i] - unit * n;
+    const int u0 = a.st0[i] + unit * (S + kKvqUnitCost) + kKvqUnitCost;   // the unit's first stage
     const int q = S / n, r = S - q * n;
     w_beg = u0 + p * q + min(p, r);
     w_end = w_beg + q + (p < r);
   }
 }
-// the CTA with a stage, shares equal
+// the CTA with a place, shares equal
 __device__ __forceinline__ int cta_of(const KvqAttnArgs &a, int stage) {
   const int wide = a.extra * (a.share + 1);
   return stage < wide ? stage / (a.share + 1) : a.extra + (stage - wide) / a.share;
 }
 
-// A stretch of a share: stages [s0, s0 + n) of one unit.
+// A stretch of a share: stages [s0, s0 + n) of one unit, `places` places long (n is 0 where they end before its stages).
 struct Stretch {
-  int i, head, rt, s0, n;
+  int i, head, rt, s0, n, places, u0;   // u0: the place of the unit's first stage
   __device__ __forceinline__ Stretch(const KvqAttnArgs &a, int at, int end) {
     i = find_seq<int32_t>(a.st0, a.n, at);
-    const int rel = at - a.st0[i], S = a.stages[i], unit = rel / S;
-    s0 = rel - unit * S;
-    n = min(S - s0, end - at);
+    const int rel = at - a.st0[i], V = a.stages[i] + kKvqUnitCost, unit = rel / V, r0 = rel - unit * V;
+    places = min(V - r0, end - at);
+    s0 = max(0, r0 - kKvqUnitCost);
+    n = max(0, r0 + places - kKvqUnitCost) - s0;
+    u0 = at - r0 + kKvqUnitCost;
     const int rts = (a.rows[i] * a.group + 8 * a.nq - 1) / (8 * a.nq);
     head = unit / rts;
     rt = unit - head * rts;
@@ -116,7 +119,7 @@ struct Stretch {
 // Where a group's copies have got to (in shared memory: one lane's business, once a stage).
 struct Cursor {
   const uint8_t *src;     // the next stage
-  int32_t at;             // the share's stage after the stretch that the cursor is in
+  int32_t at;             // the share's place after the stretch that the cursor is in
   int32_t left;           // stages of the stretch that are the group's
   int32_t issued;
 };
@@ -137,7 +140,7 @@ __device__ __forceinline__ bool issue_stage(const KvqAttnArgs &a, Cursor *cu, in
     const int t = min((a.first / (kKvqTile * Sh::KT) + x.s0 + grp) * Sh::KT, a.c.rows_pad / kKvqTile - Sh::KT);
     left = (x.n - grp + Sh::NG - 1) / Sh::NG;
     src = a.c.planes + ((size_t)a.seq[x.i] * a.c.n_kv + x.head) * a.c.plane_bytes + (size_t)t * TB;
-    cu->at = at + x.n;
+    cu->at = at + x.places;
   }
   const int g = cu->issued, slot = g % Sh::NS;
   if (g >= Sh::NS && !mbar_wait_bounded(empty + slot * 8, (g / Sh::NS - 1) & 1, a.c.err)) return false;
@@ -205,6 +208,8 @@ __global__ void __launch_bounds__(Shape<HD, T, NQ>::kThreads, Shape<HD, T, NQ>::
   uint32_t par = 0;
   for (int at = w_beg; at < w_end;) {
     const Stretch x(a, at, w_end);
+    at += x.places;
+    if (x.n == 0) continue;
     const int len = a.len[x.i], T_rows = a.rows[x.i], R = T_rows * a.group, rq = x.rt * RT;
     const size_t plane = (size_t)a.seq[x.i] * a.c.n_kv + x.head;
     load_q<HD, QS, NQ, NT>(static_cast<const T *>(a.q) + a.row0[x.i] * a.ldq + (int64_t)x.head * a.group * HD, a.ldq, a.group,
@@ -475,7 +480,6 @@ __global__ void __launch_bounds__(Shape<HD, T, NQ>::kThreads, Shape<HD, T, NQ>::
       else if (lse)
         lse[tid] = L == 0.f ? INFINITY : M + log2f(L) - range.bias;
     }
-    at += x.n;
     if (at < w_end) __syncthreads();   // the next stretch writes the queries, the references and the outputs' place
   }
   // nothing is left in flight when the CTA ends (a consumer may have given up)
@@ -526,19 +530,16 @@ template <int HD, typename T, int NQ, bool Many>
 __global__ void __launch_bounds__(kJoinThreads) kvq_join_kernel(const __grid_constant__ KvqAttnArgs a) {
   constexpr int RT = 8 * NQ, TX = Many ? 64 : kJoinThreads;
   pdl_trigger();
-  int at, first, last;   // a stage of the unit; the CTAs that have parts of it
+  int at, first, last;   // a place of the unit; the CTAs that have parts of it
   if (Many) {
     const int i = find_seq<int32_t>(a.unit0, a.n, (int)blockIdx.x / a.c.n_kv), unit = (int)blockIdx.x - a.unit0[i] * a.c.n_kv;
-    at = a.st0[i] + unit * a.stages[i];
+    at = a.st0[i] + unit * (a.stages[i] + kKvqUnitCost);
     if (!a.share) first = a.cta0[i] + unit * a.parts[i], last = first + a.parts[i] - 1;
   } else {
     at = (blockIdx.x + 1) * a.share + min((int)blockIdx.x + 1, a.extra);
   }
   const Stretch x(a, at, a.st0[a.n]);
-  if (!Many || a.share) {
-    const int u0 = at - x.s0;
-    first = cta_of(a, u0), last = cta_of(a, u0 + a.stages[x.i] - 1);
-  }
+  if (!Many || a.share) first = cta_of(a, x.u0), last = cta_of(a, x.u0 + a.stages[x.i] - 1);
   pdl_wait();   // every block, so that a later launch that waits for this one waits for what came before too
   if (first == last || (!Many && first != (int)blockIdx.x)) return;
   const int q = Many ? threadIdx.x >> 6 : 0, e = blockIdx.y * TX + threadIdx.x % TX;
@@ -704,7 +705,7 @@ cudaError_t attend_t(const KvqAttnArgs &a, cudaStream_t s) {
   e = kvq_launch(kvq_attend_kernel<HD, T, NQ>, dim3(a.ctas), dim3(Sh::kThreads), Sh::kBytes, s, a);
   // nothing to join where every share is a unit
   bool whole = a.extra == 0 || a.share == 0;
-  for (int i = 0; i < a.n; ++i) whole = whole && (a.rows[i] == 0 || (a.share ? a.stages[i] == a.share : a.parts[i] == 1));
+  for (int i = 0; i < a.n; ++i) whole = whole && (a.rows[i] == 0 || (a.share ? a.stages[i] + kKvqUnitCost == a.share : a.parts[i] == 1));
   if (e != cudaSuccess || whole) return e;
   const int units = a.unit0[a.n] * a.c.n_kv, items = 8 * NQ * HD / 4;
   if (units <= a.ctas) return kvq_launch(kvq_join_kernel<HD, T, NQ, true>, dim3(units, items / 64), dim3(kJoinThreads), 0, s, a);
