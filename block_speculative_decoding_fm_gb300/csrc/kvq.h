@@ -27,7 +27,7 @@ constexpr int kKvqSeqs = 64;       // sequences a launch
 __host__ __device__ constexpr int kvq_stage_tiles(int hd) { return hd == 256 ? 1 : 2; }
 // what beginning and ending a unit costs a CTA, in stages: a unit takes that many places before its stages' where shares
 // are dealt out, so that shares of many short units are as long as shares of one long one
-constexpr int kKvqUnitCost = 3;
+constexpr int kKvqUnitCost = 4;
 constexpr int kKvqMaxNQ = 4;       // a unit carries 8 nq query rows (block row x head of the group), nq <= 4
 
 enum KvqType : int32_t { KVQ_F32 = 0, KVQ_F16 = 1, KVQ_BF16 = 2 };
