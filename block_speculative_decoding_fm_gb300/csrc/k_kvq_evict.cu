@@ -17,6 +17,7 @@
 
 #include "dev_common.cuh"
 #include "kvq.h"
+#include "kvq_load.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -212,9 +213,9 @@ struct Mover {
 #pragma unroll
     for (int q = 0; q < kItems; ++q) {
       const int r = r0 + (q * NT + tid) / (2 * U);
-      row[q] = r < left ? __ldcg(list + r) : -1;
+      row[q] = r < left ? (int)ldg32(list + r) : -1;
     }
-    const int mine = tid < RB && r0 + tid < left ? __ldcg(list + r0 + tid) : -1;
+    const int mine = tid < RB && r0 + tid < left ? (int)ldg32(list + r0 + tid) : -1;
 #pragma unroll
     for (int q = 0; q < kItems; ++q) {
       const int u = (q * NT + tid) % (2 * U);

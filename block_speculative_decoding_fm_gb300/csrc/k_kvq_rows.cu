@@ -26,6 +26,7 @@
 
 #include "dev_common.cuh"
 #include "kvq.h"
+#include "kvq_load.cuh"
 
 namespace fm {
 namespace {
@@ -41,13 +42,6 @@ __device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either 
   return y;
 }
 
-// 32 bytes at a time
-__device__ __forceinline__ void ldg32(const void *p, uint32_t (&w)[8]) {
-  asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
-               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
-               : "l"(p));
-}
-
 // Sixteen consecutive values of a row.
 template <typename T>
 struct Sixteen {
@@ -58,11 +52,11 @@ struct Sixteen {
     for (int i = 0; i < W; i += 8) {
       if (whole) {
         uint32_t v[8];
-        ldg32(reinterpret_cast<const uint32_t *>(p) + i, v);
+        ldg256(reinterpret_cast<const uint32_t *>(p) + i, v);
 #pragma unroll
         for (int k = 0; k < 8; ++k) w[i + k] = v[k];
       } else {
-        const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p) + i / 4), v = __ldg(reinterpret_cast<const uint4 *>(p) + i / 4 + 1);
+        const uint4 u = ldg128(reinterpret_cast<const uint4 *>(p) + i / 4), v = ldg128(reinterpret_cast<const uint4 *>(p) + i / 4 + 1);
         w[i] = u.x, w[i + 1] = u.y, w[i + 2] = u.z, w[i + 3] = u.w;
         w[i + 4] = v.x, w[i + 5] = v.y, w[i + 6] = v.z, w[i + 7] = v.w;
       }
@@ -103,8 +97,8 @@ template <>
 struct Eight<float> {
   float4 a, b;
   __device__ __forceinline__ void load(const float *p) {
-    a = __ldg(reinterpret_cast<const float4 *>(p));
-    b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+    a = ldg128f(p);
+    b = ldg128f(p + 4);
   }
   __device__ __forceinline__ void get(float (&x)[8]) const {
     x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
@@ -117,7 +111,7 @@ struct Eight<float> {
 template <>
 struct Eight<__half> {
   uint4 a;
-  __device__ __forceinline__ void load(const __half *p) { a = __ldg(reinterpret_cast<const uint4 *>(p)); }
+  __device__ __forceinline__ void load(const __half *p) { a = ldg128(p); }
   __device__ __forceinline__ void get(float (&x)[8]) const {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -139,7 +133,7 @@ struct Eight<__half> {
 template <>
 struct Eight<__nv_bfloat16> {
   uint4 a;
-  __device__ __forceinline__ void load(const __nv_bfloat16 *p) { a = __ldg(reinterpret_cast<const uint4 *>(p)); }
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p) { a = ldg128(p); }
   __device__ __forceinline__ void get(float (&x)[8]) const {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {

@@ -125,23 +125,28 @@ struct Cursor {
 };
 static_assert(sizeof(Cursor) <= 32, "a cursor's place in shared memory");
 
+// the group's next stage, from where its stretch is used up; false where there is none
+template <int HD, typename Sh>
+__device__ __forceinline__ bool find_stage(const KvqAttnArgs &a, Cursor *cu, int w_end, int grp) {
+  while (cu->left == 0) {
+    const int at = cu->at;
+    if (at >= w_end) return false;
+    const Stretch x(a, at, w_end);
+    // (a unit that sees no rows has one stage, whatever is there: every score of it is masked)
+    const int t = min((a.first / (kKvqTile * Sh::KT) + x.s0 + grp) * Sh::KT, a.c.rows_pad / kKvqTile - Sh::KT);
+    cu->left = (x.n - grp + Sh::NG - 1) / Sh::NG;
+    cu->src = a.c.planes + ((size_t)a.seq[x.i] * a.c.n_kv + x.head) * a.c.plane_bytes + (size_t)t * kvq_tile_bytes(HD);
+    cu->at = at + x.places;
+  }
+  return true;
+}
 // The next of the group's stages into its ring; false where a wait gave up.
 template <int HD, typename Sh>
 __device__ __forceinline__ bool issue_stage(const KvqAttnArgs &a, Cursor *cu, int w_end, int grp, uint32_t ring,
                                             uint32_t full, uint32_t empty) {
-  constexpr int TB = kvq_tile_bytes(HD);
-  int left = cu->left;
+  if (!find_stage<HD, Sh>(a, cu, w_end, grp)) return true;
   const uint8_t *src = cu->src;
-  while (left == 0) {
-    const int at = cu->at;
-    if (at >= w_end) return true;
-    const Stretch x(a, at, w_end);
-    // (a unit that sees no rows has one stage, whatever is there: every score of it is masked)
-    const int t = min((a.first / (kKvqTile * Sh::KT) + x.s0 + grp) * Sh::KT, a.c.rows_pad / kKvqTile - Sh::KT);
-    left = (x.n - grp + Sh::NG - 1) / Sh::NG;
-    src = a.c.planes + ((size_t)a.seq[x.i] * a.c.n_kv + x.head) * a.c.plane_bytes + (size_t)t * TB;
-    cu->at = at + x.places;
-  }
+  const int left = cu->left;
   const int g = cu->issued, slot = g % Sh::NS;
   if (g >= Sh::NS && !mbar_wait_bounded(empty + slot * 8, (g / Sh::NS - 1) & 1, a.c.err)) return false;
   mbar_expect_tx(full + slot * 8, Sh::SB);
@@ -180,22 +185,25 @@ __global__ void __launch_bounds__(Shape<HD, T, NQ>::kThreads, Shape<HD, T, NQ>::
   int w_beg, w_end;
   share_of(a, blockIdx.x, w_beg, w_end);
 
-  pdl_trigger();
+  // what comes of the arguments alone is done before the wait
   if (tid == 0) {
 #pragma unroll
     for (int s = 0; s < NG * 2 * NS; ++s) mbar_init(smem_u32(bar + s), s / NS & 1 ? 4 : 1);
     mbar_fence_init();
   }
-  __syncthreads();
-  pdl_wait();
   const bool copies = lane == 0 && wq == 0;   // the lane that sends for its group's stages
   bool ok = true;
   if (copies) {
     cu->at = w_beg;
     cu->left = 0;
     cu->issued = 0;
-    for (int k = 0; k < NS - 1; ++k) ok = issue_stage<HD, Sh>(a, cu, w_end, grp, ring, full, empty);
+    find_stage<HD, Sh>(a, cu, w_end, grp);
   }
+  __syncthreads();
+  pdl_wait();
+  pdl_trigger();   // (after the wait: whoever starts behind this launch finds what came before it done)
+  if (copies)
+    for (int k = 0; k < NS - 1; ++k) ok = issue_stage<HD, Sh>(a, cu, w_end, grp, ring, full, empty);
 
   // first product: this warp's strip; second: its groups of dims gw, gw + 4 over the 32-row blocks kp, kp + KP, ...
   const int strip = wq * KS;
@@ -212,9 +220,10 @@ __global__ void __launch_bounds__(Shape<HD, T, NQ>::kThreads, Shape<HD, T, NQ>::
     if (x.n == 0) continue;
     const int len = a.len[x.i], T_rows = a.rows[x.i], R = T_rows * a.group, rq = x.rt * RT;
     const size_t plane = (size_t)a.seq[x.i] * a.c.n_kv + x.head;
+    const uint32_t vm = ldg32(a.c.vmax + plane);
     load_q<HD, QS, NQ, NT>(static_cast<const T *>(a.q) + a.row0[x.i] * a.ldq + (int64_t)x.head * a.group * HD, a.ldq, a.group,
                            rq, R, a.scale_log2, qs, tid);
-    const PRange range(__ldcg(a.c.vmax + plane));
+    const PRange range(vm);
     __syncthreads();
     const int lim_all = a.causal ? len - T_rows + rq / a.group + 1 : len;   // the rows that every query row sees end here
 
@@ -506,8 +515,8 @@ struct Joined {
       for (int k = 0; k < NB; ++k) {
         const int p = min(c + k, c1);
         const size_t slot = (size_t)p * 2 + (p == first);
-        ml[k] = __ldcg(&a.part_ml[slot * RT + r]);
-        v[k] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + (slot * RT + r) * HD + d));
+        ml[k] = ldg64f(&a.part_ml[slot * RT + r]);
+        v[k] = ldg128f(a.part_o + (slot * RT + r) * HD + d);
       }
 #pragma unroll
       for (int k = 0; k < NB; ++k) {
@@ -561,7 +570,7 @@ __global__ void __launch_bounds__(kJoinThreads) kvq_join_kernel(const __grid_con
     if (!mine) return;
     j.add<2>(a, RT, HD, r, d, first, last, first);
   }
-  const PRange range(__ldcg(a.c.vmax + (size_t)a.seq[x.i] * a.c.n_kv + x.head));
+  const PRange range(ldg32(a.c.vmax + (size_t)a.seq[x.i] * a.c.n_kv + x.head));
   const float inv = j.L == 0.f ? 0.f : range.undo / j.L;
   const int t = qr / a.group;
   store4(static_cast<T *>(a.out) + (a.row0[x.i] + t) * a.ldo + ((int64_t)x.head * a.group + qr - t * a.group) * HD + d,
@@ -590,7 +599,6 @@ __global__ void __launch_bounds__(kWThreads) kvq_weights_kernel(const __grid_con
   const int nt = min(a.wtiles, (len + kKvqTile - 1) / kKvqTile - t0), np = (nt + 1) / 2;
   const size_t plane = (size_t)a.seq[i] * a.c.n_kv + head;
   pdl_trigger();
-  pdl_wait();
   const uint8_t *src = a.c.planes + plane * a.c.plane_bytes + (size_t)t0 * kvq_tile_bytes(HD);
   auto fetch = [&](int p) {   // the K halves of pair p
     if (p < np)
@@ -607,6 +615,11 @@ __global__ void __launch_bounds__(kWThreads) kvq_weights_kernel(const __grid_con
     if (rt) __syncthreads();
 #pragma unroll
     for (int p = 0; p < kWSlots - 1; ++p) fetch(p);
+    load_q<HD, QS, NQ, kWThreads>(static_cast<const T *>(a.q) + a.row0[i] * a.ldq + (int64_t)head * a.group * HD, a.ldq,
+                                  a.group, rt * RT, R, a.scale_log2, qs, tid);
+    // The attention has begun everywhere before this launch begins, and lets nothing begin before what came ahead of it
+    // is done: rows and queries are there already, its sums and the weights are what is waited for.
+    if (rt == 0) pdl_wait();
     const float *lse = a.lse + ((size_t)(a.unit0[i] + rt) * a.c.n_kv + head) * RT;
     float ls[NQ][2];
 #pragma unroll
@@ -614,10 +627,8 @@ __global__ void __launch_bounds__(kWThreads) kvq_weights_kernel(const __grid_con
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int r = 8 * n + 2 * c + h;
-        ls[n][h] = rt * RT + r < R ? __ldcg(lse + r) : INFINITY;
+        ls[n][h] = rt * RT + r < R ? __uint_as_float(ldg32(lse + r)) : INFINITY;
       }
-    load_q<HD, QS, NQ, kWThreads>(static_cast<const T *>(a.q) + a.row0[i] * a.ldq + (int64_t)head * a.group * HD, a.ldq,
-                                  a.group, rt * RT, R, a.scale_log2, qs, tid);
     __syncthreads();
     const int lim_all = a.causal ? len - T_rows + rt * RT / a.group + 1 : len;
     float mu[NQ][2];

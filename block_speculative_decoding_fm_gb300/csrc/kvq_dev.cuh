@@ -13,6 +13,7 @@
 
 #include "dev_common.cuh"
 #include "kvq.h"
+#include "kvq_load.cuh"
 
 namespace fm {
 namespace kvq {
@@ -83,10 +84,10 @@ __device__ __forceinline__ float2 pair_f32(uint32_t w) { return __half22float2(*
 template <typename T>
 __device__ __forceinline__ void load8(const T *p, float (&x)[8]) {
   if constexpr (sizeof(T) == 4) {
-    const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+    const float4 a = ldg128f(reinterpret_cast<const float *>(p)), b = ldg128f(reinterpret_cast<const float *>(p) + 4);
     x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
   } else {
-    const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p));
+    const uint4 v = ldg128(p);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t w = word(v, i);
