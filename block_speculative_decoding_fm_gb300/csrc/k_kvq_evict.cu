@@ -5,10 +5,12 @@
 //
 // Two launches:
 //   select   one CTA a plane, or a cluster of eight: the weight of rank keep - recent by
-//            radix selection on the ordered bits, eight at a time, then the rows that stay are listed in their order, a run of rows a warp (scans, no
-//            atomics whose order could show);
+//            radix selection on the ordered bits, eight at a time, then the rows that stay
+//            are listed in their order, a run of rows a warp (scans, no atomics whose order
+//            could show);
 //   move     16 bytes of codes and their scale an item.  Into another sequence, CTAs
-//            of 64 rows and a plane each, all over the GPU.  In place, a cluster of eight CTAs a plane
+//            of 64 rows and a plane each, all over the GPU (512 planes, 2048 rows of 128
+//            kept in each: 52 us, 5.9 TB/s).  In place, a cluster of eight CTAs a plane
 //            goes through the rows in rounds: a kept row never moves up, so the rows that a round
 //            writes lie below every row that a later round reads, and a cluster barrier
 //            between a round's loads and its stores is all that is needed.
@@ -25,8 +27,9 @@ namespace fm {
 namespace {
 
 constexpr int kThreads = 512;    // in place
-constexpr int kCopies = 8;
+constexpr int kCopies = 8; 
 constexpr int kMoveThreads = 256;
+constexpr int kSelectRoom = 90 * 1024;   // bytes of keys in shared memory, where planes are few
 constexpr int kCluster = 8;      // in place; select, where planes are few
 constexpr int kItems = 4;        // 16-byte units a thread moves a round
 
@@ -55,17 +58,24 @@ __device__ __forceinline__ int block_scan(int v, int *red) {
   return base + x - v;
 }
 
-// A plane's rows over CS CTAs (a cluster of eight where planes are few), an equal run of rows each.  Histograms of 8-bit digits
-// are kept in eight copies, a lane's by its number: the weights of a plane crowd into few bins, and the same
-// address from many lanes is what shared-memory atomics are slow at (one copy of 2048 bins in one CTA: 75 us
-// for four planes of 65535 rows).
+// rows a warp's run has, whole turns of 128: nc rows over `warps`
+__host__ __device__ inline int select_run(int nc, int warps) { return (nc + warps * 128 - 1) / (warps * 128) * 128; }
+
+// A plane's rows over CS CTAs (a cluster of eight where planes are few), an equal run of rows a warp.  Histograms of 8-bit
+// digits are kept in eight copies, a lane's by its number and a bin's copies side by side: weights crowd into few bins, and
+// lanes that meet in a bank go one after the other.  A pass over few planes costs its waits: the first one reads the
+// weights, and where they fit (cached) every later one has them from shared memory, in the thread that put them there.
+// With many planes other CTAs fill the waits, and shared memory taken from L1 made the launches around this one slower.
+// The passes end early where all of the selected bin stay, for distinct weights after three mostly.
+// (512 planes of 512 to 8192 rows: 18 us; 4 of 65535 rows: 15 us, 18 without the cache.)
 template <int CS>
-__global__ void __launch_bounds__(CS == 1 ? 256 : 512, CS == 1 ? 6 : 3) kvq_select_kernel(const __grid_constant__ KvqEvictArgs a) {
+__global__ void __launch_bounds__(CS == 1 ? 256 : 512, CS == 1 ? 4 : 2) kvq_select_kernel(const __grid_constant__ KvqEvictArgs a, bool cached) {
   constexpr int NT = CS == 1 ? 256 : 512, NWarp = NT / 32;
-  __shared__ int hist[kCopies][256];
-  __shared__ int bins[256];
+  extern __shared__ __align__(16) uint32_t s_keys[];   // [warp][per], where cached
+  __shared__ __align__(16) int hist[256 * kCopies];
+  __shared__ int bins[2][256];                         // (two: a CTA may still read the last pass's)
   __shared__ int red[NWarp];
-  __shared__ int s_found[2];
+  __shared__ int s_found[3];
   __shared__ int2 s_cnt[NWarp];
   __shared__ int2 s_all;
   cg::cluster_group cl = cg::this_cluster();
@@ -80,12 +90,6 @@ __global__ void __launch_bounds__(CS == 1 ? 256 : 512, CS == 1 ? 6 : 3) kvq_sele
     list[pos] = row;
     if (kept) kept[pos] = row;
   };
-  auto sync = [&]() {
-    if (CS > 1)
-      cl.sync();
-    else
-      __syncthreads();
-  };
   if (len <= a.keep) {
     for (int r = rank * NT + tid; r < len; r += CS * NT) put(r, r);
     return;
@@ -94,11 +98,20 @@ __global__ void __launch_bounds__(CS == 1 ? 256 : 512, CS == 1 ? 6 : 3) kvq_sele
   for (int r = rank * NT + tid; r < a.recent; r += CS * NT) put(m + r, nc + r);
   if (m == 0) return;
   // a warp's run of rows; four rows' keys (a plane's rows are padded to 64)
-  const int per = (nc + CS * NWarp * 128 - 1) / (CS * NWarp * 128) * 128;
+  const int per = select_run(nc, CS * NWarp);
   const int r_beg = (rank * NWarp + w) * per, r_end = min(nc, r_beg + per);
-  auto keys = [&](int r, uint32_t (&k)[4]) {
+  uint32_t *mine = s_keys + w * per - r_beg;
+  auto read = [&](int r, uint32_t (&k)[4]) {
     const float4 v = *reinterpret_cast<const float4 *>(ws + r);
     k[0] = ordered(v.x), k[1] = ordered(v.y), k[2] = ordered(v.z), k[3] = ordered(v.w);
+  };
+  auto keys = [&](int r, uint32_t (&k)[4]) {
+    if (CS > 1 && cached) {
+      const uint4 v = *reinterpret_cast<const uint4 *>(mine + r);
+      k[0] = v.x, k[1] = v.y, k[2] = v.z, k[3] = v.w;
+    } else {
+      read(r, k);
+    }
   };
   uint32_t prefix = 0;   // the selected weight's leading bits
   int want = m;          // its rank among the rows that share them
@@ -106,37 +119,56 @@ __global__ void __launch_bounds__(CS == 1 ? 256 : 512, CS == 1 ? 6 : 3) kvq_sele
   for (int shift = 24; shift >= 0; shift -= 8) {
     for (int x = tid; x < 256 * kCopies / 4; x += NT) reinterpret_cast<int4 *>(hist)[x] = make_int4(0, 0, 0, 0);
     __syncthreads();
+    int *h = hist + lane % kCopies;
+    if (shift == 24) {
 #pragma unroll 4
-    for (int r = r_beg + 4 * lane; r < r_end; r += 128) {
-      uint32_t k[4];
-      keys(r, k);
+      for (int r = r_beg + 4 * lane; r < r_end; r += 128) {
+        uint32_t k[4];
+        read(r, k);
+        if (CS > 1 && cached) *reinterpret_cast<uint4 *>(mine + r) = make_uint4(k[0], k[1], k[2], k[3]);
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (r + q < r_end && (shift == 24 || (k[q] >> (shift + 8)) == prefix)) atomicAdd(&hist[lane % kCopies][(k[q] >> shift) & 255], 1);
+        for (int q = 0; q < 4; ++q)
+          if (r + q < r_end) atomicAdd(h + (k[q] >> 24) * kCopies, 1);
+      }
+    } else {
+#pragma unroll 4
+      for (int r = r_beg + 4 * lane; r < r_end; r += 128) {
+        uint32_t k[4];
+        keys(r, k);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (r + q < r_end && (k[q] >> (shift + 8)) == prefix) atomicAdd(h + ((k[q] >> shift) & 255) * kCopies, 1);
+      }
     }
     __syncthreads();
-    if (tid < 256) {
-      int n = 0;
-#pragma unroll
-      for (int c = 0; c < kCopies; ++c) n += hist[c][tid];
-      bins[tid] = n;
-    }
-    sync();
     // bins from the top: thread t has bin 255 - t, of all CTAs
-    int n = 0;
+    int n = 0, *b = bins[shift >> 3 & 1];
     if (tid < 256) {
-      if (CS > 1) {
 #pragma unroll
-        for (int c = 0; c < CS; ++c) n += *cl.map_shared_rank(&bins[255 - tid], c);
-      } else {
-        n = bins[255 - tid];
+      for (int c = 0; c < kCopies; c += 4) {   // (lanes begin at different copies: their banks differ)
+        const int4 v = *reinterpret_cast<const int4 *>(hist + (255 - tid) * kCopies + (c + 4 * (tid / (32 / kCopies))) % kCopies);
+        n += (v.x + v.y) + (v.z + v.w);
+      }
+      if (CS > 1) b[tid] = n;
+    }
+    if (CS > 1) {
+      cl.sync();
+      if (tid < 256) {
+        n = 0;
+#pragma unroll
+        for (int c = 0; c < CS; ++c) n += *cl.map_shared_rank(b + tid, c);
       }
     }
     const int before = block_scan<NT>(n, red);
-    if (before < want && before + n >= want) s_found[0] = 255 - tid, s_found[1] = want - before;
-    sync();   // (the counts have been read)
+    if (before < want && before + n >= want) s_found[0] = 255 - tid, s_found[1] = want - before, s_found[2] = n;
+    __syncthreads();
     prefix = (prefix << 8) | (uint32_t)s_found[0];
     want = s_found[1];
+    if (want == s_found[2]) {   // all of the bin stay: whatever is above what lies below it (they are not all rows)
+      prefix = (prefix << shift) - 1u;
+      want = 0;
+      break;
+    }
   }
   // Rows above the selected weight stay, and the first `want` that equal it: a warp counts both kinds in its run,
   // and with the counts before it writes its own, in order.
@@ -289,9 +321,18 @@ cudaError_t evict_hd(const KvqEvictArgs &a, cudaStream_t s) {
   const int planes = a.n * a.c.n_kv;
   cudaError_t e;
   if (planes * kCluster <= 320) {
+    // (two CTAs an SM; longer planes are read again in each pass)
+    int longest = 0;
+    for (int i = 0; i < a.n; ++i) longest = a.len[i] > longest ? a.len[i] : longest;
+    const int bytes = select_run(longest, kCluster * 16) * 16 * 4;
+    const bool cached = bytes <= kSelectRoom;
+    static std::atomic<uint64_t> done{0};
+    e = allow_smem(kvq_select_kernel<kCluster>, kSelectRoom, done);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(planes * kCluster);
     cfg.blockDim = dim3(512);
+    cfg.dynamicSmemBytes = cached ? bytes : 0;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -302,9 +343,9 @@ cudaError_t evict_hd(const KvqEvictArgs &a, cudaStream_t s) {
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     ++kvq_launches();
-    e = cudaLaunchKernelEx(&cfg, kvq_select_kernel<kCluster>, a);
+    e = cudaLaunchKernelEx(&cfg, kvq_select_kernel<kCluster>, a, cached);
   } else {
-    e = kvq_launch(kvq_select_kernel<1>, dim3(planes), dim3(256), 0, s, a);
+    e = kvq_launch(kvq_select_kernel<1>, dim3(planes), dim3(256), 0, s, a, false);
   }
   int most = 0;   // rows that go to another sequence
   bool same = false;

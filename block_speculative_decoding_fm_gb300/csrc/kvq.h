@@ -16,6 +16,7 @@
 #pragma once
 
 #include <cstddef>
+#include <atomic>
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -135,6 +136,19 @@ struct KvqEvictArgs {
 cudaError_t launch_kvq_evict(const KvqEvictArgs &a, int hd, cudaStream_t s);
 
 int &kvq_launches();   // this thread's launches since a call began
+
+// lets a kernel have its dynamic shared memory, once a device (done: a bit a device)
+template <typename K>
+inline cudaError_t allow_smem(K kern, int bytes, std::atomic<uint64_t> &done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 template <typename K, typename... Args>
 inline cudaError_t kvq_launch(K kern, dim3 grid, dim3 block, size_t smem, cudaStream_t s, const Args &...args) {

@@ -693,19 +693,6 @@ __global__ void __launch_bounds__(kWThreads) kvq_weights_kernel(const __grid_con
   }
 }
 
-// lets a kernel have its dynamic shared memory, once a device (done: a bit a device)
-template <typename K>
-cudaError_t allow_smem(K kern, int bytes, std::atomic<uint64_t> &done) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = 1ull << (dev & 63);
-  if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-  return e;
-}
-
 template <int HD, typename T, int NQ>
 cudaError_t attend_t(const KvqAttnArgs &a, cudaStream_t s) {
   using Sh = Shape<HD, T, NQ>;
