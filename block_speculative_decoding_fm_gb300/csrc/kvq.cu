@@ -173,6 +173,31 @@ fm_status end(fm_kvq *c, cudaStream_t s) {
   return FM_OK;
 }
 
+// The octets of query rows that a unit carries, 0 where the call has too many units.  A stage costs about 1 + nq (its codes
+// are unpacked once, then used for each octet), beginning and ending a unit 5 nq (9 nq for 256 dims) of the same: short
+// caches want many narrow units, long ones few wide ones.  (8 rows of 24 heads over 4 KV heads of 256, f32: 64 rows 4.9 us
+// with nq 1, 9.3 with 3; 16384 rows 32.4 and 30.1.  16 rows of 16 heads of 128, bf16: 4161 rows 9.7 us with nq 1, 10.0 with
+// 2; 16384 rows 18.9 and 16.7.)
+int choose_nq(int n_seqs, const int32_t *seq, const int32_t *rows, const int32_t *len, int group, int nkv, int hd, int n_sm,
+              int64_t widest) {
+  const int stage_rows = kKvqTile * kvq_stage_tiles(hd), most = (int)(widest < 8 * kKvqMaxNQ ? (widest + 7) / 8 : kKvqMaxNQ);
+  int best = 0;
+  int64_t least = 0;
+  for (int nq = 1; nq <= most; ++nq) {
+    int64_t work = 0;
+    bool fits = true;
+    for (int i = 0; i < n_seqs; ++i) {
+      const int64_t units = ((int64_t)rows[i] * group + 8 * nq - 1) / (8 * nq) * nkv;
+      const int stages = (len[seq[i]] + stage_rows - 1) / stage_rows;
+      fits = fits && units <= kMaxUnits && units * (stages + kKvqUnitCost) <= INT_MAX;
+      work += units * stages;
+    }
+    const int64_t cost = (int64_t)nq * (hd == 256 ? 9 : 5) * n_sm + work * (1 + nq);
+    if (fits && (!best || cost < least)) best = nq, least = cost;
+  }
+  return best;
+}
+
 // Deals the launch's stages to at most `most` CTAs (what the SMs hold at once).  Equal shares balance best, but a share
 // that ends one unit and begins another pays for two (queries loaded, outputs written: about kKvqUnitCost stages).
 // Where the units are no more than the CTAs, each gets CTAs of its own unless that makes the longest share that much
@@ -477,20 +502,15 @@ fm_status fm_kvq_attend(fm_kvq *c, int32_t layer, int32_t n_seqs, const int32_t 
     const int64_t r = (int64_t)n_rows_host[i] * group;
     widest = r > widest ? r : widest;
   }
-  // query rows of a unit: all of them up to 32, so that the codes are unpacked once; else tiles of about equal size
-  const int64_t row_tiles = (widest + 8 * kKvqMaxNQ - 1) / (8 * kKvqMaxNQ);
-  const int nq = (int)((widest + 8 * row_tiles - 1) / (8 * row_tiles)), unit_rows = 8 * nq;
   const int stage_rows = kKvqTile * kvq_stage_tiles(hd);
   for (int i = 0; i < n_seqs; ++i) {
     const int n = n_rows_host[i];
     if (n < 0 || n > (1 << 16)) return kfail(c, FM_ERR_INVALID_ARG, "sequence %d: %d query rows", seq_ids_host[i], n);
-    const int64_t units = ((int64_t)n * group + unit_rows - 1) / unit_rows * nkv;
-    const int64_t stages = (len[seq_ids_host[i]] + stage_rows - 1) / stage_rows;
-    if (units > kMaxUnits || units * (stages + kKvqUnitCost) > INT_MAX)
-      return kfail(c, FM_ERR_UNSUPPORTED, "sequence %d: %d query rows of %d heads in one call", seq_ids_host[i], n, n_heads);
     total += n;
     if (n > 0 && len[seq_ids_host[i]] > most) most = len[seq_ids_host[i]];
   }
+  const int nq = choose_nq(n_seqs, seq_ids_host, n_rows_host, len, group, nkv, hd, c->n_sm, widest), unit_rows = 8 * nq;
+  if (!nq) return kfail(c, FM_ERR_UNSUPPORTED, "%lld query rows of a KV head in one call", (long long)widest);
   const int64_t width = (int64_t)n_heads * hd;
   if (total > 0) {
     KTRY(check_rows(c, "q", q_dev, ldq, width, size));
