@@ -40,8 +40,10 @@ struct fm_kvq {
   std::vector<uint32_t> mark;     // [seqs] the last call that named a sequence (as a destination)
   uint32_t call = 0;
   cudaEvent_t done = nullptr;     // the last eager call's work
-  cudaStream_t last = nullptr;
+  unsigned long long last = 0;    // its stream's id (a handle may come back as another stream's)
   bool has_last = false;
+  unsigned long long stream = 0;  // this call's
+  bool eager = true;              // it is not captured
   int launches = 0;               // kernels that the last call launched
   char err[512] = "";
 };
@@ -160,15 +162,18 @@ bool capturing(cudaStream_t s) {
 
 fm_status begin(fm_kvq *c, cudaStream_t s) {
   kvq_launches() = 0;
-  if (c->has_last && c->last != s && !capturing(s)) KCK(cudaStreamWaitEvent(s, c->done, 0));
+  c->eager = !capturing(s);
+  if (!c->eager) return FM_OK;
+  KCK(cudaStreamGetId(s, &c->stream));
+  if (c->has_last && c->stream != c->last) KCK(cudaStreamWaitEvent(s, c->done, 0));
   return FM_OK;
 }
 
 fm_status end(fm_kvq *c, cudaStream_t s) {
   c->launches = kvq_launches();
-  if (capturing(s)) return FM_OK;
+  if (!c->eager) return FM_OK;
   KCK(cudaEventRecord(c->done, s));
-  c->last = s;
+  c->last = c->stream;
   c->has_last = true;
   return FM_OK;
 }
@@ -670,8 +675,18 @@ const char *fm_kvq_last_error(const fm_kvq *c) { return c ? c->err : g_kvq_error
 
 void fm_kvq_destroy(fm_kvq *c) {
   if (!c) return;
-  cudaDeviceSynchronize();
+  // On the cache's device; and a capture that this thread may be in goes on (a Python object may be collected any time),
+  // which a synchronisation of the device would end.  (Freeing waits for what runs, graphs too.)
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  int dev = -1;
+  cudaThreadExchangeStreamCaptureMode(&mode);
+  cudaGetDevice(&dev);
+  const int own = c->device;
+  if (dev != own) cudaSetDevice(own);
+  if (c->has_last) cudaEventSynchronize(c->done);
   release(c);
+  if (dev != own) cudaSetDevice(dev);
+  cudaThreadExchangeStreamCaptureMode(&mode);
 }
 
 }  // extern "C"

@@ -556,8 +556,8 @@ FM_API void fm_mtp_destroy(fm_mtp *m);
  * the call at the lengths it was captured with.  Eager calls on different
  * streams are put in the order they were issued in (they share a workspace
  * and the weights); a captured call is not, so graphs that use one cache are
- * replayed one after another, and ordered with eager calls, by the caller.
- * The cache's device must be the current device.  Device pointers are 16-byte
+ * replayed one after another, and ordered with eager calls, by the caller, and
+ * not after fm_kvq_destroy.  The cache's device must be the current device.  Device pointers are 16-byte
  * aligned, and row strides (ld, ldq, ldo: elements between rows) whole
  * multiples of 16 bytes; pointers and strides of weights and kept rows need 4
  * bytes.  One host thread at a time per cache.
@@ -616,8 +616,11 @@ FM_API fm_status fm_kvq_read(fm_kvq *c, int32_t layer, int32_t n_seqs, const int
  * sees nothing (length 0, first_row past the end, more query rows than cached
  * ones) gives zeros.  q_dev and out_dev: [sum n_rows][n_heads][head_dim] of
  * dtype, row strides ldq and ldo, packed in the order of seq_ids; they may not
- * overlap.  Scores, softmax and sums are f32; the operands keep f32 queries and
- * f32 / f16 outputs' probabilities to ~22 bits, bf16 outputs' to 11.
+ * overlap.  Scores, softmax and sums are f32.  The cache's values enter exactly
+ * as stored, f32 queries to ~22 bits (f16 and bf16 ones as they are); a
+ * probability times its row's V scale is kept to ~21 bits for f32 outputs,
+ * rounded to f16's 11 once for f16 ones and twice for bf16 ones.  A query row
+ * with a NaN or an infinity gives NaN, and one with values past 2^97 may.
  * decay >= 0 also counts the attention weight each cache row collects, per KV
  * head:  w_j = decay w_j + sum over the call's rows and the KV head's query
  * heads of p_j / sum p  (decay 1: plain accumulation; 0: this call's weights
@@ -626,7 +629,7 @@ FM_API fm_status fm_kvq_read(fm_kvq *c, int32_t layer, int32_t n_seqs, const int
  * that is NULL.  decay < 0: weights are left alone.
  * Sequence ids are distinct where weights are counted.
  * Errors: FM_ERR_INVALID_ARG, FM_ERR_UNSUPPORTED (over 2^19 query rows x heads
- *   in one sequence, or over 2^31 pairs of 32 of those and 128 keys),
+ *   in one sequence, or over 2^30 pairs of 32 of those and 64 keys),
  *   FM_ERR_CUDA.  A bounded device wait that gives up is
  *   reported by fm_kvq_synchronize.
  */
@@ -646,9 +649,9 @@ FM_API fm_status fm_kvq_set_weights(fm_kvq *c, int32_t layer, int32_t n_seqs, co
  * `recent` rows stay, and of the rows before them the keep - recent with the
  * largest weight (ties: the lowest row; NaN ranks below every number), in their
  * order.  The kept rows, with their weights, become rows 0 .. of sequence
- * dst_ids[i], whose length is then min(keep, length); a sequence of at most keep rows keeps all.  dst_ids[i] may be
- * src_ids[i] (in place), or another sequence, whose rows are replaced and
- * whose source stays as it is (a branch).  Destinations are distinct, and none
+ * dst_ids[i], whose length is then min(keep, length); a sequence of at most
+ * keep rows keeps all.  dst_ids[i] may be src_ids[i] (in place), or another
+ * sequence, whose rows are replaced and whose source stays as it is (a branch).  Destinations are distinct, and none
  * is the source of another entry.  kept_dev: int32 [n_seqs][n_kv_heads][keep]
  * or NULL receives the rows kept; entries past min(keep, length) are left as
  * they were.  0 <= recent <= keep <= max_rows.
@@ -671,7 +674,7 @@ FM_API fm_status fm_kvq_memory_bytes(const fm_kvq *c, int64_t *bytes);
 /* Wait for the stream; FM_ERR_TIMEOUT if a bounded device wait gave up since the last check (cleared). */
 FM_API fm_status fm_kvq_synchronize(fm_kvq *c, void *stream);
 FM_API const char *fm_kvq_last_error(const fm_kvq *c);   /* never NULL; NULL c: the last failed fm_kvq_create */
-/* Free everything the cache owns.  NULL is ignored. */
+/* Free everything the cache owns, once the calls issued so far are done.  NULL is ignored; a capture in progress goes on. */
 FM_API void fm_kvq_destroy(fm_kvq *c);
 
 /*
@@ -679,8 +682,8 @@ FM_API void fm_kvq_destroy(fm_kvq *c);
  * c from the next pass on (c NULL: in the head's own f32 cache again, which
  * holds what it held).  A pass stores its rows by fm_kvq_append and attends by
  * fm_kvq_attend; the rows a position may have are c's, not kv_cap's (kv_cap
- * may be 1 on a head that only ever uses c).  c has the head's n_kv_heads and head_dim, stays the caller's and
- * outlives its use.
+ * may be 1 on a head that only ever uses c).  c has the head's n_kv_heads and
+ * head_dim, stays the caller's and outlives its use.
  *   next_pos: the position after the cache's last row (the length, unless
  *     rows were evicted before).  A pass at pos0 <= next_pos rewinds
  *     next_pos - pos0 rows and appends its own.  Rows evicted between passes

@@ -59,6 +59,36 @@ def attend(q: np.ndarray, k: np.ndarray, v: np.ndarray, scale: float, causal: bo
     return out, w, mass, reach
 
 
+def attend_heads(q: np.ndarray, k: np.ndarray, v: np.ndarray, scale: float, causal: bool = False, first: int = 0):
+    """attend's results by matrix products, a KV head at a time, for cases of many rows."""
+    T, H, hd = q.shape
+    L, hkv = k.shape[0], k.shape[1]
+    out, mass, reach = np.zeros((T, H, hd)), np.zeros((T, H, hd)), np.zeros((T, H))
+    w = np.zeros((hkv, L))
+    if T == 0 or L == 0:
+        return out, w, mass, reach
+    n = H // hkv
+    size = min(GROUP, hd)
+    end = np.minimum(L, L - T + 1 + np.arange(T)) if causal else np.full(T, L)
+    seen = (np.arange(L) >= first) & (np.arange(L) < end[:, None])                    # [T, L]
+    for g in range(hkv):
+        rows = q[:, g * n:(g + 1) * n].reshape(T * n, hd)
+        see = np.repeat(seen, n, 0)
+        kk, vv = k[:, g], v[:, g]
+        top = np.repeat(np.abs(kk).reshape(L, -1, size).max(-1), size, -1)
+        s = np.where(see, rows @ kk.T * scale, -np.inf)
+        far = np.where(see, np.abs(rows) @ top.T, 0.0)
+        m = s.max(-1, keepdims=True)
+        p = np.exp(s - np.where(np.isfinite(m), m, 0.0))
+        total = p.sum(-1, keepdims=True)
+        p /= np.where(total > 0, total, 1.0)
+        out[:, g * n:(g + 1) * n] = (p @ vv).reshape(T, n, hd)
+        mass[:, g * n:(g + 1) * n] = (p @ np.abs(vv)).reshape(T, n, hd)
+        reach[:, g * n:(g + 1) * n] = abs(scale) * far.max(-1).reshape(T, n)
+        w[g] = p.sum(0)
+    return out, w, mass, reach
+
+
 def kept_rows(w: np.ndarray, keep: int, recent: int) -> np.ndarray:
     """The rows of one head that stay, in order: the last `recent`, and of the others the keep - recent with the
     largest weight, ties to the lowest row, NaN below every number."""

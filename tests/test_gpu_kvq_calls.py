@@ -1,0 +1,296 @@
+"""The 4-bit KV cache's calls (fm_kvq_*) beyond their ordinary sizes: units of many query rows over caches with work
+enough for them, more sequences than one launch takes, captured calls, and the order of streams.  The helpers and
+tolerances are test_gpu_kvq's."""
+from __future__ import annotations
+
+import gc
+
+import numpy as np
+import pytest
+
+from oracle import kvq as Q
+from test_gpu_kvq import TYPES, Cache, attend_case, built, check_out, check_weights, rows  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def shared_rows(n_seqs, hkv, hd, lens, rng, name):
+    """A cache whose sequences hold beginnings of the same rows."""
+    import torch
+    c = Cache(n_seqs, hkv, hd, max(lens))
+    base = [rows(rng, max(lens), hkv, hd, name) for _ in range(2)]
+    k, v = (torch.cat([b[0][:n] for n in lens]) for b in base)
+    c.fm.fm_kvq_append(c.c, 0, list(range(n_seqs)), k, v, lens, [0] * n_seqs)
+    ks, vs = (Q.stored(b[1]) for b in base)
+    for s, n in enumerate(lens):
+        c.k[0, s], c.v[0, s] = ks[:n], vs[:n]
+    return c
+
+
+@pytest.fixture
+def by_products(monkeypatch):
+    """attend_case's expectation by matrix products (the loops take minutes over many rows)."""
+    monkeypatch.setattr(Q, "attend", Q.attend_heads)
+
+
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("name", TYPES)
+@pytest.mark.parametrize("octets", [2, 3, 4])
+@pytest.mark.usefixtures("by_products")
+def test_wide_units(hd, name, octets):
+    """48 sequences of 8 KV heads: a unit carries two, three or four octets of query rows (few rows go by one)."""
+    rng = np.random.default_rng(hd + octets)
+    n = 48
+    lens = [520 + 13 * (i % 5) for i in range(n)]
+    c = shared_rows(n, 8, hd, lens, rng, name)
+    T = [4 * octets] * n                              # two query heads a KV head
+    T[3], T[17], T[40] = 4 * octets - 1, 0, 1
+    if octets == 4:
+        T[9] = 35                                     # three tiles of 32, the last of 6
+    attend_case(c, list(range(n)), T, 2, name, rng, causal=True, decay=0.0)
+    attend_case(c, list(range(n))[::-1], T, 2, name, rng, first=130)
+
+
+@pytest.mark.parametrize("hd", [64, 256])
+def test_many_sequences(hd):
+    """150 sequences a call, in launches of 64: every call, ragged, against each sequence by itself."""
+    import torch
+    rng = np.random.default_rng(41)
+    n, hkv = 150, 2
+    fm_lens = [int(x) for x in rng.integers(0, 140, n)]
+    fm_lens[63], fm_lens[64], fm_lens[149] = 0, 139, 65
+    c = Cache(n, hkv, hd, 140)
+    ids = [int(x) for x in rng.permutation(n)]
+    c.append(ids, [fm_lens[s] for s in ids], [0] * n, rng, "bf16")
+    c.append(ids[::-1], [1] * n, [fm_lens[s] for s in ids[::-1]], rng, "bf16")
+    attend_case(c, ids, [int(x) for x in rng.integers(0, 4, n)], 2, "f32", rng, causal=True, decay=0.0)
+    # weights of the caller's, some alike; read back by range
+    lens = [c.fm.fm_kvq_length(c.c, 0, s) for s in range(n)]
+    assert lens == [x + 1 for x in fm_lens]
+    w = rng.integers(0, 9, (n, hkv, 141)).astype(np.float32)
+    c.fm.fm_kvq_set_weights(c.c, 0, list(range(n)), torch.from_numpy(w).cuda())
+    at = [x // 3 for x in lens]
+    take = [x - y for x, y in zip(lens, at)]
+    k = torch.zeros((sum(take), hkv, hd), device="cuda")
+    v, back = torch.zeros_like(k), torch.full((n, hkv, 150), -1.0, device="cuda")
+    c.fm.fm_kvq_read(c.c, 0, ids, [at[s] for s in ids], [take[s] for s in ids], k, v, back)
+    row = 0
+    for i, s in enumerate(ids):
+        assert np.array_equal(k[row:row + take[s]].cpu().numpy(), c.k[0, s][at[s]:]), s
+        assert np.array_equal(v[row:row + take[s]].cpu().numpy(), c.v[0, s][at[s]:]), s
+        assert np.array_equal(back[i, :, :take[s]].cpu().numpy(), w[s, :, at[s]:lens[s]]), s
+        assert bool((back[i, :, take[s]:] == -1).all())
+        row += take[s]
+    # 70 in place and 40 into others that are given up
+    src = ids[:70] + ids[70:110]
+    dst = ids[:70] + ids[110:]
+    keep, recent = 40, 7
+    kept = torch.full((len(src), hkv, keep), -1, dtype=torch.int32, device="cuda")
+    c.fm.fm_kvq_evict(c.c, 0, src, dst, keep, recent, kept)
+    for i, (s, d) in enumerate(zip(src, dst)):
+        left = min(keep, lens[s])
+        assert c.fm.fm_kvq_length(c.c, 0, d) == left
+        gk, gv, gw = c.read(d)
+        for h in range(hkv):
+            want = Q.kept_rows(w[s, h, :lens[s]], keep, recent)
+            assert np.array_equal(kept[i, h, :left].cpu().numpy(), want), (s, h)
+            assert np.array_equal(gk[:, h].cpu().numpy(), c.k[0, s][want, h])
+            assert np.array_equal(gv[:, h].cpu().numpy(), c.v[0, s][want, h])
+            assert np.array_equal(gw[h], w[s, h, want])
+        assert bool((kept[i, :, left:] == -1).all())
+
+
+def test_same_sequence_twice():
+    """A call without weights may name a sequence more than once: each entry has its own query rows."""
+    rng = np.random.default_rng(42)
+    c = Cache(70, 2, 128, 300)
+    c.append([0, 1], [300, 77], [0, 0], rng, "f16")
+    attend_case(c, [0, 1, 0, 0, 1] * 14, [3, 1, 0, 5, 2] * 14, 2, "f16", rng, causal=True)
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+def test_captured_calls(in_place):
+    """Append, attention with weights, eviction and read in one graph: replayed on the cache as it was at the capture it
+    gives the eager calls' bits, also with new rows in its buffers."""
+    import torch
+    import block_speculative_decoding_fm_gb300 as fm
+    rng = np.random.default_rng(43)
+    hd, hkv, n, keep, recent = 128, 2, 500, 200, 20
+
+    def fresh():
+        c = fm.fm_kvq_create(1, 2, hkv, hd, n + 8)
+        fm.fm_kvq_append(c, 0, [0], k, v, [n], [0])
+        return c
+
+    def run(c, x):
+        fm.fm_kvq_append(c, 0, [0], x["k"], x["v"], [8], [n])
+        fm.fm_kvq_attend(c, 0, [0], x["q"], [8], x["out"], causal=True, decay=1.0, weights=x["w"])
+        fm.fm_kvq_evict(c, 0, [0], [0 if in_place else 1], keep, recent, x["kept"])
+        fm.fm_kvq_read(c, 0, [0 if in_place else 1], [0], [keep], x["ko"], x["vo"], x["wo"])
+
+    def buffers(seed):
+        r = np.random.default_rng(seed)
+        x = {a: rows(r, 8, h, hd, "bf16")[0] for a, h in (("k", hkv), ("v", hkv), ("q", 2 * hkv))}
+        x["out"] = torch.zeros_like(x["q"])
+        x["w"] = torch.zeros((1, hkv, n + 8), device="cuda")
+        x["kept"] = torch.zeros((1, hkv, keep), dtype=torch.int32, device="cuda")
+        x["ko"] = torch.zeros((keep, hkv, hd), device="cuda")
+        x["vo"] = torch.zeros_like(x["ko"])
+        x["wo"] = torch.zeros((1, hkv, keep), device="cuda")
+        return x
+
+    k, v = rows(rng, n, hkv, hd, "bf16")[0], rows(rng, n, hkv, hd, "bf16")[0]
+    wants = []
+    for seed in (1, 2):
+        c, x = fresh(), buffers(seed)
+        run(c, x)
+        fm.fm_kvq_synchronize(c)
+        wants.append(x)
+    c, x = fresh(), buffers(1)
+    fm.fm_kvq_synchronize(c)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run(c, x)
+    assert fm.fm_kvq_length(c, 0, 0 if in_place else 1) == keep
+    for want in wants:
+        # the cache as it was: its rows again (which also puts their weights to 0)
+        fm.fm_kvq_append(c, 0, [0], k, v, [n], [0])
+        for a in ("k", "v", "q"):
+            x[a].copy_(want[a])
+        torch.cuda.synchronize()
+        g.replay()
+        fm.fm_kvq_synchronize(c)
+        for a in want:
+            assert torch.equal(x[a], want[a]), a
+
+
+def test_two_graphs_share_a_cache():
+    """Two captured calls of different shapes use one workspace: replayed in turn on a stream they do not disturb each
+    other, nor an eager call between them."""
+    import torch
+    rng = np.random.default_rng(44)
+    c = Cache(2, 2, 64, 5000)
+    c.append([0, 1], [5000, 300], [0, 0], rng, "f16")
+    cases, graphs = [], []
+    for seqs, T in (([0], [16]), ([1, 0], [3, 2])):
+        q, qv = rows(rng, sum(T), 4, 64, "f16")
+        out = torch.zeros_like(q)
+        c.fm.fm_kvq_attend(c.c, 0, seqs, q, T, out)
+        torch.cuda.synchronize()
+        cases.append((seqs, T, q, out, out.clone()))
+        at = 0
+        for s, t in zip(seqs, T):
+            want, _, mass, reach = Q.attend(qv[at:at + t], c.k[0, s], c.v[0, s], 64 ** -0.5)
+            check_out(out[at:at + t], want, mass, reach, 64, c.k[0, s].shape[0], "f16", c.v[0, s])
+            at += t
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            c.fm.fm_kvq_attend(c.c, 0, seqs, q, T, out)
+        graphs.append(g)
+    for turn in range(6):
+        for (_, _, _, out, _), g in zip(cases, graphs):
+            out.zero_()
+            g.replay()
+        seqs, T, q, _, first = cases[turn % 2]
+        eager = torch.zeros_like(q)
+        c.fm.fm_kvq_attend(c.c, 0, seqs, q, T, eager)
+        torch.cuda.synchronize()
+        assert torch.equal(eager, first)
+        for _, _, _, out, first in cases:
+            assert torch.equal(out, first)
+
+
+def test_collected_under_capture():
+    """A cache that is collected while its thread captures leaves the capture as it is."""
+    import torch
+    rng = np.random.default_rng(45)
+    keep, gone = Cache(1, 1, 64, 64), Cache(1, 1, 64, 64)
+    keep.append([0], [64], [0], rng)
+    q, qv = rows(rng, 2, 1, 64, "f32")
+    out = torch.zeros_like(q)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        keep.fm.fm_kvq_attend(keep.c, 0, [0], q, [2], out)
+        del gone
+        gc.collect()
+    g.replay()
+    torch.cuda.synchronize()
+    want, _, mass, reach = Q.attend(qv, keep.k[0, 0], keep.v[0, 0], 64 ** -0.5)
+    check_out(out, want, mass, reach, 64, 64, "f32", keep.v[0, 0])
+
+
+def test_new_streams():
+    """Streams that come and go between calls (a handle may be used again): each call still finds the last one's rows."""
+    import torch
+    rng = np.random.default_rng(46)
+    c = Cache(1, 2, 128, 4100)
+    c.append([0], [4000], [0], rng, "bf16")
+    for i in range(12):
+        k, kv = rows(rng, 8, 2, 128, "bf16")
+        v, vv = rows(rng, 8, 2, 128, "bf16")
+        q, qv = rows(rng, 8, 2, 128, "bf16")
+        out = torch.zeros_like(q)
+        torch.cuda.synchronize()
+        for call in range(2):
+            s = torch.cuda.ExternalStream(make_stream())
+            with torch.cuda.stream(s):
+                if call:
+                    c.fm.fm_kvq_attend(c.c, 0, [0], q, [8], out, causal=True)
+                else:
+                    c.fm.fm_kvq_append(c.c, 0, [0], k, v, [8], [4000 + 8 * i])
+            drop_stream(s.cuda_stream)      # (its work goes on)
+        torch.cuda.synchronize()
+        for store, new in ((c.k, kv), (c.v, vv)):
+            store[0, 0] = np.concatenate([store[0, 0], Q.stored(new)])
+        want, _, mass, reach = Q.attend(qv, c.k[0, 0], c.v[0, 0], 128 ** -0.5, True)
+        check_out(out, want, mass, reach, 128, 4008 + 8 * i, "bf16", c.v[0, 0])
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+def test_query_range(name):
+    """Queries up to 2^97 (and tiny ones) with a scale that brings the scores back; far beyond, and infinite: NaN, that
+    row's alone."""
+    import torch
+    rng = np.random.default_rng(47)
+    c = Cache(1, 1, 64, 200)
+    c.append([0], [200], [0], rng, "f16")
+    for e in (-100, -60, 60, 96):
+        q, qv = rows(rng, 4, 1, 64, name)
+        q = q.clamp(-1.9, 1.9) * 2.0 ** e
+        qv = q.double().cpu().numpy()
+        bad = q.clone()
+        bad[2, 0, 5] = float("inf") if e < 0 else 2.0 ** 110
+        bad[3, 0, 60] = -bad[2, 0, 5]
+        for x, ok in ((q, [0, 1, 2, 3]), (bad, [0, 1])):
+            out = torch.zeros_like(x)
+            c.fm.fm_kvq_attend(c.c, 0, [0], x, [4], out, scale=2.0 ** -e / 8)
+            want, _, mass, reach = Q.attend(qv[ok], c.k[0, 0], c.v[0, 0], 2.0 ** -e / 8)
+            check_out(out[ok], want, mass, reach, 64, 200, name, c.v[0, 0])
+            assert len(ok) == 4 or bool(torch.isnan(out[2:]).all())
+
+
+def runtime():
+    import ctypes
+    import glob
+    import os
+    import torch
+    for p in ("libcudart.so.13", "libcudart.so", os.path.join(os.path.dirname(torch.__file__), "lib", "libcudart.so.13"),
+              *glob.glob("/usr/local/cuda/lib64/libcudart.so*")):
+        try:
+            return ctypes.CDLL(p)
+        except OSError:
+            continue
+    pytest.skip("no CUDA runtime library by name")
+
+
+def make_stream():
+    import ctypes
+    s = ctypes.c_void_p()
+    assert runtime().cudaStreamCreateWithFlags(ctypes.byref(s), 1) == 0
+    return s.value
+
+
+def drop_stream(handle):
+    import ctypes
+    assert runtime().cudaStreamDestroy(ctypes.c_void_p(handle)) == 0
