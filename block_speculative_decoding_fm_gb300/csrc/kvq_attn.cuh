@@ -157,13 +157,13 @@ __device__ __forceinline__ bool issue_stage(const KvqAttnArgs &a, Cursor *cu, in
   return true;
 }
 
-template <int HD, typename T, int NQ>
+template <int HD, typename T, int NQ, bool W>
 __global__ void __launch_bounds__(Shape<HD, T, NQ>::kThreads, Shape<HD, T, NQ>::MB)
     kvq_attend_kernel(const __grid_constant__ KvqAttnArgs a) {
   using Sh = Shape<HD, T, NQ>;
   using QT = typename Sh::QT;
   using PT = typename Sh::PT;
-  constexpr bool QS = Sh::QS, SV = Sh::SV;
+  constexpr bool QS = Sh::QS, SV = Sh::SV, SK = QS || W;
   constexpr int PS = Sh::PS, DB = Sh::DB;
   constexpr int NG = Sh::NG, NS = Sh::NS, SB = Sh::SB, TB = kvq_tile_bytes(HD), RT = Sh::RT, KS = Sh::KS, MT = Sh::MT;
   constexpr int GP = Sh::GP, KP = Sh::KP, NT = Sh::kThreads;
@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(Shape<HD, T, NQ>::kThreads, Shape<HD, T, NQ>::
     const int len = a.len[x.i], T_rows = a.rows[x.i], R = T_rows * a.group, rq = x.rt * RT;
     const size_t plane = (size_t)a.seq[x.i] * a.c.n_kv + x.head;
     const uint32_t vm = ldg32(a.c.vmax + plane);
-    load_q<HD, QS, NQ, NT>(static_cast<const T *>(a.q) + a.row0[x.i] * a.ldq + (int64_t)x.head * a.group * HD, a.ldq, a.group,
+    load_q<HD, QS, SK, NQ, NT>(static_cast<const T *>(a.q) + a.row0[x.i] * a.ldq + (int64_t)x.head * a.group * HD, a.ldq, a.group,
                            rq, R, a.scale_log2, qs, tid);
     const PRange range(vm);
     __syncthreads();
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(Shape<HD, T, NQ>::kThreads, Shape<HD, T, NQ>::
       const uint32_t pt = smem_u32(ptile) + buf * PT::kBytes;
       float s[MT][NQ][4];
       uint64_t sp[MT][NQ][2];
-      strip_scores<HD, QS, NQ, KS>(kcode + slot * SB, kscale + slot * SB, qt, lane, sp);
+      strip_scores<HD, QS, SK, NQ, KS>(kcode + slot * SB, kscale + slot * SB, qt, lane, sp);
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(Shape<HD, T, NQ>::kThreads, Shape<HD, T, NQ>::
         }
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          const float unit = t ? 1.f / kUnitHi : 1.f / kUnitLo;
+          const float unit = SV ? 1.f : t ? 1.f / kUnitHi : 1.f / kUnitLo;
           float(&y)[4] = o[u][t][n];
           y[0] = fmaf(y[0], unit, -c0) * f0, y[1] = fmaf(y[1], unit, -c1) * f1;
           y[2] = fmaf(y[2], unit, -c0) * f0, y[3] = fmaf(y[3], unit, -c1) * f1;
@@ -615,7 +615,7 @@ __global__ void __launch_bounds__(kWThreads) kvq_weights_kernel(const __grid_con
     if (rt) __syncthreads();
 #pragma unroll
     for (int p = 0; p < kWSlots - 1; ++p) fetch(p);
-    load_q<HD, QS, NQ, kWThreads>(static_cast<const T *>(a.q) + a.row0[i] * a.ldq + (int64_t)head * a.group * HD, a.ldq,
+    load_q<HD, QS, true, NQ, kWThreads>(static_cast<const T *>(a.q) + a.row0[i] * a.ldq + (int64_t)head * a.group * HD, a.ldq,
                                   a.group, rt * RT, R, a.scale_log2, qs, tid);
     // The attention has begun everywhere before this launch begins, and lets nothing begin before what came ahead of it
     // is done: rows and queries are there already, its sums and the weights are what is waited for.
@@ -645,7 +645,7 @@ __global__ void __launch_bounds__(kWThreads) kvq_weights_kernel(const __grid_con
       if (t >= nt || key0 >= len || key0 + 32 <= a.first) continue;
       const uint32_t kb = smem_u32(smem) + (k % kWSlots * 2 + (w >> 1)) * KB;
       uint64_t sp[2][NQ][2];
-      strip_scores<HD, QS, NQ, KS>(kb + la.code, kb + la.scale, smem_u32(qs), lane, sp);
+      strip_scores<HD, QS, true, NQ, KS>(kb + la.code, kb + la.scale, smem_u32(qs), lane, sp);
       float sum[4] = {0.f, 0.f, 0.f, 0.f};     // keys 8 j + lane / 4
       if (key0 >= a.first && key0 + 32 <= lim_all) {
 #pragma unroll
@@ -697,10 +697,13 @@ template <int HD, typename T, int NQ>
 cudaError_t attend_t(const KvqAttnArgs &a, cudaStream_t s) {
   using Sh = Shape<HD, T, NQ>;
   static_assert(Sh::kBytes <= 226 * 1024, "shared memory of a CTA");
-  static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(kvq_attend_kernel<HD, T, NQ>, Sh::kBytes, done);
+  // (f32 rows take their codes signed anyway)
+  constexpr bool W = sizeof(T) != 4;
+  static std::atomic<uint64_t> done[2];
+  auto kern = W && a.lse ? kvq_attend_kernel<HD, T, NQ, W> : kvq_attend_kernel<HD, T, NQ, false>;
+  cudaError_t e = allow_smem(kern, Sh::kBytes, done[W && a.lse]);
   if (e != cudaSuccess) return e;
-  e = kvq_launch(kvq_attend_kernel<HD, T, NQ>, dim3(a.ctas), dim3(Sh::kThreads), Sh::kBytes, s, a);
+  e = kvq_launch(kern, dim3(a.ctas), dim3(Sh::kThreads), Sh::kBytes, s, a);
   // nothing to join where every share is a unit
   bool whole = a.extra == 0 || a.share == 0;
   for (int i = 0; i < a.n; ++i) whole = whole && (a.rows[i] == 0 || (a.share ? a.stages[i] + kKvqUnitCost == a.share : a.parts[i] == 1));

@@ -35,6 +35,10 @@ __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
 // in the low bits of a f16 is the subnormal code * 2^-24, one digit further up
 // code * 2^-20: exact, and one AND a pair (the matrix instructions take
 // subnormals as they are).  Pairs 0 and 2 come in units of 2^-24, 1 and 3 of 2^-20.
+// What that costs is precision: the matrix instructions align their products by the
+// operands' exponents, which a subnormal has at 2^-14, so a sum keeps some 2^-17 of its
+// largest term (measured: 1e-5 off in outputs that are 1e-6 off with normal operands).
+// f16 and bf16 outputs, rounded to 2^-12 and 2^-9, do not see it.
 constexpr float kUnitHi = 0x1p-20f, kUnitLo = 0x1p-24f;
 __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t (&h)[4]) {
   h[0] = w & 0x000f000fu;
@@ -43,14 +47,15 @@ __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t (&h)[4]) {
   h[2] = w & 0x000f000fu;
   h[3] = w & 0x00f000f0u;
 }
-// the same less 8, in the same units (exact: multiples of 2^-24)
+// The same less 8, as whole numbers, for f32 outputs and for the weights: 1024 + code and 1024 + 16 code by
+// one AND-OR, then one exact addition or multiply-add a pair.
 __device__ __forceinline__ void codes_f16_signed(uint32_t w, uint32_t (&h)[4]) {
-  codes_f16(w, h);
 #pragma unroll
   for (int p = 0; p < 4; ++p) {
-    const uint32_t k = p & 1 ? 0x80808080u : 0x80088008u;   // -8 in units of 2^-20, 2^-24
-    const __half2 x = __hadd2(*reinterpret_cast<const __half2 *>(&h[p]), *reinterpret_cast<const __half2 *>(&k));
-    h[p] = *reinterpret_cast<const uint32_t *>(&x);
+    const uint32_t x = ((p < 2 ? w : w >> 8) & (p & 1 ? 0x00f000f0u : 0x000f000fu)) | 0x64006400u;
+    const __half2 y = *reinterpret_cast<const __half2 *>(&x);
+    const __half2 z = p & 1 ? __hfma2(y, __float2half2_rn(0.0625f), __float2half2_rn(-72.f)) : __hadd2(y, __float2half2_rn(-1032.f));
+    h[p] = *reinterpret_cast<const uint32_t *>(&z);
   }
 }
 
@@ -137,14 +142,14 @@ struct QTile {
 // group, head r % group of the group -- into B fragments.  Inside a group of 32
 // dims the k index of the matrix product is a permutation of the dims that a
 // word's codes dictate: lane column c holds dims 8 c .. 8 c + 7, pair p = dims (p, p + 4) of
-// them; the even pairs' codes come in units 16 times smaller, which their
+// them; the even pairs' unsigned codes come in units 16 times smaller, which their
 // queries make up for.  A row is scaled by a power of two that brings its
 // largest value to [2^7, 2^8), so q up to 2^96 fits f16 (exact for bf16 and f16
 // inputs down to 2^-22 of the row's largest); the row's factor undoes it and
-// carries the softmax scale, whose sign goes into the queries.  The codes enter the
-// product unsigned, and the start value takes their 8 off: -8 sum q over the group.
+// carries the softmax scale, whose sign goes into the queries.  Unless SK the codes enter
+// the product unsigned, and the start value takes their 8 off: -8 sum q over the group.
 // NT threads, all of which call it; the caller synchronises.
-template <int HD, bool QS, int NQ, int NT, typename T>
+template <int HD, bool QS, bool SK, int NQ, int NT, typename T>
 __device__ __forceinline__ void load_q(const T *q, int64_t ldq, int group, int r0, int R, float scale_log2, uint8_t *tile,
                                        int tid) {
   using QT = QTile<HD, QS, NQ>;
@@ -179,15 +184,15 @@ __device__ __forceinline__ void load_q(const T *q, int64_t ldq, int group, int r
       // am in [2^ex, 2^(ex + 1)); the factor 2^(7 - ex), its exponent kept in f32's normal range
       const int ex = am > 0.f && am < INFINITY ? min(96, max(-119, static_cast<int>(__float_as_uint(am) >> 23) - 127)) : 7;
       const float up = copysignf(__uint_as_float((uint32_t)(127 + 7 - ex) << 23), scale_log2);
-      if (o == 0)   // (2^20: the products' unit; never 0: a masked score is -inf times it)
+      if (o == 0)   // (2^20: the unsigned codes' unit; never 0: a masked score is -inf times it)
         reinterpret_cast<float *>(tile + QT::kMult)[r] =
-            fmaxf(fabsf(scale_log2) * __uint_as_float((uint32_t)(127 + ex - 7 + 20) << 23), 1e-37f);
+            fmaxf(fabsf(scale_log2) * __uint_as_float((uint32_t)(127 + ex - 7 + (SK ? 0 : 20)) << 23), 1e-37f);
       const int g = o >> 2, at = ((g * NQ + (r >> 3)) * 32 + (r & 7) * 4 + (o & 3)) * 16;
       float sum = 0.f;
       uint32_t hi[4], lo[4];
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
-        const float f = p & 1 ? up : 16.f * up;
+        const float f = SK || p & 1 ? up : 16.f * up;
         if constexpr (QS) {
           split2_f16(x[p] * f, x[p + 4] * f, hi[p], lo[p]);
         } else {
@@ -195,16 +200,20 @@ __device__ __forceinline__ void load_q(const T *q, int64_t ldq, int group, int r
           hi[p] = *reinterpret_cast<const uint32_t *>(&v);
           lo[p] = 0;
         }
-        const float2 h = pair_f32(hi[p]), l = pair_f32(lo[p]);
-        sum += (h.x + h.y + (l.x + l.y)) * (p & 1 ? 1.f : 0.0625f);
+        if constexpr (!SK) {
+          const float2 h = pair_f32(hi[p]), l = pair_f32(lo[p]);
+          sum += (h.x + h.y + (l.x + l.y)) * (p & 1 ? 1.f : 0.0625f);
+        }
       }
       *reinterpret_cast<uint4 *>(tile + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
       if constexpr (QS) *reinterpret_cast<uint4 *>(tile + QT::kLo + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      if ((o & 3) == 0) {
-        float *off = reinterpret_cast<float *>(tile + QT::kOff) + (g * NQ * 4 + (r >> 1)) * 4 + (r & 1);
-        off[0] = off[2] = -8.f * kUnitHi * sum;
+      if constexpr (!SK) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        if ((o & 3) == 0) {
+          float *off = reinterpret_cast<float *>(tile + QT::kOff) + (g * NQ * 4 + (r >> 1)) * 4 + (r & 1);
+          off[0] = off[2] = -8.f * kUnitHi * sum;
+        }
       }
     }
   }
@@ -237,8 +246,8 @@ __device__ __forceinline__ void row_scales(uint32_t addr, float (&d)[GB]) {
 // Scores of 8 NQ query rows against the KS keys of a strip: s[m][n] is the
 // accumulator fragment of keys 16 m + lane / 4 (first pair) and + 8 (second), query rows
 // 8 n + 2 (lane % 4) and + 1.  Per group of 32 dims the product runs over whole codes
-// (exact operands) and the row's scale meets the f32 sum.
-template <int HD, bool QS, int NQ, int KS>
+// (exact operands) and the row's scale meets the f32 sum.  SK: the codes less 8.
+template <int HD, bool QS, bool SK, int NQ, int KS>
 __device__ __forceinline__ void strip_scores(uint32_t code, uint32_t scale, uint32_t qt, int lane,
                                              uint64_t (&s)[KS / 16][NQ][2]) {
   using QT = QTile<HD, QS, NQ>;
@@ -259,10 +268,15 @@ __device__ __forceinline__ void strip_scores(uint32_t code, uint32_t scale, uint
         const int g = g0 + gi + f;
         uint32_t h[2 * MT][4];
 #pragma unroll
-        for (int j = 0; j < 2 * MT; ++j) codes_f16(w[2 * f * (GF - 1) + j], h[j]);
+        for (int j = 0; j < 2 * MT; ++j) {
+          if constexpr (SK)
+            codes_f16_signed(w[2 * f * (GF - 1) + j], h[j]);
+          else
+            codes_f16(w[2 * f * (GF - 1) + j], h[j]);
+        }
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
-          const uint4 off = lds128(qt + QT::kOff + (g * NQ + n) * 64 + (lane & 3) * 16);
+          const uint4 off = SK ? make_uint4(0, 0, 0, 0) : lds128(qt + QT::kOff + (g * NQ + n) * 64 + (lane & 3) * 16);
           const uint4 b = lds128(qt + ((g * NQ + n) * 32 + lane) * 16);
           float acc[MT][4];
 #pragma unroll
@@ -359,7 +373,7 @@ __device__ __forceinline__ uint32_t u32(__half2 v) { return *reinterpret_cast<co
 
 // O^T += V^T P^T over 32 rows of a tile (code: where the lane fetches their unit of group 0), group g:
 // o[t][n] are the accumulators of dims 32 g + 4 (lane / 4) + t (first pair) and + 2 (second), query
-// rows 8 n + 2 (lane % 4) and + 1, in the code pairs' units (t = 0: 2^-24, t = 1: 2^-20).
+// rows 8 n + 2 (lane % 4) and + 1, in the code pairs' units (t = 0: 2^-24, t = 1: 2^-20; SV: 1).
 // sc: the V scales of the rows' pairs (kvq_vscale's order).  P' = p d is rounded to
 // f16 (PS 1: p's rest joins the product before its only rounding; PS 2: hi + lo, ~22 bits).  SV: the codes enter
 // with their 8 taken off; else unsigned, and cor collects the sums of P', which the

@@ -9,6 +9,9 @@ S = sum_j p_j |v_j| and A = scale max_j sum_d |q_d| K_jd, K_jd the largest |k_j|
             by pairs); head_dim / 32 groups, the scale, log2(e) and the factor: (hd / 32 + 6) 2^-24 A; the reference's subtraction
             in the log2 domain 2^-22 x 1.45 A: delta <= (120 + hd / 32) 2^-24 A in all.  A probability is off by the factor
             e^(+-2 delta) with its sum's
+            (f32 queries, and any with weights, take whole numbers n - 8 instead, in -8 .. 7: less.  Unsigned n are subnormals,
+            by whose exponents the matrix instructions align a sum's terms: that costs f16 and bf16 outputs up to 6 bits of the
+            24 in the worst case, which is not counted here -- their own rounding leaves more)
   exp2      2^-22 each, its sum's too
   P V       P' = p d (d the f16 scale) as f16.  bf16 outputs: p rounded, then the product, 2 x 2^-11 relative.  f16 outputs: p in two
             parts (2^-22), one rounding of the product 2^-11, of the second part's 2^-22.  f32 outputs: both parts of the product
