@@ -13,6 +13,7 @@
 // caller hands over (fm_mtp_use_kvq): a pass then stores its rows there and
 // attends through fm_kvq_append and fm_kvq_attend.
 #include <algorithm>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -703,7 +704,7 @@ fm_status fm_mtp_use_kvq(fm_mtp *m, fm_kvq *c, int32_t layer, int32_t seq, int64
     return mfail(m, FM_ERR_INVALID_ARG, "the 4-bit cache has %d heads of %d, the head %d of %d", g.n_kv_heads, g.head_dim,
                  m->cfg.n_kv_heads, m->cfg.head_dim);
   if (next_pos < len || next_pos > INT32_MAX) return mfail(m, FM_ERR_INVALID_ARG, "next_pos %lld with %d rows", (long long)next_pos, len);
-  if (!(decay == decay) || decay > 3.0e38f) return mfail(m, FM_ERR_INVALID_ARG, "decay is not finite");
+  if (!std::isfinite(decay)) return mfail(m, FM_ERR_INVALID_ARG, "decay is not finite");
   if (!m->ao) {
     const size_t kvw = (size_t)kMaxRows * m->cfg.n_kv_heads * m->cfg.head_dim;
     if (!m->kst) MTRY(malloc_dev(m, &m->kst, kvw));

@@ -153,6 +153,7 @@ def test_refusals():
     c = fm.fm_kvq_create(1, 1, cfg.n_kv_heads, cfg.head_dim, 20)
     bad(fm.FM_ERR_INVALID_ARG, fm.fm_mtp_use_kvq, h, c, 0, 1, next_pos=0)
     bad(fm.FM_ERR_INVALID_ARG, fm.fm_mtp_use_kvq, h, c, 0, 0, decay=float("nan"))
+    bad(fm.FM_ERR_INVALID_ARG, fm.fm_mtp_use_kvq, h, c, 0, 0, decay=float("-inf"))
     fm.fm_mtp_forward(h, t[:4], hn[:4], 0, 0)                    # four rows in the head's own cache
     own = fm.fm_mtp_cache(h, 0, 4, np.empty((4, cfg.n_kv_heads * cfg.head_dim), np.float32)).copy()
     fm.fm_mtp_use_kvq(h, c)
