@@ -31,7 +31,7 @@ namespace {
 constexpr int kThreads = 512;    // in place
 constexpr int kCopies = 8; 
 constexpr int kMoveThreads = 256;
-constexpr int kSelectRoom = 90 * 1024;   // bytes of keys in shared memory, where planes are few
+constexpr int kSelectRoom[2] = {200 * 1024, 90 * 1024};   // bytes of keys in shared memory: a CTA an SM, two
 constexpr int kCluster = 8;      // in place; select, where planes are few
 constexpr int kMoveItems = 4;    // 16-byte units a thread moves a round
 
@@ -69,7 +69,7 @@ __host__ __device__ inline int select_run(int nc, int warps) { return (nc + warp
 // weights, and where they fit (cached) every later one has them from shared memory, in the thread that put them there.
 // With many planes other CTAs fill the waits, and shared memory taken from L1 made the launches around this one slower.
 // The passes end early where all of the selected bin stay, for distinct weights after three mostly.
-// (512 planes of 512 to 8192 rows: 18 us; 4 of 65535 rows: 15 us, 18 without the cache.)
+// (512 planes of 512 to 8192 rows: 18 us; 4 of 65535 rows: 15 us, 18 without the cache; 8 of 262144: 32 us, 41 without.)
 template <int CS>
 __global__ void __launch_bounds__(CS == 1 ? 256 : 512, CS == 1 ? 4 : 2) kvq_select_kernel(const __grid_constant__ KvqEvictArgs a, bool cached) {
   constexpr int NT = CS == 1 ? 256 : 512, NWarp = NT / 32;
@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(kMoveThreads) kvq_move_kernel(const __grid_con
 // In place: grid (cluster of a plane).  A round's rows are loaded by all before any of them is stored.  With many planes
 // other clusters fill the waits (two CTAs an SM).  With few, a round is twice as long, and the next one's loads and the
 // list's for the one after are on their way while the barrier is waited for: they read behind every row written so far.
-// (One sequence of 8 planes, 65536 of 262144 rows kept: 106 us with the selection, 157 without the loads ahead; 256 planes,
+// (One sequence of 8 planes, 65536 of 262144 rows kept: 96 us with the selection, 52 us more without the loads ahead; 256 planes,
 // 2048 of 4096 kept: 63 us, 86 with them.)
 template <int HD, bool Few>
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, Few ? 1 : 2)
@@ -361,13 +361,13 @@ cudaError_t evict_hd(const KvqEvictArgs &a, cudaStream_t s) {
   const int planes = a.n * a.c.n_kv;
   cudaError_t e;
   if (planes * kCluster <= 320) {
-    // (two CTAs an SM; longer planes are read again in each pass)
+    // (longer planes are read again in each pass)
     int longest = 0;
     for (int i = 0; i < a.n; ++i) longest = a.len[i] > longest ? a.len[i] : longest;
     const int bytes = select_run(longest, kCluster * 16) * 16 * 4;
-    const bool cached = bytes <= kSelectRoom;
+    const bool cached = bytes <= kSelectRoom[planes * kCluster > 152];
     static std::atomic<uint64_t> done{0};
-    e = allow_smem(kvq_select_kernel<kCluster>, kSelectRoom, done);
+    e = allow_smem(kvq_select_kernel<kCluster>, kSelectRoom[0], done);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(planes * kCluster);

@@ -180,8 +180,8 @@ fm_status end(fm_kvq *c, cudaStream_t s) {
 
 // The octets of query rows that a unit carries, 0 where the call has too many units.  A stage costs about 1 + nq (its codes
 // are unpacked once, then used for each octet), beginning and ending a unit 5 nq (9 nq for 256 dims) of the same: short
-// caches want many narrow units, long ones few wide ones.  (8 rows of 24 heads over 4 KV heads of 256, f32: 64 rows 4.9 us
-// with nq 1, 9.3 with 3; 16384 rows 32.4 and 30.1.  16 rows of 16 heads of 128, bf16: 4161 rows 9.7 us with nq 1, 10.0 with
+// caches want many narrow units, long ones few wide ones.  (8 rows of 24 heads over 4 KV heads of 256, f32: 64 rows 4.8 us
+// with nq 1, 8.6 with 3; 16384 rows 36.7 and 29.2.  16 rows of 16 heads of 128, bf16: 4161 rows 9.7 us with nq 1, 10.0 with
 // 2; 16384 rows 18.9 and 16.7.)
 int choose_nq(int n_seqs, const int32_t *seq, const int32_t *rows, const int32_t *len, int group, int nkv, int hd, int n_sm,
               int64_t widest) {

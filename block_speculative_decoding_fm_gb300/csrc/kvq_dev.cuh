@@ -37,7 +37,7 @@ __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
 // subnormals as they are).  Pairs 0 and 2 come in units of 2^-24, 1 and 3 of 2^-20.
 // What that costs is precision: the matrix instructions align their products by the
 // operands' exponents, which a subnormal has at 2^-14, so a sum keeps some 2^-17 of its
-// largest term (measured: 1e-5 off in outputs that are 1e-6 off with normal operands).
+// largest term (measured: f32 outputs 1e-5 off, 3e-7 with normal operands).
 // f16 and bf16 outputs, rounded to 2^-12 and 2^-9, do not see it.
 constexpr float kUnitHi = 0x1p-20f, kUnitLo = 0x1p-24f;
 __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t (&h)[4]) {
@@ -412,14 +412,26 @@ __device__ __forceinline__ void tile_pv(uint32_t code, int g, const uint32_t (&s
         l[n][j] = u32(__hfma2(h2(l[n][j]), d, __hfma2(p, d, __hneg2(x))));
       }
     }
-#pragma unroll
-    for (int st = 0; st < 2; ++st)
+    if constexpr (PS == 2) {
+      // (a sum of its own over the 32 rows: the matrix instructions cut their sums off, which over a long cache adds up:
+      // 32768 rows 2.2e-6 off, 3e-7 this way, at 2 % of the time)
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        mma_f16(o[t][n], h[2 * st][t], h[2 * st][t + 2], h[2 * st + 1][t], h[2 * st + 1][t + 2], b[n][2 * st], b[n][2 * st + 1]);
-        if constexpr (PS == 2)
-          mma_f16(o[t][n], h[2 * st][t], h[2 * st][t + 2], h[2 * st + 1][t], h[2 * st + 1][t + 2], l[n][2 * st], l[n][2 * st + 1]);
+        float acc[4];
+        mma_f16_c(acc, h[0][t], h[0][t + 2], h[1][t], h[1][t + 2], l[n][0], l[n][1], make_uint4(0, 0, 0, 0));
+        mma_f16(acc, h[2][t], h[2][t + 2], h[3][t], h[3][t + 2], l[n][2], l[n][3]);
+        mma_f16(acc, h[0][t], h[0][t + 2], h[1][t], h[1][t + 2], b[n][0], b[n][1]);
+        mma_f16(acc, h[2][t], h[2][t + 2], h[3][t], h[3][t + 2], b[n][2], b[n][3]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[t][n][e] += acc[e];
       }
+    } else {
+#pragma unroll
+      for (int st = 0; st < 2; ++st)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          mma_f16(o[t][n], h[2 * st][t], h[2 * st][t + 2], h[2 * st + 1][t], h[2 * st + 1][t + 2], b[n][2 * st], b[n][2 * st + 1]);
+    }
     if constexpr (!SV) {
       constexpr uint32_t kOnes = 0x3c003c00u;
       mma_f16(cor[n], b[n][0], b[n][1], b[n][2], b[n][3], kOnes, kOnes);
