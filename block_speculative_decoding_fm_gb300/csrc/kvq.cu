@@ -182,9 +182,10 @@ fm_status end(fm_kvq *c, cudaStream_t s) {
 // are unpacked once, then used for each octet), beginning and ending a unit 5 nq (9 nq for 256 dims) of the same: short
 // caches want many narrow units, long ones few wide ones.  (8 rows of 24 heads over 4 KV heads of 256, f32: 64 rows 4.8 us
 // with nq 1, 8.6 with 3; 16384 rows 36.7 and 29.2.  16 rows of 16 heads of 128, bf16: 4161 rows 9.7 us with nq 1, 10.0 with
-// 2; 16384 rows 18.9 and 16.7.)
+// 2; 16384 rows 18.9 and 16.7.)  In the pass over the weights a CTA takes a sequence's row tiles one after another, about 7
+// each.  (With weights, 8 rows of 32 heads over 8 KV heads of 128, 1042 rows: 11.6 us, 15.0 without that term.)
 int choose_nq(int n_seqs, const int32_t *seq, const int32_t *rows, const int32_t *len, int group, int nkv, int hd, int n_sm,
-              int64_t widest) {
+              int64_t widest, bool weights) {
   const int stage_rows = kKvqTile * kvq_stage_tiles(hd), most = (int)(widest < 8 * kKvqMaxNQ ? (widest + 7) / 8 : kKvqMaxNQ);
   int best = 0;
   int64_t least = 0;
@@ -197,7 +198,8 @@ int choose_nq(int n_seqs, const int32_t *seq, const int32_t *rows, const int32_t
       fits = fits && units <= kMaxUnits && units * (stages + kKvqUnitCost) <= INT_MAX;
       work += units * stages;
     }
-    const int64_t cost = (int64_t)nq * (hd == 256 ? 9 : 5) * n_sm + work * (1 + nq);
+    int64_t cost = (int64_t)nq * (hd == 256 ? 9 : 5) * n_sm + work * (1 + nq);
+    if (weights) cost += (widest + 8 * nq - 1) / (8 * nq) * 7 * n_sm;
     if (fits && (!best || cost < least)) best = nq, least = cost;
   }
   return best;
@@ -514,7 +516,7 @@ fm_status fm_kvq_attend(fm_kvq *c, int32_t layer, int32_t n_seqs, const int32_t 
     total += n;
     if (n > 0 && len[seq_ids_host[i]] > most) most = len[seq_ids_host[i]];
   }
-  const int nq = choose_nq(n_seqs, seq_ids_host, n_rows_host, len, group, nkv, hd, c->n_sm, widest), unit_rows = 8 * nq;
+  const int nq = choose_nq(n_seqs, seq_ids_host, n_rows_host, len, group, nkv, hd, c->n_sm, widest, keep_w), unit_rows = 8 * nq;
   if (!nq) return kfail(c, FM_ERR_UNSUPPORTED, "%lld query rows of a KV head in one call", (long long)widest);
   const int64_t width = (int64_t)n_heads * hd;
   if (total > 0) {

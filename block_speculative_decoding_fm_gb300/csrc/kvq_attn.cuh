@@ -16,6 +16,11 @@
 // SM, and a unit's end needs no exchange inside a group.  The group shares one reference a row; it moves
 // only when a score beats it by 2^8, and the barrier that hands P over tells everyone whether one did.
 //
+// One query row is bound by memory: 524288 rows of 8 KV heads of 128 in 101 us, 6.0 TB/s (0.88 of a plain copy), 24 heads
+// over 4 of 256 in 107 us, 5.6 TB/s.  Sixteen are bound by the tensor and the integer pipes together: bf16 144 us (4.2 TB/s),
+// f16 157 us, f32 243 us, whose queries and probabilities are two operands each.  Short caches are a chain of waits:
+// of 26 us over 32769 rows of 16 heads, 18 are the stream, 2 the queries, 1 the output, 3 the join.
+//
 // With at most 32 query rows the product is a skinny one, and the codes pass from shared memory (ldmatrix)
 // through a few integer operations straight into mma.sync fragments: they never go back to shared
 // memory as f16, which a tcgen05 operand would need (64 KB written and read again per 128 rows of
@@ -32,7 +37,11 @@ namespace {
 using namespace kvq;
 
 constexpr float kLazy = 8.f;               // log2 of the growth a reference tolerates
-constexpr int kWThreads = 128, kWSlots = 4;   // the weights pass: pairs of tiles in shared memory
+constexpr int kWThreads = 128;             // the weights pass
+// its pairs of tiles in shared memory: about 37 KB, with which an SM holds the four CTAs that the pass is dealt out for (more
+// at once share unevenly: 16 rows over 32768 of 128 dims 48 us with two or three pairs, 41 with four; 256 dims 36 us with
+// two, 38 with four)
+__host__ __device__ constexpr int w_slots(int hd) { return 512 / hd; }
 
 constexpr int imin(int a, int b) { return a < b ? a : b; }
 constexpr int imax(int a, int b) { return a > b ? a : b; }
@@ -583,13 +592,15 @@ __global__ void __launch_bounds__(kJoinThreads) kvq_join_kernel(const __grid_con
 // known, K alone is read again (from L2 where it still is there) and the scores
 // formed a second time, which needs no store of rows x keys.  One CTA owns a
 // run of tiles, so nothing is added atomically.  Grid (sequence x run, KV head).
+// Bound by unpacking the codes and by the exponentials (issue 55 %, tensor pipe 24 %): 524288 rows of 8 KV heads of 128,
+// 16 query rows: 108 us, 2.8 TB/s; 32769 rows of 16: 13 us.
 template <int HD, typename T, int NQ>
 __global__ void __launch_bounds__(kWThreads) kvq_weights_kernel(const __grid_constant__ KvqAttnArgs a) {
   constexpr bool QS = sizeof(T) == 4;
   constexpr int KB = kvq_k_bytes(HD), RT = 8 * NQ, KS = 32;
   using QT = QTile<HD, QS, NQ>;
   extern __shared__ __align__(128) uint8_t smem[];
-  uint8_t *qs = smem + kWSlots * 2 * KB;
+  uint8_t *qs = smem + w_slots(HD) * 2 * KB;
   // a row's sum so far (a warp's own rows: lane 4 g + j has key 8 j + g of its strip of a pair of tiles)
   float *acc = reinterpret_cast<float *>(qs + QT::kBytes);
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g8 = lane >> 2, c = lane & 3;
@@ -606,7 +617,7 @@ __global__ void __launch_bounds__(kWThreads) kvq_weights_kernel(const __grid_con
       for (int h = 0; h < 2; ++h)
         if (2 * p + h < nt)
           for (int e = tid; e < KB / 16; e += kWThreads)
-            cp_async16(smem_u32(smem) + (p % kWSlots * 2 + h) * KB + e * 16, src + (size_t)(2 * p + h) * kvq_tile_bytes(HD) + e * 16, 16);
+            cp_async16(smem_u32(smem) + (p % w_slots(HD) * 2 + h) * KB + e * 16, src + (size_t)(2 * p + h) * kvq_tile_bytes(HD) + e * 16, 16);
     cp_async_commit();
   };
   const LaneAt<HD, KS> la((w & 1) * 32, lane);
@@ -614,7 +625,7 @@ __global__ void __launch_bounds__(kWThreads) kvq_weights_kernel(const __grid_con
   for (int rt = 0; rt < rts; ++rt) {
     if (rt) __syncthreads();
 #pragma unroll
-    for (int p = 0; p < kWSlots - 1; ++p) fetch(p);
+    for (int p = 0; p < w_slots(HD) - 1; ++p) fetch(p);
     load_q<HD, QS, true, NQ, kWThreads>(static_cast<const T *>(a.q) + a.row0[i] * a.ldq + (int64_t)head * a.group * HD, a.ldq,
                                   a.group, rt * RT, R, a.scale_log2, qs, tid);
     // The attention has begun everywhere before this launch begins, and lets nothing begin before what came ahead of it
@@ -638,12 +649,12 @@ __global__ void __launch_bounds__(kWThreads) kvq_weights_kernel(const __grid_con
       for (int h = 0; h < 2; ++h) mu[n][h] = *reinterpret_cast<const float *>(qs + QT::kMult + (8 * n + 2 * c + h) * 4);
 #pragma unroll 1
     for (int k = 0; k < np; ++k) {
-      cp_async_wait<kWSlots - 2>();
+      cp_async_wait<w_slots(HD) - 2>();
       __syncthreads();   // everyone's copies of this pair; everyone is done with the pair before it, whose place is next
-      fetch(k + kWSlots - 1);
+      fetch(k + w_slots(HD) - 1);
       const int t = 2 * k + (w >> 1), key0 = (t0 + t) * kKvqTile + (w & 1) * 32;
       if (t >= nt || key0 >= len || key0 + 32 <= a.first) continue;
-      const uint32_t kb = smem_u32(smem) + (k % kWSlots * 2 + (w >> 1)) * KB;
+      const uint32_t kb = smem_u32(smem) + (k % w_slots(HD) * 2 + (w >> 1)) * KB;
       uint64_t sp[2][NQ][2];
       strip_scores<HD, QS, true, NQ, KS>(kb + la.code, kb + la.scale, smem_u32(qs), lane, sp);
       float sum[4] = {0.f, 0.f, 0.f, 0.f};     // keys 8 j + lane / 4
@@ -715,7 +726,7 @@ cudaError_t attend_t(const KvqAttnArgs &a, cudaStream_t s) {
 }
 template <int HD, typename T, int NQ>
 cudaError_t weights_t(const KvqAttnArgs &a, cudaStream_t s) {
-  constexpr int smem = kWSlots * 2 * kvq_k_bytes(HD) + QTile<HD, sizeof(T) == 4, NQ>::kBytes + kKvqWeightTiles / 2 * kWThreads * 4;
+  constexpr int smem = w_slots(HD) * 2 * kvq_k_bytes(HD) + QTile<HD, sizeof(T) == 4, NQ>::kBytes + kKvqWeightTiles / 2 * kWThreads * 4;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_smem(kvq_weights_kernel<HD, T, NQ>, smem, done);
   if (e != cudaSuccess) return e;
