@@ -247,6 +247,67 @@ def test_new_streams():
         check_out(out, want, mass, reach, 128, 4008 + 8 * i, "bf16", c.v[0, 0])
 
 
+def test_offsets_past_32_bits():
+    """A plane of 2^24 rows of 256 (4.8 GB), the longest a cache takes, and another behind it: every call at its end."""
+    import torch
+    import block_speculative_decoding_fm_gb300 as fm
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB of device memory")
+    rng = np.random.default_rng(48)
+    hd, n, chunk = 256, 1 << 24, 1 << 20
+    c = fm.fm_kvq_create(1, 2, 1, hd, n)
+    filler = torch.randn((chunk, 1, hd), device="cuda", dtype=torch.bfloat16)
+    tail = 333
+    for at in range(0, n, chunk):
+        fm.fm_kvq_append(c, 0, [0], filler, filler, [chunk], [at])
+    k, kv = rows(rng, tail, 1, hd, "bf16")
+    v, vv = rows(rng, tail, 1, hd, "bf16")
+    fm.fm_kvq_append(c, 0, [0], k, v, [tail], [n - tail])
+    assert fm.fm_kvq_length(c, 0, 0) == n
+    ks, vs = Q.stored(kv), Q.stored(vv)
+    back = [torch.zeros((tail, 1, hd), device="cuda") for _ in range(2)]
+    fm.fm_kvq_read(c, 0, [0], [n - tail], [tail], *back)
+    assert np.array_equal(back[0].cpu().numpy(), ks) and np.array_equal(back[1].cpu().numpy(), vs)
+    w = torch.zeros((1, 1, n), device="cuda")
+    for T, name in ((1, "bf16"), (9, "f32")):
+        q, qv = rows(rng, T, 6, hd, name)
+        out = torch.zeros_like(q)
+        fm.fm_kvq_attend(c, 0, [0], q, [T], out, causal=True, first_row=n - tail, decay=0.0, weights=w)
+        want, ww, mass, reach = Q.attend(qv, ks, vs, hd ** -0.5, True)
+        check_out(out, want, mass, reach, hd, tail, name, vs)
+        check_weights(w[0, :, n - tail:].cpu().numpy().astype(np.float64), ww, reach, hd, tail, 6 * T)
+        assert float(w[0, 0, :n - tail].abs().max()) == 0.0
+    # all rows: the filler is one chunk over and over, and a query of zeros weighs every row alike
+    out = torch.zeros((1, 6, hd), device="cuda")
+    fm.fm_kvq_attend(c, 0, [0], out.clone(), [1], out)
+    full = [torch.zeros((chunk, 1, hd), device="cuda") for _ in range(2)]
+    fm.fm_kvq_read(c, 0, [0], [0], [chunk], *full)
+    f = full[1][:, 0].double()
+    mean = (f.sum(0) * (n // chunk) - f[chunk - tail:].sum(0) + torch.from_numpy(vs[:, 0]).cuda().sum(0)) / n
+    # (equal probabilities: a sum of n / 304 rows of up to 4 in f32 a CTA, over n: n / 304 x 2^-24 x the mean |v| of 0.8)
+    assert float((out[0].double() - mean).abs().max()) <= n / 304 * 2.0 ** -24 * 0.8
+    # eviction into the plane behind: distinct weights, whose largest lie anywhere
+    order = torch.randperm(n, device="cuda", generator=torch.Generator(device="cuda").manual_seed(5))
+    fm.fm_kvq_set_weights(c, 0, [0], order.float()[None, None])
+    keep, recent = 1000, 10
+    kept = torch.zeros((1, 1, keep), dtype=torch.int32, device="cuda")
+    for dst in (1, 0):
+        fm.fm_kvq_evict(c, 0, [0], [dst], keep, recent, kept)
+        top = torch.topk(order[:n - recent], keep - recent).indices.sort().values
+        want = torch.cat([top, torch.arange(n - recent, n, device="cuda")])
+        assert torch.equal(kept[0, 0].long(), want)
+        got = [torch.zeros((keep, 1, hd), device="cuda") for _ in range(2)]
+        weights = torch.zeros((1, 1, keep), device="cuda")
+        fm.fm_kvq_read(c, 0, [dst], [0], [keep], *got, weights)
+        assert torch.equal(weights[0, 0], order[want].float())
+        src = want % chunk
+        for x, y, z in zip(got, full, (ks, vs)):
+            end = torch.from_numpy(z.astype(np.float32)).cuda()
+            ref = torch.where((want >= n - tail)[:, None, None], end[(want - (n - tail)).clamp(min=0)], y[src])
+            assert torch.equal(x, ref)
+    fm.fm_kvq_destroy(c)
+
+
 @pytest.mark.parametrize("name", ["f32", "bf16"])
 def test_query_range(name):
     """Queries up to 2^97 (and tiny ones) with a scale that brings the scores back; far beyond, and infinite: NaN, that
