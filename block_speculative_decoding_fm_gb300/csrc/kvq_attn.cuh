@@ -558,6 +558,8 @@ __global__ void __launch_bounds__(kJoinThreads) kvq_join_kernel(const __grid_con
   }
   const Stretch x(a, at, a.st0[a.n]);
   if (!Many || a.share) first = cta_of(a, x.u0), last = cta_of(a, x.u0 + a.stages[x.i] - 1);
+  // (the attention, which has begun everywhere, found what came before it done: the largest scale is there)
+  const uint32_t vm = ldg32(a.c.vmax + (size_t)a.seq[x.i] * a.c.n_kv + x.head);
   pdl_wait();   // every block, so that a later launch that waits for this one waits for what came before too
   if (first == last || (!Many && first != (int)blockIdx.x)) return;
   const int q = Many ? threadIdx.x >> 6 : 0, e = blockIdx.y * TX + threadIdx.x % TX;
@@ -579,7 +581,7 @@ __global__ void __launch_bounds__(kJoinThreads) kvq_join_kernel(const __grid_con
     if (!mine) return;
     j.add<2>(a, RT, HD, r, d, first, last, first);
   }
-  const PRange range(ldg32(a.c.vmax + (size_t)a.seq[x.i] * a.c.n_kv + x.head));
+  const PRange range(vm);
   const float inv = j.L == 0.f ? 0.f : range.undo / j.L;
   const int t = qr / a.group;
   store4(static_cast<T *>(a.out) + (a.row0[x.i] + t) * a.ldo + ((int64_t)x.head * a.group + qr - t * a.group) * HD + d,
@@ -621,7 +623,12 @@ __global__ void __launch_bounds__(kWThreads) kvq_weights_kernel(const __grid_con
     cp_async_commit();
   };
   const LaneAt<HD, KS> la((w & 1) * 32, lane);
-  for (int p = 0; p < np; ++p) acc[p * kWThreads + tid] = 0.f;
+  auto key_of = [&](int p) { return (t0 + 2 * p + (w >> 1)) * kKvqTile + (w & 1) * 32 + 8 * c + g8; };
+  float *ws = a.c.weights + plane * a.c.rows_pad;
+  for (int p = 0; p < np; ++p) {   // (what the rows collected before is there too, like the rows: below)
+    const int key = key_of(p);
+    acc[p * kWThreads + tid] = a.decay != 0.f && 2 * p + (w >> 1) < nt && key < len ? a.decay * __uint_as_float(ldg32(ws + key)) : 0.f;
+  }
   for (int rt = 0; rt < rts; ++rt) {
     if (rt) __syncthreads();
 #pragma unroll
@@ -629,7 +636,7 @@ __global__ void __launch_bounds__(kWThreads) kvq_weights_kernel(const __grid_con
     load_q<HD, QS, true, NQ, kWThreads>(static_cast<const T *>(a.q) + a.row0[i] * a.ldq + (int64_t)head * a.group * HD, a.ldq,
                                   a.group, rt * RT, R, a.scale_log2, qs, tid);
     // The attention has begun everywhere before this launch begins, and lets nothing begin before what came ahead of it
-    // is done: rows and queries are there already, its sums and the weights are what is waited for.
+    // is done: rows, weights and queries are there already, its sums are what is waited for.
     if (rt == 0) pdl_wait();
     const float *lse = a.lse + ((size_t)(a.unit0[i] + rt) * a.c.n_kv + head) * RT;
     float ls[NQ][2];
@@ -694,11 +701,10 @@ __global__ void __launch_bounds__(kWThreads) kvq_weights_kernel(const __grid_con
     }
   }
   for (int k = 0; k < np; ++k) {
-    const int t = 2 * k + (w >> 1), key = (t0 + t) * kKvqTile + (w & 1) * 32 + 8 * c + g8;
-    if (t < nt && key < len) {
-      float v = acc[k * kWThreads + tid], *p = a.c.weights + plane * a.c.rows_pad + key;
-      if (a.decay != 0.f) v = fmaf(a.decay, *p, v);
-      *p = v;
+    const int key = key_of(k);
+    if (2 * k + (w >> 1) < nt && key < len) {
+      const float v = acc[k * kWThreads + tid];
+      ws[key] = v;
       if (a.w_out) a.w_out[((size_t)(a.call0 + i) * a.c.n_kv + head) * a.ldw + key] = v;
     }
   }
