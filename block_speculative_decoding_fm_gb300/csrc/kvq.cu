@@ -29,6 +29,7 @@ struct fm_kvq {
   int device = 0, n_sm = 0;
   int rows_pad = 0;
   size_t plane_bytes = 0;
+  void *block = nullptr;          // all device memory
   uint8_t *planes = nullptr;
   float *weights = nullptr, *part_o = nullptr, *lse = nullptr;
   uint32_t *vmax = nullptr;
@@ -250,23 +251,8 @@ void deal(KvqAttnArgs &a, int64_t most, int groups, int nkv, int unit_rows) {
   a.ctas = ctas;
 }
 
-template <typename T>
-fm_status dev_alloc(fm_kvq *c, T **p, size_t n) {
-  void *q = nullptr;
-  const size_t b = (n ? n : 1) * sizeof(T);
-  if (cudaMalloc(&q, b) != cudaSuccess) {
-    cudaGetLastError();
-    return kfail(c, FM_ERR_OOM, "device allocation of %zu bytes failed", b);
-  }
-  *p = static_cast<T *>(q);
-  c->bytes += (int64_t)b;
-  return FM_OK;
-}
-
 void release(fm_kvq *c) {
-  for (void *p : {(void *)c->planes, (void *)c->weights, (void *)c->part_o, (void *)c->lse, (void *)c->vmax,
-                  (void *)c->part_ml, (void *)c->list, (void *)c->dev_err})
-    if (p) cudaFree(p);
+  if (c->block) cudaFree(c->block);
   if (c->done) cudaEventDestroy(c->done);
   delete c;
 }
@@ -280,18 +266,37 @@ fm_status setup(fm_kvq *c, cudaStream_t s) {
   c->plane_bytes = (size_t)(c->rows_pad / kKvqTile) * kvq_tile_bytes(g.head_dim);
   const size_t planes = (size_t)g.n_layers * g.n_seqs * g.n_kv_heads;
   c->slots = 2 * kKvqMaxCtas * c->n_sm;
-  KTRY(dev_alloc(c, &c->planes, planes * c->plane_bytes));
-  KTRY(dev_alloc(c, &c->weights, planes * c->rows_pad));
-  KTRY(dev_alloc(c, &c->vmax, planes));
-  KTRY(dev_alloc(c, &c->part_o, (size_t)c->slots * 8 * kKvqMaxNQ * g.head_dim));
-  KTRY(dev_alloc(c, &c->part_ml, (size_t)c->slots * 8 * kKvqMaxNQ));
-  KTRY(dev_alloc(c, &c->lse, (size_t)kMaxUnits * 8 * kKvqMaxNQ));
-  KTRY(dev_alloc(c, &c->list, (size_t)(g.n_seqs < kKvqSeqs ? g.n_seqs : kKvqSeqs) * g.n_kv_heads * c->rows_pad));
-  KTRY(dev_alloc(c, &c->dev_err, 4));
+  // one allocation, every part on a 256-byte boundary
+  const size_t sizes[8] = {planes * c->plane_bytes,
+                           planes * c->rows_pad * sizeof(float),
+                           planes * sizeof(uint32_t),
+                           (size_t)c->slots * 8 * kKvqMaxNQ * g.head_dim * sizeof(float),
+                           (size_t)c->slots * 8 * kKvqMaxNQ * sizeof(float2),
+                           (size_t)kMaxUnits * 8 * kKvqMaxNQ * sizeof(float),
+                           (size_t)(g.n_seqs < kKvqSeqs ? g.n_seqs : kKvqSeqs) * g.n_kv_heads * c->rows_pad * sizeof(int32_t),
+                           4 * sizeof(int32_t)};
+  size_t at[8], total = 0;
+  for (int i = 0; i < 8; ++i) {
+    at[i] = total;
+    total += (sizes[i] + 255) / 256 * 256;
+  }
+  // (more planes than any address space holds would wrap the product)
+  if (planes > ((size_t)1 << 48) / c->plane_bytes || cudaMalloc(&c->block, total) != cudaSuccess) {
+    cudaGetLastError();
+    return kfail(c, FM_ERR_OOM, "%zu planes of %zu bytes: the device allocation failed", planes, c->plane_bytes);
+  }
+  c->bytes = (int64_t)total;
+  uint8_t *b = static_cast<uint8_t *>(c->block);
+  c->planes = b + at[0];
+  c->weights = reinterpret_cast<float *>(b + at[1]);
+  c->vmax = reinterpret_cast<uint32_t *>(b + at[2]);
+  c->part_o = reinterpret_cast<float *>(b + at[3]);
+  c->part_ml = reinterpret_cast<float2 *>(b + at[4]);
+  c->lse = reinterpret_cast<float *>(b + at[5]);
+  c->list = reinterpret_cast<int32_t *>(b + at[6]);
+  c->dev_err = reinterpret_cast<int32_t *>(b + at[7]);
   // rows behind a sequence's end are read with the last tile: they hold finite values from the start
-  KCK(cudaMemsetAsync(c->planes, 0, planes * c->plane_bytes, s));
-  KCK(cudaMemsetAsync(c->weights, 0, planes * c->rows_pad * sizeof(float), s));
-  KCK(cudaMemsetAsync(c->vmax, 0, planes * sizeof(uint32_t), s));
+  KCK(cudaMemsetAsync(b, 0, at[3], s));   // (weights and largest scales too)
   KCK(cudaMemsetAsync(c->dev_err, 0, 16, s));
   KCK(cudaEventCreateWithFlags(&c->done, cudaEventDisableTiming));
   KCK(cudaStreamSynchronize(s));

@@ -200,6 +200,19 @@ def test_two_graphs_share_a_cache():
             assert torch.equal(out, first)
 
 
+@pytest.mark.parametrize("shape", [(1024, 65536, 256, 256, 1 << 24), (1024, 65521, 241, 64, 1 << 24), (8, 4096, 8, 128, 1 << 24)])
+def test_too_large(shape):
+    """Sizes past the device's memory, and past what 64 bits count: refused, and the next cache is made as usual."""
+    import block_speculative_decoding_fm_gb300 as fm
+    with pytest.raises(fm.FmError) as e:
+        fm.fm_kvq_create(*shape)
+    assert e.value.status == fm.FM_ERR_OOM
+    rng = np.random.default_rng(49)
+    c = Cache(1, 1, 64, 64)
+    c.append([0], [64], [0], rng)
+    assert np.array_equal(c.read(0)[0].cpu().numpy(), c.k[0, 0])
+
+
 def test_collected_under_capture():
     """A cache that is collected while its thread captures leaves the capture as it is."""
     import torch
