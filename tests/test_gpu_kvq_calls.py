@@ -108,6 +108,57 @@ def test_same_sequence_twice():
     attend_case(c, [0, 1, 0, 0, 1] * 14, [3, 1, 0, 5, 2] * 14, 2, "f16", rng, causal=True)
 
 
+def test_source_twice():
+    """One sequence read twice in a call, and branched into two others by one eviction; it stays as it is."""
+    import torch
+    rng = np.random.default_rng(50)
+    c = Cache(4, 2, 64, 200)
+    c.append([2, 3], [150, 20], [0, 0], rng, "f16")
+    w = rng.normal(size=(1, 2, 150)).astype(np.float32)
+    c.fm.fm_kvq_set_weights(c.c, 0, [2], torch.from_numpy(w).cuda())
+    k = torch.zeros((40, 2, 64), device="cuda")
+    c.fm.fm_kvq_read(c.c, 0, [2, 2, 3], [100, 90, 0], [10, 25, 5], k)
+    want = np.concatenate([c.k[0, 2][100:110], c.k[0, 2][90:115], c.k[0, 3][:5]])
+    assert np.array_equal(k.cpu().numpy(), want)
+    c.fm.fm_kvq_evict(c.c, 0, [2, 2, 3], [0, 1, 3], 60, 9)
+    assert [c.fm.fm_kvq_length(c.c, 0, s) for s in range(4)] == [60, 60, 150, 20]
+    for d in (0, 1):
+        gk, gv, gw = c.read(d)
+        for h in range(2):
+            rows_kept = Q.kept_rows(w[0, h], 60, 9)
+            assert np.array_equal(gk[:, h].cpu().numpy(), c.k[0, 2][rows_kept, h])
+            assert np.array_equal(gv[:, h].cpu().numpy(), c.v[0, 2][rows_kept, h])
+            assert np.array_equal(gw[h], w[0, h, rows_kept])
+    assert np.array_equal(c.read(2)[0].cpu().numpy(), c.k[0, 2]) and np.array_equal(c.read(3)[0].cpu().numpy(), c.k[0, 3])
+
+
+def test_nothing_to_do():
+    """Calls without rows: no query rows (weights counted or not), empty sequences, a keep of none, all rows kept."""
+    import torch
+    rng = np.random.default_rng(51)
+    c = Cache(3, 2, 128, 100)
+    c.append([0], [70], [0], rng, "bf16")
+    none = torch.empty((0, 4, 128), device="cuda")
+    before = c.read(0)
+    w = torch.full((2, 2, 100), -3.0, device="cuda")
+    for decay, weights in ((None, None), (0.0, w)):
+        c.fm.fm_kvq_attend(c.c, 0, [0, 1], none, [0, 0], none.clone(), decay=decay, weights=weights)
+    assert bool((w == -3).all())
+    out = torch.full((3, 4, 128), 5.0, device="cuda")
+    c.fm.fm_kvq_attend(c.c, 0, [1, 2], torch.ones_like(out), [1, 2], out, decay=1.0)
+    assert bool((out == 0).all())
+    kv = torch.empty((0, 2, 128), device="cuda")
+    c.fm.fm_kvq_append(c.c, 0, [1, 2], kv, kv, [0, 0], [0, 0])
+    c.fm.fm_kvq_read(c.c, 0, [1, 0], [0, 70], [0, 0], kv, kv)
+    c.fm.fm_kvq_set_weights(c.c, 0, [1, 2], torch.empty((2, 2, 0), device="cuda"))
+    c.fm.fm_kvq_evict(c.c, 0, [0, 1], [0, 1], 100, 0)
+    for x, y in zip(before, c.read(0)):
+        assert np.array_equal(np.asarray(x.cpu() if hasattr(x, "cpu") else x), np.asarray(y.cpu() if hasattr(y, "cpu") else y))
+    c.fm.fm_kvq_evict(c.c, 0, [0], [2], 0, 0)
+    assert [c.fm.fm_kvq_length(c.c, 0, s) for s in range(3)] == [70, 0, 0]
+    c.fm.fm_kvq_synchronize(c.c)
+
+
 @pytest.mark.parametrize("in_place", [True, False])
 def test_captured_calls(in_place):
     """Append, attention with weights, eviction and read in one graph: replayed on the cache as it was at the capture it
