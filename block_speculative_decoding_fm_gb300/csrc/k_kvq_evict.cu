@@ -300,7 +300,6 @@ __global__ void __launch_bounds__(kMoveThreads) kvq_move_kernel(const __grid_con
   pdl_trigger();
   pdl_wait();
   if (a.src[i] == a.dst[i]) return;
-  if (blockIdx.x == 0 && threadIdx.x == 0) a.c.vmax[pd] = a.c.vmax[ps];
   if (r0 >= left) return;
   M m;
   m.find(a.list + (size_t)pl * a.c.rows_pad, r0, left, threadIdx.x);

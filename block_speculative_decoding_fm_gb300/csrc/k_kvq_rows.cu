@@ -226,7 +226,6 @@ __global__ void __launch_bounds__(kThreads) kvq_append_kernel(const __grid_const
   constexpr int O = HD / 16;                    // lanes a row
   constexpr int RP = kThreads / O;              // rows a pass of the block
   constexpr int NP = kKvqTile / RP;
-  __shared__ float red[kThreads / 32];
   pdl_trigger();
   const int i = find_seq(a.tile0, a.n, blockIdx.x);
   const int at = a.at[i], rows = a.rows[i];
@@ -244,7 +243,6 @@ __global__ void __launch_bounds__(kThreads) kvq_append_kernel(const __grid_const
 #pragma unroll
   for (int p = 0; p < NP; ++p)
     if (first + p * RP >= 0 && first + p * RP < rows) in[p].load(src + (int64_t)p * RP * a.ld, whole);
-  float dmax = 0.f;
 #pragma unroll
   for (int p = 0; p < NP; ++p) {
     const int tr = p * RP + r0;
@@ -278,17 +276,6 @@ __global__ void __launch_bounds__(kThreads) kvq_append_kernel(const __grid_const
     *reinterpret_cast<uint2 *>(half_tile + kvq_unit(tr, g, HD) + (o & 1) * 8) = w;
     if ((o & 1) == 0) *reinterpret_cast<__half *>(half_tile + kvq_scale(tr, g, HD, isv)) = dh;
     if (!isv && o == 0) a.c.weights[plane * a.c.rows_pad + tile * kKvqTile + tr] = 0.f;
-    dmax = fmaxf(dmax, ad);
-  }
-  if (isv) {   // the plane's largest |V scale| (an upper bound that only grows: the order of the CTAs is no matter)
-    dmax = warp_max(dmax);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = dmax;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-#pragma unroll
-      for (int j = 1; j < kThreads / 32; ++j) dmax = fmaxf(dmax, red[j]);
-      atomicMax(a.c.vmax + plane, __float_as_uint(dmax));
-    }
   }
 }
 

@@ -32,7 +32,6 @@ struct fm_kvq {
   void *block = nullptr;          // all device memory
   uint8_t *planes = nullptr;
   float *weights = nullptr, *part_o = nullptr, *lse = nullptr;
-  uint32_t *vmax = nullptr;
   float2 *part_ml = nullptr;
   int32_t *list = nullptr, *dev_err = nullptr;
   int slots = 0;                  // partial results the workspace holds
@@ -91,7 +90,6 @@ KvqCache view(const fm_kvq *c, int layer) {
   v.planes = c->planes + p0 * c->plane_bytes;
   v.plane_bytes = c->plane_bytes;
   v.weights = c->weights + p0 * c->rows_pad;
-  v.vmax = c->vmax + p0;
   v.rows_pad = c->rows_pad;
   v.n_kv = c->cfg.n_kv_heads;
   v.err = c->dev_err;
@@ -267,16 +265,15 @@ fm_status setup(fm_kvq *c, cudaStream_t s) {
   const size_t planes = (size_t)g.n_layers * g.n_seqs * g.n_kv_heads;
   c->slots = 2 * kKvqMaxCtas * c->n_sm;
   // one allocation, every part on a 256-byte boundary
-  const size_t sizes[8] = {planes * c->plane_bytes,
+  const size_t sizes[7] = {planes * c->plane_bytes,
                            planes * c->rows_pad * sizeof(float),
-                           planes * sizeof(uint32_t),
                            (size_t)c->slots * 8 * kKvqMaxNQ * g.head_dim * sizeof(float),
                            (size_t)c->slots * 8 * kKvqMaxNQ * sizeof(float2),
                            (size_t)kMaxUnits * 8 * kKvqMaxNQ * sizeof(float),
                            (size_t)(g.n_seqs < kKvqSeqs ? g.n_seqs : kKvqSeqs) * g.n_kv_heads * c->rows_pad * sizeof(int32_t),
                            4 * sizeof(int32_t)};
-  size_t at[8], total = 0;
-  for (int i = 0; i < 8; ++i) {
+  size_t at[7], total = 0;
+  for (int i = 0; i < 7; ++i) {
     at[i] = total;
     total += (sizes[i] + 255) / 256 * 256;
   }
@@ -289,14 +286,13 @@ fm_status setup(fm_kvq *c, cudaStream_t s) {
   uint8_t *b = static_cast<uint8_t *>(c->block);
   c->planes = b + at[0];
   c->weights = reinterpret_cast<float *>(b + at[1]);
-  c->vmax = reinterpret_cast<uint32_t *>(b + at[2]);
-  c->part_o = reinterpret_cast<float *>(b + at[3]);
-  c->part_ml = reinterpret_cast<float2 *>(b + at[4]);
-  c->lse = reinterpret_cast<float *>(b + at[5]);
-  c->list = reinterpret_cast<int32_t *>(b + at[6]);
-  c->dev_err = reinterpret_cast<int32_t *>(b + at[7]);
+  c->part_o = reinterpret_cast<float *>(b + at[2]);
+  c->part_ml = reinterpret_cast<float2 *>(b + at[3]);
+  c->lse = reinterpret_cast<float *>(b + at[4]);
+  c->list = reinterpret_cast<int32_t *>(b + at[5]);
+  c->dev_err = reinterpret_cast<int32_t *>(b + at[6]);
   // rows behind a sequence's end are read with the last tile: they hold finite values from the start
-  KCK(cudaMemsetAsync(b, 0, at[3], s));   // (weights and largest scales too)
+  KCK(cudaMemsetAsync(b, 0, at[2], s));   // (weights too)
   KCK(cudaMemsetAsync(c->dev_err, 0, 16, s));
   KCK(cudaEventCreateWithFlags(&c->done, cudaEventDisableTiming));
   KCK(cudaStreamSynchronize(s));

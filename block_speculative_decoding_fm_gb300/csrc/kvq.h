@@ -55,7 +55,6 @@ struct KvqCache {
   uint8_t *planes;        // [seqs][kv heads] planes of plane_bytes
   size_t plane_bytes;
   float *weights;         // [seqs][kv heads][rows_pad] accumulated attention weights
-  uint32_t *vmax;         // [seqs][kv heads] bits of the largest |V scale| the plane has held
   int32_t rows_pad;       // rows of a plane (a multiple of 64)
   int32_t n_kv;
   int32_t *err;           // raised when a bounded wait gives up

@@ -228,15 +228,13 @@ __global__ void __launch_bounds__(Shape<HD, T, NQ>::kThreads, Shape<HD, T, NQ>::
     at += x.places;
     if (x.n == 0) continue;
     const int len = a.len[x.i], T_rows = a.rows[x.i], R = T_rows * a.group, rq = x.rt * RT;
-    const size_t plane = (size_t)a.seq[x.i] * a.c.n_kv + x.head;
-    const uint32_t vm = ldg32(a.c.vmax + plane);
     load_q<HD, QS, SK, NQ, NT>(static_cast<const T *>(a.q) + a.row0[x.i] * a.ldq + (int64_t)x.head * a.group * HD, a.ldq, a.group,
                            rq, R, a.scale_log2, qs, tid);
-    const PRange range(vm);
     __syncthreads();
     const int lim_all = a.causal ? len - T_rows + rq / a.group + 1 : len;   // the rows that every query row sees end here
 
     float o[GP][2][NQ][4], cor[GP][NQ][4], m[NQ][2];
+    int shift = 15;                          // of this warp's V scales
 #pragma unroll
     for (int u = 0; u < GP; ++u)
 #pragma unroll
@@ -291,7 +289,7 @@ __global__ void __launch_bounds__(Shape<HD, T, NQ>::kThreads, Shape<HD, T, NQ>::
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
         const float2 mu = *reinterpret_cast<const float2 *>(qs + QT::kMult + (8 * n + 2 * c) * 4);
-        const float b0 = range.bias - (m[n][0] == -INFINITY ? 0.f : m[n][0]), b1 = range.bias - (m[n][1] == -INFINITY ? 0.f : m[n][1]);
+        const float b0 = kBias - (m[n][0] == -INFINITY ? 0.f : m[n][0]), b1 = kBias - (m[n][1] == -INFINITY ? 0.f : m[n][1]);
         const uint64_t mm = pack2(mu.x, mu.y), bb = pack2(b0, b1);
         float x0 = -INFINITY, x1 = -INFINITY;
 #pragma unroll
@@ -351,7 +349,7 @@ __global__ void __launch_bounds__(Shape<HD, T, NQ>::kThreads, Shape<HD, T, NQ>::
             for (int u = 0; u < GP; ++u) cor[u][n][0] *= f, cor[u][n][1] *= f, cor[u][n][2] *= f, cor[u][n][3] *= f;
           }
           const float2 mu = *reinterpret_cast<const float2 *>(qs + QT::kMult + (8 * n + 2 * c) * 4);
-          const float b0 = range.bias - (n0 == -INFINITY ? 0.f : n0), b1 = range.bias - (n1 == -INFINITY ? 0.f : n1);
+          const float b0 = kBias - (n0 == -INFINITY ? 0.f : n0), b1 = kBias - (n1 == -INFINITY ? 0.f : n1);
 #pragma unroll
           for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -379,16 +377,52 @@ __global__ void __launch_bounds__(Shape<HD, T, NQ>::kThreads, Shape<HD, T, NQ>::
             const uint4 v = lds128(vscale + slot * SB + key / kKvqTile * TB + 4 * u * 128 + key % kKvqTile / 2);
             sc[kb][u][0] = v.x, sc[kb][u][1] = v.y, sc[kb][u][2] = v.z, sc[kb][u][3] = v.w;
           }
-        if (range.shifted) {
+        // Rows outside the view -- behind the end they are whatever the slot held before -- count with a scale of 0.
+        if (tile0 * kKvqTile < a.first || (tile0 + Sh::KT) * kKvqTile > len) {
+#pragma unroll
+          for (int kb = 0; kb < NB; ++kb)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int row = tile0 * kKvqTile + 32 * (kb * KP + kp) + 8 * j + 2 * c;   // (the word's low half; its high half: row + 1)
+              const uint32_t keep = (row >= a.first && row < len ? 0xffffu : 0u) | (row + 1 >= a.first && row + 1 < len ? 0xffff0000u : 0u);
+#pragma unroll
+              for (int u = 0; u < GP; ++u) sc[kb][u][j] &= keep;
+            }
+        }
+        // does one ask for a lower shift?  (2 to 3 % of the time with 16 rows; looked for ahead of P's barrier, in scales fetched
+        // twice, 9 %)
+        __half2 top2 = __habs2(h2(sc[0][0][0]));
+#pragma unroll
+        for (int kb = 0; kb < NB; ++kb)
+#pragma unroll
+          for (int u = 0; u < GP; ++u)
+#pragma unroll
+            for (int j = kb + u == 0; j < 4; ++j) top2 = __hmax2(top2, __habs2(h2(sc[kb][u][j])));
+        uint32_t top = max(u32(top2) & 0xffffu, u32(top2) >> 16);
+        if (__any_sync(0xffffffffu, top >= shift_limit(shift))) {
+          top = __reduce_max_sync(0xffffffffu, top);
+          const int to = shift_for(top);
+          const float f = pow2f(to - shift);
+          shift = to;
+#pragma unroll
+          for (int u = 0; u < GP; ++u)
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                o[u][0][n][e] *= f, o[u][1][n][e] *= f;
+                if constexpr (!SV) cor[u][n][e] *= f;
+              }
+            }
+        }
+        if (shift != 0) {
+          const __half2 up = shift_factor(shift);
 #pragma unroll
           for (int kb = 0; kb < NB; ++kb)
 #pragma unroll
             for (int u = 0; u < GP; ++u)
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&sc[kb][u][j]), range.up);
-                sc[kb][u][j] = *reinterpret_cast<const uint32_t *>(&y);
-              }
+              for (int j = 0; j < 4; ++j) sc[kb][u][j] = u32(__hmul2(h2(sc[kb][u][j]), up));
         }
 #pragma unroll
         for (int kb = 0; kb < NB; ++kb) {
@@ -434,6 +468,7 @@ __global__ void __launch_bounds__(Shape<HD, T, NQ>::kThreads, Shape<HD, T, NQ>::
       s_row[tid] = make_float2(M, L);
     }
     __syncthreads();
+    const float undo = pow2f(-shift);
     // in the values' own unit and with the rows' common references; every part but the first group's into shared memory
     float *ob = reinterpret_cast<float *>(smem + NG * NS * SB) + (size_t)((grp * KP + kp - 1) * Sh::G + (GP == 1 ? gw : wq * GP)) * (2 * NQ * 128) + lane * 4;
 #pragma unroll
@@ -441,7 +476,7 @@ __global__ void __launch_bounds__(Shape<HD, T, NQ>::kThreads, Shape<HD, T, NQ>::
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
         const float M0 = s_row[8 * n + 2 * c].x, M1 = s_row[8 * n + 2 * c + 1].x;
-        const float f0 = m[n][0] == M0 ? 1.f : ex2(m[n][0] - M0), f1 = m[n][1] == M1 ? 1.f : ex2(m[n][1] - M1);
+        const float f0 = undo * (m[n][0] == M0 ? 1.f : ex2(m[n][0] - M0)), f1 = undo * (m[n][1] == M1 ? 1.f : ex2(m[n][1] - M1));
         float c0 = 0.f, c1 = 0.f;
         if constexpr (!SV) {
           const float all = 8.f * (cor[u][n][0] + cor[u][n][2]);   // of query row lane / 4
@@ -483,7 +518,7 @@ __global__ void __launch_bounds__(Shape<HD, T, NQ>::kThreads, Shape<HD, T, NQ>::
             if (!whole) {
               *reinterpret_cast<float4 *>(a.part_o + (slot_g * RT + r) * HD + d) = y;
             } else if (qr < R) {
-              const float L = s_row[r].y, inv = L == 0.f ? 0.f : range.undo / L;
+              const float L = s_row[r].y, inv = L == 0.f ? 0.f : 1.f / L;
               const int t = qr / a.group;
               store4(static_cast<T *>(a.out) + (a.row0[x.i] + t) * a.ldo + ((int64_t)x.head * a.group + qr - t * a.group) * HD + d,
                      make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
@@ -496,7 +531,7 @@ __global__ void __launch_bounds__(Shape<HD, T, NQ>::kThreads, Shape<HD, T, NQ>::
       if (!whole)
         a.part_ml[slot_g * RT + tid] = make_float2(M, L);
       else if (lse)
-        lse[tid] = L == 0.f ? INFINITY : M + log2f(L) - range.bias;
+        lse[tid] = L == 0.f ? INFINITY : M + log2f(L) - kBias;
     }
     if (at < w_end) __syncthreads();   // the next stretch writes the queries, the references and the outputs' place
   }
@@ -558,8 +593,6 @@ __global__ void __launch_bounds__(kJoinThreads) kvq_join_kernel(const __grid_con
   }
   const Stretch x(a, at, a.st0[a.n]);
   if (!Many || a.share) first = cta_of(a, x.u0), last = cta_of(a, x.u0 + a.stages[x.i] - 1);
-  // (the attention, which has begun everywhere, found what came before it done: the largest scale is there)
-  const uint32_t vm = ldg32(a.c.vmax + (size_t)a.seq[x.i] * a.c.n_kv + x.head);
   pdl_wait();   // every block, so that a later launch that waits for this one waits for what came before too
   if (first == last || (!Many && first != (int)blockIdx.x)) return;
   const int q = Many ? threadIdx.x >> 6 : 0, e = blockIdx.y * TX + threadIdx.x % TX;
@@ -581,13 +614,12 @@ __global__ void __launch_bounds__(kJoinThreads) kvq_join_kernel(const __grid_con
     if (!mine) return;
     j.add<2>(a, RT, HD, r, d, first, last, first);
   }
-  const PRange range(vm);
-  const float inv = j.L == 0.f ? 0.f : range.undo / j.L;
+  const float inv = j.L == 0.f ? 0.f : 1.f / j.L;
   const int t = qr / a.group;
   store4(static_cast<T *>(a.out) + (a.row0[x.i] + t) * a.ldo + ((int64_t)x.head * a.group + qr - t * a.group) * HD + d,
          make_float4(j.acc.x * inv, j.acc.y * inv, j.acc.z * inv, j.acc.w * inv));
   if (a.lse && d == 0)
-    a.lse[((size_t)(a.unit0[x.i] + x.rt) * a.c.n_kv + x.head) * RT + r] = j.L == 0.f ? INFINITY : j.M + log2f(j.L) - range.bias;
+    a.lse[((size_t)(a.unit0[x.i] + x.rt) * a.c.n_kv + x.head) * RT + r] = j.L == 0.f ? INFINITY : j.M + log2f(j.L) - kBias;
 }
 
 // weights[j] = decay weights[j] + sum_r p_rj / sum_j p_rj: with every row's sum

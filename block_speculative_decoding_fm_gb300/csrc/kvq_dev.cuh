@@ -350,23 +350,27 @@ __device__ __forceinline__ void put_p(uint32_t tile, int key0, int lane, const f
   }
 }
 
-// How P' = p d is brought into f16's range: p carries 2^bias (the sums too, so
-// it leaves with the division), d carries 2^shift.  p <= 2^8 (the reference moves
-// late) and d 2^shift <= vmax 2^shift < 2^e, so bias = 7 - max(e, 0) keeps p and P'
-// below 2^15; shift raises scales below 2^-6 (exactly: f16 times a power of two).
-struct PRange {
-  float bias, undo;      // undo: 2^-shift
-  __half2 up;            // 2^shift
-  bool shifted;
-  __device__ __forceinline__ explicit PRange(uint32_t vmax_bits) {
-    const int e = max(-24, static_cast<int>(vmax_bits >> 23) - 126);
-    const int shift = e >= -6 ? 0 : min(-e, 15);
-    shifted = shift > 0;
-    bias = static_cast<float>(7 - max(e + shift, 0));
-    undo = __uint_as_float((uint32_t)(127 - shift) << 23);
-    up = __float2half2_rn(__uint_as_float((uint32_t)(127 + shift) << 23));
-  }
-};
+// How P' = p d is brought into f16's range: p carries 2^7 (the sums too, so it leaves
+// with the division) and is at most 2^15, as the reference moves when a score beats it
+// by 2^8; d carries 2^shift with |d| 2^shift < 2, so P' < 2^16.  Every warp has a shift of
+// its own for the scales it multiplies, which begins at 15 and goes down where a scale
+// of a row in view asks for it (what the warp holds is brought to the new one): 0 while the
+// largest scale is 2^-7 to 2, so that ordinary rows need no multiplication.  Raising a
+// scale is exact; lowering one keeps 2^-25 of the largest.
+constexpr float kBias = 7.f;
+// |d| from here on asks for a lower shift (f16 bits of 2^(1 - shift); infinity, which no scale is, for -15)
+__device__ __forceinline__ uint32_t shift_limit(int shift) { return (uint32_t)(16 - shift) << 10; }
+// the shift that the scale `bits`, at or over the limit, asks for: it lies in [2^(e - 1), 2^e)
+__device__ __forceinline__ int shift_for(uint32_t bits) {
+  const int e = static_cast<int>(bits >> 10) - 14;
+  return e > 1 ? max(-e, -15) : e >= -6 ? 0 : -e;
+}
+__device__ __forceinline__ __half2 shift_factor(int shift) {
+  const uint32_t h = shift > -15 ? (uint32_t)(15 + shift) << 10 : 0x200u;   // (2^-15 is a subnormal)
+  const uint32_t w = h * 0x10001u;
+  return *reinterpret_cast<const __half2 *>(&w);
+}
+__device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
 __device__ __forceinline__ __half2 h2(uint32_t w) { return *reinterpret_cast<const __half2 *>(&w); }
 __device__ __forceinline__ uint32_t u32(__half2 v) { return *reinterpret_cast<const uint32_t *>(&v); }

@@ -619,7 +619,11 @@ FM_API fm_status fm_kvq_read(fm_kvq *c, int32_t layer, int32_t n_seqs, const int
  * overlap.  Scores, softmax and sums are f32.  The cache's values enter exactly
  * as stored, f32 queries to ~22 bits (f16 and bf16 ones as they are); a
  * probability times its row's V scale is kept to ~21 bits for f32 outputs,
- * rounded to f16's 11 once for f16 ones and twice for bf16 ones.  A query row
+ * rounded to f16's 11 once for f16 ones and twice for bf16 ones, and a key's
+ * part to 2^-24 of the largest |v| of its KV head that the call sees; a
+ * probability below 2^-32 of the row's largest may count as 0.  Rows that the
+ * call does not see (behind the length, ahead of first_row, overwritten or
+ * evicted) have no part in any of it.  A query row
  * with a NaN or an infinity gives NaN, and one with values past 2^97 may.
  * decay >= 0 also counts the attention weight each cache row collects, per KV
  * head:  w_j = decay w_j + sum over the call's rows and the KV head's query
