@@ -532,17 +532,20 @@ fm_status mtp_checks(fm_mtp *m, int M, const int32_t *tokens, const float *hn, i
   if (!tokens || !hn) return mfail(m, FM_ERR_INVALID_ARG, "null tokens or hidden rows");
   if (pos0 < 0 || kv_lo < 0 || kv_lo > pos0) return mfail(m, FM_ERR_INVALID_ARG, "kv_lo %d outside [0, pos0 %d]", kv_lo, pos0);
   if (m->kvq) return FM_OK;   // (the 4-bit cache's own size counts)
-  if (pos0 + M > c.kv_cap) return mfail(m, FM_ERR_INVALID_ARG, "pos0 + n_rows = %d > kv_cap %d", pos0 + M, c.kv_cap);
+  const int64_t end = (int64_t)pos0 + M;
+  if (end > c.kv_cap) return mfail(m, FM_ERR_INVALID_ARG, "pos0 + n_rows = %lld > kv_cap %d", (long long)end, c.kv_cap);
   return FM_OK;
 }
 
 // with a 4-bit cache: `rows` rows from pos0 on fit, before anything is launched
-fm_status mtp_kvq_checks(fm_mtp *m, int rows, int pos0, int kv_lo) {
+fm_status mtp_kvq_checks(fm_mtp *m, int64_t rows, int pos0, int kv_lo) {
   if (!m->kvq) return FM_OK;
   int32_t row = 0;
   MTRY(kvq_row_of(m, pos0, &row));
-  if (row + (int64_t)rows > m->kvq_rows)
-    return mfail(m, FM_ERR_CONTEXT_FULL, "row %d + %d rows, the 4-bit cache holds %d", row, rows, m->kvq_rows);
+  if (row + rows > m->kvq_rows)
+    return mfail(m, FM_ERR_CONTEXT_FULL, "row %d + %lld rows, the 4-bit cache holds %d", row, (long long)rows, m->kvq_rows);
+  if (pos0 + rows > INT32_MAX)
+    return mfail(m, FM_ERR_INVALID_ARG, "pos0 %d + %lld rows: positions end at %d", pos0, (long long)rows, INT32_MAX);
   if (kv_lo > 0 && row != pos0)
     return mfail(m, FM_ERR_UNSUPPORTED, "kv_lo %d after an eviction: rows are no longer at their positions", kv_lo);
   return FM_OK;
@@ -672,9 +675,11 @@ fm_status fm_mtp_draft(fm_mtp *m, int32_t n_rows, const int32_t *tokens_dev, con
   m->last_launches = 0;
   MTRY(mtp_checks(m, n_rows, tokens_dev, hn_dev, pos0, kv_lo));
   if (!drafts_dev) return mfail(m, FM_ERR_INVALID_ARG, "null drafts");
-  if (depth < 1 || (!m->kvq && pos0 + n_rows + depth - 1 > m->cfg.kv_cap))
+  const int64_t all = (int64_t)n_rows + depth - 1;   // rows of all passes
+  if (depth < 1) return mfail(m, FM_ERR_INVALID_ARG, "depth %d", depth);
+  if (!m->kvq && pos0 + all > m->cfg.kv_cap)
     return mfail(m, FM_ERR_INVALID_ARG, "depth %d outside [1, %d]", depth, m->cfg.kv_cap - pos0 - n_rows + 1);
-  MTRY(mtp_kvq_checks(m, n_rows + depth - 1, pos0, kv_lo));
+  MTRY(mtp_kvq_checks(m, all, pos0, kv_lo));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int H = m->cfg.hidden;
   MTRY(mtp_pass(m, n_rows, tokens_dev, hn_dev, H, pos0, kv_lo, nullptr, s));

@@ -172,3 +172,44 @@ def test_refusals():
     fm.fm_mtp_use_kvq(h, None)                                   # the own cache, as it was
     assert np.array_equal(fm.fm_mtp_cache(h, 0, 4, np.empty_like(own)), own)
     fm.fm_mtp_destroy(h)
+
+
+def test_sums_past_32_bits():
+    """Depths and positions whose sums pass 2^31 are refused before anything is launched, with the 4-bit cache and without."""
+    import torch
+    import block_speculative_decoding_fm_gb300 as fm
+    cfg = S.mtp_micro_config(kv_cap=16)
+    h = fm.fm_mtp_create(cfg, fm.weight_items(S.gen_mtp_weights(cfg, 1306)))
+    t = torch.zeros((8,), dtype=torch.int32, device="cuda")
+    hn = torch.zeros((8, cfg.hidden), dtype=torch.float32, device="cuda")
+    d = torch.zeros((8,), dtype=torch.int32, device="cuda")
+    top = 2 ** 31 - 1
+
+    def bad(status, f, *a):
+        with pytest.raises(fm.FmError) as e:
+            f(*a)
+        assert e.value.status == status, e.value
+        assert fm.fm_mtp_last_launch_count(h) == 0
+
+    inv = fm.FM_ERR_INVALID_ARG
+    bad(inv, fm.fm_mtp_forward, h, t, hn, top, 0)
+    bad(inv, fm.fm_mtp_forward, h, t, hn, top - 7, 0)
+    for depth in (top, top - 1, top - 8, 0, -1):
+        bad(inv, fm.fm_mtp_draft, h, t, hn, 0, 0, depth, d)
+        bad(inv, fm.fm_mtp_draft, h, t[:1], hn[:1], 15, 0, depth, d)
+    c = fm.fm_kvq_create(1, 1, cfg.n_kv_heads, cfg.head_dim, 40)
+    fm.fm_mtp_use_kvq(h, c)
+    for depth in (top, top - 1, top - 6, top - 7, 34):
+        bad(fm.FM_ERR_CONTEXT_FULL, fm.fm_mtp_draft, h, t, hn, 0, 0, depth, d)
+    bad(inv, fm.fm_mtp_draft, h, t, hn, 0, 0, 0, d)
+    bad(inv, fm.fm_mtp_draft, h, t, hn, 0, 0, -2 ** 31, d)
+    assert fm.fm_kvq_length(c, 0, 0) == 0
+    # late positions, as after evictions
+    fm.fm_mtp_use_kvq(h, c, next_pos=top - 3)
+    bad(inv, fm.fm_mtp_forward, h, t, hn, top - 3, 0)
+    bad(inv, fm.fm_mtp_forward, h, t[:4], hn[:4], top - 3, 0)
+    bad(inv, fm.fm_mtp_draft, h, t[:2], hn[:2], top - 3, 0, 3, d)
+    fm.fm_mtp_forward(h, t[:3], hn[:3], top - 3, 0)
+    bad(inv, fm.fm_mtp_forward, h, t[:1], hn[:1], top, 0)
+    assert fm.fm_kvq_length(c, 0, 0) == 3
+    fm.fm_mtp_destroy(h)
