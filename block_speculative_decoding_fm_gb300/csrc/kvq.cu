@@ -48,6 +48,8 @@ struct fm_kvq {
   char err[512] = "";
 };
 
+int fm::kvq_device(const fm_kvq *c) { return c->device; }
+
 namespace {
 
 constexpr int kMaxUnits = 1 << 15;   // (row tile, KV head) units of a launch

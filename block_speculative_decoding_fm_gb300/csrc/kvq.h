@@ -20,7 +20,11 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+struct fm_kvq;
+
 namespace fm {
+
+int kvq_device(const fm_kvq *c);   // the device that a cache is on
 
 constexpr int kKvqTile = 64;       // rows a tile
 constexpr int kKvqSeqs = 64;       // sequences a launch

@@ -24,6 +24,7 @@
 #include "../../include/fm.h"
 #include "dev_common.cuh"
 #include "fm_internal.h"
+#include "kvq.h"
 
 namespace fm {
 namespace {
@@ -291,7 +292,7 @@ using namespace fm;
 struct fm_mtp {
   fm_mtp_config cfg{};
   std::string err;
-  int n_sm = 0;
+  int device = 0, n_sm = 0;
   std::vector<void *> allocs;
   // a Q8_0 product: the repacked table (slices of K in tile order), out features, in features, slices
   struct Lin {
@@ -540,6 +541,9 @@ fm_status mtp_checks(fm_mtp *m, int M, const int32_t *tokens, const float *hn, i
 // with a 4-bit cache: `rows` rows from pos0 on fit, before anything is launched
 fm_status mtp_kvq_checks(fm_mtp *m, int64_t rows, int pos0, int kv_lo) {
   if (!m->kvq) return FM_OK;
+  int dev = -1;
+  MCK(cudaGetDevice(&dev));
+  if (dev != m->device) return mfail(m, FM_ERR_INVALID_ARG, "the current device is %d, the head's and its 4-bit cache's is %d", dev, m->device);
   int32_t row = 0;
   MTRY(kvq_row_of(m, pos0, &row));
   if (row + rows > m->kvq_rows)
@@ -579,9 +583,8 @@ fm_status fm_mtp_create(const fm_mtp_config *cfg, const fm_tensor *weights, int3
   std::unordered_map<std::string, const fm_tensor *> ts;
   for (int i = 0; i < n_weights; ++i)
     if (weights[i].name) ts[weights[i].name] = &weights[i];
-  int dev = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&m->n_sm, cudaDevAttrMultiProcessorCount, dev);
+  cudaGetDevice(&m->device);
+  cudaDeviceGetAttribute(&m->n_sm, cudaDevAttrMultiProcessorCount, m->device);
   fm_status st;
 #define STEP(expr)              \
   if ((st = (expr)) != FM_OK) { \
@@ -708,6 +711,8 @@ fm_status fm_mtp_use_kvq(fm_mtp *m, fm_kvq *c, int32_t layer, int32_t seq, int64
   if (g.n_kv_heads != m->cfg.n_kv_heads || g.head_dim != m->cfg.head_dim)
     return mfail(m, FM_ERR_INVALID_ARG, "the 4-bit cache has %d heads of %d, the head %d of %d", g.n_kv_heads, g.head_dim,
                  m->cfg.n_kv_heads, m->cfg.head_dim);
+  if (kvq_device(c) != m->device)
+    return mfail(m, FM_ERR_INVALID_ARG, "the 4-bit cache is on device %d, the head on %d", kvq_device(c), m->device);
   if (next_pos < len || next_pos > INT32_MAX) return mfail(m, FM_ERR_INVALID_ARG, "next_pos %lld with %d rows", (long long)next_pos, len);
   if (!std::isfinite(decay)) return mfail(m, FM_ERR_INVALID_ARG, "decay is not finite");
   if (!m->ao) {

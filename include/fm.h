@@ -697,10 +697,10 @@ FM_API void fm_kvq_destroy(fm_kvq *c);
  *     for an eviction; < 0 does not.
  * Passes then also fail with FM_ERR_STATE (pos0 > next_pos, or a rewind past
  * the rows that are left), FM_ERR_CONTEXT_FULL (the rows do not fit c),
- * FM_ERR_INVALID_ARG (positions past 2^31 - 1) and FM_ERR_UNSUPPORTED (kv_lo > 0
- * after an eviction); nothing is launched then.
+ * FM_ERR_INVALID_ARG (positions past 2^31 - 1, another current device) and
+ * FM_ERR_UNSUPPORTED (kv_lo > 0 after an eviction); nothing is launched then.
  * fm_mtp_cache with rows > 0 answers FM_ERR_STATE.
- * Errors: FM_ERR_INVALID_ARG (other heads or head_dim, no such layer or
+ * Errors: FM_ERR_INVALID_ARG (another device, other heads or head_dim, no such layer or
  *   sequence, next_pos below the length, decay not finite), FM_ERR_OOM.
  */
 FM_API fm_status fm_mtp_use_kvq(fm_mtp *m, fm_kvq *c, int32_t layer, int32_t seq, int64_t next_pos, float decay);

@@ -213,3 +213,27 @@ def test_sums_past_32_bits():
     bad(inv, fm.fm_mtp_forward, h, t[:1], hn[:1], top, 0)
     assert fm.fm_kvq_length(c, 0, 0) == 3
     fm.fm_mtp_destroy(h)
+
+
+def test_devices():
+    """A cache of another device is refused, and so is a pass while another device is the current one."""
+    import torch
+    import block_speculative_decoding_fm_gb300 as fm
+    if torch.cuda.device_count() < 2:
+        pytest.skip("needs two devices")
+    cfg = S.mtp_micro_config(kv_cap=16)
+    h = fm.fm_mtp_create(cfg, fm.weight_items(S.gen_mtp_weights(cfg, 1307)))
+    c = fm.fm_kvq_create(1, 1, cfg.n_kv_heads, cfg.head_dim, 20)
+    with torch.cuda.device(1):
+        other = fm.fm_kvq_create(1, 1, cfg.n_kv_heads, cfg.head_dim, 20)
+    with pytest.raises(fm.FmError) as e:
+        fm.fm_mtp_use_kvq(h, other)
+    assert e.value.status == fm.FM_ERR_INVALID_ARG
+    fm.fm_mtp_use_kvq(h, c)
+    t = torch.zeros((2,), dtype=torch.int32, device="cuda:0")
+    hn = torch.zeros((2, cfg.hidden), dtype=torch.float32, device="cuda:0")
+    with torch.cuda.device(1), pytest.raises(fm.FmError) as e:
+        fm.fm_mtp_forward(h, t, hn, 0, 0)
+    assert e.value.status == fm.FM_ERR_INVALID_ARG and fm.fm_mtp_last_launch_count(h) == 0
+    fm.fm_mtp_forward(h, t, hn, 0, 0)
+    fm.fm_mtp_destroy(h)
