@@ -40,7 +40,7 @@ EXPORTS = ["fm_create", "fm_time_conditioning", "fm_context_append", "fm_context
            "fm_mtp_last_error", "fm_mtp_destroy",
            "fm_kvq_create", "fm_kvq_append", "fm_kvq_read", "fm_kvq_attend", "fm_kvq_set_weights", "fm_kvq_evict",
            "fm_kvq_length", "fm_kvq_get_config", "fm_kvq_last_launch_count", "fm_mtp_use_kvq",
-           "fm_kvq_memory_bytes", "fm_kvq_synchronize", "fm_kvq_last_error", "fm_kvq_destroy"]
+           "fm_kvq_memory_bytes", "fm_kvq_synchronize", "fm_kvq_selftest_wait_timeout", "fm_kvq_last_error", "fm_kvq_destroy"]
 
 
 class FmConfig(ctypes.Structure):
@@ -151,6 +151,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "fm_mtp_use_kvq": (I32, [P, P, I32, I32, I64, ctypes.c_float]),
         "fm_kvq_memory_bytes": (I32, [P, ctypes.POINTER(I64)]),
         "fm_kvq_synchronize": (I32, [P, P]),
+        "fm_kvq_selftest_wait_timeout": (I32, [P, I32, P]),
         "fm_kvq_last_error": (ctypes.c_char_p, [P]),
         "fm_kvq_destroy": (None, [P]),
     }
@@ -708,6 +709,12 @@ def fm_kvq_memory_bytes(c) -> int:
 def fm_kvq_synchronize(c, stream=None) -> None:
     """Wait for the stream; raise FmError(FM_ERR_TIMEOUT) if a bounded device wait gave up since the last check."""
     _kvq_check(load_library().fm_kvq_synchronize(c, _stream(stream)), c)
+
+
+def fm_kvq_selftest_wait_timeout(c, budget_us: int, stream=None) -> None:
+    """Run a bounded device wait that cannot complete; it gives up after budget_us and the next fm_kvq_synchronize raises
+    FmError(FM_ERR_TIMEOUT)."""
+    _kvq_check(load_library().fm_kvq_selftest_wait_timeout(c, budget_us, _stream(stream)), c)
 
 
 def fm_kvq_destroy(c) -> None:

@@ -15,6 +15,7 @@
 #include <vector>
 
 #include "../../include/fm.h"
+#include "fm_internal.h"
 #include "kvq.h"
 
 using namespace fm;
@@ -673,6 +674,19 @@ fm_status fm_kvq_synchronize(fm_kvq *c, void *stream) {
     KCK(cudaMemsetAsync(c->dev_err, 0, 4, s));
     return kfail(c, FM_ERR_TIMEOUT, "a bounded device wait gave up");
   }
+  return FM_OK;
+}
+
+fm_status fm_kvq_selftest_wait_timeout(fm_kvq *c, int32_t budget_us, void *stream) {
+  if (!c) return FM_ERR_INVALID_ARG;
+  if (budget_us < 1 || budget_us > 1000000) return kfail(c, FM_ERR_INVALID_ARG, "budget_us outside [1, 1000000]");
+  int dev = -1, khz = 0;
+  KCK(cudaGetDevice(&dev));
+  if (dev != c->device) return kfail(c, FM_ERR_INVALID_ARG, "the current device is %d, the cache's is %d", dev, c->device);
+  KCK(cudaDeviceGetAttribute(&khz, cudaDevAttrClockRate, dev));
+  if (khz <= 0) khz = 2000000;
+  KCK(launch_wait_selftest(c->dev_err, (long long)budget_us * (khz / 1000), static_cast<cudaStream_t>(stream)));
+  c->launches = 1;
   return FM_OK;
 }
 

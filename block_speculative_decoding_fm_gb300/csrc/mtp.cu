@@ -746,6 +746,10 @@ fm_status fm_mtp_cache(fm_mtp *m, int32_t which, int32_t rows, float *dst, void 
     return e == 2 ? mfail(m, FM_ERR_INVALID_ARG, "a token outside [0, vocab) reached the embedding")
                   : mfail(m, FM_ERR_TIMEOUT, "a bounded device wait gave up");
   }
+  if (m->kvq) {   // (the passes' attention raises the cache's word)
+    const fm_status st = fm_kvq_synchronize(m->kvq, stream);
+    if (st != FM_OK) return mfail(m, st, "4-bit cache: %s", fm_kvq_last_error(m->kvq));
+  }
   return FM_OK;
 }
 

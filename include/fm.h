@@ -677,6 +677,9 @@ FM_API fm_status fm_kvq_last_launch_count(const fm_kvq *c, int32_t *count);
 FM_API fm_status fm_kvq_memory_bytes(const fm_kvq *c, int64_t *bytes);
 /* Wait for the stream; FM_ERR_TIMEOUT if a bounded device wait gave up since the last check (cleared). */
 FM_API fm_status fm_kvq_synchronize(fm_kvq *c, void *stream);
+/* fm_selftest_wait_timeout for a cache: a bounded wait that gives up after budget_us (1 .. 1e6) raises the cache's error
+   word, which the next fm_kvq_synchronize reports.  Errors: FM_ERR_INVALID_ARG, FM_ERR_CUDA. */
+FM_API fm_status fm_kvq_selftest_wait_timeout(fm_kvq *c, int32_t budget_us, void *stream);
 FM_API const char *fm_kvq_last_error(const fm_kvq *c);   /* never NULL; NULL c: the last failed fm_kvq_create */
 /* Free everything the cache owns, once the calls issued so far are done.  NULL is ignored; a capture in progress goes on. */
 FM_API void fm_kvq_destroy(fm_kvq *c);
@@ -699,7 +702,8 @@ FM_API void fm_kvq_destroy(fm_kvq *c);
  * the rows that are left), FM_ERR_CONTEXT_FULL (the rows do not fit c),
  * FM_ERR_INVALID_ARG (positions past 2^31 - 1, another current device) and
  * FM_ERR_UNSUPPORTED (kv_lo > 0 after an eviction); nothing is launched then.
- * fm_mtp_cache with rows > 0 answers FM_ERR_STATE.
+ * fm_mtp_cache with rows > 0 answers FM_ERR_STATE; with rows = 0 it also reports
+ * (and clears) a bounded wait of c's that gave up, as fm_kvq_synchronize does.
  * Errors: FM_ERR_INVALID_ARG (another device, other heads or head_dim, no such layer or
  *   sequence, next_pos below the length, decay not finite), FM_ERR_OOM.
  */

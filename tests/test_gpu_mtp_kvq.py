@@ -237,3 +237,38 @@ def test_devices():
     assert e.value.status == fm.FM_ERR_INVALID_ARG and fm.fm_mtp_last_launch_count(h) == 0
     fm.fm_mtp_forward(h, t, hn, 0, 0)
     fm.fm_mtp_destroy(h)
+
+
+def test_wait_that_gives_up():
+    """A bounded wait that gives up: the cache reports it once, and so does the head that uses the cache."""
+    import torch
+    import block_speculative_decoding_fm_gb300 as fm
+    cfg = S.mtp_micro_config(kv_cap=16)
+    h = fm.fm_mtp_create(cfg, fm.weight_items(S.gen_mtp_weights(cfg, 1308)))
+    c = fm.fm_kvq_create(1, 1, cfg.n_kv_heads, cfg.head_dim, 20)
+    none = np.empty((1,), np.float32)
+
+    def timeout(f, *a):
+        with pytest.raises(fm.FmError) as e:
+            f(*a)
+        assert e.value.status == fm.FM_ERR_TIMEOUT, e.value
+        f(*a)                                          # reported once
+
+    for budget in (0, 1000001):
+        with pytest.raises(fm.FmError) as e:
+            fm.fm_kvq_selftest_wait_timeout(c, budget)
+        assert e.value.status == fm.FM_ERR_INVALID_ARG
+    fm.fm_kvq_synchronize(c)
+    fm.fm_kvq_selftest_wait_timeout(c, 20000)
+    timeout(fm.fm_kvq_synchronize, c)
+    fm.fm_mtp_use_kvq(h, c)
+    t = torch.zeros((2,), dtype=torch.int32, device="cuda")
+    hn = torch.zeros((2, cfg.hidden), dtype=torch.float32, device="cuda")
+    fm.fm_mtp_forward(h, t, hn, 0, 0)
+    fm.fm_mtp_cache(h, 0, 0, none)
+    fm.fm_kvq_selftest_wait_timeout(c, 20000)
+    fm.fm_mtp_forward(h, t, hn, 2, 0)
+    timeout(fm.fm_mtp_cache, h, 0, 0, none)
+    fm.fm_mtp_forward(h, t, hn, 2, 0)                  # the head and the cache stay usable
+    fm.fm_mtp_cache(h, 0, 0, none)
+    fm.fm_mtp_destroy(h)
