@@ -142,6 +142,11 @@ fm_status type_of(fm_kvq *c, int dtype, int32_t *type, int *size) {
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
+fm_status check_words(fm_kvq *c, const char *what, const void *p) {
+  if (reinterpret_cast<uintptr_t>(p) & 3) return kfail(c, FM_ERR_INVALID_ARG, "%s: a misaligned pointer (4 bytes)", what);
+  return FM_OK;
+}
+
 fm_status check_rows(fm_kvq *c, const char *what, const void *p, int64_t ld, int64_t width, int size) {
   if (!p || !aligned16(p)) return kfail(c, FM_ERR_INVALID_ARG, "%s: a null or misaligned pointer (16 bytes)", what);
   if (ld < width || (ld * size) % 16)
@@ -415,6 +420,7 @@ fm_status fm_kvq_read(fm_kvq *c, int32_t layer, int32_t n_seqs, const int32_t *s
     total += n_rows_host[i];
     most = n_rows_host[i] > most ? n_rows_host[i] : most;
   }
+  KTRY(check_words(c, "weights", weights_dev));
   const int64_t width = (int64_t)c->cfg.n_kv_heads * c->cfg.head_dim;
   if (total > 0) {
     if (k_dev) KTRY(check_rows(c, "k", k_dev, ld, width, size));
@@ -466,6 +472,7 @@ fm_status fm_kvq_set_weights(fm_kvq *c, int32_t layer, int32_t n_seqs, const int
   for (int i = 0; i < n_seqs; ++i) most = len[seq_ids_host[i]] > most ? len[seq_ids_host[i]] : most;
   if (most > 0 && (!weights_dev || ldw < most))
     return kfail(c, FM_ERR_INVALID_ARG, "weights: null, or row stride %lld with %d rows", (long long)ldw, most);
+  KTRY(check_words(c, "weights", weights_dev));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   KTRY(begin(c, s));
   KvqRowsArgs a;
@@ -503,6 +510,7 @@ fm_status fm_kvq_attend(fm_kvq *c, int32_t layer, int32_t n_seqs, const int32_t 
   if (first_row > c->cfg.max_rows) first_row = c->cfg.max_rows;   // (past every row either way)
   if (!(decay == decay) || std::isinf(decay)) return kfail(c, FM_ERR_INVALID_ARG, "decay is not finite");
   const bool keep_w = decay >= 0.f;
+  KTRY(check_words(c, "weights", weights_dev));
   if (!keep_w && weights_dev) return kfail(c, FM_ERR_INVALID_ARG, "weights wanted, but decay < 0 keeps none");
   if (keep_w) KTRY(check_distinct(c, n_seqs, seq_ids_host));
   const int32_t *len = lengths(c, layer);
@@ -611,6 +619,7 @@ fm_status fm_kvq_evict(fm_kvq *c, int32_t layer, int32_t n_seqs, const int32_t *
   KTRY(check_call(c, layer, n_seqs, dst_ids_host));
   if (keep < 0 || keep > c->cfg.max_rows || recent < 0 || recent > keep)
     return kfail(c, FM_ERR_INVALID_ARG, "keep %d (of at most %d), recent %d", keep, c->cfg.max_rows, recent);
+  KTRY(check_words(c, "kept rows", kept_dev));
   KTRY(check_distinct(c, n_seqs, dst_ids_host));
   // a sequence that is written is read by its own move alone
   for (int i = 0; i < n_seqs; ++i)

@@ -559,8 +559,8 @@ FM_API void fm_mtp_destroy(fm_mtp *m);
  * replayed one after another, and ordered with eager calls, by the caller, and
  * not after fm_kvq_destroy.  The cache's device must be the current device.  Device pointers are 16-byte
  * aligned, and row strides (ld, ldq, ldo: elements between rows) whole
- * multiples of 16 bytes; pointers and strides of weights and kept rows need 4
- * bytes.  One host thread at a time per cache.
+ * multiples of 16 bytes; pointers to weights and kept rows are 4-byte aligned
+ * (FM_ERR_INVALID_ARG otherwise).  One host thread at a time per cache.
  * ------------------------------------------------------------------------ */
 typedef struct fm_kvq_config {
   int32_t n_layers;    /* 1 .. 1024 */

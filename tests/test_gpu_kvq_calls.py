@@ -395,6 +395,32 @@ def test_query_range(name):
             assert len(ok) == 4 or bool(torch.isnan(out[2:]).all())
 
 
+def test_misaligned_words():
+    """Pointers to weights and kept rows that are no whole words are refused, and nothing moves."""
+    import ctypes
+    import torch
+    import block_speculative_decoding_fm_gb300 as fm
+    c = fm.fm_kvq_create(1, 1, 1, 64, 40)
+    x = torch.ones((30, 1, 64), device="cuda")
+    fm.fm_kvq_append(c, 0, [0], x, x, [30], [0])
+    lib = fm.load_library()
+    room = torch.zeros(200, device="cuda")
+    one = (ctypes.c_int32 * 1)
+    s, n, zero = one(0), one(30), one(0)
+    q, o = torch.ones((1, 1, 64), device="cuda"), torch.zeros((1, 1, 64), device="cuda")
+    stream = torch.cuda.current_stream().cuda_stream
+    for off in (1, 2, 3):
+        p = ctypes.c_void_p(room.data_ptr() + off)
+        assert lib.fm_kvq_read(c, 0, 1, s, zero, n, None, None, fm.FM_DTYPE_F32, 64, p, 40, stream) == fm.FM_ERR_INVALID_ARG
+        assert lib.fm_kvq_set_weights(c, 0, 1, s, p, 40, stream) == fm.FM_ERR_INVALID_ARG
+        assert lib.fm_kvq_attend(c, 0, 1, s, one(1), q.data_ptr(), fm.FM_DTYPE_F32, 1, 64, 0.125, 0, 0, o.data_ptr(), 64, 1.0, p,
+                                 40, stream) == fm.FM_ERR_INVALID_ARG
+        assert lib.fm_kvq_evict(c, 0, 1, s, s, 10, 2, p, stream) == fm.FM_ERR_INVALID_ARG
+        assert b"misaligned" in lib.fm_kvq_last_error(c)
+    fm.fm_kvq_synchronize(c)
+    assert fm.fm_kvq_length(c, 0, 0) == 30 and not bool(room.any()) and not bool(o.any())
+
+
 def runtime():
     import ctypes
     import glob
