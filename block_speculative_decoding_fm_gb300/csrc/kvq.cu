@@ -185,14 +185,20 @@ fm_status end(fm_kvq *c, cudaStream_t s) {
   return FM_OK;
 }
 
+// Stages of a unit over `len` rows of which those from `first` on are seen: one at least.
+int stages_of(int len, int first, int stage_rows) {
+  const int s0 = first / stage_rows, s1 = (len + stage_rows - 1) / stage_rows;
+  return s1 > s0 ? s1 - s0 : 1;
+}
+
 // The octets of query rows that a unit carries, 0 where the call has too many units.  A stage costs about 1 + nq (its codes
 // are unpacked once, then used for each octet), beginning and ending a unit 5 nq (9 nq for 256 dims) of the same: short
 // caches want many narrow units, long ones few wide ones.  (8 rows of 24 heads over 4 KV heads of 256, f32: 64 rows 4.8 us
 // with nq 1, 8.6 with 3; 16384 rows 36.7 and 29.2.  16 rows of 16 heads of 128, bf16: 4161 rows 9.7 us with nq 1, 10.0 with
 // 2; 16384 rows 18.9 and 16.7.)  In the pass over the weights a CTA takes a sequence's row tiles one after another, about 7
 // each.  (With weights, 8 rows of 32 heads over 8 KV heads of 128, 1042 rows: 11.6 us, 15.0 without that term.)
-int choose_nq(int n_seqs, const int32_t *seq, const int32_t *rows, const int32_t *len, int group, int nkv, int hd, int n_sm,
-              int64_t widest, bool weights) {
+int choose_nq(int n_seqs, const int32_t *seq, const int32_t *rows, const int32_t *len, int first, int group, int nkv, int hd,
+              int n_sm, int64_t widest, bool weights) {
   const int stage_rows = kKvqTile * kvq_stage_tiles(hd), most = (int)(widest < 8 * kKvqMaxNQ ? (widest + 7) / 8 : kKvqMaxNQ);
   int best = 0;
   int64_t least = 0;
@@ -201,7 +207,7 @@ int choose_nq(int n_seqs, const int32_t *seq, const int32_t *rows, const int32_t
     bool fits = true;
     for (int i = 0; i < n_seqs; ++i) {
       const int64_t units = ((int64_t)rows[i] * group + 8 * nq - 1) / (8 * nq) * nkv;
-      const int stages = (len[seq[i]] + stage_rows - 1) / stage_rows;
+      const int stages = stages_of(len[seq[i]], first, stage_rows);
       fits = fits && units <= kMaxUnits && units * (stages + kKvqUnitCost) <= INT_MAX;
       work += units * stages;
     }
@@ -528,7 +534,8 @@ fm_status fm_kvq_attend(fm_kvq *c, int32_t layer, int32_t n_seqs, const int32_t 
     total += n;
     if (n > 0 && len[seq_ids_host[i]] > most) most = len[seq_ids_host[i]];
   }
-  const int nq = choose_nq(n_seqs, seq_ids_host, n_rows_host, len, group, nkv, hd, c->n_sm, widest, keep_w), unit_rows = 8 * nq;
+  const int nq = choose_nq(n_seqs, seq_ids_host, n_rows_host, len, first_row, group, nkv, hd, c->n_sm, widest, keep_w),
+            unit_rows = 8 * nq;
   if (!nq) return kfail(c, FM_ERR_UNSUPPORTED, "%lld query rows of a KV head in one call", (long long)widest);
   const int64_t width = (int64_t)n_heads * hd;
   if (total > 0) {
@@ -570,7 +577,7 @@ fm_status fm_kvq_attend(fm_kvq *c, int32_t layer, int32_t n_seqs, const int32_t 
       const int n = n_rows_host[i], L = len[seq_ids_host[i]], j = a.n;
       const int rts = (int)(((int64_t)n * group + unit_rows - 1) / unit_rows);
       const int t1 = (L + kKvqTile - 1) / kKvqTile;
-      const int s0 = first_row / stage_rows, s1 = (L + stage_rows - 1) / stage_rows, stages = s1 > s0 ? s1 - s0 : 1;
+      const int stages = stages_of(L, first_row, stage_rows);
       const int64_t more = (int64_t)rts * nkv * (stages + kKvqUnitCost);
       if (j && (units + (int64_t)rts * nkv > kMaxUnits || work + more > INT_MAX)) break;
       a.seq[j] = seq_ids_host[i];

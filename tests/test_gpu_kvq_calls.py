@@ -421,6 +421,33 @@ def test_misaligned_words():
     assert fm.fm_kvq_length(c, 0, 0) == 30 and not bool(room.any()) and not bool(o.any())
 
 
+def test_window_over_a_long_cache():
+    """65,536 query rows of 8 heads over the last rows of 2^24: a call goes by the rows that it sees, not by those before
+    them."""
+    import torch
+    import block_speculative_decoding_fm_gb300 as fm
+    if torch.cuda.mem_get_info()[0] < 20 << 30:
+        pytest.skip("needs 20 GB of device memory")
+    rng = np.random.default_rng(51)
+    hd, n, chunk, tail, T, H = 64, 1 << 24, 1 << 21, 200, 1 << 16, 8
+    c = fm.fm_kvq_create(1, 1, 1, hd, n)
+    filler = torch.ones((chunk, 1, hd), device="cuda", dtype=torch.bfloat16)
+    for at in range(0, n, chunk):
+        fm.fm_kvq_append(c, 0, [0], filler, filler, [chunk], [at])
+    k, kv = rows(rng, tail, 1, hd, "bf16")
+    v, vv = rows(rng, tail, 1, hd, "bf16")
+    fm.fm_kvq_append(c, 0, [0], k, v, [tail], [n - tail])
+    ks, vs = Q.stored(kv), Q.stored(vv)
+    q = torch.randn((T, H, hd), device="cuda", generator=torch.Generator(device="cuda").manual_seed(3)).to(torch.bfloat16)
+    out = torch.full_like(q, 9.0)
+    fm.fm_kvq_attend(c, 0, [0], q, [T], out, first_row=n - tail)
+    fm.fm_kvq_synchronize(c)
+    at = [0, 1, 31, 32, 4095, T // 2, T - 1]
+    want, _, mass, reach = Q.attend_heads(q[at].double().cpu().numpy(), ks, vs, hd ** -0.5)
+    check_out(out[at], want, mass, reach, hd, tail, "bf16", vs)
+    fm.fm_kvq_destroy(c)
+
+
 def runtime():
     import ctypes
     import glob
