@@ -632,9 +632,11 @@ FM_API fm_status fm_kvq_read(fm_kvq *c, int32_t layer, int32_t n_seqs, const int
  * writes the new weights to weights_dev (f32 [n_seqs][n_kv_heads][ldw]) unless
  * that is NULL.  decay < 0: weights are left alone.
  * Sequence ids are distinct where weights are counted.
- * Errors: FM_ERR_INVALID_ARG, FM_ERR_UNSUPPORTED (over 2^19 query rows x heads
- *   in one sequence, or over 2^30 pairs of 32 of those and 64 keys),
- *   FM_ERR_CUDA.  A bounded device wait that gives up is
+ * Errors: FM_ERR_INVALID_ARG (..., over 65,536 query rows of a sequence, over
+ *   1,024 query heads a KV head), FM_ERR_UNSUPPORTED (a sequence's rows make
+ *   units of 32 query rows x heads of a KV head: over 2^15 units, or over
+ *   2^31 - 1 stages in them, a unit having one for each 128 cache rows from
+ *   first_row on, or 64 with head_dim 256, and four more), FM_ERR_CUDA.  A bounded device wait that gives up is
  *   reported by fm_kvq_synchronize.
  */
 FM_API fm_status fm_kvq_attend(fm_kvq *c, int32_t layer, int32_t n_seqs, const int32_t *seq_ids_host,

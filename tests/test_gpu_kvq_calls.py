@@ -448,6 +448,51 @@ def test_window_over_a_long_cache():
     fm.fm_kvq_destroy(c)
 
 
+@pytest.mark.parametrize("nkv,group", [(1, 16), (2, 8)])
+def test_most_query_rows(nkv, group):
+    """2^15 units of 32 rows in one call, the most it takes, with the weights; one head more, one row more and one more head
+    a KV head than may be are refused, and nothing is written."""
+    import torch
+    import block_speculative_decoding_fm_gb300 as fm
+    rng = np.random.default_rng(52)
+    hd, n, T = 64, 100, 1 << 16
+    c = Cache(1, nkv, hd, n)
+    c.append([0], [n], [0], rng, "bf16")
+    g = torch.Generator(device="cuda").manual_seed(4)
+    q = torch.randn((T, nkv * group, hd), device="cuda", generator=g).to(torch.bfloat16)
+    out, w = torch.full_like(q, 9.0), torch.full((1, nkv, n), -1.0, device="cuda")
+    fm.fm_kvq_attend(c.c, 0, [0], q, [T], out, decay=0.0, weights=w)
+    fm.fm_kvq_synchronize(c.c)
+    at = [0, 1, 4095, T // 2 + 1, T - 1]
+    want, _, mass, reach = Q.attend_heads(q[at].double().cpu().numpy(), c.k[0, 0], c.v[0, 0], hd ** -0.5)
+    check_out(out[at], want, mass, reach, hd, n, "bf16", c.v[0, 0])
+    for h in range(nkv):
+        k = torch.from_numpy(c.k[0, 0][:, h]).cuda()
+        p = torch.zeros(n, dtype=torch.float64, device="cuda")
+        for x in q[:, h * group:(h + 1) * group].split(T // 8):
+            p += torch.softmax(x.double().reshape(-1, hd) @ k.T * hd ** -0.5, -1).sum(0)
+        # (a sum in f32 of 2^15 tiles' parts: 2^15 roundings of 2^-24 of the sum so far, 2^-9 if all went one way; they do not,
+        # which leaves room for the probabilities' own errors)
+        assert float((w[0, h].double() / p - 1).abs().max()) < 2.0 ** -9
+
+    def bad(status, q, n_rows):
+        o = torch.full_like(q, 9.0)
+        with pytest.raises(fm.FmError) as e:
+            fm.fm_kvq_attend(c.c, 0, [0], q, [n_rows], o)
+        assert e.value.status == status
+        torch.cuda.synchronize()
+        assert bool((o == 9.0).all())
+
+    bad(fm.FM_ERR_UNSUPPORTED, torch.zeros((T, nkv * (group + 1), hd), dtype=torch.float16, device="cuda"), T)
+    bad(fm.FM_ERR_INVALID_ARG, torch.zeros((T + 1, nkv, hd), dtype=torch.float16, device="cuda"), T + 1)
+    bad(fm.FM_ERR_INVALID_ARG, torch.zeros((1, nkv * 1025, hd), dtype=torch.float16, device="cuda"), 1)
+    many = torch.randn((3, nkv * 1024, hd), device="cuda", generator=g).to(torch.float16)
+    out = torch.zeros_like(many)
+    fm.fm_kvq_attend(c.c, 0, [0], many, [3], out, causal=True)
+    want, _, mass, reach = Q.attend_heads(many.double().cpu().numpy(), c.k[0, 0], c.v[0, 0], hd ** -0.5, True)
+    check_out(out, want, mass, reach, hd, n, "f16", c.v[0, 0])
+
+
 def runtime():
     import ctypes
     import glob
