@@ -575,6 +575,15 @@ def _kvq_weights(x, n: int, c, what: str):
     return x.data_ptr(), x.shape[2]
 
 
+def _decay(decay: Optional[float]) -> float:
+    """The library's decay: below 0 where weights are left alone, which a caller says by None."""
+    if decay is None:
+        return -1.0
+    if decay < 0:
+        raise FmError(FM_ERR_INVALID_ARG, f"decay {decay}: at least 0, or None to leave the weights alone")
+    return decay
+
+
 def fm_kvq_create(n_layers: int, n_seqs: int, n_kv_heads: int, head_dim: int, max_rows: int,
                   stream=None) -> KvqCache:
     """An empty KV cache held in 4 bits, on the current device."""
@@ -628,7 +637,7 @@ def fm_kvq_attend(c, layer: int, seq_ids: Sequence[int], q, n_rows: Sequence[int
     """Attention of n_rows[i] query rows of each sequence over its cache rows first_row .. (causal: the rows are the
     cache's last ones).  q, out: CUDA tensors [sum(n_rows), n_heads, head_dim] of one dtype (float32, float16,
     bfloat16); n_heads a multiple of n_kv_heads; scale: 1 / sqrt(head_dim) unless given.  decay: None leaves the
-    rows' weights alone; a number d counts them, w = d w + this call's, into weights too (CUDA float32 [n_seqs,
+    rows' weights alone; a number d >= 0 counts them, w = d w + this call's, into weights too (CUDA float32 [n_seqs,
     n_kv_heads, rows] or None)."""
     n, total = len(seq_ids), sum(n_rows)
     qp, dtype, heads, ldq = _kvq_rows(q, total, None, c, "q")
@@ -641,7 +650,7 @@ def fm_kvq_attend(c, layer: int, seq_ids: Sequence[int], q, n_rows: Sequence[int
     _kvq_check(load_library().fm_kvq_attend(
         c, layer, n, _addr(seq_ids_), _addr(n_rows_), qp, dtype, heads, ldq,
         c._head_dim ** -0.5 if scale is None else scale, 1 if causal else 0, first_row, op, ldo,
-        -1.0 if decay is None else decay, wp, ldw, _stream(stream)), c)
+        _decay(decay), wp, ldw, _stream(stream)), c)
 
 
 def fm_kvq_set_weights(c, layer: int, seq_ids: Sequence[int], weights, stream=None) -> None:
@@ -696,7 +705,7 @@ def fm_mtp_use_kvq(m, c, layer: int = 0, seq: int = 0, next_pos: Optional[int] =
     not).  The head keeps c alive while it uses it."""
     if c is not None and next_pos is None:
         next_pos = fm_kvq_length(c, layer, seq)
-    _mtp_check(load_library().fm_mtp_use_kvq(m, c, layer, seq, next_pos or 0, -1.0 if decay is None else decay), m)
+    _mtp_check(load_library().fm_mtp_use_kvq(m, c, layer, seq, next_pos or 0, _decay(decay)), m)
     m._kvq = c
 
 

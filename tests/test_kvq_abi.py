@@ -43,3 +43,11 @@ def test_null_handles(lib):
     assert lib.fm_kvq_last_error(None) is not None
     lib.fm_kvq_destroy(None)
     fm.fm_kvq_destroy(None)
+
+
+def test_negative_decay(lib):
+    """None leaves the weights alone; a negative number is no decay (the library would leave them alone too)."""
+    for d in (-0.5, -1.0, float("-inf")):
+        with pytest.raises(fm.FmError) as e:
+            fm.fm_mtp_use_kvq(None, None, decay=d)
+        assert e.value.status == fm.FM_ERR_INVALID_ARG and "decay" in str(e.value)
