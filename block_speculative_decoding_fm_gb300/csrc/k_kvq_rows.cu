@@ -93,66 +93,26 @@ struct Sixteen {
   }
 };
 
+// Eight consecutive values of a row, rounded once each.
+__device__ __forceinline__ void store8(float *p, const float (&x)[8]) {
+  reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+  reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
 template <typename T>
-struct Eight;
-template <>
-struct Eight<float> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const float *p) {
-    a = ldg128f(p);
-    b = ldg128f(p + 4);
-  }
-  __device__ __forceinline__ void get(float (&x)[8]) const {
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-  }
-  static __device__ __forceinline__ void store(float *p, const float (&x)[8]) {
-    reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-  }
-};
-template <>
-struct Eight<__half> {
-  uint4 a;
-  __device__ __forceinline__ void load(const __half *p) { a = ldg128(p); }
-  __device__ __forceinline__ void get(float (&x)[8]) const {
+__device__ __forceinline__ void store8(T *p, const float (&x)[8]) {
+  uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t w = word(a, i);
-      const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
-      x[2 * i] = f.x, x[2 * i + 1] = f.y;
-    }
-  }
-  static __device__ __forceinline__ void store(__half *p, const float (&x)[8]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (std::is_same<T, __half>::value) {
       const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
       w[i] = *reinterpret_cast<const uint32_t *>(&h);
-    }
-    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-  }
-};
-template <>
-struct Eight<__nv_bfloat16> {
-  uint4 a;
-  __device__ __forceinline__ void load(const __nv_bfloat16 *p) { a = ldg128(p); }
-  __device__ __forceinline__ void get(float (&x)[8]) const {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t w = word(a, i);
-      x[2 * i] = __uint_as_float(w << 16), x[2 * i + 1] = __uint_as_float(w & 0xffff0000u);
-    }
-  }
-  static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&x)[8]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    } else {
       const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
       w[i] = *reinterpret_cast<const uint32_t *>(&h);
     }
-    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
   }
-};
+  *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
 
 // the sequence whose tiles hold x (n <= 64 prefix sums)
 __device__ __forceinline__ int find_seq(const int32_t *pre, int n, int x) {
@@ -319,7 +279,7 @@ __global__ void __launch_bounds__(kThreads) kvq_read_kernel(const __grid_constan
     float x[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = f * static_cast<float>(static_cast<int>((w[p] >> (4 * e)) & 15u) - 8);
-    Eight<T>::store(dst + (a.row0[i] + r) * a.ld, x);
+    store8(dst + (a.row0[i] + r) * a.ld, x);
   }
 }
 

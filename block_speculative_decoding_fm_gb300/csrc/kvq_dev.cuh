@@ -152,6 +152,7 @@ struct QTile {
 template <int HD, bool QS, bool SK, int NQ, int NT, typename T>
 __device__ __forceinline__ void load_q(const T *q, int64_t ldq, int group, int r0, int R, float scale_log2, uint8_t *tile,
                                        int tid) {
+  static_assert(!QS || SK, "split queries meet signed codes: the start value has no low part");
   using QT = QTile<HD, QS, NQ>;
   constexpr int O = HD / 8;
   // (the loads of two rounds in flight together)
@@ -201,8 +202,8 @@ __device__ __forceinline__ void load_q(const T *q, int64_t ldq, int group, int r
           lo[p] = 0;
         }
         if constexpr (!SK) {
-          const float2 h = pair_f32(hi[p]), l = pair_f32(lo[p]);
-          sum += (h.x + h.y + (l.x + l.y)) * (p & 1 ? 1.f : 0.0625f);
+          const float2 h = pair_f32(hi[p]);
+          sum += (h.x + h.y) * (p & 1 ? 1.f : 0.0625f);
         }
       }
       *reinterpret_cast<uint4 *>(tile + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
@@ -387,6 +388,7 @@ __device__ __forceinline__ uint32_t u32(__half2 v) { return *reinterpret_cast<co
 template <int HD, int PS, bool SV, int NQ, int KS>
 __device__ __forceinline__ void tile_pv(uint32_t code, int g, const uint32_t (&sc)[4], uint32_t pt, int key0, int lane,
                                         float (&o)[2][NQ][4], float (&cor)[NQ][4]) {
+  static_assert(PS != 2 || SV, "the sums that unsigned codes need have no second part");
   using PT = PTile<NQ, PS, KS>;
   uint32_t w[4], h[4][4];
   ldsm_x4_trans(code ^ (g << 4), w[0], w[1], w[2], w[3]);
@@ -439,7 +441,6 @@ __device__ __forceinline__ void tile_pv(uint32_t code, int g, const uint32_t (&s
     if constexpr (!SV) {
       constexpr uint32_t kOnes = 0x3c003c00u;
       mma_f16(cor[n], b[n][0], b[n][1], b[n][2], b[n][3], kOnes, kOnes);
-      if constexpr (PS == 2) mma_f16(cor[n], l[n][0], l[n][1], l[n][2], l[n][3], kOnes, kOnes);
     }
   }
 }
