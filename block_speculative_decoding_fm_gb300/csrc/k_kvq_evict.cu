@@ -29,7 +29,7 @@ namespace fm {
 namespace {
 
 constexpr int kThreads = 512;    // in place
-constexpr int kCopies = 8; 
+constexpr int kCopies = 8;       // of a histogram
 constexpr int kMoveThreads = 256;
 constexpr int kSelectRoom[2] = {200 * 1024, 90 * 1024};   // bytes of keys in shared memory: a CTA an SM, two
 constexpr int kCluster = 8;      // in place; select, where planes are few
@@ -359,12 +359,14 @@ template <int HD>
 cudaError_t evict_hd(const KvqEvictArgs &a, cudaStream_t s) {
   const int planes = a.n * a.c.n_kv;
   cudaError_t e;
-  if (planes * kCluster <= 320) {
+  // a cluster a plane while two CTAs an SM hold them all (38 planes of 32,768 rows: select and move 45 us, 72 with a CTA a
+  // plane; 8 planes: 18 and 49; of 4,096 rows 38 planes: 22 and 14 to 16, 8 planes: 12 and 14)
+  if (planes * kCluster <= 2 * a.n_sm) {
     // (longer planes are read again in each pass)
     int longest = 0;
     for (int i = 0; i < a.n; ++i) longest = a.len[i] > longest ? a.len[i] : longest;
     const int bytes = select_run(longest, kCluster * 16) * 16 * 4;
-    const bool cached = bytes <= kSelectRoom[planes * kCluster > 152];
+    const bool cached = bytes <= kSelectRoom[planes * kCluster > a.n_sm];
     static std::atomic<uint64_t> done{0};
     e = allow_smem(kvq_select_kernel<kCluster>, kSelectRoom[0], done);
     if (e != cudaSuccess) return e;
@@ -400,7 +402,7 @@ cudaError_t evict_hd(const KvqEvictArgs &a, cudaStream_t s) {
     e = kvq_launch(kvq_move_kernel<HD>, dim3((most + rb - 1) / rb, planes), dim3(kMoveThreads), 0, s, a);
   }
   if (e == cudaSuccess && same)
-    e = kvq_launch(planes * kCluster <= 160 ? kvq_move_in_place_kernel<HD, true> : kvq_move_in_place_kernel<HD, false>,
+    e = kvq_launch(planes * kCluster <= a.n_sm ? kvq_move_in_place_kernel<HD, true> : kvq_move_in_place_kernel<HD, false>,
                    dim3(planes * kCluster), dim3(kThreads), 0, s, a);
   return e;
 }

@@ -639,6 +639,7 @@ fm_status fm_kvq_evict(fm_kvq *c, int32_t layer, int32_t n_seqs, const int32_t *
   memset(&a, 0, sizeof a);
   a.c = view(c, layer);
   a.keep = keep;
+  a.n_sm = c->n_sm;
   a.recent = recent;
   a.kept = kept_dev;
   a.list = c->list;

@@ -131,6 +131,7 @@ constexpr int kKvqWeightTiles = 16;   // tiles a CTA of the weights pass covers 
 struct KvqEvictArgs {
   KvqCache c;
   int32_t n, keep, recent;
+  int32_t n_sm;           // of the device, by which the launches are shaped
   int32_t *kept;          // [call sequences][n_kv][keep] or null
   int32_t *list;          // [n][n_kv][rows_pad] scratch: the rows kept, in order
   int32_t call0;
