@@ -617,7 +617,10 @@ FM_API fm_status fm_kvq_read(fm_kvq *c, int32_t layer, int32_t n_seqs, const int
  * ones) gives zeros.  q_dev and out_dev: [sum n_rows][n_heads][head_dim] of
  * dtype, row strides ldq and ldo, packed in the order of seq_ids; they may not
  * overlap.  Scores, softmax and sums are f32.  The cache's values enter exactly
- * as stored, f32 queries to ~22 bits (f16 and bf16 ones as they are); a
+ * as stored, f32 queries to ~22 bits (f16 and bf16 ones as they are).  f32 calls
+ * and those that count weights sum products to f32's precision; f16 and bf16
+ * ones without weights keep ~2^-17 of a sum's largest term, below their outputs'
+ * rounding, so that the same queries may give other last bits with weights.  A
  * probability times its row's V scale is kept to ~21 bits for f32 outputs,
  * rounded to f16's 11 once for f16 ones and twice for bf16 ones, and a key's
  * part to 2^-24 of the largest |v| of its KV head that the call sees; a

@@ -9,7 +9,7 @@ import numpy as np
 import pytest
 
 from oracle import kvq as Q
-from test_gpu_kvq import TYPES, Cache, attend_case, built, check_out, check_weights, rows  # noqa: F401
+from test_gpu_kvq import TYPES, Cache, attend_case, built, check_out, check_weights, rows, ttype  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -491,6 +491,36 @@ def test_most_query_rows(nkv, group):
     fm.fm_kvq_attend(c.c, 0, [0], many, [3], out, causal=True)
     want, _, mass, reach = Q.attend_heads(many.double().cpu().numpy(), c.k[0, 0], c.v[0, 0], hd ** -0.5, True)
     check_out(out, want, mass, reach, hd, n, "f16", c.v[0, 0])
+
+
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("name", TYPES)
+@pytest.mark.parametrize("big", [20.0, 400.0, 2000.0])
+def test_outlier_channel(hd, name, big):
+    """A channel that gives every score the same large part: what differs between the keys stays, with weights and without.
+    The scores' own tolerance is large here (reach 1,000 and more), so the outputs are also held to what f32 scores lose
+    by a plain sum of hd products of that size: each of its hd roundings 2^-25 reach off, sqrt(hd) of them together, three
+    such deviations."""
+    import torch
+    rng = np.random.default_rng(53)
+    L, T = 700, 16
+    k = rng.normal(size=(L, 1, hd))
+    k[:, 0, 5] = 8.0
+    q = rng.normal(size=(T, 1, hd)) * 2
+    q[:, 0, 5] = big * np.sign(rng.normal(size=T))
+    k, q, v = (torch.from_numpy(x.astype(np.float32)).to(ttype(name)).cuda() for x in (k, q, rng.normal(size=(L, 1, hd))))
+    c = Cache(1, 1, hd, L)
+    c.fm.fm_kvq_append(c.c, 0, [0], k, v, [L], [0])
+    ks, vs = (Q.stored(x.double().cpu().numpy()) for x in (k, v))
+    want, _, mass, reach = Q.attend_heads(q.double().cpu().numpy(), ks, vs, hd ** -0.5)
+    for decay in (None, 0.0):
+        out = torch.zeros_like(q)
+        c.fm.fm_kvq_attend(c.c, 0, [0], q, [T], out, decay=decay)
+        check_out(out, want, mass, reach, hd, L, name, vs)
+        off = np.linalg.norm(out.double().cpu().numpy() - want) / np.linalg.norm(want)
+        step = torch.finfo(out.dtype).eps / 2
+        p = {"f32": 2.0 ** -21, "f16": 2.0 ** -11, "bf16": 2.0 ** -10}[name]
+        assert off <= step + p + 3 * 2.0 ** -25 * hd ** 0.5 * reach.max() * 2 ** 0.5, off
 
 
 def runtime():
