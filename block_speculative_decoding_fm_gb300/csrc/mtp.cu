@@ -711,8 +711,11 @@ fm_status fm_mtp_use_kvq(fm_mtp *m, fm_kvq *c, int32_t layer, int32_t seq, int64
   if (g.n_kv_heads != m->cfg.n_kv_heads || g.head_dim != m->cfg.head_dim)
     return mfail(m, FM_ERR_INVALID_ARG, "the 4-bit cache has %d heads of %d, the head %d of %d", g.n_kv_heads, g.head_dim,
                  m->cfg.n_kv_heads, m->cfg.head_dim);
-  if (kvq_device(c) != m->device)
-    return mfail(m, FM_ERR_INVALID_ARG, "the 4-bit cache is on device %d, the head on %d", kvq_device(c), m->device);
+  int dev = -1;
+  MCK(cudaGetDevice(&dev));
+  if (kvq_device(c) != m->device || dev != m->device)
+    return mfail(m, FM_ERR_INVALID_ARG, "the 4-bit cache is on device %d, the head on %d, the current one is %d", kvq_device(c),
+                 m->device, dev);
   if (next_pos < len || next_pos > INT32_MAX) return mfail(m, FM_ERR_INVALID_ARG, "next_pos %lld with %d rows", (long long)next_pos, len);
   if (!std::isfinite(decay)) return mfail(m, FM_ERR_INVALID_ARG, "decay is not finite");
   if (!m->ao) {

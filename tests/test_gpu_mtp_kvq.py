@@ -229,6 +229,9 @@ def test_devices():
     with pytest.raises(fm.FmError) as e:
         fm.fm_mtp_use_kvq(h, other)
     assert e.value.status == fm.FM_ERR_INVALID_ARG
+    with torch.cuda.device(1), pytest.raises(fm.FmError) as e:        # its rows' buffers would be there
+        fm.fm_mtp_use_kvq(h, c)
+    assert e.value.status == fm.FM_ERR_INVALID_ARG
     fm.fm_mtp_use_kvq(h, c)
     t = torch.zeros((2,), dtype=torch.int32, device="cuda:0")
     hn = torch.zeros((2, cfg.hidden), dtype=torch.float32, device="cuda:0")
