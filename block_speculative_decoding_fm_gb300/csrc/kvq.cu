@@ -541,6 +541,7 @@ fm_status fm_kvq_attend(fm_kvq *c, int32_t layer, int32_t n_seqs, const int32_t 
   if (total > 0) {
     KTRY(check_rows(c, "q", q_dev, ldq, width, size));
     KTRY(check_rows(c, "out", out_dev, ldo, width, size));
+    if (q_dev == out_dev) return kfail(c, FM_ERR_INVALID_ARG, "out is q: rows are still read when others are written");
     if (weights_dev && ldw < most)
       return kfail(c, FM_ERR_INVALID_ARG, "weights: row stride %lld, %d rows", (long long)ldw, most);
   }

@@ -616,7 +616,7 @@ FM_API fm_status fm_kvq_read(fm_kvq *c, int32_t layer, int32_t n_seqs, const int
  * sees nothing (length 0, first_row past the end, more query rows than cached
  * ones) gives zeros.  q_dev and out_dev: [sum n_rows][n_heads][head_dim] of
  * dtype, row strides ldq and ldo, packed in the order of seq_ids; they may not
- * overlap.  Scores, softmax and sums are f32.  The cache's values enter exactly
+ * overlap (out_dev == q_dev is refused).  Scores, softmax and sums are f32.  The cache's values enter exactly
  * as stored, f32 queries to ~22 bits (f16 and bf16 ones as they are).  f32 calls
  * and those that count weights sum products to f32's precision; f16 and bf16
  * ones without weights keep ~2^-17 of a sum's largest term, below their outputs'

@@ -523,6 +523,25 @@ def test_outlier_channel(hd, name, big):
         assert off <= step + p + 3 * 2.0 ** -25 * hd ** 0.5 * reach.max() * 2 ** 0.5, off
 
 
+def test_outputs_over_queries():
+    """The queries' own rows as the outputs' are refused: other CTAs, and the weights' pass, still read them."""
+    import torch
+    import block_speculative_decoding_fm_gb300 as fm
+    c = fm.fm_kvq_create(1, 1, 1, 64, 40)
+    x = torch.ones((30, 1, 64), device="cuda")
+    fm.fm_kvq_append(c, 0, [0], x, x, [30], [0])
+    q = torch.ones((2, 1, 64), device="cuda")
+    with pytest.raises(fm.FmError) as e:
+        fm.fm_kvq_attend(c, 0, [0], q, [2], q, decay=1.0)
+    assert e.value.status == fm.FM_ERR_INVALID_ARG
+    fm.fm_kvq_attend(c, 0, [0], q, [0], q)               # no rows: nothing to do
+    fm.fm_kvq_synchronize(c)
+    assert bool((q == 1).all())
+    w = torch.full((1, 1, 30), -1.0, device="cuda")
+    fm.fm_kvq_read(c, 0, [0], [0], [30], weights=w)
+    assert bool((w == 0).all())
+
+
 def runtime():
     import ctypes
     import glob
