@@ -18,9 +18,9 @@
 // written as 0.5625 n bytes.  Two lanes share a group, 16 consecutive values each
 // (32-byte loads; the lane's codes are half of the group's 16-byte unit), and a
 // thread has all its rows' loads in flight.  (Eight values a lane: the scale's and the
-// extremes' instructions weigh twice as much, 100 us for 32768 rows of 2 x 16 heads x 128 f16.)  That many rows take 58 us;
-// 262144 rows of 8 KV heads of 128, bf16: 232 us, 5.9 TB/s, and 65536 of them back out 54 us, 6.3 TB/s with what L2
-// still holds of the writes.
+// extremes' instructions weigh twice as much, 100 us for 32768 rows of 2 x 16 heads x 128 f16.)  That many rows take 57 us;
+// 262144 rows of 8 KV heads of 128, bf16: 226 us, 6.1 TB/s, and 65536 of them back out 55 us, 6.3 TB/s with what L2
+// still holds of the writes; 65536 f32 rows of 4 x 256: 127 us, 4.8 TB/s, each way.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -1,6 +1,7 @@
 // kvq.cu -- the 4-bit KV cache's host calls: argument checks, the lengths, the
 // split of a call's work over the SMs, the launches (k_kvq_rows.cu,
-// k_kvq_attn.cu, k_kvq_evict.cu).
+// kvq_attn.cuh by way of k_kvq_attn64.cu, k_kvq_attn128.cu and k_kvq_attn256.cu,
+// k_kvq_evict.cu).
 //
 // Every value that a call needs on the device rides in the kernels' argument
 // blocks (64 sequences a launch), so nothing is copied or allocated after
@@ -193,10 +194,11 @@ int stages_of(int len, int first, int stage_rows) {
 
 // The octets of query rows that a unit carries, 0 where the call has too many units.  A stage costs about 1 + nq (its codes
 // are unpacked once, then used for each octet), beginning and ending a unit 5 nq (9 nq for 256 dims) of the same: short
-// caches want many narrow units, long ones few wide ones.  (8 rows of 24 heads over 4 KV heads of 256, f32: 64 rows 4.8 us
-// with nq 1, 8.6 with 3; 16384 rows 36.7 and 29.2.  16 rows of 16 heads of 128, bf16: 4161 rows 9.7 us with nq 1, 10.0 with
-// 2; 16384 rows 18.9 and 16.7.)  In the pass over the weights a CTA takes a sequence's row tiles one after another, about 7
-// each.  (With weights, 8 rows of 32 heads over 8 KV heads of 128, 1042 rows: 11.6 us, 15.0 without that term.)
+// caches want many narrow units, long ones few wide ones.  (8 rows of 24 heads over 4 KV heads of 256, f32: 64 rows 5.3 us
+// with nq 1, 10.5 with 3; 16384 rows 38.0 and 31.2, and 34.3 with 2, which the rule takes.  16 rows of 16 heads of 128, bf16:
+// 4161 rows 9.6 us with nq 1, 10.3 with 2; 16384 rows 19.3 and 17.0.)  In the pass over the weights a CTA takes a sequence's
+// row tiles one after another, about 7 each.  (With weights, 8 rows of 32 heads over 8 KV heads of 128, 1042 rows: 13.3 us,
+// 16.8 with nq 1, which the rule without that term takes.)
 int choose_nq(int n_seqs, const int32_t *seq, const int32_t *rows, const int32_t *len, int first, int group, int nkv, int hd,
               int n_sm, int64_t widest, bool weights) {
   const int stage_rows = kKvqTile * kvq_stage_tiles(hd), most = (int)(widest < 8 * kKvqMaxNQ ? (widest + 7) / 8 : kKvqMaxNQ);
@@ -221,8 +223,8 @@ int choose_nq(int n_seqs, const int32_t *seq, const int32_t *rows, const int32_t
 // Deals the launch's stages to at most `most` CTAs (what the SMs hold at once).  Equal shares balance best, but a share
 // that ends one unit and begins another pays for two (queries loaded, outputs written: about kKvqUnitCost stages).
 // Where the units are no more than the CTAs, each gets CTAs of its own unless that makes the longest share that much
-// longer.  (16 rows of 16 heads over 4161 rows of 128: 14.3 us by equal shares, 10.3 us this way; 32 ragged sequences
-// whose longest would set the pace stay with equal shares.)
+// longer.  (16 rows of 16 heads over 4161 rows of 128: 10.9 us by equal shares, 9.7 us this way; 8 rows of 24 heads over 64
+// rows of 4 x 256, f32: 9.7 and 5.3; 32 ragged sequences whose longest would set the pace stay with equal shares.)
 void deal(KvqAttnArgs &a, int64_t most, int groups, int nkv, int unit_rows) {
   const int64_t W = a.st0[a.n];
   auto units = [&](int i) { return ((int64_t)a.rows[i] * a.group + unit_rows - 1) / unit_rows * nkv; };

@@ -16,16 +16,18 @@
 // SM, and a unit's end needs no exchange inside a group.  The group shares one reference a row; it moves
 // only when a score beats it by 2^8, and the barrier that hands P over tells everyone whether one did.
 //
-// One query row is bound by memory: 524288 rows of 8 KV heads of 128 in 101 us, 6.0 TB/s (0.88 of a plain copy), 24 heads
-// over 4 of 256 in 107 us, 5.6 TB/s.  Sixteen are bound by the tensor and the integer pipes together: bf16 144 us (4.2 TB/s),
-// f16 157 us, f32 243 us, whose queries and probabilities are two operands each.  Short caches are a chain of waits:
-// of 26 us over 32769 rows of 16 heads, 18 are the stream, 2 the queries, 1 the output, 3 the join.
+// One query row is bound by memory: 524288 rows of 8 KV heads of 128 in 104 us, 5.8 TB/s (0.86 of a plain copy), 24 heads
+// over 4 of 256 in 112 us, 5.4 TB/s.  Sixteen are bound by the chain of a warp's steps (codes unpacked, product, exponential,
+// barrier, product), each waiting for the one before, with 16 warps an SM to fill the waits: the tensor pipe is 37 to 39 % busy
+// and the issue slots 45 to 49 %.  bf16 149 us (4.0 TB/s), f16 164 us, f32 244 us, whose queries and probabilities are two
+// operands each.  Short caches are a chain of waits between CTAs: of 26 us over 32769 rows of 16 heads, 18 are the stream, 2 the
+// queries, 1 the output, 3 the join.
 //
 // With at most 32 query rows the product is a skinny one, and the codes pass from shared memory (ldmatrix)
 // through a few integer operations straight into mma.sync fragments: they never go back to shared
 // memory as f16, which a tcgen05 operand would need (64 KB written and read again per 128 rows of
 // head dim 128: 1024 cycles of shared memory against the 784 cycles in which an SM's share of HBM
-// delivers their 18 KB).
+// delivers their 18 KB).  (A first operand in TMEM, which the scores could have, has not been tried.)
 #include <atomic>
 #include <type_traits>
 

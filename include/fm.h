@@ -557,10 +557,11 @@ FM_API void fm_mtp_destroy(fm_mtp *m);
  * streams are put in the order they were issued in (they share a workspace
  * and the weights); a captured call is not, so graphs that use one cache are
  * replayed one after another, and ordered with eager calls, by the caller, and
- * not after fm_kvq_destroy.  The cache's device must be the current device.  Device pointers are 16-byte
- * aligned, and row strides (ld, ldq, ldo: elements between rows) whole
- * multiples of 16 bytes; pointers to weights and kept rows are 4-byte aligned
- * (FM_ERR_INVALID_ARG otherwise).  One host thread at a time per cache.
+ * not after fm_kvq_destroy.  The cache's device must be the current device.
+ * Device pointers are 16-byte aligned, and row strides (ld, ldq, ldo: elements
+ * between rows) whole multiples of 16 bytes; pointers to weights and kept rows are
+ * 4-byte aligned (FM_ERR_INVALID_ARG otherwise).  One host thread at a time per
+ * cache.
  * ------------------------------------------------------------------------ */
 typedef struct fm_kvq_config {
   int32_t n_layers;    /* 1 .. 1024 */
@@ -616,18 +617,21 @@ FM_API fm_status fm_kvq_read(fm_kvq *c, int32_t layer, int32_t n_seqs, const int
  * sees nothing (length 0, first_row past the end, more query rows than cached
  * ones) gives zeros.  q_dev and out_dev: [sum n_rows][n_heads][head_dim] of
  * dtype, row strides ldq and ldo, packed in the order of seq_ids; they may not
- * overlap (out_dev == q_dev is refused).  Scores, softmax and sums are f32.  The cache's values enter exactly
- * as stored, f32 queries to ~22 bits (f16 and bf16 ones as they are).  f32 calls
- * and those that count weights sum products to f32's precision; f16 and bf16
- * ones without weights keep ~2^-17 of a sum's largest term, below their outputs'
- * rounding, so that the same queries may give other last bits with weights.  A
- * probability times its row's V scale is kept to ~21 bits for f32 outputs,
- * rounded to f16's 11 once for f16 ones and twice for bf16 ones, and a key's
- * part to 2^-24 of the largest |v| of its KV head that the call sees; a
- * probability below 2^-32 of the row's largest may count as 0.  Rows that the
- * call does not see (behind the length, ahead of first_row, overwritten or
- * evicted) have no part in any of it.  A query row
- * with a NaN or an infinity gives NaN, and one with values past 2^97 may.
+ * overlap (out_dev == q_dev is refused).
+ *
+ * Scores, softmax and sums are f32.  The cache's values enter exactly as stored,
+ * f32 queries to ~22 bits (f16 and bf16 ones as they are).  Products are summed
+ * to f32's precision in f32 calls and in the scores of calls that count weights;
+ * the other sums of f16 and bf16 calls keep ~2^-17 of their largest term, below
+ * the outputs' own rounding (so the same queries may give other last bits with
+ * weights than without).  A probability times its row's V scale is kept to ~21
+ * bits for f32 outputs, rounded to f16's 11 once for f16 ones and twice for bf16
+ * ones, and a key's part to 2^-24 of the largest |v| of its KV head that the call
+ * sees; a probability below 2^-32 of the row's largest may count as 0.  Rows that
+ * the call does not see (behind the length, ahead of first_row, overwritten or
+ * evicted) have no part in any of it.  A query row with a NaN or an infinity
+ * gives NaN, and one with values past 2^97 may.
+ *
  * decay >= 0 also counts the attention weight each cache row collects, per KV
  * head:  w_j = decay w_j + sum over the call's rows and the KV head's query
  * heads of p_j / sum p  (decay 1: plain accumulation; 0: this call's weights
@@ -635,7 +639,7 @@ FM_API fm_status fm_kvq_read(fm_kvq *c, int32_t layer, int32_t n_seqs, const int
  * writes the new weights to weights_dev (f32 [n_seqs][n_kv_heads][ldw]) unless
  * that is NULL.  decay < 0: weights are left alone.
  * Sequence ids are distinct where weights are counted.
- * Errors: FM_ERR_INVALID_ARG (..., over 65,536 query rows of a sequence, over
+ * Errors: FM_ERR_INVALID_ARG (also: over 65,536 query rows of a sequence or over
  *   1,024 query heads a KV head), FM_ERR_UNSUPPORTED (a sequence's rows make
  *   units of 32 query rows x heads of a KV head: over 2^15 units, or over
  *   2^31 - 1 stages in them, a unit having one for each 128 cache rows from
