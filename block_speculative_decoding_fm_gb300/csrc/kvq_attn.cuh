@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(Shape<HD, T, NQ>::kThreads, Shape<HD, T, NQ>::
               for (int u = 0; u < GP; ++u) sc[kb][u][j] &= keep;
             }
         }
-        // does one ask for a lower shift?  (2 to 3 % of the time with 16 rows; looked for ahead of P's barrier, in scales fetched
+        // does one ask for a lower shift?  (1 to 3 % of the time; looked for ahead of P's barrier, in scales fetched
         // twice, 9 %)
         __half2 top2 = __habs2(h2(sc[0][0][0]));
 #pragma unroll
@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(Shape<HD, T, NQ>::kThreads, Shape<HD, T, NQ>::
             }
         }
         if (shift != 0) {
-          const __half2 up = shift_factor(shift);
+          const __half2 up = shift_factor(shift > 0 ? shift : shift - shift / 2);
 #pragma unroll
           for (int kb = 0; kb < NB; ++kb)
 #pragma unroll
@@ -426,14 +426,20 @@ __global__ void __launch_bounds__(Shape<HD, T, NQ>::kThreads, Shape<HD, T, NQ>::
 #pragma unroll
               for (int j = 0; j < 4; ++j) sc[kb][u][j] = u32(__hmul2(h2(sc[kb][u][j]), up));
         }
+        auto pv = [&](auto low, __half2 by) {
 #pragma unroll
-        for (int kb = 0; kb < NB; ++kb) {
-          const int key = 32 * (kb * KP + kp);
+          for (int kb = 0; kb < NB; ++kb) {
+            const int key = 32 * (kb * KP + kp);
 #pragma unroll
-          for (int u = 0; u < GP; ++u)
-            tile_pv<HD, PS, SV, NQ, KS>(vcode + slot * SB + key / kKvqTile * TB + key % kKvqTile * (HD / 2), gw + 4 * u,
-                                        sc[kb][u], pt, key, lane, o[u], cor[u]);
-        }
+            for (int u = 0; u < GP; ++u)
+              tile_pv<HD, PS, SV, decltype(low)::value, NQ, KS>(vcode + slot * SB + key / kKvqTile * TB + key % kKvqTile * (HD / 2),
+                                                                gw + 4 * u, sc[kb][u], by, pt, key, lane, o[u], cor[u]);
+          }
+        };
+        if (shift >= 0)
+          pv(std::false_type(), h2(0));
+        else
+          pv(std::true_type(), shift_factor(shift / 2));
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(empty + slot * 8);

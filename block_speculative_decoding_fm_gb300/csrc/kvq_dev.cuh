@@ -358,7 +358,8 @@ __device__ __forceinline__ void put_p(uint32_t tile, int key0, int lane, const f
 // its own for the scales it multiplies, which begins at 15 and goes down where a scale
 // of a row in view asks for it (what the warp holds is brought to the new one): 0 while the
 // largest scale is 2^-7 to 2, so that ordinary rows need no multiplication.  Raising a
-// scale is exact; lowering one keeps 2^-25 of the largest.
+// scale is exact.  A shift below 0 is halved between d and p, so that neither leaves f16's
+// normal range for it while d is 2^-7 at least and p 2^-13; P' keeps 2^-25 of its largest.
 constexpr float kBias = 7.f;
 // |d| from here on asks for a lower shift (f16 bits of 2^(1 - shift); infinity, which no scale is, for -15)
 __device__ __forceinline__ uint32_t shift_limit(int shift) { return (uint32_t)(16 - shift) << 10; }
@@ -386,8 +387,9 @@ __device__ __forceinline__ uint32_t u32(__half2 v) { return *reinterpret_cast<co
 // end takes off eight times: a product with ones whose first operand is an octet's P'
 // fragments as they are, so that row lane / 4 sums the keys of the first and third
 // eight for query row lane / 4 of the octet, and row lane / 4 + 8 the others.
-template <int HD, int PS, bool SV, int NQ, int KS>
-__device__ __forceinline__ void tile_pv(uint32_t code, int g, const uint32_t (&sc)[4], uint32_t pt, int key0, int lane,
+// Low: p is lowered by the factor `low` first (the scales' shift is below 0).
+template <int HD, int PS, bool SV, bool Low, int NQ, int KS>
+__device__ __forceinline__ void tile_pv(uint32_t code, int g, const uint32_t (&sc)[4], __half2 low, uint32_t pt, int key0, int lane,
                                         float (&o)[2][NQ][4], float (&cor)[NQ][4]) {
   static_assert(PS != 2 || SV, "the sums that unsigned codes need have no second part");
   using PT = PTile<NQ, PS, KS>;
@@ -408,6 +410,10 @@ __device__ __forceinline__ void tile_pv(uint32_t code, int g, const uint32_t (&s
     if constexpr (PS) ldsm_x4(at + PT::kLo, l[n]);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
+      if constexpr (Low) {
+        b[n][j] = u32(__hmul2(h2(b[n][j]), low));
+        if constexpr (PS) l[n][j] = u32(__hmul2(h2(l[n][j]), low));
+      }
       const __half2 p = h2(b[n][j]), d = h2(sc[j]);
       if constexpr (PS == 0) {
         b[n][j] = u32(__hmul2(p, d));

@@ -627,9 +627,8 @@ FM_API fm_status fm_kvq_read(fm_kvq *c, int32_t layer, int32_t n_seqs, const int
  * weights than without).  A probability times its row's V scale is kept to ~21
  * bits for f32 outputs, rounded to f16's 11 once for f16 ones and twice for bf16
  * ones, and a key's part to 2^-24 of the largest |v| of its KV head that the call
- * sees; a probability below 2^-32 of the row's largest may count as 0.  Rows that
- * the call does not see (behind the length, ahead of first_row, overwritten or
- * evicted) have no part in any of it.  A query row with a NaN or an infinity
+ * sees.  Rows that the call does not see (behind the length, ahead of first_row,
+ * overwritten or evicted) have no part in any of it.  A query row with a NaN or an infinity
  * gives NaN, and one with values past 2^97 may.
  *
  * decay >= 0 also counts the attention weight each cache row collects, per KV

@@ -7,7 +7,7 @@ import numpy as np
 import pytest
 
 from oracle import kvq as Q
-from test_gpu_kvq import TYPES, Cache, built, check_out, rows  # noqa: F401
+from test_gpu_kvq import TYPES, Cache, built, check_out, rows, ttype  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -179,3 +179,28 @@ def test_sizes_in_one_sequence(hd, name, jump):
     # (small queries: every row keeps some weight)
     for causal in (False, True):
         check_large(c, name, rng, 0.1 / jump, causal)
+
+
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("name", TYPES)
+@pytest.mark.parametrize("big", [3e3, 8e4, 5e5])
+def test_large_row_of_no_weight(hd, name, big):
+    """A row in view with values up to what the cache can hold, whose key points away from every query, beside ordinary ones.
+    P' of the keys that count (p from 1/4, a V scale from 2^-5) is 2^-14 at least in units of 2^(7 - 15) and kept to 2^-25: f32
+    outputs within 2^-11; 16-bit ones within a step of their own."""
+    import torch
+    rng = np.random.default_rng(hd + 6)
+    L, n, H = 1500, 16, 2
+    k, v, q = rng.normal(size=(L, 1, hd)), rng.normal(size=(L, 1, hd)) * 0.5, rng.normal(size=(n, H, hd)) * 2
+    k[:, 0, 0], q[:, :, 0] = 6.0, 30.0
+    k[17, 0, 0], v[17] = -6.0, big * np.sign(v[17])
+    dk, dv = (torch.from_numpy(x.astype(np.float32)).cuda() for x in (k, v))
+    dq = torch.from_numpy(q.astype(np.float32)).to(ttype(name)).cuda()
+    c = Cache(1, 1, hd, L)
+    c.fm.fm_kvq_append(c.c, 0, [0], dk, dv, [L], [0])
+    ks, vs = Q.stored(k.astype(np.float32)), Q.stored(v.astype(np.float32))
+    want, w, _, _ = Q.attend_heads(dq.double().cpu().numpy(), ks, vs, hd ** -0.5)
+    assert w[0, 17] < 1e-10
+    got = out_of(c, 0, dq).double().cpu().numpy()
+    off = np.linalg.norm(got - want) / np.linalg.norm(want)
+    assert off <= {"f32": 2.0 ** -11, "f16": 2.0 ** -11, "bf16": 2.0 ** -8}[name], off
