@@ -16,10 +16,10 @@
 // SM, and a unit's end needs no exchange inside a group.  The group shares one reference a row; it moves
 // only when a score beats it by 2^8, and the barrier that hands P over tells everyone whether one did.
 //
-// One query row is bound by memory: 524288 rows of 8 KV heads of 128 in 104 us, 5.8 TB/s (0.86 of a plain copy), 24 heads
+// One query row is bound by memory: 524288 rows of 8 KV heads of 128 in 105 us, 5.8 TB/s (0.85 of a plain copy), 24 heads
 // over 4 of 256 in 112 us, 5.4 TB/s.  Sixteen are bound by the chain of a warp's steps (codes unpacked, product, exponential,
-// barrier, product), each waiting for the one before, with 16 warps an SM to fill the waits: the tensor pipe is 37 to 39 % busy
-// and the issue slots 45 to 49 %.  bf16 149 us (4.0 TB/s), f16 164 us, f32 244 us, whose queries and probabilities are two
+// barrier, product), each waiting for the one before, with 16 warps an SM to fill the waits: the tensor pipe is 38 to 39 % busy
+// and the issue slots 47 to 49 %.  bf16 147 us (4.1 TB/s), f16 160 us, f32 246 us, whose queries and probabilities are two
 // operands each.  Short caches are a chain of waits between CTAs: of 26 us over 32769 rows of 16 heads, 18 are the stream, 2 the
 // queries, 1 the output, 3 the join.
 //

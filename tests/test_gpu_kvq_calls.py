@@ -9,7 +9,8 @@ import numpy as np
 import pytest
 
 from oracle import kvq as Q
-from test_gpu_kvq import TYPES, Cache, attend_case, built, check_out, check_weights, rows, ttype  # noqa: F401
+from test_gpu_kvq import TYPES, Cache, attend_case, built, check_out, check_weights, rows  # noqa: F401
+from test_gpu_kvq import ttype
 
 pytestmark = pytest.mark.gpu
 
