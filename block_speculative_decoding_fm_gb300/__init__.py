@@ -40,7 +40,12 @@ EXPORTS = ["fm_create", "fm_time_conditioning", "fm_context_append", "fm_context
            "fm_mtp_last_error", "fm_mtp_destroy",
            "fm_kvq_create", "fm_kvq_append", "fm_kvq_read", "fm_kvq_attend", "fm_kvq_set_weights", "fm_kvq_evict",
            "fm_kvq_length", "fm_kvq_get_config", "fm_kvq_last_launch_count", "fm_mtp_use_kvq",
-           "fm_kvq_memory_bytes", "fm_kvq_synchronize", "fm_kvq_selftest_wait_timeout", "fm_kvq_last_error", "fm_kvq_destroy"]
+           "fm_kvq_memory_bytes", "fm_kvq_synchronize", "fm_kvq_selftest_wait_timeout", "fm_kvq_last_error", "fm_kvq_destroy",
+           "fm_paged_create", "fm_paged_write", "fm_paged_attend", "fm_paged_workspace_bytes", "fm_paged_get_config",
+           "fm_paged_last_launch_count", "fm_paged_synchronize", "fm_paged_selftest_wait_timeout", "fm_paged_last_error",
+           "fm_paged_destroy"]
+FM_ROPE_INTERLEAVED, FM_ROPE_HALF = 0, 1
+FM_ROPE_PLAIN, FM_ROPE_LINEAR, FM_ROPE_BY_PARTS = 0, 1, 2
 
 
 class FmConfig(ctypes.Structure):
@@ -82,6 +87,25 @@ class FmMtpConfig(ctypes.Structure):
 class FmKvqConfig(ctypes.Structure):
     _fields_ = [("n_layers", ctypes.c_int32), ("n_seqs", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("max_rows", ctypes.c_int32)]
+
+
+class FmPagedConfig(ctypes.Structure):
+    _fields_ = [("n_layers", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("page_rows", ctypes.c_int32),
+                ("n_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("rot_dims", ctypes.c_int32), ("rot_layout", ctypes.c_int32),
+                ("rope_scaling", ctypes.c_int32), ("rope_rows", ctypes.c_int32), ("theta", ctypes.c_float),
+                ("rope_factor", ctypes.c_float), ("rope_low", ctypes.c_float), ("rope_high", ctypes.c_float),
+                ("rope_gain", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
+class FmPagedBatch(ctypes.Structure):
+    _fields_ = [("starts", ctypes.c_void_p), ("lengths", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("table_ld", ctypes.c_int64), ("n_seqs", ctypes.c_int32), ("n_tokens", ctypes.c_int32),
+                ("table_pages", ctypes.c_int32), ("max_new", ctypes.c_int32)]
+
+
+class FmPagedRows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
 class FmError(RuntimeError):
@@ -154,6 +178,16 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "fm_kvq_selftest_wait_timeout": (I32, [P, I32, P]),
         "fm_kvq_last_error": (ctypes.c_char_p, [P]),
         "fm_kvq_destroy": (None, [P]),
+        "fm_paged_create": (I32, [ctypes.POINTER(FmPagedConfig), P, P, P, ctypes.POINTER(P)]),
+        "fm_paged_write": (I32, [P, I32, P, P, P, P, I32, P, P, P, P]),
+        "fm_paged_attend": (I32, [P, I32, P, P, P, ctypes.c_float, I32, I32, I32, P, I64, P]),
+        "fm_paged_workspace_bytes": (I32, [P, I32, ctypes.POINTER(I64)]),
+        "fm_paged_get_config": (I32, [P, ctypes.POINTER(FmPagedConfig)]),
+        "fm_paged_last_launch_count": (I32, [P, ctypes.POINTER(I32)]),
+        "fm_paged_synchronize": (I32, [P, P]),
+        "fm_paged_selftest_wait_timeout": (I32, [P, I32, P]),
+        "fm_paged_last_error": (ctypes.c_char_p, [P]),
+        "fm_paged_destroy": (None, [P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -730,3 +764,176 @@ def fm_kvq_destroy(c) -> None:
     if c is not None and c.value:
         load_library().fm_kvq_destroy(c)
         c.value = None
+
+
+class PagedCache(ctypes.c_void_p):
+    """The handle of a paged KV cache; freed by fm_paged_destroy, or with the last reference to it.  Holds its pool."""
+
+    def __del__(self):
+        if self.value and _lib is not None:
+            _lib.fm_paged_destroy(self)
+            self.value = None
+
+
+class PagedBatch:
+    """A batch's place in a paged cache (fm_paged_batch); holds the tensors it was made from."""
+
+    __slots__ = ("arg", "tensors", "n_tokens", "workspace_bytes", "cache")
+
+
+def _paged_check(status: int, c=None):
+    if status != FM_OK:
+        lib = load_library()
+        raise FmError(status, f"{lib.fm_status_str(status).decode()}: {lib.fm_paged_last_error(c).decode()}")
+
+
+def fm_paged_create(k_pool, v_pool, n_heads: int, rot_dims: int = 0, layout: int = FM_ROPE_INTERLEAVED, theta: float = 1e4,
+                    scaling: int = FM_ROPE_PLAIN, factor: float = 1.0, original_rows: int = 0, low: float = 1.0,
+                    high: float = 32.0, gain: float = 1.0, eps: float = 1e-6, stream=None) -> PagedCache:
+    """A KV cache in pages over the caller's pool: k_pool, v_pool, contiguous CUDA tensors [n_layers, n_pages, n_kv_heads,
+    page_rows, head_dim] of float16 or bfloat16, on the current device.  n_heads query heads read it.  The first rot_dims
+    of a head are rotated by position in `layout`'s pairs, the angles scaled as `scaling` says."""
+    import torch
+    dtypes = {torch.float16: FM_DTYPE_F16, torch.bfloat16: FM_DTYPE_BF16}
+    if k_pool.dtype not in dtypes or v_pool.dtype != k_pool.dtype or v_pool.shape != k_pool.shape or k_pool.dim() != 5:
+        raise ValueError("k_pool and v_pool must be float16 or bfloat16 tensors [layers, pages, kv_heads, page_rows, head_dim] of "
+                         "one shape and dtype")
+    if not (k_pool.is_cuda and k_pool.is_contiguous() and v_pool.is_contiguous()) or v_pool.device != k_pool.device:
+        raise ValueError("k_pool and v_pool must be contiguous and on one CUDA device")
+    if k_pool.get_device() != torch.cuda.current_device():
+        raise ValueError(f"the pool is on cuda:{k_pool.get_device()}, the current device is cuda:{torch.cuda.current_device()}")
+    layers, pages, kv_heads, page_rows, head_dim = k_pool.shape
+    g = FmPagedConfig(layers, pages, page_rows, n_heads, kv_heads, head_dim, dtypes[k_pool.dtype], rot_dims, layout, scaling,
+                      original_rows, theta, factor, low, high, gain, eps)
+    c = PagedCache()
+    _paged_check(load_library().fm_paged_create(ctypes.byref(g), k_pool.data_ptr(), v_pool.data_ptr(), _stream(stream),
+                                                ctypes.byref(c)))
+    c._pool, c._heads, c._kv_heads, c._head_dim = (k_pool, v_pool), n_heads, kv_heads, head_dim
+    c._dtype, c._code, c._device = k_pool.dtype, dtypes[k_pool.dtype], k_pool.get_device()
+    return c
+
+
+def fm_paged_batch(c, starts, lengths, table, n_tokens: int, max_new: Optional[int] = None) -> PagedBatch:
+    """The place of a batch's new rows: starts [n_seqs + 1], lengths [n_seqs] and table [n_seqs, pages], int32 CUDA tensors
+    whose values the calls read when they run (so they may be rewritten in place, between a graph's replays too).  n_tokens:
+    packed rows; max_new: the most new rows a sequence may have (n_tokens unless given)."""
+    import torch
+    n = lengths.shape[0]
+    for x, what, shape in ((starts, "starts", (n + 1,)), (lengths, "lengths", (n,)), (table, "table", (n, table.shape[-1]))):
+        if x.dtype != torch.int32 or x.get_device() != c._device or tuple(x.shape) != shape:
+            raise ValueError(f"{what} must be an int32 tensor {list(shape)} on cuda:{c._device}")
+        if x.numel() and x.shape[-1] > 1 and x.stride(-1) != 1:
+            raise ValueError(f"{what} must be contiguous along its last axis")
+    b = PagedBatch()
+    ld = table.stride(0) if n > 1 else table.shape[1]
+    b.arg = FmPagedBatch(starts.data_ptr(), lengths.data_ptr(), table.data_ptr(), ld, n, n_tokens, table.shape[1],
+                         n_tokens if max_new is None else max_new)
+    b.tensors, b.n_tokens, b.cache = (starts, lengths, table), n_tokens, c
+    b.workspace_bytes = fm_paged_workspace_bytes(c, b.arg.max_new)
+    return b
+
+
+def _paged_rows(x, heads: int, batch: PagedBatch, c, dtype, what: str) -> FmPagedRows:
+    """The library's view of a tensor [>= n_tokens, heads, head_dim] whose last axis is contiguous."""
+    shape, stride = x.shape, x.stride()
+    if x.dtype != dtype or x.get_device() != c._device:
+        raise ValueError(f"{what} must be a {dtype} tensor on cuda:{c._device}")
+    if len(shape) != 3 or shape[0] < batch.n_tokens or shape[1] != heads or shape[2] != c._head_dim:
+        raise ValueError(f"{what} has shape {tuple(shape)}, expected [{batch.n_tokens}, {heads}, {c._head_dim}]")
+    if stride[2] != 1:
+        raise ValueError(f"{what}: a row's values must be contiguous")
+    return FmPagedRows(x.data_ptr(), stride[0], stride[1])
+
+
+def _paged_norm(w, c, what: str):
+    import torch
+    if w is None:
+        return None
+    if w.dtype != torch.float32 or w.get_device() != c._device or tuple(w.shape) != (c._head_dim,) or not w.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous float32 tensor [{c._head_dim}] on cuda:{c._device}")
+    return w.data_ptr()
+
+
+def _paged_of(c, batch: PagedBatch):
+    if batch.cache is not c:
+        raise ValueError("the batch was made for another cache")
+    return ctypes.byref(batch.arg)
+
+
+def fm_paged_write(c, layer: int, batch: PagedBatch, q=None, k=None, v=None, q_out=None, q_norm=None, k_norm=None,
+                   stream=None) -> None:
+    """The batch's new rows into the pages of `layer`: k (normed by k_norm, rotated) and v, and q (normed by q_norm, rotated)
+    into q_out.  q: [n_tokens, n_heads, head_dim], k, v: [n_tokens, n_kv_heads, head_dim], of float32 or the pool's type, any
+    stride between tokens and heads (whole 16 bytes); q_out: of the pool's type.  q and q_out, or k and v, may be None;
+    norms: float32 [head_dim] or None."""
+    import torch
+    first = q if q is not None else k
+    f32 = first is not None and first.dtype == torch.float32
+    t = torch.float32 if f32 else c._dtype
+    args = []
+    for x, heads, dtype, what in ((q, c._heads, t, "q"), (k, c._kv_heads, t, "k"), (v, c._kv_heads, t, "v"),
+                                  (q_out, c._heads, c._dtype, "q_out")):
+        args.append(None if x is None else ctypes.byref(_paged_rows(x, heads, batch, c, dtype, what)))
+    _paged_check(load_library().fm_paged_write(c, layer, _paged_of(c, batch), args[0], args[1], args[2],
+                                               FM_DTYPE_F32 if f32 else c._code, _paged_norm(q_norm, c, "q_norm"),
+                                               _paged_norm(k_norm, c, "k_norm"), args[3], _stream(stream)), c)
+
+
+def fm_paged_attend(c, layer: int, batch: PagedBatch, q, out, scale: Optional[float] = None, causal: bool = True, window: int = 0,
+                    sinks: int = 0, workspace=None, stream=None) -> None:
+    """Attention of the batch's new rows over the pages of `layer`; q, out: [n_tokens, n_heads, head_dim] of the pool's type.
+    scale: 1 / sqrt(head_dim) unless given; window: rows a row sees back from its own (0: all), and the first `sinks` rows
+    besides.  workspace: a CUDA uint8 tensor of at least batch.workspace_bytes that nothing else uses until the call is done;
+    one is allocated in the call's stream (or the graph's pool) unless given."""
+    if workspace is None:
+        import torch
+        if stream is None:
+            workspace = torch.empty(batch.workspace_bytes, dtype=torch.uint8, device=q.device)
+        else:
+            other = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream), device=q.device)
+            with torch.cuda.stream(other):
+                workspace = torch.empty(batch.workspace_bytes, dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != c._device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{c._device}")
+    qr = _paged_rows(q, c._heads, batch, c, c._dtype, "q")
+    o = _paged_rows(out, c._heads, batch, c, c._dtype, "out")
+    _paged_check(load_library().fm_paged_attend(
+        c, layer, _paged_of(c, batch), ctypes.byref(qr), ctypes.byref(o), c._head_dim ** -0.5 if scale is None else scale,
+        1 if causal else 0, window, sinks, workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream)), c)
+
+
+def fm_paged_workspace_bytes(c, max_new: int) -> int:
+    v = ctypes.c_int64()
+    _paged_check(load_library().fm_paged_workspace_bytes(c, max_new, ctypes.byref(v)), c)
+    return v.value
+
+
+def fm_paged_get_config(c) -> FmPagedConfig:
+    g = FmPagedConfig()
+    _paged_check(load_library().fm_paged_get_config(c, ctypes.byref(g)), c)
+    return g
+
+
+def fm_paged_last_launch_count(c) -> int:
+    n = ctypes.c_int32()
+    _paged_check(load_library().fm_paged_last_launch_count(c, ctypes.byref(n)), c)
+    return n.value
+
+
+def fm_paged_synchronize(c, stream=None) -> None:
+    """Wait for the stream; raise FmError(FM_ERR_TIMEOUT) if a bounded device wait gave up, FmError(FM_ERR_INVALID_ARG) if a
+    batch's starts, lengths or pages pointed outside, since the last check."""
+    _paged_check(load_library().fm_paged_synchronize(c, _stream(stream)), c)
+
+
+def fm_paged_selftest_wait_timeout(c, budget_us: int, stream=None) -> None:
+    """Run a bounded device wait that cannot complete; it gives up after budget_us and the next fm_paged_synchronize raises
+    FmError(FM_ERR_TIMEOUT)."""
+    _paged_check(load_library().fm_paged_selftest_wait_timeout(c, budget_us, _stream(stream)), c)
+
+
+def fm_paged_destroy(c) -> None:
+    if c is not None and c.value:
+        load_library().fm_paged_destroy(c)
+        c.value = None
+        c._pool = None

@@ -1,0 +1,195 @@
+// k_paged_write.cu -- a batch's new rows into a paged cache: per-head RMSNorm of queries and keys, the position
+// rotation, the store to q_out and to the pages, in one pass.
+//
+//   y = x / sqrt(mean(x^2) + eps) * w;   (u, v) -> gain (u cos t - v sin t, u sin t + v cos t) for the pairs of the first
+//   rot dims, t = pos f_i;   V is stored as it is
+// Sums and rotation are f32; the one rounding is the store's.  Angles: positions go far and f_i need not be small, so the
+// turns pos f_i / 2 pi are taken in 64-bit fixed point (f_i / 2 pi in units of 2^-64, whole turns fall out of the
+// product; what is left of the error is f_i's own, an f64's), and only the fraction of a turn becomes an f32.
+//
+// Bound: memory (each value read and written once).  A CTA takes `tokens` tokens (one where the batch is small, so that a
+// single token's heads spread over `split` CTAs): its threads first compute the tokens' sines and cosines, one a thread,
+// then each group of head_dim / 8 lanes takes (token, head) rows, 8 values a lane: one or two 16-byte loads, the mean by
+// shuffles, the partner of a pair from the same lane or, in the half layout, from the lane rot / 16 away.
+#include "paged_dev.cuh"
+
+namespace fm {
+namespace {
+
+constexpr int kWThreads = 256;
+constexpr int kWTokens = 8;        // tokens of a CTA at most
+
+// The sequence of packed row t: the last i with starts[i] <= t (a warp's 32-way search).
+__device__ __forceinline__ int find_seq(const PagedBatch &b, int t, int lane) {
+  int lo = 0, hi = b.n_seqs;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32, i = lo + lane * step;
+    const uint32_t below = __ballot_sync(0xffffffffu, i < hi && __ldcg(b.starts + i) <= t);
+    const int k = below ? 31 - __clz(below) : 0;
+    lo += k * step;
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
+template <int HD, bool BF16, bool F32IN>
+__global__ void __launch_bounds__(kWThreads) fm_paged_write_kernel(const __grid_constant__ PagedWriteArgs a) {
+  constexpr int kLanes = HD / 8;                    // of a row
+  constexpr int kGroups = kWThreads / kLanes;       // rows at a time
+  __shared__ float2 turn[kWTokens][HD / 2];         // (cos, sin) times gain
+  __shared__ int4 where[kWTokens];                  // the token's row in the pool (first KV head; -1: none), done or not
+  const PagedBatch &b = a.b;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int t0 = blockIdx.x * a.tokens, n = min(a.tokens, b.n_tokens - t0);
+  pdl_trigger();
+  pdl_wait();
+  if (warp < n) {
+    const int t = t0 + warp, seq = find_seq(b, t, lane);
+    const PagedSeq q = paged_seq(b, seq);
+    const int pos = q.len - q.n_new + (t - q.s0);
+    const bool in = t >= q.s0 && t - q.s0 < q.n_new;   // (rows behind the last sequence are left as they are)
+    int64_t row = -1;
+    if (in && pos >= 0) {
+      const int id = __ldcg(b.table + seq * b.table_ld + (pos >> b.page_log));
+      if (id >= 0 && id < b.n_pages)
+        row = ((int64_t)(b.page0 + id) * b.n_kv << b.page_log) + (pos & ((1 << b.page_log) - 1));
+    }
+    if (in && row < 0 && lane == 0 && (a.k.p || pos < 0)) b.err[1] = 1;
+    if (lane == 0) where[warp] = make_int4((int)row, pos, in && pos >= 0, 0);
+  }
+  __syncthreads();
+  const int pairs = a.rot >> 1;
+  for (int i = threadIdx.x; i < n * pairs; i += kWThreads) {
+    const int t = i / pairs, p = i - t * pairs;
+    if (where[t].z) {
+      const uint64_t x = (uint64_t)(uint32_t)where[t].y * __ldg(a.freq + p);   // turns, whole ones dropped
+      float sn, cs;
+      sincospif((float)((int32_t)(x >> 32)) * (1.f / 2147483648.f), &sn, &cs);  // half turns in [-1, 1)
+      turn[t][p] = make_float2(cs * a.gain, sn * a.gain);
+    }
+  }
+  __syncthreads();
+  const int group = threadIdx.x / kLanes, gl = threadIdx.x % kLanes, d0 = gl * 8;
+  const int nq = a.q.p ? b.n_kv * b.group : 0, nk = a.k.p ? b.n_kv : 0;
+  // this CTA's heads
+  const int per = (a.slots + a.split - 1) / a.split, h0 = blockIdx.y * per, hn = max(0, min(per, a.slots - h0));
+  const int warp_group = (threadIdx.x & ~31) / kLanes;                 // (a warp's rows run their rounds together)
+  for (int i0 = 0; i0 + warp_group < n * hn; i0 += kGroups) {
+    const int i = i0 + group;
+    const int t = min(i, n * hn - 1) / hn, h = h0 + min(i, n * hn - 1) - t * hn;
+    const int4 w = where[t];
+    const bool live = i < n * hn && w.z;
+    const int kind = h < nq ? 0 : h < nq + nk ? 1 : 2, head = h - (kind == 0 ? 0 : kind == 1 ? nq : nq + nk);
+    const PagedRows &src = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
+    const int64_t at = (int64_t)(t0 + t) * src.ld + (int64_t)head * src.hs + d0;
+    float x[8];
+    if (live) {
+      if constexpr (F32IN) {
+        const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(src.p) + at);
+        const float4 u = __ldcs(p), v = __ldcs(p + 1);
+        x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
+      } else {
+        const uint4 u = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(src.p) + at));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t y = word(u, e);
+          float2 f;
+          if constexpr (BF16)
+            f = make_float2(__uint_as_float(y << 16), __uint_as_float(y & 0xffff0000u));
+          else
+            f = __half22float2(*reinterpret_cast<const __half2 *>(&y));
+          x[2 * e] = f.x;
+          x[2 * e + 1] = f.y;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = 0.f;
+    }
+    const float *nw = kind == 0 ? a.q_norm : kind == 1 ? a.k_norm : nullptr;
+    float ss = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss += x[e] * x[e];
+#pragma unroll
+    for (int o = kLanes >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    if (nw) {
+      const float r = rsqrtf(ss * (1.f / HD) + a.eps);
+      const float4 u = __ldg(reinterpret_cast<const float4 *>(nw + d0)), v = __ldg(reinterpret_cast<const float4 *>(nw + d0) + 1);
+      x[0] *= r * u.x, x[1] *= r * u.y, x[2] *= r * u.z, x[3] *= r * u.w;
+      x[4] *= r * v.x, x[5] *= r * v.y, x[6] *= r * v.z, x[7] *= r * v.w;
+    }
+    if (a.half) {
+      // pairs (i, i + rot / 2): the partner's 8 values lie in the lane rot / 16 further, or back
+      const int far = a.rot >> 4;                    // lanes
+      const bool low = gl < far, turned = gl < 2 * far;
+      float y[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = __shfl_sync(0xffffffffu, x[e], (threadIdx.x & 31) - gl + (turned ? (low ? gl + far : gl - far) : gl));
+      if (turned && kind != 2) {
+        const float4 *cs = reinterpret_cast<const float4 *>(&turn[t][(low ? gl : gl - far) * 8]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float4 c = cs[e];
+          x[2 * e] = low ? x[2 * e] * c.x - y[2 * e] * c.y : y[2 * e] * c.y + x[2 * e] * c.x;
+          x[2 * e + 1] = low ? x[2 * e + 1] * c.z - y[2 * e + 1] * c.w : y[2 * e + 1] * c.w + x[2 * e + 1] * c.z;
+        }
+      }
+    } else if (d0 < a.rot && kind != 2) {
+      const float4 *cs = reinterpret_cast<const float4 *>(&turn[t][gl * 4]);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float4 c = cs[e];
+        const float u0 = x[4 * e], v0 = x[4 * e + 1], u1 = x[4 * e + 2], v1 = x[4 * e + 3];
+        x[4 * e] = u0 * c.x - v0 * c.y;
+        x[4 * e + 1] = u0 * c.y + v0 * c.x;
+        x[4 * e + 2] = u1 * c.z - v1 * c.w;
+        x[4 * e + 3] = u1 * c.w + v1 * c.z;
+      }
+    }
+    if (!live) continue;
+    uint16_t *dst;
+    if (kind == 0) {
+      dst = static_cast<uint16_t *>(a.qo.p) + (int64_t)(t0 + t) * a.qo.ld + (int64_t)head * a.qo.hs;
+    } else {
+      if (w.x < 0) continue;                         // (the table has no page for it)
+      dst = static_cast<uint16_t *>(kind == 1 ? a.k_pool : a.v_pool) + ((int64_t)w.x + ((int64_t)head << b.page_log)) * HD;
+    }
+    *reinterpret_cast<uint4 *>(dst + d0) =
+        make_uint4(pack2<BF16>(x[0], x[1]), pack2<BF16>(x[2], x[3]), pack2<BF16>(x[4], x[5]), pack2<BF16>(x[6], x[7]));
+  }
+}
+
+template <int HD>
+cudaError_t launch_hd(const PagedWriteArgs &a, dim3 grid, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = kWThreads;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (a.bf16)
+    return a.in_f32 ? cudaLaunchKernelEx(&cfg, fm_paged_write_kernel<HD, true, true>, a)
+                    : cudaLaunchKernelEx(&cfg, fm_paged_write_kernel<HD, true, false>, a);
+  return a.in_f32 ? cudaLaunchKernelEx(&cfg, fm_paged_write_kernel<HD, false, true>, a)
+                  : cudaLaunchKernelEx(&cfg, fm_paged_write_kernel<HD, false, false>, a);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_write(const PagedWriteArgs &args, int n_sm, cudaStream_t s) {
+  PagedWriteArgs a = args;
+  const int rows = kWThreads / (a.hd / 8);          // (token, head) rows a CTA takes at a time
+  // Small batches: a token a CTA and its heads over several CTAs, until the SMs have two CTAs each.  Large ones: as many
+  // tokens a CTA as still leave eight a SM.
+  a.tokens = 1;
+  while (a.tokens < kWTokens && (int64_t)a.b.n_tokens / (2 * a.tokens) >= 8ll * n_sm) a.tokens *= 2;
+  a.split = 1;
+  while (a.slots > rows * a.split && (int64_t)a.b.n_tokens * 2 * a.split <= 2ll * n_sm) a.split *= 2;
+  const dim3 grid((a.b.n_tokens + a.tokens - 1) / a.tokens, a.split);
+  return a.hd == 64 ? launch_hd<64>(a, grid, s) : a.hd == 128 ? launch_hd<128>(a, grid, s) : launch_hd<256>(a, grid, s);
+}
+
+}  // namespace fm

@@ -1,0 +1,463 @@
+// paged_dev.cuh -- what the paged cache's kernels share: reading a batch's metadata, the key tiles that a
+// unit of query rows sees, and how the tiles of a launch are dealt to its CTAs.
+//
+// A unit is (sequence, KV head, tile of query rows: token x query head of the group); it sees a list of key
+// tiles, those of the first `sinks` rows and those from the window's first row to the causal end.  The
+// lengths are on the device (a captured call is replayed with other lengths), so every CTA adds up the
+// launch's tiles by itself and takes an equal, contiguous share: about 1 us for 32 sequences, once a launch,
+// against a second launch for a plan.  A unit that is cut between CTAs leaves unnormalised parts, which the
+// join kernel adds in the order of their CTAs (so the same call gives the same bits).
+#pragma once
+
+#include "dev_common.cuh"
+#include "paged.h"
+
+namespace fm {
+
+__device__ __forceinline__ void tma_2d_row(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_3d_box(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if constexpr (BF16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+  } else {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+  }
+}
+
+// The halves of a word that are infinite or NaN, as a mask of their bits.
+template <bool BF16>
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+  constexpr uint32_t e = BF16 ? 0x7f80u : 0x7c00u;
+  return ((w & e) == e ? 0xffffu : 0u) | ((w >> 16 & e) == e ? 0xffff0000u : 0u);
+}
+
+struct PagedSeq {
+  int s0, n_new, len;   // first packed row, new rows, rows held (the new ones are the last)
+};
+
+// Sequence i, or one without rows where its numbers point outside the batch or the table.
+__device__ __forceinline__ PagedSeq paged_seq(const PagedBatch &b, int i) {
+  PagedSeq q;
+  const int s0 = __ldcg(b.starts + i), s1 = __ldcg(b.starts + i + 1), len = __ldcg(b.lengths + i);
+  const bool ok = s0 >= 0 && s1 >= s0 && s1 <= b.n_tokens && len >= 0 && (int64_t)len <= ((int64_t)b.table_pages << b.page_log);
+  if (!ok) b.err[1] = 1;
+  q.s0 = s0;
+  q.n_new = ok ? s1 - s0 : 0;
+  q.len = ok ? len : 0;
+  return q;
+}
+
+// The key tiles (of kTile rows) that query tokens ta .. tb of a sequence see between them.
+struct PagedSpan {
+  int lo, hi;        // rows lo <= j < hi, and those below `sinks`
+  int lt, ns, n;     // the list: tiles 0 .. ns - 1, then lt, lt + 1, ...; n in all, one at least
+  int all_hi, all_lo;   // rows below all_hi are ahead of every token's end, those from all_lo on inside every window
+  __device__ __forceinline__ int tile(int i) const { return i < ns ? i : lt + i - ns; }
+};
+
+template <int kTile>
+__device__ __forceinline__ PagedSpan paged_span(const PagedAttnArgs &a, const PagedSeq &q, int ta, int tb) {
+  PagedSpan s;
+  const int pos0 = q.len - q.n_new;
+  s.hi = a.causal ? max(0, min(q.len, pos0 + tb + 1)) : q.len;
+  s.all_hi = a.causal ? pos0 + ta + 1 : q.len;
+  s.lo = a.window ? max(0, pos0 + ta - a.window + 1) : 0;
+  s.all_lo = a.window ? pos0 + tb - a.window + 1 : 0;
+  if (s.lo > s.hi) s.lo = s.hi;
+  s.lt = s.lo / kTile;
+  const int ht = (s.hi + kTile - 1) / kTile;
+  s.ns = a.window ? min((min(a.sinks, s.hi) + kTile - 1) / kTile, s.lt) : 0;
+  s.n = max(1, s.ns + max(0, ht - s.lt));
+  return s;
+}
+
+// Whether some token of the unit does not see some row of the tile.
+template <int kTile>
+__device__ __forceinline__ bool paged_masked(const PagedAttnArgs &a, const PagedSpan &s, int key0) {
+  return key0 + kTile > s.all_hi || (key0 < s.all_lo && key0 + kTile > a.sinks);
+}
+// Whether the token at position pos sees row j (j >= 0).
+__device__ __forceinline__ bool paged_sees(const PagedAttnArgs &a, const PagedSeq &q, int pos, int j) {
+  return j < q.len && (!a.causal || j <= pos) && (!a.window || j > pos - a.window || j < a.sinks);
+}
+
+// Where row `row` of the sequence lies in the pool (a page the unit does not see, or one that the table has no
+// valid number for, reads as zeros): the tensor map's row.
+__device__ __forceinline__ int paged_row(const PagedAttnArgs &a, const PagedSpan &s, int seq, int head, int row) {
+  const PagedBatch &b = a.b;
+  const int pg = row >> b.page_log, r0 = pg << b.page_log, r1 = r0 + (1 << b.page_log);
+  if (!((r0 < s.hi && r1 > s.lo) || (a.window && r0 < min(a.sinks, s.hi)))) return a.oob_row;
+  const int id = __ldcg(b.table + seq * b.table_ld + pg);
+  if (id < 0 || id >= b.n_pages) {
+    b.err[1] = 1;
+    return a.oob_row;
+  }
+  return (((b.page0 + id) * b.n_kv + head) << b.page_log) + (row - r0);
+}
+
+// A unit's shape: kFlat: kRows consecutive (token, head) rows; otherwise kSub tiles of whole tokens, 128 / group each.
+template <int kRows, bool kFlat>
+struct PagedTiles {
+  static constexpr int kSub = kFlat ? 1 : kRows / 128;
+  static __device__ __forceinline__ int tokens(int group) { return 128 / group; }   // of a 128-row tile
+  static __device__ __forceinline__ int count(const PagedSeq &q, int group) {
+    if (kFlat) return (q.n_new * group + kRows - 1) / kRows;
+    const int t = kSub * tokens(group);
+    return (q.n_new + t - 1) / t;
+  }
+  static __device__ __forceinline__ int first(int tile, int group) {
+    return kFlat ? tile * kRows / group : tile * kSub * tokens(group);
+  }
+  static __device__ __forceinline__ int last(const PagedSeq &q, int tile, int group) {
+    if (kFlat) return (min(q.n_new * group, (tile + 1) * kRows) - 1) / group;
+    return min(q.n_new, (tile + 1) * kSub * tokens(group)) - 1;
+  }
+};
+
+// One CTA's part of a unit: key tiles begin .. end - 1 of its list.
+struct PagedSeg {
+  PagedSeq q;
+  PagedSpan s;
+  int seq, head, tile, begin, end;
+  __device__ __forceinline__ bool whole() const { return begin == 0 && end == s.n; }
+};
+
+struct PagedStart {       // where a CTA's share begins
+  long long left;         // places of its share
+  long long share;
+  int seq, head, tile, off;
+};
+
+// Walks a CTA's share.  A unit takes kCost places before its tiles', what beginning and ending one costs in tiles.
+template <int kRows, bool kFlat, int kTile, int kCost>
+struct PagedWalk {
+  using Tiles = PagedTiles<kRows, kFlat>;
+  long long left, share;
+  int seq, head, tile, off, tiles;
+  PagedSeq q;
+  bool loaded;
+
+  __device__ __forceinline__ void init(const PagedStart &p) {
+    left = p.left, share = p.share, seq = p.seq, head = p.head, tile = p.tile, off = p.off;
+    loaded = false;
+  }
+  // The CTAs that the unit of a segment with begin == 0 is cut into: this share ended with the segment, the rest of the
+  // unit fills the shares behind it.
+  __device__ __forceinline__ int parts(const PagedSeg &g) const {
+    return 1 + (int)((g.s.n - g.end + share - 1) / share);
+  }
+  __device__ __forceinline__ bool next(const PagedAttnArgs &a, PagedSeg &g) {
+    const PagedBatch &b = a.b;
+    while (left > 0 && seq < b.n_seqs) {
+      if (!loaded) {
+        q = paged_seq(b, seq);
+        tiles = Tiles::count(q, b.group);
+        loaded = true;
+      }
+      if (tiles == 0) {
+        ++seq;
+        loaded = false;
+        continue;
+      }
+      g.q = q;
+      g.seq = seq, g.head = head, g.tile = tile;
+      g.s = paged_span<kTile>(a, q, Tiles::first(tile, b.group), Tiles::last(q, tile, b.group));
+      const int total = g.s.n + kCost;
+      const int take = (int)min((long long)(total - off), left);
+      g.begin = max(0, off - kCost);
+      g.end = max(0, off + take - kCost);
+      left -= take;
+      off += take;
+      if (off == total) {
+        off = 0;
+        if (++tile == tiles) {
+          tile = 0;
+          if (++head == b.n_kv) {
+            head = 0;
+            ++seq;
+            loaded = false;
+          }
+        }
+      }
+      if (g.end > g.begin) return true;
+    }
+    return false;
+  }
+};
+
+// Adds up the launch's places and finds where this CTA's share begins.  Every thread of the CTA calls it; sh: kThreads
+// long longs and a PagedStart in shared memory.  Shares are at least kLeast places.
+template <int kRows, bool kFlat, int kTile, int kCost, int kLeast, int kThreads>
+__device__ __forceinline__ void paged_plan(const PagedAttnArgs &a, long long *sh, PagedStart *out) {
+  using Tiles = PagedTiles<kRows, kFlat>;
+  const PagedBatch &b = a.b;
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  constexpr int kWarps = kThreads / 32;
+  // places of one KV head of a sequence; sequences of many tiles are summed by the whole warp
+  auto one = [&](const PagedSeq &q, int i) -> int {
+    return paged_span<kTile>(a, q, Tiles::first(i, b.group), Tiles::last(q, i, b.group)).n + kCost;
+  };
+  auto cost = [&](int i) -> long long {
+    PagedSeq q = {0, 0, 0};
+    if (i < b.n_seqs) q = paged_seq(b, i);
+    const int nt = Tiles::count(q, b.group);
+    long long c = 0;
+    if (nt <= 4)
+      for (int j = 0; j < nt; ++j) c += one(q, j);
+    for (uint32_t m = __ballot_sync(0xffffffffu, nt > 4); m; m &= m - 1) {
+      const int src = __ffs(m) - 1;
+      PagedSeq r;
+      r.s0 = 0;
+      r.n_new = __shfl_sync(0xffffffffu, q.n_new, src);
+      r.len = __shfl_sync(0xffffffffu, q.len, src);
+      const int n = __shfl_sync(0xffffffffu, nt, src);
+      long long x = 0;
+      for (int j = lane; j < n; j += 32) x += one(r, j);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+      if (lane == src) c = x;
+    }
+    return c;
+  };
+  // sums of the threads' places over the whole launch; with one round of sequences the threads keep their own
+  long long mine = 0, all = 0;
+  const int rounds = (b.n_seqs + kThreads - 1) / kThreads;
+  for (int r = 0; r < rounds; ++r) {
+    mine = cost(r * kThreads + t) * b.n_kv;
+    all += mine;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+  if (lane == 0) sh[warp] = all;
+  __syncthreads();
+  all = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) all += sh[w];
+  long long share = (all + gridDim.x - 1) / gridDim.x;
+  if (share < kLeast) share = kLeast;
+  const long long from = share * blockIdx.x;
+  if (t == 0) {
+    out->share = share;
+    out->left = from < all ? min(share, all - from) : 0;
+    out->seq = b.n_seqs;
+    out->head = out->tile = out->off = 0;
+  }
+  __syncthreads();
+  if (from >= all) return;
+  // the sequence that holds place `from`
+  long long before = 0;
+  for (int r = 0; r < rounds; ++r) {
+    if (rounds > 1) mine = cost(r * kThreads + t) * b.n_kv;
+    long long x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) sh[warp] = x;
+    __syncthreads();
+    long long lower = before;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) lower += sh[w];
+      before += sh[w];
+    }
+    const long long end = lower + x, begin = end - mine;
+    if (mine > 0 && from >= begin && from < end) {
+      sh[kWarps] = from - begin;
+      out->seq = r * kThreads + t;
+    }
+    if (before > from) break;   // (the same for every thread)
+  }
+  __syncthreads();
+  // the KV head and the tile in it
+  if (warp == 0) {
+    const PagedSeq q = paged_seq(b, out->seq);
+    const int nt = Tiles::count(q, b.group);
+    long long x = 0;
+    for (int j = lane; j < nt; j += 32) x += one(q, j);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    const long long rest = sh[kWarps];
+    const int head = (int)(rest / x);
+    long long in = rest - head * x;
+    for (int j0 = 0; j0 < nt; j0 += 32) {
+      const int j = j0 + lane;
+      const long long c = j < nt ? one(q, j) : 0;
+      long long e = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, e, o);
+        if (lane >= o) e += y;
+      }
+      if (c > 0 && in >= e - c && in < e) {
+        out->head = head;
+        out->tile = j;
+        out->off = (int)(in - (e - c));
+      }
+      const long long sum = __shfl_sync(0xffffffffu, e, 31);
+      if (in < sum) break;
+      in -= sum;
+    }
+  }
+  __syncthreads();
+}
+
+// The sum over the infinite and NaN values of V, column d, in masked tiles of the segment, that the token at `pos` sees
+// (each counted with weight 1, which gives the infinity or NaN that any positive weight would).  Only asked where the
+// segment met one: such values are taken out of the tile ahead of the product, where a weight of 0 would make NaN of them
+// for rows that do not see them.
+template <int kTile, bool BF16>
+__device__ __noinline__ float paged_poison(const PagedAttnArgs &a, const PagedSeg &g, int hd, int pos, int d) {
+  float sum = 0.f;
+  const uint16_t *v = static_cast<const uint16_t *>(a.v_pool);
+  for (int i = g.begin; i < g.end; ++i) {
+    const int key0 = g.s.tile(i) * kTile;
+    if (!paged_masked<kTile>(a, g.s, key0)) continue;
+    for (int j = key0; j < key0 + kTile; ++j) {
+      if (!paged_sees(a, g.q, pos, j)) continue;
+      const int row = paged_row(a, g.s, g.seq, g.head, j);
+      if (row == a.oob_row) continue;
+      const uint32_t x = v[(int64_t)row * hd + d];
+      if (!not_finite<BF16>(x)) continue;
+      sum += BF16 ? __uint_as_float(x << 16) : __half2float(__ushort_as_half((unsigned short)x));
+    }
+  }
+  return sum;
+}
+
+// Joins the parts of the units that were cut.  Block (i, y): the unit that CTA i began; a warp takes a row at a time, or
+// a share of the row's parts where kSplit > 1 warps work on one row.
+template <int HD, int kRows, bool kFlat, bool BF16, int kSplit>
+__global__ void __launch_bounds__(512) fm_paged_join_kernel(const __grid_constant__ PagedAttnArgs a) {
+  using Tiles = PagedTiles<kRows, kFlat>;
+  __shared__ float4 acc[kSplit > 1 ? 16 : 1][kSplit > 1 ? HD / 4 : 1];
+  pdl_trigger();
+  pdl_wait();
+  const int4 d = __ldcg(a.desc + blockIdx.x);
+  if (d.w == 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const PagedSeq q = paged_seq(a.b, d.x);
+  const int group = a.b.group, cta = blockIdx.x;
+  constexpr int kWarpRows = 16 / kSplit;      // rows a round of the block
+  constexpr int kVec = HD / 128 > 0 ? HD / 128 : 1;   // float4 a lane
+  for (int r0 = blockIdx.y * kWarpRows; r0 < kRows; r0 += gridDim.y * kWarpRows) {
+    const int row = r0 + warp / kSplit, sub = warp % kSplit;
+    int token, head;
+    bool valid;
+    if (kFlat) {
+      const int r = d.z * kRows + row;
+      token = r / group;
+      head = r - token * group;
+      valid = r < q.n_new * group;
+    } else {
+      const int tt = Tiles::tokens(group), in = row & 127;
+      token = (d.z * Tiles::kSub + (row >> 7)) * tt + in / group;
+      head = in % group;
+      valid = in < tt * group && token < q.n_new;
+    }
+    auto slot = [&](int p) -> size_t { return p == 0 ? 2 * (size_t)cta + 1 : 2 * (size_t)(cta + p); };
+    float top = -INFINITY;
+    if (valid)
+      for (int p = lane; p < d.w; p += 32) top = fmaxf(top, __ldcg(a.part_ml + slot(p) * kRows + row).x);
+    top = warp_max(top);
+    float l = 0.f;
+    float4 o[kVec];
+#pragma unroll
+    for (int v = 0; v < kVec; ++v) o[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (valid && !(top == -INFINITY)) {
+      // sums of weights: every warp of the row adds all of them, in order
+      for (int p0 = 0; p0 < d.w; p0 += 32) {
+        const int p = p0 + lane;
+        float w = 0.f;
+        if (p < d.w) {
+          const float2 ml = __ldcg(a.part_ml + slot(p) * kRows + row);
+          w = ml.x == -INFINITY ? 0.f : ex2(ml.x - top) * ml.y;
+        }
+        l += warp_sum(w);
+      }
+      constexpr int kAhead = kVec == 2 ? 4 : 8;
+      for (int p0 = sub; p0 < d.w; p0 += kSplit * kAhead) {
+        float4 x[kAhead][kVec];
+        float w[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          const int p = p0 + u * kSplit;
+          w[u] = 0.f;
+          if (p < d.w) {
+            const float m = __ldcg(a.part_ml + slot(p) * kRows + row).x;
+            w[u] = m == -INFINITY ? 0.f : ex2(m - top);
+#pragma unroll
+            for (int v = 0; v < kVec; ++v)
+              if (4 * lane + 128 * v < HD)
+                x[u][v] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + (slot(p) * kRows + row) * HD) + lane + 32 * v);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+          if (p0 + u * kSplit < d.w)
+#pragma unroll
+            for (int v = 0; v < kVec; ++v)
+              if (4 * lane + 128 * v < HD) {
+                o[v].x += w[u] * x[u][v].x;
+                o[v].y += w[u] * x[u][v].y;
+                o[v].z += w[u] * x[u][v].z;
+                o[v].w += w[u] * x[u][v].w;
+              }
+      }
+    }
+    if constexpr (kSplit > 1) {
+      __syncthreads();
+#pragma unroll
+      for (int v = 0; v < kVec; ++v)
+        if (4 * lane + 128 * v < HD) acc[warp][lane + 32 * v] = o[v];
+      __syncthreads();
+      if (sub == 0) {
+#pragma unroll
+        for (int s = 1; s < kSplit; ++s)
+#pragma unroll
+          for (int v = 0; v < kVec; ++v)
+            if (4 * lane + 128 * v < HD) {
+              const float4 x = acc[warp + s][lane + 32 * v];
+              o[v].x += x.x;
+              o[v].y += x.y;
+              o[v].z += x.z;
+              o[v].w += x.w;
+            }
+      }
+    }
+    if (valid && sub == 0) {
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      uint16_t *out = static_cast<uint16_t *>(a.out.p) + (int64_t)(q.s0 + token) * a.out.ld +
+                      (int64_t)(d.y * group + head) * a.out.hs;
+#pragma unroll
+      for (int v = 0; v < kVec; ++v)
+        if (4 * lane + 128 * v < HD)
+          *reinterpret_cast<uint2 *>(out + 4 * lane + 128 * v) =
+              make_uint2(pack2<BF16>(o[v].x * inv, o[v].y * inv), pack2<BF16>(o[v].z * inv, o[v].w * inv));
+    }
+  }
+}
+
+}  // namespace fm

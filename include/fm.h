@@ -717,6 +717,153 @@ FM_API void fm_kvq_destroy(fm_kvq *c);
  */
 FM_API fm_status fm_mtp_use_kvq(fm_mtp *m, fm_kvq *c, int32_t layer, int32_t seq, int64_t next_pos, float decay);
 
+/* ------------------------------------------------------------------------
+ * A KV cache in pages: a batch's new rows are written to it with the per-head
+ * norms and the position rotation in the same pass (fm_paged_write), and
+ * attended over from there (fm_paged_attend), with or without a sliding window
+ * and a few first rows that stay visible.  The pages keep one contiguous cache
+ * a sequence; this one has no counterpart there.  It stands by itself, or holds
+ * the MTP head's rows (fm_mtp_use_paged).
+ *
+ * The pool is the caller's: K and V apart, each
+ * [n_layers][n_pages][n_kv_heads][page_rows][head_dim] of dtype, 16-byte
+ * aligned, alive and in place as long as the handle is used.  What lies in it
+ * is plain values, so pages may be shared, copied and handed round.
+ *
+ * A batch (fm_paged_batch) says which rows are new and where sequences lie.
+ * Its numbers are on the device: a captured call reads them again at every
+ * replay.  Sequence i's new rows are rows starts[i] .. starts[i + 1] - 1 of the
+ * packed rows; lengths[i] rows are in the cache once they are written, the new
+ * ones the last, so a new row t of n has position lengths[i] - n + t.  Row j of
+ * the sequence is row j % page_rows of page table[i][j / page_rows].  Several
+ * sequences may name one page to read from; a row that a call writes is named
+ * once.  Packed rows behind starts[n_seqs] and rows that no call names are left
+ * as they are.
+ * A sequence whose starts or length point outside the packed rows or the table
+ * is left out of the call; a page outside the pool that is needed is read as
+ * zeros and not written; fm_paged_synchronize reports both.
+ *
+ * Calls allocate and copy nothing and change nothing in the handle: several
+ * may run at once, from several host threads, on several streams and in
+ * several graphs, as long as each has its own workspace and what they write is
+ * apart.  The cache's device must be the current device.  Row pointers are
+ * 16-byte aligned, their strides whole multiples of 16 bytes; a row's head_dim
+ * values are contiguous.  Strides of an axis of one entry are not looked at.
+ * ------------------------------------------------------------------------ */
+#define FM_ROPE_INTERLEAVED 0   /* pairs (2 i, 2 i + 1) */
+#define FM_ROPE_HALF 1          /* pairs (i, i + rot_dims / 2) */
+#define FM_ROPE_PLAIN 0         /* angle pos f_i, f_i = theta^(-2 i / rot_dims) */
+#define FM_ROPE_LINEAR 1        /* f_i / rope_factor */
+#define FM_ROPE_BY_PARTS 2      /* f_i (r + (1 - r) / rope_factor), r = clamp((rope_rows f_i / 2 pi - rope_low) / (rope_high - rope_low), 0, 1):
+                                   pairs that turn at least rope_high times over rope_rows rows keep their angle, those
+                                   that turn at most rope_low times are stretched */
+
+typedef struct fm_paged_config {
+  int32_t n_layers;      /* 1 .. 1024 */
+  int32_t n_pages;       /* pages a layer */
+  int32_t page_rows;     /* 16, 32, 64, 128 or 256 */
+  int32_t n_heads;       /* query heads, a multiple of n_kv_heads, at most 128 times as many */
+  int32_t n_kv_heads;    /* 1 .. 256 */
+  int32_t head_dim;      /* 64, 128 or 256 */
+  int32_t dtype;         /* FM_DTYPE_F16 or FM_DTYPE_BF16: the pool's, and the attention's rows' */
+  int32_t rot_dims;      /* rotated dims of a head, the first ones: a multiple of 16, 0 for none */
+  int32_t rot_layout;    /* FM_ROPE_INTERLEAVED or FM_ROPE_HALF */
+  int32_t rope_scaling;  /* FM_ROPE_PLAIN, FM_ROPE_LINEAR or FM_ROPE_BY_PARTS */
+  int32_t rope_rows;     /* BY_PARTS: the context the angles were made for */
+  float theta;           /* RoPE base, at least 1 */
+  float rope_factor;     /* LINEAR, BY_PARTS: at least 1 */
+  float rope_low, rope_high;   /* BY_PARTS: turns */
+  float rope_gain;       /* the rotated dims are multiplied by it (1; scaled contexts may want more) */
+  float eps;             /* of the norms */
+} fm_paged_config;       /* (the rope fields and theta are not looked at where rot_dims is 0) */
+
+typedef struct fm_paged_batch {
+  const int32_t *starts;    /* device [n_seqs + 1], never falling */
+  const int32_t *lengths;   /* device [n_seqs] */
+  const int32_t *table;     /* device [n_seqs][table_pages], rows table_ld entries apart */
+  int64_t table_ld;
+  int32_t n_seqs;           /* 0 .. 65536 */
+  int32_t n_tokens;         /* packed rows that q, k, v and out hold (starts[n_seqs] of them at most are new) */
+  int32_t table_pages;      /* pages a sequence may have; at most 2^30 rows */
+  int32_t max_new;          /* the most new rows a sequence may have: chooses the attention kernel and its workspace
+                               (more of them than that are attended over all the same) */
+} fm_paged_batch;
+
+/* Rows [n_tokens][heads][head_dim]: data, and elements between tokens and between heads. */
+typedef struct fm_paged_rows {
+  void *data;
+  int64_t token_stride, head_stride;
+} fm_paged_rows;
+
+typedef struct fm_paged fm_paged;
+
+/*
+ * fm_paged_create -- a cache over the caller's pool, on the current device (the pool's).  Synchronises the stream.
+ * Errors: FM_ERR_INVALID_ARG, FM_ERR_UNSUPPORTED (head_dim, page_rows, heads a
+ *   KV head, a pool of over 2^31 - 257 rows of heads), FM_ERR_OOM, FM_ERR_CUDA; *out is NULL on
+ *   failure and the reason is in fm_paged_last_error(NULL).
+ */
+FM_API fm_status fm_paged_create(const fm_paged_config *cfg, void *k_pool_dev, void *v_pool_dev, void *stream,
+                                 fm_paged **out);
+
+/*
+ * fm_paged_write -- per new row and head: q and k are divided by their root
+ * mean square, sqrt(mean x^2 + eps), and multiplied by q_norm / k_norm (f32
+ * [head_dim], 16-byte aligned; NULL: no norm), rotated at the row's position,
+ * and rounded once to the pool's type; q goes to q_out, k and v (v as it is) to
+ * the row's place in layer's pages.  q and q_out may be NULL (rows of context),
+ * or k and v (queries alone; the pages are then not looked at).  dtype:
+ * FM_DTYPE_F32 or the pool's.  Norms and rotation are f32; a position's angle
+ * is taken from 64-bit turns, so far positions lose nothing.  q_out may be q
+ * itself (the same type and strides).  Rows with a negative position (more new
+ * rows than the length) are not written, and reported.
+ * Errors: FM_ERR_INVALID_ARG, FM_ERR_UNSUPPORTED (limits above, 2^31 - 1 rows of heads in
+ *   a batch), FM_ERR_CUDA.
+ */
+FM_API fm_status fm_paged_write(fm_paged *c, int32_t layer, const fm_paged_batch *batch, const fm_paged_rows *q,
+                                const fm_paged_rows *k, const fm_paged_rows *v, int32_t dtype,
+                                const float *q_norm_dev, const float *k_norm_dev, const fm_paged_rows *q_out,
+                                void *stream);
+
+/*
+ * fm_paged_attend -- per new row (position p) and query head h:
+ *   out = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale q . k_j),
+ * over KV head h / (n_heads / n_kv_heads) and the rows j < length that it sees:
+ * all of them; with causal != 0 those with j <= p; with a window > 0 (causal
+ * only) those of them with j > p - window, and the first `sinks` (those with
+ * j <= p).  A row that sees nothing gives zeros.  q and out are of the pool's type and do not overlap
+ * (out->data == q->data is refused).
+ * Scores, weights' sums and outputs are summed in f32; each weight is rounded
+ * once to the pool's type where it multiplies v, the output once at the end.  A
+ * row that is not seen has no part in the result, whatever it holds (pages
+ * outside every window of the call's rows are not read, their table entries
+ * may be stale).  Of a key whose weight is below 2^-24 (f16) of the largest one
+ * the part may be lost.
+ * workspace_dev: fm_paged_workspace_bytes(c, batch->max_new) bytes on the device, 16-byte
+ * aligned, its contents of no matter; no other call may use it until this one is done.
+ * Errors: FM_ERR_INVALID_ARG, FM_ERR_UNSUPPORTED, FM_ERR_CUDA.  A bounded
+ *   device wait that gives up is reported by fm_paged_synchronize.
+ */
+FM_API fm_status fm_paged_attend(fm_paged *c, int32_t layer, const fm_paged_batch *batch, const fm_paged_rows *q,
+                                 const fm_paged_rows *out, float scale, int32_t causal, int32_t window,
+                                 int32_t sinks, void *workspace_dev, int64_t workspace_bytes, void *stream);
+
+/* The workspace of calls with batches of at most max_new new rows a sequence.  Errors: FM_ERR_INVALID_ARG. */
+FM_API fm_status fm_paged_workspace_bytes(const fm_paged *c, int32_t max_new, int64_t *bytes);
+/* The configuration the cache was made with.  Errors: FM_ERR_INVALID_ARG. */
+FM_API fm_status fm_paged_get_config(const fm_paged *c, fm_paged_config *cfg);
+/* Kernel launches issued by this host thread's last write or attend. */
+FM_API fm_status fm_paged_last_launch_count(const fm_paged *c, int32_t *count);
+/* Wait for the stream; FM_ERR_TIMEOUT if a bounded device wait gave up, FM_ERR_INVALID_ARG if a batch's numbers pointed
+   outside, since the last check (cleared; what other streams still run may raise them again). */
+FM_API fm_status fm_paged_synchronize(fm_paged *c, void *stream);
+/* fm_selftest_wait_timeout for a paged cache.  Errors: FM_ERR_INVALID_ARG, FM_ERR_CUDA. */
+FM_API fm_status fm_paged_selftest_wait_timeout(fm_paged *c, int32_t budget_us, void *stream);
+FM_API const char *fm_paged_last_error(const fm_paged *c);   /* never NULL; this host thread's last failed fm_paged call */
+/* Free what the handle owns (not the pool).  NULL is ignored; a capture in progress goes on.  Graphs that hold its calls
+   are not replayed afterwards. */
+FM_API void fm_paged_destroy(fm_paged *c);
+
 #ifdef __cplusplus
 }
 #endif
