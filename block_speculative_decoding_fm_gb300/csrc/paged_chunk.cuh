@@ -6,7 +6,8 @@
 // head of the group): the heads of a group share every key tile, so a tile holds 128 / group whole tokens.
 //   warp 0         the queries of a unit (one box a tile and 64 dims) and the key tiles (a box a page and 64 dims) into a ring
 //   warp 1         the products; an elected lane issues them
-//   warps 2 ..     four a query tile: scores -> weights, the outputs
+//   warps 2, 3     see that masked tiles of V hold finite values only
+//   warps 4 ..     four a query tile, a thread a row: scores -> weights, the outputs
 // Two query tiles (kNT = 2, head dims 64 and 128) share every K and V tile and take turns: while one's scores become
 // weights, the other's products run.  With one tile (kNT = 1: head dim 256, whose outputs fill half of tensor memory, or
 // at most 128 rows a unit) the next key tile's scores are computed ahead into a second buffer instead.
@@ -27,15 +28,18 @@ constexpr int kChunkLeast = 4;     // places a share has at least
 
 template <int HD, int NT>
 struct ChunkCfg {
+  using Walk = PagedWalk<128 * NT, false, kChunkKeys, kChunkCost>;
   static constexpr int kP = HD / 64;                        // panels of 64 dims
-  static constexpr int kKeys = HD == 256 ? 64 : 128;        // keys a ring stage: 16 or 32 KB
-  static constexpr int kSub = kChunkKeys / kKeys;           // stages a tile
-  static constexpr int kStage = kKeys * HD * 2;
-  static constexpr int kPanel = kKeys * 128;
+  static constexpr int kDims = HD < 128 ? HD : 128;         // dims a ring stage: 128 keys, 16 or 32 KB
+  static constexpr int kSub = HD / kDims;                   // stages a tile
+  static constexpr int kStage = kChunkKeys * kDims * 2;
+  static constexpr int kPanel = kChunkKeys * 128;
   static constexpr int kQ = NT * 128 * HD * 2;
   static constexpr int kStages = (HD == 64 ? 10 : 5) + (HD == 128 && NT == 1 ? 1 : 0);
-  static constexpr int kSmem = kQ + kStages * kStage + 16 * kStages + 16 * 8 + 16 * 8 + 8 * 32 + 64;
-  static constexpr int kThreads = 64 + 128 * NT;
+  static constexpr int kThreads = 128 + 128 * NT;
+  static constexpr int kSums = 16;                          // long longs that the plan takes
+  static constexpr int kSmem = kQ + kStages * kStage + 16 * kStages + 128 + 8 * kSums + sizeof(PagedStart) + (4 + 4 * NT) * sizeof(PagedWarp<Walk>);
+  static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
   static constexpr int kO = 256;                            // first column of the outputs (scores: 0 .. 255)
   // place in the ring's order of tile j's K and V, of a segment of n tiles
   __device__ static int kpos(int j, int n) { return NT == 2 ? 2 * j : j == 0 ? 0 : 2 * j - 1; }
@@ -50,14 +54,14 @@ __device__ __forceinline__ void umma_ts_elect16(uint32_t d_tmem, uint32_t a_tmem
       "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
-// operand stored [keys][dims] with dims (N) contiguous: panels of 64 dims `lbo` bytes apart, 8 keys 1024 bytes apart
-__device__ __forceinline__ uint64_t desc_n_sw128(uint32_t saddr, uint32_t lbo) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
+// Shared-memory descriptors of 128-byte-swizzled operands as their low word (the address, and for operands stored [keys]
+// [dims] the distance of panels of 64 dims); the high word (8 rows are 1024 bytes) is a constant, so that a product needs
+// one register of its own an operand: the instruction takes uniform registers, and each value moved there costs it time.
+__device__ __forceinline__ uint32_t lo_k(uint32_t saddr) { return (saddr & 0x3FFFFu) >> 4 | 1u << 16; }
+__device__ __forceinline__ uint32_t lo_n(uint32_t saddr, uint32_t lbo) { return (saddr & 0x3FFFFu) >> 4 | (lbo >> 4) << 16; }
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(d) : "r"(lo), "n"((1024 >> 4) | 1 << 14 | 2 << 29));
   return d;
 }
 // 32 columns of this thread's lane, without waiting for them
@@ -73,17 +77,38 @@ __device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float *f) {
       : "r"(taddr));
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
-__device__ __forceinline__ void tmem_st32_async(uint32_t taddr, const uint32_t *v) {
+__device__ __forceinline__ void tmem_st16_async(uint32_t taddr, const uint32_t *v) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
-      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(taddr),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(taddr),
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
-      "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
-      "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+
+// The bits below bit n.
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
+// Bits 15 and 31 say whether the word's halves are infinite or NaN (an exponent of ones is carried into the sign's place).
+template <bool BF16>
+__device__ __forceinline__ uint32_t above(uint32_t w) { return (w & 0x7fff7fffu) + (BF16 ? 0x00800080u : 0x04000400u); }
+// Four lanes' 16-byte pieces, transposed: lane q had pieces 0 .. 3 of its row, and has piece q of the four lanes' rows.
+__device__ __forceinline__ void transpose4(uint4 (&v)[4], int lane) {
+  auto swap = [&](uint4 &x, uint4 &y, int step, bool upper) {   // y of the lower lane for x of the upper one
+    uint4 s = upper ? x : y, r;
+    r.x = __shfl_xor_sync(0xffffffffu, s.x, step);
+    r.y = __shfl_xor_sync(0xffffffffu, s.y, step);
+    r.z = __shfl_xor_sync(0xffffffffu, s.z, step);
+    r.w = __shfl_xor_sync(0xffffffffu, s.w, step);
+    if (upper)
+      x = r;
+    else
+      y = r;
+  };
+  swap(v[0], v[1], 1, lane & 1);
+  swap(v[2], v[3], 1, lane & 1);
+  swap(v[0], v[2], 2, lane & 2);
+  swap(v[1], v[3], 2, lane & 2);
+}
 
 template <int HD, int NT, bool BF16>
 __global__ void __launch_bounds__(ChunkCfg<HD, NT>::kThreads, 1)
@@ -102,13 +127,15 @@ __global__ void __launch_bounds__(ChunkCfg<HD, NT>::kThreads, 1)
   const uint32_t qfull = b2, qfree = b2 + 8;
   auto sfull = [&](int s) { return b2 + 16 + 8 * s; };     // a score buffer's products are done
   auto pfull = [&](int s) { return b2 + 32 + 8 * s; };     // its weights are stored
-  auto pvdone = [&](int t) { return b2 + 48 + 8 * t; };    // a tile's O += P V is done
+  auto pvdone = [&](int s) { return b2 + 48 + 8 * s; };    // O += P V is done: kNT = 2 a query tile's last, kNT = 1 a buffer's
   const uint32_t drained = b2 + 64, tslot = b2 + 72;
-  const uint32_t vready = b2 + 96;                         // a masked tile's V is there
+  const uint32_t vready = b2 + 96, vclean = b2 + 104;      // a masked tile's V is there, and holds finite values only
   int *poison = reinterpret_cast<int *>(gbase + (b2 - base) + 80);             // [4]: a segment that met a non-finite V
-  long long *sh = reinterpret_cast<long long *>(gbase + (b2 - base) + 128);    // [kThreads / 32 + 1]
-  PagedStart *start = reinterpret_cast<PagedStart *>(sh + 12);
+  long long *sh = reinterpret_cast<long long *>(gbase + (b2 - base) + 128);    // [kSums]
+  PagedStart *start = reinterpret_cast<PagedStart *>(sh + C::kSums);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  PagedWarp<typename C::Walk> &w = reinterpret_cast<PagedWarp<typename C::Walk> *>(start + 1)[warp];
+  const PagedSeg &g = w.g;
   const PagedBatch &b = a.b;
 
   pdl_trigger();
@@ -130,6 +157,7 @@ __global__ void __launch_bounds__(ChunkCfg<HD, NT>::kThreads, 1)
     }
     mbar_init(drained, 1);
     mbar_init(vready, 1);
+    mbar_init(vclean, 64);
     mbar_fence_init();
   }
   if (warp == 1) tmem_alloc<512>(tslot);
@@ -139,30 +167,29 @@ __global__ void __launch_bounds__(ChunkCfg<HD, NT>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = lds32(tslot);
-  PagedWalk<kRows, false, kChunkKeys, kChunkCost> walk;
-  walk.init(*start);
-  PagedSeg g;
+  w.init(*start, b.group, lane);
   const int tt = Tiles::tokens(b.group);
   // query rows of tile t of the segment's unit
   auto rows_of = [&](const PagedSeg &s, int t) {
     return max(0, min(tt, s.q.n_new - (s.tile * NT + t) * tt)) * b.group;
   };
 
+  // registers of a thread: 384 at 168 become 256 at 208 for scores and weights, and 128 at 88
+  if (NT == 2 && warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
   if (warp == 0) {
-    const int box_log = min(b.page_log, 6), boxes = C::kKeys >> box_log;
+    const int box_log = min(b.page_log, 6), boxes = kChunkKeys >> box_log;
     const int box = lane & (boxes - 1), panel = lane / boxes;
-    const bool mine = panel < C::kP;
+    const bool mine = panel < C::kDims / 64;
     uint32_t c = 0, segs = 0;
     bool ok = true;
-    while (ok && walk.next(a, g)) {
+    while (ok && w.next(a, lane)) {
       const int n = g.end - g.begin, nt = NT == 2 && rows_of(g, 1) > 0 ? 2 : 1;
       auto row_of = [&](int u) {   // of the u-th stage of the segment
-        const int e = u / C::kSub, sub = u % C::kSub;
+        const int e = u / C::kSub;
         const int j = NT == 2 ? e >> 1 : e == 0 ? 0 : (e & 1) ? min((e + 1) >> 1, n - 1) : (e - 2) >> 1;
-        return mine ? paged_row(a, g.s, g.seq, g.head, g.s.tile(g.begin + j) * kChunkKeys + sub * C::kKeys + (box << box_log)) : 0;
+        return mine ? paged_row(a, g.s, g.seq, g.head, g.s.tile(g.begin + j) * kChunkKeys + (box << box_log)) : 0;
       };
-      int row = row_of(0);
-      ok = mbar_wait_warp(qfree, (segs & 1) ^ 1, b.err);
+      ok = paged_wait_warp(qfree, (segs & 1) ^ 1, b.err);
       if (!ok) break;
       if (lane == 0) {
         mbar_expect_tx(qfull, nt * C::kP * tt * b.group * 128);
@@ -171,17 +198,18 @@ __global__ void __launch_bounds__(ChunkCfg<HD, NT>::kThreads, 1)
             tma_3d_box(qbuf + (t * C::kP + p) * 16384, &a.tq, p * 64, g.head * b.group, g.q.s0 + (g.tile * NT + t) * tt, qfull);
       }
       ++segs;
+      int row = row_of(0);
       for (int u = 0; u < 2 * n * C::kSub; ++u) {
         const int e = u / C::kSub;
         const bool is_k = NT == 2 ? !(e & 1) : e == 0 || ((e & 1) && e < 2 * n - 1);
-        const int next = u + 1 < 2 * n * C::kSub ? row_of(u + 1) : 0;
-        ok = mbar_wait_warp(empty(c), phase(c) ^ 1, b.err);
+        const int next = (u + 1) % C::kSub ? row : u + 1 < 2 * n * C::kSub ? row_of(u + 1) : 0;
+        ok = paged_wait_warp(empty(c), phase(c) ^ 1, b.err);
         if (!ok) break;
         if (lane == 0) mbar_expect_tx(full(c), C::kStage);
         __syncwarp();
         if (mine)
           tma_2d_row(ring + (c % C::kStages) * C::kStage + panel * C::kPanel + (box << box_log) * 128, is_k ? &a.tk : &a.tv,
-                     panel * 64, row, full(c));
+                     u % C::kSub * C::kDims + panel * 64, row, full(c));
         ++c;
         row = next;
       }
@@ -190,81 +218,98 @@ __global__ void __launch_bounds__(ChunkCfg<HD, NT>::kThreads, 1)
     for (uint32_t u = c > (uint32_t)C::kStages ? c - C::kStages : 0; u < c; ++u) mbar_wait_drain(full(u), phase(u));
     if (segs) mbar_wait_drain(qfull, (segs - 1) & 1);
   } else if (warp == 1) {
-    constexpr uint32_t IS = umma_idesc(128, C::kKeys, BF16);
-    constexpr uint32_t IO = umma_idesc(128, HD, BF16) | (1u << 16);   // V with its dims contiguous
+    // A product takes the tensor pipe 64 cycles and this warp 36 to issue; the pipe holds eight.  A wait costs 90 cycles and a
+    // commit 100 even where nothing is waited for, so there are few: key tiles are waited for while products are queued, and
+    // the ring's stages are given back by the warps that see the scores behind them.  (Two threads that issue, one a query
+    // tile, cost less each, but the tiles then run in step and weights and products take turns: 585 us for 454.)
+    constexpr uint32_t IS = umma_idesc(128, kChunkKeys, BF16);
+    constexpr uint32_t IO = umma_idesc(128, C::kDims, BF16) | (1u << 16);   // V with its dims contiguous
     uint32_t c0 = 0, segs = 0, tiles = 0;      // ring places, segments and (kNT = 1) tiles behind
-    uint32_t np[2] = {0, 0};                   // weights taken from each score buffer
+    uint32_t np[2] = {0, 0}, nv = 0;           // weights taken from each score buffer, masked tiles behind
     bool ok = true;
-    while (ok && walk.next(a, g)) {
-      const int n = g.end - g.begin, nt = NT == 2 && rows_of(g, 1) > 0 ? 2 : 1;
+    while (ok && w.next(a, lane)) {
+      const PagedSpan span = g.s;
+      const int n = g.end - g.begin, begin = g.begin, nt = NT == 2 && rows_of(g, 1) > 0 ? 2 : 1;
+      auto stage = [&](int pos) { return ring + ((c0 + pos) % C::kStages) * C::kStage; };
       auto wait_stage = [&](int pos) {
-        for (int s = 0; ok && s < C::kSub; ++s) {
+#pragma unroll
+        for (int s = 0; s < C::kSub; ++s) {
           const uint32_t c = c0 + pos * C::kSub + s;
-          ok = mbar_wait_warp(full(c), phase(c), b.err);
+          ok = ok && paged_wait_warp(full(c), phase(c), b.err);
         }
-      };
-      auto free_stage = [&](int pos) {
-        for (int s = 0; s < C::kSub; ++s) umma_commit_elect(empty(c0 + pos * C::kSub + s));
       };
       // scores of query tile t against key tile j into buffer s
       auto scores = [&](int t, int j, int s) {
+        const uint32_t d = tmem + 128 * s, q0 = lo_k(qbuf + t * C::kP * 16384);
 #pragma unroll
         for (int sub = 0; sub < C::kSub; ++sub) {
-          const uint32_t kt = ring + ((c0 + C::kpos(j, n) * C::kSub + sub) % C::kStages) * C::kStage;
+          const uint32_t k0 = lo_k(stage(C::kpos(j, n) * C::kSub + sub));
 #pragma unroll
-          for (int kk = 0; kk < HD / 16; ++kk)
-            umma_ss_elect(tmem + 128 * s + C::kKeys * sub, umma_desc_sw128(qbuf + (t * C::kP + (kk >> 2)) * 16384) + 2 * (kk & 3),
-                          umma_desc_sw128(kt + (kk >> 2) * C::kPanel) + 2 * (kk & 3), IS, kk > 0 ? 1u : 0u);
+          for (int kk = 0; kk < C::kDims / 16; ++kk)
+            umma_ss_elect(d, desc_of(q0 + ((sub * (C::kDims / 64) + (kk >> 2)) * 16384 + (kk & 3) * 32) / 16),
+                          desc_of(k0 + ((kk >> 2) * C::kPanel + (kk & 3) * 32) / 16), IS, sub || kk ? 1u : 0u);
         }
         umma_commit_elect(sfull(s));
       };
+      // outputs of query tile t += its weights of tile j, V
       auto product = [&](int t, int j, int s) {
+        const uint32_t d = tmem + C::kO + t * HD, pt = tmem + 128 * s;
 #pragma unroll
-        for (int kk = 0; kk < kChunkKeys / 16; ++kk) {
-          const int sub = kk / (C::kKeys / 16), in = kk % (C::kKeys / 16);
-          const uint32_t vt = ring + ((c0 + C::vpos(j, n) * C::kSub + sub) % C::kStages) * C::kStage;
-          umma_ts_elect16(tmem + C::kO + t * HD, tmem + 128 * s + 8 * kk, desc_n_sw128(vt + in * 2048, C::kPanel), IO,
-                          (j | kk) ? 1u : 0u);
+        for (int sub = 0; sub < C::kSub; ++sub) {
+          const uint32_t v0 = lo_n(stage(C::vpos(j, n) * C::kSub + sub), C::kPanel);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            umma_ts_elect16(d + sub * C::kDims, pt + 8 * kk, desc_of(v0 + kk * 2048 / 16), IO, kk ? 1u : j ? 1u : 0u);
         }
-        umma_commit_elect(pvdone(t));
       };
-      ok = mbar_wait_warp(qfull, segs & 1, b.err);
+      // a masked tile's V, once it is there, is handed to the warps that look it over
+      auto clean = [&](int j) {
+        if (!paged_masked<kChunkKeys>(a, span, span.tile(begin + j) * kChunkKeys)) return;
+        if (ok && lane == 0) mbar_arrive(vready);
+        ok = ok && paged_wait_warp(vclean, nv++ & 1, b.err);
+      };
+      ok = paged_wait_warp(qfull, segs & 1, b.err);
       wait_stage(C::kpos(0, n));
       if (!ok) break;
       tc_fence_after();
       if (NT == 2) {
         for (int t = 0; t < nt; ++t) scores(t, 0, t);
-        free_stage(C::kpos(0, n));
       } else {
-        for (int j = 0; j < 2 && j < n; ++j) {
-          if (j) wait_stage(C::kpos(j, n));
+        scores(0, 0, tiles & 1);
+        if (n > 1) {
+          wait_stage(C::kpos(1, n));
           if (!ok) break;
-          scores(0, j, (tiles + j) & 1);
-          free_stage(C::kpos(j, n));
+          scores(0, 1, (tiles + 1) & 1);
         }
       }
-      if (ok && n <= (NT == 2 ? 1 : 2)) umma_commit_elect(qfree);
       for (int j = 0; ok && j < n; ++j) {
         wait_stage(C::vpos(j, n));
-        if (ok && lane == 0 && paged_masked<kChunkKeys>(a, g.s, g.s.tile(g.begin + j) * kChunkKeys)) mbar_arrive(vready);
-        __syncwarp();
-        for (int t = 0; ok && t < nt; ++t) {
-          const int s = NT == 2 ? t : (tiles + j) & 1;
-          ok = ok && mbar_wait_warp(pfull(s), np[s] & 1, b.err);
-          if (!ok) break;
-          ++np[s];
-          tc_fence_after();
-          product(t, j, s);
-          if (t == nt - 1) free_stage(C::vpos(j, n));
-          const int jn = j + (NT == 2 ? 1 : 2);
-          if (jn < n) {
-            if (t == 0) wait_stage(C::kpos(jn, n));
+        clean(j);
+        if (NT == 2) {
+          if (j + 1 < n) wait_stage(C::kpos(j + 1, n));
+          for (int t = 0; ok && t < nt; ++t) {
+            ok = paged_wait_warp(pfull(t), np[t]++ & 1, b.err);
             if (!ok) break;
-            scores(t, jn, s);
-            if (t == nt - 1) {
-              free_stage(C::kpos(jn, n));
-              if (jn == n - 1) umma_commit_elect(qfree);
-            }
+            tc_fence_after();
+            product(t, j, t);
+            if (j + 1 < n)
+              scores(t, j + 1, t);
+            else
+              umma_commit_elect(pvdone(t));
+          }
+        } else {
+          const int s = (tiles + j) & 1;
+          ok = ok && paged_wait_warp(pfull(s), np[s]++ & 1, b.err);
+          if (!ok) break;
+          tc_fence_after();
+          product(0, j, s);
+          umma_commit_elect(pvdone(s));
+#pragma unroll
+          for (int sub = 0; sub < C::kSub; ++sub) umma_commit_elect(empty(c0 + C::vpos(j, n) * C::kSub + sub));
+          if (j + 2 < n) {                     // (the ring may not hold it before V is free)
+            wait_stage(C::kpos(j + 2, n));
+            if (!ok) break;
+            scores(0, j + 2, s);
           }
         }
       }
@@ -274,59 +319,79 @@ __global__ void __launch_bounds__(ChunkCfg<HD, NT>::kThreads, 1)
     }
     umma_commit_elect(drained);   // every product issued above has completed when this arrives
     mbar_wait_drain(drained, 0);
-  } else {
-    const int t = NT == 2 ? (warp - 2) >> 2 : 0, quad = warp & 3, in = quad * 32 + lane;
-    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
-    const float thr = 8.f / a.scale_log2;
-    uint32_t c0 = 0, segs = 0, tiles = 0;
-    uint32_t ns[2] = {0, 0}, npv = 0, nv = 0;   // scores taken from each buffer, products behind, masked tiles behind
+  } else if (warp < 4) {
+    // Masked tiles of V: infinities and NaN out of them (a weight of 0 times one would be NaN), while the scores become
+    // weights.  (The ring's own barriers cannot be waited on here: they may be a whole turn behind.)
+    uint32_t c0 = 0, segs = 0, nv = 0;
     bool ok = true;
-    int4 desc = make_int4(0, 0, 0, 0);
-    while (walk.next(a, g)) {
+    while (ok && w.next(a, lane)) {
       const int n = g.end - g.begin;
-      const int rows = rows_of(g, t), token = (g.tile * NT + t) * tt + in / b.group;
-      if (g.begin == 0 && !g.whole()) desc = make_int4(g.seq, g.head, g.tile, walk.parts(g));
-      if (rows == 0) {       // (the unit has no second tile)
-        c0 += 2 * n * C::kSub;
-        ++segs;
-        continue;
-      }
-      const bool active = quad * 32 < rows;      // some row of this warp is one
-      const int pos = g.q.len - g.q.n_new + token;
-      const int hi = a.causal ? min(g.q.len, pos + 1) : g.q.len;
-      const int lo = a.window ? pos - a.window + 1 : 0, sink = a.window ? a.sinks : 0;
-      float m = -INFINITY, l = 0.f;
-      for (int j = 0; j < n; ++j) {
-        const int s = NT == 2 ? t : (tiles + j) & 1;
-        const int key0 = g.s.tile(g.begin + j) * kChunkKeys;
-        const bool masked = paged_masked<kChunkKeys>(a, g.s, key0);
-        if (masked && t == 0) {
-          // infinities and NaN of V: out of the tile (a weight of 0 times one would be NaN)
-          // (the ring's own barriers cannot be waited on here: they may be a whole turn behind)
-          bool bad = false;
-          if (ok) ok = mbar_wait_warp(vready, nv & 1, b.err);
-          ++nv;
-          for (int sub = 0; sub < C::kSub; ++sub) {
-            const uint32_t c = c0 + C::vpos(j, n) * C::kSub + sub;
-            const uint32_t vt = ring + (c % C::kStages) * C::kStage;
-            for (int u = in; ok && u < C::kStage / 16; u += 128) {
-              const uint4 x = lds128(vt + u * 16);
-              const uint4 w = make_uint4(not_finite<BF16>(x.x), not_finite<BF16>(x.y), not_finite<BF16>(x.z), not_finite<BF16>(x.w));
-              if (w.x | w.y | w.z | w.w) {
-                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};\n" ::"r"(vt + u * 16), "r"(x.x & ~w.x), "r"(x.y & ~w.y),
-                             "r"(x.z & ~w.z), "r"(x.w & ~w.w)
-                             : "memory");
-                bad = true;
-              }
-            }
+      for (int j = 0; ok && j < n; ++j) {
+        if (!paged_masked<kChunkKeys>(a, g.s, g.s.tile(g.begin + j) * kChunkKeys)) continue;
+        ok = paged_wait_warp(vready, nv++ & 1, b.err);
+        if (!ok) break;
+#pragma unroll
+        for (int sub = 0; sub < C::kSub; ++sub) {
+          const uint32_t vt = ring + ((c0 + C::vpos(j, n) * C::kSub + sub) % C::kStages) * C::kStage + ((warp & 1) * 32 + lane) * 16;
+          uint32_t found = 0;
+#pragma unroll 8
+          for (int u = 0; u < C::kStage; u += 64 * 16) {
+            const uint4 x = lds128(vt + u);
+            found |= above<BF16>(x.x) | above<BF16>(x.y) | above<BF16>(x.z) | above<BF16>(x.w);
           }
-          if (bad) {
+          if (found & 0x80008000u) {
+            for (int u = 0; u < C::kStage; u += 64 * 16) {
+              const uint4 x = lds128(vt + u);
+              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};\n" ::"r"(vt + u), "r"(x.x & ~not_finite<BF16>(x.x)),
+                           "r"(x.y & ~not_finite<BF16>(x.y)), "r"(x.z & ~not_finite<BF16>(x.z)), "r"(x.w & ~not_finite<BF16>(x.w))
+                           : "memory");
+            }
             fence_proxy_async();
             poison[segs & 3] = (int)segs + 1;
           }
         }
-        if (ok) ok = mbar_wait_warp(sfull(s), ns[s] & 1, b.err);
+        mbar_arrive(vclean);
+      }
+      c0 += 2 * n * C::kSub;
+      ++segs;
+    }
+  } else {
+    // ---- four warps a query tile, a thread a row ----
+    if (NT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n");
+    const int t = (warp - 4) >> 2, quad = warp & 3, in = quad * 32 + lane;
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+    const float thr = 8.f / a.scale_log2;       // a row's reference moves where a score beats it by 2^8
+    uint32_t c0 = 0, segs = 0, tiles = 0;
+    uint32_t ns[2] = {0, 0}, npv = 0;           // scores taken from each buffer, products behind
+    bool ok = true;
+    if (threadIdx.x == 128) a.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+    while (w.next(a, lane)) {
+      const int n = g.end - g.begin;
+      const int rows = rows_of(g, t), token = (g.tile * NT + t) * tt + in / b.group;
+      if (threadIdx.x == 128 && g.begin == 0 && !g.whole()) a.desc[blockIdx.x] = make_int4(g.seq, g.head, g.tile, w.walk.parts(g));
+      if (rows == 0) {                          // (the unit has no second tile)
+        c0 += 2 * n * C::kSub;
+        ++segs;
+        continue;
+      }
+      const bool active = quad * 32 < rows;     // some row of this warp is one
+      // the thread that gives the ring's stages back: scores of the last query tile are there when all before them is done
+      const bool frees = quad == 0 && lane == 0 && (NT == 1 || t == 1 || rows_of(g, 1) == 0);
+      const int pos = g.q.len - g.q.n_new + token;
+      float m = -INFINITY;
+      uint64_t sum[2] = {0, 0};                 // of weights: two packed pairs
+      for (int j = 0; j < n; ++j) {
+        const int s = NT == 2 ? t : (tiles + j) & 1;
+        const int key0 = g.s.tile(g.begin + j) * kChunkKeys;
+        const bool masked = paged_masked<kChunkKeys>(a, g.s, key0);
+        if (ok) ok = paged_wait_warp(sfull(s), ns[s] & 1, b.err);
         ++ns[s];
+        if (frees && ok) {
+          if (NT == 2 && j > 0) mbar_arrive(empty(c0 + C::vpos(j - 1, n)));
+#pragma unroll
+          for (int sub = 0; sub < C::kSub; ++sub) mbar_arrive(empty(c0 + C::kpos(j, n) * C::kSub + sub));
+          if (j == n - 1) mbar_arrive(qfree);
+        }
         if (ok && active) {
           tc_fence_after();
           float x[128];
@@ -334,24 +399,38 @@ __global__ void __launch_bounds__(ChunkCfg<HD, NT>::kThreads, 1)
           for (int q = 0; q < 4; ++q) tmem_ld32_async(lanes + 128 * s + 32 * q, x + 32 * q);
           tmem_wait_ld();
           if (masked) {
+            // a bit a key: ahead of the end, and inside the window or among the first
+            const int hi = a.causal ? min(g.q.len, pos + 1) : g.q.len, lo = a.window ? pos - a.window + 1 : 0;
 #pragma unroll
-            for (int e = 0; e < 128; ++e) {
-              const int key = key0 + e;
-              if (!(key < hi && (key >= lo || key < sink))) x[e] = -INFINITY;
+            for (int q = 0; q < 4; ++q) {
+              const int k = key0 + 32 * q;
+              const uint32_t see = below(hi - k) & (~below(lo - k) | below((a.window ? a.sinks : 0) - k));
+              if (__any_sync(0xffffffffu, see != 0xffffffffu)) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) x[32 * q + e] = see & (1u << e) ? x[32 * q + e] : -INFINITY;
+              }
             }
           }
-          float top = x[0];
+          float tops[4];
 #pragma unroll
-          for (int e = 1; e < 128; ++e) top = fmaxf(top, x[e]);
+          for (int q = 0; q < 4; ++q) {
+            tops[q] = x[q];
+#pragma unroll
+            for (int e = 4 + q; e < 128; e += 8) tops[q] = fmaxf(fmaxf(tops[q], x[e]), e + 4 < 128 ? x[e + 4] : x[e]);
+          }
+          const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
           const bool move = top > m + thr;
           if (__any_sync(0xffffffffu, move)) {
             const float f = move ? ex2((m - top) * a.scale_log2) : 1.f;
             if (move) m = top;
-            l *= f;
+            const uint64_t f2 = f2_make(f, f);
+            sum[0] = f2_fma(sum[0], f2, 0);
+            sum[1] = f2_fma(sum[1], f2, 0);
             if (j > 0) {
-              if (NT == 1) ok = mbar_wait_warp(pvdone(0), (npv + j - 1) & 1, b.err);
+              if (NT == 1) ok = paged_wait_warp(pvdone(s ^ 1), (ns[s ^ 1] - 1) & 1, b.err);   // (the last tile's product)
               if (ok) {
-#pragma unroll
+                tc_fence_after();
+#pragma unroll 1
                 for (int q = 0; q < HD / 32; ++q) {
                   float o[32];
                   tmem_ld32(lanes + C::kO + t * HD + 32 * q, o);
@@ -362,60 +441,84 @@ __global__ void __launch_bounds__(ChunkCfg<HD, NT>::kThreads, 1)
               }
             }
           }
-          const float off = m == -INFINITY ? 0.f : m * a.scale_log2;
-          uint32_t w[64];
+          const float off = m == -INFINITY ? 0.f : -m * a.scale_log2;
+          const uint64_t scale2 = f2_make(a.scale_log2, a.scale_log2), off2 = f2_make(off, off);
 #pragma unroll
-          for (int e = 0; e < 64; ++e) {
-            const float p0 = ex2(fmaf(x[2 * e], a.scale_log2, -off)), p1 = ex2(fmaf(x[2 * e + 1], a.scale_log2, -off));
-            l += p0 + p1;
-            w[e] = pack2<BF16>(p0, p1);
+          for (int q = 0; q < 4; ++q) {
+            uint32_t p[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float p0, p1;
+              f2_get(f2_fma(f2_make(x[32 * q + 2 * e], x[32 * q + 2 * e + 1]), scale2, off2), p0, p1);
+              p0 = ex2(p0);
+              p1 = ex2(p1);
+              sum[e & 1] = f2_add(sum[e & 1], f2_make(p0, p1));
+              p[e] = pack2<BF16>(p0, p1);
+            }
+            tmem_st16_async(lanes + 128 * s + 16 * q, p);
           }
-          tmem_st32_async(lanes + 128 * s, w);
-          tmem_st32_async(lanes + 128 * s + 32, w + 32);
           tmem_wait_st();
           tc_fence_before();
         }
-        // With one tile the scores run a tile ahead of the products: the last product but one is waited for here, ahead of
-        // this warp's arrival, since its phase cannot be told from the next but one once the last product is done.
-        if (NT == 1 && j > 0 && j == n - 1 && ok) ok = mbar_wait_warp(pvdone(0), (npv + j - 1) & 1, b.err);
         mbar_arrive(pfull(s));
       }
       // ---- the outputs ----
-      if (ok) ok = mbar_wait_warp(pvdone(t), (npv + n - 1) & 1, b.err);
-      npv += n;
+      float l, l2;
+      f2_get(f2_add(sum[0], sum[1]), l, l2);
+      l += l2;
+      const int last = NT == 2 ? t : (tiles + n - 1) & 1;
+      if (ok) ok = paged_wait_warp(pvdone(last), (NT == 2 ? npv++ : ns[last] - 1) & 1, b.err);
+      if (NT == 2 && frees && ok) mbar_arrive(empty(c0 + C::vpos(n - 1, n)));
       tc_fence_after();
       if (ok && active) {
         const bool valid = in < rows, whole = g.whole();
         const bool bad = reinterpret_cast<volatile int *>(poison)[segs & 3] == (int)segs + 1;
         const size_t slot = 2 * (size_t)blockIdx.x + (g.begin == 0 ? 1 : 0);
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        uint16_t *out = static_cast<uint16_t *>(a.out.p) + (int64_t)(g.q.s0 + token) * a.out.ld +
-                        (int64_t)(g.head * b.group + in % b.group) * a.out.hs;
-        float *po = a.part_o + (slot * kRows + 128 * t + in) * HD;
-        if (valid && !whole) a.part_ml[slot * kRows + 128 * t + in] = make_float2(m == -INFINITY ? m : m * a.scale_log2, l);
+        // a quad of lanes writes 64 bytes of its four rows, one after another
+        int64_t at[4];
+        bool there[4];
 #pragma unroll
-        for (int q = 0; q < HD / 32; ++q) {
+        for (int i = 0; i < 4; ++i) {
+          const int r = (in & ~3) + i, tk = r / b.group;
+          there[i] = r < rows;
+          at[i] = (int64_t)(g.q.s0 + (g.tile * NT + t) * tt + tk) * a.out.ld + (int64_t)(g.head * b.group + r - tk * b.group) * a.out.hs +
+                  8 * (lane & 3);
+        }
+        uint16_t *out = static_cast<uint16_t *>(a.out.p);
+        if (valid && !whole)
+          a.part_ml[slot * kRows + 128 * t + in] = make_float2(m == -INFINITY ? m : m * a.scale_log2, l);
+#pragma unroll 1
+        for (int c = 0; c < HD; c += 32) {
           float o[32];
-          tmem_ld32(lanes + C::kO + t * HD + 32 * q, o);
-          if (valid && bad) {
-            const PagedSeg held = g;
-            for (int e = 0; e < 32; ++e) {
-              const float x = paged_poison<kChunkKeys, BF16>(a, held, HD, pos, 32 * q + e);
+          tmem_ld32(lanes + C::kO + t * HD + c, o);
+          if (bad) {
+            if (valid) {
+              const PagedSeg held = g;
+              for (int e = 0; e < 32; ++e) {
+                const float x = paged_poison<kChunkKeys, BF16>(a, held, HD, pos, c + e);
 #pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (k == e) o[k] += x;
+                for (int k = 0; k < 32; ++k)
+                  if (k == e) o[k] += x;
+              }
             }
+            __syncwarp();
           }
-          if (valid && whole) {
+          if (whole) {
+            uint4 v[4];
 #pragma unroll
-            for (int e = 0; e < 32; e += 8)
-              *reinterpret_cast<uint4 *>(out + 32 * q + e) =
-                  make_uint4(pack2<BF16>(o[e] * inv, o[e + 1] * inv), pack2<BF16>(o[e + 2] * inv, o[e + 3] * inv),
-                             pack2<BF16>(o[e + 4] * inv, o[e + 5] * inv), pack2<BF16>(o[e + 6] * inv, o[e + 7] * inv));
+            for (int i = 0; i < 4; ++i)
+              v[i] = make_uint4(pack2<BF16>(o[8 * i] * inv, o[8 * i + 1] * inv), pack2<BF16>(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                                pack2<BF16>(o[8 * i + 4] * inv, o[8 * i + 5] * inv), pack2<BF16>(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+            transpose4(v, lane);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (there[i]) *reinterpret_cast<uint4 *>(out + at[i] + c) = v[i];
           } else if (valid) {
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<float4 *>(po + 32 * q + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+              *reinterpret_cast<float4 *>(paged_part<HD, kRows>(a, slot, 128 * t + in, c + e)) =
+                  make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
           }
           __syncwarp();
         }
@@ -425,7 +528,6 @@ __global__ void __launch_bounds__(ChunkCfg<HD, NT>::kThreads, 1)
       tiles += n;
       ++segs;
     }
-    if (threadIdx.x == 64) a.desc[blockIdx.x] = desc;
   }
   tc_fence_before();
   __syncthreads();

@@ -33,6 +33,59 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
   return y;
 }
+// A bounded wait as mbar_wait_bounded, without a time hint: a thread wakes 30 cycles sooner (82 after the arrival, where the
+// hinted form takes 112), which counts where products and weights hand over to each other every 1,000 cycles.
+__device__ __forceinline__ bool paged_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool paged_wait_long(uint32_t bar, uint32_t parity, int32_t *err) {
+  const long long t0 = clock64();
+  long long next = t0 + 8192;
+  while (!paged_try(bar, parity)) {
+    const long long t = clock64();
+    if (t > next) {
+      if (*reinterpret_cast<volatile int32_t *>(err)) return false;
+      if (t - t0 > kWaitBudgetCycles) {
+        atomicExch(err, 1);
+        return false;
+      }
+      next = t + 8192;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool paged_wait(uint32_t bar, uint32_t parity, int32_t *err) {
+  if (paged_try(bar, parity)) return true;
+  return paged_wait_long(bar, parity, err);
+}
+__device__ __forceinline__ bool paged_wait_warp(uint32_t bar, uint32_t parity, int32_t *err) {
+  const bool ok = paged_wait(bar, parity, err);
+  return __all_sync(0xffffffffu, ok);
+}
+
+// Two f32 values in one 64-bit register: packed arithmetic at two results an instruction.
+__device__ __forceinline__ uint64_t f2_make(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void f2_get(uint64_t v, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;\n" : "=f"(lo), "=f"(hi) : "l"(v)); }
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   if constexpr (BF16) {
@@ -145,6 +198,7 @@ struct PagedSeg {
 struct PagedStart {       // where a CTA's share begins
   long long left;         // places of its share
   long long share;
+  PagedSeq q;
   int seq, head, tile, off;
 };
 
@@ -157,9 +211,11 @@ struct PagedWalk {
   PagedSeq q;
   bool loaded;
 
-  __device__ __forceinline__ void init(const PagedStart &p) {
+  __device__ __forceinline__ void init(const PagedStart &p, int group) {
     left = p.left, share = p.share, seq = p.seq, head = p.head, tile = p.tile, off = p.off;
-    loaded = false;
+    q = p.q;
+    tiles = left > 0 ? Tiles::count(q, group) : 0;
+    loaded = true;
   }
   // The CTAs that the unit of a segment with begin == 0 is cut into: this share ended with the segment, the rest of the
   // unit fills the shares behind it.
@@ -205,8 +261,27 @@ struct PagedWalk {
   }
 };
 
-// Adds up the launch's places and finds where this CTA's share begins.  Every thread of the CTA calls it; sh: kThreads
-// long longs and a PagedStart in shared memory.  Shares are at least kLeast places.
+// A warp's walk and present segment, in shared memory: the tile loops need the registers.
+template <class Walk>
+struct PagedWarp {
+  Walk walk;
+  PagedSeg g;
+  int more;
+  __device__ __forceinline__ void init(const PagedStart &p, int group, int lane) {
+    if (lane == 0) walk.init(p, group);
+  }
+  __device__ __forceinline__ bool next(const PagedAttnArgs &a, int lane) {
+    __syncwarp();
+    int more = 0;
+    if (lane == 0) more = walk.next(a, g);
+    more = __shfl_sync(0xffffffffu, more, 0);
+    __syncwarp();
+    return more != 0;
+  }
+};
+
+// Adds up the launch's places and finds where this CTA's share begins.  Every thread of the CTA calls it; sh: a
+// long long a warp, and the start, in shared memory.  Shares are at least kLeast places.
 template <int kRows, bool kFlat, int kTile, int kCost, int kLeast, int kThreads>
 __device__ __forceinline__ void paged_plan(const PagedAttnArgs &a, long long *sh, PagedStart *out) {
   using Tiles = PagedTiles<kRows, kFlat>;
@@ -217,8 +292,8 @@ __device__ __forceinline__ void paged_plan(const PagedAttnArgs &a, long long *sh
   auto one = [&](const PagedSeq &q, int i) -> int {
     return paged_span<kTile>(a, q, Tiles::first(i, b.group), Tiles::last(q, i, b.group)).n + kCost;
   };
-  auto cost = [&](int i) -> long long {
-    PagedSeq q = {0, 0, 0};
+  auto cost = [&](int i, PagedSeq &q) -> long long {
+    q = {0, 0, 0};
     if (i < b.n_seqs) q = paged_seq(b, i);
     const int nt = Tiles::count(q, b.group);
     long long c = 0;
@@ -239,42 +314,36 @@ __device__ __forceinline__ void paged_plan(const PagedAttnArgs &a, long long *sh
     }
     return c;
   };
-  // sums of the threads' places over the whole launch; with one round of sequences the threads keep their own
-  long long mine = 0, all = 0;
+  // Sums of the threads' places, in the order of the sequences.  One round of kThreads sequences: its scan gives the sum as
+  // well; more: a first walk for the sum, a second that stops at the share's sequence.
   const int rounds = (b.n_seqs + kThreads - 1) / kThreads;
-  for (int r = 0; r < rounds; ++r) {
-    mine = cost(r * kThreads + t) * b.n_kv;
-    all += mine;
+  PagedSeq q;
+  long long mine = 0, all = 0;
+  if (rounds > 1) {
+    for (int r = 0; r < rounds; ++r) all += cost(r * kThreads + t, q);
+    all *= b.n_kv;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+    if (lane == 0) sh[warp] = all;
+    __syncthreads();
+    all = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) all += sh[w];
+    __syncthreads();
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-  if (lane == 0) sh[warp] = all;
-  __syncthreads();
-  all = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) all += sh[w];
-  long long share = (all + gridDim.x - 1) / gridDim.x;
-  if (share < kLeast) share = kLeast;
-  const long long from = share * blockIdx.x;
   if (t == 0) {
-    out->share = share;
-    out->left = from < all ? min(share, all - from) : 0;
+    out->left = 0;
     out->seq = b.n_seqs;
-    out->head = out->tile = out->off = 0;
   }
-  __syncthreads();
-  if (from >= all) return;
-  // the sequence that holds place `from`
-  long long before = 0;
+  long long before = 0, share = 0, from = 0;
   for (int r = 0; r < rounds; ++r) {
-    if (rounds > 1) mine = cost(r * kThreads + t) * b.n_kv;
+    mine = cost(r * kThreads + t, q) * b.n_kv;
     long long x = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long y = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += y;
     }
-    __syncthreads();
     if (lane == 31) sh[warp] = x;
     __syncthreads();
     long long lower = before;
@@ -283,45 +352,50 @@ __device__ __forceinline__ void paged_plan(const PagedAttnArgs &a, long long *sh
       if (w < warp) lower += sh[w];
       before += sh[w];
     }
-    const long long end = lower + x, begin = end - mine;
-    if (mine > 0 && from >= begin && from < end) {
-      sh[kWarps] = from - begin;
-      out->seq = r * kThreads + t;
+    if (rounds == 1) all = before;
+    if (r == 0) {
+      share = (all >> 31) ? (all + gridDim.x - 1) / gridDim.x : (long long)(((uint32_t)all + gridDim.x - 1) / gridDim.x);
+      if (share < kLeast) share = kLeast;
+      from = share * blockIdx.x;
     }
+    const long long end = lower + x, begin = end - mine;
+    const uint32_t holds = __ballot_sync(0xffffffffu, from >= begin && from < end);
+    if (holds) {   // this warp has the sequence that holds place `from`: the KV head and the tile in it
+      const int src = __ffs(holds) - 1;
+      PagedSeq h;
+      h.s0 = __shfl_sync(0xffffffffu, q.s0, src);
+      h.n_new = __shfl_sync(0xffffffffu, q.n_new, src);
+      h.len = __shfl_sync(0xffffffffu, q.len, src);
+      const long long rest = __shfl_sync(0xffffffffu, from - begin, src), of = __shfl_sync(0xffffffffu, mine, src) / b.n_kv;
+      const int head = (rest >> 31) || (of >> 31) ? (int)(rest / of) : (int)((uint32_t)rest / (uint32_t)of);
+      const int nt = Tiles::count(h, b.group);
+      long long in = rest - head * of;
+      for (int j0 = 0; j0 < nt; j0 += 32) {
+        const int j = j0 + lane;
+        const int c = j < nt ? one(h, j) : 0;
+        long long e = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long y = __shfl_up_sync(0xffffffffu, e, o);
+          if (lane >= o) e += y;
+        }
+        if (c > 0 && in >= e - c && in < e) {
+          out->share = share;
+          out->left = min(share, all - from);
+          out->q = h;
+          out->seq = r * kThreads + (warp << 5) + src;
+          out->head = head;
+          out->tile = j;
+          out->off = (int)(in - (e - c));
+        }
+        const long long sum = __shfl_sync(0xffffffffu, e, 31);
+        if (in < sum) break;
+        in -= sum;
+      }
+    }
+    __syncthreads();
     if (before > from) break;   // (the same for every thread)
   }
-  __syncthreads();
-  // the KV head and the tile in it
-  if (warp == 0) {
-    const PagedSeq q = paged_seq(b, out->seq);
-    const int nt = Tiles::count(q, b.group);
-    long long x = 0;
-    for (int j = lane; j < nt; j += 32) x += one(q, j);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    const long long rest = sh[kWarps];
-    const int head = (int)(rest / x);
-    long long in = rest - head * x;
-    for (int j0 = 0; j0 < nt; j0 += 32) {
-      const int j = j0 + lane;
-      const long long c = j < nt ? one(q, j) : 0;
-      long long e = c;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, e, o);
-        if (lane >= o) e += y;
-      }
-      if (c > 0 && in >= e - c && in < e) {
-        out->head = head;
-        out->tile = j;
-        out->off = (int)(in - (e - c));
-      }
-      const long long sum = __shfl_sync(0xffffffffu, e, 31);
-      if (in < sum) break;
-      in -= sum;
-    }
-  }
-  __syncthreads();
 }
 
 // The sum over the infinite and NaN values of V, column d, in masked tiles of the segment, that the token at `pos` sees
@@ -345,6 +419,13 @@ __device__ __noinline__ float paged_poison(const PagedAttnArgs &a, const PagedSe
     }
   }
   return sum;
+}
+
+// Where column d of a row of a part lies: 8 columns of every row together, so that threads a row each write next to
+// one another.
+template <int HD, int kRows>
+__device__ __forceinline__ float *paged_part(const PagedAttnArgs &a, size_t slot, int row, int d) {
+  return a.part_o + ((slot * (HD / 8) + (d >> 3)) * kRows + row) * 8 + (d & 7);
 }
 
 // Joins the parts of the units that were cut.  Block (i, y): the unit that CTA i began; a warp takes a row at a time, or
@@ -411,7 +492,7 @@ __global__ void __launch_bounds__(512) fm_paged_join_kernel(const __grid_constan
 #pragma unroll
             for (int v = 0; v < kVec; ++v)
               if (4 * lane + 128 * v < HD)
-                x[u][v] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + (slot(p) * kRows + row) * HD) + lane + 32 * v);
+                x[u][v] = __ldcg(reinterpret_cast<const float4 *>(paged_part<HD, kRows>(a, slot(p), row, 4 * lane + 128 * v)));
           }
         }
 #pragma unroll

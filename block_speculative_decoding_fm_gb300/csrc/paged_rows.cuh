@@ -40,11 +40,12 @@ constexpr int kRowsThreads = 160;
 
 template <int HD>
 struct RowsCfg {
+  using Walk = PagedWalk<kRowsUnit, true, kRowsKeys, kRowsCost>;
   static constexpr int kStage = 2 * kRowsKeys * HD * 2;                   // K then V, panels of 64 dims
   static constexpr int kStages = HD == 64 ? 4 : 3;
   static constexpr int kCtas = HD == 64 ? 3 : HD == 128 ? 2 : 1;          // an SM holds
   static constexpr int kMerge = 2 * kRowsUnit * HD * 4;
-  static constexpr int kSmem = kStages * kStage + kMerge + 4 * kRowsUnit * 8 + 16 * kStages + 64 + 8 * 32;
+  static constexpr int kSmem = kStages * kStage + kMerge + 4 * kRowsUnit * 8 + 16 * kStages + 64 + sizeof(PagedStart) + 16 + 5 * sizeof(PagedWarp<Walk>);
 };
 
 template <int HD, bool BF16>
@@ -64,6 +65,8 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<HD>::kCtas)
   PagedStart *start = reinterpret_cast<PagedStart *>(sh + 8);
   int *poison = reinterpret_cast<int *>(start + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  PagedWarp<typename C::Walk> &w = reinterpret_cast<PagedWarp<typename C::Walk> *>(poison + 4)[warp];
+  const PagedSeg &g = w.g;
   const PagedBatch &b = a.b;
 
   pdl_trigger();
@@ -79,9 +82,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<HD>::kCtas)
   }
   pdl_wait();
   paged_plan<kRowsUnit, true, kRowsKeys, kRowsCost, kRowsLeast, kRowsThreads>(a, sh, start);
-  PagedWalk<kRowsUnit, true, kRowsKeys, kRowsCost> walk;
-  walk.init(*start);
-  PagedSeg g;
+  w.init(*start, b.group, lane);
 
   if (warp == 4) {
     // ---- fetch: a lane a (page box, panel) ----
@@ -90,7 +91,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<HD>::kCtas)
     const bool mine = panel < kP;
     uint32_t c = 0;                               // stages asked for
     bool ok = true;
-    while (ok && walk.next(a, g)) {
+    while (ok && w.next(a, lane)) {
       auto row_of = [&](int i) { return mine ? paged_row(a, g.s, g.seq, g.head, g.s.tile(i) * kRowsKeys + (box << box_log)) : 0; };
       int row = row_of(g.begin);
       for (int i = g.begin; i < g.end; ++i) {
@@ -123,8 +124,8 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<HD>::kCtas)
   const int vrow = 16 * warp + (lane & 15), vun = lane >> 4;                            // V transposed
   uint32_t c = 0;
   bool ok = true;
-  int4 desc = make_int4(0, 0, 0, 0);
-  while (walk.next(a, g)) {
+  if (threadIdx.x == 0) a.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+  while (w.next(a, lane)) {
     const int r0 = g.tile * kRowsUnit, rows = min(kRowsUnit, g.q.n_new * b.group - r0);
     const int pos0 = g.q.len - g.q.n_new;
     int tok[2];
@@ -261,7 +262,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<HD>::kCtas)
     named_sync(1, 128);
     const bool whole = g.whole();
     const size_t slot = 2 * (size_t)blockIdx.x + (g.begin == 0 ? 1 : 0);
-    if (!whole && g.begin == 0) desc = make_int4(g.seq, g.head, g.tile, walk.parts(g));
+    if (threadIdx.x == 0 && !whole && g.begin == 0) a.desc[blockIdx.x] = make_int4(g.seq, g.head, g.tile, w.walk.parts(g));
     for (int u = threadIdx.x; u < kRowsUnit * HD / 8; u += 128) {
       const int row = u / (HD / 8), d = (u % (HD / 8)) * 8;
       if (row >= rows) break;
@@ -296,7 +297,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<HD>::kCtas)
             make_uint4(pack2<BF16>(v[0] * inv, v[1] * inv), pack2<BF16>(v[2] * inv, v[3] * inv),
                        pack2<BF16>(v[4] * inv, v[5] * inv), pack2<BF16>(v[6] * inv, v[7] * inv));
       } else {
-        float4 *po = reinterpret_cast<float4 *>(a.part_o + (slot * kRowsUnit + row) * HD + d);
+        float4 *po = reinterpret_cast<float4 *>(paged_part<HD, kRowsUnit>(a, slot, row, d));
         po[0] = make_float4(v[0], v[1], v[2], v[3]);
         po[1] = make_float4(v[4], v[5], v[6], v[7]);
         if (d == 0) a.part_ml[slot * kRowsUnit + row] = make_float2(mt == -INFINITY ? mt : mt * a.scale_log2, lt);
@@ -308,7 +309,6 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<HD>::kCtas)
       named_sync(1, 128);
     }
   }
-  if (threadIdx.x == 0) a.desc[blockIdx.x] = desc;
 }
 
 }  // namespace fm
