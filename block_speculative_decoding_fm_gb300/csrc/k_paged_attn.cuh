@@ -22,8 +22,8 @@ cudaError_t allow_smem(K kern, int bytes, std::atomic<uint64_t> &done) {
   return e;
 }
 
-template <typename K>
-cudaError_t launch_pdl(K kern, dim3 grid, int threads, int smem, cudaStream_t s, const PagedAttnArgs &a) {
+template <typename K, typename... More>
+cudaError_t launch_pdl(K kern, dim3 grid, int threads, int smem, cudaStream_t s, const PagedAttnArgs &a, More... more) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = threads;
@@ -34,7 +34,7 @@ cudaError_t launch_pdl(K kern, dim3 grid, int threads, int smem, cudaStream_t s,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, a);
+  return cudaLaunchKernelEx(&cfg, kern, a, more...);
 }
 
 template <int HD, bool BF16>
@@ -43,7 +43,7 @@ cudaError_t rows_call(const PagedAttnArgs &a, int n_sm, cudaStream_t s) {
   cudaError_t e = allow_smem(fm_paged_rows_kernel<HD, BF16>, RowsCfg<HD>::kSmem, done);
   const int ctas = n_sm * RowsCfg<HD>::kCtas;
   if (e == cudaSuccess) e = launch_pdl(fm_paged_rows_kernel<HD, BF16>, dim3(ctas), kRowsThreads, RowsCfg<HD>::kSmem, s, a);
-  if (e == cudaSuccess) e = launch_pdl(fm_paged_join_kernel<HD, kRowsUnit, true, BF16, 4>, dim3(ctas, 4), 512, 0, s, a);
+  if (e == cudaSuccess) e = launch_pdl(fm_paged_join_kernel<HD, kRowsUnit, true, BF16, 4>, dim3(n_sm, HD / 64, 1), kJoinThreads, 0, s, a, ctas);
   return e;
 }
 
@@ -53,7 +53,7 @@ cudaError_t chunk_call(const PagedAttnArgs &a, int n_sm, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_smem(fm_paged_chunk_kernel<HD, NT, BF16>, C::kSmem, done);
   if (e == cudaSuccess) e = launch_pdl(fm_paged_chunk_kernel<HD, NT, BF16>, dim3(n_sm), C::kThreads, C::kSmem, s, a);
-  if (e == cudaSuccess) e = launch_pdl(fm_paged_join_kernel<HD, 128 * NT, false, BF16, 1>, dim3(n_sm, 8 * NT), 512, 0, s, a);
+  if (e == cudaSuccess) e = launch_pdl(fm_paged_join_kernel<HD, 128 * NT, false, BF16, 1>, dim3(n_sm, HD / 64, NT), kJoinThreads, 0, s, a, n_sm);
   return e;
 }
 

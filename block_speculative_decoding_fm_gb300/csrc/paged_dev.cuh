@@ -428,115 +428,114 @@ __device__ __forceinline__ float *paged_part(const PagedAttnArgs &a, size_t slot
   return a.part_o + ((slot * (HD / 8) + (d >> 3)) * kRows + row) * 8 + (d & 7);
 }
 
-// Joins the parts of the units that were cut.  Block (i, y): the unit that CTA i began; a warp takes a row at a time, or
-// a share of the row's parts where kSplit > 1 warps work on one row.
+// Joins the parts of the units that were cut.  Blocks take the CTAs' cut units in turn (x), 64 columns each (y), and rows in
+// steps; a thread takes 8 columns of a row, kSplit threads share a row's parts.  Parts lie so that neighbouring threads,
+// neighbouring rows, read on from each other.  (One block a unit and warp a row read as well, but the blocks of calls that cut
+// little took 4 us to come and go.)
+constexpr int kJoinThreads = 512;
 template <int HD, int kRows, bool kFlat, bool BF16, int kSplit>
-__global__ void __launch_bounds__(512) fm_paged_join_kernel(const __grid_constant__ PagedAttnArgs a) {
+__global__ void __launch_bounds__(kJoinThreads) fm_paged_join_kernel(const __grid_constant__ PagedAttnArgs a, int ctas) {
   using Tiles = PagedTiles<kRows, kFlat>;
-  __shared__ float4 acc[kSplit > 1 ? 16 : 1][kSplit > 1 ? HD / 4 : 1];
+  constexpr int kStep = kJoinThreads / (8 * kSplit);      // rows at a time
+  static_assert(kStep <= kRows, "rows of a step");
+  __shared__ float acc[kSplit > 1 ? kSplit - 1 : 1][kSplit > 1 ? kStep * 8 : 1][9];
   pdl_trigger();
   pdl_wait();
-  const int4 d = __ldcg(a.desc + blockIdx.x);
-  if (d.w == 0) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const PagedSeq q = paged_seq(a.b, d.x);
-  const int group = a.b.group, cta = blockIdx.x;
-  constexpr int kWarpRows = 16 / kSplit;      // rows a round of the block
-  constexpr int kVec = HD / 128 > 0 ? HD / 128 : 1;   // float4 a lane
-  for (int r0 = blockIdx.y * kWarpRows; r0 < kRows; r0 += gridDim.y * kWarpRows) {
-    const int row = r0 + warp / kSplit, sub = warp % kSplit;
-    int token, head;
-    bool valid;
-    if (kFlat) {
-      const int r = d.z * kRows + row;
-      token = r / group;
-      head = r - token * group;
-      valid = r < q.n_new * group;
-    } else {
-      const int tt = Tiles::tokens(group), in = row & 127;
-      token = (d.z * Tiles::kSub + (row >> 7)) * tt + in / group;
-      head = in % group;
-      valid = in < tt * group && token < q.n_new;
-    }
+  const int group = a.b.group, zs = gridDim.z;
+  const int r = threadIdx.x % kStep, c = threadIdx.x / kStep % 8, sub = threadIdx.x / (kStep * 8);
+  for (int cta = blockIdx.x; cta < ctas; cta += gridDim.x) {
+    const int4 d = __ldcg(a.desc + cta);
+    if (d.w == 0) continue;
+    const PagedSeq q = paged_seq(a.b, d.x);
     auto slot = [&](int p) -> size_t { return p == 0 ? 2 * (size_t)cta + 1 : 2 * (size_t)(cta + p); };
-    float top = -INFINITY;
-    if (valid)
-      for (int p = lane; p < d.w; p += 32) top = fmaxf(top, __ldcg(a.part_ml + slot(p) * kRows + row).x);
-    top = warp_max(top);
-    float l = 0.f;
-    float4 o[kVec];
-#pragma unroll
-    for (int v = 0; v < kVec; ++v) o[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (valid && !(top == -INFINITY)) {
-      // sums of weights: every warp of the row adds all of them, in order
-      for (int p0 = 0; p0 < d.w; p0 += 32) {
-        const int p = p0 + lane;
-        float w = 0.f;
-        if (p < d.w) {
-          const float2 ml = __ldcg(a.part_ml + slot(p) * kRows + row);
-          w = ml.x == -INFINITY ? 0.f : ex2(ml.x - top) * ml.y;
-        }
-        l += warp_sum(w);
+    for (int r0 = blockIdx.z * kStep; r0 < kRows; r0 += zs * kStep) {
+      const int row = r0 + r;
+      int token, head;
+      bool valid;
+      if (kFlat) {
+        const int f = d.z * kRows + row;
+        token = f / group;
+        head = f - token * group;
+        valid = f < q.n_new * group;
+      } else {
+        const int tt = Tiles::tokens(group), in = row & 127;
+        token = (d.z * Tiles::kSub + (row >> 7)) * tt + in / group;
+        head = in % group;
+        valid = in < tt * group && token < q.n_new;
       }
-      constexpr int kAhead = kVec == 2 ? 4 : 8;
-      for (int p0 = sub; p0 < d.w; p0 += kSplit * kAhead) {
-        float4 x[kAhead][kVec];
-        float w[kAhead];
+      // one pass with the running maximum, kAhead parts in flight
+      constexpr int kAhead = 4;
+      float top = -INFINITY, l = 0.f, o[8];
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-          const int p = p0 + u * kSplit;
-          w[u] = 0.f;
-          if (p < d.w) {
-            const float m = __ldcg(a.part_ml + slot(p) * kRows + row).x;
-            w[u] = m == -INFINITY ? 0.f : ex2(m - top);
+      for (int e = 0; e < 8; ++e) o[e] = 0.f;
+      if (valid)
+        for (int p0 = sub; p0 < d.w; p0 += kSplit * kAhead) {
+          float2 ml[kAhead];
+          float4 x[kAhead][2];
 #pragma unroll
-            for (int v = 0; v < kVec; ++v)
-              if (4 * lane + 128 * v < HD)
-                x[u][v] = __ldcg(reinterpret_cast<const float4 *>(paged_part<HD, kRows>(a, slot(p), row, 4 * lane + 128 * v)));
+          for (int u = 0; u < kAhead; ++u) {
+            const int p = p0 + u * kSplit;
+            ml[u] = make_float2(-INFINITY, 0.f);
+            if (p < d.w) {
+              const float4 *src = reinterpret_cast<const float4 *>(paged_part<HD, kRows>(a, slot(p), row, blockIdx.y * 64 + 8 * c));
+              ml[u] = __ldcg(a.part_ml + slot(p) * kRows + row);
+              x[u][0] = __ldcg(src);
+              x[u][1] = __ldcg(src + 1);
+            }
+          }
+          float t = top;
+#pragma unroll
+          for (int u = 0; u < kAhead; ++u) t = fmaxf(t, ml[u].x);
+          const float f = top == -INFINITY ? 0.f : ex2(top - t);
+          top = t;
+          l *= f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[e] *= f;
+#pragma unroll
+          for (int u = 0; u < kAhead; ++u) {
+            if (ml[u].x == -INFINITY) continue;
+            const float w = ex2(ml[u].x - t);
+            l += w * ml[u].y;
+            o[0] += w * x[u][0].x, o[1] += w * x[u][0].y, o[2] += w * x[u][0].z, o[3] += w * x[u][0].w;
+            o[4] += w * x[u][1].x, o[5] += w * x[u][1].y, o[6] += w * x[u][1].z, o[7] += w * x[u][1].w;
           }
         }
+      if constexpr (kSplit > 1) {
+        __shared__ float2 tl[kSplit][kStep * 8];
+        const int at = c * kStep + r;
+        __syncthreads();
+        tl[sub][at] = make_float2(top, l);
+        __syncthreads();
+        float t = -INFINITY;
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u)
-          if (p0 + u * kSplit < d.w)
+        for (int u = 0; u < kSplit; ++u) t = fmaxf(t, tl[u][at].x);
+        const float f = top == -INFINITY ? 0.f : ex2(top - t);
 #pragma unroll
-            for (int v = 0; v < kVec; ++v)
-              if (4 * lane + 128 * v < HD) {
-                o[v].x += w[u] * x[u][v].x;
-                o[v].y += w[u] * x[u][v].y;
-                o[v].z += w[u] * x[u][v].z;
-                o[v].w += w[u] * x[u][v].w;
-              }
+        for (int e = 0; e < 8; ++e) o[e] *= f;
+        if (sub > 0)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc[sub - 1][at][e] = o[e];
+        __syncthreads();
+        if (sub == 0) {
+          l = 0.f;
+#pragma unroll
+          for (int u = 0; u < kSplit; ++u) {
+            const float2 x = tl[u][at];
+            l += x.x == -INFINITY ? 0.f : ex2(x.x - t) * x.y;
+          }
+#pragma unroll
+          for (int u = 1; u < kSplit; ++u)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] += acc[u - 1][at][e];
+        }
       }
-    }
-    if constexpr (kSplit > 1) {
-      __syncthreads();
-#pragma unroll
-      for (int v = 0; v < kVec; ++v)
-        if (4 * lane + 128 * v < HD) acc[warp][lane + 32 * v] = o[v];
-      __syncthreads();
-      if (sub == 0) {
-#pragma unroll
-        for (int s = 1; s < kSplit; ++s)
-#pragma unroll
-          for (int v = 0; v < kVec; ++v)
-            if (4 * lane + 128 * v < HD) {
-              const float4 x = acc[warp + s][lane + 32 * v];
-              o[v].x += x.x;
-              o[v].y += x.y;
-              o[v].z += x.z;
-              o[v].w += x.w;
-            }
+      if (valid && sub == 0) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        uint16_t *out = static_cast<uint16_t *>(a.out.p) + (int64_t)(q.s0 + token) * a.out.ld +
+                        (int64_t)(d.y * group + head) * a.out.hs + blockIdx.y * 64 + 8 * c;
+        *reinterpret_cast<uint4 *>(out) = make_uint4(pack2<BF16>(o[0] * inv, o[1] * inv), pack2<BF16>(o[2] * inv, o[3] * inv),
+                                                     pack2<BF16>(o[4] * inv, o[5] * inv), pack2<BF16>(o[6] * inv, o[7] * inv));
       }
-    }
-    if (valid && sub == 0) {
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      uint16_t *out = static_cast<uint16_t *>(a.out.p) + (int64_t)(q.s0 + token) * a.out.ld +
-                      (int64_t)(d.y * group + head) * a.out.hs;
-#pragma unroll
-      for (int v = 0; v < kVec; ++v)
-        if (4 * lane + 128 * v < HD)
-          *reinterpret_cast<uint2 *>(out + 4 * lane + 128 * v) =
-              make_uint2(pack2<BF16>(o[v].x * inv, o[v].y * inv), pack2<BF16>(o[v].z * inv, o[v].w * inv));
     }
   }
 }
