@@ -8,9 +8,12 @@
 // product; what is left of the error is f_i's own, an f64's), and only the fraction of a turn becomes an f32.
 //
 // Bound: memory (each value read and written once).  A CTA takes `tokens` tokens (one where the batch is small, so that a
-// single token's heads spread over `split` CTAs): its threads first compute the tokens' sines and cosines, one a thread,
-// then each group of head_dim / 8 lanes takes (token, head) rows, 8 values a lane: one or two 16-byte loads, the mean by
-// shuffles, the partner of a pair from the same lane or, in the half layout, from the lane rot / 16 away.
+// single token's heads spread over `split` CTAs): its threads first compute the tokens' sines and cosines, one a thread, and
+// lay out where each head's rows are read and written; then each group of head_dim / 8 lanes takes heads of a token, 8 values
+// a lane: one or two 16-byte loads, the mean by shuffles, the partner of a pair from the same lane or, in the half layout,
+// from the lane rot / 16 away.  What counts is instructions a row: choosing q, k or v and its strides for each row took a
+// third of them.  (Four values from each partner instead of eight neighbours save the shuffles but halve the loads' width:
+// 357 us for 32,768 rows of 24/4 x 256 where this form's first version took 264.)
 #include "paged_dev.cuh"
 
 namespace fm {
@@ -18,6 +21,7 @@ namespace {
 
 constexpr int kWThreads = 256;
 constexpr int kWTokens = 8;        // tokens of a CTA at most
+constexpr int kWHeads = 512;       // heads of a CTA at most (their table is 24 KB of shared memory)
 
 // The sequence of packed row t: the last i with starts[i] <= t (a warp's 32-way search).
 __device__ __forceinline__ int find_seq(const PagedBatch &b, int t, int lane) {
@@ -32,12 +36,22 @@ __device__ __forceinline__ int find_seq(const PagedBatch &b, int t, int lane) {
   return lo;
 }
 
+// Where a head's rows lie: bytes; dst_ld a token for queries, a row of the pool for keys and values.
+struct Head {
+  const uint8_t *src;
+  uint8_t *dst;
+  int64_t src_ld, dst_ld;
+  int kind, pad[3];                                 // 0 q, 1 k, 2 v
+};
+
 template <int HD, bool BF16, bool F32IN>
 __global__ void __launch_bounds__(kWThreads) fm_paged_write_kernel(const __grid_constant__ PagedWriteArgs a) {
   constexpr int kLanes = HD / 8;                    // of a row
   constexpr int kGroups = kWThreads / kLanes;       // rows at a time
   __shared__ float2 turn[kWTokens][HD / 2];         // (cos, sin) times gain
-  __shared__ int4 where[kWTokens];                  // the token's row in the pool (first KV head; -1: none), done or not
+  __shared__ int4 where[kWTokens];                  // the token's row in the pool (first KV head; -1: none), position, done or not
+  extern __shared__ __align__(16) uint8_t dyn[];
+  Head *heads = reinterpret_cast<Head *>(dyn);      // of this CTA
   const PagedBatch &b = a.b;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t0 = blockIdx.x * a.tokens, n = min(a.tokens, b.n_tokens - t0);
@@ -58,6 +72,20 @@ __global__ void __launch_bounds__(kWThreads) fm_paged_write_kernel(const __grid_
     if (lane == 0) where[warp] = make_int4((int)row, pos, in && pos >= 0, 0);
   }
   __syncthreads();
+  const int nq = a.q.p ? b.n_kv * b.group : 0, nk = a.k.p ? b.n_kv : 0;
+  const int per = (a.slots + a.split - 1) / a.split, h0 = blockIdx.y * per, h1 = min(a.slots, h0 + per);
+  for (int h = h0 + threadIdx.x; h < h1; h += kWThreads) {
+    const int kind = h < nq ? 0 : h < nq + nk ? 1 : 2, head = h - (kind == 0 ? 0 : kind == 1 ? nq : nq + nk);
+    const PagedRows &src = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
+    Head g;
+    g.src = static_cast<const uint8_t *>(src.p) + head * src.hs * (F32IN ? 4 : 2);
+    g.src_ld = src.ld * (F32IN ? 4 : 2);
+    g.dst = kind == 0 ? static_cast<uint8_t *>(a.qo.p) + head * a.qo.hs * 2
+                      : static_cast<uint8_t *>(kind == 1 ? a.k_pool : a.v_pool) + ((int64_t)head << b.page_log) * HD * 2;
+    g.dst_ld = kind == 0 ? a.qo.ld * 2 : HD * 2;
+    g.kind = kind;
+    heads[h - h0] = g;
+  }
   const int pairs = a.rot >> 1;
   for (int i = threadIdx.x; i < n * pairs; i += kWThreads) {
     const int t = i / pairs, p = i - t * pairs;
@@ -70,92 +98,89 @@ __global__ void __launch_bounds__(kWThreads) fm_paged_write_kernel(const __grid_
   }
   __syncthreads();
   const int group = threadIdx.x / kLanes, gl = threadIdx.x % kLanes, d0 = gl * 8;
-  const int nq = a.q.p ? b.n_kv * b.group : 0, nk = a.k.p ? b.n_kv : 0;
-  // this CTA's heads
-  const int per = (a.slots + a.split - 1) / a.split, h0 = blockIdx.y * per, hn = max(0, min(per, a.slots - h0));
-  const int warp_group = (threadIdx.x & ~31) / kLanes;                 // (a warp's rows run their rounds together)
-  for (int i0 = 0; i0 + warp_group < n * hn; i0 += kGroups) {
-    const int i = i0 + group;
-    const int t = min(i, n * hn - 1) / hn, h = h0 + min(i, n * hn - 1) - t * hn;
-    const int4 w = where[t];
-    const bool live = i < n * hn && w.z;
-    const int kind = h < nq ? 0 : h < nq + nk ? 1 : 2, head = h - (kind == 0 ? 0 : kind == 1 ? nq : nq + nk);
-    const PagedRows &src = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
-    const int64_t at = (int64_t)(t0 + t) * src.ld + (int64_t)head * src.hs + d0;
-    float x[8];
-    if (live) {
-      if constexpr (F32IN) {
-        const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(src.p) + at);
-        const float4 u = __ldcs(p), v = __ldcs(p + 1);
-        x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
+  const int far = a.half ? a.rot >> 4 : 0;             // half layout: the partner's distance in lanes
+  const bool turned = d0 < a.rot, low = gl < far;
+  const int partner = (threadIdx.x & 31) + (turned && a.half ? (low ? far : -far) : 0);
+  const float sign = low ? -1.f : 1.f;
+  for (int t = 0; t < n; ++t) {
+    if (!where[t].z) continue;
+    // this lane's (cos, sin): of its 8 pairs in the half layout, of its 4 otherwise
+    const float2 *cs = &turn[t][a.half ? (low ? gl : gl - far) * 8 : gl * 4];
+    const int64_t row = where[t].x;
+    for (int h = h0 + group, hw = h0 + (threadIdx.x & ~31) / kLanes; hw < h1; h += kGroups, hw += kGroups) {   // (warps go round together)
+      const bool live = h < h1;
+      const Head &hd = heads[live ? h - h0 : 0];
+      const int kind = hd.kind;
+      uint4 raw[F32IN ? 2 : 1];
+      if (live) {
+        const uint4 *p = reinterpret_cast<const uint4 *>(hd.src + (int64_t)(t0 + t) * hd.src_ld) + gl * (F32IN ? 2 : 1);
+        raw[0] = __ldcs(p);
+        if constexpr (F32IN) raw[1] = __ldcs(p + 1);
       } else {
-        const uint4 u = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(src.p) + at));
+        raw[0] = make_uint4(0, 0, 0, 0);
+        if constexpr (F32IN) raw[1] = raw[0];
+      }
+      uint4 y16 = raw[0];
+      if (F32IN || !__all_sync(0xffffffffu, kind == 2)) {   // (V of the pool's type as it is)
+        float x[8];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const uint32_t y = word(u, e);
-          float2 f;
-          if constexpr (BF16)
-            f = make_float2(__uint_as_float(y << 16), __uint_as_float(y & 0xffff0000u));
-          else
-            f = __half22float2(*reinterpret_cast<const __half2 *>(&y));
-          x[2 * e] = f.x;
-          x[2 * e + 1] = f.y;
+          if constexpr (F32IN) {
+            x[e] = __uint_as_float(word(raw[0], e));
+            x[4 + e] = __uint_as_float(word(raw[1], e));
+          } else {
+            const uint32_t w = word(raw[0], e);
+            float2 f;
+            if constexpr (BF16)
+              f = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+            else
+              f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+            x[2 * e] = f.x;
+            x[2 * e + 1] = f.y;
+          }
         }
-      }
-    } else {
+        if (a.q_norm || a.k_norm) {
+          float ss = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = 0.f;
-    }
-    const float *nw = kind == 0 ? a.q_norm : kind == 1 ? a.k_norm : nullptr;
-    float ss = 0.f;
+          for (int e = 0; e < 8; ++e) ss += x[e] * x[e];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss += x[e] * x[e];
-#pragma unroll
-    for (int o = kLanes >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (nw) {
-      const float r = rsqrtf(ss * (1.f / HD) + a.eps);
-      const float4 u = __ldg(reinterpret_cast<const float4 *>(nw + d0)), v = __ldg(reinterpret_cast<const float4 *>(nw + d0) + 1);
-      x[0] *= r * u.x, x[1] *= r * u.y, x[2] *= r * u.z, x[3] *= r * u.w;
-      x[4] *= r * v.x, x[5] *= r * v.y, x[6] *= r * v.z, x[7] *= r * v.w;
-    }
-    if (a.half) {
-      // pairs (i, i + rot / 2): the partner's 8 values lie in the lane rot / 16 further, or back
-      const int far = a.rot >> 4;                    // lanes
-      const bool low = gl < far, turned = gl < 2 * far;
-      float y[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = __shfl_sync(0xffffffffu, x[e], (threadIdx.x & 31) - gl + (turned ? (low ? gl + far : gl - far) : gl));
-      if (turned && kind != 2) {
-        const float4 *cs = reinterpret_cast<const float4 *>(&turn[t][(low ? gl : gl - far) * 8]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float4 c = cs[e];
-          x[2 * e] = low ? x[2 * e] * c.x - y[2 * e] * c.y : y[2 * e] * c.y + x[2 * e] * c.x;
-          x[2 * e + 1] = low ? x[2 * e + 1] * c.z - y[2 * e + 1] * c.w : y[2 * e + 1] * c.w + x[2 * e + 1] * c.z;
+          for (int o = kLanes >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          const float *nw = kind == 0 ? a.q_norm : kind == 1 ? a.k_norm : nullptr;
+          if (nw) {
+            const float r = rsqrtf(ss * (1.f / HD) + a.eps);
+            const float4 u = __ldg(reinterpret_cast<const float4 *>(nw + d0)), v = __ldg(reinterpret_cast<const float4 *>(nw + d0) + 1);
+            x[0] *= r * u.x, x[1] *= r * u.y, x[2] *= r * u.z, x[3] *= r * u.w;
+            x[4] *= r * v.x, x[5] *= r * v.y, x[6] *= r * v.z, x[7] *= r * v.w;
+          }
         }
-      }
-    } else if (d0 < a.rot && kind != 2) {
-      const float4 *cs = reinterpret_cast<const float4 *>(&turn[t][gl * 4]);
+        if (a.half) {
+          float y[8];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float4 c = cs[e];
-        const float u0 = x[4 * e], v0 = x[4 * e + 1], u1 = x[4 * e + 2], v1 = x[4 * e + 3];
-        x[4 * e] = u0 * c.x - v0 * c.y;
-        x[4 * e + 1] = u0 * c.y + v0 * c.x;
-        x[4 * e + 2] = u1 * c.z - v1 * c.w;
-        x[4 * e + 3] = u1 * c.w + v1 * c.z;
+          for (int e = 0; e < 8; ++e) y[e] = __shfl_sync(0xffffffffu, x[e], partner);
+          if (turned && kind != 2) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float4 c = reinterpret_cast<const float4 *>(cs)[e];
+              x[2 * e] = x[2 * e] * c.x + sign * y[2 * e] * c.y;
+              x[2 * e + 1] = x[2 * e + 1] * c.z + sign * y[2 * e + 1] * c.w;
+            }
+          }
+        } else if (turned && kind != 2) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float4 c = reinterpret_cast<const float4 *>(cs)[e];
+            const float u0 = x[4 * e], v0 = x[4 * e + 1], u1 = x[4 * e + 2], v1 = x[4 * e + 3];
+            x[4 * e] = u0 * c.x - v0 * c.y;
+            x[4 * e + 1] = u0 * c.y + v0 * c.x;
+            x[4 * e + 2] = u1 * c.z - v1 * c.w;
+            x[4 * e + 3] = u1 * c.w + v1 * c.z;
+          }
+        }
+        y16 = make_uint4(pack2<BF16>(x[0], x[1]), pack2<BF16>(x[2], x[3]), pack2<BF16>(x[4], x[5]), pack2<BF16>(x[6], x[7]));
       }
+      if (live && (kind == 0 || row >= 0))              // (row < 0: the table has no page for it)
+        *(reinterpret_cast<uint4 *>(hd.dst + (kind == 0 ? (int64_t)(t0 + t) : row) * hd.dst_ld) + gl) = y16;
     }
-    if (!live) continue;
-    uint16_t *dst;
-    if (kind == 0) {
-      dst = static_cast<uint16_t *>(a.qo.p) + (int64_t)(t0 + t) * a.qo.ld + (int64_t)head * a.qo.hs;
-    } else {
-      if (w.x < 0) continue;                         // (the table has no page for it)
-      dst = static_cast<uint16_t *>(kind == 1 ? a.k_pool : a.v_pool) + ((int64_t)w.x + ((int64_t)head << b.page_log)) * HD;
-    }
-    *reinterpret_cast<uint4 *>(dst + d0) =
-        make_uint4(pack2<BF16>(x[0], x[1]), pack2<BF16>(x[2], x[3]), pack2<BF16>(x[4], x[5]), pack2<BF16>(x[6], x[7]));
   }
 }
 
@@ -165,6 +190,7 @@ cudaError_t launch_hd(const PagedWriteArgs &a, dim3 grid, cudaStream_t s) {
   cfg.gridDim = grid;
   cfg.blockDim = kWThreads;
   cfg.stream = s;
+  cfg.dynamicSmemBytes = (a.slots + a.split - 1) / a.split * sizeof(Head);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -188,6 +214,7 @@ cudaError_t launch_paged_write(const PagedWriteArgs &args, int n_sm, cudaStream_
   while (a.tokens < kWTokens && (int64_t)a.b.n_tokens / (2 * a.tokens) >= 8ll * n_sm) a.tokens *= 2;
   a.split = 1;
   while (a.slots > rows * a.split && (int64_t)a.b.n_tokens * 2 * a.split <= 2ll * n_sm) a.split *= 2;
+  a.split = a.split > (a.slots + kWHeads - 1) / kWHeads ? a.split : (a.slots + kWHeads - 1) / kWHeads;
   const dim3 grid((a.b.n_tokens + a.tokens - 1) / a.tokens, a.split);
   return a.hd == 64 ? launch_hd<64>(a, grid, s) : a.hd == 128 ? launch_hd<128>(a, grid, s) : launch_hd<256>(a, grid, s);
 }

@@ -24,7 +24,7 @@ namespace fm {
 
 constexpr int kChunkKeys = 128;    // keys a tile
 constexpr int kChunkCost = 2;      // a unit's own cost in tiles
-constexpr int kChunkLeast = 4;     // places a share has at least
+constexpr int kChunkLeast = 3;     // places a share has at least
 
 template <int HD, int NT>
 struct ChunkCfg {
