@@ -45,7 +45,8 @@ struct RowsCfg {
   static constexpr int kStages = HD == 64 ? 4 : 3;
   static constexpr int kCtas = HD == 64 ? 3 : HD == 128 ? 2 : 1;          // an SM holds
   static constexpr int kMerge = 2 * kRowsUnit * HD * 4;
-  static constexpr int kSmem = kStages * kStage + kMerge + 4 * kRowsUnit * 8 + 16 * kStages + 64 + sizeof(PagedStart) + 16 + 5 * sizeof(PagedWarp<Walk>);
+  static constexpr int kSmem = kStages * kStage + kMerge + 4 * kRowsUnit * 8 + 16 * kStages + 64 + sizeof(PagedStart) + 16 + 2 * sizeof(PagedWarp<Walk>);
+  static_assert(kCtas * (kSmem + 1024) <= 228 * 1024, "shared memory of an SM");
 };
 
 template <int HD, bool BF16>
@@ -65,7 +66,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<HD>::kCtas)
   PagedStart *start = reinterpret_cast<PagedStart *>(sh + 8);
   int *poison = reinterpret_cast<int *>(start + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  PagedWarp<typename C::Walk> &w = reinterpret_cast<PagedWarp<typename C::Walk> *>(poison + 4)[warp];
+  PagedWarp<typename C::Walk> &w = reinterpret_cast<PagedWarp<typename C::Walk> *>(poison + 4)[warp < 4 ? 0 : 1];   // (one for the four)
   const PagedSeg &g = w.g;
   const PagedBatch &b = a.b;
 
@@ -82,7 +83,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<HD>::kCtas)
   }
   pdl_wait();
   paged_plan<kRowsUnit, true, kRowsKeys, kRowsCost, kRowsLeast, kRowsThreads>(a, sh, start);
-  w.init(*start, b.group, lane);
+  if (warp == 0 || warp == 4) w.init(*start, b.group, lane);
 
   if (warp == 4) {
     // ---- fetch: a lane a (page box, panel) ----
@@ -125,7 +126,10 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<HD>::kCtas)
   uint32_t c = 0;
   bool ok = true;
   if (threadIdx.x == 0) a.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
-  while (w.next(a, lane)) {
+  for (;;) {
+    if (threadIdx.x == 0) w.more = w.walk.next(a, w.g);
+    named_sync(1, 128);
+    if (!w.more) break;
     const int r0 = g.tile * kRowsUnit, rows = min(kRowsUnit, g.q.n_new * b.group - r0);
     const int pos0 = g.q.len - g.q.n_new;
     int tok[2];
