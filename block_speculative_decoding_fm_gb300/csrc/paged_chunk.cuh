@@ -184,10 +184,22 @@ __global__ void __launch_bounds__(ChunkCfg<HD, NT>::kThreads, 1)
     bool ok = true;
     while (ok && w.next(a, lane)) {
       const int n = g.end - g.begin, nt = NT == 2 && rows_of(g, 1) > 0 ? 2 : 1;
-      auto row_of = [&](int u) {   // of the u-th stage of the segment
-        const int e = u / C::kSub;
-        const int j = NT == 2 ? e >> 1 : e == 0 ? 0 : (e & 1) ? min((e + 1) >> 1, n - 1) : (e - 2) >> 1;
-        return mine ? paged_row(a, g.s, g.seq, g.head, g.s.tile(g.begin + j) * kChunkKeys + (box << box_log)) : 0;
+      // where this lane's rows of a key tile lie
+      auto row_of = [&](int j) {
+        return mine && j < n ? paged_row(a, g.s, g.seq, g.head, g.s.tile(g.begin + j) * kChunkKeys + (box << box_log)) : 0;
+      };
+      auto fetch = [&](const CUtensorMap *map, int row) {
+#pragma unroll
+        for (int sub = 0; ok && sub < C::kSub; ++sub) {
+          ok = paged_wait_warp(empty(c), phase(c) ^ 1, b.err);
+          if (!ok) break;
+          if (lane == 0) mbar_expect_tx(full(c), C::kStage);
+          __syncwarp();
+          if (mine)
+            tma_2d_row(ring + (c % C::kStages) * C::kStage + panel * C::kPanel + (box << box_log) * 128, map,
+                       sub * C::kDims + panel * 64, row, full(c));
+          ++c;
+        }
       };
       ok = paged_wait_warp(qfree, (segs & 1) ^ 1, b.err);
       if (!ok) break;
@@ -198,20 +210,14 @@ __global__ void __launch_bounds__(ChunkCfg<HD, NT>::kThreads, 1)
             tma_3d_box(qbuf + (t * C::kP + p) * 16384, &a.tq, p * 64, g.head * b.group, g.q.s0 + (g.tile * NT + t) * tt, qfull);
       }
       ++segs;
-      int row = row_of(0);
-      for (int u = 0; u < 2 * n * C::kSub; ++u) {
-        const int e = u / C::kSub;
-        const bool is_k = NT == 2 ? !(e & 1) : e == 0 || ((e & 1) && e < 2 * n - 1);
-        const int next = (u + 1) % C::kSub ? row : u + 1 < 2 * n * C::kSub ? row_of(u + 1) : 0;
-        ok = paged_wait_warp(empty(c), phase(c) ^ 1, b.err);
-        if (!ok) break;
-        if (lane == 0) mbar_expect_tx(full(c), C::kStage);
-        __syncwarp();
-        if (mine)
-          tma_2d_row(ring + (c % C::kStages) * C::kStage + panel * C::kPanel + (box << box_log) * 128, is_k ? &a.tk : &a.tv,
-                     u % C::kSub * C::kDims + panel * 64, row, full(c));
-        ++c;
-        row = next;
+      // (the table is asked two tiles ahead)
+      int before = 0, row = row_of(0), next = row_of(1);
+      for (int j = 0; ok && j <= n; ++j) {
+        const int ahead = row_of(j + 2);
+        if (j < n) fetch(&a.tk, row);
+        if (NT == 2 && j < n) fetch(&a.tv, row);
+        if (NT == 1 && j > 0) fetch(&a.tv, before);   // V behind the next tile's K: the scores run a tile ahead
+        before = row, row = next, next = ahead;
       }
     }
     // the CTA leaves only after its copies have landed

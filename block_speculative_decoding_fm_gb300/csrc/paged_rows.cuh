@@ -94,11 +94,11 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<HD>::kCtas)
     bool ok = true;
     while (ok && w.next(a, lane)) {
       auto row_of = [&](int i) { return mine ? paged_row(a, g.s, g.seq, g.head, g.s.tile(i) * kRowsKeys + (box << box_log)) : 0; };
-      int row = row_of(g.begin);
+      int row = row_of(g.begin), next = g.begin + 1 < g.end ? row_of(g.begin + 1) : 0;
       for (int i = g.begin; i < g.end; ++i) {
-        const int next = i + 1 < g.end ? row_of(i + 1) : 0;
+        const int ahead = i + 2 < g.end ? row_of(i + 2) : 0;   // (the table is asked two stages ahead)
         const int s = c % C::kStages;
-        ok = mbar_wait_warp(empty(s), ((c / C::kStages) & 1) ^ 1, a.b.err);
+        ok = paged_wait_warp(empty(s), ((c / C::kStages) & 1) ^ 1, a.b.err);
         if (!ok) break;
         if (lane == 0) mbar_expect_tx(full(s), C::kStage);
         __syncwarp();
@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<HD>::kCtas)
           tma_2d_row(dst + kP * kPanel, &a.tv, panel * 64, row, full(s));
         }
         ++c;
-        row = next;
+        row = next, next = ahead;
       }
     }
     // the CTA leaves only after its copies have landed
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<HD>::kCtas)
     for (int i = g.begin; i < g.end; ++i, ++c) {
       const int st = c % C::kStages, key0 = g.s.tile(i) * kRowsKeys;
       const bool masked = paged_masked<kRowsKeys>(a, g.s, key0);
-      if (ok) ok = mbar_wait_warp(full(st), (c / C::kStages) & 1, a.b.err);
+      if (ok) ok = paged_wait_warp(full(st), (c / C::kStages) & 1, a.b.err);
       const uint32_t kt = base + st * C::kStage, vt = kt + kP * kPanel;
       float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
