@@ -43,7 +43,7 @@ EXPORTS = ["fm_create", "fm_time_conditioning", "fm_context_append", "fm_context
            "fm_kvq_memory_bytes", "fm_kvq_synchronize", "fm_kvq_selftest_wait_timeout", "fm_kvq_last_error", "fm_kvq_destroy",
            "fm_paged_create", "fm_paged_write", "fm_paged_attend", "fm_paged_workspace_bytes", "fm_paged_get_config",
            "fm_paged_last_launch_count", "fm_paged_synchronize", "fm_paged_selftest_wait_timeout", "fm_paged_last_error",
-           "fm_paged_destroy"]
+           "fm_paged_destroy", "fm_mtp_use_paged"]
 FM_ROPE_INTERLEAVED, FM_ROPE_HALF = 0, 1
 FM_ROPE_PLAIN, FM_ROPE_LINEAR, FM_ROPE_BY_PARTS = 0, 1, 2
 
@@ -188,6 +188,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "fm_paged_selftest_wait_timeout": (I32, [P, I32, P]),
         "fm_paged_last_error": (ctypes.c_char_p, [P]),
         "fm_paged_destroy": (None, [P]),
+        "fm_mtp_use_paged": (I32, [P, P, I32, P, I32, I32, I32]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -740,7 +741,7 @@ def fm_mtp_use_kvq(m, c, layer: int = 0, seq: int = 0, next_pos: Optional[int] =
     if c is not None and next_pos is None:
         next_pos = fm_kvq_length(c, layer, seq)
     _mtp_check(load_library().fm_mtp_use_kvq(m, c, layer, seq, next_pos or 0, _decay(decay)), m)
-    m._kvq = c
+    m._kvq, m._paged = c, None
 
 
 def fm_kvq_memory_bytes(c) -> int:
@@ -937,3 +938,17 @@ def fm_paged_destroy(c) -> None:
         load_library().fm_paged_destroy(c)
         c.value = None
         c._pool = None
+
+
+def fm_mtp_use_paged(m, c, layer: int = 0, table=None, window: int = 0, sinks: int = 0) -> None:
+    """Keep the MTP head's rows in `layer` of the paged cache c (None: in its own f32 cache).  table: a contiguous CUDA int32
+    tensor [pages], the pages of the head's sequence; window, sinks: as fm_paged_attend's.  The head keeps c and table alive
+    while it uses them."""
+    if c is not None:
+        import torch
+        if table is None or table.dtype != torch.int32 or table.get_device() != c._device or table.dim() != 1 or \
+                not table.is_contiguous():
+            raise ValueError(f"table must be a contiguous int32 tensor [pages] on cuda:{c._device}")
+    _mtp_check(load_library().fm_mtp_use_paged(m, c, layer, _ptr(table) if c is not None else None,
+                                               table.shape[0] if c is not None else 0, window, sinks), m)
+    m._paged, m._kvq = None if c is None else (c, table), None

@@ -11,7 +11,9 @@
 // that enough SMs stream the weights; the consumer of the output sums the
 // slices.  The KV cache is f32, as the page keeps it, or a 4-bit cache that the
 // caller hands over (fm_mtp_use_kvq): a pass then stores its rows there and
-// attends through fm_kvq_append and fm_kvq_attend.
+// attends through fm_kvq_append and fm_kvq_attend; or a paged cache
+// (fm_mtp_use_paged), by fm_paged_write, which takes the norms and the rotation
+// along, and fm_paged_attend.
 #include <algorithm>
 #include <cmath>
 #include <cstdarg>
@@ -25,6 +27,7 @@
 #include "dev_common.cuh"
 #include "fm_internal.h"
 #include "kvq.h"
+#include "paged.h"
 
 namespace fm {
 namespace {
@@ -245,6 +248,36 @@ __global__ void __launch_bounds__(kThreads) mtp_gate_kernel(const float *o, cons
   store_y8(ylm, m, c0, v);
 }
 
+// the same for attention rows of 16 bits (a paged cache's type).
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads) mtp_gate16_kernel(const uint16_t *o, const float *qkv, int ldq, int nh, int hd,
+                                                              uint8_t *ylm) {
+  pdl_trigger();
+  pdl_wait();
+  const int m = blockIdx.y, c0 = 8 * (blockIdx.x * kThreads + threadIdx.x);
+  if (c0 >= nh * hd) return;
+  const int h = c0 / hd;
+  const uint4 x = __ldcg(reinterpret_cast<const uint4 *>(o + (size_t)m * nh * hd + c0));
+  float v[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t w = word(x, e >> 1) >> (16 * (e & 1)) & 0xffffu;
+    const float y = BF16 ? __uint_as_float(w << 16) : __half2float(__ushort_as_half((unsigned short)w));
+    const float gate = __ldcg(qkv + (size_t)m * ldq + h * 2 * hd + hd + (c0 - h * hd) + e);
+    v[e] = y / (1.f + expf(-gate));
+  }
+  store_y8(ylm, m, c0, v);
+}
+
+// a pass's batch: starts 0, rows; the length with them
+__global__ void mtp_batch_kernel(int32_t *meta, int rows, int length) {
+  pdl_trigger();
+  pdl_wait();
+  meta[0] = 0;
+  meta[1] = rows;
+  meta[2] = length;
+}
+
 // silu(gate) * up from the stacked gate / up product, as the operand of ffn_down.
 __global__ void __launch_bounds__(kThreads) mtp_silu_mul_kernel(const float *gu, int I, uint8_t *ylm) {
   pdl_trigger();
@@ -317,6 +350,16 @@ struct fm_mtp {
   int64_t next_pos = 0;          // the position after the cache's last row
   int kvq_rows = 0;              // rows a sequence of it holds
   float *kst = nullptr, *vst = nullptr, *ao = nullptr;   // a pass's rows before they are stored, and its attention rows
+  // the rows in a paged cache (fm_mtp_use_paged)
+  fm_paged *paged = nullptr;
+  int paged_layer = 0, paged_window = 0, paged_sinks = 0;
+  bool paged_bf16 = false;
+  fm_paged_batch batch{};
+  int64_t paged_rows = 0;        // rows its table has pages for
+  int32_t *meta = nullptr;
+  uint16_t *q16 = nullptr, *ao16 = nullptr;
+  uint8_t *paged_ws = nullptr;
+  int64_t paged_ws_bytes = 0;
 };
 
 namespace {
@@ -481,6 +524,37 @@ fm_status kvq_rows_attend(fm_mtp *m, int M, int pos0, int kv_lo, cudaStream_t s)
   return FM_OK;
 }
 
+#define MPAGED(expr)                                                                            \
+  do {                                                                                           \
+    const fm_status s_ = (expr);                                                                 \
+    if (s_ != FM_OK) return mfail(m, s_, "paged cache: %s", fm_paged_last_error(m->paged));      \
+    int32_t n_ = 0;                                                                              \
+    fm_paged_last_launch_count(m->paged, &n_);                                                   \
+    m->last_launches += n_;                                                                      \
+  } while (0)
+
+// a pass's rows into the paged cache (norms and rotation with them), its queries over it, gated
+fm_status paged_rows_attend(fm_mtp *m, int M, int pos0, cudaStream_t s) {
+  const fm_mtp_config &c = m->cfg;
+  const int nh = c.n_heads, nkv = c.n_kv_heads, hd = c.head_dim;
+  MCK(launch(mtp_batch_kernel, dim3(1), dim3(1), s, m->meta, M, pos0 + M));
+  ++m->last_launches;
+  fm_paged_batch b = m->batch;
+  b.n_tokens = M;
+  b.max_new = M;
+  const fm_paged_rows q = {m->y, m->qkv.N, 2 * hd}, k = {m->y + (size_t)nh * 2 * hd, m->qkv.N, hd},
+                      v = {m->y + (size_t)nh * 2 * hd + (size_t)nkv * hd, m->qkv.N, hd}, q16 = {m->q16, (int64_t)nh * hd, hd},
+                      o16 = {m->ao16, (int64_t)nh * hd, hd};
+  MPAGED(fm_paged_write(m->paged, m->paged_layer, &b, &q, &k, &v, FM_DTYPE_F32, m->n_q, m->n_k, &q16, s));
+  MPAGED(fm_paged_attend(m->paged, m->paged_layer, &b, &q16, &o16, 1.0f / sqrtf((float)hd), 1, m->paged_window, m->paged_sinks,
+                         m->paged_ws, m->paged_ws_bytes, s));
+  const dim3 grid((nh * hd / 8 + kThreads - 1) / kThreads, M);
+  MCK(launch(m->paged_bf16 ? mtp_gate16_kernel<true> : mtp_gate16_kernel<false>, grid, dim3(kThreads), s,
+             (const uint16_t *)m->ao16, (const float *)m->y, m->qkv.N, nh, hd, m->ylm));
+  ++m->last_launches;
+  return FM_OK;
+}
+
 // MTPHead.forward over M rows; drafts: per-row argmax of the lm_head, or null
 fm_status mtp_pass(fm_mtp *m, int M, const int32_t *tokens, const float *hn, int ldh, int pos0, int kv_lo,
                    int32_t *drafts, cudaStream_t s) {
@@ -495,19 +569,23 @@ fm_status mtp_pass(fm_mtp *m, int M, const int32_t *tokens, const float *hn, int
   ++m->last_launches;
   MTRY(run_lin(m, m->qkv, M, m->y, nullptr, s));
   const bool q4 = m->kvq != nullptr;
-  MCK(launch(mtp_qk_prep_kernel, dim3(M, nh + 2 * nkv), dim3(hd), s, (const float *)m->y, m->qkv.N, nh, nkv, hd,
-             c.rot_dims, (double)c.theta, c.eps, (const float *)m->n_q, (const float *)m->n_k, pos0, q4 ? 0 : pos0, m->Q,
-             q4 ? m->kst : m->kc, q4 ? m->vst : m->vc));
-  ++m->last_launches;
-  if (q4) {
-    MTRY(kvq_rows_attend(m, M, pos0, kv_lo, s));
-    MCK(launch(mtp_gate_kernel, dim3((nh * hd / 8 + kThreads - 1) / kThreads, M), dim3(kThreads), s, (const float *)m->ao,
-               (const float *)m->y, m->qkv.N, nh, hd, m->ylm));
+  if (m->paged) {
+    MTRY(paged_rows_attend(m, M, pos0, s));
   } else {
-    MCK(launch(mtp_attn_kernel, dim3(M, nh), dim3(kThreads), s, (const float *)m->Q, (const float *)m->y, m->qkv.N,
-               (const float *)m->kc, (const float *)m->vc, nh, nkv, hd, pos0, kv_lo, 1.0f / sqrtf((float)hd), m->ylm));
+    MCK(launch(mtp_qk_prep_kernel, dim3(M, nh + 2 * nkv), dim3(hd), s, (const float *)m->y, m->qkv.N, nh, nkv, hd,
+               c.rot_dims, (double)c.theta, c.eps, (const float *)m->n_q, (const float *)m->n_k, pos0, q4 ? 0 : pos0, m->Q,
+               q4 ? m->kst : m->kc, q4 ? m->vst : m->vc));
+    ++m->last_launches;
+    if (q4) {
+      MTRY(kvq_rows_attend(m, M, pos0, kv_lo, s));
+      MCK(launch(mtp_gate_kernel, dim3((nh * hd / 8 + kThreads - 1) / kThreads, M), dim3(kThreads), s, (const float *)m->ao,
+                 (const float *)m->y, m->qkv.N, nh, hd, m->ylm));
+    } else {
+      MCK(launch(mtp_attn_kernel, dim3(M, nh), dim3(kThreads), s, (const float *)m->Q, (const float *)m->y, m->qkv.N,
+                 (const float *)m->kc, (const float *)m->vc, nh, nkv, hd, pos0, kv_lo, 1.0f / sqrtf((float)hd), m->ylm));
+    }
+    ++m->last_launches;
   }
-  ++m->last_launches;
   // attn_output's slices land beside the q/k/v rows' gates (read above): a separate region
   float *yo = m->y + (size_t)kMaxRows * m->qkv.N;
   MTRY(run_lin(m, m->o, M, yo, nullptr, s));
@@ -532,7 +610,7 @@ fm_status mtp_checks(fm_mtp *m, int M, const int32_t *tokens, const float *hn, i
   if (M < 1 || M > c.max_rows) return mfail(m, FM_ERR_INVALID_ARG, "n_rows %d outside [1, %d]", M, c.max_rows);
   if (!tokens || !hn) return mfail(m, FM_ERR_INVALID_ARG, "null tokens or hidden rows");
   if (pos0 < 0 || kv_lo < 0 || kv_lo > pos0) return mfail(m, FM_ERR_INVALID_ARG, "kv_lo %d outside [0, pos0 %d]", kv_lo, pos0);
-  if (m->kvq) return FM_OK;   // (the 4-bit cache's own size counts)
+  if (m->kvq || m->paged) return FM_OK;   // (that cache's own size counts)
   const int64_t end = (int64_t)pos0 + M;
   if (end > c.kv_cap) return mfail(m, FM_ERR_INVALID_ARG, "pos0 + n_rows = %lld > kv_cap %d", (long long)end, c.kv_cap);
   return FM_OK;
@@ -552,6 +630,18 @@ fm_status mtp_kvq_checks(fm_mtp *m, int64_t rows, int pos0, int kv_lo) {
     return mfail(m, FM_ERR_INVALID_ARG, "pos0 %d + %lld rows: positions end at %d", pos0, (long long)rows, INT32_MAX);
   if (kv_lo > 0 && row != pos0)
     return mfail(m, FM_ERR_UNSUPPORTED, "kv_lo %d after an eviction: rows are no longer at their positions", kv_lo);
+  return FM_OK;
+}
+
+// with a paged cache: `rows` rows from pos0 on have pages, before anything is launched
+fm_status mtp_paged_checks(fm_mtp *m, int64_t rows, int pos0, int kv_lo) {
+  if (!m->paged) return FM_OK;
+  int dev = -1;
+  MCK(cudaGetDevice(&dev));
+  if (dev != m->device) return mfail(m, FM_ERR_INVALID_ARG, "the current device is %d, the head's and its paged cache's is %d", dev, m->device);
+  if (pos0 + rows > m->paged_rows)
+    return mfail(m, FM_ERR_CONTEXT_FULL, "pos0 %d + %lld rows, the table has pages for %lld", pos0, (long long)rows, (long long)m->paged_rows);
+  if (kv_lo > 0) return mfail(m, FM_ERR_UNSUPPORTED, "kv_lo %d over a paged cache: its window says what a row sees", kv_lo);
   return FM_OK;
 }
 
@@ -665,6 +755,7 @@ fm_status fm_mtp_forward(fm_mtp *m, int32_t n_rows, const int32_t *tokens_dev, c
   m->last_launches = 0;
   MTRY(mtp_checks(m, n_rows, tokens_dev, hn_dev, pos0, kv_lo));
   MTRY(mtp_kvq_checks(m, n_rows, pos0, kv_lo));
+  MTRY(mtp_paged_checks(m, n_rows, pos0, kv_lo));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   MTRY(mtp_pass(m, n_rows, tokens_dev, hn_dev, m->cfg.hidden, pos0, kv_lo, drafts_dev, s));
   if (hout_dev)
@@ -680,9 +771,10 @@ fm_status fm_mtp_draft(fm_mtp *m, int32_t n_rows, const int32_t *tokens_dev, con
   if (!drafts_dev) return mfail(m, FM_ERR_INVALID_ARG, "null drafts");
   const int64_t all = (int64_t)n_rows + depth - 1;   // rows of all passes
   if (depth < 1) return mfail(m, FM_ERR_INVALID_ARG, "depth %d", depth);
-  if (!m->kvq && pos0 + all > m->cfg.kv_cap)
+  if (!m->kvq && !m->paged && pos0 + all > m->cfg.kv_cap)
     return mfail(m, FM_ERR_INVALID_ARG, "depth %d outside [1, %d]", depth, m->cfg.kv_cap - pos0 - n_rows + 1);
   MTRY(mtp_kvq_checks(m, all, pos0, kv_lo));
+  MTRY(mtp_paged_checks(m, all, pos0, kv_lo));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int H = m->cfg.hidden;
   MTRY(mtp_pass(m, n_rows, tokens_dev, hn_dev, H, pos0, kv_lo, nullptr, s));
@@ -702,6 +794,7 @@ fm_status fm_mtp_use_kvq(fm_mtp *m, fm_kvq *c, int32_t layer, int32_t seq, int64
   if (!m) return FM_ERR_INVALID_ARG;
   if (!c) {
     m->kvq = nullptr;
+    m->paged = nullptr;
     return FM_OK;
   }
   fm_kvq_config g;
@@ -724,6 +817,7 @@ fm_status fm_mtp_use_kvq(fm_mtp *m, fm_kvq *c, int32_t layer, int32_t seq, int64
     if (!m->vst) MTRY(malloc_dev(m, &m->vst, kvw));
     MTRY(malloc_dev(m, &m->ao, (size_t)kMaxRows * m->cfg.n_heads * m->cfg.head_dim));
   }
+  m->paged = nullptr;
   m->kvq = c;
   m->kvq_layer = layer;
   m->kvq_seq = seq;
@@ -733,10 +827,59 @@ fm_status fm_mtp_use_kvq(fm_mtp *m, fm_kvq *c, int32_t layer, int32_t seq, int64
   return FM_OK;
 }
 
+fm_status fm_mtp_use_paged(fm_mtp *m, fm_paged *c, int32_t layer, const int32_t *table_dev, int32_t table_pages, int32_t window,
+                           int32_t sinks) {
+  if (!m) return FM_ERR_INVALID_ARG;
+  if (!c) {
+    m->kvq = nullptr;
+    m->paged = nullptr;
+    return FM_OK;
+  }
+  fm_paged_config g;
+  if (fm_paged_get_config(c, &g) != FM_OK || layer < 0 || layer >= g.n_layers)
+    return mfail(m, FM_ERR_INVALID_ARG, "the paged cache has no layer %d", layer);
+  if (g.n_kv_heads != m->cfg.n_kv_heads || g.n_heads != m->cfg.n_heads || g.head_dim != m->cfg.head_dim)
+    return mfail(m, FM_ERR_INVALID_ARG, "the paged cache has %d heads over %d of %d, the head %d over %d of %d", g.n_heads, g.n_kv_heads,
+                 g.head_dim, m->cfg.n_heads, m->cfg.n_kv_heads, m->cfg.head_dim);
+  if (g.rot_dims != m->cfg.rot_dims || g.eps != m->cfg.eps ||
+      (g.rot_dims > 0 && (g.theta != m->cfg.theta || g.rot_layout != FM_ROPE_HALF)))
+    return mfail(m, FM_ERR_INVALID_ARG, "the paged cache rotates %d dims (layout %d, theta %g, eps %g), the head %d (half, %g, %g)", g.rot_dims,
+                 g.rot_layout, g.theta, g.eps, m->cfg.rot_dims, m->cfg.theta, m->cfg.eps);
+  int dev = -1;
+  MCK(cudaGetDevice(&dev));
+  if (paged_device(c) != m->device || dev != m->device)
+    return mfail(m, FM_ERR_INVALID_ARG, "the paged cache is on device %d, the head on %d, the current one is %d", paged_device(c), m->device, dev);
+  if (!table_dev || reinterpret_cast<uintptr_t>(table_dev) % 4 || table_pages < 1 || (int64_t)table_pages * g.page_rows > kPagedMaxRows)
+    return mfail(m, FM_ERR_INVALID_ARG, "table: null or misaligned, or %d pages", table_pages);
+  if (window < 0 || sinks < 0 || (sinks > 0 && window == 0)) return mfail(m, FM_ERR_INVALID_ARG, "window %d, sinks %d", window, sinks);
+  const size_t rows = (size_t)kMaxRows * m->cfg.n_heads * m->cfg.head_dim;
+  if (!m->meta) MTRY(malloc_dev(m, &m->meta, 4));
+  if (!m->q16) MTRY(malloc_dev(m, &m->q16, rows));
+  if (!m->ao16) MTRY(malloc_dev(m, &m->ao16, rows));
+  int64_t need = 0;
+  if (fm_paged_workspace_bytes(c, m->cfg.max_rows, &need) != FM_OK) return mfail(m, FM_ERR_INVALID_ARG, "the paged cache's workspace");
+  if (m->paged_ws_bytes < need) {   // (a smaller one of an earlier cache stays until the head goes: passes may still use it)
+    m->paged_ws = nullptr;
+    m->paged_ws_bytes = 0;
+    MTRY(malloc_dev(m, &m->paged_ws, (size_t)need));
+    m->paged_ws_bytes = need;
+  }
+  m->kvq = nullptr;
+  m->paged = c;
+  m->paged_layer = layer;
+  m->paged_window = window;
+  m->paged_sinks = sinks;
+  m->paged_bf16 = g.dtype == FM_DTYPE_BF16;
+  m->paged_rows = (int64_t)table_pages * g.page_rows;
+  m->batch = {m->meta, m->meta + 2, table_dev, table_pages, 1, 0, table_pages, 0};
+  return FM_OK;
+}
+
 fm_status fm_mtp_cache(fm_mtp *m, int32_t which, int32_t rows, float *dst, void *stream) {
   if (!m) return FM_ERR_INVALID_ARG;
   if ((which != 0 && which != 1) || rows < 0 || rows > m->cfg.kv_cap || !dst)
     return mfail(m, FM_ERR_INVALID_ARG, "bad cache copy arguments");
+  if (m->paged && rows > 0) return mfail(m, FM_ERR_STATE, "the rows are in a paged cache, whose pool is the caller's");
   if (m->kvq && rows > 0) return mfail(m, FM_ERR_STATE, "the rows are in a 4-bit cache: fm_kvq_read reads them");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   MCK(cudaMemcpyAsync(dst, which ? m->vc : m->kc, (size_t)rows * m->cfg.n_kv_heads * m->cfg.head_dim * 4,
@@ -752,6 +895,10 @@ fm_status fm_mtp_cache(fm_mtp *m, int32_t which, int32_t rows, float *dst, void 
   if (m->kvq) {   // (the passes' attention raises the cache's word)
     const fm_status st = fm_kvq_synchronize(m->kvq, stream);
     if (st != FM_OK) return mfail(m, st, "4-bit cache: %s", fm_kvq_last_error(m->kvq));
+  }
+  if (m->paged) {
+    const fm_status st = fm_paged_synchronize(m->paged, stream);
+    if (st != FM_OK) return mfail(m, st, "paged cache: %s", fm_paged_last_error(m->paged));
   }
   return FM_OK;
 }

@@ -864,6 +864,29 @@ FM_API const char *fm_paged_last_error(const fm_paged *c);   /* never NULL; this
    are not replayed afterwards. */
 FM_API void fm_paged_destroy(fm_paged *c);
 
+/*
+ * fm_mtp_use_paged -- keep the MTP head's rows in layer of the paged cache c
+ * from the next pass on (c NULL: in the head's own f32 cache again, which holds
+ * what it held; fm_mtp_use_kvq and this call replace each other).  A pass
+ * writes its rows by fm_paged_write, norms and rotation with them, and attends
+ * by fm_paged_attend in the pool's type (f16 or bf16: the rows' roundings).  The
+ * row of position p is row p of the sequence whose pages table_dev (device
+ * int32 [table_pages], read when passes run, its pages changed only between
+ * them) names; rows below a pass's pos0 were written by earlier passes or by
+ * fm_paged_write.  The table's rows, not kv_cap, bound the positions (kv_cap
+ * may be 1).  window, sinks: as fm_paged_attend's (0, 0: every row is seen).
+ * c has the head's n_heads, n_kv_heads, head_dim, rot_dims, theta and eps, the half layout, and any
+ * scaling of the angles; it stays the caller's and outlives its use.
+ * Passes then also fail with FM_ERR_CONTEXT_FULL (positions past the table),
+ * FM_ERR_UNSUPPORTED (kv_lo > 0) and FM_ERR_INVALID_ARG (another current
+ * device); nothing is launched then.  fm_mtp_cache with rows > 0 answers
+ * FM_ERR_STATE; with rows = 0 it also reports what fm_paged_synchronize does.
+ * Errors: FM_ERR_INVALID_ARG (another device, configuration or layer, table, window or
+ *   sinks), FM_ERR_OOM.
+ */
+FM_API fm_status fm_mtp_use_paged(fm_mtp *m, fm_paged *c, int32_t layer, const int32_t *table_dev,
+                                  int32_t table_pages, int32_t window, int32_t sinks);
+
 #ifdef __cplusplus
 }
 #endif
