@@ -779,7 +779,7 @@ class PagedCache(ctypes.c_void_p):
 class PagedBatch:
     """A batch's place in a paged cache (fm_paged_batch); holds the tensors it was made from."""
 
-    __slots__ = ("arg", "tensors", "n_tokens", "workspace_bytes", "cache")
+    __slots__ = ("arg", "at", "tensors", "n_tokens", "workspace_bytes", "cache")
 
 
 def _paged_check(status: int, c=None):
@@ -810,7 +810,9 @@ def fm_paged_create(k_pool, v_pool, n_heads: int, rot_dims: int = 0, layout: int
     _paged_check(load_library().fm_paged_create(ctypes.byref(g), k_pool.data_ptr(), v_pool.data_ptr(), _stream(stream),
                                                 ctypes.byref(c)))
     c._pool, c._heads, c._kv_heads, c._head_dim = (k_pool, v_pool), n_heads, kv_heads, head_dim
-    c._dtype, c._code, c._device = k_pool.dtype, dtypes[k_pool.dtype], k_pool.get_device()
+    c._dtype, c._code, c._device, c._f32 = k_pool.dtype, dtypes[k_pool.dtype], k_pool.get_device(), torch.float32
+    empty, uint8, device = torch.empty, torch.uint8, k_pool.device
+    c._workspace = lambda n: empty(n, dtype=uint8, device=device)
     return c
 
 
@@ -829,36 +831,30 @@ def fm_paged_batch(c, starts, lengths, table, n_tokens: int, max_new: Optional[i
     ld = table.stride(0) if n > 1 else table.shape[1]
     b.arg = FmPagedBatch(starts.data_ptr(), lengths.data_ptr(), table.data_ptr(), ld, n, n_tokens, table.shape[1],
                          n_tokens if max_new is None else max_new)
-    b.tensors, b.n_tokens, b.cache = (starts, lengths, table), n_tokens, c
+    b.at, b.tensors, b.n_tokens, b.cache = ctypes.addressof(b.arg), (starts, lengths, table), n_tokens, c
     b.workspace_bytes = fm_paged_workspace_bytes(c, b.arg.max_new)
     return b
 
 
-def _paged_rows(x, heads: int, batch: PagedBatch, c, dtype, what: str) -> FmPagedRows:
-    """The library's view of a tensor [>= n_tokens, heads, head_dim] whose last axis is contiguous."""
-    shape, stride = x.shape, x.stride()
-    if x.dtype != dtype or x.get_device() != c._device:
+def _paged_rows(x, heads: int, n_tokens: int, c, dtype, what: str) -> array.array:
+    """The library's view (an fm_paged_rows; a quarter of the time that a ctypes structure takes) of a tensor [>= n_tokens,
+    heads, head_dim] whose last axis is contiguous."""
+    if x.dtype is not dtype or x.get_device() != c._device:
         raise ValueError(f"{what} must be a {dtype} tensor on cuda:{c._device}")
-    if len(shape) != 3 or shape[0] < batch.n_tokens or shape[1] != heads or shape[2] != c._head_dim:
-        raise ValueError(f"{what} has shape {tuple(shape)}, expected [{batch.n_tokens}, {heads}, {c._head_dim}]")
+    shape, stride = x.shape, x.stride()
+    if len(shape) != 3 or shape[0] < n_tokens or shape[1] != heads or shape[2] != c._head_dim:
+        raise ValueError(f"{what} has shape {tuple(shape)}, expected [{n_tokens}, {heads}, {c._head_dim}]")
     if stride[2] != 1:
         raise ValueError(f"{what}: a row's values must be contiguous")
-    return FmPagedRows(x.data_ptr(), stride[0], stride[1])
+    return array.array("q", (x.data_ptr(), stride[0], stride[1]))
 
 
 def _paged_norm(w, c, what: str):
-    import torch
     if w is None:
         return None
-    if w.dtype != torch.float32 or w.get_device() != c._device or tuple(w.shape) != (c._head_dim,) or not w.is_contiguous():
+    if w.dtype is not c._f32 or w.get_device() != c._device or w.shape != (c._head_dim,) or not w.is_contiguous():
         raise ValueError(f"{what} must be a contiguous float32 tensor [{c._head_dim}] on cuda:{c._device}")
     return w.data_ptr()
-
-
-def _paged_of(c, batch: PagedBatch):
-    if batch.cache is not c:
-        raise ValueError("the batch was made for another cache")
-    return ctypes.byref(batch.arg)
 
 
 def fm_paged_write(c, layer: int, batch: PagedBatch, q=None, k=None, v=None, q_out=None, q_norm=None, k_norm=None,
@@ -867,17 +863,18 @@ def fm_paged_write(c, layer: int, batch: PagedBatch, q=None, k=None, v=None, q_o
     into q_out.  q: [n_tokens, n_heads, head_dim], k, v: [n_tokens, n_kv_heads, head_dim], of float32 or the pool's type, any
     stride between tokens and heads (whole 16 bytes); q_out: of the pool's type.  q and q_out, or k and v, may be None;
     norms: float32 [head_dim] or None."""
-    import torch
-    first = q if q is not None else k
-    f32 = first is not None and first.dtype == torch.float32
-    t = torch.float32 if f32 else c._dtype
-    args = []
-    for x, heads, dtype, what in ((q, c._heads, t, "q"), (k, c._kv_heads, t, "k"), (v, c._kv_heads, t, "v"),
-                                  (q_out, c._heads, c._dtype, "q_out")):
-        args.append(None if x is None else ctypes.byref(_paged_rows(x, heads, batch, c, dtype, what)))
-    _paged_check(load_library().fm_paged_write(c, layer, _paged_of(c, batch), args[0], args[1], args[2],
-                                               FM_DTYPE_F32 if f32 else c._code, _paged_norm(q_norm, c, "q_norm"),
-                                               _paged_norm(k_norm, c, "k_norm"), args[3], _stream(stream)), c)
+    if batch.cache is not c:
+        raise ValueError("the batch was made for another cache")
+    first, n = q if q is not None else k, batch.n_tokens
+    t = c._f32 if first is not None and first.dtype is c._f32 else c._dtype
+    q_ = None if q is None else _paged_rows(q, c._heads, n, c, t, "q")
+    k_ = None if k is None else _paged_rows(k, c._kv_heads, n, c, t, "k")
+    v_ = None if v is None else _paged_rows(v, c._kv_heads, n, c, t, "v")
+    o_ = None if q_out is None else _paged_rows(q_out, c._heads, n, c, c._dtype, "q_out")
+    _paged_check(_lib.fm_paged_write(
+        c, layer, batch.at, None if q_ is None else _addr(q_), None if k_ is None else _addr(k_), None if v_ is None else _addr(v_),
+        FM_DTYPE_F32 if t is c._f32 else c._code, _paged_norm(q_norm, c, "q_norm"), _paged_norm(k_norm, c, "k_norm"),
+        None if o_ is None else _addr(o_), _stream(stream)), c)
 
 
 def fm_paged_attend(c, layer: int, batch: PagedBatch, q, out, scale: Optional[float] = None, causal: bool = True, window: int = 0,
@@ -886,21 +883,27 @@ def fm_paged_attend(c, layer: int, batch: PagedBatch, q, out, scale: Optional[fl
     scale: 1 / sqrt(head_dim) unless given; window: rows a row sees back from its own (0: all), and the first `sinks` rows
     besides.  workspace: a CUDA uint8 tensor of at least batch.workspace_bytes that nothing else uses until the call is done;
     one is allocated in the call's stream (or the graph's pool) unless given."""
+    if batch.cache is not c:
+        raise ValueError("the batch was made for another cache")
+    size = batch.workspace_bytes
     if workspace is None:
-        import torch
         if stream is None:
-            workspace = torch.empty(batch.workspace_bytes, dtype=torch.uint8, device=q.device)
+            workspace = c._workspace(size)
         else:
+            import torch
             other = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream), device=q.device)
             with torch.cuda.stream(other):
-                workspace = torch.empty(batch.workspace_bytes, dtype=torch.uint8, device=q.device)
+                workspace = c._workspace(size)
     elif workspace.get_device() != c._device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on cuda:{c._device}")
-    qr = _paged_rows(q, c._heads, batch, c, c._dtype, "q")
-    o = _paged_rows(out, c._heads, batch, c, c._dtype, "out")
-    _paged_check(load_library().fm_paged_attend(
-        c, layer, _paged_of(c, batch), ctypes.byref(qr), ctypes.byref(o), c._head_dim ** -0.5 if scale is None else scale,
-        1 if causal else 0, window, sinks, workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream)), c)
+    else:
+        size = workspace.nbytes
+    n = batch.n_tokens
+    q_ = _paged_rows(q, c._heads, n, c, c._dtype, "q")
+    o_ = _paged_rows(out, c._heads, n, c, c._dtype, "out")
+    _paged_check(_lib.fm_paged_attend(
+        c, layer, batch.at, _addr(q_), _addr(o_), c._head_dim ** -0.5 if scale is None else scale, 1 if causal else 0, window, sinks,
+        workspace.data_ptr(), size, _stream(stream)), c)
 
 
 def fm_paged_workspace_bytes(c, max_new: int) -> int:
