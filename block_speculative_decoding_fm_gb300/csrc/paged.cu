@@ -180,7 +180,8 @@ fm_status check_call(const fm_paged *c, int layer, const fm_paged_batch *b, Page
                    (long long)b->table_ld, b->table_pages);
   }
   *out = {b->starts, b->lengths, b->table, b->table_ld, b->n_seqs, b->n_tokens, b->table_pages, c->page_log, g.n_pages,
-          layer * g.n_pages, g.n_kv_heads, g.n_heads / g.n_kv_heads, c->dev_err};
+          layer * g.n_pages, g.n_kv_heads, g.n_heads / g.n_kv_heads, 128 / (g.n_heads / g.n_kv_heads),
+          65536u / (uint32_t)(g.n_heads / g.n_kv_heads) + 1, c->dev_err};
   return FM_OK;
 }
 

@@ -31,6 +31,8 @@ struct PagedBatch {
   int32_t n_pages;          // of a layer
   int32_t page0;            // the layer's first page, counted over the pool
   int32_t n_kv, group;
+  int32_t tile_tokens;      // whole tokens of a 128-row tile
+  uint32_t group_inv;       // r / group = r group_inv / 2^16 for r < 128
   int32_t *err;             // [0] a bounded wait gave up, [1] the batch points outside the cache
 };
 

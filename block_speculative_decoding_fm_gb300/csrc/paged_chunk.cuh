@@ -135,7 +135,6 @@ __global__ void __launch_bounds__(ChunkCfg<HD, NT>::kThreads, 1)
   PagedStart *start = reinterpret_cast<PagedStart *>(sh + C::kSums);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   PagedWarp<typename C::Walk> &w = reinterpret_cast<PagedWarp<typename C::Walk> *>(start + 1)[warp];
-  const PagedSeg &g = w.g;
   const PagedBatch &b = a.b;
 
   pdl_trigger();
@@ -167,8 +166,8 @@ __global__ void __launch_bounds__(ChunkCfg<HD, NT>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = lds32(tslot);
-  w.init(*start, b.group, lane);
-  const int tt = Tiles::tokens(b.group);
+  w.init(*start, b, lane);
+  const int tt = b.tile_tokens;
   // query rows of tile t of the segment's unit
   auto rows_of = [&](const PagedSeg &s, int t) {
     return max(0, min(tt, s.q.n_new - (s.tile * NT + t) * tt)) * b.group;
@@ -183,6 +182,7 @@ __global__ void __launch_bounds__(ChunkCfg<HD, NT>::kThreads, 1)
     uint32_t c = 0, segs = 0;
     bool ok = true;
     while (ok && w.next(a, lane)) {
+      const PagedSeg &g = w.seg();
       const int n = g.end - g.begin, nt = NT == 2 && rows_of(g, 1) > 0 ? 2 : 1;
       // where this lane's rows of a key tile lie
       auto row_of = [&](int j) {
@@ -234,6 +234,7 @@ __global__ void __launch_bounds__(ChunkCfg<HD, NT>::kThreads, 1)
     uint32_t np[2] = {0, 0}, nv = 0;           // weights taken from each score buffer, masked tiles behind
     bool ok = true;
     while (ok && w.next(a, lane)) {
+      const PagedSeg &g = w.seg();
       const PagedSpan span = g.s;
       const int n = g.end - g.begin, begin = g.begin, nt = NT == 2 && rows_of(g, 1) > 0 ? 2 : 1;
       auto stage = [&](int pos) { return ring + ((c0 + pos) % C::kStages) * C::kStage; };
@@ -331,6 +332,7 @@ __global__ void __launch_bounds__(ChunkCfg<HD, NT>::kThreads, 1)
     uint32_t c0 = 0, segs = 0, nv = 0;
     bool ok = true;
     while (ok && w.next(a, lane)) {
+      const PagedSeg &g = w.seg();
       const int n = g.end - g.begin;
       for (int j = 0; ok && j < n; ++j) {
         if (!paged_masked<kChunkKeys>(a, g.s, g.s.tile(g.begin + j) * kChunkKeys)) continue;
@@ -372,8 +374,9 @@ __global__ void __launch_bounds__(ChunkCfg<HD, NT>::kThreads, 1)
     bool ok = true;
     if (threadIdx.x == 128) a.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
     while (w.next(a, lane)) {
+      const PagedSeg &g = w.seg();
       const int n = g.end - g.begin;
-      const int rows = rows_of(g, t), token = (g.tile * NT + t) * tt + in / b.group;
+      const int rows = rows_of(g, t), token = (g.tile * NT + t) * tt + (int)(in * b.group_inv >> 16);
       if (threadIdx.x == 128 && g.begin == 0 && !g.whole()) a.desc[blockIdx.x] = make_int4(g.seq, g.head, g.tile, w.walk.parts(g));
       if (rows == 0) {                          // (the unit has no second tile)
         c0 += 2 * n * C::kSub;
@@ -473,20 +476,22 @@ __global__ void __launch_bounds__(ChunkCfg<HD, NT>::kThreads, 1)
       f2_get(f2_add(sum[0], sum[1]), l, l2);
       l += l2;
       const int last = NT == 2 ? t : (tiles + n - 1) & 1;
+      const bool starts = g.begin == 0, whole = g.whole();
+      if (lane == 0) w.look(a);                 // (while the last product runs)
       if (ok) ok = paged_wait_warp(pvdone(last), (NT == 2 ? npv++ : ns[last] - 1) & 1, b.err);
       if (NT == 2 && frees && ok) mbar_arrive(empty(c0 + C::vpos(n - 1, n)));
       tc_fence_after();
       if (ok && active) {
-        const bool valid = in < rows, whole = g.whole();
+        const bool valid = in < rows;
         const bool bad = reinterpret_cast<volatile int *>(poison)[segs & 3] == (int)segs + 1;
-        const size_t slot = 2 * (size_t)blockIdx.x + (g.begin == 0 ? 1 : 0);
+        const size_t slot = 2 * (size_t)blockIdx.x + (starts ? 1 : 0);
         const float inv = l == 0.f ? 0.f : 1.f / l;
         // a quad of lanes writes 64 bytes of its four rows, one after another
         int64_t at[4];
         bool there[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int r = (in & ~3) + i, tk = r / b.group;
+          const int r = (in & ~3) + i, tk = r * b.group_inv >> 16;
           there[i] = r < rows;
           at[i] = (int64_t)(g.q.s0 + (g.tile * NT + t) * tt + tk) * a.out.ld + (int64_t)(g.head * b.group + r - tk * b.group) * a.out.hs +
                   8 * (lane & 3);

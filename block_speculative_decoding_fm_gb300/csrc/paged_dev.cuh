@@ -172,18 +172,17 @@ __device__ __forceinline__ int paged_row(const PagedAttnArgs &a, const PagedSpan
 template <int kRows, bool kFlat>
 struct PagedTiles {
   static constexpr int kSub = kFlat ? 1 : kRows / 128;
-  static __device__ __forceinline__ int tokens(int group) { return 128 / group; }   // of a 128-row tile
-  static __device__ __forceinline__ int count(const PagedSeq &q, int group) {
-    if (kFlat) return (q.n_new * group + kRows - 1) / kRows;
-    const int t = kSub * tokens(group);
+  static __device__ __forceinline__ int count(const PagedSeq &q, const PagedBatch &b) {
+    if (kFlat) return (q.n_new * b.group + kRows - 1) / kRows;
+    const int t = kSub * b.tile_tokens;
     return (q.n_new + t - 1) / t;
   }
-  static __device__ __forceinline__ int first(int tile, int group) {
-    return kFlat ? tile * kRows / group : tile * kSub * tokens(group);
+  static __device__ __forceinline__ int first(int tile, const PagedBatch &b) {
+    return kFlat ? tile * kRows / b.group : tile * kSub * b.tile_tokens;
   }
-  static __device__ __forceinline__ int last(const PagedSeq &q, int tile, int group) {
-    if (kFlat) return (min(q.n_new * group, (tile + 1) * kRows) - 1) / group;
-    return min(q.n_new, (tile + 1) * kSub * tokens(group)) - 1;
+  static __device__ __forceinline__ int last(const PagedSeq &q, int tile, const PagedBatch &b) {
+    if (kFlat) return (min(q.n_new * b.group, (tile + 1) * kRows) - 1) / b.group;
+    return min(q.n_new, (tile + 1) * kSub * b.tile_tokens) - 1;
   }
 };
 
@@ -211,10 +210,10 @@ struct PagedWalk {
   PagedSeq q;
   bool loaded;
 
-  __device__ __forceinline__ void init(const PagedStart &p, int group) {
+  __device__ __forceinline__ void init(const PagedStart &p, const PagedBatch &b) {
     left = p.left, share = p.share, seq = p.seq, head = p.head, tile = p.tile, off = p.off;
     q = p.q;
-    tiles = left > 0 ? Tiles::count(q, group) : 0;
+    tiles = left > 0 ? Tiles::count(q, b) : 0;
     loaded = true;
   }
   // The CTAs that the unit of a segment with begin == 0 is cut into: this share ended with the segment, the rest of the
@@ -227,7 +226,7 @@ struct PagedWalk {
     while (left > 0 && seq < b.n_seqs) {
       if (!loaded) {
         q = paged_seq(b, seq);
-        tiles = Tiles::count(q, b.group);
+        tiles = Tiles::count(q, b);
         loaded = true;
       }
       if (tiles == 0) {
@@ -237,7 +236,7 @@ struct PagedWalk {
       }
       g.q = q;
       g.seq = seq, g.head = head, g.tile = tile;
-      g.s = paged_span<kTile>(a, q, Tiles::first(tile, b.group), Tiles::last(q, tile, b.group));
+      g.s = paged_span<kTile>(a, q, Tiles::first(tile, b), Tiles::last(q, tile, b));
       const int total = g.s.n + kCost;
       const int take = (int)min((long long)(total - off), left);
       g.begin = max(0, off - kCost);
@@ -261,23 +260,39 @@ struct PagedWalk {
   }
 };
 
-// A warp's walk and present segment, in shared memory: the tile loops need the registers.
+// A warp's walk and its present segment, in shared memory: the tile loops need the registers.  The next segment may be worked
+// out ahead (look), while something else is waited for: finding it takes one thread 1,300 cycles.
 template <class Walk>
 struct PagedWarp {
   Walk walk;
-  PagedSeg g;
-  int more;
-  __device__ __forceinline__ void init(const PagedStart &p, int group, int lane) {
-    if (lane == 0) walk.init(p, group);
+  PagedSeg g[2];
+  int more, at;
+  bool ahead;
+  __device__ __forceinline__ void init(const PagedStart &p, const PagedBatch &b, int lane) {
+    if (lane == 0) {
+      walk.init(p, b);
+      at = 1;
+      ahead = false;
+    }
+  }
+  // by one thread
+  __device__ __forceinline__ void look(const PagedAttnArgs &a) {
+    more = walk.next(a, g[at ^ 1]);
+    ahead = true;
+  }
+  __device__ __forceinline__ bool step(const PagedAttnArgs &a) {
+    if (!ahead) look(a);
+    ahead = false;
+    at ^= 1;
+    return more != 0;
   }
   __device__ __forceinline__ bool next(const PagedAttnArgs &a, int lane) {
     __syncwarp();
-    int more = 0;
-    if (lane == 0) more = walk.next(a, g);
-    more = __shfl_sync(0xffffffffu, more, 0);
+    if (lane == 0) step(a);
     __syncwarp();
     return more != 0;
   }
+  __device__ __forceinline__ const PagedSeg &seg() const { return g[at]; }
 };
 
 // Adds up the launch's places and finds where this CTA's share begins.  Every thread of the CTA calls it; sh: a
@@ -290,12 +305,12 @@ __device__ __forceinline__ void paged_plan(const PagedAttnArgs &a, long long *sh
   constexpr int kWarps = kThreads / 32;
   // places of one KV head of a sequence; sequences of many tiles are summed by the whole warp
   auto one = [&](const PagedSeq &q, int i) -> int {
-    return paged_span<kTile>(a, q, Tiles::first(i, b.group), Tiles::last(q, i, b.group)).n + kCost;
+    return paged_span<kTile>(a, q, Tiles::first(i, b), Tiles::last(q, i, b)).n + kCost;
   };
   auto cost = [&](int i, PagedSeq &q) -> long long {
     q = {0, 0, 0};
     if (i < b.n_seqs) q = paged_seq(b, i);
-    const int nt = Tiles::count(q, b.group);
+    const int nt = Tiles::count(q, b);
     long long c = 0;
     if (nt <= 4)
       for (int j = 0; j < nt; ++j) c += one(q, j);
@@ -368,7 +383,7 @@ __device__ __forceinline__ void paged_plan(const PagedAttnArgs &a, long long *sh
       h.len = __shfl_sync(0xffffffffu, q.len, src);
       const long long rest = __shfl_sync(0xffffffffu, from - begin, src), of = __shfl_sync(0xffffffffu, mine, src) / b.n_kv;
       const int head = (rest >> 31) || (of >> 31) ? (int)(rest / of) : (int)((uint32_t)rest / (uint32_t)of);
-      const int nt = Tiles::count(h, b.group);
+      const int nt = Tiles::count(h, b);
       long long in = rest - head * of;
       for (int j0 = 0; j0 < nt; j0 += 32) {
         const int j = j0 + lane;
@@ -421,11 +436,11 @@ __device__ __noinline__ float paged_poison(const PagedAttnArgs &a, const PagedSe
   return sum;
 }
 
-// Where column d of a row of a part lies: 8 columns of every row together, so that threads a row each write next to
+// Where column d of a row of a part lies: 4 columns of every row together, so that threads a row each write and read next to
 // one another.
 template <int HD, int kRows>
 __device__ __forceinline__ float *paged_part(const PagedAttnArgs &a, size_t slot, int row, int d) {
-  return a.part_o + ((slot * (HD / 8) + (d >> 3)) * kRows + row) * 8 + (d & 7);
+  return a.part_o + ((slot * (HD / 4) + (d >> 2)) * kRows + row) * 4 + (d & 3);
 }
 
 // Joins the parts of the units that were cut.  Blocks take the CTAs' cut units in turn (x), 64 columns each (y), and rows in
@@ -458,9 +473,9 @@ __global__ void __launch_bounds__(kJoinThreads) fm_paged_join_kernel(const __gri
         head = f - token * group;
         valid = f < q.n_new * group;
       } else {
-        const int tt = Tiles::tokens(group), in = row & 127;
-        token = (d.z * Tiles::kSub + (row >> 7)) * tt + in / group;
-        head = in % group;
+        const int tt = a.b.tile_tokens, in = row & 127, tk = in * a.b.group_inv >> 16;
+        token = (d.z * Tiles::kSub + (row >> 7)) * tt + tk;
+        head = in - tk * group;
         valid = in < tt * group && token < q.n_new;
       }
       // one pass with the running maximum, kAhead parts in flight
@@ -477,10 +492,10 @@ __global__ void __launch_bounds__(kJoinThreads) fm_paged_join_kernel(const __gri
             const int p = p0 + u * kSplit;
             ml[u] = make_float2(-INFINITY, 0.f);
             if (p < d.w) {
-              const float4 *src = reinterpret_cast<const float4 *>(paged_part<HD, kRows>(a, slot(p), row, blockIdx.y * 64 + 8 * c));
+              const int d0 = blockIdx.y * 64 + 8 * c;
               ml[u] = __ldcg(a.part_ml + slot(p) * kRows + row);
-              x[u][0] = __ldcg(src);
-              x[u][1] = __ldcg(src + 1);
+              x[u][0] = __ldcg(reinterpret_cast<const float4 *>(paged_part<HD, kRows>(a, slot(p), row, d0)));
+              x[u][1] = __ldcg(reinterpret_cast<const float4 *>(paged_part<HD, kRows>(a, slot(p), row, d0 + 4)));
             }
           }
           float t = top;

@@ -45,7 +45,7 @@ struct RowsCfg {
   static constexpr int kStages = HD == 64 ? 4 : 3;
   static constexpr int kCtas = HD == 64 ? 3 : HD == 128 ? 2 : 1;          // an SM holds
   static constexpr int kMerge = 2 * kRowsUnit * HD * 4;
-  static constexpr int kSmem = kStages * kStage + kMerge + 4 * kRowsUnit * 8 + 16 * kStages + 64 + sizeof(PagedStart) + 16 + 2 * sizeof(PagedWarp<Walk>);
+  static constexpr int kSmem = kStages * kStage + kMerge + 4 * kRowsUnit * 8 + 16 * kStages + 16 + 2 * sizeof(PagedWarp<Walk>);
   static_assert(kCtas * (kSmem + 1024) <= 228 * 1024, "shared memory of an SM");
 };
 
@@ -62,12 +62,12 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<HD>::kCtas)
   const uint32_t bars = smem_u32(ml + 4 * kRowsUnit);
   auto full = [&](int s) { return bars + 8 * s; };
   auto empty = [&](int s) { return bars + 8 * (C::kStages + s); };
-  long long *sh = reinterpret_cast<long long *>(gbase + (bars - base) + 16 * C::kStages);   // [8]
+  // (the plan's, read before the first stage is there; the sums' memory afterwards)
+  long long *sh = reinterpret_cast<long long *>(ml);                                         // [8]
   PagedStart *start = reinterpret_cast<PagedStart *>(sh + 8);
-  int *poison = reinterpret_cast<int *>(start + 1);
+  int *poison = reinterpret_cast<int *>(gbase + (bars - base) + 16 * C::kStages);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   PagedWarp<typename C::Walk> &w = reinterpret_cast<PagedWarp<typename C::Walk> *>(poison + 4)[warp < 4 ? 0 : 1];   // (one for the four)
-  const PagedSeg &g = w.g;
   const PagedBatch &b = a.b;
 
   pdl_trigger();
@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<HD>::kCtas)
   }
   pdl_wait();
   paged_plan<kRowsUnit, true, kRowsKeys, kRowsCost, kRowsLeast, kRowsThreads>(a, sh, start);
-  if (warp == 0 || warp == 4) w.init(*start, b.group, lane);
+  if (warp == 0 || warp == 4) w.init(*start, b, lane);
 
   if (warp == 4) {
     // ---- fetch: a lane a (page box, panel) ----
@@ -93,6 +93,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<HD>::kCtas)
     uint32_t c = 0;                               // stages asked for
     bool ok = true;
     while (ok && w.next(a, lane)) {
+      const PagedSeg &g = w.seg();
       auto row_of = [&](int i) { return mine ? paged_row(a, g.s, g.seq, g.head, g.s.tile(i) * kRowsKeys + (box << box_log)) : 0; };
       int row = row_of(g.begin), next = g.begin + 1 < g.end ? row_of(g.begin + 1) : 0;
       for (int i = g.begin; i < g.end; ++i) {
@@ -127,9 +128,10 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<HD>::kCtas)
   bool ok = true;
   if (threadIdx.x == 0) a.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
   for (;;) {
-    if (threadIdx.x == 0) w.more = w.walk.next(a, w.g);
+    if (threadIdx.x == 0) w.step(a);
     named_sync(1, 128);
     if (!w.more) break;
+    const PagedSeg &g = w.seg();
     const int r0 = g.tile * kRowsUnit, rows = min(kRowsUnit, g.q.n_new * b.group - r0);
     const int pos0 = g.q.len - g.q.n_new;
     int tok[2];
@@ -301,9 +303,8 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<HD>::kCtas)
             make_uint4(pack2<BF16>(v[0] * inv, v[1] * inv), pack2<BF16>(v[2] * inv, v[3] * inv),
                        pack2<BF16>(v[4] * inv, v[5] * inv), pack2<BF16>(v[6] * inv, v[7] * inv));
       } else {
-        float4 *po = reinterpret_cast<float4 *>(paged_part<HD, kRowsUnit>(a, slot, row, d));
-        po[0] = make_float4(v[0], v[1], v[2], v[3]);
-        po[1] = make_float4(v[4], v[5], v[6], v[7]);
+        *reinterpret_cast<float4 *>(paged_part<HD, kRowsUnit>(a, slot, row, d)) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4 *>(paged_part<HD, kRowsUnit>(a, slot, row, d + 4)) = make_float4(v[4], v[5], v[6], v[7]);
         if (d == 0) a.part_ml[slot * kRowsUnit + row] = make_float2(mt == -INFINITY ? mt : mt * a.scale_log2, lt);
       }
     }
