@@ -226,7 +226,8 @@ __global__ void __launch_bounds__(ChunkCfg<HD, NT>::kThreads, 1)
   } else if (warp == 1) {
     // A product takes the tensor pipe 64 cycles and this warp 36 to issue; the pipe holds eight.  A wait costs 90 cycles and a
     // commit 100 even where nothing is waited for, so there are few: key tiles are waited for while products are queued, and
-    // the ring's stages are given back by the warps that see the scores behind them.  (Two threads that issue, one a query
+    // with two query tiles the ring's stages are given back by the warps that see the scores behind them (with one, whose
+    // ring holds little more than a tile of head dim 256, at once).  (Two threads that issue, one a query
     // tile, cost less each, but the tiles then run in step and weights and products take turns: 585 us for 454.)
     constexpr uint32_t IS = umma_idesc(128, kChunkKeys, BF16);
     constexpr uint32_t IO = umma_idesc(128, C::kDims, BF16) | (1u << 16);   // V with its dims contiguous
@@ -244,6 +245,10 @@ __global__ void __launch_bounds__(ChunkCfg<HD, NT>::kThreads, 1)
           const uint32_t c = c0 + pos * C::kSub + s;
           ok = ok && paged_wait_warp(full(c), phase(c), b.err);
         }
+      };
+      auto free_stage = [&](int pos) {
+#pragma unroll
+        for (int s = 0; s < C::kSub; ++s) umma_commit_elect(empty(c0 + pos * C::kSub + s));
       };
       // scores of query tile t against key tile j into buffer s
       auto scores = [&](int t, int j, int s) {
@@ -283,10 +288,12 @@ __global__ void __launch_bounds__(ChunkCfg<HD, NT>::kThreads, 1)
         for (int t = 0; t < nt; ++t) scores(t, 0, t);
       } else {
         scores(0, 0, tiles & 1);
+        free_stage(C::kpos(0, n));
         if (n > 1) {
           wait_stage(C::kpos(1, n));
           if (!ok) break;
           scores(0, 1, (tiles + 1) & 1);
+          free_stage(C::kpos(1, n));
         }
       }
       for (int j = 0; ok && j < n; ++j) {
@@ -311,12 +318,12 @@ __global__ void __launch_bounds__(ChunkCfg<HD, NT>::kThreads, 1)
           tc_fence_after();
           product(0, j, s);
           umma_commit_elect(pvdone(s));
-#pragma unroll
-          for (int sub = 0; sub < C::kSub; ++sub) umma_commit_elect(empty(c0 + C::vpos(j, n) * C::kSub + sub));
+          free_stage(C::vpos(j, n));
           if (j + 2 < n) {                     // (the ring may not hold it before V is free)
             wait_stage(C::kpos(j + 2, n));
             if (!ok) break;
             scores(0, j + 2, s);
+            free_stage(C::kpos(j + 2, n));
           }
         }
       }
@@ -397,8 +404,7 @@ __global__ void __launch_bounds__(ChunkCfg<HD, NT>::kThreads, 1)
         ++ns[s];
         if (frees && ok) {
           if (NT == 2 && j > 0) mbar_arrive(empty(c0 + C::vpos(j - 1, n)));
-#pragma unroll
-          for (int sub = 0; sub < C::kSub; ++sub) mbar_arrive(empty(c0 + C::kpos(j, n) * C::kSub + sub));
+          if (NT == 2) mbar_arrive(empty(c0 + C::kpos(j, n)));
           if (j == n - 1) mbar_arrive(qfree);
         }
         if (ok && active) {

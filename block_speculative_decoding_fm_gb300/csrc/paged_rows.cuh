@@ -34,8 +34,8 @@ __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uin
 
 constexpr int kRowsUnit = 16;      // query rows a unit
 constexpr int kRowsKeys = 64;      // keys a stage
-constexpr int kRowsCost = 3;       // a unit's own cost in stages (queries, first fetch, outputs)
-constexpr int kRowsLeast = 6;      // places a share has at least
+constexpr int kRowsCost = 4;       // a unit's own cost in stages (queries, first fetch, outputs)
+constexpr int kRowsLeast = 5;      // places a share has at least
 constexpr int kRowsThreads = 160;
 
 template <int HD>
