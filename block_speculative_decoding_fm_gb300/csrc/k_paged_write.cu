@@ -102,24 +102,34 @@ __global__ void __launch_bounds__(kWThreads) fm_paged_write_kernel(const __grid_
   const bool turned = d0 < a.rot, low = gl < far;
   const int partner = (threadIdx.x & 31) + (turned && a.half ? (low ? far : -far) : 0);
   const float sign = low ? -1.f : 1.f;
-  for (int t = 0; t < n; ++t) {
-    if (!where[t].z) continue;
-    // this lane's (cos, sin): of its 8 pairs in the half layout, of its 4 otherwise
-    const float2 *cs = &turn[t][a.half ? (low ? gl : gl - far) * 8 : gl * 4];
-    const int64_t row = where[t].x;
-    for (int h = h0 + group, hw = h0 + (threadIdx.x & ~31) / kLanes; hw < h1; h += kGroups, hw += kGroups) {   // (warps go round together)
-      const bool live = h < h1;
-      const Head &hd = heads[live ? h - h0 : 0];
+  // (token, round of heads) one after another, the next rows asked for before these are worked on: a warp has two rows in flight
+  const int rounds = (h1 - h0 + kGroups - 1) / kGroups, steps = n * rounds;
+  uint4 raw[F32IN ? 2 : 1], next[F32IN ? 2 : 1];
+  auto ask = [&](int t, int i, uint4 *to) {
+    const int h = i * kGroups + group;
+    to[0] = make_uint4(0, 0, 0, 0);
+    if constexpr (F32IN) to[1] = to[0];
+    if (h < h1 - h0 && where[t].z) {
+      const uint4 *p = reinterpret_cast<const uint4 *>(heads[h].src + (int64_t)(t0 + t) * heads[h].src_ld) + gl * (F32IN ? 2 : 1);
+      to[0] = __ldcs(p);
+      if constexpr (F32IN) to[1] = __ldcs(p + 1);
+    }
+  };
+  if (steps > 0) ask(0, 0, next);
+  int t = 0, i = 0;
+  for (int step = 0; step < steps; ++step) {
+    raw[0] = next[0];
+    if constexpr (F32IN) raw[1] = next[1];
+    const int tn = i + 1 < rounds ? t : t + 1, in = i + 1 < rounds ? i + 1 : 0;
+    if (step + 1 < steps) ask(tn, in, next);
+    {
+      // this lane's (cos, sin): of its 8 pairs in the half layout, of its 4 otherwise
+      const float2 *cs = &turn[t][a.half ? (low ? gl : gl - far) * 8 : gl * 4];
+      const int64_t row = where[t].x;
+      const int h = i * kGroups + group;
+      const bool live = h < h1 - h0 && where[t].z;
+      const Head &hd = heads[h < h1 - h0 ? h : 0];
       const int kind = hd.kind;
-      uint4 raw[F32IN ? 2 : 1];
-      if (live) {
-        const uint4 *p = reinterpret_cast<const uint4 *>(hd.src + (int64_t)(t0 + t) * hd.src_ld) + gl * (F32IN ? 2 : 1);
-        raw[0] = __ldcs(p);
-        if constexpr (F32IN) raw[1] = __ldcs(p + 1);
-      } else {
-        raw[0] = make_uint4(0, 0, 0, 0);
-        if constexpr (F32IN) raw[1] = raw[0];
-      }
       uint4 y16 = raw[0];
       if (F32IN || !__all_sync(0xffffffffu, kind == 2)) {   // (V of the pool's type as it is)
         float x[8];
@@ -181,6 +191,7 @@ __global__ void __launch_bounds__(kWThreads) fm_paged_write_kernel(const __grid_
       if (live && (kind == 0 || row >= 0))              // (row < 0: the table has no page for it)
         *(reinterpret_cast<uint4 *>(hd.dst + (kind == 0 ? (int64_t)(t0 + t) : row) * hd.dst_ld) + gl) = y16;
     }
+    t = tn, i = in;
   }
 }
 

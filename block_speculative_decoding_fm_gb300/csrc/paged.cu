@@ -304,7 +304,7 @@ fm_status fm_paged_attend(fm_paged *c, int32_t layer, const fm_paged_batch *batc
   PTRY(check_call(c, layer, batch, &a.b));
   const fm_paged_config &g = c->cfg;
   if (!q || !out) return pfail(FM_ERR_INVALID_ARG, "null q or out");
-  if (!(scale > 0.f) || !std::isfinite(scale)) return pfail(FM_ERR_INVALID_ARG, "scale %g: positive", scale);
+  if (!(scale >= 1e-30f && scale <= 1e30f)) return pfail(FM_ERR_INVALID_ARG, "scale %g: 1e-30 to 1e30", scale);
   if (window < 0 || sinks < 0) return pfail(FM_ERR_INVALID_ARG, "window %d, sinks %d", window, sinks);
   if (window > 0 && !causal) return pfail(FM_ERR_INVALID_ARG, "a window without causal order");
   if (sinks > 0 && window == 0) return pfail(FM_ERR_INVALID_ARG, "sinks without a window");

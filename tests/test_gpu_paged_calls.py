@@ -320,6 +320,7 @@ def test_refusals():
     for call in (lambda: fm.fm_paged_attend(c, 1, b, q, out), lambda: fm.fm_paged_attend(c, -1, b, q, out),
                  lambda: fm.fm_paged_attend(c, 0, b, q, q), lambda: fm.fm_paged_attend(c, 0, b, q, out, scale=0.0),
                  lambda: fm.fm_paged_attend(c, 0, b, q, out, scale=float("nan")), lambda: fm.fm_paged_attend(c, 0, b, q, out, scale=-1.0),
+                 lambda: fm.fm_paged_attend(c, 0, b, q, out, scale=1e-38), lambda: fm.fm_paged_attend(c, 0, b, q, out, scale=float("inf")),
                  lambda: fm.fm_paged_attend(c, 0, b, q, out, window=-1), lambda: fm.fm_paged_attend(c, 0, b, q, out, sinks=1),
                  lambda: fm.fm_paged_attend(c, 0, b, q, out, causal=False, window=4), lambda: fm.fm_paged_attend(c, 0, b, q, out, window=4, sinks=-1),
                  lambda: fm.fm_paged_write(c, 0, b), lambda: fm.fm_paged_write(c, 0, b, q), lambda: fm.fm_paged_write(c, 0, b, None, k),
