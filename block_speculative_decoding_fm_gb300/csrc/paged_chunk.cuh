@@ -14,8 +14,13 @@
 // Products of one CTA run in the order they were issued, so a score buffer may be written behind the product that
 // reads the weights in it.
 //
-// Bound: 4 * 128 * 128 * head_dim flop a pair of tiles against 4 * 128 * head_dim bytes: the tensor pipe for chunks, memory
-// for a few tokens over a long cache.
+// P enters the second product rounded once to the pool's type, as paged_rows.cuh says; sums, outputs and references are f32.
+//
+// Bound: 4 * 128 * 128 * head_dim flop a query and a key tile against 4 * 128 * head_dim bytes: the tensor pipe for chunks, memory
+// for a few tokens over a long cache.  Measured: 2,048 rows over 34,816 of 16 x 128 bf16 404 us (1.40 PFLOP/s, 0.72 of the measured
+// bf16 rate, tensor pipe 67 %); prompts of 33-4,001 rows of 24/4 x 256 807 us (1.02 PFLOP/s); 1-17 rows of 32 sequences of 16 x 128
+// over 512-8,192 in pages of 64 179 us (0.88 of the copy rate), of 16 207 us.  What is left: a tile's chain (scores, 890 cycles of
+// weights with a warp a scheduler, products) against 2,048 cycles of products a pair of tiles.
 #pragma once
 
 #include "paged_dev.cuh"
@@ -23,8 +28,10 @@
 namespace fm {
 
 constexpr int kChunkKeys = 128;    // keys a tile
-constexpr int kChunkCost = 2;      // a unit's own cost in tiles
-constexpr int kChunkLeast = 3;     // places a share has at least
+// A unit's own cost in tiles, and the places a share has at least.  (1 and 2: prompts of 24/4 x 256 846 us; 2 and 3: 811; 3 and 4:
+// 803, but eight rows over 4,161 21.0 us for 19.5 and prompts of 1,024 of 16 x 128 73.9 for 70.6.)
+constexpr int kChunkCost = 2;
+constexpr int kChunkLeast = 3;
 
 template <int HD, int NT>
 struct ChunkCfg {

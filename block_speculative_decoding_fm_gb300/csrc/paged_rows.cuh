@@ -34,8 +34,10 @@ __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uin
 
 constexpr int kRowsUnit = 16;      // query rows a unit
 constexpr int kRowsKeys = 64;      // keys a stage
-constexpr int kRowsCost = 4;       // a unit's own cost in stages (queries, first fetch, outputs)
-constexpr int kRowsLeast = 5;      // places a share has at least
+// A unit's own cost in stages (queries, first fetch, outputs), and the places a share has at least.  (3 and 6: 22.0 us for a
+// windowed token of 32 sequences, 97 us for 16 rows over 65,537; 4 and 5: 21.9 and 96.)
+constexpr int kRowsCost = 4;
+constexpr int kRowsLeast = 5;
 constexpr int kRowsThreads = 160;
 
 template <int HD>
