@@ -384,3 +384,22 @@ def test_devices():
     with torch.cuda.device(1):
         refused(INVALID, lambda: fm.fm_paged_attend(B.c, 0, B.b, q, torch.empty_like(q), workspace=torch.empty((B.b.workspace_bytes,), dtype=torch.uint8, device="cuda:0")))
         refused(INVALID, lambda: fm.fm_paged_synchronize(B.c))
+
+
+@pytest.mark.parametrize("heads,seqs", [((16, 1, 128), 50), ((8, 2, 64), 64), ((4, 6, 256), 64)])
+@pytest.mark.parametrize("new", [1, 2, 20])
+def test_stages_are_read_before_they_are_refilled(heads, seqs, new):
+    """Every SM's CTAs fetch at the memory's pace, so a stage is filled again as soon as it is given back: the same call gives
+    the same bits however the warps run, and the oracle's values."""
+    B = Batch([(1 + i % new, 1023 + i % 7) for i in range(seqs)], *heads, 64, TYPES["bf16"], seed=41).create().fill_rows()
+    q = B.queries()
+    first = torch.empty_like(q)
+    fm.fm_paged_attend(B.c, 0, B.b, q, first)
+    differs = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(100):
+        out = torch.full_like(q, 7.0)
+        fm.fm_paged_attend(B.c, 0, B.b, q, out)
+        differs += (out != first).any()
+    fm.fm_paged_synchronize(B.c)
+    assert int(differs) == 0
+    check_attend(B, q, first)
