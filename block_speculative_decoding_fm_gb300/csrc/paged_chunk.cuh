@@ -18,7 +18,7 @@
 //
 // Bound: 4 * 128 * 128 * head_dim flop a query and a key tile against 4 * 128 * head_dim bytes: the tensor pipe for chunks, memory
 // for a few tokens over a long cache.  Measured: 2,048 rows over 34,816 of 16 x 128 bf16 404 us (1.40 PFLOP/s, 0.72 of the measured
-// bf16 rate, tensor pipe 67 %); prompts of 33-4,001 rows of 24/4 x 256 807 us (1.02 PFLOP/s); 1-17 rows of 32 sequences of 16 x 128
+// bf16 rate, tensor pipe 67 %); prompts of 33-4,001 rows of 24/4 x 256 788 us (1.04 PFLOP/s); 1-17 rows of 32 sequences of 16 x 128
 // over 512-8,192 in pages of 64 179 us (0.88 of the copy rate), of 16 207 us.  What is left: a tile's chain (scores, 890 cycles of
 // weights with a warp a scheduler, products) against 2,048 cycles of products a pair of tiles.
 #pragma once
@@ -95,9 +95,15 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 
 // The bits below bit n.
 __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
-// Bits 15 and 31 say whether the word's halves are infinite or NaN (an exponent of ones is carried into the sign's place).
+// 0 x w + sum in both halves: a sum stays 0 until a half of w is infinite or NaN.
 template <bool BF16>
-__device__ __forceinline__ uint32_t above(uint32_t w) { return (w & 0x7fff7fffu) + (BF16 ? 0x00800080u : 0x04000400u); }
+__device__ __forceinline__ uint32_t none(uint32_t w, uint32_t sum) {
+  if constexpr (BF16)
+    asm("fma.rn.bf16x2 %0, %1, %2, %0;\n" : "+r"(sum) : "r"(w), "r"(0));
+  else
+    asm("fma.rn.f16x2 %0, %1, %2, %0;\n" : "+r"(sum) : "r"(w), "r"(0));
+  return sum;
+}
 // Four lanes' 16-byte pieces, transposed: lane q had pieces 0 .. 3 of its row, and has piece q of the four lanes' rows.
 __device__ __forceinline__ void transpose4(uint4 (&v)[4], int lane) {
   auto swap = [&](uint4 &x, uint4 &y, int step, bool upper) {   // y of the lower lane for x of the upper one
@@ -343,6 +349,9 @@ __global__ void __launch_bounds__(ChunkCfg<HD, NT>::kThreads, 1)
   } else if (warp < 4) {
     // Masked tiles of V: infinities and NaN out of them (a weight of 0 times one would be NaN), while the scores become
     // weights.  (The ring's own barriers cannot be waited on here: they may be a whole turn behind.)
+    // A word is one fused multiply-add, four sums at a time; the loop is short because it runs once or twice a unit, from
+    // instructions that have left the caches since (exponents compared by three integer operations a word and both
+    // halves of head dim 256 unrolled: 153 us for the windowed chunk of 8,191 rows, 145 so).
     uint32_t c0 = 0, segs = 0, nv = 0;
     bool ok = true;
     while (ok && w.next(a, lane)) {
@@ -352,16 +361,17 @@ __global__ void __launch_bounds__(ChunkCfg<HD, NT>::kThreads, 1)
         if (!paged_masked<kChunkKeys>(a, g.s, g.s.tile(g.begin + j) * kChunkKeys)) continue;
         ok = paged_wait_warp(vready, nv++ & 1, b.err);
         if (!ok) break;
-#pragma unroll
+#pragma unroll 1
         for (int sub = 0; sub < C::kSub; ++sub) {
           const uint32_t vt = ring + ((c0 + C::vpos(j, n) * C::kSub + sub) % C::kStages) * C::kStage + ((warp & 1) * 32 + lane) * 16;
-          uint32_t found = 0;
-#pragma unroll 8
+          uint4 sum = make_uint4(0, 0, 0, 0);
+#pragma unroll 4
           for (int u = 0; u < C::kStage; u += 64 * 16) {
             const uint4 x = lds128(vt + u);
-            found |= above<BF16>(x.x) | above<BF16>(x.y) | above<BF16>(x.z) | above<BF16>(x.w);
+            sum = make_uint4(none<BF16>(x.x, sum.x), none<BF16>(x.y, sum.y), none<BF16>(x.z, sum.z), none<BF16>(x.w, sum.w));
           }
-          if (found & 0x80008000u) {
+          if ((sum.x | sum.y | sum.z | sum.w) & 0x7fff7fffu) {
+#pragma unroll 1
             for (int u = 0; u < C::kStage; u += 64 * 16) {
               const uint4 x = lds128(vt + u);
               asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};\n" ::"r"(vt + u), "r"(x.x & ~not_finite<BF16>(x.x)),
