@@ -18,7 +18,7 @@
 //
 // Bound: 4 * 128 * 128 * head_dim flop a query and a key tile against 4 * 128 * head_dim bytes: the tensor pipe for chunks, memory
 // for a few tokens over a long cache.  Measured: 2,048 rows over 34,816 of 16 x 128 bf16 404 us (1.40 PFLOP/s, 0.72 of the measured
-// bf16 rate, tensor pipe 67 %); prompts of 33-4,001 rows of 24/4 x 256 788 us (1.04 PFLOP/s); 1-17 rows of 32 sequences of 16 x 128
+// bf16 rate, tensor pipe 67 %); prompts of 33-4,001 rows of 24/4 x 256 792 us (1.03 PFLOP/s); 1-17 rows of 32 sequences of 16 x 128
 // over 512-8,192 in pages of 64 179 us (0.88 of the copy rate), of 16 207 us.  What is left: a tile's chain (scores, 890 cycles of
 // weights with a warp a scheduler, products) against 2,048 cycles of products a pair of tiles.
 #pragma once
@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(ChunkCfg<HD, NT>::kThreads, 1)
     // weights.  (The ring's own barriers cannot be waited on here: they may be a whole turn behind.)
     // A word is one fused multiply-add, four sums at a time; the loop is short because it runs once or twice a unit, from
     // instructions that have left the caches since (exponents compared by three integer operations a word and both
-    // halves of head dim 256 unrolled: 153 us for the windowed chunk of 8,191 rows, 145 so).
+    // halves of head dim 256 unrolled: 153 us for the windowed chunk of 8,191 rows, 146 so).
     uint32_t c0 = 0, segs = 0, nv = 0;
     bool ok = true;
     while (ok && w.next(a, lane)) {
