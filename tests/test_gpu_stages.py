@@ -5,6 +5,8 @@ from __future__ import annotations
 import numpy as np
 import pytest
 
+import fm_synth as S
+from gpu_common import REL_L2, Pair, rel_l2, tokens_match
 from oracle import kvq as Q
 from test_gpu_kvq import TYPES, built, check_out, rows  # noqa: F401
 from test_gpu_kvq_calls import shared_rows
@@ -34,3 +36,22 @@ def test_kvq_attention(hd, hkv, group, T, name):
         want, _, mass, reach = Q.attend_heads(qv[s * T:(s + 1) * T], c.k[0, s], c.v[0, s], hd ** -0.5)
         check_out(first[s * T:(s + 1) * T], want, mass, reach, hd, lens[s], name, c.v[0, s])
     c.fm.fm_kvq_destroy(c.c)
+
+
+@pytest.mark.parametrize("target_dim", [384, 512, 2560])
+def test_lm_head(target_dim):
+    """A Q8_0 table of several tiles a CTA: the same hidden rows, the same bits of the logits and the same tokens, and the
+    oracle's values."""
+    cfg = S.tiny_config(max_ctx=64).replace(lm_format=S.LM_Q8_0, target_dim=target_dim, vocab=40000)
+    p = Pair(cfg, 62)
+    p.append(0, S.gen_features(S.streams(62)["features"], 30, cfg.feat_dim), 0)
+    got, ref = p.draft(0, 123, 30)
+    first = p.logits()
+    for _ in range(20):
+        assert np.array_equal(p.logits(), first)
+    for _ in range(50):
+        again, _ = p.draft(0, 123, 30, oracle=False)
+        assert np.array_equal(again, got)
+    assert rel_l2(first, ref.logits) < REL_L2
+    assert tokens_match(got, ref.tokens, ref.logits) and np.array_equal(got, np.argmax(first, axis=-1))
+    p.close()
