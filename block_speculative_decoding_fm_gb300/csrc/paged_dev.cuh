@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(kJoinThreads) fm_paged_join_kernel(const __gri
           for (int e = 0; e < 8; ++e) o[e] *= f;
 #pragma unroll
           for (int u = 0; u < kAhead; ++u) {
-            if (ml[u].x == -INFINITY) continue;
+            if (ml[u].y == 0.f) continue;   // (no part, or no weight in it; one whose scores are all NaN has a sum of NaN)
             const float w = ex2(ml[u].x - t);
             l += w * ml[u].y;
             o[0] += w * x[u][0].x, o[1] += w * x[u][0].y, o[2] += w * x[u][0].z, o[3] += w * x[u][0].w;
@@ -536,7 +536,7 @@ __global__ void __launch_bounds__(kJoinThreads) fm_paged_join_kernel(const __gri
 #pragma unroll
           for (int u = 0; u < kSplit; ++u) {
             const float2 x = tl[u][at];
-            l += x.x == -INFINITY ? 0.f : ex2(x.x - t) * x.y;
+            l += x.y == 0.f ? 0.f : ex2(x.x - t) * x.y;
           }
 #pragma unroll
           for (int u = 1; u < kSplit; ++u)

@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<HD>::kCtas)
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         const float2 x = ml[w * kRowsUnit + row];
-        lt += x.x == -INFINITY ? 0.f : ex2((x.x - mt) * a.scale_log2) * x.y;
+        lt += x.y == 0.f ? 0.f : ex2((x.x - mt) * a.scale_log2) * x.y;   // (scores that are all NaN: a sum of NaN)
       }
       float v[8];
 #pragma unroll
