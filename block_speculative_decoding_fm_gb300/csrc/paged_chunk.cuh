@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(ChunkCfg<HD, NT>::kThreads, 1)
         const bool valid = in < rows;
         const bool bad = reinterpret_cast<volatile int *>(poison)[segs & 3] == (int)segs + 1;
         const size_t slot = 2 * (size_t)blockIdx.x + (starts ? 1 : 0);
-        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const float inv = paged_inv(a, g.q, pos, l);
         // a quad of lanes writes 64 bytes of its four rows, one after another
         int64_t at[4];
         bool there[4];

@@ -154,6 +154,13 @@ __device__ __forceinline__ bool paged_sees(const PagedAttnArgs &a, const PagedSe
   return j < q.len && (!a.causal || j <= pos) && (!a.window || j > pos - a.window || j < a.sinks);
 }
 
+// What a row's summed outputs are multiplied by: 1 / the sum of its weights.  Without weight are a row that sees nothing (zeros) and
+// one that sees only scores of minus infinity (0 / 0).
+__device__ __forceinline__ float paged_inv(const PagedAttnArgs &a, const PagedSeq &q, int pos, float l) {
+  if (l != 0.f) return 1.f / l;
+  return q.len > 0 && (!a.causal || pos >= 0) ? __int_as_float(0x7fc00000) : 0.f;
+}
+
 // Where row `row` of the sequence lies in the pool (a page the unit does not see, or one that the table has no
 // valid number for, reads as zeros): the tensor map's row.
 __device__ __forceinline__ int paged_row(const PagedAttnArgs &a, const PagedSpan &s, int seq, int head, int row) {
@@ -545,7 +552,7 @@ __global__ void __launch_bounds__(kJoinThreads) fm_paged_join_kernel(const __gri
         }
       }
       if (valid && sub == 0) {
-        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const float inv = paged_inv(a, q, q.len - q.n_new + token, l);
         uint16_t *out = static_cast<uint16_t *>(a.out.p) + (int64_t)(q.s0 + token) * a.out.ld +
                         (int64_t)(d.y * group + head) * a.out.hs + blockIdx.y * 64 + 8 * c;
         *reinterpret_cast<uint4 *>(out) = make_uint4(pack2<BF16>(o[0] * inv, o[1] * inv), pack2<BF16>(o[2] * inv, o[3] * inv),

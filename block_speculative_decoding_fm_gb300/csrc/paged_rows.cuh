@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<HD>::kCtas)
         for (int e = 0; e < 8; ++e) v[e] += paged_poison<kRowsKeys, BF16>(a, held, HD, pos0 + t, d + e);
       }
       if (whole) {
-        const float inv = lt == 0.f ? 0.f : 1.f / lt;
+        const float inv = paged_inv(a, g.q, pos0 + t, lt);
         uint16_t *out = static_cast<uint16_t *>(a.out.p) + (int64_t)(g.q.s0 + t) * a.out.ld +
                         (int64_t)(g.head * b.group + r - t * b.group) * a.out.hs + d;
         *reinterpret_cast<uint4 *>(out) =

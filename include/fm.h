@@ -831,7 +831,8 @@ FM_API fm_status fm_paged_write(fm_paged *c, int32_t layer, const fm_paged_batch
  * over KV head h / (n_heads / n_kv_heads) and the rows j < length that it sees:
  * all of them; with causal != 0 those with j <= p; with a window > 0 (causal
  * only) those of them with j > p - window, and the first `sinks` (those with
- * j <= p).  A row that sees nothing gives zeros.  q and out are of the pool's type and do not overlap
+ * j <= p).  A row that sees nothing gives zeros, one that sees only scores of minus
+ * infinity NaN (0 / 0).  q and out are of the pool's type and do not overlap
  * (out->data == q->data is refused); scale is 1e-30 to 1e30.
  * Scores, weights' sums and outputs are summed in f32; each weight is rounded
  * once to the pool's type where it multiplies v, the output once at the end.  A

@@ -43,3 +43,23 @@ def test_nan_keys(heads, new, past):
     got = attend(B, q)
     assert got[:new, :heads[1]].isnan().all()
     assert torch.equal(got[new:], want[new:]) and torch.equal(got[:, heads[1]:], want[:, heads[1]:])
+
+
+@pytest.mark.parametrize("t", ["f16", "bf16"])
+@pytest.mark.parametrize("heads,new,past", CUT + WHOLE)
+def test_scores_of_minus_infinity(heads, new, past, t):
+    """Keys whose scores are minus infinity have no weight, as those far below the others have none; a row that sees nothing
+    else is 0 / 0, and one that sees nothing stays zeros."""
+    B = Batch([(new, past), (new, -new)], *heads, 128, TYPES[t], seed=53).create().fill_rows()
+    q = B.queries().abs() + 0.5
+    few = past // 2
+    outs = []
+    for x in (float("-inf"), -30000.0):
+        for j in range(0, few, 128):
+            B.k_pool[0, int(B.table_np[0, j // 128]), :, :few - j] = x
+        outs.append(attend(B, q))
+    assert torch.equal(outs[0], outs[1]) and outs[0].isfinite().all() and (outs[0][new:] == 0).all()
+    for j in range(0, new + past, 128):
+        B.k_pool[0, int(B.table_np[0, j // 128])] = float("-inf")
+    got = attend(B, q)
+    assert got[:new].isnan().all() and (got[new:] == 0).all()
