@@ -371,15 +371,19 @@ __global__ void __launch_bounds__(ChunkCfg<HD, NT>::kThreads, 1)
             sum = make_uint4(none<BF16>(x.x, sum.x), none<BF16>(x.y, sum.y), none<BF16>(x.z, sum.z), none<BF16>(x.w, sum.w));
           }
           if ((sum.x | sum.y | sum.z | sum.w) & 0x7fff7fffu) {
+            const int key0 = g.s.tile(g.begin + j) * kChunkKeys;
 #pragma unroll 1
             for (int u = 0; u < C::kStage; u += 64 * 16) {
               const uint4 x = lds128(vt + u);
-              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};\n" ::"r"(vt + u), "r"(x.x & ~not_finite<BF16>(x.x)),
-                           "r"(x.y & ~not_finite<BF16>(x.y)), "r"(x.z & ~not_finite<BF16>(x.z)), "r"(x.w & ~not_finite<BF16>(x.w))
+              const uint4 f = make_uint4(not_finite<BF16>(x.x), not_finite<BF16>(x.y), not_finite<BF16>(x.z), not_finite<BF16>(x.w));
+              if (!(f.x | f.y | f.z | f.w)) continue;
+              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};\n" ::"r"(vt + u), "r"(x.x & ~f.x), "r"(x.y & ~f.y), "r"(x.z & ~f.z),
+                           "r"(x.w & ~f.w)
                            : "memory");
+              const int row = (((warp & 1) * 32 + lane) * 16 + u) / 128 % kChunkKeys;
+              if (paged_seen(a, g.s, key0 + row)) poison[segs & 3] = (int)segs + 1;
             }
             fence_proxy_async();
-            poison[segs & 3] = (int)segs + 1;
           }
         }
         mbar_arrive(vclean);

@@ -154,6 +154,11 @@ __device__ __forceinline__ bool paged_sees(const PagedAttnArgs &a, const PagedSe
   return j < q.len && (!a.causal || j <= pos) && (!a.window || j > pos - a.window || j < a.sinks);
 }
 
+// Whether some token of the unit sees row j.
+__device__ __forceinline__ bool paged_seen(const PagedAttnArgs &a, const PagedSpan &s, int j) {
+  return j < s.hi && (j >= s.lo || (a.window && j < a.sinks));
+}
+
 // What a row's summed outputs are multiplied by: 1 / the sum of its weights.  Without weight are a row that sees nothing (zeros) and
 // one that sees only scores of minus infinity (0 / 0).
 __device__ __forceinline__ float paged_inv(const PagedAttnArgs &a, const PagedSeq &q, int pos, float l) {
@@ -422,7 +427,7 @@ __device__ __forceinline__ void paged_plan(const PagedAttnArgs &a, long long *sh
 
 // The sum over the infinite and NaN values of V, column d, in masked tiles of the segment, that the token at `pos` sees
 // (each counted with weight 1, which gives the infinity or NaN that any positive weight would).  Only asked where the
-// segment met one: such values are taken out of the tile ahead of the product, where a weight of 0 would make NaN of them
+// segment met one in a row that some token of it sees: such values are taken out of the tile ahead of the product, where a weight of 0 would make NaN of them
 // for rows that do not see them.
 template <int kTile, bool BF16>
 __device__ __noinline__ float paged_poison(const PagedAttnArgs &a, const PagedSeg &g, int hd, int pos, int d) {

@@ -154,7 +154,6 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<HD>::kCtas)
 #pragma unroll
     for (int d = 0; d < HD / 8; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    bool bad = false;
     for (int i = g.begin; i < g.end; ++i, ++c) {
       const int st = c % C::kStages, key0 = g.s.tile(i) * kRowsKeys;
       const bool masked = paged_masked<kRowsKeys>(a, g.s, key0);
@@ -184,7 +183,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<HD>::kCtas)
                          "r"(x.z & ~n.z), "r"(x.w & ~n.w)
                          : "memory");
             fence_proxy_async();   // (the stage's next copy comes after this store)
-            bad = true;
+            if (paged_seen(a, g.s, key0 + 16 * warp + (u % 128) / 8)) *poison = 1;   // (read at the unit's end)
           }
         }
         __syncwarp();
@@ -237,7 +236,6 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<HD>::kCtas)
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
       if (c4 == 0) ml[warp * kRowsUnit + g8 + 8 * h] = make_float2(m[h], l[h]);
     }
-    if (bad) *poison = 1;
     named_sync(1, 128);
     const bool any_bad = *reinterpret_cast<volatile int *>(poison) != 0;
     float top[2];
