@@ -533,12 +533,10 @@ __global__ void __launch_bounds__(ChunkCfg<HD, NT>::kThreads, 1)
           if (bad) {
             if (valid) {
               const PagedSeg held = g;
-              for (int e = 0; e < 32; ++e) {
-                const float x = paged_poison<kChunkKeys, BF16>(a, held, HD, pos, c + e);
+              float more[32] = {};
+              paged_poison<kChunkKeys, BF16, 32>(a, held, HD, pos, c, more);
 #pragma unroll
-                for (int k = 0; k < 32; ++k)
-                  if (k == e) o[k] += x;
-              }
+              for (int e = 0; e < 32; ++e) o[e] += more[e];
             }
             __syncwarp();
           }

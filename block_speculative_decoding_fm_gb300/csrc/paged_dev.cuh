@@ -425,27 +425,39 @@ __device__ __forceinline__ void paged_plan(const PagedAttnArgs &a, long long *sh
   }
 }
 
-// The sum over the infinite and NaN values of V, column d, in masked tiles of the segment, that the token at `pos` sees
-// (each counted with weight 1, which gives the infinity or NaN that any positive weight would).  Only asked where the
-// segment met one in a row that some token of it sees: such values are taken out of the tile ahead of the product, where a weight of 0 would make NaN of them
-// for rows that do not see them.
-template <int kTile, bool BF16>
-__device__ __noinline__ float paged_poison(const PagedAttnArgs &a, const PagedSeg &g, int hd, int pos, int d) {
-  float sum = 0.f;
-  const uint16_t *v = static_cast<const uint16_t *>(a.v_pool);
+// The infinite and NaN values of V, columns d .. d + kCols - 1, in masked tiles of the segment, that the token at `pos` sees, added to
+// sum (each counted with weight 1, which gives the infinity or NaN that any positive weight would).  Only asked where the
+// segment met one in a row that some token of it sees: such values are taken out of the tile ahead of the product, where a
+// weight of 0 would make NaN of them for rows that do not see them.  Keys outside, columns inside: a row's place is looked up
+// once a page, and the threads of a warp read the same words.
+template <int kTile, bool BF16, int kCols>
+__device__ __noinline__ void paged_poison(const PagedAttnArgs &a, const PagedSeg &g, int hd, int pos, int d, float *sum) {
+  const uint16_t *v = static_cast<const uint16_t *>(a.v_pool) + d;
+  const int in_page = (1 << a.b.page_log) - 1;
   for (int i = g.begin; i < g.end; ++i) {
     const int key0 = g.s.tile(i) * kTile;
     if (!paged_masked<kTile>(a, g.s, key0)) continue;
-    for (int j = key0; j < key0 + kTile; ++j) {
-      if (!paged_sees(a, g.q, pos, j)) continue;
-      const int row = paged_row(a, g.s, g.seq, g.head, j);
-      if (row == a.oob_row) continue;
-      const uint32_t x = v[(int64_t)row * hd + d];
-      if (!not_finite<BF16>(x)) continue;
-      sum += BF16 ? __uint_as_float(x << 16) : __half2float(__ushort_as_half((unsigned short)x));
+    const int end = min(key0 + kTile, g.s.hi);
+    int row = a.oob_row;
+    for (int j = key0; j < end; ++j) {
+      if (j == key0 || (j & in_page) == 0)
+        row = paged_row(a, g.s, g.seq, g.head, j);
+      else if (row != a.oob_row)
+        ++row;
+      if (row == a.oob_row || !paged_sees(a, g.q, pos, j)) continue;
+      const uint4 *x = reinterpret_cast<const uint4 *>(v + (int64_t)row * hd);
+#pragma unroll 1
+      for (int c = 0; c < kCols / 8; ++c) {
+        const uint4 y = x[c];
+        if (!(not_finite<BF16>(y.x) | not_finite<BF16>(y.y) | not_finite<BF16>(y.z) | not_finite<BF16>(y.w))) continue;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t h = word(y, e >> 1) >> (16 * (e & 1)) & 0xffffu;
+          if (not_finite<BF16>(h)) sum[8 * c + e] += BF16 ? __uint_as_float(h << 16) : __half2float(__ushort_as_half((unsigned short)h));
+        }
+      }
     }
   }
-  return sum;
 }
 
 // Where column d of a row of a part lies: 4 columns of every row together, so that threads a row each write and read next to

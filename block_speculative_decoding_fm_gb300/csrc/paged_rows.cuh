@@ -296,7 +296,10 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<HD>::kCtas)
       }
       if (any_bad) {
         const PagedSeg held = g;
-        for (int e = 0; e < 8; ++e) v[e] += paged_poison<kRowsKeys, BF16>(a, held, HD, pos0 + t, d + e);
+        float more[8] = {};
+        paged_poison<kRowsKeys, BF16, 8>(a, held, HD, pos0 + t, d, more);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += more[e];
       }
       if (whole) {
         const float inv = paged_inv(a, g.q, pos0 + t, lt);

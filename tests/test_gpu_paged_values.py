@@ -2,10 +2,12 @@
 CTAs and joined."""
 from __future__ import annotations
 
+import numpy as np
 import pytest
 import torch
 
 import block_speculative_decoding_fm_gb300 as fm
+from oracle import paged as P
 from paged_common import TYPES, Batch
 from test_gpu_paged import attend
 
@@ -99,3 +101,28 @@ def test_time_of_garbage_in_hidden_rows(seqs, heads, page, window, sinks):
         us.append(sorted(times)[4] * 250)
     assert torch.equal(*outs)
     assert us[1] < 2 * us[0], us
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (150, 20)])
+@pytest.mark.parametrize("page", [16, 256])
+@pytest.mark.parametrize("t", ["f16", "bf16"])
+@pytest.mark.parametrize("heads,new", [((2, 2, 64), 3), ((1, 6, 256), 2), ((1, 2, 128), 40), ((1, 2, 64), 200), ((1, 3, 256), 90)])
+def test_infinite_values(heads, new, t, page, window, sinks):
+    """Infinities and NaN of V, one to a few a column, in rows all over a sequence: each output is infinite or NaN just where
+    the sum over the rows that it sees is (small queries: no weight underflows)."""
+    B = Batch([(new, 400), (new, 90)], *heads, page, TYPES[t], seed=55).create().fill_rows()
+    q = B.queries(0.1)
+    for i, n in enumerate(B.lengths):
+        for j in list(range(n - new, n)) + [int(x) for x in B.rng.integers(0, n, size=12)]:
+            for x in (float("inf"), float("-inf"), float("nan")):
+                d = B.rng.integers(0, B.hd, size=1 + B.hd // 64)
+                B.v_pool[0, int(B.table_np[i, j // page]), int(B.rng.integers(0, B.kv)), j % page, torch.from_numpy(d).cuda()] = x
+    got = attend(B, q, window=window, sinks=sinks).double().cpu().numpy()
+    qn, first = q.double().cpu().numpy(), 0
+    for i, n in enumerate(B.n):
+        with np.errstate(invalid="ignore"):
+            want, _, _ = P.attend(qn[first:first + n], B.rows(i, B.k_pool), B.rows(i, B.v_pool), B.hd ** -0.5, True, window, sinks)
+        for test in (np.isnan, np.isposinf, np.isneginf):
+            assert np.array_equal(test(got[first:first + n]), test(want)), test.__name__
+        assert np.isfinite(want).any() and np.isinf(want).any() and np.isnan(want).any()
+        first += n
