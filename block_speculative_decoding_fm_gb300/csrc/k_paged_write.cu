@@ -24,8 +24,29 @@ constexpr int kWThreads = 256;
 constexpr int kWTokens = 8;        // tokens of a CTA at most
 constexpr int kWHeads = 512;       // heads of a CTA at most (their table is 24 KB of shared memory)
 
-// The sequence of packed row t: the last i with starts[i] <= t (a warp's 32-way search).
-__device__ __forceinline__ int find_seq(const PagedBatch &b, int t, int lane) {
+// The sequence that holds packed row t, by a look at each, and its numbers (none: those of one without rows).
+__device__ __forceinline__ int scan_seqs(const PagedBatch &b, int t, int lane, PagedSeq &q) {
+  q = {0, 0, 0};
+#pragma unroll 1
+  for (int i0 = 0; i0 < b.n_seqs; i0 += 32) {
+    PagedSeq r = {0, 0, 0};
+    bool ok = false;
+    if (i0 + lane < b.n_seqs) r = paged_seq(b, i0 + lane, ok);
+    const uint32_t holds = __ballot_sync(0xffffffffu, ok && t >= r.s0 && t - r.s0 < r.n_new);
+    if (holds) {
+      const int src = __ffs(holds) - 1;
+      q.s0 = __shfl_sync(0xffffffffu, r.s0, src);
+      q.n_new = __shfl_sync(0xffffffffu, r.n_new, src);
+      q.len = __shfl_sync(0xffffffffu, r.len, src);
+      return i0 + src;
+    }
+  }
+  return 0;
+}
+// The sequence of packed row t, and its numbers: the last i with starts[i] <= t (a warp's 32-way search).  Starts outside the batch
+// lead the search astray, but then to a sequence that they are the numbers of; the one that holds t is then looked for one by
+// one, so that a bad number costs the rows of its own sequences alone.
+__device__ __forceinline__ int find_seq(const PagedBatch &b, int t, int lane, PagedSeq &q) {
   int lo = 0, hi = b.n_seqs;
   while (hi - lo > 1) {
     const int step = (hi - lo + 31) / 32, i = lo + lane * step;
@@ -34,6 +55,12 @@ __device__ __forceinline__ int find_seq(const PagedBatch &b, int t, int lane) {
     lo += k * step;
     hi = min(hi, lo + step);
   }
+  bool ok;
+  q = paged_seq(b, lo, ok);
+  if (ok) return lo;
+  PagedSeq held;
+  lo = scan_seqs(b, t, lane, held);
+  q = held;
   return lo;
 }
 
@@ -59,8 +86,9 @@ __global__ void __launch_bounds__(kWThreads) fm_paged_write_kernel(const __grid_
   pdl_trigger();
   pdl_wait();
   if (warp < n) {
-    const int t = t0 + warp, seq = find_seq(b, t, lane);
-    const PagedSeq q = paged_seq(b, seq);
+    const int t = t0 + warp;
+    PagedSeq q;
+    const int seq = find_seq(b, t, lane, q);
     const int pos = q.len - q.n_new + (t - q.s0);
     const bool in = t >= q.s0 && t - q.s0 < q.n_new;   // (rows behind the last sequence are left as they are)
     int64_t row = -1;

@@ -108,16 +108,20 @@ struct PagedSeq {
   int s0, n_new, len;   // first packed row, new rows, rows held (the new ones are the last)
 };
 
-// Sequence i, or one without rows where its numbers point outside the batch or the table.
-__device__ __forceinline__ PagedSeq paged_seq(const PagedBatch &b, int i) {
+// Sequence i, or one without rows where its numbers point outside the batch or the table (ok: they do not).
+__device__ __forceinline__ PagedSeq paged_seq(const PagedBatch &b, int i, bool &ok) {
   PagedSeq q;
   const int s0 = __ldcg(b.starts + i), s1 = __ldcg(b.starts + i + 1), len = __ldcg(b.lengths + i);
-  const bool ok = s0 >= 0 && s1 >= s0 && s1 <= b.n_tokens && len >= 0 && (int64_t)len <= ((int64_t)b.table_pages << b.page_log);
+  ok = s0 >= 0 && s1 >= s0 && s1 <= b.n_tokens && len >= 0 && (int64_t)len <= ((int64_t)b.table_pages << b.page_log);
   if (!ok) b.err[1] = 1;
-  q.s0 = s0;
+  q.s0 = ok ? s0 : 0;
   q.n_new = ok ? s1 - s0 : 0;
   q.len = ok ? len : 0;
   return q;
+}
+__device__ __forceinline__ PagedSeq paged_seq(const PagedBatch &b, int i) {
+  bool ok;
+  return paged_seq(b, i, ok);
 }
 
 // The key tiles (of kTile rows) that query tokens ta .. tb of a sequence see between them.

@@ -1,0 +1,65 @@
+"""Batches of the paged cache whose numbers are wrong or unusual: what a call leaves out, and what it does all the same."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import block_speculative_decoding_fm_gb300 as fm
+from paged_common import TYPES, Batch
+
+pytestmark = pytest.mark.gpu
+INVALID = fm.FM_ERR_INVALID_ARG
+
+
+def refused(status, call):
+    with pytest.raises(fm.FmError) as e:
+        call()
+    assert e.value.status == status, str(e.value)
+
+
+@pytest.mark.parametrize("seqs", [1, 7, 32, 33, 200])
+@pytest.mark.parametrize("value", [-1, -2 ** 31, 2 ** 31 - 1, None])
+def test_a_bad_start_costs_its_own_sequences(seqs, value):
+    """One start outside the packed rows: the write leaves out the sequences that it begins and ends, as the attention does, writes
+    the others' rows and reports it.  (None: a length past the table.)"""
+    rng = np.random.default_rng(seqs)
+    B = Batch([(int(rng.integers(1, 4)), int(rng.integers(0, 30))) for _ in range(seqs)], 1, 2, 64, 16, TYPES["f16"], seed=56, fill=3.0, pad=3)
+    B.create(rot_dims=16)
+    x = torch.from_numpy(rng.normal(size=(B.total, 4, 64))).half().cuda()
+    w = torch.ones(64, device="cuda")
+
+    def write():
+        q = torch.full((B.total, 2, 64), 9.0, dtype=B.t, device="cuda")
+        B.k_pool.fill_(3.0), B.v_pool.fill_(3.0)
+        fm.fm_paged_write(B.c, 0, B.b, x[:, :2], x[:, 2:3], x[:, 3:], q, w, w)
+        return q, B.k_pool.clone(), B.v_pool.clone()
+
+    good = write()
+    fm.fm_paged_synchronize(B.c)
+    first = np.concatenate([[0], np.cumsum(B.n)])
+    for i in sorted({0, seqs // 3, seqs // 2, seqs - 1, seqs}):
+        saved = B.starts.clone(), B.len_dev.clone()
+        if value is None:
+            i = min(i, seqs - 1)
+            B.len_dev[i] = 2 ** 30
+            lost = [i]
+        else:
+            B.starts[i] = value
+            lost = [j for j in (i - 1, i) if 0 <= j < seqs]
+        got = write()
+        refused(INVALID, lambda: fm.fm_paged_synchronize(B.c))
+        want = [y.clone() for y in good]
+        for j in lost:
+            want[0][first[j]:first[j + 1]] = 9.0
+            for p in range(B.lengths[j] - B.n[j], B.lengths[j]):
+                for pool in want[1:]:
+                    pool[0, int(B.table_np[j, p // 16]), :, p % 16] = 3.0
+        for a, b in zip(got, want):
+            assert torch.equal(a, b), (i, lost)
+        out = torch.full((B.total, 2, 64), 9.0, dtype=B.t, device="cuda")
+        fm.fm_paged_attend(B.c, 0, B.b, good[0], out)
+        refused(INVALID, lambda: fm.fm_paged_synchronize(B.c))
+        left = [t for j in lost for t in range(first[j], first[j + 1])] + list(range(B.total - 3, B.total))
+        assert (out == 9.0).flatten(1).all(1).nonzero()[:, 0].tolist() == sorted(left)
+        B.starts.copy_(saved[0]), B.len_dev.copy_(saved[1])
