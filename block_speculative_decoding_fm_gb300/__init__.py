@@ -926,7 +926,8 @@ def fm_paged_last_launch_count(c) -> int:
 
 def fm_paged_synchronize(c, stream=None) -> None:
     """Wait for the stream; raise FmError(FM_ERR_TIMEOUT) if a bounded device wait gave up, FmError(FM_ERR_INVALID_ARG) if a
-    batch's starts, lengths or pages pointed outside, since the last check."""
+    batch's starts, lengths or pages pointed outside, since the last check.  Where both happened, the next call raises the
+    second."""
     _paged_check(load_library().fm_paged_synchronize(c, _stream(stream)), c)
 
 

@@ -10,6 +10,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <mutex>
 #include <new>
 #include <vector>
 
@@ -30,7 +31,9 @@ struct fm_paged {
   CUtensorMap tk, tv;
   void *block = nullptr;         // all device memory: frequencies, error words
   uint64_t *freq = nullptr;
-  int32_t *dev_err = nullptr;
+  int32_t *dev_err = nullptr;    // what went wrong: a wait gave up, a batch pointed outside
+  int32_t *taken = nullptr;      // the error that a check takes, under its lock
+  std::mutex taking;
 };
 
 namespace {
@@ -123,6 +126,14 @@ fm_status check_config(const fm_paged_config &g) {
   return FM_OK;
 }
 
+// One error taken out of the handle's words: read and cleared in one step, so that one that another stream raises meanwhile stays
+// for the next check, as the second kind does where there are both.
+__global__ void paged_take_kernel(int32_t *err, int32_t *taken) {
+  const int wait = atomicExch(err, 0);
+  taken[0] = wait;
+  taken[1] = wait ? 0 : atomicExch(err + 1, 0);
+}
+
 void release(fm_paged *c) {
   if (c->block) cudaFree(c->block);
   delete c;
@@ -145,6 +156,7 @@ fm_status setup(fm_paged *c, cudaStream_t s) {
   }
   c->freq = static_cast<uint64_t *>(c->block);
   c->dev_err = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(c->block) + 1024);
+  c->taken = c->dev_err + 32;   // (a line of its own)
   uint64_t host[(1024 + 256) / 8] = {};
   for (int i = 0; i < g.rot_dims / 2; ++i) {
     // f / 2 pi in units of 2^-64: two 32-bit digits, the second from the first's exact remainder
@@ -368,8 +380,12 @@ fm_status fm_paged_synchronize(fm_paged *c, void *stream) {
   PCK(cudaMemcpyAsync(e, c->dev_err, sizeof e, cudaMemcpyDeviceToHost, s));
   PCK(cudaStreamSynchronize(s));
   if (!e[0] && !e[1]) return FM_OK;
-  PCK(cudaMemsetAsync(c->dev_err, 0, sizeof e, s));
+  std::lock_guard<std::mutex> lock(c->taking);
+  paged_take_kernel<<<1, 1, 0, s>>>(c->dev_err, c->taken);
+  PCK(cudaGetLastError());
+  PCK(cudaMemcpyAsync(e, c->taken, sizeof e, cudaMemcpyDeviceToHost, s));
   PCK(cudaStreamSynchronize(s));
+  if (!e[0] && !e[1]) return FM_OK;   // (another thread's check has reported it)
   return e[0] ? pfail(FM_ERR_TIMEOUT, "a bounded device wait gave up")
               : pfail(FM_ERR_INVALID_ARG, "a batch's starts, lengths or pages lay outside the batch, its table or the pool");
 }

@@ -856,7 +856,8 @@ FM_API fm_status fm_paged_get_config(const fm_paged *c, fm_paged_config *cfg);
 /* Kernel launches issued by this host thread's last write or attend. */
 FM_API fm_status fm_paged_last_launch_count(const fm_paged *c, int32_t *count);
 /* Wait for the stream; FM_ERR_TIMEOUT if a bounded device wait gave up, FM_ERR_INVALID_ARG if a batch's numbers pointed
-   outside, since the last check (cleared; what other streams still run may raise them again). */
+   outside, since the last check.  What it reports is cleared, the first of the two ahead of the second, which the next call
+   reports; what other streams still run may raise them again. */
 FM_API fm_status fm_paged_synchronize(fm_paged *c, void *stream);
 /* fm_selftest_wait_timeout for a paged cache.  Errors: FM_ERR_INVALID_ARG, FM_ERR_CUDA. */
 FM_API fm_status fm_paged_selftest_wait_timeout(fm_paged *c, int32_t budget_us, void *stream);

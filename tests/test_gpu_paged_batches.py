@@ -63,3 +63,49 @@ def test_a_bad_start_costs_its_own_sequences(seqs, value):
         left = [t for j in lost for t in range(first[j], first[j + 1])] + list(range(B.total - 3, B.total))
         assert (out == 9.0).flatten(1).all(1).nonzero()[:, 0].tolist() == sorted(left)
         B.starts.copy_(saved[0]), B.len_dev.copy_(saved[1])
+
+
+def test_both_errors_are_reported():
+    """A batch that pointed outside and a wait that gave up: one check reports the wait, the next the batch, then neither; on
+    any stream."""
+    B = Batch([(2, 30), (1, 5)], 1, 2, 64, 16, TYPES["f16"], seed=57).create().fill_rows()
+    q = B.queries()
+    out = torch.empty_like(q)
+    for stream in (torch.cuda.current_stream(), torch.cuda.Stream()):
+        B.len_dev[0] = -1
+        fm.fm_paged_write(B.c, 0, B.b, q, None, None, out)
+        torch.cuda.synchronize()
+        fm.fm_paged_selftest_wait_timeout(B.c, 1000, stream=stream)
+        refused(fm.FM_ERR_TIMEOUT, lambda: fm.fm_paged_synchronize(B.c, stream=stream))
+        refused(INVALID, lambda: fm.fm_paged_synchronize(B.c, stream=stream))
+        fm.fm_paged_synchronize(B.c, stream=stream)
+        B.len_dev[0] = B.lengths[0]
+    fm.fm_paged_write(B.c, 0, B.b, q, None, None, out)
+    fm.fm_paged_synchronize(B.c)
+
+
+def test_threads_report_an_error_once():
+    """Four host threads check their streams at the same time: one of them reports."""
+    import threading
+    B = Batch([(2, 30)], 1, 2, 64, 16, TYPES["f16"], seed=58).create().fill_rows()
+    q, streams = B.queries(), [torch.cuda.Stream() for _ in range(4)]
+    out = torch.empty_like(q)
+    for _ in range(20):
+        B.len_dev[0] = -1
+        fm.fm_paged_write(B.c, 0, B.b, q, None, None, out)
+        torch.cuda.synchronize()
+        found, gate = [], threading.Barrier(4)
+
+        def check(s):
+            gate.wait()
+            try:
+                fm.fm_paged_synchronize(B.c, stream=s)
+            except fm.FmError as e:
+                found.append(e.status)
+
+        threads = [threading.Thread(target=check, args=(s,)) for s in streams]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        assert found == [INVALID]
