@@ -858,10 +858,10 @@ fm_status fm_mtp_use_paged(fm_mtp *m, fm_paged *c, int32_t layer, const int32_t 
   if (!m->ao16) MTRY(malloc_dev(m, &m->ao16, rows));
   int64_t need = 0;
   if (fm_paged_workspace_bytes(c, m->cfg.max_rows, &need) != FM_OK) return mfail(m, FM_ERR_INVALID_ARG, "the paged cache's workspace");
-  if (m->paged_ws_bytes < need) {   // (a smaller one of an earlier cache stays until the head goes: passes may still use it)
-    m->paged_ws = nullptr;
-    m->paged_ws_bytes = 0;
-    MTRY(malloc_dev(m, &m->paged_ws, (size_t)need));
+  if (m->paged_ws_bytes < need) {   // (an earlier, smaller one stays until the head goes: passes may still use it)
+    uint8_t *ws = nullptr;
+    MTRY(malloc_dev(m, &ws, (size_t)need));
+    m->paged_ws = ws;
     m->paged_ws_bytes = need;
   }
   m->kvq = nullptr;
