@@ -150,7 +150,11 @@ __global__ void __launch_bounds__(ChunkCfg<HD, NT>::kThreads, 1)
   PagedWarp<typename C::Walk> &w = reinterpret_cast<PagedWarp<typename C::Walk> *>(start + 1)[warp];
   const PagedBatch &b = a.b;
 
-  pdl_trigger();
+  // Tensor memory ahead of the trigger: a later launch that started first could take it, and would wait for this one.
+  if (warp == 1) {
+    tmem_alloc<512>(tslot);
+    pdl_trigger();
+  }
   if (threadIdx.x == 0) {
     asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&a.tk)) : "memory");
     asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&a.tv)) : "memory");
@@ -172,7 +176,6 @@ __global__ void __launch_bounds__(ChunkCfg<HD, NT>::kThreads, 1)
     mbar_init(vclean, 64);
     mbar_fence_init();
   }
-  if (warp == 1) tmem_alloc<512>(tslot);
   pdl_wait();
   tc_fence_before();
   paged_plan<kRows, false, kChunkKeys, kChunkCost, kChunkLeast, C::kThreads>(a, sh, start);

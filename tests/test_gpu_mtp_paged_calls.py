@@ -72,3 +72,30 @@ def test_a_failed_call_changes_nothing():
     p.fm.fm_paged_synchronize(c)
     assert k[0, 0, :, 1].any() and torch.equal(k[0, 0, :, 0], before[0, 0, :, 0])
     p.close()
+
+
+def test_beside_other_launches_with_tensor_memory():
+    """Chunks of head dim 64, whose CTAs leave room on an SM, and passes of a head, one behind the other in a stream: each gets its
+    tensor memory, and what it gives alone."""
+    import torch
+    from paged_common import Batch
+    cfg = S.mtp_micro_config()
+    p = MtpPair(cfg, 1414)
+    B = Batch([(40, 300), (3, 900), (64, 10)], 2, 2, 64, 32, torch.bfloat16, seed=59).create().fill_rows()
+    q = B.queries()
+    t, hn = torch.tensor([9, 8, 7], dtype=torch.int32, device="cuda"), torch.from_numpy(S.gen_mtp_hidden(p.rng, 3, cfg.hidden)).cuda()
+    results = []
+    for _ in range(60):
+        out, h = torch.zeros_like(q), torch.zeros((3, cfg.hidden), device="cuda")
+        p.fm.fm_paged_attend(B.c, 0, B.b, q, out)
+        p.fm.fm_mtp_forward(p.h, t, hn, 0, 0, h)
+        p.fm.fm_paged_attend(B.c, 0, B.b, q, out)
+        results.append((out, h))
+    p.fm.fm_paged_synchronize(B.c)
+    for out, h in results[1:]:
+        assert torch.equal(out, results[0][0]) and torch.equal(h, results[0][1])
+    alone = torch.zeros_like(q)
+    p.fm.fm_paged_attend(B.c, 0, B.b, q, alone)
+    torch.cuda.synchronize()
+    assert torch.equal(alone, results[0][0])
+    p.close()
