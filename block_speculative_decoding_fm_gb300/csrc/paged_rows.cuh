@@ -204,13 +204,14 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<HD>::kCtas)
             o[d][2 * h + 1] *= f;
           }
         }
-        const float off = m[h] == -INFINITY ? 0.f : m[h] * a.scale_log2;
+        float off = m[h] == -INFINITY ? 0.f : m[h] * a.scale_log2, first = 0.f;
+        if (fabsf(off) > kFarReference) first = m[h], off = 0.f;   // (taken off the score itself)
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             float &p = s[n][2 * h + e];
-            p = ex2(fmaf(p, a.scale_log2, -off));
+            p = ex2(fmaf(p - first, a.scale_log2, -off));
             l[h] += p;
           }
       }

@@ -839,7 +839,7 @@ FM_API fm_status fm_paged_write(fm_paged *c, int32_t layer, const fm_paged_batch
  * row that is not seen has no part in the result, whatever it holds (pages
  * outside every window of the call's rows are not read, their table entries
  * may be stale).  Of a key whose weight is below 2^-24 (f16) of the largest one
- * the part may be lost.
+ * the part may be lost.  scale q . k past f32's range counts as infinite.
  * workspace_dev: fm_paged_workspace_bytes(c, batch->max_new) bytes on the device, 16-byte
  * aligned, its contents of no matter; no other call may use it until this one is done.
  * Errors: FM_ERR_INVALID_ARG, FM_ERR_UNSUPPORTED, FM_ERR_CUDA.  A bounded

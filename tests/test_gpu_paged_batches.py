@@ -6,7 +6,9 @@ import pytest
 import torch
 
 import block_speculative_decoding_fm_gb300 as fm
-from paged_common import TYPES, Batch
+from oracle import paged as P
+from paged_common import TYPES, Batch, half_step
+from test_gpu_paged import BLOCKS, CHUNKS, TOKENS
 
 pytestmark = pytest.mark.gpu
 INVALID = fm.FM_ERR_INVALID_ARG
@@ -109,3 +111,62 @@ def test_threads_report_an_error_once():
         for t in threads:
             t.join()
         assert found == [INVALID]
+
+
+KINDS = [(TOKENS, (2, 2, 64)), (BLOCKS, (2, 1, 128)), (CHUNKS, (2, 1, 128)), (CHUNKS, (1, 3, 64)), (CHUNKS, (1, 3, 256)), (BLOCKS, (1, 8, 128))]
+
+
+@pytest.mark.parametrize("scale", [1e-30, 1e30])
+@pytest.mark.parametrize("seqs,heads", KINDS)
+def test_ends_of_the_scale(seqs, heads, scale):
+    """All scores equal to rounding: the mean of the rows.  One score far above the others: its row, or the mean of those that share
+    it (from 512 on bf16 keys go in steps of 4)."""
+    B = Batch(seqs, *heads, 32, TYPES["bf16"], seed=61).create().fill_rows()
+    q = torch.ones((B.total, B.heads, B.hd), dtype=B.t, device="cuda")
+    B.k_pool.fill_(0.0)
+    for i, n in enumerate(B.lengths):       # a row's size is its place: the last seen one is the largest
+        for j in range(n):
+            B.k_pool[0, int(B.table_np[i, j // 32]), :, j % 32, :2] = float(j + 1) if j < 256 else 256.0 + 2 * (j - 255)
+    out = torch.full_like(q, 7.0)
+    fm.fm_paged_attend(B.c, 0, B.b, q, out, scale=scale)
+    fm.fm_paged_synchronize(B.c)
+    got, first = out.double().cpu().numpy(), 0
+    for i, n in enumerate(B.n):
+        if n:
+            ones = np.ones((n, B.heads, B.hd))
+            want, mass, _ = P.attend(ones, B.rows(i, B.k_pool), B.rows(i, B.v_pool), scale)
+            # (weights are 1, or 0: their sum is exact, the products' sums are off by 2^-20 of the mass, the output by half a step)
+            assert (np.abs(got[first:first + n] - want) <= half_step(B.t) * np.abs(want) + 2.0 ** -18 * mass).all()
+        first += n
+
+
+@pytest.mark.parametrize("size", [2.0 ** 8, 2.0 ** 11, 2.0 ** 13, 2.0 ** 15, 2.0 ** 40])
+@pytest.mark.parametrize("seqs,heads", KINDS)
+@pytest.mark.parametrize("t", ["f16", "bf16"])
+def test_far_scores(seqs, heads, t, size):
+    """Scaled scores from 2^16 on to beyond what an exponent holds, of either sign, in whole numbers that a factor of two separates:
+    the largest one's row alone."""
+    if t == "f16" and size > 2.0 ** 15:
+        pytest.skip("not an f16")
+    B = Batch(seqs, *heads, 32, TYPES[t], seed=64).create().fill_rows()
+    q = torch.zeros((B.total, B.heads, B.hd), dtype=B.t, device="cuda")
+    q[:, :, 0] = size
+    for sign in (1.0, -1.0):
+        B.k_pool.fill_(0.0)
+        for i, n in enumerate(B.lengths):
+            steps = torch.randperm(n, generator=torch.Generator().manual_seed(i)).double() % 127 + 129   # (eight bits)
+            steps[torch.arange(n) % 9 == 0] = 0.0
+            for j in range(n):
+                B.k_pool[0, int(B.table_np[i, j // 32]), :, j % 32, 0] = sign * float(steps[j]) * size / 256
+        out = torch.full_like(q, 7.0)
+        fm.fm_paged_attend(B.c, 0, B.b, q, out, scale=1.0)
+        fm.fm_paged_synchronize(B.c)
+        got, first = out.double().cpu().numpy(), 0
+        for i, n in enumerate(B.n):
+            if n:
+                want, mass, _ = P.attend(q[first:first + n].double().cpu().numpy(), B.rows(i, B.k_pool), B.rows(i, B.v_pool), 1.0)
+                # A weight is not 1 but 2^r, r what rounding reference * scale leaves (up to 2^-24 of it, the same for all weights of a
+                # row): its own rounding to the pool's type, half a step, moves the output and not the sum of weights.
+                e = half_step(B.t)
+                assert (np.abs(got[first:first + n] - want) <= e * np.abs(want) + (e * (1 + e) + 2.0 ** -18) * mass).all(), sign
+            first += n
