@@ -7,7 +7,7 @@ import torch
 
 import block_speculative_decoding_fm_gb300 as fm
 from oracle import paged as P
-from paged_common import TYPES, Batch, half_step
+from paged_common import TYPES, Batch, check_attend, half_step
 from test_gpu_paged import BLOCKS, CHUNKS, TOKENS
 
 pytestmark = pytest.mark.gpu
@@ -116,6 +116,18 @@ def test_threads_report_an_error_once():
 KINDS = [(TOKENS, (2, 2, 64)), (BLOCKS, (2, 1, 128)), (CHUNKS, (2, 1, 128)), (CHUNKS, (1, 3, 64)), (CHUNKS, (1, 3, 256)), (BLOCKS, (1, 8, 128))]
 
 
+@pytest.mark.parametrize("scale", [0.03, 0.5, 1.0])
+@pytest.mark.parametrize("seqs,heads", KINDS)
+@pytest.mark.parametrize("t", ["f16", "bf16"])
+def test_scale(seqs, heads, t, scale):
+    B = Batch(seqs, *heads, 32, TYPES[t], seed=60).create().fill_rows()
+    q = B.queries(0.5)
+    out = torch.full_like(q, 7.0)
+    fm.fm_paged_attend(B.c, 0, B.b, q, out, scale=scale)
+    fm.fm_paged_synchronize(B.c)
+    check_attend(B, q, out, scale=scale)
+
+
 @pytest.mark.parametrize("scale", [1e-30, 1e30])
 @pytest.mark.parametrize("seqs,heads", KINDS)
 def test_ends_of_the_scale(seqs, heads, scale):
@@ -170,3 +182,30 @@ def test_far_scores(seqs, heads, t, size):
                 e = half_step(B.t)
                 assert (np.abs(got[first:first + n] - want) <= e * np.abs(want) + (e * (1 + e) + 2.0 ** -18) * mass).all(), sign
             first += n
+
+
+@pytest.mark.parametrize("max_new", [0, 1, 20, 129])
+@pytest.mark.parametrize("seqs,heads", [(CHUNKS, (2, 1, 64)), (CHUNKS, (1, 2, 128)), (CHUNKS, (1, 3, 256)), (BLOCKS, (1, 6, 256))])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (60, 5)])
+def test_more_rows_than_max_new(seqs, heads, max_new, window, sinks):
+    """A sequence with more new rows than the batch says: the kernel that was chosen for fewer attends over all of them."""
+    B = Batch(seqs, *heads, 32, TYPES["bf16"], seed=62).create().fill_rows()
+    q = B.queries()
+    b = fm.fm_paged_batch(B.c, B.starts, B.len_dev, B.table, B.total, max_new)
+    out = torch.full_like(q, 7.0)
+    fm.fm_paged_attend(B.c, 0, b, q, out, window=window, sinks=sinks)
+    fm.fm_paged_synchronize(B.c)
+    check_attend(B, q, out, window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("heads,new,past", [((1, 1, 128), 40, 4000), ((1, 4, 64), 16, 9000), ((1, 6, 256), 24, 3000)])
+def test_long_rows_in_small_tiles(heads, new, past):
+    """Tiles of 16 rows over a long sequence, each cut between CTAs."""
+    B = Batch([(new, past)], *heads, 64, TYPES["f16"], seed=63).create().fill_rows()
+    q = B.queries()
+    b = fm.fm_paged_batch(B.c, B.starts, B.len_dev, B.table, B.total, 1)
+    for causal in (True, False):
+        out = torch.full_like(q, 7.0)
+        fm.fm_paged_attend(B.c, 0, b, q, out, causal=causal)
+        fm.fm_paged_synchronize(B.c)
+        check_attend(B, q, out, causal=causal)
