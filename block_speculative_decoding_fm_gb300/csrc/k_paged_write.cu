@@ -13,8 +13,9 @@
 // a lane: one or two 16-byte loads, the mean by shuffles, the partner of a pair from the same lane or, in the half layout,
 // from the lane rot / 16 away.  What counts is instructions a row: choosing q, k or v and its strides for each row took a
 // third of them.  (Four values from each partner instead of eight neighbours save the shuffles but halve the loads' width:
-// 357 us for 32,768 rows of 24/4 x 256 where this form's first version took 264.)  Measured: 212 us for those rows, 5.1 TB/s
-// (0.76 of the copy rate; issue slots 77 % taken), 5.7 us for 1-17 rows of 32 sequences of 16 x 128, 3.1 us for one token.
+// 357 us for 32,768 rows of 24/4 x 256 where this form's first version took 264.)  Measured: 213 us for those rows, 5.0 TB/s
+// (0.75 of the copy rate; issue slots 77 % taken); on the GPU alone 5.8 us for 1-17 rows of 32 sequences of 16 x 128 and 3.3 us for
+// one token, whose calls take 9 us of the host.
 #include "paged_dev.cuh"
 
 namespace fm {

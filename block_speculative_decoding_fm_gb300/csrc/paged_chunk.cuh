@@ -6,7 +6,7 @@
 // head of the group): the heads of a group share every key tile, so a tile holds 128 / group whole tokens.
 //   warp 0         the queries of a unit (one box a tile and 64 dims) and the key tiles (a box a page and 64 dims) into a ring
 //   warp 1         the products; an elected lane issues them
-//   warps 2, 3     see that masked tiles of V hold finite values only
+//   warps 2, 3     see that masked tiles of V hold finite values only, and note where a row that is seen did not
 //   warps 4 ..     four a query tile, a thread a row: scores -> weights, the outputs
 // Two query tiles (kNT = 2, head dims 64 and 128) share every K and V tile and take turns: while one's scores become
 // weights, the other's products run.  With one tile (kNT = 1: head dim 256, whose outputs fill half of tensor memory, or
@@ -17,10 +17,13 @@
 // P enters the second product rounded once to the pool's type, as paged_rows.cuh says; sums, outputs and references are f32.
 //
 // Bound: 4 * 128 * 128 * head_dim flop a query and a key tile against 4 * 128 * head_dim bytes: the tensor pipe for chunks, memory
-// for a few tokens over a long cache.  Measured: 2,048 rows over 34,816 of 16 x 128 bf16 404 us (1.40 PFLOP/s, 0.72 of the measured
-// bf16 rate, tensor pipe 67 %); prompts of 33-4,001 rows of 24/4 x 256 792 us (1.03 PFLOP/s); 1-17 rows of 32 sequences of 16 x 128
-// over 512-8,192 in pages of 64 179 us (0.88 of the copy rate), of 16 207 us.  What is left: a tile's chain (scores, 890 cycles of
-// weights with a warp a scheduler, products) against 2,048 cycles of products a pair of tiles.
+// for a few tokens over a long cache.  Measured, calls one after another for seconds: 2,048 rows over 34,816 of 16 x 128 bf16 454 us
+// (1.25 PFLOP/s, 0.64 of the measured bf16 rate; the card is at its power limit then, at 1,485 of 2,070 MHz -- the first tens of
+// calls take 390-405 us, 1.40-1.45 PFLOP/s, tensor pipe 67 %); prompts of 33-4,001 rows of 24/4 x 256 817 us (1.00 PFLOP/s; 790 in
+// a short graph).  In short graphs: 1-17 rows of 32 sequences of 16 x 128 over 512-8,192 in pages of 64 179 us (0.88 of the copy
+// rate), of 16 206; 512 rows over 8,704 of 8 x 128 34 (floor 9); eight prompts of 1,024 of 16 x 128 68-72 (floor 20).  What is
+// left: a tile's chain (scores, 890 cycles of weights with a warp a scheduler, products) against 2,048 cycles of products a
+// pair of tiles; in short chunks the units' ends and starts.
 #pragma once
 
 #include "paged_dev.cuh"
@@ -354,7 +357,8 @@ __global__ void __launch_bounds__(ChunkCfg<HD, NT>::kThreads, 1)
     // weights.  (The ring's own barriers cannot be waited on here: they may be a whole turn behind.)
     // A word is one fused multiply-add, four sums at a time; the loop is short because it runs once or twice a unit, from
     // instructions that have left the caches since (exponents compared by three integer operations a word and both
-    // halves of head dim 256 unrolled: 153 us for the windowed chunk of 8,191 rows, 146 so).
+    // halves of head dim 256 unrolled: 153 us for the windowed chunk of 8,191 rows, 146 so; 148 with the place of what is found
+    // looked at, so that garbage in hidden rows stays cheap).
     uint32_t c0 = 0, segs = 0, nv = 0;
     bool ok = true;
     while (ok && w.next(a, lane)) {

@@ -732,7 +732,8 @@ FM_API fm_status fm_mtp_use_kvq(fm_mtp *m, fm_kvq *c, int32_t layer, int32_t seq
  *
  * A batch (fm_paged_batch) says which rows are new and where sequences lie.
  * Its numbers are on the device: a captured call reads them again at every
- * replay.  Sequence i's new rows are rows starts[i] .. starts[i + 1] - 1 of the
+ * replay.  (A table's rows are at least table_pages entries apart, one sequence's
+ * too.)  Sequence i's new rows are rows starts[i] .. starts[i + 1] - 1 of the
  * packed rows; lengths[i] rows are in the cache once they are written, the new
  * ones the last, so a new row t of n has position lengths[i] - n + t.  Row j of
  * the sequence is row j % page_rows of page table[i][j / page_rows].  Several
@@ -741,7 +742,8 @@ FM_API fm_status fm_mtp_use_kvq(fm_mtp *m, fm_kvq *c, int32_t layer, int32_t seq
  * as they are.
  * A sequence whose starts or length point outside the packed rows or the table
  * is left out of the call; a page outside the pool that is needed is read as
- * zeros and not written; fm_paged_synchronize reports both.
+ * zeros and not written; fm_paged_synchronize reports both.  Starts that fall
+ * within the packed rows are not looked for: whose rows are written is then open.
  *
  * Calls allocate and copy nothing and change nothing in the handle: several
  * may run at once, from several host threads, on several streams and in
@@ -756,7 +758,9 @@ FM_API fm_status fm_mtp_use_kvq(fm_mtp *m, fm_kvq *c, int32_t layer, int32_t seq
 #define FM_ROPE_LINEAR 1        /* f_i / rope_factor */
 #define FM_ROPE_BY_PARTS 2      /* f_i (r + (1 - r) / rope_factor), r = clamp((rope_rows f_i / 2 pi - rope_low) / (rope_high - rope_low), 0, 1):
                                    pairs that turn at least rope_high times over rope_rows rows keep their angle, those
-                                   that turn at most rope_low times are stretched */
+                                   that turn at most rope_low times are stretched.  The ramp between is over turns, as the
+                                   method's paper has it; implementations that ramp over the pair's index between borders
+                                   rounded to whole pairs give the middle pairs other angles, which are not to be had here */
 
 typedef struct fm_paged_config {
   int32_t n_layers;      /* 1 .. 1024 */
@@ -840,6 +844,8 @@ FM_API fm_status fm_paged_write(fm_paged *c, int32_t layer, const fm_paged_batch
  * outside every window of the call's rows are not read, their table entries
  * may be stale).  Of a key whose weight is below 2^-24 (f16) of the largest one
  * the part may be lost.  scale q . k past f32's range counts as infinite.
+ * Infinities and NaN of V that some rows of a unit see and others do not take a
+ * slow path (1 us and up a key tile); in rows that none sees they cost nothing.
  * workspace_dev: fm_paged_workspace_bytes(c, batch->max_new) bytes on the device, 16-byte
  * aligned, its contents of no matter; no other call may use it until this one is done.
  * Errors: FM_ERR_INVALID_ARG, FM_ERR_UNSUPPORTED, FM_ERR_CUDA.  A bounded
