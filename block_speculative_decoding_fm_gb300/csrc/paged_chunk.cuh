@@ -404,7 +404,8 @@ __global__ void __launch_bounds__(ChunkCfg<HD, NT>::kThreads, 1)
     const int t = (warp - 4) >> 2, quad = warp & 3, in = quad * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
     const float thr = 8.f / a.scale_log2;       // a row's reference moves where a score beats it by 2^8
-    // the power of two below the scale, whose products are exact, for far references (scores less reference, for all: 10 % slower)
+    // For far references the power of two below the scale, whose products are exact; a weight w becomes up to sqrt(w), but there a
+    // score's last bit is a factor of two or more.  (The reference taken off every score: 10 % slower.)
     const float far = __int_as_float(__float_as_int(a.scale_log2) & 0x7f800000);
     uint32_t c0 = 0, segs = 0, tiles = 0;
     uint32_t ns[2] = {0, 0}, npv = 0;           // scores taken from each buffer, products behind

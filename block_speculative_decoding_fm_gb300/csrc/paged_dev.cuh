@@ -164,8 +164,8 @@ __device__ __forceinline__ bool paged_seen(const PagedAttnArgs &a, const PagedSp
 }
 
 // A weight is exp2(score scale - reference scale), one multiply-add whose second product is rounded: all weights of a reference are
-// off by the same factor, which falls out, as long as an exponent holds it.  Past this size of the product (neighbouring f32
-// scores are then at least a factor of two apart) the kernels see to it that nothing is rounded.
+// off by the same factor, which falls out, as long as an exponent holds it.  Past this size of the product the kernels see to it
+// that it is exact.
 constexpr float kFarReference = 16777216.f;
 
 // What a row's summed outputs are multiplied by: 1 / the sum of its weights.  Without weight are a row that sees nothing (zeros) and

@@ -843,7 +843,9 @@ FM_API fm_status fm_paged_write(fm_paged *c, int32_t layer, const fm_paged_batch
  * row that is not seen has no part in the result, whatever it holds (pages
  * outside every window of the call's rows are not read, their table entries
  * may be stale).  Of a key whose weight is below 2^-24 (f16) of the largest one
- * the part may be lost.  scale q . k past f32's range counts as infinite.
+ * the part may be lost.  scale q . k past f32's range counts as infinite; past
+ * 2^24, where a score's last bit is a factor of two or more, weights below the
+ * largest are as rough as that.
  * Infinities and NaN of V that some rows of a unit see and others do not take a
  * slow path (1 us and up a key tile); in rows that none sees they cost nothing.
  * workspace_dev: fm_paged_workspace_bytes(c, batch->max_new) bytes on the device, 16-byte
